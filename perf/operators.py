@@ -172,7 +172,7 @@ def prepare(case, seed):
         st["p"] = _randn(g, at).mul_(0.02).mul_(used)
         st["grad"] = _randn(g, at).mul_(1e-3).mul_(used).to(TYPES[case["g"]])
         st["scale"] = torch.full((1,), 0.7, device="cuda")   # of clipping the gradient's norm
-        st["copy"] = torch.empty(at, dtype=torch.bfloat16, device="cuda") if case["copy"] else None
+        st["copy"] = torch.zeros(at, dtype=torch.bfloat16, device="cuda") if case["copy"] else None
         m = _randn(g, at).mul_(3e-4).mul_(used)
         v = _randn(g, at).square_().mul_(1e-6).mul_(used)
         if case["bits"] == 32:
