@@ -69,6 +69,62 @@ class GemmProblem(ctypes.Structure):
                    float(alpha), float(beta), transA.encode(), transB.encode())
 
 
+AMSIM_F32 = 0
+AMSIM_BF16 = 1
+AMSIM_REDUCE_MEAN = 0
+AMSIM_REDUCE_SUM = 1
+REDUCTIONS = {"mean": AMSIM_REDUCE_MEAN, "sum": AMSIM_REDUCE_SUM}
+AMSIM_ADAMW_BLOCK = 256
+AMSIM_BLOCK_NORM_MAX_COLS = 16384
+
+
+class BlockNormDesc(ctypes.Structure):
+    """amsim_block_norm_desc (row strides of 0 mean dense rows)."""
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "gate_rows", "ldx", "ldy", "ldr", "ldn", "lddx", "lddy", "lddr",
+                                               "lddn")] +
+                [(n, ctypes.c_int) for n in ("cols", "x_type", "y_type", "n_type")] +
+                [("alpha", ctypes.c_float), ("eps", ctypes.c_float)])
+
+
+class VocabLossDesc(ctypes.Structure):
+    """amsim_vocab_loss_desc (row strides of 0 mean dense rows)."""
+    _fields_ = ([(n, ctypes.c_int64) for n in ("tokens", "ignore_index", "ld_h", "ld_w", "ld_dh", "ld_dw")] +
+                [(n, ctypes.c_int) for n in ("vocab", "dim", "reduction")])
+
+
+class AdamwTensor(ctypes.Structure):
+    """amsim_adamw_tensor: one tensor of a step."""
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("g_type", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+    @classmethod
+    def make(cls, p, g, m, v, m_scale=None, v_scale=None, copy=None, weight_decay=0.0, lr_scale=1.0):
+        """From contiguous CUDA tensors: p fp32; g fp32 or bf16; m, v fp32, or int8 and uint8 codes with their
+        block scales; copy bf16 or None.  The tensors must outlive the table."""
+        import torch
+        n, eight = p.numel(), m_scale is not None
+        want = [("p", p, torch.float32, n), ("m", m, torch.int8 if eight else torch.float32, n),
+                ("v", v, torch.uint8 if eight else torch.float32, n), ("g", g, g.dtype, n)]
+        blocks = -(-n // AMSIM_ADAMW_BLOCK)
+        if eight:
+            want += [("m_scale", m_scale, torch.float32, blocks), ("v_scale", v_scale, torch.float32, blocks)]
+        if copy is not None:
+            want.append(("copy", copy, torch.bfloat16, n))
+        for name, t, dtype, size in want:
+            if t is None or t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != size:
+                raise TypeError(f"AdamwTensor: {name} must be a contiguous CUDA tensor of {size} {dtype} values")
+        return cls(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale), _ptr(copy), n, float(lr_scale),
+                   float(weight_decay), _dtype(g), 0)
+
+
+class AdamwHyper(ctypes.Structure):
+    """amsim_adamw_hyper."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("grad_scale", ctypes.c_void_p)]
+
+
 def build():
     from . import build_ext
     return build_ext.build()
@@ -124,6 +180,15 @@ def lib():
         "amsim_dwconv2d_workspace_size": ([ctypes.POINTER(ConvDesc), i32, vp], sz),
         "amsim_softmax_rows": ([vp, vp, i64, i32, vp], i32),
         "amsim_softmax_rows_backward": ([vp, vp, vp, i64, i32, vp], i32),
+        "amsim_block_norm_fwd": ([ctypes.POINTER(BlockNormDesc)] + [vp] * 10, i32),
+        "amsim_block_norm_bwd": ([ctypes.POINTER(BlockNormDesc)] + [vp] * 15 + [sz, vp], i32),
+        "amsim_block_norm_workspace_size": ([ctypes.POINTER(BlockNormDesc)], sz),
+        "amsim_vocab_loss": ([ctypes.POINTER(VocabLossDesc)] + [vp] * 8 + [sz, vp], i32),
+        "amsim_vocab_loss_grad": ([ctypes.POINTER(VocabLossDesc)] + [vp] * 10 + [sz, vp], i32),
+        "amsim_vocab_loss_workspace_size": ([ctypes.POINTER(VocabLossDesc), i32], sz),
+        "amsim_vocab_loss_workspace_min": ([ctypes.POINTER(VocabLossDesc), i32], sz),
+        "amsim_adamw_step": ([i32, ctypes.POINTER(AdamwTensor), ctypes.POINTER(AdamwHyper), vp], i32),
+        "amsim_adamw_moment_values": ([vp, vp, i32, i64, vp, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -475,6 +540,62 @@ def amsim_softmax_rows(S, P, rows, cols, stream=None):
                                                           _stream(stream)))
 
 
+def amsim_block_norm_fwd(desc: BlockNormDesc, x, y, gate, w_post, w_pre, r, n, rstd_post, rstd_pre, stream=None):
+    _check("amsim_block_norm_fwd",
+           lib().amsim_block_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre),
+                                      _ptr(r), _ptr(n), _ptr(rstd_post), _ptr(rstd_pre), _stream(stream)))
+
+
+def amsim_block_norm_bwd(desc: BlockNormDesc, dr, dn, r, y, gate, w_post, w_pre, rstd_post, rstd_pre, dx, dy, dgate,
+                         dw_post, dw_pre, ws=None, ws_bytes=None, stream=None):
+    ws_bytes = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check("amsim_block_norm_bwd",
+           lib().amsim_block_norm_bwd(ctypes.byref(desc), _ptr(dr), _ptr(dn), _ptr(r), _ptr(y), _ptr(gate),
+                                      _ptr(w_post), _ptr(w_pre), _ptr(rstd_post), _ptr(rstd_pre), _ptr(dx), _ptr(dy),
+                                      _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(ws), ws_bytes,
+                                      _stream(stream)))
+
+
+def amsim_block_norm_workspace_size(desc: BlockNormDesc) -> int:
+    return int(lib().amsim_block_norm_workspace_size(ctypes.byref(desc)))
+
+
+def amsim_vocab_loss(desc: VocabLossDesc, h, w, targets, row_weight, loss, row_loss, lse, ws=None, ws_bytes=None,
+                     stream=None):
+    ws_bytes = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check("amsim_vocab_loss",
+           lib().amsim_vocab_loss(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(targets), _ptr(row_weight), _ptr(loss),
+                                  _ptr(row_loss), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def amsim_vocab_loss_grad(desc: VocabLossDesc, h, w, targets, row_weight, loss, row_loss, lse, dh, dw, ws=None,
+                          ws_bytes=None, stream=None):
+    ws_bytes = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check("amsim_vocab_loss_grad",
+           lib().amsim_vocab_loss_grad(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(targets), _ptr(row_weight),
+                                       _ptr(loss), _ptr(row_loss), _ptr(lse), _ptr(dh), _ptr(dw), _ptr(ws), ws_bytes,
+                                       _stream(stream)))
+
+
+def amsim_vocab_loss_workspace_size(desc: VocabLossDesc, which: int) -> int:
+    return int(lib().amsim_vocab_loss_workspace_size(ctypes.byref(desc), int(which)))
+
+
+def amsim_vocab_loss_workspace_min(desc: VocabLossDesc, which: int) -> int:
+    return int(lib().amsim_vocab_loss_workspace_min(ctypes.byref(desc), int(which)))
+
+
+def amsim_adamw_step(tensors, hyper: AdamwHyper, stream=None):
+    """tensors: a ctypes array of AdamwTensor (adamw_table)."""
+    _check("amsim_adamw_step", lib().amsim_adamw_step(len(tensors), tensors, ctypes.byref(hyper), _stream(stream)))
+
+
+def amsim_adamw_moment_values(codes, scales, second: bool, n: int, out, stream=None):
+    _check("amsim_adamw_moment_values",
+           lib().amsim_adamw_moment_values(_ptr(codes), _ptr(scales), 1 if second else 0, int(n), _ptr(out),
+                                           _stream(stream)))
+
+
 # ------------------------------------------------------------------ conveniences (still marshalling only)
 def workspace(nbytes: int, device=None):
     """A caller-owned scratch buffer (uint8 torch tensor, 256-byte aligned by the caching allocator)."""
@@ -496,3 +617,170 @@ def gemm(A, B, lut, *, transA=False, transB=False, alpha=1.0, beta=0.0, C=None, 
     amsim_gemm("T" if transA else "N", "T" if transB else "N", m, n, k, alpha, A, max(1, A.shape[1]), B,
                max(1, B.shape[1]), beta, C, max(1, n), lut, ws=ws, stream=stream)
     return C
+
+
+def _dtype(t) -> int:
+    """amsim_dtype of a tensor (or of a torch dtype)."""
+    import torch
+    dtype = getattr(t, "dtype", t)
+    if dtype == torch.float32:
+        return AMSIM_F32
+    if dtype == torch.bfloat16:
+        return AMSIM_BF16
+    raise TypeError(f"exact operators take fp32 or bf16 tensors, not {dtype}")
+
+
+def _rows(name, t, rows, cols, dtype=None) -> int:
+    """Row stride of a CUDA matrix of `rows` x `cols` whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {rows} x {cols}, not {tuple(t.shape)}")
+    if not t.is_cuda or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be a CUDA tensor{'' if dtype is None else ' of ' + str(dtype)}")
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _vector(name, t, n, dtype):
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous values")
+
+
+def _block_norm_desc(first, y, gate, w_post, w_pre, alpha, eps):
+    """Descriptor of a block norm over rows like `first`'s, its vectors checked."""
+    import torch
+    if first.dim() != 2:
+        raise ValueError("block norms take matrices of rows x channels")
+    rows, cols = first.shape
+    d = BlockNormDesc(rows=rows, cols=cols, alpha=alpha, eps=eps)
+    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
+        if t is not None:
+            _vector(name, t, cols, torch.float32)
+    if gate is not None:
+        groups = gate.numel() // cols
+        _vector("gate", gate, max(1, groups) * cols, torch.float32)
+        if groups < 1 or rows % groups:
+            raise ValueError(f"gate must have one row of {cols} values for every so many of the {rows} rows")
+        d.gate_rows = rows // groups
+    return d
+
+
+def block_norm(x, y=None, w_post=None, w_pre=None, *, gate=None, alpha=1.0, eps=1e-6, n_dtype=None):
+    """r = x + alpha gate rms_norm(y) w_post and n = rms_norm(r) w_pre: (r, n, rstd_post, rstd_pre).
+
+    x: rows x channels, fp32 or bf16; y the same shape (or None: r is x itself); w_post None: y enters as it is;
+    gate: [groups, channels], one row for each rows / groups consecutive rows, or None.  n has type `n_dtype` (y's,
+    or x's).  rstd_post is None without w_post."""
+    import torch
+    d = _block_norm_desc(x, y, gate, w_post, w_pre, alpha, eps)
+    rows, cols = x.shape
+    d.x_type, d.ldx = _dtype(x), _rows("x", x, rows, cols)
+    if y is not None:
+        d.y_type, d.ldy = _dtype(y), _rows("y", y, rows, cols)
+    n = torch.empty((rows, cols), dtype=n_dtype or (x if y is None else y).dtype, device=x.device)
+    d.n_type = _dtype(n)
+    r = x if y is None else torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    rstd_pre = torch.empty(rows, dtype=torch.float32, device=x.device)
+    rstd_post = None if w_post is None else torch.empty_like(rstd_pre)
+    amsim_block_norm_fwd(d, x, y, gate, w_post, w_pre, None if y is None else r, n, rstd_post, rstd_pre)
+    return r, n, rstd_post, rstd_pre
+
+
+def block_norm_backward(dr, dn, r, y, w_post, w_pre, rstd_post, rstd_pre, *, gate=None, alpha=1.0):
+    """Gradients of block_norm: (dx, dy, dgate, dw_post, dw_pre), None where there was no such input.  dr or dn may
+    be None (zeros); r, rstd_post and rstd_pre are block_norm's."""
+    import torch
+    d = _block_norm_desc(r, y, gate, w_post, w_pre, alpha, 0.0)
+    rows, cols = r.shape
+    d.x_type, d.ldr = _dtype(r), _rows("r", r, rows, cols)
+    if dr is not None:
+        d.lddr = _rows("dr", dr, rows, cols, r.dtype)
+    if dn is not None:
+        d.n_type, d.lddn = _dtype(dn), _rows("dn", dn, rows, cols)
+        _vector("rstd_pre", rstd_pre, rows, torch.float32)
+    dx = torch.empty((rows, cols), dtype=r.dtype, device=r.device)
+    dy = dgate = dw_post = dw_pre = None
+    if y is not None:
+        d.y_type, d.ldy = _dtype(y), _rows("y", y, rows, cols)
+        dy = torch.empty((rows, cols), dtype=y.dtype, device=r.device)
+    if gate is not None:
+        dgate = torch.empty_like(gate)
+    if w_post is not None:
+        _vector("rstd_post", rstd_post, rows, torch.float32)
+        dw_post = torch.empty_like(w_post)
+    if w_pre is not None:
+        dw_pre = torch.empty_like(w_pre) if dn is not None else torch.zeros_like(w_pre)
+    nb = amsim_block_norm_workspace_size(d)
+    ws = workspace(nb, r.device) if nb else None
+    amsim_block_norm_bwd(d, dr, dn, r, y, gate, w_post, w_pre, rstd_post, rstd_pre, dx, dy, dgate, dw_post,
+                         dw_pre if dn is not None else None, ws=ws)
+    return dx, dy, dgate, dw_post, dw_pre
+
+
+def _vocab_desc(h, w, targets, row_weight, ignore_index, reduction):
+    import torch
+    if h.dim() != 2 or w.dim() != 2:
+        raise ValueError("the vocabulary loss takes h [tokens, dim] and w [vocab, dim]")
+    tokens, dim = h.shape
+    d = VocabLossDesc(tokens=tokens, vocab=w.shape[0], dim=dim, ignore_index=ignore_index,
+                      reduction=REDUCTIONS[reduction])
+    d.ld_h = _rows("h", h, tokens, dim, torch.bfloat16)
+    d.ld_w = _rows("w", w, w.shape[0], dim, torch.bfloat16)
+    _vector("targets", targets, tokens, torch.int64)
+    if row_weight is not None:
+        _vector("row_weight", row_weight, tokens, torch.float32)
+    return d
+
+
+def vocab_loss(h, w, targets, *, row_weight=None, ignore_index=-100, reduction="mean"):
+    """Cross entropy of softmax(h w^T) against the targets, without the logits: (loss [1], row_loss, lse).
+    h [tokens, dim] and w [vocab, dim] bf16, targets int64; reduction "mean" (over the tokens' weights) or "sum"."""
+    import torch
+    d = _vocab_desc(h, w, targets, row_weight, ignore_index, reduction)
+    out = torch.empty((2, d.tokens), dtype=torch.float32, device=h.device)
+    loss = torch.empty(1, dtype=torch.float32, device=h.device)
+    ws = workspace(amsim_vocab_loss_workspace_size(d, 0), h.device)
+    amsim_vocab_loss(d, h, w, targets, row_weight, loss, out[0], out[1], ws=ws)
+    return loss, out[0], out[1]
+
+
+def vocab_loss_grad(h, w, targets, *, row_weight=None, ignore_index=-100, reduction="mean"):
+    """vocab_loss and the loss's gradients: (loss, row_loss, lse, dh, dw), dh and dw bf16."""
+    import torch
+    d = _vocab_desc(h, w, targets, row_weight, ignore_index, reduction)
+    out = torch.empty((2, d.tokens), dtype=torch.float32, device=h.device)
+    loss = torch.empty(1, dtype=torch.float32, device=h.device)
+    dh = torch.empty((d.tokens, d.dim), dtype=torch.bfloat16, device=h.device)
+    dw = torch.empty((d.vocab, d.dim), dtype=torch.bfloat16, device=h.device)
+    ws = workspace(amsim_vocab_loss_workspace_size(d, 1), h.device)
+    amsim_vocab_loss_grad(d, h, w, targets, row_weight, loss, out[0], out[1], dh, dw, ws=ws)
+    return loss, out[0], out[1], dh, dw
+
+
+def adamw_table(tensors):
+    """The table adamw_step takes, from AdamwTensor entries; it holds their addresses only."""
+    tensors = list(tensors)
+    return (AdamwTensor * len(tensors))(*tensors)
+
+
+def adamw_step(table, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, step, grad_scale=None):
+    """One AdamW step over a table of tensors; `step` counts from 1, grad_scale is one fp32 CUDA value or None."""
+    if grad_scale is not None:
+        import torch
+        _vector("grad_scale", grad_scale, 1, torch.float32)
+    amsim_adamw_step(table, AdamwHyper(lr, beta1, beta2, eps, step, _ptr(grad_scale)))
+
+
+def adamw_moment_values(codes, scales):
+    """fp32 values of an 8-bit moment's codes (int8: first moment, uint8: second), in the codes' shape."""
+    import torch
+    n = codes.numel()
+    if codes.dtype not in (torch.int8, torch.uint8):
+        raise TypeError("moment codes are int8 (first moment) or uint8 (second)")
+    _vector("codes", codes, n, codes.dtype)
+    _vector("scales", scales, -(-n // AMSIM_ADAMW_BLOCK), torch.float32)
+    out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
+    amsim_adamw_moment_values(codes, scales, codes.dtype == torch.uint8, n, out)
+    return out

@@ -1,0 +1,848 @@
+// Softmax cross entropy over a large vocabulary without keeping the logits,
+// with the gradients of the hidden states and of the vocabulary weights.
+//
+// z = h W^T (tokens x vocab) is computed tile by tile on the tensor cores and
+// reduced where it is computed: each row of a 128-column piece leaves its
+// maximum and its sum of exponentials, from which a merge makes lse and the
+// loss.  For the gradients the piece also leaves 16 bits per logit, the
+// distance to the piece's maximum in steps of 2^-11 (a relative error of the
+// probability of at most 2^-12, a sixteenth of a bf16 rounding): half the traffic of fp32
+// logits, and no second h W^T product.  A pass over them writes
+// G = exp(z - lse) - onehot in bf16 in place, and two more products give
+// dh = G W and dW = G^T h.
+//
+// All three products run in one kernel: bf16 operands copied by TMA into
+// 128-byte swizzled tiles, tcgen05 matrix instructions of 128 x 256 x 16 by
+// one thread, two fp32 accumulators in tensor memory, so that eight warps
+// reduce or write one tile while the next is being computed.  dh and dW read
+// G, W and h as they lie in memory: an operand whose rows run along M or N
+// instead of K only changes its descriptor.
+#include <algorithm>
+
+#include "tensor_core.cuh"
+
+namespace {
+
+using namespace amsim;
+using bf16 = __nv_bfloat16;
+
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+constexpr int kPiece = 128;                        // columns that share a maximum
+constexpr int kStages = 4;
+constexpr int kStageA = kTileM * kTileK * 2, kStageB = kTileN * kTileK * 2;
+constexpr int kStage = kStageA + kStageB;          // 48 KB
+constexpr int kBox = 64;                           // elements of a 128-byte row
+constexpr int kFirstEpilogueWarp = 2;              // after the copy and the matrix warp
+constexpr int kThreads = (kFirstEpilogueWarp + 8) * 32;
+constexpr int kSmem = kStages * kStage + 1024 + 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSteps = 2048.0f;                  // code steps per unit of the logit
+
+enum Product { kLogits = 0, kDh = 1, kDw = 2 };
+
+// Steps of the reduction that one accumulator takes before it is handed over.
+// The tensor cores add with truncation: each of the additions of 16 products
+// pulls a sum towards zero, and over 4096 products a logit came out 2e-6 low
+// (relative), which lse and the loss inherit.  So logits are handed over every
+// 1024 products and added with rounding in registers (3e-7, as at a width of
+// 1024); dh and dw, rounded to bf16, take their whole reduction in one.
+template <int PRODUCT>
+constexpr int kSegment = PRODUCT == kLogits ? 16 : 0x7FFFFFFF;
+
+struct ProductParams {
+    int m, n, kblocks;              // rows, columns, steps of 64 of the reduction
+    int mt, nt, splits, per_split;  // tiles, parts of the reduction and their steps
+    int group;                      // row tiles visited together
+    // kLogits
+    const int64_t *targets;         // of the chunk's rows
+    float *target_logit;
+    float2 *stats;                  // [piece][rows]: maximum, sum of exponentials
+    uint16_t *codes;                // [rows][ld_codes], or null
+    long long ld_codes;
+    // kDh, kDw
+    bf16 *out;
+    long long ld_out;
+    int vec;                        // out takes 16-byte stores
+    const float *scale;             // 1 / A
+    float *acc;                     // fp32 sums of earlier chunks (kDw) or the splits' sums (kDh)
+    int acc_read, acc_write;
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// a = b where i == j.  A chain of these picks one of many registers; written
+// in C, the compiler indexes a copy of them in local memory instead.
+__device__ __forceinline__ void select_if(float &a, float b, int i, int j)
+{
+    asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\tselp.f32 %0, %1, %0, p;\n\t}" : "+f"(a) : "f"(b), "r"(i), "r"(j));
+}
+
+struct Tile {
+    int m, n, split;
+};
+// Tiles in the order they are taken: `group` row tiles by every column tile,
+// so that a wave of CTAs reads few distinct operand tiles.
+__device__ __forceinline__ Tile tile_at(const ProductParams &p, int i)
+{
+    Tile t;
+    const int per = p.mt * p.nt;
+    t.split = i / per;
+    i -= t.split * per;
+    const int full = p.group * p.nt, g = i / full, m0 = g * p.group;
+    const int rows = min(p.group, p.mt - m0);
+    i -= g * full;
+    t.n = i / rows;
+    t.m = m0 + i - t.n * rows;
+    return t;
+}
+
+// One 128-column piece of a row of logits, in the registers of its thread.
+// fmaxf skips NaN; the sum does not, so a NaN logit makes the row's lse NaN.
+template <bool MASKED>
+__device__ __forceinline__ void reduce_piece(const ProductParams &p, const float (&z)[kPiece], int row, int col0)
+{
+    if (row >= p.m) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j)
+        if (!MASKED || col0 + j < p.n) top = fmaxf(top, z[j]);
+    const float shift = top == -INFINITY ? 0.0f : top * kLog2e;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j)
+        if (!MASKED || col0 + j < p.n) sum[j & 3] += exp2_fast(fmaf(z[j], kLog2e, -shift));
+    p.stats[(long long)(col0 / kPiece) * p.m + row] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    const long long d = p.targets[row] - col0;
+    if (d >= 0 && d < kPiece && col0 + d < p.n) {
+        float pick = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) select_if(pick, z[j], (int)d, j);
+        p.target_logit[row] = pick;
+    }
+    if (!p.codes) return;
+    uint16_t *dst = p.codes + row * p.ld_codes + col0;
+#pragma unroll
+    for (int j = 0; j < kPiece / 8; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = __float2uint_rn(fminf((top - z[8 * j + 2 * e]) * kSteps, 65535.0f)) |
+                   __float2uint_rn(fminf((top - z[8 * j + 2 * e + 1]) * kSteps, 65535.0f)) << 16;
+        if (!MASKED || col0 + j * 8 < p.n)
+            *reinterpret_cast<uint4 *>(dst + j * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// 32 columns of a row: added to the fp32 sums, or scaled, rounded and written.
+__device__ __forceinline__ void store_chunk(const ProductParams &p, const uint32_t (&r)[32], int row, int col, int split,
+                                            float scale)
+{
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+    if (p.acc) {
+        float *acc = p.acc + ((long long)split * p.m + row) * p.n + col;
+        const int left = min(32, p.n - col);
+        if (p.acc_read) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < left) v[j] += acc[j];
+        }
+        if (p.acc_write) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < left) acc[j] = v[j];
+            return;
+        }
+    }
+    bf16 *dst = p.out + row * p.ld_out + col;
+    if (p.vec) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (col + j * 8 < p.n)
+                *reinterpret_cast<uint4 *>(dst + j * 8) =
+                    make_uint4(pack2(v[8 * j] * scale, v[8 * j + 1] * scale),
+                               pack2(v[8 * j + 2] * scale, v[8 * j + 3] * scale),
+                               pack2(v[8 * j + 4] * scale, v[8 * j + 5] * scale),
+                               pack2(v[8 * j + 6] * scale, v[8 * j + 7] * scale));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (col + j < p.n) dst[j] = __float2bfloat16_rn(v[j] * scale);
+    }
+}
+
+__device__ __forceinline__ void store_piece(const ProductParams &p, uint32_t tmem, int row, int col0, int split)
+{
+    uint32_t r[32];
+    const bool on = row < p.m;
+    const float scale = p.out ? *p.scale : 1.0f;
+#pragma unroll
+    for (int c = 0; c < kPiece / 32; ++c) {
+        tc::tmem_load32(tmem + c * 32, r);
+        tc::tmem_load_wait(r);
+        const int col = col0 + c * 32;
+        if (on && col < p.n) store_chunk(p, r, row, col, split, scale);
+    }
+}
+
+template <int PRODUCT>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const ProductParams p, const __grid_constant__ CUtensorMap amap,
+                   const __grid_constant__ CUtensorMap bmap)
+{
+    constexpr bool a_mn = PRODUCT == kDw, b_mn = PRODUCT != kLogits;
+    extern __shared__ uint8_t raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + kStages * kStage);
+    uint64_t *empty = full + kStages, *ready = empty + kStages, *taken = ready + 2, *drained = taken + 2;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(drained + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0 && lane == 0) {
+        tc::prefetch_map(&amap);
+        tc::prefetch_map(&bmap);
+        for (int i = 0; i < kStages; ++i) {
+            tc::bar_init(full + i, 1);
+            tc::bar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(ready + i, 1);
+            tc::bar_init(taken + i, 8 * 32);
+        }
+        tc::bar_init(drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tc::tmem_alloc<512>(slot);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *slot;
+    const int tiles = p.mt * p.nt * p.splits;
+    bool aborted = false;
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t phase = 0;
+            long long issued = 0;
+            for (int i = blockIdx.x; i < tiles && !aborted; i += gridDim.x) {
+                const Tile t = tile_at(p, i);
+                const int m0 = t.m * kTileM, n0 = t.n * kTileN;
+                const int k1 = min(p.kblocks, (t.split + 1) * p.per_split);
+                for (int k = t.split * p.per_split; k < k1; ++k) {
+                    if (!tc::bar_wait(empty + s, phase ^ 1, aborted)) break;
+                    uint8_t *a = ring + s * kStage, *b = a + kStageA;
+                    tc::bar_expect(full + s, kStage);
+                    if constexpr (a_mn) {
+#pragma unroll
+                        for (int j = 0; j < kTileM / kBox; ++j)
+                            tc::load_box(a + j * kBox * kTileK * 2, &amap, m0 + j * kBox, k * kTileK, full + s);
+                    } else {
+                        tc::load_box(a, &amap, k * kTileK, m0, full + s);
+                    }
+                    if constexpr (b_mn) {
+#pragma unroll
+                        for (int j = 0; j < kTileN / kBox; ++j)
+                            tc::load_box(b + j * kBox * kTileK * 2, &bmap, n0 + j * kBox, k * kTileK, full + s);
+                    } else {
+                        tc::load_box(b, &bmap, k * kTileK, n0, full + s);
+                    }
+                    ++issued;
+                    if (++s == kStages) { s = 0; phase ^= 1; }
+                }
+            }
+            if (aborted) {      // copies still in flight land before the CTA's memory goes away
+                bool gave_up = false;
+                for (long long j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
+                    tc::bar_wait(full + j % kStages, (uint32_t)(j / kStages & 1), gave_up);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = tc::instr_desc(kTileM, kTileN, a_mn, b_mn);
+            int s = 0;
+            uint32_t phase = 0, count = 0;
+            for (int i = blockIdx.x; i < tiles && !aborted; i += gridDim.x) {
+                const Tile t = tile_at(p, i);
+                const int k0 = t.split * p.per_split, k1 = min(p.kblocks, (t.split + 1) * p.per_split);
+                uint32_t half = 0, d = 0;
+                for (int k = k0; k < k1; ++k) {
+                    const bool fresh = (k - k0) % kSegment<PRODUCT> == 0;
+                    if (fresh) {
+                        half = count & 1;
+                        if (!tc::bar_wait(taken + half, (count >> 1 & 1) ^ 1, aborted)) break;
+                        tc::fence_after();
+                        d = tmem + half * kTileN;
+                        ++count;
+                    }
+                    if (!tc::bar_wait(full + s, phase, aborted)) break;
+                    tc::fence_after();
+                    const uint32_t a = tc::smem_addr(ring + s * kStage), b = a + kStageA;
+#pragma unroll
+                    for (int j = 0; j < kTileK / 16; ++j) {
+                        const uint64_t ad = a_mn ? tc::operand_desc(a + j * 2048, kBox * kTileK * 2, 1024)
+                                                 : tc::operand_desc(a + j * 32, 16, 1024);
+                        const uint64_t bd = b_mn ? tc::operand_desc(b + j * 2048, kBox * kTileK * 2, 1024)
+                                                 : tc::operand_desc(b + j * 32, 16, 1024);
+                        tc::mma(d, ad, bd, idesc, !fresh || j > 0);
+                    }
+                    tc::mma_commit(empty + s);
+                    if (++s == kStages) { s = 0; phase ^= 1; }
+                    if (k + 1 == k1 || (k + 1 - k0) % kSegment<PRODUCT> == 0) tc::mma_commit(ready + half);
+                }
+            }
+            if (aborted) {      // instructions still running finish before the memory goes away
+                bool gave_up = false;
+                tc::mma_commit(drained);
+                tc::bar_wait(drained, 0, gave_up);
+            }
+        }
+    } else {
+        // the first four of these warps take columns [0, 128) of a tile, the
+        // others the rest; a warp reads the 32 rows of tensor memory that its
+        // number modulo 4 allows
+        const int part = (warp - kFirstEpilogueWarp) >> 2, quarter = warp & 3;
+        uint32_t count = 0;
+        // the next accumulator is complete; every lane waits, and the warp goes on together
+        auto next = [&](uint32_t &addr, uint32_t &half) {
+            half = count & 1;
+            const bool ok = tc::bar_wait(ready + half, count >> 1 & 1, aborted);
+            ++count;
+            tc::fence_after();
+            addr = tmem + half * kTileN + part * kPiece + ((uint32_t)quarter * 32 << 16);
+            return __all_sync(0xFFFFFFFFu, ok) != 0;
+        };
+        for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
+            const Tile t = tile_at(p, i);
+            const int row = t.m * kTileM + quarter * 32 + lane, col0 = t.n * kTileN + part * kPiece;
+            uint32_t addr, half;
+            if constexpr (PRODUCT == kLogits) {
+                float z[kPiece];
+                bool ok = true;
+                for (int k = 0; k < p.kblocks; k += kSegment<PRODUCT>) {
+                    if (!(ok = next(addr, half))) break;
+#pragma unroll
+                    for (int c = 0; c < kPiece / 32; ++c) {
+                        uint32_t r[32];
+                        tc::tmem_load32(addr + c * 32, r);
+                        tc::tmem_load_wait(r);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float x = __uint_as_float(r[j]);
+                            z[c * 32 + j] = k ? z[c * 32 + j] + x : x;
+                        }
+                    }
+                    tc::fence_before();
+                    tc::bar_arrive(taken + half);
+                }
+                if (!ok) break;
+                if (col0 + kPiece <= p.n) reduce_piece<false>(p, z, row, col0);
+                else if (col0 < p.n) reduce_piece<true>(p, z, row, col0);
+            } else {
+                if (!next(addr, half)) break;
+                if (col0 < p.n) store_piece(p, addr, row, col0, t.split);
+                tc::fence_before();
+                tc::bar_arrive(taken + half);
+            }
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 1) tc::tmem_free<512>(tmem);
+}
+
+// ------------------------------------------------------------------ losses
+// What the row kernels share over a call.
+struct Totals {
+    unsigned int done;       // blocks of the merge that have finished
+    float scale;             // 1 / A
+    double loss;             // sum of weight * row loss of the chunks so far
+};
+
+struct MergeParams {
+    const float2 *stats;
+    const float *target_logit;
+    const int64_t *targets;       // of the chunk
+    const int64_t *all_targets;
+    const float *row_weight;      // of all tokens, or null
+    float *row_loss, *lse;        // of the chunk (scratch when the caller wants none)
+    float *weight;                // of the chunk: the weight of a token that counts and has a valid target, else 0
+    float *loss;
+    Totals *totals;
+    long long tokens, first, ignore;   // all tokens, the chunk's first
+    int rows, pieces, vocab, mean;
+    int first_chunk, last_chunk;
+};
+
+__device__ __forceinline__ double block_total(double x, double *red)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.0;
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) x += red[i];
+    return x;
+}
+
+// lse and loss of each row from its pieces (lane by lane over the rows, so
+// that a warp reads neighbouring rows); the last block adds the losses.
+constexpr int kMergeThreads = 256, kMergeRows = 32;
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p)
+{
+    __shared__ float2 part[kMergeThreads / 32][kMergeRows];
+    __shared__ double red[kMergeThreads / 32];
+    __shared__ bool last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x * kMergeRows + lane;
+    float top = -INFINITY, sum = 0.0f;
+    if (row < p.rows) {
+        for (int i = warp; i < p.pieces; i += kMergeThreads / 32) {
+            const float2 s = p.stats[(long long)i * p.rows + row];
+            const float t = fmaxf(top, s.x);
+            if (t != -INFINITY) {
+                sum = sum * exp2_fast((top - t) * kLog2e) + s.y * exp2_fast((s.x - t) * kLog2e);
+                top = t;
+            } else {
+                sum += s.y;                // a row of -inf or NaN logits
+            }
+        }
+    }
+    part[warp][lane] = make_float2(top, sum);
+    __syncthreads();
+    if (warp == 0 && row < p.rows) {
+        for (int i = 1; i < kMergeThreads / 32; ++i) {
+            const float2 s = part[i][lane];
+            const float t = fmaxf(top, s.x);
+            if (t != -INFINITY) {
+                sum = sum * exp2_fast((top - t) * kLog2e) + s.y * exp2_fast((s.x - t) * kLog2e);
+                top = t;
+            } else {
+                sum += s.y;
+            }
+        }
+        const float lse = top + logf(sum);
+        const long long target = p.targets[row];
+        const bool counts = target != p.ignore, valid = target >= 0 && target < p.vocab;
+        p.lse[row] = lse;
+        p.row_loss[row] = !counts ? 0.0f : valid ? lse - p.target_logit[row] : __uint_as_float(0x7FC00000u);
+        p.weight[row] = !counts || !valid ? 0.0f : p.row_weight ? p.row_weight[p.first + row] : 1.0f;
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(&p.totals->done, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double loss = 0.0, weight = 0.0;
+    for (int i = threadIdx.x; i < p.rows; i += kMergeThreads)
+        if (p.targets[i] != p.ignore)
+            loss += (double)(p.row_weight ? p.row_weight[p.first + i] : 1.0f) * (double)__ldcg(p.row_loss + i);
+    loss = block_total(loss, red);
+    if (p.mean && p.first_chunk) {
+        for (long long i = threadIdx.x; i < p.tokens; i += kMergeThreads)
+            if (p.all_targets[i] != p.ignore) weight += p.row_weight ? (double)p.row_weight[i] : 1.0;
+        weight = block_total(weight, red);
+    }
+    if (threadIdx.x == 0) {
+        Totals *t = p.totals;
+        if (p.first_chunk) t->scale = !p.mean ? 1.0f : weight != 0.0 ? (float)(1.0 / weight) : 0.0f;
+        else loss += t->loss;
+        t->loss = loss;
+        t->done = 0;
+        if (p.last_chunk) *p.loss = (float)(loss * (double)t->scale);
+    }
+}
+
+// Codes to G, in place: G = weight (exp(top - lse - code / 2048) - [col == target]).
+struct GradParams {
+    uint16_t *codes;
+    const float2 *stats;
+    const float *lse, *weight;
+    const int64_t *targets;
+    long long ld;
+    int rows, vocab;
+};
+constexpr int kGradThreads = 256;
+__global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
+{
+    const int row = blockIdx.y;
+    const int col = ((int)blockIdx.x * kGradThreads + (int)threadIdx.x) * 8;
+    if (col >= p.vocab) return;
+    const float w = p.weight[row];
+    uint4 *at = reinterpret_cast<uint4 *>(p.codes + row * p.ld + col);
+    if (w == 0.0f) {
+        *at = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const float top = p.stats[(long long)(col / kPiece) * p.rows + row].x;
+    const float base = (top - p.lse[row]) * kLog2e;
+    const long long d = p.targets[row] - col;
+    const uint4 q = *at;
+    const uint32_t c[4] = {q.x, q.y, q.z, q.w};
+    float g[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t code = j & 1 ? c[j >> 1] >> 16 : c[j >> 1] & 0xFFFFu;
+        g[j] = code == 65535u ? 0.0f : exp2_fast(fmaf((float)code, -kLog2e / kSteps, base));
+        if (d == j) g[j] -= 1.0f;
+        g[j] *= w;
+    }
+    *at = make_uint4(pack2(g[0], g[1]), pack2(g[2], g[3]), pack2(g[4], g[5]), pack2(g[6], g[7]));
+}
+
+// dh of a row range from the splits' sums, in split order.
+__global__ void __launch_bounds__(256) join_kernel(const float *acc, int splits, long long rows, int cols,
+                                                   const float *scale, bf16 *out, long long ld)
+{
+    const long long n = rows * cols;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        float s = 0.0f;
+        for (int k = 0; k < splits; ++k) s += acc[k * n + i];
+        out[i / cols * ld + i % cols] = __float2bfloat16_rn(s * *scale);
+    }
+}
+
+// An operand whose rows TMA cannot take (base or row stride not a multiple of
+// 16 bytes) is copied into rows that it can.
+__global__ void __launch_bounds__(256) pack_kernel(const bf16 *src, long long ld, bf16 *dst, long long ld_dst,
+                                                   long long rows, int cols)
+{
+    const long long n = rows * cols;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256)
+        dst[i / cols * ld_dst + i % cols] = src[i / cols * ld + i % cols];
+}
+
+__global__ void zero_loss_kernel(float *loss) { *loss = 0.0f; }
+
+// ------------------------------------------------------------------ host
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+long long up8(long long x) { return (x + 7) & ~7LL; }
+
+int launched()
+{
+    const int rc = cuda_status(cudaGetLastError());
+    if (rc == AMSIM_OK) count_launch();
+    return rc;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Map of a bf16 matrix, `inner` contiguous elements by `outer` rows of stride
+// `ld`; boxes of 64 x `box` elements, zeros outside.
+int matrix_map(CUtensorMap *map, const void *base, long long inner, long long outer, long long ld, int box)
+{
+    static const EncodeTiled encode = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
+    if (!encode) return AMSIM_EUNSUPPORTED;
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t boxes[2] = {(cuuint32_t)kBox, (cuuint32_t)box}, ones[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, boxes, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? AMSIM_OK
+               : AMSIM_EUNSUPPORTED;
+}
+
+struct Matrix {
+    const bf16 *p;
+    long long ld;
+};
+
+int check(const amsim_vocab_loss_desc *d)
+{
+    if (!d || d->tokens < 0 || d->tokens > (int64_t)1 << 40 || d->vocab < 1 || d->vocab > 0x7FFFFF00 || d->dim < 1 ||
+        d->dim > 0x7FFFFF00)
+        return AMSIM_EINVAL;
+    for (int64_t ld : {d->ld_h, d->ld_w, d->ld_dh, d->ld_dw})
+        if (ld != 0 && (ld < d->dim || ld > (int64_t)1 << 38)) return AMSIM_EINVAL;
+    if (d->reduction != AMSIM_REDUCE_MEAN && d->reduction != AMSIM_REDUCE_SUM) return AMSIM_EINVAL;
+    return AMSIM_OK;
+}
+
+int device_sms()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+        cudaGetLastError();
+        return 0;
+    }
+    return sms;
+}
+
+// Scratch of a call over chunks of `rows` tokens.
+struct Layout {
+    size_t totals, row_loss, lse, weight, target_logit, stats, codes, dw_acc, dh_acc, pack_h, pack_w, bytes;
+    long long ld_codes, ld_pack;
+    int dh_splits;
+};
+
+constexpr size_t kCodesCap = (size_t)4 << 30;
+constexpr long long kMostRows = 32768;         // of a chunk
+
+// Parts of dh's reduction over the vocabulary when its tiles do not fill the
+// GPU: each part's fp32 sums go to scratch and a join adds them.
+int dh_splits(long long rows, const amsim_vocab_loss_desc *d, int sms)
+{
+    const long long tiles = ((rows + kTileM - 1) / kTileM) * ((d->dim + kTileN - 1) / kTileN);
+    const int kblocks = (d->vocab + kTileK - 1) / kTileK;
+    if (tiles * 2 > sms) return 1;
+    return (int)std::max<long long>(1, std::min<long long>(sms / tiles, kblocks / 8));
+}
+
+Layout layout(const amsim_vocab_loss_desc *d, bool grad, long long rows, bool pack_h, bool pack_w, int sms)
+{
+    Layout l{};
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t r = at;
+        at += up256(n);
+        return r;
+    };
+    const long long pieces = (d->vocab + kPiece - 1) / kPiece;
+    l.totals = take(sizeof(Totals));
+    l.row_loss = take((size_t)rows * 4);
+    l.lse = take((size_t)rows * 4);
+    l.weight = take((size_t)rows * 4);
+    l.target_logit = take((size_t)rows * 4);
+    l.stats = take((size_t)pieces * rows * 8);
+    l.ld_pack = up8(d->dim);
+    l.ld_codes = up8(d->vocab);
+    l.dh_splits = 1;
+    if (grad) {
+        l.codes = take((size_t)rows * l.ld_codes * 2);
+        if (rows < d->tokens) l.dw_acc = take((size_t)d->vocab * d->dim * 4);
+        l.dh_splits = dh_splits(rows, d, sms);
+        if (l.dh_splits > 1) l.dh_acc = take((size_t)l.dh_splits * rows * d->dim * 4);
+    }
+    if (pack_h) l.pack_h = take((size_t)d->tokens * l.ld_pack * 2);
+    if (pack_w) l.pack_w = take((size_t)d->vocab * l.ld_pack * 2);
+    l.bytes = at;
+    return l;
+}
+
+bool tma_rows(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+long long full_rows(const amsim_vocab_loss_desc *d)
+{
+    long long rows = std::min<long long>(d->tokens, kMostRows);
+    const long long cap = (long long)(kCodesCap / ((size_t)up8(d->vocab) * 2));
+    if (rows > cap) rows = std::max<long long>(kTileM, cap / kTileM * kTileM);
+    return std::min<long long>(rows, d->tokens);
+}
+
+template <int PRODUCT>
+int launch_product(const ProductParams &p, const CUtensorMap &a, const CUtensorMap &b, int sms, cudaStream_t st)
+{
+    const cudaError_t attr =
+        cudaFuncSetAttribute(product_kernel<PRODUCT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (attr != cudaSuccess) return cuda_status(attr);
+    const long long tiles = (long long)p.mt * p.nt * p.splits;
+    if (tiles > 0x7FFFFFFFLL - sms) return AMSIM_EUNSUPPORTED;
+    const int grid = (int)std::min<long long>(tiles, sms);
+    product_kernel<PRODUCT><<<grid, kThreads, kSmem, st>>>(p, a, b);
+    return launched();
+}
+
+ProductParams product(long long m, long long n, long long k, int splits)
+{
+    ProductParams p{};
+    p.m = (int)m;
+    p.n = (int)n;
+    p.kblocks = (int)((k + kTileK - 1) / kTileK);
+    p.mt = (int)((m + kTileM - 1) / kTileM);
+    p.nt = (int)((n + kTileN - 1) / kTileN);
+    p.per_split = (p.kblocks + splits - 1) / splits;
+    p.splits = (p.kblocks + p.per_split - 1) / p.per_split;
+    p.group = 16;
+    return p;
+}
+
+int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w, const int64_t *targets,
+        const float *row_weight, float *loss, float *row_loss, float *lse, void *dh, void *dw, void *ws,
+        size_t ws_bytes, cudaStream_t st)
+{
+    int rc = check(d);
+    if (rc) return rc;
+    if (!loss || !w || !aligned(w, 2) || !aligned(loss, 4) || (grad && (!dw || !aligned(dw, 2)))) return AMSIM_EINVAL;
+    const long long ld_h = d->ld_h ? d->ld_h : d->dim, ld_w = d->ld_w ? d->ld_w : d->dim;
+    const long long ld_dh = d->ld_dh ? d->ld_dh : d->dim, ld_dw = d->ld_dw ? d->ld_dw : d->dim;
+    if (d->tokens == 0) {
+        if (grad && cudaMemset2DAsync(dw, (size_t)ld_dw * 2, 0, (size_t)d->dim * 2, (size_t)d->vocab, st) !=
+                        cudaSuccess) {
+            cudaGetLastError();
+            return AMSIM_ECUDA;
+        }
+        zero_loss_kernel<<<1, 1, 0, st>>>(loss);
+        return launched();
+    }
+    if (!h || !targets || !ws || !aligned(h, 2) || !aligned(targets, 8) || !aligned(row_weight, 4) ||
+        !aligned(row_loss, 4) || !aligned(lse, 4) || !aligned(ws, 256) || (grad && (!dh || !aligned(dh, 2))))
+        return AMSIM_EINVAL;
+    const int sms = device_sms();
+    if (!sms) return AMSIM_ECUDA;
+    const bool pack_h = !tma_rows(h, ld_h), pack_w = !tma_rows(w, ld_w);
+    long long rows = full_rows(d);
+    Layout l = layout(d, grad, rows, pack_h, pack_w, sms);
+    while (l.bytes > ws_bytes) {              // smaller chunks: whole row tiles, down to one
+        if (rows <= kTileM) return AMSIM_EINVAL;
+        rows = std::max<long long>(kTileM, (rows / 2 + kTileM - 1) / kTileM * kTileM);
+        l = layout(d, grad, rows, pack_h, pack_w, sms);
+    }
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    Totals *totals = reinterpret_cast<Totals *>(base + l.totals);
+    if (cudaMemsetAsync(totals, 0, sizeof(Totals), st) != cudaSuccess) {
+        cudaGetLastError();
+        return AMSIM_ECUDA;
+    }
+    Matrix H{static_cast<const bf16 *>(h), ld_h}, W{static_cast<const bf16 *>(w), ld_w};
+    auto pack = [&](Matrix &m, size_t off, long long n) {
+        bf16 *dst = reinterpret_cast<bf16 *>(base + off);
+        pack_kernel<<<(unsigned)std::min<long long>((n * d->dim + 1023) / 1024, sms * 8), 256, 0, st>>>(
+            m.p, m.ld, dst, l.ld_pack, n, d->dim);
+        m = Matrix{dst, l.ld_pack};
+        return launched();
+    };
+    if (pack_h && (rc = pack(H, l.pack_h, d->tokens))) return rc;
+    if (pack_w && (rc = pack(W, l.pack_w, d->vocab))) return rc;
+
+    uint16_t *codes = grad ? reinterpret_cast<uint16_t *>(base + l.codes) : nullptr;
+    const bf16 *g = reinterpret_cast<const bf16 *>(codes);
+    float2 *stats = reinterpret_cast<float2 *>(base + l.stats);
+    float *target_logit = reinterpret_cast<float *>(base + l.target_logit);
+    float *weight = reinterpret_cast<float *>(base + l.weight);
+    float *dw_acc = reinterpret_cast<float *>(base + l.dw_acc);
+    for (long long t0 = 0; t0 < d->tokens; t0 += rows) {
+        const long long n = std::min(rows, d->tokens - t0);
+        const bool first = t0 == 0, last = t0 + n == d->tokens;
+        CUtensorMap am, bm;
+        ProductParams p = product(n, d->vocab, d->dim, 1);
+        p.targets = targets + t0;
+        p.target_logit = target_logit;
+        p.stats = stats;
+        p.codes = codes;
+        p.ld_codes = l.ld_codes;
+        if ((rc = matrix_map(&am, H.p + t0 * H.ld, d->dim, n, H.ld, kTileM)) ||
+            (rc = matrix_map(&bm, W.p, d->dim, d->vocab, W.ld, kTileN)) ||
+            (rc = launch_product<kLogits>(p, am, bm, sms, st)))
+            return rc;
+        MergeParams q{};
+        q.stats = stats;
+        q.target_logit = target_logit;
+        q.targets = targets + t0;
+        q.all_targets = targets;
+        q.row_weight = row_weight;
+        q.row_loss = row_loss ? row_loss + t0 : reinterpret_cast<float *>(base + l.row_loss);
+        q.lse = lse ? lse + t0 : reinterpret_cast<float *>(base + l.lse);
+        q.weight = weight;
+        q.loss = loss;
+        q.totals = totals;
+        q.tokens = d->tokens;
+        q.first = t0;
+        q.ignore = d->ignore_index;
+        q.rows = (int)n;
+        q.pieces = (d->vocab + kPiece - 1) / kPiece;
+        q.vocab = d->vocab;
+        q.mean = d->reduction == AMSIM_REDUCE_MEAN;
+        q.first_chunk = first;
+        q.last_chunk = last;
+        merge_kernel<<<(unsigned)((n + kMergeRows - 1) / kMergeRows), kMergeThreads, 0, st>>>(q);
+        if ((rc = launched())) return rc;
+        if (!grad) continue;
+        GradParams e{codes, stats, q.lse, weight, targets + t0, l.ld_codes, (int)n, d->vocab};
+        grad_kernel<<<dim3((unsigned)((d->vocab + kGradThreads * 8 - 1) / (kGradThreads * 8)), (unsigned)n),
+                      kGradThreads, 0, st>>>(e);
+        if ((rc = launched())) return rc;
+        // dh = G W
+        p = product(n, d->dim, d->vocab, l.dh_splits);
+        bf16 *dh_out = static_cast<bf16 *>(dh) + t0 * ld_dh;
+        if (p.splits > 1) {
+            p.acc = reinterpret_cast<float *>(base + l.dh_acc);
+            p.acc_write = 1;
+        } else {
+            p.out = dh_out;
+            p.ld_out = ld_dh;
+            p.vec = tma_rows(dh_out, ld_dh) && d->dim % 8 == 0;
+        }
+        p.scale = &totals->scale;
+        if ((rc = matrix_map(&am, g, d->vocab, n, l.ld_codes, kTileM)) ||
+            (rc = matrix_map(&bm, W.p, d->dim, d->vocab, W.ld, kTileK)) ||
+            (rc = launch_product<kDh>(p, am, bm, sms, st)))
+            return rc;
+        if (p.splits > 1) {
+            join_kernel<<<(unsigned)std::min<long long>((n * d->dim + 255) / 256, sms * 8), 256, 0, st>>>(
+                p.acc, p.splits, n, d->dim, &totals->scale, dh_out, ld_dh);
+            if ((rc = launched())) return rc;
+        }
+        // dW = G^T h, over the chunks so far
+        p = product(d->vocab, d->dim, n, 1);
+        p.scale = &totals->scale;
+        if (!(first && last)) {
+            p.acc = dw_acc;
+            p.acc_read = !first;
+            p.acc_write = !last;
+        }
+        if (last) {
+            p.out = static_cast<bf16 *>(dw);
+            p.ld_out = ld_dw;
+            p.vec = tma_rows(dw, ld_dw) && d->dim % 8 == 0;
+        }
+        if ((rc = matrix_map(&am, g, d->vocab, n, l.ld_codes, kTileK)) ||
+            (rc = matrix_map(&bm, H.p + t0 * H.ld, d->dim, n, H.ld, kTileK)) ||
+            (rc = launch_product<kDw>(p, am, bm, sms, st)))
+            return rc;
+    }
+    return AMSIM_OK;
+}
+
+}  // namespace
+
+extern "C" int amsim_vocab_loss(const amsim_vocab_loss_desc *desc, const void *h, const void *w,
+                                const int64_t *targets, const float *row_weight, float *loss, float *row_loss,
+                                float *lse, void *ws, size_t ws_bytes, amsim_stream_t stream)
+{
+    return run(desc, false, h, w, targets, row_weight, loss, row_loss, lse, nullptr, nullptr, ws, ws_bytes,
+               static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int amsim_vocab_loss_grad(const amsim_vocab_loss_desc *desc, const void *h, const void *w,
+                                     const int64_t *targets, const float *row_weight, float *loss, float *row_loss,
+                                     float *lse, void *dh, void *dw, void *ws, size_t ws_bytes, amsim_stream_t stream)
+{
+    return run(desc, true, h, w, targets, row_weight, loss, row_loss, lse, dh, dw, ws, ws_bytes,
+               static_cast<cudaStream_t>(stream));
+}
+
+// Both sizes leave room for packed copies where a row stride asks for them (a
+// base address off 16 bytes is not in the descriptor: such a call packs too,
+// and the sizes cover it).
+extern "C" size_t amsim_vocab_loss_workspace_size(const amsim_vocab_loss_desc *desc, int which)
+{
+    if (check(desc) || (which != 0 && which != 1) || desc->tokens == 0) return 0;
+    const int sms = device_sms();
+    return layout(desc, which == 1, full_rows(desc), true, true, sms ? sms : 1).bytes;
+}
+
+extern "C" size_t amsim_vocab_loss_workspace_min(const amsim_vocab_loss_desc *desc, int which)
+{
+    if (check(desc) || (which != 0 && which != 1) || desc->tokens == 0) return 0;
+    const int sms = device_sms();
+    return layout(desc, which == 1, std::min<long long>(desc->tokens, kTileM), true, true, sms ? sms : 1).bytes;
+}

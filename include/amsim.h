@@ -21,7 +21,8 @@
  *   beta are IEEE fp32 scalings, not simulated.
  *
  * Conventions for every call:
- *   - All tensors are fp32, dense, row-major (C order), owned by the caller.
+ *   - All tensors are fp32, dense, row-major (C order), owned by the caller
+ *     (the exact operators at the end also take bf16 and row strides).
  *     Pointers named "host_*" are host memory; all others are device memory
  *     of the device that was current when the LUT handle was built.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Calls only
@@ -534,6 +535,188 @@ int amsim_softmax_rows(const float *S, float *P, int64_t rows, int cols, amsim_s
  */
 int amsim_softmax_rows_backward(const float *P, const float *dP, float *dS, int64_t rows, int cols,
                                 amsim_stream_t stream);
+
+/* ------------------------------------------------------------------ exact operators of a training step */
+
+/*
+ * What stands between and after the approximate contractions when a language
+ * model is trained with them: the norms around a block, the loss over the
+ * vocabulary, the optimizer.  None of them is simulated; all arithmetic is
+ * IEEE fp32 (the loss's products are exact products of bf16 operands), and a
+ * result of a narrower type is rounded once, to nearest even.  The ApproxTrain
+ * page has no counterpart; there they are the host framework's.
+ */
+enum amsim_dtype { AMSIM_F32 = 0, AMSIM_BF16 = 1 };
+
+/*
+ * The block norm: the RMS norm after a block, the block's gate, the residual
+ * scale and the RMS norm before the next block in one pass over a row of
+ * `cols` channels,
+ *   u = y * rstd(y) * w_post          (or y when w_post is null),
+ *   r = x + alpha * gate * u          (or x when y is null),
+ *   n = r * rstd(r) * w_pre           (not computed when n is null),
+ *   rstd(t) = 1 / sqrt(mean(t^2) + eps).
+ * x is the residual stream, y the block's output, r the new residual stream
+ * and n the next block's input.  The norm of r takes r before it is rounded to
+ * its type.  Norm weights and gates are fp32.  `gate` (or null: ones) has one
+ * row of `cols` values for each `gate_rows` consecutive rows (0: one for all).
+ */
+typedef struct amsim_block_norm_desc {
+    int64_t rows;
+    int64_t gate_rows;               /* rows per row of the gate; divides `rows`; 0: all rows share one */
+    int64_t ldx, ldy, ldr, ldn;      /* row strides in elements, >= cols; 0: cols */
+    int64_t lddx, lddy, lddr, lddn;  /* the same of the gradients (backward) */
+    int cols;                        /* 1 .. AMSIM_BLOCK_NORM_MAX_COLS */
+    int x_type, y_type, n_type;      /* amsim_dtype of x, r, dx, dr; of y, dy; of n, dn */
+    float alpha, eps;                /* eps >= 0 */
+} amsim_block_norm_desc;
+#define AMSIM_BLOCK_NORM_MAX_COLS 16384
+
+/*
+ * Forward.  x: rows x cols; y or null; w_post, w_pre: cols values or null
+ * (w_post null: no norm after the block; w_pre null with n: unit weights);
+ * r: written, or null (allowed only when n is not); n: written, or null.
+ * rstd_post, rstd_pre: `rows` values each, written for the backward pass, or
+ * null.  r may alias x or y; n may alias y (equal types and strides).
+ * Errors: AMSIM_EINVAL for a null x, no output, a bad size, stride, type or
+ * eps, or a gate without y; AMSIM_EUNSUPPORTED for more channels than
+ * AMSIM_BLOCK_NORM_MAX_COLS.  rows == 0 is a no-op.
+ */
+int amsim_block_norm_fwd(const amsim_block_norm_desc *desc, const void *x, const void *y, const float *gate,
+                         const float *w_post, const float *w_pre, void *r, void *n, float *rstd_post,
+                         float *rstd_pre, amsim_stream_t stream);
+
+/*
+ * Backward.  r, y, rstd_post, rstd_pre: the forward pass's; dr: gradient of r
+ * (null: zeros), dn: gradient of n (null: n was not used).  Written:
+ *   dx = dr + rstd_pre * (t - rh * mean(t * rh)),  t = dn * w_pre, rh = r * rstd_pre,
+ *   dy = rstd_post * (s - yh * mean(s * yh)),      s = alpha * gate * dx * w_post, yh = y * rstd_post
+ *        (alpha * gate * dx without a norm after the block),
+ *   dgate  = sum over the rows that share it of alpha * dx * yh * w_post   (alpha * dx * y),
+ *   dw_post = sum over rows of alpha * gate * dx * yh,
+ *   dw_pre  = sum over rows of dn * rh.
+ * Outputs that are null are not computed; dy, dgate and dw_post need y, dw_pre
+ * needs dn.  dx may alias dr; dy may alias y or dn (equal types and strides).
+ * Row sums are kept per row share in scratch and added in share order.
+ * Scratch: amsim_block_norm_workspace_size; with less (even none) a call uses
+ * fewer row shares, down to one, which needs none.
+ */
+int amsim_block_norm_bwd(const amsim_block_norm_desc *desc, const void *dr, const void *dn, const void *r,
+                         const void *y, const float *gate, const float *w_post, const float *w_pre,
+                         const float *rstd_post, const float *rstd_pre, void *dx, void *dy, float *dgate,
+                         float *dw_post, float *dw_pre, void *ws, size_t ws_bytes, amsim_stream_t stream);
+
+/* Bytes of scratch with which amsim_block_norm_bwd fills the GPU. */
+size_t amsim_block_norm_workspace_size(const amsim_block_norm_desc *desc);
+
+/*
+ * The vocabulary loss: softmax cross entropy of the logits h W^T against one
+ * target per token, without keeping the logits.
+ *   z[t,v] = sum_d h[t,d] w[v,d],  lse[t] = log sum_v exp z[t,v],
+ *   row_loss[t] = lse[t] - z[t, target[t]],
+ *   loss = sum_t a[t] row_loss[t] / A,
+ * with a[t] the token's weight (row_weight[t], or 1), A = sum_t a[t] over the
+ * tokens that count (AMSIM_REDUCE_MEAN) or 1 (AMSIM_REDUCE_SUM).  A token
+ * whose target is `ignore_index` does not count: row_loss 0, no gradient, and
+ * with no token that counts the loss is 0.  Any other target outside
+ * [0, vocab) makes row_loss and loss NaN and adds no gradient.
+ * h: tokens x dim, w: vocab x dim, both bf16; products are exact, sums fp32.
+ */
+enum amsim_reduction { AMSIM_REDUCE_MEAN = 0, AMSIM_REDUCE_SUM = 1 };
+typedef struct amsim_vocab_loss_desc {
+    int64_t tokens;
+    int64_t ignore_index;
+    int64_t ld_h, ld_w, ld_dh, ld_dw; /* row strides in elements, >= dim; 0: dim */
+    int vocab, dim;                   /* >= 1 */
+    int reduction;                    /* amsim_reduction */
+} amsim_vocab_loss_desc;
+
+/*
+ * The loss alone (evaluation).  targets: `tokens` values; row_weight: `tokens`
+ * fp32 values or null; loss: 1 value; row_loss, lse: `tokens` values each, or
+ * null.  Scratch: at least amsim_vocab_loss_workspace_min(desc, 0) bytes,
+ * else AMSIM_EINVAL; more than amsim_vocab_loss_workspace_size(desc, 0) is not
+ * used.  tokens == 0 writes loss 0.
+ */
+int amsim_vocab_loss(const amsim_vocab_loss_desc *desc, const void *h, const void *w, const int64_t *targets,
+                     const float *row_weight, float *loss, float *row_loss, float *lse, void *ws,
+                     size_t ws_bytes, amsim_stream_t stream);
+
+/*
+ * The loss and its gradients, both bf16 and written:
+ *   G[t,v] = a[t] / A * (exp(z[t,v] - lse[t]) - [v == target[t]]),
+ *   dh = G W (tokens x dim),  dw = G^T h (vocab x dim).
+ * The tokens are taken in chunks whose exponentials (16 bits each) fit the
+ * scratch; one chunk when ws_bytes reaches amsim_vocab_loss_workspace_size.
+ * G is rounded to bf16 for its two products.  Scratch as above with which = 1.
+ */
+int amsim_vocab_loss_grad(const amsim_vocab_loss_desc *desc, const void *h, const void *w, const int64_t *targets,
+                          const float *row_weight, float *loss, float *row_loss, float *lse, void *dh, void *dw,
+                          void *ws, size_t ws_bytes, amsim_stream_t stream);
+
+/*
+ * Bytes of scratch of the two calls (which: 0 the loss, 1 with gradients) for
+ * the fastest plan (its exponentials capped at 4 GiB), and the least a call
+ * runs with.  0 for an invalid descriptor.
+ */
+size_t amsim_vocab_loss_workspace_size(const amsim_vocab_loss_desc *desc, int which);
+size_t amsim_vocab_loss_workspace_min(const amsim_vocab_loss_desc *desc, int which);
+
+/*
+ * One AdamW step over many tensors (decoupled weight decay, no amsgrad), in
+ * one launch per 400 tensors.  For each element, in fp32 and in this order:
+ *   g' = g * grad_scale,  m' = m * beta1 + g' * (1 - beta1),
+ *   v' = v * beta2 + (g' * g') * (1 - beta2),
+ *   p' = p * (1 - lr * wd) - m' / (sqrt(v') * (1 / sqrt(1 - beta2^step)) + eps) * (lr / (1 - beta1^step))
+ * (each product, sum, root and quotient rounded to fp32; lr and wd are the
+ * tensor's: lr = hyper.lr * lr_scale).  p is updated in place, and its bf16
+ * rounding is also written to `copy` when that is not null.
+ * Moments: fp32 (m_scale and v_scale null), or 8-bit codes in blocks of
+ * AMSIM_ADAMW_BLOCK elements from the tensor's first (the last may be short):
+ *   m = sign(q) (|q| / 127)^2 m_scale[block],  q in [-127, 127] (int8),
+ *   v = (q / 255)^4 v_scale[block],            q in [0, 255] (uint8),
+ * where a block's scale is the largest magnitude of its new moments and codes
+ * round to nearest in the root domain; a second moment above zero keeps a code
+ * of at least 1, so that its update stays bounded.  p is updated with the new
+ * moments before they are rounded to codes.  A block with a non-finite moment
+ * gets a NaN scale and reads back as NaN.
+ * All tensors of a call have the same kind of moments.  Tensors must not
+ * overlap.  `tensors` is host memory, read during the call; no device table is
+ * kept, so a captured graph holds the pointers of its capture.
+ */
+#define AMSIM_ADAMW_BLOCK 256
+typedef struct amsim_adamw_tensor {
+    float *p;
+    const void *g;
+    void *m, *v;               /* float, or int8_t / uint8_t codes */
+    float *m_scale, *v_scale;  /* ceil(n / AMSIM_ADAMW_BLOCK) values each, or null: fp32 moments */
+    void *copy;                /* bf16, or null */
+    int64_t n;
+    float lr_scale, weight_decay;
+    int g_type;                /* amsim_dtype */
+    int reserved;              /* 0 */
+} amsim_adamw_tensor;
+typedef struct amsim_adamw_hyper {
+    double lr, beta1, beta2, eps;
+    int64_t step;              /* 1 for the first */
+    const float *grad_scale;   /* one device value multiplied into every gradient, or null */
+} amsim_adamw_hyper;
+
+/*
+ * Errors: AMSIM_EINVAL for a null pointer, n < 0, a count outside [0, 2^20],
+ * betas outside [0, 1), step < 1, non-finite lr, eps or weight decay, eps < 0,
+ * or tensors with different kinds of moments.
+ */
+int amsim_adamw_step(int count, const amsim_adamw_tensor *tensors, const amsim_adamw_hyper *hyper,
+                     amsim_stream_t stream);
+
+/*
+ * The values of 8-bit moments (for a checkpoint, or to widen the state):
+ * out[i] = the value of codes[i], i < n.  second != 0: codes and scales of a
+ * second moment (uint8), else of a first (int8).
+ */
+int amsim_adamw_moment_values(const void *codes, const float *scales, int second, int64_t n, float *out,
+                              amsim_stream_t stream);
 
 #ifdef __cplusplus
 }
