@@ -77,14 +77,17 @@ __device__ __forceinline__ unsigned long long now_ns()
 
 // Wait for the phase of `bar` with parity `parity`; after kWaitLimitNs the
 // timeout is recorded, `aborted` set, and every later wait of the thread
-// returns at once, so the thread runs to its end.
+// returns at once, so the thread runs to its end.  The timer is read once in
+// 1024 polls: a read takes longer than the waits between the roles of a CTA.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, bool &aborted)
 {
     if (aborted) return false;
-    if (bar_try(bar, parity)) return true;
-    const unsigned long long t0 = now_ns();
-    while (!bar_try(bar, parity)) {
-        if (now_ns() - t0 > kWaitLimitNs) {
+    unsigned long long t0 = 0;
+    for (uint32_t i = 1; !bar_try(bar, parity); ++i) {
+        if (i & 1023) continue;
+        const unsigned long long t = now_ns();
+        if (!t0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
             aborted = true;
             atomicOr(&g_wait_timeouts, (unsigned)AMSIM_WAIT_COPY);
             return false;
@@ -93,15 +96,62 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, bool &a
     return true;
 }
 
-// Box at (x, y) of a 2-D tensor map into shared memory; completes on `bar`.
-__device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
+// ------------------------------------------------------------------ CTA pairs
+// The kernels run in clusters of two CTAs on neighbouring SMs, which the
+// matrix instructions treat as one: rank 0 leads.
+__device__ __forceinline__ uint32_t pair_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Address of `p` (an address of this CTA's shared memory) in the leader's.
+__device__ __forceinline__ uint32_t leader_addr(const void *p)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+    return r;
+}
+
+// All threads of both CTAs; memory written before is seen after.
+__device__ __forceinline__ void pair_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrive on a barrier of the pair by its cluster address.
+__device__ __forceinline__ void bar_arrive_at(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Box at (x, y) of a 2-D tensor map into this CTA's shared memory; completes on
+// a barrier of the pair, given by its cluster address.
+__device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+
+// A staged box from shared memory to (x, y) of a 2-D tensor map; elements
+// outside the tensor are not written.
+__device__ __forceinline__ void store_box(const CUtensorMap *map, int x, int y, const void *src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(smem_addr(src))
+                 : "memory");
+}
+__device__ __forceinline__ void stores_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The thread's committed stores have read their shared memory / are done.
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Shared-memory writes of this thread before become visible to copies issued after.
+__device__ __forceinline__ void fence_staged() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
@@ -109,20 +159,20 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 }
 
 // ------------------------------------------------------------------ tcgen05
-// The whole warp allocates `COLS` columns of tensor memory and writes their
-// address to shared memory; the same warp frees them.
+// A warp of each CTA of the pair allocates `COLS` columns of its SM's tensor
+// memory and writes their address to shared memory; the same warp frees them.
 template <int COLS>
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "n"(COLS)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "n"(COLS)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 
 template <int COLS>
 __device__ __forceinline__ void tmem_free(uint32_t addr)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "n"(COLS) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "n"(COLS) : "memory");
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -148,22 +198,27 @@ __host__ __device__ constexpr uint32_t instr_desc(int m, int n, int a_mn, int b_
            (uint32_t)(m >> 4) << 24;
 }
 
-// D (tensor memory) = A B, + D when `acc`; 16 steps of K, one issuing thread.
+// D (tensor memory of both CTAs) = A B, + D when `acc`; 16 steps of K, one
+// issuing thread of the leader.  Each CTA holds its half of A's rows, its half
+// of B's columns, and the accumulator of its rows.
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
 
-// `bar` gets one arrival when every matrix instruction issued so far is done.
+// `bar` of both CTAs gets one arrival when every matrix instruction issued so far is done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
 }
 
 // 32 accumulator columns of the calling thread's row (its lane of tensor

@@ -26,15 +26,18 @@ namespace {
 using namespace amsim;
 using bf16 = __nv_bfloat16;
 
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+constexpr int kTileM = 256, kTileN = 256, kTileK = 64;   // of a CTA pair
+constexpr int kHalfM = kTileM / 2, kHalfN = kTileN / 2;   // what each CTA holds of A and of B
 constexpr int kPiece = 128;                        // columns that share a maximum
-constexpr int kStages = 4;
-constexpr int kStageA = kTileM * kTileK * 2, kStageB = kTileN * kTileK * 2;
-constexpr int kStage = kStageA + kStageB;          // 48 KB
+constexpr int kStages = 6;
+constexpr int kStageA = kHalfM * kTileK * 2, kStageB = kHalfN * kTileK * 2;
+constexpr int kStage = kStageA + kStageB;          // 32 KB
 constexpr int kBox = 64;                           // elements of a 128-byte row
 constexpr int kFirstEpilogueWarp = 2;              // after the copy and the matrix warp
 constexpr int kThreads = (kFirstEpilogueWarp + 8) * 32;
-constexpr int kSmem = kStages * kStage + 1024 + 256;
+constexpr int kBuffer = 32 * 128;                  // of a warp: 32 rows of 128 bytes on their way out
+constexpr int kSmem = kStages * kStage + 8 * kBuffer + 1024 + 256;
+static_assert(kSmem <= amsim::kMaxSmemPerCta, "shared memory of a CTA");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSteps = 2048.0f;                  // code steps per unit of the logit
 
@@ -57,14 +60,14 @@ struct ProductParams {
     const int64_t *targets;         // of the chunk's rows
     float *target_logit;
     float2 *stats;                  // [piece][rows]: maximum, sum of exponentials
-    uint16_t *codes;                // [rows][ld_codes], or null
-    long long ld_codes;
+    const uint16_t *codes;          // null: not wanted; else the output map is over them
     // kDh, kDw
     bf16 *out;
     long long ld_out;
-    int vec;                        // out takes 16-byte stores
+    int boxes;                      // out goes through the tensor map
     const float *scale;             // 1 / A
     float *acc;                     // fp32 sums of earlier chunks (kDw) or the splits' sums (kDh)
+    long long ld_acc, split_rows;   // its row stride and rows per split
     int acc_read, acc_write;
 };
 
@@ -107,22 +110,51 @@ __device__ __forceinline__ Tile tile_at(const ProductParams &p, int i)
     return t;
 }
 
+// What leaves a tile goes through a warp's buffer of 32 rows by 128 bytes,
+// swizzled like the operand tiles (a row's 16-byte words exchanged by the row
+// number modulo 8: no bank conflicts), and out by a box copy.  Stores straight
+// from the registers, a row per lane, touch 32 lines per instruction: they held
+// the logits' epilogue at 12.7 us a tile where the products took 4.3.
+struct Out {
+    uint8_t *buffer;
+    const CUtensorMap *map;
+    int lane;
+
+    // begin, the eight 16-byte words of every lane's row, end: the warp's rows
+    // from `y`, 128 bytes from column `x` (in elements of the map's type), if any
+    // of them is inside.
+    __device__ __forceinline__ void begin() const
+    {
+        if (lane == 0) tc::stores_read();
+        __syncwarp();
+    }
+    __device__ __forceinline__ void word(int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) const
+    {
+        reinterpret_cast<uint4 *>(buffer + lane * 128)[j ^ (lane & 7)] = make_uint4(a, b, c, d);
+    }
+    __device__ __forceinline__ void end(int x, int y, bool inside) const
+    {
+        tc::fence_staged();
+        __syncwarp();
+        if (lane == 0 && inside) {
+            tc::store_box(map, x, y, buffer);
+            tc::stores_commit();
+        }
+    }
+};
+
 // One 128-column piece of a row of logits, in the registers of its thread.
 // fmaxf skips NaN; the sum does not, so a NaN logit makes the row's lse NaN.
+// The code of a logit is the rounding of a sum with 2^23: its low 16 bits.
 template <bool MASKED>
-__device__ __forceinline__ void reduce_piece(const ProductParams &p, const float (&z)[kPiece], int row, int col0)
+__device__ __forceinline__ void reduce_piece(const ProductParams &p, const float (&z)[kPiece], int row, int col0,
+                                             const Out &out)
 {
-    if (row >= p.m) return;
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kPiece; ++j)
         if (!MASKED || col0 + j < p.n) top = fmaxf(top, z[j]);
-    const float shift = top == -INFINITY ? 0.0f : top * kLog2e;
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j)
-        if (!MASKED || col0 + j < p.n) sum[j & 3] += exp2_fast(fmaf(z[j], kLog2e, -shift));
-    p.stats[(long long)(col0 / kPiece) * p.m + row] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (row < p.m) {
     const long long d = p.targets[row] - col0;
     if (d >= 0 && d < kPiece && col0 + d < p.n) {
         float pick = 0.0f;
@@ -130,85 +162,113 @@ __device__ __forceinline__ void reduce_piece(const ProductParams &p, const float
         for (int j = 0; j < kPiece; ++j) select_if(pick, z[j], (int)d, j);
         p.target_logit[row] = pick;
     }
-    if (!p.codes) return;
-    uint16_t *dst = p.codes + row * p.ld_codes + col0;
+    }
+    const float shift = top == -INFINITY ? 0.0f : top * kLog2e;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < kPiece / 8; ++j) {
-        uint32_t w[4];
+    for (int j = 0; j < kPiece; ++j)
+        if (!MASKED || col0 + j < p.n) sum[j & 3] += exp2_fast(fmaf(z[j], kLog2e, -shift));
+    if (row < p.m) p.stats[(long long)(col0 / kPiece) * p.m + row] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (p.codes) {
+        constexpr float kBase = 8388608.0f, kLast = kBase + 65535.0f;
+        auto code = [&](int j) {
+            const float a = fminf(fmaf(top - z[2 * j], kSteps, kBase), kLast);
+            const float b = fminf(fmaf(top - z[2 * j + 1], kSteps, kBase), kLast);
+            return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
+        };
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = __float2uint_rn(fminf((top - z[8 * j + 2 * e]) * kSteps, 65535.0f)) |
-                   __float2uint_rn(fminf((top - z[8 * j + 2 * e + 1]) * kSteps, 65535.0f)) << 16;
-        if (!MASKED || col0 + j * 8 < p.n)
-            *reinterpret_cast<uint4 *>(dst + j * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int c = 0; c < kPiece / kBox; ++c) {
+            out.begin();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = c * 32 + j * 4;
+                out.word(j, code(i), code(i + 1), code(i + 2), code(i + 3));
+            }
+            out.end(col0 + c * kBox, row - out.lane, (!MASKED || col0 + c * kBox < p.n) && row - out.lane < p.m);
+        }
     }
 }
 
-// 32 columns of a row: added to the fp32 sums, or scaled, rounded and written.
-__device__ __forceinline__ void store_chunk(const ProductParams &p, const uint32_t (&r)[32], int row, int col, int split,
-                                            float scale)
+// A 128-column piece of a row of dh or dw: added to the fp32 sums, or scaled,
+// rounded and written; `release` is called when tensor memory has been read.
+template <typename F>
+__device__ __forceinline__ void store_piece(const ProductParams &p, uint32_t tmem, int row, int col0, int split,
+                                            const Out &out, F release)
 {
-    float v[32];
+    const bool on = row < p.m, warp_on = row - out.lane < p.m && col0 < p.n;
+    const float scale = p.out ? *p.scale : 1.0f;
+    float *acc = p.acc ? p.acc + (split * p.split_rows + row) * p.ld_acc + col0 : nullptr;
+    if (p.acc_write || !p.boxes) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-    if (p.acc) {
-        float *acc = p.acc + ((long long)split * p.m + row) * p.n + col;
-        const int left = min(32, p.n - col);
+        for (int c = 0; c < kPiece / 32; ++c) {
+            uint32_t r[32];
+            tc::tmem_load32(tmem + c * 32, r);
+            tc::tmem_load_wait(r);
+            if (c == kPiece / 32 - 1) release();
+            const int left = on ? p.n - (col0 + c * 32) : 0;
+            if (p.acc_read) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j < left) r[j] = __float_as_uint(__uint_as_float(r[j]) + acc[c * 32 + j]);
+            }
+            if (p.acc_write) {
+                out.begin();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) out.word(j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                out.end(col0 + c * 32, (int)(split * p.split_rows) + row - out.lane,
+                        warp_on && col0 + c * 32 < p.n);
+            } else {
+                bf16 *dst = p.out + row * p.ld_out + col0 + c * 32;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j < left) dst[j] = __float2bfloat16_rn(__uint_as_float(r[j]) * scale);
+            }
+        }
+        return;
+    }
+    uint32_t w[kPiece / 2];
+#pragma unroll
+    for (int c = 0; c < kPiece / 32; ++c) {
+        uint32_t r[32];
+        tc::tmem_load32(tmem + c * 32, r);
+        tc::tmem_load_wait(r);
+        const int left = on ? p.n - (col0 + c * 32) : 0;
         if (p.acc_read) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (j < left) v[j] += acc[j];
+                if (j < left) r[j] = __float_as_uint(__uint_as_float(r[j]) + acc[c * 32 + j]);
         }
-        if (p.acc_write) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < left) acc[j] = v[j];
-            return;
+        for (int j = 0; j < 16; ++j)
+            w[c * 16 + j] = pack2(__uint_as_float(r[2 * j]) * scale, __uint_as_float(r[2 * j + 1]) * scale);
+    }
+    release();
+#pragma unroll
+    for (int c = 0; c < kPiece / kBox; ++c) {
+        out.begin();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = c * 32 + j * 4;
+            out.word(j, w[i], w[i + 1], w[i + 2], w[i + 3]);
         }
-    }
-    bf16 *dst = p.out + row * p.ld_out + col;
-    if (p.vec) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (col + j * 8 < p.n)
-                *reinterpret_cast<uint4 *>(dst + j * 8) =
-                    make_uint4(pack2(v[8 * j] * scale, v[8 * j + 1] * scale),
-                               pack2(v[8 * j + 2] * scale, v[8 * j + 3] * scale),
-                               pack2(v[8 * j + 4] * scale, v[8 * j + 5] * scale),
-                               pack2(v[8 * j + 6] * scale, v[8 * j + 7] * scale));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (col + j < p.n) dst[j] = __float2bfloat16_rn(v[j] * scale);
-    }
-}
-
-__device__ __forceinline__ void store_piece(const ProductParams &p, uint32_t tmem, int row, int col0, int split)
-{
-    uint32_t r[32];
-    const bool on = row < p.m;
-    const float scale = p.out ? *p.scale : 1.0f;
-#pragma unroll
-    for (int c = 0; c < kPiece / 32; ++c) {
-        tc::tmem_load32(tmem + c * 32, r);
-        tc::tmem_load_wait(r);
-        const int col = col0 + c * 32;
-        if (on && col < p.n) store_chunk(p, r, row, col, split, scale);
+        out.end(col0 + c * kBox, row - out.lane, warp_on && col0 + c * kBox < p.n);
     }
 }
 
 template <int PRODUCT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const ProductParams p, const __grid_constant__ CUtensorMap amap,
-                   const __grid_constant__ CUtensorMap bmap)
+                   const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap omap)
 {
     constexpr bool a_mn = PRODUCT == kDw, b_mn = PRODUCT != kLogits;
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t *full = reinterpret_cast<uint64_t *>(ring + kStages * kStage);
+    uint8_t *buffers = ring + kStages * kStage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(buffers + 8 * kBuffer);
     uint64_t *empty = full + kStages, *ready = empty + kStages, *taken = ready + 2, *drained = taken + 2;
     uint32_t *slot = reinterpret_cast<uint32_t *>(drained + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)tc::pair_rank(), pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
     if (warp == 0 && lane == 0) {
         tc::prefetch_map(&amap);
         tc::prefetch_map(&bmap);
@@ -218,61 +278,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(ready + i, 1);
-            tc::bar_init(taken + i, 8 * 32);
+            tc::bar_init(taken + i, 2 * 8);            // a lane of each epilogue warp of the pair
         }
         tc::bar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tc::tmem_alloc<512>(slot);
     tc::fence_before();
-    __syncthreads();
+    tc::pair_sync();
     tc::fence_after();
     const uint32_t tmem = *slot;
     const int tiles = p.mt * p.nt * p.splits;
     bool aborted = false;
     if (warp == 0) {
+        // both CTAs copy their halves; the bytes of both are counted on the leader's barrier
         if (lane == 0) {
             int s = 0;
             uint32_t phase = 0;
             long long issued = 0;
-            for (int i = blockIdx.x; i < tiles && !aborted; i += gridDim.x) {
+            for (int i = pair; i < tiles && !aborted; i += pairs) {
                 const Tile t = tile_at(p, i);
-                const int m0 = t.m * kTileM, n0 = t.n * kTileN;
+                const int m0 = t.m * kTileM + rank * kHalfM, n0 = t.n * kTileN + rank * kHalfN;
                 const int k1 = min(p.kblocks, (t.split + 1) * p.per_split);
                 for (int k = t.split * p.per_split; k < k1; ++k) {
                     if (!tc::bar_wait(empty + s, phase ^ 1, aborted)) break;
                     uint8_t *a = ring + s * kStage, *b = a + kStageA;
-                    tc::bar_expect(full + s, kStage);
+                    const uint32_t bar = tc::leader_addr(full + s);
+                    if (rank == 0) tc::bar_expect(full + s, 2 * kStage);
                     if constexpr (a_mn) {
 #pragma unroll
-                        for (int j = 0; j < kTileM / kBox; ++j)
-                            tc::load_box(a + j * kBox * kTileK * 2, &amap, m0 + j * kBox, k * kTileK, full + s);
+                        for (int j = 0; j < kHalfM / kBox; ++j)
+                            tc::load_box(a + j * kBox * kTileK * 2, &amap, m0 + j * kBox, k * kTileK, bar);
                     } else {
-                        tc::load_box(a, &amap, k * kTileK, m0, full + s);
+                        tc::load_box(a, &amap, k * kTileK, m0, bar);
                     }
                     if constexpr (b_mn) {
 #pragma unroll
-                        for (int j = 0; j < kTileN / kBox; ++j)
-                            tc::load_box(b + j * kBox * kTileK * 2, &bmap, n0 + j * kBox, k * kTileK, full + s);
+                        for (int j = 0; j < kHalfN / kBox; ++j)
+                            tc::load_box(b + j * kBox * kTileK * 2, &bmap, n0 + j * kBox, k * kTileK, bar);
                     } else {
-                        tc::load_box(b, &bmap, k * kTileK, n0, full + s);
+                        tc::load_box(b, &bmap, k * kTileK, n0, bar);
                     }
                     ++issued;
                     if (++s == kStages) { s = 0; phase ^= 1; }
                 }
             }
-            if (aborted) {      // copies still in flight land before the CTA's memory goes away
-                bool gave_up = false;
-                for (long long j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
-                    tc::bar_wait(full + j % kStages, (uint32_t)(j / kStages & 1), gave_up);
-            }
+            // Every copy has landed and every release has arrived before the
+            // CTA's memory goes away: a released stage's copies were read.
+            bool gave_up = false;
+            for (long long j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
+                tc::bar_wait(empty + j % kStages, (uint32_t)(j / kStages & 1), gave_up);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             constexpr uint32_t idesc = tc::instr_desc(kTileM, kTileN, a_mn, b_mn);
             int s = 0;
             uint32_t phase = 0, count = 0;
-            for (int i = blockIdx.x; i < tiles && !aborted; i += gridDim.x) {
+            for (int i = pair; i < tiles && !aborted; i += pairs) {
                 const Tile t = tile_at(p, i);
                 const int k0 = t.split * p.per_split, k1 = min(p.kblocks, (t.split + 1) * p.per_split);
                 uint32_t half = 0, d = 0;
@@ -312,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // others the rest; a warp reads the 32 rows of tensor memory that its
         // number modulo 4 allows
         const int part = (warp - kFirstEpilogueWarp) >> 2, quarter = warp & 3;
+        const Out out{buffers + (warp - kFirstEpilogueWarp) * kBuffer, &omap, lane};
         uint32_t count = 0;
         // the next accumulator is complete; every lane waits, and the warp goes on together
         auto next = [&](uint32_t &addr, uint32_t &half) {
@@ -322,9 +385,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             addr = tmem + half * kTileN + part * kPiece + ((uint32_t)quarter * 32 << 16);
             return __all_sync(0xFFFFFFFFu, ok) != 0;
         };
-        for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
+        const uint32_t taken_at[2] = {tc::leader_addr(taken), tc::leader_addr(taken + 1)};
+        // the accumulator has been read: one arrival per warp, on the leader's barrier
+        auto release = [&](uint32_t half) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive_at(taken_at[half]);
+        };
+        for (int i = pair; i < tiles; i += pairs) {
             const Tile t = tile_at(p, i);
-            const int row = t.m * kTileM + quarter * 32 + lane, col0 = t.n * kTileN + part * kPiece;
+            const int row = t.m * kTileM + rank * kHalfM + quarter * 32 + lane, col0 = t.n * kTileN + part * kPiece;
             uint32_t addr, half;
             if constexpr (PRODUCT == kLogits) {
                 float z[kPiece];
@@ -342,23 +412,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             z[c * 32 + j] = k ? z[c * 32 + j] + x : x;
                         }
                     }
-                    tc::fence_before();
-                    tc::bar_arrive(taken + half);
+                    release(half);
                 }
                 if (!ok) break;
-                if (col0 + kPiece <= p.n) reduce_piece<false>(p, z, row, col0);
-                else if (col0 < p.n) reduce_piece<true>(p, z, row, col0);
+                if (col0 + kPiece <= p.n) reduce_piece<false>(p, z, row, col0, out);
+                else if (col0 < p.n) reduce_piece<true>(p, z, row, col0, out);
             } else {
                 if (!next(addr, half)) break;
-                if (col0 < p.n) store_piece(p, addr, row, col0, t.split);
-                tc::fence_before();
-                tc::bar_arrive(taken + half);
+                store_piece(p, addr, row, col0, t.split, out, [&] { release(half); });
             }
         }
+        if (lane == 0) tc::stores_done();
     }
     __syncwarp();
     tc::fence_before();
-    __syncthreads();
+    tc::pair_sync();
     tc::fence_after();
     if (warp == 1) tc::tmem_free<512>(tmem);
 }
@@ -368,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct Totals {
     unsigned int done;       // blocks of the merge that have finished
     float scale;             // 1 / A
-    double loss;             // sum of weight * row loss of the chunks so far
+    float loss;              // sum of weight * row loss of the chunks so far
 };
 
 struct MergeParams {
@@ -386,54 +454,67 @@ struct MergeParams {
     int first_chunk, last_chunk;
 };
 
-__device__ __forceinline__ double block_total(double x, double *red)
+// A running sum with the rounding errors carried along (compensated
+// summation): thousands of terms per thread stay at one rounding, without fp64,
+// whose units are few here (32 warps adding doubles took 20 us).
+struct Sum {
+    float s = 0.0f, lost = 0.0f;
+    __device__ __forceinline__ void add(float x)
+    {
+        const float y = __fsub_rn(x, lost), t = __fadd_rn(s, y);
+        lost = __fsub_rn(__fsub_rn(t, s), y);
+        s = t;
+    }
+};
+
+// The block's total in a fixed order, in every thread of warp 0.
+__device__ __forceinline__ float block_total(float x, float *red)
 {
 #pragma unroll
     for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
-    x = 0.0;
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) x += red[i];
+    x = threadIdx.x < blockDim.x >> 5 ? red[threadIdx.x] : 0.0f;
+    if (threadIdx.x < 32)
+#pragma unroll
+        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
     return x;
+}
+
+// Adds a piece's exponentials: (maximum, sum) pairs.  Where both maxima are
+// -inf (or only NaN was seen), the sums are 0 or NaN and stay so.
+__device__ __forceinline__ void add_piece(float &top, float &sum, float2 s)
+{
+    const float t = fmaxf(top, s.x);
+    if (t == -INFINITY) {
+        sum += s.y;
+    } else {
+        sum = sum * exp2_fast((top - t) * kLog2e) + s.y * exp2_fast((s.x - t) * kLog2e);
+        top = t;
+    }
 }
 
 // lse and loss of each row from its pieces (lane by lane over the rows, so
 // that a warp reads neighbouring rows); the last block adds the losses.
-constexpr int kMergeThreads = 256, kMergeRows = 32;
+constexpr int kMergeThreads = 1024, kMergeRows = 32;
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p)
 {
     __shared__ float2 part[kMergeThreads / 32][kMergeRows];
-    __shared__ double red[kMergeThreads / 32];
+    __shared__ float red[kMergeThreads / 32];
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * kMergeRows + lane;
     float top = -INFINITY, sum = 0.0f;
     if (row < p.rows) {
-        for (int i = warp; i < p.pieces; i += kMergeThreads / 32) {
-            const float2 s = p.stats[(long long)i * p.rows + row];
-            const float t = fmaxf(top, s.x);
-            if (t != -INFINITY) {
-                sum = sum * exp2_fast((top - t) * kLog2e) + s.y * exp2_fast((s.x - t) * kLog2e);
-                top = t;
-            } else {
-                sum += s.y;                // a row of -inf or NaN logits
-            }
-        }
+#pragma unroll 4
+        for (int i = warp; i < p.pieces; i += kMergeThreads / 32) add_piece(top, sum, p.stats[(long long)i * p.rows + row]);
     }
     part[warp][lane] = make_float2(top, sum);
     __syncthreads();
     if (warp == 0 && row < p.rows) {
-        for (int i = 1; i < kMergeThreads / 32; ++i) {
-            const float2 s = part[i][lane];
-            const float t = fmaxf(top, s.x);
-            if (t != -INFINITY) {
-                sum = sum * exp2_fast((top - t) * kLog2e) + s.y * exp2_fast((s.x - t) * kLog2e);
-                top = t;
-            } else {
-                sum += s.y;
-            }
-        }
+#pragma unroll 8
+        for (int i = 1; i < kMergeThreads / 32; ++i) add_piece(top, sum, part[i][lane]);
         const float lse = top + logf(sum);
         const long long target = p.targets[row];
         const bool counts = target != p.ignore, valid = target >= 0 && target < p.vocab;
@@ -447,23 +528,23 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
     __syncthreads();
     if (!last) return;
     __threadfence();
-    double loss = 0.0, weight = 0.0;
+    Sum losses, weights;
     for (int i = threadIdx.x; i < p.rows; i += kMergeThreads)
         if (p.targets[i] != p.ignore)
-            loss += (double)(p.row_weight ? p.row_weight[p.first + i] : 1.0f) * (double)__ldcg(p.row_loss + i);
-    loss = block_total(loss, red);
+            losses.add((p.row_weight ? p.row_weight[p.first + i] : 1.0f) * __ldcg(p.row_loss + i));
+    float loss = block_total(losses.s, red), weight = 0.0f;
     if (p.mean && p.first_chunk) {
         for (long long i = threadIdx.x; i < p.tokens; i += kMergeThreads)
-            if (p.all_targets[i] != p.ignore) weight += p.row_weight ? (double)p.row_weight[i] : 1.0;
-        weight = block_total(weight, red);
+            if (p.all_targets[i] != p.ignore) weights.add(p.row_weight ? p.row_weight[i] : 1.0f);
+        weight = block_total(weights.s, red);
     }
     if (threadIdx.x == 0) {
         Totals *t = p.totals;
-        if (p.first_chunk) t->scale = !p.mean ? 1.0f : weight != 0.0 ? (float)(1.0 / weight) : 0.0f;
+        if (p.first_chunk) t->scale = !p.mean ? 1.0f : weight != 0.0f ? 1.0f / weight : 0.0f;
         else loss += t->loss;
         t->loss = loss;
         t->done = 0;
-        if (p.last_chunk) *p.loss = (float)(loss * (double)t->scale);
+        if (p.last_chunk) *p.loss = loss * t->scale;
     }
 }
 
@@ -505,15 +586,16 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
 }
 
 // dh of a row range from the splits' sums, in split order.
-__global__ void __launch_bounds__(256) join_kernel(const float *acc, int splits, long long rows, int cols,
-                                                   const float *scale, bf16 *out, long long ld)
+__global__ void __launch_bounds__(256) join_kernel(const float *acc, int splits, long long split_rows, long long ld_acc,
+                                                   int cols, const float *scale, bf16 *out, long long ld)
 {
-    const long long n = rows * cols;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-        float s = 0.0f;
-        for (int k = 0; k < splits; ++k) s += acc[k * n + i];
-        out[i / cols * ld + i % cols] = __float2bfloat16_rn(s * *scale);
-    }
+    const long long row = blockIdx.y;
+    const int col = (int)(blockIdx.x * 256 + threadIdx.x);
+    if (col >= cols) return;
+    const float *src = acc + row * ld_acc + col;
+    float s = 0.0f;
+    for (int k = 0; k < splits; ++k) s += src[k * split_rows * ld_acc];
+    out[row * ld + col] = __float2bfloat16_rn(s * *scale);
 }
 
 // An operand whose rows TMA cannot take (base or row stride not a multiple of
@@ -544,16 +626,19 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Map of a bf16 matrix, `inner` contiguous elements by `outer` rows of stride
-// `ld`; boxes of 64 x `box` elements, zeros outside.
-int matrix_map(CUtensorMap *map, const void *base, long long inner, long long outer, long long ld, int box)
+// Map of a bf16 (or fp32) matrix, `inner` contiguous elements by `outer` rows of
+// stride `ld`; boxes of 128 bytes by `box` rows, zeros outside.
+int matrix_map(CUtensorMap *map, const void *base, long long inner, long long outer, long long ld, int box,
+               bool fp32 = false)
 {
     static const EncodeTiled encode = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
     if (!encode) return AMSIM_EUNSUPPORTED;
+    const int size = fp32 ? 4 : 2;
     const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t boxes[2] = {(cuuint32_t)kBox, (cuuint32_t)box}, ones[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, boxes, ones,
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * size};
+    const cuuint32_t boxes[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box}, ones[2] = {1, 1};
+    return encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                  const_cast<void *>(base), dims, strides, boxes, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? AMSIM_OK
@@ -590,7 +675,7 @@ int device_sms()
 // Scratch of a call over chunks of `rows` tokens.
 struct Layout {
     size_t totals, row_loss, lse, weight, target_logit, stats, codes, dw_acc, dh_acc, pack_h, pack_w, bytes;
-    long long ld_codes, ld_pack;
+    long long ld_codes, ld_pack, ld_acc, split_rows;
     int dh_splits;
 };
 
@@ -602,9 +687,9 @@ constexpr long long kMostRows = 32768;         // of a chunk
 int dh_splits(long long rows, const amsim_vocab_loss_desc *d, int sms)
 {
     const long long tiles = ((rows + kTileM - 1) / kTileM) * ((d->dim + kTileN - 1) / kTileN);
-    const int kblocks = (d->vocab + kTileK - 1) / kTileK;
-    if (tiles * 2 > sms) return 1;
-    return (int)std::max<long long>(1, std::min<long long>(sms / tiles, kblocks / 8));
+    const int kblocks = (d->vocab + kTileK - 1) / kTileK, pairs = sms / 2;
+    if (tiles * 2 > pairs) return 1;
+    return (int)std::max<long long>(1, std::min<long long>(pairs / tiles, kblocks / 8));
 }
 
 Layout layout(const amsim_vocab_loss_desc *d, bool grad, long long rows, bool pack_h, bool pack_w, int sms)
@@ -625,12 +710,14 @@ Layout layout(const amsim_vocab_loss_desc *d, bool grad, long long rows, bool pa
     l.stats = take((size_t)pieces * rows * 8);
     l.ld_pack = up8(d->dim);
     l.ld_codes = up8(d->vocab);
+    l.ld_acc = (d->dim + 3) & ~3LL;
+    l.split_rows = (rows + kTileM - 1) / kTileM * kTileM;   // whole tiles: a box never reaches the next split
     l.dh_splits = 1;
     if (grad) {
         l.codes = take((size_t)rows * l.ld_codes * 2);
-        if (rows < d->tokens) l.dw_acc = take((size_t)d->vocab * d->dim * 4);
+        if (rows < d->tokens) l.dw_acc = take((size_t)d->vocab * l.ld_acc * 4);
         l.dh_splits = dh_splits(rows, d, sms);
-        if (l.dh_splits > 1) l.dh_acc = take((size_t)l.dh_splits * rows * d->dim * 4);
+        if (l.dh_splits > 1) l.dh_acc = take((size_t)l.dh_splits * l.split_rows * l.ld_acc * 4);
     }
     if (pack_h) l.pack_h = take((size_t)d->tokens * l.ld_pack * 2);
     if (pack_w) l.pack_w = take((size_t)d->vocab * l.ld_pack * 2);
@@ -649,15 +736,16 @@ long long full_rows(const amsim_vocab_loss_desc *d)
 }
 
 template <int PRODUCT>
-int launch_product(const ProductParams &p, const CUtensorMap &a, const CUtensorMap &b, int sms, cudaStream_t st)
+int launch_product(const ProductParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, int sms,
+                   cudaStream_t st)
 {
     const cudaError_t attr =
         cudaFuncSetAttribute(product_kernel<PRODUCT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (attr != cudaSuccess) return cuda_status(attr);
     const long long tiles = (long long)p.mt * p.nt * p.splits;
     if (tiles > 0x7FFFFFFFLL - sms) return AMSIM_EUNSUPPORTED;
-    const int grid = (int)std::min<long long>(tiles, sms);
-    product_kernel<PRODUCT><<<grid, kThreads, kSmem, st>>>(p, a, b);
+    const int grid = 2 * (int)std::min<long long>(tiles, std::max(1, sms / 2));
+    product_kernel<PRODUCT><<<grid, kThreads, kSmem, st>>>(p, a, b, o);
     return launched();
 }
 
@@ -671,7 +759,7 @@ ProductParams product(long long m, long long n, long long k, int splits)
     p.nt = (int)((n + kTileN - 1) / kTileN);
     p.per_split = (p.kblocks + splits - 1) / splits;
     p.splits = (p.kblocks + p.per_split - 1) / p.per_split;
-    p.group = 16;
+    p.group = 8;
     return p;
 }
 
@@ -732,16 +820,16 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
     for (long long t0 = 0; t0 < d->tokens; t0 += rows) {
         const long long n = std::min(rows, d->tokens - t0);
         const bool first = t0 == 0, last = t0 + n == d->tokens;
-        CUtensorMap am, bm;
+        CUtensorMap am, bm, om;
         ProductParams p = product(n, d->vocab, d->dim, 1);
         p.targets = targets + t0;
         p.target_logit = target_logit;
         p.stats = stats;
         p.codes = codes;
-        p.ld_codes = l.ld_codes;
-        if ((rc = matrix_map(&am, H.p + t0 * H.ld, d->dim, n, H.ld, kTileM)) ||
-            (rc = matrix_map(&bm, W.p, d->dim, d->vocab, W.ld, kTileN)) ||
-            (rc = launch_product<kLogits>(p, am, bm, sms, st)))
+        if ((rc = matrix_map(&am, H.p + t0 * H.ld, d->dim, n, H.ld, kHalfM)) ||
+            (rc = matrix_map(&bm, W.p, d->dim, d->vocab, W.ld, kHalfN)) ||
+            (grad && (rc = matrix_map(&om, codes, d->vocab, n, l.ld_codes, 32))) ||
+            (rc = launch_product<kLogits>(p, am, bm, grad ? om : am, sms, st)))
             return rc;
         MergeParams q{};
         q.stats = stats;
@@ -773,22 +861,27 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         // dh = G W
         p = product(n, d->dim, d->vocab, l.dh_splits);
         bf16 *dh_out = static_cast<bf16 *>(dh) + t0 * ld_dh;
+        p.scale = &totals->scale;
         if (p.splits > 1) {
             p.acc = reinterpret_cast<float *>(base + l.dh_acc);
+            p.ld_acc = l.ld_acc;
+            p.split_rows = l.split_rows;
             p.acc_write = 1;
+            rc = matrix_map(&om, p.acc, d->dim, p.splits * l.split_rows, l.ld_acc, 32, true);
         } else {
             p.out = dh_out;
             p.ld_out = ld_dh;
-            p.vec = tma_rows(dh_out, ld_dh) && d->dim % 8 == 0;
+            p.boxes = tma_rows(dh_out, ld_dh);
+            om = am;
+            if (p.boxes) rc = matrix_map(&om, dh_out, d->dim, n, ld_dh, 32);
         }
-        p.scale = &totals->scale;
-        if ((rc = matrix_map(&am, g, d->vocab, n, l.ld_codes, kTileM)) ||
+        if (rc || (rc = matrix_map(&am, g, d->vocab, n, l.ld_codes, kHalfM)) ||
             (rc = matrix_map(&bm, W.p, d->dim, d->vocab, W.ld, kTileK)) ||
-            (rc = launch_product<kDh>(p, am, bm, sms, st)))
+            (rc = launch_product<kDh>(p, am, bm, om, sms, st)))
             return rc;
         if (p.splits > 1) {
-            join_kernel<<<(unsigned)std::min<long long>((n * d->dim + 255) / 256, sms * 8), 256, 0, st>>>(
-                p.acc, p.splits, n, d->dim, &totals->scale, dh_out, ld_dh);
+            join_kernel<<<dim3((unsigned)((d->dim + 255) / 256), (unsigned)n), 256, 0, st>>>(
+                p.acc, p.splits, l.split_rows, l.ld_acc, d->dim, &totals->scale, dh_out, ld_dh);
             if ((rc = launched())) return rc;
         }
         // dW = G^T h, over the chunks so far
@@ -796,17 +889,22 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         p.scale = &totals->scale;
         if (!(first && last)) {
             p.acc = dw_acc;
+            p.ld_acc = l.ld_acc;
             p.acc_read = !first;
             p.acc_write = !last;
         }
+        om = am;
         if (last) {
             p.out = static_cast<bf16 *>(dw);
             p.ld_out = ld_dw;
-            p.vec = tma_rows(dw, ld_dw) && d->dim % 8 == 0;
+            p.boxes = tma_rows(dw, ld_dw);
+            if (p.boxes) rc = matrix_map(&om, dw, d->dim, d->vocab, ld_dw, 32);
+        } else {
+            rc = matrix_map(&om, dw_acc, d->dim, d->vocab, l.ld_acc, 32, true);
         }
-        if ((rc = matrix_map(&am, g, d->vocab, n, l.ld_codes, kTileK)) ||
+        if (rc || (rc = matrix_map(&am, g, d->vocab, n, l.ld_codes, kTileK)) ||
             (rc = matrix_map(&bm, H.p + t0 * H.ld, d->dim, n, H.ld, kTileK)) ||
-            (rc = launch_product<kDw>(p, am, bm, sms, st)))
+            (rc = launch_product<kDw>(p, am, bm, om, sms, st)))
             return rc;
     }
     return AMSIM_OK;
