@@ -79,21 +79,26 @@ __device__ __forceinline__ unsigned long long now_ns()
 // timeout is recorded, `aborted` set, and every later wait of the thread
 // returns at once, so the thread runs to its end.  The timer is read once in
 // 1024 polls: a read takes longer than the waits between the roles of a CTA.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, bool &aborted)
+__device__ __noinline__ bool bar_wait_slow(uint64_t *bar, uint32_t parity)
 {
-    if (aborted) return false;
     unsigned long long t0 = 0;
     for (uint32_t i = 1; !bar_try(bar, parity); ++i) {
         if (i & 1023) continue;
         const unsigned long long t = now_ns();
         if (!t0) t0 = t;
         if (t - t0 > kWaitLimitNs) {
-            aborted = true;
             atomicOr(&g_wait_timeouts, (unsigned)AMSIM_WAIT_COPY);
             return false;
         }
     }
     return true;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, bool &aborted)
+{
+    if (aborted) return false;
+    if (bar_try(bar, parity)) return true;
+    aborted = !bar_wait_slow(bar, parity);
+    return !aborted;
 }
 
 // ------------------------------------------------------------------ CTA pairs
@@ -184,11 +189,9 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 // K-major operands (64 bf16 of K per row): stride = next 8 rows, leading unused.
 // MN-major operands (64 bf16 of M or N per row): stride = next 8 steps of K,
 // leading = next 64 rows of M or N.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t leading, uint32_t stride)
-{
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// The low word alone moves with the address, by 1 per 16 bytes.
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t leading) { return addr >> 4 | leading >> 4 << 16; }
+__host__ __device__ constexpr uint32_t desc_high(uint32_t stride) { return stride >> 4 | 1u << 14 | 2u << 29; }
 
 // Instruction descriptor: fp32 accumulator, bf16 A and B, their majors (0 K,
 // 1 MN), the M x N shape.
@@ -201,13 +204,16 @@ __host__ __device__ constexpr uint32_t instr_desc(int m, int n, int a_mn, int b_
 // D (tensor memory of both CTAs) = A B, + D when `acc`; 16 steps of K, one
 // issuing thread of the leader.  Each CTA holds its half of A's rows, its half
 // of B's columns, and the accumulator of its rows.
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_low, uint32_t a_high, uint32_t b_low, uint32_t b_high,
+                                    uint32_t idesc, bool acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(a_high), "r"(b_low), "r"(b_high), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
 

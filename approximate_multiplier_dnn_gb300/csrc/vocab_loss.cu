@@ -293,6 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // both CTAs copy their halves; the bytes of both are counted on the leader's barrier
         if (lane == 0) {
+            const uint32_t full_at = tc::leader_addr(full);
             int s = 0;
             uint32_t phase = 0;
             long long issued = 0;
@@ -303,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int k = t.split * p.per_split; k < k1; ++k) {
                     if (!tc::bar_wait(empty + s, phase ^ 1, aborted)) break;
                     uint8_t *a = ring + s * kStage, *b = a + kStageA;
-                    const uint32_t bar = tc::leader_addr(full + s);
+                    const uint32_t bar = full_at + s * 8;
                     if (rank == 0) tc::bar_expect(full + s, 2 * kStage);
                     if constexpr (a_mn) {
 #pragma unroll
@@ -331,36 +332,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
+            // One thread feeds both SMs' tensor cores 512 cycles of work per step
+            // of 64: what it computes per step is kept to an add per operand.
             constexpr uint32_t idesc = tc::instr_desc(kTileM, kTileN, a_mn, b_mn);
+            constexpr uint32_t high = tc::desc_high(1024);
+            constexpr uint32_t lead_a = a_mn ? kBox * kTileK * 2 : 16, lead_b = b_mn ? kBox * kTileK * 2 : 16;
+            constexpr uint32_t step_a = (a_mn ? 2048 : 32) / 16, step_b = (b_mn ? 2048 : 32) / 16;
+            const uint32_t a0 = tc::desc_low(tc::smem_addr(ring), lead_a);
+            const uint32_t b0 = tc::desc_low(tc::smem_addr(ring) + kStageA, lead_b);
             int s = 0;
             uint32_t phase = 0, count = 0;
             for (int i = pair; i < tiles && !aborted; i += pairs) {
                 const Tile t = tile_at(p, i);
-                const int k0 = t.split * p.per_split, k1 = min(p.kblocks, (t.split + 1) * p.per_split);
-                uint32_t half = 0, d = 0;
-                for (int k = k0; k < k1; ++k) {
-                    const bool fresh = (k - k0) % kSegment<PRODUCT> == 0;
-                    if (fresh) {
-                        half = count & 1;
-                        if (!tc::bar_wait(taken + half, (count >> 1 & 1) ^ 1, aborted)) break;
-                        tc::fence_after();
-                        d = tmem + half * kTileN;
-                        ++count;
-                    }
-                    if (!tc::bar_wait(full + s, phase, aborted)) break;
+                int left = min(p.kblocks, (t.split + 1) * p.per_split) - t.split * p.per_split;
+                while (left > 0 && !aborted) {
+                    const int n = min(left, kSegment<PRODUCT>);
+                    const uint32_t half = count & 1, d = tmem + half * kTileN;
+                    if (!tc::bar_wait(taken + half, (count >> 1 & 1) ^ 1, aborted)) break;
                     tc::fence_after();
-                    const uint32_t a = tc::smem_addr(ring + s * kStage), b = a + kStageA;
+                    for (int k = 0; k < n; ++k) {
+                        if (!tc::bar_wait(full + s, phase, aborted)) break;
+                        tc::fence_after();
+                        const uint32_t a = a0 + s * (kStage / 16), b = b0 + s * (kStage / 16);
 #pragma unroll
-                    for (int j = 0; j < kTileK / 16; ++j) {
-                        const uint64_t ad = a_mn ? tc::operand_desc(a + j * 2048, kBox * kTileK * 2, 1024)
-                                                 : tc::operand_desc(a + j * 32, 16, 1024);
-                        const uint64_t bd = b_mn ? tc::operand_desc(b + j * 2048, kBox * kTileK * 2, 1024)
-                                                 : tc::operand_desc(b + j * 32, 16, 1024);
-                        tc::mma(d, ad, bd, idesc, !fresh || j > 0);
+                        for (int j = 0; j < kTileK / 16; ++j)
+                            tc::mma(d, a + j * step_a, high, b + j * step_b, high, idesc, j > 0 || k > 0);
+                        tc::mma_commit(empty + s);
+                        if (++s == kStages) { s = 0; phase ^= 1; }
                     }
-                    tc::mma_commit(empty + s);
-                    if (++s == kStages) { s = 0; phase ^= 1; }
-                    if (k + 1 == k1 || (k + 1 - k0) % kSegment<PRODUCT> == 0) tc::mma_commit(ready + half);
+                    tc::mma_commit(ready + half);
+                    ++count;
+                    left -= n;
                 }
             }
             if (aborted) {      // instructions still running finish before the memory goes away
