@@ -101,6 +101,24 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, bool &a
     return !aborted;
 }
 
+// The same by a whole warp, all of whose lanes get one answer, so that its
+// control flow stays uniform.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, bool &aborted)
+{
+    if (aborted) return false;
+    if (__all_sync(0xFFFFFFFFu, bar_try(bar, parity))) return true;
+    aborted = !__all_sync(0xFFFFFFFFu, bar_wait_slow(bar, parity));
+    return !aborted;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // ------------------------------------------------------------------ CTA pairs
 // The kernels run in clusters of two CTAs on neighbouring SMs, which the
 // matrix instructions treat as one: rank 0 leads.

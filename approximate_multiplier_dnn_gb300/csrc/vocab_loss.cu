@@ -267,7 +267,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(buffers + 8 * kBuffer);
     uint64_t *empty = full + kStages, *ready = empty + kStages, *taken = ready + 2, *drained = taken + 2;
     uint32_t *slot = reinterpret_cast<uint32_t *>(drained + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the roles' loops are uniform over a warp (one lane issues): the copies and
+    // matrix instructions take their operands from uniform registers
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)tc::pair_rank(), pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
     if (warp == 0 && lane == 0) {
         tc::prefetch_map(&amap);
@@ -292,19 +294,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool aborted = false;
     if (warp == 0) {
         // both CTAs copy their halves; the bytes of both are counted on the leader's barrier
-        if (lane == 0) {
-            const uint32_t full_at = tc::leader_addr(full);
-            int s = 0;
-            uint32_t phase = 0;
-            long long issued = 0;
-            for (int i = pair; i < tiles && !aborted; i += pairs) {
-                const Tile t = tile_at(p, i);
-                const int m0 = t.m * kTileM + rank * kHalfM, n0 = t.n * kTileN + rank * kHalfN;
-                const int k1 = min(p.kblocks, (t.split + 1) * p.per_split);
-                for (int k = t.split * p.per_split; k < k1; ++k) {
-                    if (!tc::bar_wait(empty + s, phase ^ 1, aborted)) break;
-                    uint8_t *a = ring + s * kStage, *b = a + kStageA;
-                    const uint32_t bar = full_at + s * 8;
+        const bool one = tc::elect_one();
+        const uint32_t full_at = tc::leader_addr(full);
+        int s = 0;
+        uint32_t phase = 0;
+        long long issued = 0;
+        for (int i = pair; i < tiles && !aborted; i += pairs) {
+            const Tile t = tile_at(p, i);
+            const int m0 = t.m * kTileM + rank * kHalfM, n0 = t.n * kTileN + rank * kHalfN;
+            const int k1 = min(p.kblocks, (t.split + 1) * p.per_split);
+            for (int k = t.split * p.per_split; k < k1; ++k) {
+                if (!tc::warp_wait(empty + s, phase ^ 1, aborted)) break;
+                uint8_t *a = ring + s * kStage, *b = a + kStageA;
+                const uint32_t bar = full_at + s * 8;
+                if (one) {
                     if (rank == 0) tc::bar_expect(full + s, 2 * kStage);
                     if constexpr (a_mn) {
 #pragma unroll
@@ -320,20 +323,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     } else {
                         tc::load_box(b, &bmap, k * kTileK, n0, bar);
                     }
-                    ++issued;
-                    if (++s == kStages) { s = 0; phase ^= 1; }
                 }
+                ++issued;
+                if (++s == kStages) { s = 0; phase ^= 1; }
             }
-            // Every copy has landed and every release has arrived before the
-            // CTA's memory goes away: a released stage's copies were read.
-            bool gave_up = false;
-            for (long long j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
-                tc::bar_wait(empty + j % kStages, (uint32_t)(j / kStages & 1), gave_up);
         }
+        // Every copy has landed and every release has arrived before the CTA's
+        // memory goes away: a released stage's copies were read.
+        bool gave_up = false;
+        for (long long j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
+            tc::warp_wait(empty + j % kStages, (uint32_t)(j / kStages & 1), gave_up);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // One thread feeds both SMs' tensor cores 512 cycles of work per step
-            // of 64: what it computes per step is kept to an add per operand.
+        if (rank == 0) {
+            // One lane feeds both SMs' tensor cores 512 cycles of work per step
+            // of 64: what is computed per step is kept to an add per operand.
+            const bool one = tc::elect_one();
             constexpr uint32_t idesc = tc::instr_desc(kTileM, kTileN, a_mn, b_mn);
             constexpr uint32_t high = tc::desc_high(1024);
             constexpr uint32_t lead_a = a_mn ? kBox * kTileK * 2 : 16, lead_b = b_mn ? kBox * kTileK * 2 : 16;
@@ -348,27 +352,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 while (left > 0 && !aborted) {
                     const int n = min(left, kSegment<PRODUCT>);
                     const uint32_t half = count & 1, d = tmem + half * kTileN;
-                    if (!tc::bar_wait(taken + half, (count >> 1 & 1) ^ 1, aborted)) break;
+                    if (!tc::warp_wait(taken + half, (count >> 1 & 1) ^ 1, aborted)) break;
                     tc::fence_after();
                     for (int k = 0; k < n; ++k) {
-                        if (!tc::bar_wait(full + s, phase, aborted)) break;
+                        if (!tc::warp_wait(full + s, phase, aborted)) break;
                         tc::fence_after();
                         const uint32_t a = a0 + s * (kStage / 16), b = b0 + s * (kStage / 16);
+                        if (one) {
 #pragma unroll
-                        for (int j = 0; j < kTileK / 16; ++j)
-                            tc::mma(d, a + j * step_a, high, b + j * step_b, high, idesc, j > 0 || k > 0);
-                        tc::mma_commit(empty + s);
+                            for (int j = 0; j < kTileK / 16; ++j)
+                                tc::mma(d, a + j * step_a, high, b + j * step_b, high, idesc, j > 0 || k > 0);
+                            tc::mma_commit(empty + s);
+                            if (k + 1 == n) tc::mma_commit(ready + half);
+                        }
                         if (++s == kStages) { s = 0; phase ^= 1; }
                     }
-                    tc::mma_commit(ready + half);
                     ++count;
                     left -= n;
                 }
             }
             if (aborted) {      // instructions still running finish before the memory goes away
                 bool gave_up = false;
-                tc::mma_commit(drained);
-                tc::bar_wait(drained, 0, gave_up);
+                if (one) tc::mma_commit(drained);
+                tc::warp_wait(drained, 0, gave_up);
             }
         }
     } else {
@@ -378,14 +384,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int part = (warp - kFirstEpilogueWarp) >> 2, quarter = warp & 3;
         const Out out{buffers + (warp - kFirstEpilogueWarp) * kBuffer, &omap, lane};
         uint32_t count = 0;
-        // the next accumulator is complete; every lane waits, and the warp goes on together
+        // the next accumulator is complete
         auto next = [&](uint32_t &addr, uint32_t &half) {
             half = count & 1;
-            const bool ok = tc::bar_wait(ready + half, count >> 1 & 1, aborted);
+            const bool ok = tc::warp_wait(ready + half, count >> 1 & 1, aborted);
             ++count;
             tc::fence_after();
             addr = tmem + half * kTileN + part * kPiece + ((uint32_t)quarter * 32 << 16);
-            return __all_sync(0xFFFFFFFFu, ok) != 0;
+            return ok;
         };
         const uint32_t taken_at[2] = {tc::leader_addr(taken), tc::leader_addr(taken + 1)};
         // the accumulator has been read: one arrival per warp, on the leader's barrier
