@@ -132,6 +132,21 @@ struct Out {
     {
         reinterpret_cast<uint4 *>(buffer + lane * 128)[j ^ (lane & 7)] = make_uint4(a, b, c, d);
     }
+    // the same, by the warp's own coalesced stores, for rows that box copies
+    // cannot write: `rows` x `cols` elements of 16 bits to `dst`
+    __device__ __forceinline__ void end_rows(bf16 *dst, long long ld, int rows, int cols) const
+    {
+        __syncwarp();
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) {
+            const uint16_t *row = reinterpret_cast<const uint16_t *>(buffer + r * 128);
+#pragma unroll
+            for (int e = lane; e < 64; e += 32)
+                if (r < rows && e < cols)
+                    reinterpret_cast<uint16_t *>(dst)[r * ld + e] = row[((e >> 3) ^ (r & 7)) * 8 + (e & 7)];
+        }
+        __syncwarp();
+    }
     __device__ __forceinline__ void end(int x, int y, bool inside) const
     {
         tc::fence_staged();
@@ -150,18 +165,22 @@ template <bool MASKED>
 __device__ __forceinline__ void reduce_piece(const ProductParams &p, const float (&z)[kPiece], int row, int col0,
                                              const Out &out)
 {
-    float top = -INFINITY;
+    float tops[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) tops[j] = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kPiece; ++j)
-        if (!MASKED || col0 + j < p.n) top = fmaxf(top, z[j]);
+        if (!MASKED || col0 + j < p.n) tops[j & 7] = fmaxf(tops[j & 7], z[j]);
+    const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                            fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
     if (row < p.m) {
-    const long long d = p.targets[row] - col0;
-    if (d >= 0 && d < kPiece && col0 + d < p.n) {
-        float pick = 0.0f;
+        const long long d = p.targets[row] - col0;
+        if (d >= 0 && d < kPiece && col0 + d < p.n) {
+            float pick = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) select_if(pick, z[j], (int)d, j);
-        p.target_logit[row] = pick;
-    }
+            for (int j = 0; j < kPiece; ++j) select_if(pick, z[j], (int)d, j);
+            p.target_logit[row] = pick;
+        }
     }
     const float shift = top == -INFINITY ? 0.0f : top * kLog2e;
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -198,7 +217,7 @@ __device__ __forceinline__ void store_piece(const ProductParams &p, uint32_t tme
     const bool on = row < p.m, warp_on = row - out.lane < p.m && col0 < p.n;
     const float scale = p.out ? *p.scale : 1.0f;
     float *acc = p.acc ? p.acc + (split * p.split_rows + row) * p.ld_acc + col0 : nullptr;
-    if (p.acc_write || !p.boxes) {
+    if (p.acc_write) {
 #pragma unroll
         for (int c = 0; c < kPiece / 32; ++c) {
             uint32_t r[32];
@@ -211,18 +230,10 @@ __device__ __forceinline__ void store_piece(const ProductParams &p, uint32_t tme
                 for (int j = 0; j < 32; ++j)
                     if (j < left) r[j] = __float_as_uint(__uint_as_float(r[j]) + acc[c * 32 + j]);
             }
-            if (p.acc_write) {
-                out.begin();
+            out.begin();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) out.word(j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                out.end(col0 + c * 32, (int)(split * p.split_rows) + row - out.lane,
-                        warp_on && col0 + c * 32 < p.n);
-            } else {
-                bf16 *dst = p.out + row * p.ld_out + col0 + c * 32;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j < left) dst[j] = __float2bfloat16_rn(__uint_as_float(r[j]) * scale);
-            }
+            for (int j = 0; j < 8; ++j) out.word(j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            out.end(col0 + c * 32, (int)(split * p.split_rows) + row - out.lane, warp_on && col0 + c * 32 < p.n);
         }
         return;
     }
@@ -251,7 +262,9 @@ __device__ __forceinline__ void store_piece(const ProductParams &p, uint32_t tme
             const int i = c * 32 + j * 4;
             out.word(j, w[i], w[i + 1], w[i + 2], w[i + 3]);
         }
-        out.end(col0 + c * kBox, row - out.lane, warp_on && col0 + c * kBox < p.n);
+        const int row0 = row - out.lane, col = col0 + c * kBox;
+        if (p.boxes) out.end(col, row0, warp_on && col < p.n);
+        else out.end_rows(p.out + row0 * p.ld_out + col, p.ld_out, warp_on ? p.m - row0 : 0, p.n - col);
     }
 }
 
@@ -557,6 +570,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
 }
 
 // Codes to G, in place: G = weight (exp(top - lse - code / 2048) - [col == target]).
+// 4 bytes of traffic per element; the conversion of a code goes through the
+// mantissa of 2^23 + code, since the conversion instructions share the
+// exponential's unit, which alone needs 0.4 of the time of the bytes.
 struct GradParams {
     uint16_t *codes;
     const float2 *stats;
@@ -565,32 +581,56 @@ struct GradParams {
     long long ld;
     int rows, vocab;
 };
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 256, kGradSteps = 4;
+constexpr int kGradCols = kGradThreads * 8 * kGradSteps;      // of a block
 __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
 {
     const int row = blockIdx.y;
-    const int col = ((int)blockIdx.x * kGradThreads + (int)threadIdx.x) * 8;
-    if (col >= p.vocab) return;
+    const int col0 = (int)blockIdx.x * kGradCols + (int)threadIdx.x * 8;
+    uint16_t *codes = p.codes + row * p.ld;
     const float w = p.weight[row];
-    uint4 *at = reinterpret_cast<uint4 *>(p.codes + row * p.ld + col);
     if (w == 0.0f) {
-        *at = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kGradSteps; ++k)
+            if (col0 + k * kGradThreads * 8 < p.vocab)
+                *reinterpret_cast<uint4 *>(codes + col0 + k * kGradThreads * 8) = make_uint4(0, 0, 0, 0);
         return;
     }
-    const float top = p.stats[(long long)(col / kPiece) * p.rows + row].x;
-    const float base = (top - p.lse[row]) * kLog2e;
-    const long long d = p.targets[row] - col;
-    const uint4 q = *at;
-    const uint32_t c[4] = {q.x, q.y, q.z, q.w};
-    float g[8];
+    uint4 q[kGradSteps];
+    float base[kGradSteps];
+    const float lse = p.lse[row];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t code = j & 1 ? c[j >> 1] >> 16 : c[j >> 1] & 0xFFFFu;
-        g[j] = code == 65535u ? 0.0f : exp2_fast(fmaf((float)code, -kLog2e / kSteps, base));
-        if (d == j) g[j] -= 1.0f;
-        g[j] *= w;
+    for (int k = 0; k < kGradSteps; ++k) {
+        const int col = col0 + k * kGradThreads * 8;
+        if (col < p.vocab) {
+            q[k] = *reinterpret_cast<const uint4 *>(codes + col);
+            base[k] = p.stats[(long long)(col / kPiece) * p.rows + row].x;
+        }
     }
-    *at = make_uint4(pack2(g[0], g[1]), pack2(g[2], g[3]), pack2(g[4], g[5]), pack2(g[6], g[7]));
+    const long long target = p.targets[row];
+#pragma unroll
+    for (int k = 0; k < kGradSteps; ++k) {
+        const int col = col0 + k * kGradThreads * 8;
+        if (col >= p.vocab) break;
+        const float shift = (base[k] - lse) * kLog2e;
+        const uint32_t c[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+        float g[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t bits = __byte_perm(c[j >> 1], 0x4B00u, j & 1 ? 0x5432 : 0x5410);
+            const float code = __uint_as_float(bits) - 8388608.0f;
+            // the last code stands for everything from 32 below the maximum on
+            g[j] = code == 65535.0f ? 0.0f : exp2_fast(fmaf(code, -kLog2e / kSteps, shift));
+        }
+        const long long d = target - col;
+        if (d >= 0 && d < 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j == (int)d) g[j] -= 1.0f;
+        }
+        *reinterpret_cast<uint4 *>(codes + col) = make_uint4(pack2(g[0] * w, g[1] * w), pack2(g[2] * w, g[3] * w),
+                                                             pack2(g[4] * w, g[5] * w), pack2(g[6] * w, g[7] * w));
+    }
 }
 
 // dh of a row range from the splits' sums, in split order.
@@ -606,14 +646,35 @@ __global__ void __launch_bounds__(256) join_kernel(const float *acc, int splits,
     out[row * ld + col] = __float2bfloat16_rn(s * *scale);
 }
 
-// An operand whose rows TMA cannot take (base or row stride not a multiple of
-// 16 bytes) is copied into rows that it can.
-__global__ void __launch_bounds__(256) pack_kernel(const bf16 *src, long long ld, bf16 *dst, long long ld_dst,
-                                                   long long rows, int cols)
+// Copies an operand into rows of whole 128-byte lines.  Eight elements per
+// thread, read as 32-bit words even where the rows are only 2-byte aligned;
+// single elements at the tensor's start and at the rows' ends, so that nothing
+// outside the rows' span is read.
+constexpr int kPackThreads = 256;
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint16_t *src, long long ld, uint16_t *dst,
+                                                            long long ld_dst, long long rows, int cols, int block_rows)
 {
-    const long long n = rows * cols;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256)
-        dst[i / cols * ld_dst + i % cols] = src[i / cols * ld + i % cols];
+    const int chunks = (cols + 7) / 8;
+    const long long r0 = (long long)blockIdx.x * block_rows;
+    const int n = (int)min((long long)block_rows, rows - r0) * chunks;
+    for (int i = threadIdx.x; i < n; i += kPackThreads) {
+        const int r = i / chunks, c = (i - r * chunks) * 8;
+        const uint16_t *from = src + (r0 + r) * ld + c;
+        uint16_t *to = dst + (r0 + r) * ld_dst + c;
+        const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(from) & 2);
+        if (c + 8 < cols && (!odd || r0 + r + c > 0)) {
+            const uint32_t *word = reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)3);
+            uint32_t w[5];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = word[j];
+            w[4] = odd ? word[4] : 0u;
+            *reinterpret_cast<uint4 *>(to) =
+                make_uint4(__funnelshift_r(w[0], w[1], odd * 8), __funnelshift_r(w[1], w[2], odd * 8),
+                           __funnelshift_r(w[2], w[3], odd * 8), __funnelshift_r(w[3], w[4], odd * 8));
+        } else {
+            for (int j = 0; j < 8 && c + j < cols; ++j) to[j] = from[j];
+        }
+    }
 }
 
 __global__ void zero_loss_kernel(float *loss) { *loss = 0.0f; }
@@ -621,7 +682,6 @@ __global__ void zero_loss_kernel(float *loss) { *loss = 0.0f; }
 // ------------------------------------------------------------------ host
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-long long up8(long long x) { return (x + 7) & ~7LL; }
 
 int launched()
 {
@@ -716,8 +776,8 @@ Layout layout(const amsim_vocab_loss_desc *d, bool grad, long long rows, bool pa
     l.weight = take((size_t)rows * 4);
     l.target_logit = take((size_t)rows * 4);
     l.stats = take((size_t)pieces * rows * 8);
-    l.ld_pack = up8(d->dim);
-    l.ld_codes = up8(d->vocab);
+    l.ld_codes = (d->vocab + 63) & ~63LL;       // rows of whole 128-byte lines
+    l.ld_pack = (d->dim + 63) & ~63LL;
     l.ld_acc = (d->dim + 3) & ~3LL;
     l.split_rows = (rows + kTileM - 1) / kTileM * kTileM;   // whole tiles: a box never reaches the next split
     l.dh_splits = 1;
@@ -735,10 +795,22 @@ Layout layout(const amsim_vocab_loss_desc *d, bool grad, long long rows, bool pa
 
 bool tma_rows(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
+// An operand is copied into aligned rows when TMA cannot take its own (base or
+// stride off 16 bytes).  h is copied also when its rows are not whole 128-byte
+// lines, so that each 128-byte row of a tile straddles two, and there are
+// enough tokens: 1024 x 50021 x 1000 with gradients takes 298 us without the
+// copy and 273 with it, 512 tokens 186 and 183, 128 tokens 123 and 128.  W is
+// not: the copy gained 1 % at 4096 tokens and lost 5 % at 1531.
+constexpr int64_t kPackTokens = 1024;
+bool pack_h(const void *h, int64_t ld, int64_t tokens)
+{
+    return !tma_rows(h, ld) || (tokens >= kPackTokens && (ld % 64 != 0 || !aligned(h, 128)));
+}
+
 long long full_rows(const amsim_vocab_loss_desc *d)
 {
     long long rows = std::min<long long>(d->tokens, kMostRows);
-    const long long cap = (long long)(kCodesCap / ((size_t)up8(d->vocab) * 2));
+    const long long cap = (long long)(kCodesCap / ((size_t)((d->vocab + 63) & ~63LL) * 2));
     if (rows > cap) rows = std::max<long long>(kTileM, cap / kTileM * kTileM);
     return std::min<long long>(rows, d->tokens);
 }
@@ -794,13 +866,13 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         return AMSIM_EINVAL;
     const int sms = device_sms();
     if (!sms) return AMSIM_ECUDA;
-    const bool pack_h = !tma_rows(h, ld_h), pack_w = !tma_rows(w, ld_w);
+    const bool copy_h = pack_h(h, ld_h, d->tokens), copy_w = !tma_rows(w, ld_w);
     long long rows = full_rows(d);
-    Layout l = layout(d, grad, rows, pack_h, pack_w, sms);
+    Layout l = layout(d, grad, rows, copy_h, copy_w, sms);
     while (l.bytes > ws_bytes) {              // smaller chunks: whole row tiles, down to one
         if (rows <= kTileM) return AMSIM_EINVAL;
         rows = std::max<long long>(kTileM, (rows / 2 + kTileM - 1) / kTileM * kTileM);
-        l = layout(d, grad, rows, pack_h, pack_w, sms);
+        l = layout(d, grad, rows, copy_h, copy_w, sms);
     }
     uint8_t *base = static_cast<uint8_t *>(ws);
     Totals *totals = reinterpret_cast<Totals *>(base + l.totals);
@@ -811,13 +883,15 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
     Matrix H{static_cast<const bf16 *>(h), ld_h}, W{static_cast<const bf16 *>(w), ld_w};
     auto pack = [&](Matrix &m, size_t off, long long n) {
         bf16 *dst = reinterpret_cast<bf16 *>(base + off);
-        pack_kernel<<<(unsigned)std::min<long long>((n * d->dim + 1023) / 1024, sms * 8), 256, 0, st>>>(
-            m.p, m.ld, dst, l.ld_pack, n, d->dim);
+        const int block_rows = std::max(1, 2048 / ((d->dim + 7) / 8));
+        pack_kernel<<<(unsigned)((n + block_rows - 1) / block_rows), kPackThreads, 0, st>>>(
+            reinterpret_cast<const uint16_t *>(m.p), m.ld, reinterpret_cast<uint16_t *>(dst), l.ld_pack, n, d->dim,
+            block_rows);
         m = Matrix{dst, l.ld_pack};
         return launched();
     };
-    if (pack_h && (rc = pack(H, l.pack_h, d->tokens))) return rc;
-    if (pack_w && (rc = pack(W, l.pack_w, d->vocab))) return rc;
+    if (copy_h && (rc = pack(H, l.pack_h, d->tokens))) return rc;
+    if (copy_w && (rc = pack(W, l.pack_w, d->vocab))) return rc;
 
     uint16_t *codes = grad ? reinterpret_cast<uint16_t *>(base + l.codes) : nullptr;
     const bf16 *g = reinterpret_cast<const bf16 *>(codes);
@@ -863,8 +937,7 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         if ((rc = launched())) return rc;
         if (!grad) continue;
         GradParams e{codes, stats, q.lse, weight, targets + t0, l.ld_codes, (int)n, d->vocab};
-        grad_kernel<<<dim3((unsigned)((d->vocab + kGradThreads * 8 - 1) / (kGradThreads * 8)), (unsigned)n),
-                      kGradThreads, 0, st>>>(e);
+        grad_kernel<<<dim3((unsigned)((d->vocab + kGradCols - 1) / kGradCols), (unsigned)n), kGradThreads, 0, st>>>(e);
         if ((rc = launched())) return rc;
         // dh = G W
         p = product(n, d->dim, d->vocab, l.dh_splits);
