@@ -10,6 +10,7 @@ library is not built or no GPU is present.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -270,10 +271,25 @@ def _ptr(t) -> int | None:
     raise TypeError(f"cannot take a pointer of {type(t)}")
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """torch's current stream on the current device, as a raw handle."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        get, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if get is not None and device is not None:
+            _raw_stream = lambda: get(device())     # without building a Stream object: a tenth of the time
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return _raw_stream()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -632,13 +648,14 @@ def _dtype(t) -> int:
 
 def _rows(name, t, rows, cols, dtype=None) -> int:
     """Row stride of a CUDA matrix of `rows` x `cols` whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if tuple(t.shape) != (rows, cols):
         raise ValueError(f"{name} must be {rows} x {cols}, not {tuple(t.shape)}")
     if not t.is_cuda or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be a CUDA tensor{'' if dtype is None else ' of ' + str(dtype)}")
-    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+    outer, inner = t.stride()
+    if cols > 1 and inner != 1 or rows > 1 and outer < cols:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.stride(0) if rows > 1 else cols
+    return outer if rows > 1 else cols
 
 
 def _vector(name, t, n, dtype):
@@ -648,23 +665,41 @@ def _vector(name, t, n, dtype):
         raise ValueError(f"{name} must hold {n} contiguous values")
 
 
-def _block_norm_desc(first, y, gate, w_post, w_pre, alpha, eps):
-    """Descriptor of a block norm over rows like `first`'s, its vectors checked."""
+# Descriptors and scratch sizes by the sizes and types of a call: a small call's
+# time is the host's, and building them costs more than its launch.
+@functools.lru_cache(maxsize=1024)
+def _block_norm_plan(rows, cols, gate_rows, x, y, n, r, dr, dn, alpha, eps, backward):
+    """(descriptor by reference, scratch bytes); x, y, n: (type, row stride)."""
+    d = BlockNormDesc(rows=rows, cols=cols, gate_rows=gate_rows, alpha=alpha, eps=eps, x_type=x[0], ldx=x[1],
+                      y_type=y[0], ldy=y[1], n_type=n[0], ldr=r, lddr=dr, lddn=dn)
+    return ctypes.byref(d), amsim_block_norm_workspace_size(d) if backward else 0
+
+
+@functools.lru_cache(maxsize=1024)
+def _vocab_plan(tokens, vocab, dim, ld_h, ld_w, ignore_index, reduction):
+    """(descriptor by reference, scratch bytes of the loss, of the gradients)."""
+    d = VocabLossDesc(tokens=tokens, vocab=vocab, dim=dim, ld_h=ld_h, ld_w=ld_w, ignore_index=ignore_index,
+                      reduction=REDUCTIONS[reduction])
+    return ctypes.byref(d), amsim_vocab_loss_workspace_size(d, 0), amsim_vocab_loss_workspace_size(d, 1)
+
+
+def _gate_rows(first, gate, w_post, w_pre):
+    """Rows per row of the gate (0 without one), the vectors of a block norm over rows like `first`'s checked."""
     import torch
     if first.dim() != 2:
         raise ValueError("block norms take matrices of rows x channels")
     rows, cols = first.shape
-    d = BlockNormDesc(rows=rows, cols=cols, alpha=alpha, eps=eps)
-    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-        if t is not None:
-            _vector(name, t, cols, torch.float32)
-    if gate is not None:
-        groups = gate.numel() // cols
-        _vector("gate", gate, max(1, groups) * cols, torch.float32)
-        if groups < 1 or rows % groups:
-            raise ValueError(f"gate must have one row of {cols} values for every so many of the {rows} rows")
-        d.gate_rows = rows // groups
-    return d
+    if w_post is not None:
+        _vector("w_post", w_post, cols, torch.float32)
+    if w_pre is not None:
+        _vector("w_pre", w_pre, cols, torch.float32)
+    if gate is None:
+        return 0
+    groups = gate.numel() // cols
+    _vector("gate", gate, max(1, groups) * cols, torch.float32)
+    if groups < 1 or rows % groups:
+        raise ValueError(f"gate must have one row of {cols} values for every so many of the {rows} rows")
+    return rows // groups
 
 
 def block_norm(x, y=None, w_post=None, w_pre=None, *, gate=None, alpha=1.0, eps=1e-6, n_dtype=None):
@@ -674,17 +709,20 @@ def block_norm(x, y=None, w_post=None, w_pre=None, *, gate=None, alpha=1.0, eps=
     gate: [groups, channels], one row for each rows / groups consecutive rows, or None.  n has type `n_dtype` (y's,
     or x's).  rstd_post is None without w_post."""
     import torch
-    d = _block_norm_desc(x, y, gate, w_post, w_pre, alpha, eps)
+    gate_rows = _gate_rows(x, gate, w_post, w_pre)
     rows, cols = x.shape
-    d.x_type, d.ldx = _dtype(x), _rows("x", x, rows, cols)
-    if y is not None:
-        d.y_type, d.ldy = _dtype(y), _rows("y", y, rows, cols)
-    n = torch.empty((rows, cols), dtype=n_dtype or (x if y is None else y).dtype, device=x.device)
-    d.n_type = _dtype(n)
-    r = x if y is None else torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    rstd_pre = torch.empty(rows, dtype=torch.float32, device=x.device)
-    rstd_post = None if w_post is None else torch.empty_like(rstd_pre)
-    amsim_block_norm_fwd(d, x, y, gate, w_post, w_pre, None if y is None else r, n, rstd_post, rstd_pre)
+    xs = (_dtype(x), _rows("x", x, rows, cols))
+    ys = (AMSIM_F32, 0) if y is None else (_dtype(y), _rows("y", y, rows, cols))
+    empty, device = torch.empty, x.device
+    n = empty((rows, cols), dtype=n_dtype or (x if y is None else y).dtype, device=device)
+    desc, _ = _block_norm_plan(rows, cols, gate_rows, xs, ys, (_dtype(n), 0), 0, 0, 0, alpha, eps, False)
+    r = x if y is None else empty((rows, cols), dtype=x.dtype, device=device)
+    rstd_pre = empty(rows, dtype=torch.float32, device=device)
+    rstd_post = None if w_post is None else empty(rows, dtype=torch.float32, device=device)
+    _check("amsim_block_norm_fwd",
+           lib().amsim_block_norm_fwd(desc, x.data_ptr(), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre),
+                                      None if y is None else r.data_ptr(), n.data_ptr(), _ptr(rstd_post),
+                                      rstd_pre.data_ptr(), _current_stream()))
     return r, n, rstd_post, rstd_pre
 
 
@@ -692,71 +730,80 @@ def block_norm_backward(dr, dn, r, y, w_post, w_pre, rstd_post, rstd_pre, *, gat
     """Gradients of block_norm: (dx, dy, dgate, dw_post, dw_pre), None where there was no such input.  dr or dn may
     be None (zeros); r, rstd_post and rstd_pre are block_norm's."""
     import torch
-    d = _block_norm_desc(r, y, gate, w_post, w_pre, alpha, 0.0)
+    gate_rows = _gate_rows(r, gate, w_post, w_pre)
     rows, cols = r.shape
-    d.x_type, d.ldr = _dtype(r), _rows("r", r, rows, cols)
+    f32, empty, device = torch.float32, torch.empty, r.device
+    ys, ns, lddr, lddn = (AMSIM_F32, 0), (AMSIM_F32, 0), 0, 0
+    ldr = _rows("r", r, rows, cols)
     if dr is not None:
-        d.lddr = _rows("dr", dr, rows, cols, r.dtype)
+        lddr = _rows("dr", dr, rows, cols, r.dtype)
     if dn is not None:
-        d.n_type, d.lddn = _dtype(dn), _rows("dn", dn, rows, cols)
-        _vector("rstd_pre", rstd_pre, rows, torch.float32)
-    dx = torch.empty((rows, cols), dtype=r.dtype, device=r.device)
+        ns, lddn = (_dtype(dn), 0), _rows("dn", dn, rows, cols)
+        _vector("rstd_pre", rstd_pre, rows, f32)
+    dx = empty((rows, cols), dtype=r.dtype, device=device)
     dy = dgate = dw_post = dw_pre = None
     if y is not None:
-        d.y_type, d.ldy = _dtype(y), _rows("y", y, rows, cols)
-        dy = torch.empty((rows, cols), dtype=y.dtype, device=r.device)
+        ys = (_dtype(y), _rows("y", y, rows, cols))
+        dy = empty((rows, cols), dtype=y.dtype, device=device)
     if gate is not None:
         dgate = torch.empty_like(gate)
     if w_post is not None:
-        _vector("rstd_post", rstd_post, rows, torch.float32)
+        _vector("rstd_post", rstd_post, rows, f32)
         dw_post = torch.empty_like(w_post)
     if w_pre is not None:
         dw_pre = torch.empty_like(w_pre) if dn is not None else torch.zeros_like(w_pre)
-    nb = amsim_block_norm_workspace_size(d)
-    ws = workspace(nb, r.device) if nb else None
-    amsim_block_norm_bwd(d, dr, dn, r, y, gate, w_post, w_pre, rstd_post, rstd_pre, dx, dy, dgate, dw_post,
-                         dw_pre if dn is not None else None, ws=ws)
+    desc, nb = _block_norm_plan(rows, cols, gate_rows, (_dtype(r), 0), ys, ns, ldr, lddr, lddn, alpha, 0.0, True)
+    ws = empty(nb, dtype=torch.uint8, device=device) if nb else None
+    _check("amsim_block_norm_bwd",
+           lib().amsim_block_norm_bwd(desc, _ptr(dr), _ptr(dn), r.data_ptr(), _ptr(y), _ptr(gate), _ptr(w_post),
+                                      _ptr(w_pre), _ptr(rstd_post), _ptr(rstd_pre), dx.data_ptr(), _ptr(dy),
+                                      _ptr(dgate), _ptr(dw_post), _ptr(dw_pre) if dn is not None else None, _ptr(ws),
+                                      nb, _current_stream()))
     return dx, dy, dgate, dw_post, dw_pre
 
 
-def _vocab_desc(h, w, targets, row_weight, ignore_index, reduction):
+def _vocab_call(h, w, targets, row_weight, ignore_index, reduction):
     import torch
     if h.dim() != 2 or w.dim() != 2:
         raise ValueError("the vocabulary loss takes h [tokens, dim] and w [vocab, dim]")
     tokens, dim = h.shape
-    d = VocabLossDesc(tokens=tokens, vocab=w.shape[0], dim=dim, ignore_index=ignore_index,
-                      reduction=REDUCTIONS[reduction])
-    d.ld_h = _rows("h", h, tokens, dim, torch.bfloat16)
-    d.ld_w = _rows("w", w, w.shape[0], dim, torch.bfloat16)
+    vocab = w.shape[0]
+    bf16 = torch.bfloat16
+    plan = _vocab_plan(tokens, vocab, dim, _rows("h", h, tokens, dim, bf16), _rows("w", w, vocab, dim, bf16),
+                       ignore_index, reduction)
     _vector("targets", targets, tokens, torch.int64)
     if row_weight is not None:
         _vector("row_weight", row_weight, tokens, torch.float32)
-    return d
+    empty, device = torch.empty, h.device
+    row = empty(tokens, dtype=torch.float32, device=device)
+    return plan, empty(1, dtype=torch.float32, device=device), row, torch.empty_like(row)
 
 
 def vocab_loss(h, w, targets, *, row_weight=None, ignore_index=-100, reduction="mean"):
     """Cross entropy of softmax(h w^T) against the targets, without the logits: (loss [1], row_loss, lse).
     h [tokens, dim] and w [vocab, dim] bf16, targets int64; reduction "mean" (over the tokens' weights) or "sum"."""
     import torch
-    d = _vocab_desc(h, w, targets, row_weight, ignore_index, reduction)
-    out = torch.empty((2, d.tokens), dtype=torch.float32, device=h.device)
-    loss = torch.empty(1, dtype=torch.float32, device=h.device)
-    ws = workspace(amsim_vocab_loss_workspace_size(d, 0), h.device)
-    amsim_vocab_loss(d, h, w, targets, row_weight, loss, out[0], out[1], ws=ws)
-    return loss, out[0], out[1]
+    (desc, nb, _), loss, row, lse = _vocab_call(h, w, targets, row_weight, ignore_index, reduction)
+    ws = torch.empty(nb, dtype=torch.uint8, device=h.device)
+    _check("amsim_vocab_loss",
+           lib().amsim_vocab_loss(desc, h.data_ptr(), w.data_ptr(), targets.data_ptr(), _ptr(row_weight),
+                                  loss.data_ptr(), row.data_ptr(), lse.data_ptr(), ws.data_ptr(), nb,
+                                  _current_stream()))
+    return loss, row, lse
 
 
 def vocab_loss_grad(h, w, targets, *, row_weight=None, ignore_index=-100, reduction="mean"):
     """vocab_loss and the loss's gradients: (loss, row_loss, lse, dh, dw), dh and dw bf16."""
     import torch
-    d = _vocab_desc(h, w, targets, row_weight, ignore_index, reduction)
-    out = torch.empty((2, d.tokens), dtype=torch.float32, device=h.device)
-    loss = torch.empty(1, dtype=torch.float32, device=h.device)
-    dh = torch.empty((d.tokens, d.dim), dtype=torch.bfloat16, device=h.device)
-    dw = torch.empty((d.vocab, d.dim), dtype=torch.bfloat16, device=h.device)
-    ws = workspace(amsim_vocab_loss_workspace_size(d, 1), h.device)
-    amsim_vocab_loss_grad(d, h, w, targets, row_weight, loss, out[0], out[1], dh, dw, ws=ws)
-    return loss, out[0], out[1], dh, dw
+    (desc, _, nb), loss, row, lse = _vocab_call(h, w, targets, row_weight, ignore_index, reduction)
+    empty, bf16, device = torch.empty, torch.bfloat16, h.device
+    dh, dw = empty(h.shape, dtype=bf16, device=device), empty(w.shape, dtype=bf16, device=device)
+    ws = empty(nb, dtype=torch.uint8, device=device)
+    _check("amsim_vocab_loss_grad",
+           lib().amsim_vocab_loss_grad(desc, h.data_ptr(), w.data_ptr(), targets.data_ptr(), _ptr(row_weight),
+                                       loss.data_ptr(), row.data_ptr(), lse.data_ptr(), dh.data_ptr(), dw.data_ptr(),
+                                       ws.data_ptr(), nb, _current_stream()))
+    return loss, row, lse, dh, dw
 
 
 def adamw_table(tensors):
@@ -776,11 +823,13 @@ def adamw_step(table, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, step, grad_scale=
 def adamw_moment_values(codes, scales):
     """fp32 values of an 8-bit moment's codes (int8: first moment, uint8: second), in the codes' shape."""
     import torch
-    n = codes.numel()
-    if codes.dtype not in (torch.int8, torch.uint8):
+    n, second = codes.numel(), codes.dtype == torch.uint8
+    if not second and codes.dtype != torch.int8:
         raise TypeError("moment codes are int8 (first moment) or uint8 (second)")
     _vector("codes", codes, n, codes.dtype)
     _vector("scales", scales, -(-n // AMSIM_ADAMW_BLOCK), torch.float32)
     out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
-    amsim_adamw_moment_values(codes, scales, codes.dtype == torch.uint8, n, out)
+    _check("amsim_adamw_moment_values",
+           lib().amsim_adamw_moment_values(codes.data_ptr(), scales.data_ptr(), 1 if second else 0, n, out.data_ptr(),
+                                           _current_stream()))
     return out

@@ -122,6 +122,8 @@ struct TmaRawMap {
 // Encode a tiled fp32 tensor map (zero fill out of bounds) into `map` (a
 // CUtensorMap); AMSIM_EUNSUPPORTED when the driver refuses it.
 int encode_tensor_map(::CUtensorMap_st *map, const TmaRawMap &m);
+// The current device and (cached) its number of SMs; -1 without a device.
+int current_device(int *sms);
 // The driver's cuTensorMapEncodeTiled (null when the driver lacks it), for maps of other types.
 void *tensor_map_encoder();
 struct ConvRaw {

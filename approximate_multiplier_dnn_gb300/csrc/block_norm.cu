@@ -60,13 +60,8 @@ int64_t stride(int64_t ld, int cols) { return ld ? ld : cols; }
 
 int device_sms()
 {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
-        cudaGetLastError();
-        return 0;
-    }
-    return sms;
+    int sms = 0;
+    return amsim::current_device(&sms) < 0 ? 0 : sms;
 }
 
 int check(const amsim_block_norm_desc *d)

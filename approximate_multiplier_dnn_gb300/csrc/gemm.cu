@@ -1161,6 +1161,17 @@ void set_last_path(int bits) { g_last_path = bits; }
 
 int encode_tensor_map(CUtensorMap_st *map, const TmaRawMap &m) { return encode_raw_spec(map, m); }
 
+int current_device(int *sms)
+{
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return -1;
+    }
+    *sms = device_sms(dev);
+    return dev;
+}
+
 void *tensor_map_encoder() { return reinterpret_cast<void *>(encode_tiled()); }
 
 }  // namespace amsim

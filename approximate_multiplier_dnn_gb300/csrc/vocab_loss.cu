@@ -18,6 +18,7 @@
 // G, W and h as they lie in memory: an operand whose rows run along M or N
 // instead of K only changes its descriptor.
 #include <algorithm>
+#include <atomic>
 
 #include "tensor_core.cuh"
 
@@ -60,6 +61,7 @@ struct ProductParams {
     const int64_t *targets;         // of the chunk's rows
     float *target_logit;
     float2 *stats;                  // [piece][rows]: maximum, sum of exponentials
+    unsigned int *done;             // the merge's count of blocks, zeroed here
     const uint16_t *codes;          // null: not wanted; else the output map is over them
     // kDh, kDw
     bf16 *out;
@@ -299,6 +301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tc::tmem_alloc<512>(slot);
+    if (PRODUCT == kLogits && blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
     tc::fence_before();
     tc::pair_sync();
     tc::fence_after();
@@ -564,7 +567,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
         if (p.first_chunk) t->scale = !p.mean ? 1.0f : weight != 0.0f ? 1.0f / weight : 0.0f;
         else loss += t->loss;
         t->loss = loss;
-        t->done = 0;
         if (p.last_chunk) *p.loss = loss * t->scale;
     }
 }
@@ -731,13 +733,8 @@ int check(const amsim_vocab_loss_desc *d)
 
 int device_sms()
 {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
-        cudaGetLastError();
-        return 0;
-    }
-    return sms;
+    int sms = 0;
+    return current_device(&sms) < 0 ? 0 : sms;
 }
 
 // Scratch of a call over chunks of `rows` tokens.
@@ -819,9 +816,16 @@ template <int PRODUCT>
 int launch_product(const ProductParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, int sms,
                    cudaStream_t st)
 {
-    const cudaError_t attr =
-        cudaFuncSetAttribute(product_kernel<PRODUCT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (attr != cudaSuccess) return cuda_status(attr);
+    static std::atomic<uint64_t> allowed{0};          // devices on which the kernel may have its shared memory
+    int n = 0;
+    const int dev = current_device(&n);
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (!bit || !(allowed.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(product_kernel<PRODUCT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return cuda_status(e);
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     const long long tiles = (long long)p.mt * p.nt * p.splits;
     if (tiles > 0x7FFFFFFFLL - sms) return AMSIM_EUNSUPPORTED;
     const int grid = 2 * (int)std::min<long long>(tiles, std::max(1, sms / 2));
@@ -876,10 +880,6 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
     }
     uint8_t *base = static_cast<uint8_t *>(ws);
     Totals *totals = reinterpret_cast<Totals *>(base + l.totals);
-    if (cudaMemsetAsync(totals, 0, sizeof(Totals), st) != cudaSuccess) {
-        cudaGetLastError();
-        return AMSIM_ECUDA;
-    }
     Matrix H{static_cast<const bf16 *>(h), ld_h}, W{static_cast<const bf16 *>(w), ld_w};
     auto pack = [&](Matrix &m, size_t off, long long n) {
         bf16 *dst = reinterpret_cast<bf16 *>(base + off);
@@ -907,6 +907,7 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         p.targets = targets + t0;
         p.target_logit = target_logit;
         p.stats = stats;
+        p.done = &totals->done;
         p.codes = codes;
         if ((rc = matrix_map(&am, H.p + t0 * H.ld, d->dim, n, H.ld, kHalfM)) ||
             (rc = matrix_map(&bm, W.p, d->dim, d->vocab, W.ld, kHalfN)) ||
