@@ -9,52 +9,65 @@ namespace {
 
 using amsim::bn::Params;
 
-// dgate, dw_post and dw_pre from the shares' sums, in share order.  A block
-// takes 32 channels; its warps take the shares in turn and add up at the end.
-__global__ void __launch_bounds__(512) sums_kernel(const Params p, int blocks)
+// dgate, dw_post and dw_pre from the shares' sums, in a fixed order: a block
+// takes 32 channels, its 32 warps every 32nd share, eight loads at a time.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32) sums_kernel(const Params p, int blocks)
 {
-    __shared__ float part[16][33];
+    __shared__ float part[kSumWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (int)blockIdx.x * 32 + lane;
     const bool on = c < p.cols;
     auto total = [&](const float *src, long long n) {
         float s = 0.0f;
-        if (on)
-            for (long long i = warp; i < n; i += 16) s += src[i * p.cols + c];
+        if (on) {
+#pragma unroll 8
+            for (long long i = warp; i < n; i += kSumWarps) s += src[i * p.cols + c];
+        }
         __syncthreads();
         part[warp][lane] = s;
         __syncthreads();
-        s = 0.0f;
-        if (warp == 0)
+        s = part[lane][warp];                  // channel `warp` of the block: its shares across the lanes
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s += part[i][lane];
-        return s;                              // warp 0 holds the sum
+        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        return s;                              // every lane of warp i: channel i
     };
+    const int mine = (int)blockIdx.x * 32 + warp;
+    const bool out = lane == 0 && mine < p.cols;
     if (blockIdx.y == 0) {
         if (!p.dw_pre || !p.part_pre) return;
         const float s = total(p.part_pre, blocks);
-        if (warp == 0 && on) p.dw_pre[c] = s;
+        if (out) p.dw_pre[mine] = s;
         return;
     }
     if (p.splits == 1) {
         if (!p.dw_post || !p.part_post) return;
         const float s = total(p.part_post, blocks);
-        if (warp == 0 && on) p.dw_post[c] = s;
+        if (out) p.dw_post[mine] = s;
         return;
     }
     if (!p.part_gate) return;
     const long long groups = p.items / p.splits;
-    const float w = on && p.w_post ? p.w_post[c] : 1.0f;
+    const float w = out && p.w_post ? p.w_post[mine] : 1.0f;
     float dw = 0.0f;
     for (long long g = 0; g < groups; ++g) {
         const float s = total(p.part_gate + g * p.splits * p.cols, p.splits);
-        if (p.dgate && warp == 0 && on) p.dgate[g * p.cols + c] = p.alpha * w * s;
-        dw = fmaf(p.alpha * (on && p.gate ? p.gate[g * p.cols + c] : 1.0f), s, dw);
+        if (out && p.dgate) p.dgate[g * p.cols + mine] = p.alpha * w * s;
+        dw = fmaf(p.alpha * (out && p.gate ? p.gate[g * p.cols + mine] : 1.0f), s, dw);
     }
-    if (p.dw_post && warp == 0 && on) p.dw_post[c] = dw;
+    if (out && p.dw_post) p.dw_post[mine] = dw;
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// Rows that take a thread's four channels as one load, and whole-row bulk copies.
+bool vector_rows(const void *p, int64_t ld, size_t size)
+{
+    return !p || (aligned(p, 4 * size) && ld % 4 == 0);
+}
+bool bulk_rows(const void *p, int64_t ld, size_t size, int cols)
+{
+    return !p || (aligned(p, 16) && ld * (int64_t)size % 16 == 0 && cols * size % 16 == 0);
+}
 size_t type_size(int t) { return t == AMSIM_BF16 ? 2 : 4; }
 int64_t stride(int64_t ld, int cols) { return ld ? ld : cols; }
 
@@ -77,21 +90,56 @@ int check(const amsim_block_norm_desc *d)
     return AMSIM_OK;
 }
 
-// Steps of 8 channels per thread, threads per row and rows per block: one step
-// while a row fits 512 threads, so that a row's loads are spread over as many
-// threads as possible; narrow rows share blocks of 128 threads.
+// Steps of 4 channels per thread, threads per row and rows per block: two steps
+// up to 256 threads a row, four beyond (one for the narrowest rows, whose
+// second would be empty); narrow rows share blocks of 128 threads.
 struct Shape {
     int nv, tpr, rpb;
 };
-Shape shape(int cols)
+Shape shape(int cols, bool vec)
 {
     Shape s;
-    const int steps = (cols + 7) / 8;
-    s.nv = steps <= 512 ? 1 : 2;
+    const int steps = (cols + amsim::bn::kE - 1) / amsim::bn::kE;
+    s.nv = steps <= 32 && vec ? 1 : steps <= 512 ? 2 : 4;
     s.tpr = ((steps + s.nv - 1) / s.nv + 31) / 32 * 32;
     s.rpb = std::max(1, 128 / s.tpr);
     return s;
 }
+
+// The ring's shape: up to 256 threads per row, and as many rows ahead as the
+// blocks that share an SM have room for.  slots < 2: the row is too wide.
+#ifndef RING_COLS
+#define RING_COLS 512
+#endif
+constexpr int kRingCols = RING_COLS;
+struct RingShape {
+    int nv, tpr, blocks, slots, slot_bytes;   // blocks: resident per SM
+};
+RingShape ring_shape(int cols, int slot_bytes, bool bwd)
+{
+    RingShape s{};
+    const Shape d = shape(cols, true);
+    if (d.nv == 1 || d.tpr > 512) return s;
+    s.nv = d.nv;
+    s.tpr = d.tpr;
+    s.blocks = std::max(1, std::min(16, amsim::bn::ring_blocks(bwd, s.nv) * 256 / s.tpr));
+    s.slot_bytes = slot_bytes;
+    // what is not for rows: barriers, sums, the block's own kilobyte, and backward the weights
+    const int rest = 2048 + amsim::bn::kRingBarBytes + (bwd ? 8 * cols : 0);
+    for (;; --s.blocks) {
+        s.slots = std::min(8, (amsim::kMaxSmemPerCta / s.blocks - rest) / slot_bytes);
+        if (s.slots >= 2 || s.blocks == 1) return s;
+    }
+}
+
+// The ring needs rows to stream: at least two per resident block.
+bool ring_pays(int64_t rows, int cols, const RingShape &r, int sms)
+{
+    return r.slots >= 2 && cols >= kRingCols && rows >= (int64_t)2 * sms * r.blocks;
+}
+
+// Resident blocks per SM of the kernels that load directly: about 1024 threads.
+int direct_blocks(const Shape &s) { return std::max(1, 1024 / (s.tpr * s.rpb)); }
 
 // The backward pass's shares: `splits` per row of the gate, `blocks` thread
 // blocks that take them.  `slots`: how many [cols] sums the scratch holds.
@@ -100,13 +148,13 @@ struct Shares {
     int64_t item_rows, items;
     int blocks;
 };
-Shares shares(const amsim_block_norm_desc *d, const Shape &s, int sms, int64_t slots)
+Shares shares(const amsim_block_norm_desc *d, int per_sm, int rpb, int sms, int64_t slots)
 {
     const int64_t gate_rows = d->gate_rows ? d->gate_rows : d->rows;
     const int64_t groups = d->rows / gate_rows;
-    // about 1024 threads per SM, at least 4 passes of a block over its rows
-    int64_t want = std::max<int64_t>(1, (int64_t)sms * std::max(1, 1024 / (s.tpr * s.rpb)));
-    want = std::min(want, std::max<int64_t>(1, d->rows / (4 * s.rpb)));
+    // every SM full, at least 4 passes of a block over its rows
+    int64_t want = std::max<int64_t>(1, (int64_t)sms * per_sm);
+    want = std::min(want, std::max<int64_t>(1, d->rows / (4 * rpb)));
     Shares r;
     for (;;) {
         int64_t splits = std::max<int64_t>(1, want / groups);
@@ -155,27 +203,50 @@ extern "C" int amsim_block_norm_fwd(const amsim_block_norm_desc *d, const void *
     p.ldn = stride(d->ldn, d->cols);
     p.alpha = d->alpha;
     p.eps = d->eps;
-    bool vec = d->cols % 8 == 0;
-    for (const void *q : {x, y, (const void *)r, (const void *)n, (const void *)gate, (const void *)w_post,
-                          (const void *)w_pre})
-        vec = vec && aligned(q, 16);
-    vec = vec && p.ldx * xs % 16 == 0 && p.ldr * xs % 16 == 0 && p.ldy * ys % 16 == 0 && p.ldn * ns % 16 == 0;
-    const Shape s = shape(d->cols);
-    p.tpr = s.tpr;
-    p.rpb = s.rpb;
-    const int64_t grid = (d->rows + s.rpb - 1) / s.rpb;
+    bool vec = d->cols % amsim::bn::kE == 0;
+    for (const void *q : {(const void *)gate, (const void *)w_post, (const void *)w_pre}) vec = vec && aligned(q, 16);
+    vec = vec && vector_rows(x, p.ldx, xs) && vector_rows(y, p.ldy, ys) && vector_rows(r, p.ldr, xs) &&
+          vector_rows(n, p.ldn, ns);
+    const bool bulk = vec && bulk_rows(x, p.ldx, xs, d->cols) && bulk_rows(y, p.ldy, ys, d->cols);
+    using amsim::bn::kRing;
+    using amsim::bn::kScalar;
+    using amsim::bn::kVector;
+    const int sms = device_sms();
+    if (!sms) return AMSIM_ECUDA;
+    const Shape s = shape(d->cols, vec);
+    const RingShape ring = ring_shape(
+        d->cols, amsim::bn::ring_bytes(d->cols, (int)xs) + (y ? amsim::bn::ring_bytes(d->cols, (int)ys) : 0), false);
+    int nv = s.nv;
+    int64_t grid;
+    amsim::bn::Loads loads = vec ? kVector : kScalar;
+    if (bulk && ring_pays(d->rows, d->cols, ring, sms)) {
+        loads = kRing;
+        nv = ring.nv;
+        p.tpr = ring.tpr;
+        p.rpb = 1;
+        p.slots = ring.slots;
+        p.slot_bytes = ring.slot_bytes;
+        p.block_rows = (d->rows + (int64_t)sms * ring.blocks - 1) / ((int64_t)sms * ring.blocks);
+        grid = (d->rows + p.block_rows - 1) / p.block_rows;
+    } else {
+        p.tpr = s.tpr;
+        p.rpb = s.rpb;
+        grid = (d->rows + s.rpb - 1) / s.rpb;
+    }
     if (grid > 0x7FFFFFFF) return AMSIM_EINVAL;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return d->x_type == AMSIM_F32
-               ? amsim::bn::launch_f32(false, s.nv, vec, d->y_type, d->n_type, p, (unsigned)grid, st)
-               : amsim::bn::launch_bf16(false, s.nv, vec, d->y_type, d->n_type, p, (unsigned)grid, st);
+               ? amsim::bn::launch_f32(false, nv, loads, d->y_type, d->n_type, p, (unsigned)grid, st)
+               : amsim::bn::launch_bf16(false, nv, loads, d->y_type, d->n_type, p, (unsigned)grid, st);
 }
 
 extern "C" size_t amsim_block_norm_workspace_size(const amsim_block_norm_desc *d)
 {
     if (check(d) || d->rows == 0) return 0;
     const int sms = device_sms();
-    const Shares h = shares(d, shape(d->cols), sms ? sms : 1, INT64_MAX);
+    const Shape s = shape(d->cols, true);
+    const Shares h = shares(d, std::max(direct_blocks(s), ring_shape(d->cols, 1, true).blocks), s.rpb, sms ? sms : 1,
+                            INT64_MAX);
     if (h.blocks == 1 && h.splits == 1) return 0;
     const int64_t n = (h.splits > 1 ? h.items : h.blocks) + h.blocks;
     return (size_t)n * (size_t)d->cols * 4;
@@ -234,20 +305,35 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
     p.lddy = stride(d->lddy, d->cols);
     p.alpha = d->alpha;
     p.eps = d->eps;
-    bool vec = d->cols % 8 == 0;
-    for (const void *q : {dr, dn, r, y, (const void *)dx, (const void *)dy, (const void *)gate, (const void *)w_post,
-                          (const void *)w_pre})
-        vec = vec && aligned(q, 16);
-    vec = vec && p.ldr * xs % 16 == 0 && p.lddr * xs % 16 == 0 && p.lddx * xs % 16 == 0 && p.ldy * ys % 16 == 0 &&
-          p.lddy * ys % 16 == 0 && p.lddn * ns % 16 == 0;
-    const Shape s = shape(d->cols);
-    p.tpr = s.tpr;
-    p.rpb = s.rpb;
+    bool vec = d->cols % amsim::bn::kE == 0;
+    for (const void *q : {(const void *)gate, (const void *)w_post, (const void *)w_pre}) vec = vec && aligned(q, 16);
+    vec = vec && vector_rows(r, p.ldr, xs) && vector_rows(dr, p.lddr, xs) && vector_rows(dx, p.lddx, xs) &&
+          vector_rows(y, p.ldy, ys) && vector_rows(dy, p.lddy, ys) && vector_rows(dn, p.lddn, ns);
+    const bool bulk = vec && bulk_rows(r, p.ldr, xs, d->cols) && bulk_rows(dr, p.lddr, xs, d->cols) &&
+                      bulk_rows(y, p.ldy, ys, d->cols) && bulk_rows(dn, p.lddn, ns, d->cols);
     const int sms = device_sms();
     if (!sms) return AMSIM_ECUDA;
+    const Shape s = shape(d->cols, vec);
+    const int rx = amsim::bn::ring_bytes(d->cols, (int)xs);
+    const RingShape ring =
+        ring_shape(d->cols, (dr ? rx : 0) + (dn ? rx + amsim::bn::ring_bytes(d->cols, (int)ns) : 0) +
+                                (y ? amsim::bn::ring_bytes(d->cols, (int)ys) : 0), true);
+    int nv = s.nv, per_sm = direct_blocks(s);
+    amsim::bn::Loads loads = vec ? amsim::bn::kVector : amsim::bn::kScalar;
+    p.tpr = s.tpr;
+    p.rpb = s.rpb;
+    if (bulk && ring_pays(d->rows, d->cols, ring, sms)) {
+        loads = amsim::bn::kRing;
+        nv = ring.nv;
+        p.tpr = ring.tpr;
+        p.rpb = 1;
+        p.slots = ring.slots;
+        p.slot_bytes = ring.slot_bytes;
+        per_sm = ring.blocks;
+    }
     const bool sums = dgate || dw_post || dw_pre;
     const int64_t slots = sums ? (ws ? (int64_t)(ws_bytes / ((size_t)d->cols * 4)) : 0) : INT64_MAX;
-    const Shares h = shares(d, s, sms, slots);
+    const Shares h = shares(d, per_sm, p.rpb, sms, slots);
     p.splits = h.splits;
     p.item_rows = h.item_rows;
     p.items = h.items;
@@ -263,10 +349,10 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
         p.part_pre = dw_pre;
     }
     rc = d->x_type == AMSIM_F32
-             ? amsim::bn::launch_f32(true, s.nv, vec, d->y_type, d->n_type, p, (unsigned)h.blocks, st)
-             : amsim::bn::launch_bf16(true, s.nv, vec, d->y_type, d->n_type, p, (unsigned)h.blocks, st);
+             ? amsim::bn::launch_f32(true, nv, loads, d->y_type, d->n_type, p, (unsigned)h.blocks, st)
+             : amsim::bn::launch_bf16(true, nv, loads, d->y_type, d->n_type, p, (unsigned)h.blocks, st);
     if (rc || !sums || direct) return rc;
-    sums_kernel<<<dim3((unsigned)((d->cols + 31) / 32), 2), 512, 0, st>>>(p, h.blocks);
+    sums_kernel<<<dim3((unsigned)((d->cols + 31) / 32), 2), kSumWarps * 32, 0, st>>>(p, h.blocks);
     rc = amsim::cuda_status(cudaGetLastError());
     if (rc == AMSIM_OK) amsim::count_launch();
     return rc;

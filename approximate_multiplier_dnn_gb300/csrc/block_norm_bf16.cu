@@ -1,8 +1,8 @@
 // Block norm kernels with a bf16 residual stream.
 #include "block_norm.cuh"
 
-int amsim::bn::launch_bf16(bool bwd, int nv, bool vec, int y_type, int n_type, const Params &p, unsigned grid,
+int amsim::bn::launch_bf16(bool bwd, int nv, Loads loads, int y_type, int n_type, const Params &p, unsigned grid,
                            cudaStream_t st)
 {
-    return launch_stream<bf16>(bwd, nv, vec, y_type, n_type, p, grid, st);
+    return launch_stream<bf16>(bwd, nv, loads, y_type, n_type, p, grid, st);
 }

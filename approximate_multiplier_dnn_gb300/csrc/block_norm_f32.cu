@@ -1,8 +1,8 @@
 // Block norm kernels with an fp32 residual stream.
 #include "block_norm.cuh"
 
-int amsim::bn::launch_f32(bool bwd, int nv, bool vec, int y_type, int n_type, const Params &p, unsigned grid,
+int amsim::bn::launch_f32(bool bwd, int nv, Loads loads, int y_type, int n_type, const Params &p, unsigned grid,
                           cudaStream_t st)
 {
-    return launch_stream<float>(bwd, nv, vec, y_type, n_type, p, grid, st);
+    return launch_stream<float>(bwd, nv, loads, y_type, n_type, p, grid, st);
 }

@@ -160,6 +160,46 @@ def test_backward(amd, rows, cols, x, y, n):
     check_bwd(amd, a, r, post, pre, 0.7, got, x, y, rows)
 
 
+# enough rows for the kernels that stream rows through shared memory
+MANY = [(2600, 512), (1300, 1000), (1300, 2048), (700, 2056), (660, 4096), (1301, 1024)]
+
+
+@pytest.mark.parametrize("rows,cols", MANY)
+@pytest.mark.parametrize("x,y,n", [("f32", "f32", "f32"), ("bf16", "bf16", "bf16"), ("f32", "bf16", "bf16"),
+                                   ("bf16", "f32", "f32"), ("bf16", "f32", "bf16")])
+@pytest.mark.parametrize("groups", [1, 20])
+def test_many_rows(amd, rows, cols, x, y, n, groups):
+    rows -= rows % groups
+    a = make(rows, cols, x, y, n, groups, seed=rows + 7 * cols)
+    r, nn, post, pre = amd.block_norm(a["x"], a["y"], a["w_post"], a["w_pre"], gate=a["gate"], alpha=0.5, eps=1e-5,
+                                      n_dtype=a["n_type"])
+    R, N, P, Q, sr, sn = ref_fwd(a, 0.5, 1e-5)
+    check(r, R, K * sr + HALF[x] * (1 + K) * np.abs(R), "r")
+    check(nn, N, 2 * K * sn + K * np.abs(N) + HALF[n] * (1 + K) * np.abs(N) + K * np.abs(N).max(), "n")
+    check(post, P, K * P, "rstd_post")
+    check(pre, Q, 2 * K * Q, "rstd_pre")
+    got = amd.block_norm_backward(a["dr"], a["dn"], r, a["y"], a["w_post"], a["w_pre"], post, pre, gate=a["gate"],
+                                  alpha=0.5)
+    check_bwd(amd, a, r, post, pre, 0.5, got, x, y, rows)
+    assert amd.amsim_device_errors() == (amd.AMSIM_OK, 0)
+
+
+@pytest.mark.parametrize("drop", ["dr", "dn", "y", "w_post", "w_pre", "gate"])
+def test_many_rows_without_parts(amd, drop):
+    a = make(2600, 512, "f32", "bf16", "f32", 4, seed=9)
+    a[drop] = None
+    if drop == "y":
+        a["w_post"] = a["gate"] = None
+    r, n, post, pre = amd.block_norm(a["x"], a["y"], a["w_post"], a["w_pre"], gate=a["gate"], alpha=0.7,
+                                     n_dtype=a["n_type"])
+    R, N, P, Q, sr, sn = ref_fwd(a, 0.7, 1e-6)
+    check(r, R, K * sr, "r")
+    check(n, N, 4 * K * sn + K * np.abs(N).max(), "n")
+    got = amd.block_norm_backward(a["dr"], a["dn"], r, a["y"], a["w_post"], a["w_pre"], post, pre, gate=a["gate"],
+                                  alpha=0.7)
+    check_bwd(amd, a, r, post, pre, 0.7, got, "f32", "bf16", 2600)
+
+
 @pytest.mark.parametrize("groups", [2, 5, 300, 600])
 def test_backward_shared_gates(amd, groups):
     """A gate row's gradient is the sum over the rows that share it, few or one."""
