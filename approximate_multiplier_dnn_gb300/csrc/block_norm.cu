@@ -90,9 +90,9 @@ int check(const amsim_block_norm_desc *d)
     return AMSIM_OK;
 }
 
-// Steps of 4 channels per thread, threads per row and rows per block: two steps
-// up to 256 threads a row, four beyond (one for the narrowest rows, whose
-// second would be empty); narrow rows share blocks of 128 threads.
+// Steps of 4 channels per thread, threads per row and rows per block: four
+// steps, so that what a row costs per thread is spread over 16 channels, fewer
+// where that would not fill a warp; narrow rows share blocks of 128 threads.
 struct Shape {
     int nv, tpr, rpb;
 };
@@ -100,31 +100,26 @@ Shape shape(int cols, bool vec)
 {
     Shape s;
     const int steps = (cols + amsim::bn::kE - 1) / amsim::bn::kE;
-    s.nv = steps <= 32 && vec ? 1 : steps <= 512 ? 2 : 4;
+    s.nv = steps <= 32 && vec ? 1 : steps <= 96 ? 2 : 4;
     s.tpr = ((steps + s.nv - 1) / s.nv + 31) / 32 * 32;
     s.rpb = std::max(1, 128 / s.tpr);
     return s;
 }
 
-// The ring's shape: up to 256 threads per row, and as many rows ahead as the
-// blocks that share an SM have room for.  slots < 2: the row is too wide.
-#ifndef RING_COLS
-#define RING_COLS 512
-#endif
-constexpr int kRingCols = RING_COLS;
+// The ring's shape: as many rows ahead as the blocks that share an SM have
+// room for.  slots < 2: the row is too wide (or too narrow).
 struct RingShape {
-    int nv, tpr, blocks, slots, slot_bytes;   // blocks: resident per SM
+    int tpr, blocks, slots, slot_bytes;   // blocks: resident per SM
 };
 RingShape ring_shape(int cols, int slot_bytes, bool bwd)
 {
     RingShape s{};
     const Shape d = shape(cols, true);
-    if (d.nv == 1 || d.tpr > 512) return s;
-    s.nv = d.nv;
+    if (d.nv != amsim::bn::kRingNV || d.tpr > 512) return s;
     s.tpr = d.tpr;
-    s.blocks = std::max(1, std::min(16, amsim::bn::ring_blocks(bwd, s.nv) * 256 / s.tpr));
+    s.blocks = std::max(1, std::min(16, amsim::bn::ring_threads(bwd) / s.tpr));
     s.slot_bytes = slot_bytes;
-    // what is not for rows: barriers, sums, the block's own kilobyte, and backward the weights
+    // what is not for rows: barriers, sums, the block's own kilobyte, backward the weights
     const int rest = 2048 + amsim::bn::kRingBarBytes + (bwd ? 8 * cols : 0);
     for (;; --s.blocks) {
         s.slots = std::min(8, (amsim::kMaxSmemPerCta / s.blocks - rest) / slot_bytes);
@@ -133,9 +128,9 @@ RingShape ring_shape(int cols, int slot_bytes, bool bwd)
 }
 
 // The ring needs rows to stream: at least two per resident block.
-bool ring_pays(int64_t rows, int cols, const RingShape &r, int sms)
+bool ring_pays(int64_t rows, const RingShape &r, int sms)
 {
-    return r.slots >= 2 && cols >= kRingCols && rows >= (int64_t)2 * sms * r.blocks;
+    return r.slots >= 2 && rows >= (int64_t)2 * sms * r.blocks;
 }
 
 // Resident blocks per SM of the kernels that load directly: about 1024 threads.
@@ -216,12 +211,11 @@ extern "C" int amsim_block_norm_fwd(const amsim_block_norm_desc *d, const void *
     const Shape s = shape(d->cols, vec);
     const RingShape ring = ring_shape(
         d->cols, amsim::bn::ring_bytes(d->cols, (int)xs) + (y ? amsim::bn::ring_bytes(d->cols, (int)ys) : 0), false);
-    int nv = s.nv;
+    const bool full = y && w_post && r && n && rstd_post && rstd_pre;
     int64_t grid;
     amsim::bn::Loads loads = vec ? kVector : kScalar;
-    if (bulk && ring_pays(d->rows, d->cols, ring, sms)) {
+    if (bulk && ring_pays(d->rows, ring, sms) && (full || ring.tpr <= 256)) {
         loads = kRing;
-        nv = ring.nv;
         p.tpr = ring.tpr;
         p.rpb = 1;
         p.slots = ring.slots;
@@ -236,8 +230,8 @@ extern "C" int amsim_block_norm_fwd(const amsim_block_norm_desc *d, const void *
     if (grid > 0x7FFFFFFF) return AMSIM_EINVAL;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return d->x_type == AMSIM_F32
-               ? amsim::bn::launch_f32(false, nv, loads, d->y_type, d->n_type, p, (unsigned)grid, st)
-               : amsim::bn::launch_bf16(false, nv, loads, d->y_type, d->n_type, p, (unsigned)grid, st);
+               ? amsim::bn::launch_fwd_f32(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)grid, st)
+               : amsim::bn::launch_fwd_bf16(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)grid, st);
 }
 
 extern "C" size_t amsim_block_norm_workspace_size(const amsim_block_norm_desc *d)
@@ -318,13 +312,13 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
     const RingShape ring =
         ring_shape(d->cols, (dr ? rx : 0) + (dn ? rx + amsim::bn::ring_bytes(d->cols, (int)ns) : 0) +
                                 (y ? amsim::bn::ring_bytes(d->cols, (int)ys) : 0), true);
-    int nv = s.nv, per_sm = direct_blocks(s);
+    const bool full = dr && dn && y && w_post && dx && dy;
+    int per_sm = direct_blocks(s);
     amsim::bn::Loads loads = vec ? amsim::bn::kVector : amsim::bn::kScalar;
     p.tpr = s.tpr;
     p.rpb = s.rpb;
-    if (bulk && ring_pays(d->rows, d->cols, ring, sms)) {
+    if (bulk && ring_pays(d->rows, ring, sms) && (full || ring.tpr <= 256)) {
         loads = amsim::bn::kRing;
-        nv = ring.nv;
         p.tpr = ring.tpr;
         p.rpb = 1;
         p.slots = ring.slots;
@@ -349,8 +343,8 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
         p.part_pre = dw_pre;
     }
     rc = d->x_type == AMSIM_F32
-             ? amsim::bn::launch_f32(true, nv, loads, d->y_type, d->n_type, p, (unsigned)h.blocks, st)
-             : amsim::bn::launch_bf16(true, nv, loads, d->y_type, d->n_type, p, (unsigned)h.blocks, st);
+             ? amsim::bn::launch_bwd_f32(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)h.blocks, st)
+             : amsim::bn::launch_bwd_bf16(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)h.blocks, st);
     if (rc || !sums || direct) return rc;
     sums_kernel<<<dim3((unsigned)((d->cols + 31) / 32), 2), kSumWarps * 32, 0, st>>>(p, h.blocks);
     rc = amsim::cuda_status(cudaGetLastError());

@@ -2,9 +2,13 @@
 // block's gate and the residual scale.
 //
 // HBM-bound: the forward pass reads x and y and writes r and n, the backward
-// pass reads y, r, dr, dn and writes dx, dy, each once.  A row is held in the
-// registers of the threads that share it (8 channels per thread and step), so
-// both norms of a row and everything between them take one pass over memory.
+// pass reads y, r, dr, dn and writes dx, dy, each once.  The threads of a row
+// hold 16 channels each (fewer for narrow rows), and both norms of a row and
+// everything between them happen in one pass over memory.  With 44 bytes per
+// nanosecond and SM the bound leaves about 20 issue slots per channel, so the
+// arithmetic goes through the packed fp32 instructions, two channels each, and
+// what a row costs besides its channels (sums across warps, addresses, roots)
+// is spread over many channels per thread.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -26,27 +30,40 @@ struct Params {
     long long rows, gate_rows;
     long long ldx, ldy, ldr, ldn, lddr, lddn, lddx, lddy;
     long long item_rows, items;            // backward: rows per share, shares
+    long long block_rows;                  // ring forward: rows of a thread block
     int splits;                            // backward: shares per row of the gate
     int cols;
     int tpr, rpb;                          // threads per row, rows per thread block
     int slots, slot_bytes;                 // ring kernels: rows ahead in shared memory, bytes of one
-    long long block_rows;                  // ring forward: rows of a thread block
     float alpha, eps;
 };
 
+// ------------------------------------------------------------------ pairs
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 // Channels a thread takes at a step: 16 bytes of fp32, 8 of bf16, so that a
 // warp's loads and stores are whole neighbouring sectors whichever the type.
-constexpr int kE = 4;
+constexpr int kE = 4, kP = 2;
 struct Four {
-    float v[kE];
+    float2 p[kP];
 };
 
-template <typename T>
-__device__ __forceinline__ float get(const T *p);
-template <>
-__device__ __forceinline__ float get<float>(const float *p) { return *p; }
-template <>
-__device__ __forceinline__ float get<bf16>(const bf16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(bf16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
@@ -101,14 +118,12 @@ __device__ __forceinline__ Four widen(const Raw<T> &d)
 {
     Four r;
     if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) r.v[e] = __uint_as_float(d.w[e]);
+        r.p[0] = make_float2(__uint_as_float(d.w[0]), __uint_as_float(d.w[1]));
+        r.p[1] = make_float2(__uint_as_float(d.w[2]), __uint_as_float(d.w[3]));
     } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            r.v[2 * e] = __uint_as_float(d.w[e] << 16);
-            r.v[2 * e + 1] = __uint_as_float(d.w[e] & 0xFFFF0000u);
-        }
+        for (int e = 0; e < kP; ++e)
+            r.p[e] = make_float2(__uint_as_float(d.w[e] << 16), __uint_as_float(d.w[e] & 0xFFFF0000u));
     }
     return r;
 }
@@ -120,9 +135,9 @@ __device__ __forceinline__ void store4(T *row, int k, int t, int tpr, int cols, 
         const int c = channel<true>(k, 0, t, tpr);
         if (c >= cols) return;
         if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float4 *>(row + c) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+            *reinterpret_cast<float4 *>(row + c) = make_float4(r.p[0].x, r.p[0].y, r.p[1].x, r.p[1].y);
         } else {
-            const __nv_bfloat162 a = __floats2bfloat162_rn(r.v[0], r.v[1]), b = __floats2bfloat162_rn(r.v[2], r.v[3]);
+            const __nv_bfloat162 a = __float22bfloat162_rn(r.p[0]), b = __float22bfloat162_rn(r.p[1]);
             *reinterpret_cast<uint2 *>(row + c) =
                 make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
         }
@@ -130,7 +145,7 @@ __device__ __forceinline__ void store4(T *row, int k, int t, int tpr, int cols, 
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
             const int c = channel<false>(k, e, t, tpr);
-            if (c < cols) put(row + c, r.v[e]);
+            if (c < cols) put(row + c, e & 1 ? r.p[e >> 1].y : r.p[e >> 1].x);
         }
     }
 }
@@ -139,121 +154,232 @@ __device__ __forceinline__ void store4(T *row, int k, int t, int tpr, int cols, 
 template <bool VEC>
 __device__ __forceinline__ Four weights(const float *w, int k, int t, int tpr, int cols)
 {
-    Four r;
-    if (!w) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) r.v[e] = 1.0f;
-        return r;
-    }
+    if (!w) return Four{{both(1.0f), both(1.0f)}};
     Raw<float> d;
     load_raw<VEC, float>(d, w, k, t, tpr, cols);
     return widen(d);
 }
 
-// Sum of `x` over the threads of a row (its warps are neighbours in the
-// block).  `which` alternates between two buffers, so that one barrier per sum
-// is enough.
-__device__ __forceinline__ float row_sum(float x, int warps, float (*red)[32], int &which)
+// alpha gate w_post
+template <bool VEC>
+__device__ __forceinline__ Four weights_u(const Params &p, const float *gate, int k, int t, int cols)
 {
+    Four w = weights<VEC>(p.w_post, k, t, p.tpr, cols);
+    const Four g = weights<VEC>(gate, k, t, p.tpr, cols);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-    if (warps == 1) return x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *buf = red[which];
-    which ^= 1;
-    if (lane == 0) buf[warp] = x;
-    __syncthreads();
-    const int first = warp / warps * warps;
-    x = lane < warps ? buf[first + lane] : 0.0f;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-    return x;
+    for (int e = 0; e < kP; ++e) w.p[e] = mul2(w.p[e], mul2(both(p.alpha), g.p[e]));
+    return w;
 }
 
-// Three such sums behind one barrier.
-struct Three {
-    float v[3];
+// Sums of S values over the threads of a row (its warps are neighbours in the
+// block), S of them behind one barrier.  `which` alternates between two
+// buffers, so that a barrier per call is enough.
+template <int S>
+struct Sums {
+    float v[S];
 };
-__device__ __forceinline__ Three row_sums(Three x, int warps, float (*red)[3][32], int &which)
+template <int S>
+__device__ __forceinline__ void row_sums(Sums<S> &x, int warps, float (*red)[S][32], int &which)
 {
 #pragma unroll
     for (int d = 16; d; d >>= 1)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) x.v[i] += __shfl_xor_sync(0xFFFFFFFFu, x.v[i], d);
-    if (warps == 1) return x;
+        for (int i = 0; i < S; ++i) x.v[i] += __shfl_xor_sync(0xFFFFFFFFu, x.v[i], d);
+    if (warps == 1) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float (*buf)[32] = red[which];
     which ^= 1;
-    if (lane < 3) buf[lane][warp] = lane == 0 ? x.v[0] : lane == 1 ? x.v[1] : x.v[2];
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < S; ++i) buf[i][warp] = x.v[i];
     __syncthreads();
     const int first = warp / warps * warps;
+    if (warps <= 8) {
+        const int j = lane & 7;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        float v = lane < warps ? buf[i][first + lane] : 0.0f;
+        for (int i = 0; i < S; ++i) x.v[i] = j < warps ? buf[i][first + j] : 0.0f;
+    } else {
 #pragma unroll
-        for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-        x.v[i] = v;
+        for (int i = 0; i < S; ++i) x.v[i] = lane < warps ? buf[i][first + lane] : 0.0f;
+#pragma unroll
+        for (int d = 16; d > 4; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < S; ++i) x.v[i] += __shfl_xor_sync(0xFFFFFFFFu, x.v[i], d);
     }
-    return x;
+#pragma unroll
+    for (int d = 4; d; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < S; ++i) x.v[i] += __shfl_xor_sync(0xFFFFFFFFu, x.v[i], d);
 }
 
-template <int NV, int THREADS, bool VEC, typename X, typename Y, typename N>
-__global__ void __launch_bounds__(THREADS) fwd_kernel(const Params p)
+// The parts of a call.  Kernels built for FULL calls (every part there) test
+// none of them.
+template <bool FULL>
+struct Parts {
+    const Params &p;
+    __device__ __forceinline__ bool y() const { return FULL || p.y; }
+    __device__ __forceinline__ bool post() const { return FULL || p.w_post; }
+    __device__ __forceinline__ bool r() const { return FULL || p.r; }
+    __device__ __forceinline__ bool n() const { return FULL || p.n; }
+    __device__ __forceinline__ bool dr() const { return FULL || p.dr; }
+    __device__ __forceinline__ bool dn() const { return FULL || p.dn; }
+    __device__ __forceinline__ bool dx() const { return FULL || p.dx; }
+    __device__ __forceinline__ bool dy() const { return FULL || p.dy; }
+};
+
+// ------------------------------------------------------------------ one row
+// Forward.  `xr`, `yr`: the thread's words of the row; `wu(k)`: alpha gate
+// w_post, `wq(k)`: w_pre; `met(barrier)` runs after the first sum (or where it
+// would be), `barrier` telling whether every thread was waited for there.
+template <int NV, bool VEC, bool FULL, typename X, typename Y, typename N, typename WU, typename WQ, typename F>
+__device__ __forceinline__ void fwd_row(const Params &p, const Raw<X> (&xr)[NV], const Raw<Y> (&yr)[NV], X *ro, N *no,
+                                        long long row, bool on, int t, int cols, int warps, float (*red)[1][32],
+                                        int &which, WU wu, WQ wq, F met)
 {
-    __shared__ float red[2][32];
-    int which = 0;
-    const int t = threadIdx.x % p.tpr, warps = p.tpr >> 5;
-    const long long row = (long long)blockIdx.x * p.rpb + threadIdx.x / p.tpr;
-    const bool on = row < p.rows;
-    const int cols = on ? p.cols : 0;
-    const X *x = static_cast<const X *>(p.x) + row * p.ldx;
-    const Y *y = static_cast<const Y *>(p.y) + row * p.ldy;
-    Raw<X> xr[NV];
-    Raw<Y> yr[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) load_raw<VEC, X>(xr[k], x, k, t, p.tpr, cols);
-    if (p.y) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) load_raw<VEC, Y>(yr[k], y, k, t, p.tpr, cols);
-    }
+    const Parts<FULL> has{p};
     const float inv = 1.0f / (float)p.cols;
     float post = 1.0f;
-    if (p.y && p.w_post) {
-        float s = 0.0f;
+    if (has.post()) {
+        float2 s2 = both(0.0f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const Four a = widen(yr[k]);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) s = fmaf(a.v[e], a.v[e], s);
+            for (int e = 0; e < kP; ++e) s2 = fma2(a.p[e], a.p[e], s2);
         }
-        post = 1.0f / sqrtf(fmaf(row_sum(s, warps, red, which), inv, p.eps));
-        if (on && t == 0 && p.rstd_post) p.rstd_post[row] = post;
+        Sums<1> s{{s2.x + s2.y}};
+        row_sums(s, warps, red, which);
+        post = rsqrtf(fmaf(s.v[0], inv, p.eps));
+        if (on && t == 0 && (FULL || p.rstd_post)) p.rstd_post[row] = post;
     }
-    const float *gate = p.gate ? p.gate + row / p.gate_rows * p.cols : nullptr;
+    met(has.post() && warps > 1);
     Four r[NV];
-    float s = 0.0f;
+    float2 s2 = both(0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         r[k] = widen(xr[k]);
-        if (p.y) {
-            const Four a = widen(yr[k]);
-            const Four w = weights<VEC>(p.w_post, k, t, p.tpr, cols), g = weights<VEC>(gate, k, t, p.tpr, cols);
+        if (has.y()) {
+            const Four a = widen(yr[k]), w = wu(k);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) r[k].v[e] = fmaf(post * a.v[e], w.v[e] * (p.alpha * g.v[e]), r[k].v[e]);
+            for (int e = 0; e < kP; ++e) r[k].p[e] = fma2(mul2(both(post), a.p[e]), w.p[e], r[k].p[e]);
         }
 #pragma unroll
-        for (int e = 0; e < kE; ++e) s = fmaf(r[k].v[e], r[k].v[e], s);
-        if (p.r) store4<VEC, X>(static_cast<X *>(p.r) + row * p.ldr, k, t, p.tpr, cols, r[k]);
+        for (int e = 0; e < kP; ++e) s2 = fma2(r[k].p[e], r[k].p[e], s2);
+        if (has.r()) store4<VEC, X>(ro, k, t, p.tpr, cols, r[k]);
     }
-    if (!p.n) return;
-    const float pre = 1.0f / sqrtf(fmaf(row_sum(s, warps, red, which), inv, p.eps));
-    if (on && t == 0 && p.rstd_pre) p.rstd_pre[row] = pre;
+    if (!has.n()) return;
+    Sums<1> s{{s2.x + s2.y}};
+    row_sums(s, warps, red, which);
+    const float pre = rsqrtf(fmaf(s.v[0], inv, p.eps));
+    if (on && t == 0 && (FULL || p.rstd_pre)) p.rstd_pre[row] = pre;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const Four w = weights<VEC>(p.w_pre, k, t, p.tpr, cols);
+        const Four w = wq(k);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) r[k].v[e] = r[k].v[e] * pre * w.v[e];
-        store4<VEC, N>(static_cast<N *>(p.n) + row * p.ldn, k, t, p.tpr, cols, r[k]);
+        for (int e = 0; e < kP; ++e) r[k].p[e] = mul2(mul2(r[k].p[e], both(pre)), w.p[e]);
+        store4<VEC, N>(no, k, t, p.tpr, cols, r[k]);
+    }
+}
+
+// A thread's words of one step of a row in the backward pass.
+template <typename X, typename Y, typename N>
+struct Step {
+    Raw<X> dr, r;
+    Raw<Y> y;
+    Raw<N> dn;
+};
+
+// Backward.  The second norm's mean is wanted of s = wu dx, which itself
+// contains the first norm's mean m = mean(t rh); as
+//   dx = q - pre m rh,  q = dr + pre t,
+//   mean(s yh) = mean(wu yh q) - pre m mean(wu yh rh),
+// all three means come from one pass over the row and one barrier.  Between the
+// passes a thread keeps q, and loads r and y again (KEEP false: from shared
+// memory or the L1 cache); the rest of its registers are the column sums', two
+// per channel.
+template <int NV, bool VEC, bool FULL, bool KEEP, typename X, typename Y, typename N, typename LOAD, typename WQ,
+          typename WU, typename F>
+__device__ __forceinline__ void bwd_row(const Params &p, float pre, float post, X *dxo, Y *dyo, int t, int cols,
+                                        int warps, float (*red)[3][32], int &which, float2 (&a)[NV * kP],
+                                        float2 (&b)[NV * kP], LOAD load, WQ wq, WU wu, F met)
+{
+    const Parts<FULL> has{p};
+    const float inv = 1.0f / (float)p.cols;
+    Four q[NV];
+    Step<X, Y, N> in[KEEP ? NV : 1];
+    float2 s2[3] = {both(0.0f), both(0.0f), both(0.0f)};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        Step<X, Y, N> &w = in[KEEP ? k : 0];
+        w = load(k, true);
+        if (has.dr()) q[k] = widen(w.dr);
+        else q[k] = Four{{both(0.0f), both(0.0f)}};
+        Four rh;
+        if (has.dn()) {
+            rh = widen(w.r);
+            const Four n = widen(w.dn), v = wq(k);
+#pragma unroll
+            for (int e = 0; e < kP; ++e) {
+                rh.p[e] = mul2(rh.p[e], both(pre));
+                const float2 t = mul2(n.p[e], v.p[e]);
+                s2[0] = fma2(t, rh.p[e], s2[0]);
+                b[k * kP + e] = fma2(n.p[e], rh.p[e], b[k * kP + e]);
+                q[k].p[e] = fma2(both(pre), t, q[k].p[e]);
+            }
+        }
+        if (has.y()) {
+            const Four y = widen(w.y), v = wu(k);
+#pragma unroll
+            for (int e = 0; e < kP; ++e) {
+                const float2 u = mul2(v.p[e], mul2(y.p[e], both(post)));
+                s2[1] = fma2(u, q[k].p[e], s2[1]);
+                if (has.dn()) s2[2] = fma2(u, rh.p[e], s2[2]);
+            }
+        }
+    }
+    Sums<3> sum{{s2[0].x + s2[0].y, s2[1].x + s2[1].y, s2[2].x + s2[2].y}};
+    const bool means = has.dn() || (has.y() && has.post());
+    if (means) row_sums(sum, warps, red, which);
+    met(means && warps > 1);
+    const float m = pre * (sum.v[0] * inv), mr = -m * pre;
+    const float s = !has.post() ? 0.0f : (has.dn() ? fmaf(-m, sum.v[2], sum.v[1]) : sum.v[1]) * inv;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        Step<X, Y, N> &w = in[KEEP ? k : 0];
+        if (!KEEP) w = load(k, false);
+        if (has.dn()) {
+            const Four r = widen(w.r);
+#pragma unroll
+            for (int e = 0; e < kP; ++e) q[k].p[e] = fma2(both(mr), r.p[e], q[k].p[e]);
+        }
+        if (has.dx()) store4<VEC, X>(dxo, k, t, p.tpr, cols, q[k]);
+        if (!has.y()) continue;
+        const Four y = widen(w.y), v = wu(k);
+        Four o;
+#pragma unroll
+        for (int e = 0; e < kP; ++e) {
+            const float2 yh = mul2(y.p[e], both(post));
+            a[k * kP + e] = fma2(q[k].p[e], yh, a[k * kP + e]);
+            o.p[e] = mul2(both(post), fma2(yh, both(-s), mul2(q[k].p[e], v.p[e])));
+        }
+        if (has.dy()) store4<VEC, Y>(dyo, k, t, p.tpr, cols, o);
+    }
+}
+
+// A channel's sum over a share's rows leaves: to the share's slot when several
+// make up a row of the gate, else to dgate and the block's slot of dw_post.
+__device__ __forceinline__ void leave_a(const Params &p, float v, int c, long long item, long long gi,
+                                        const float *gate, bool fresh)
+{
+    if (c >= p.cols) return;
+    if (p.splits > 1) {
+        p.part_gate[item * p.cols + c] = v;
+        return;
+    }
+    if (p.dgate) p.dgate[gi * p.cols + c] = p.alpha * (p.w_post ? p.w_post[c] : 1.0f) * v;
+    if (p.dw_post) {
+        float *slot = p.part_post + (long long)blockIdx.x * p.cols + c;
+        *slot = fmaf(p.alpha * (gate ? gate[c] : 1.0f), v, fresh ? 0.0f : *slot);
     }
 }
 
@@ -272,124 +398,31 @@ __device__ __forceinline__ float group_sum(float x, int tpr, int rpb, float *buf
     return x;
 }
 
-// A channel's sum over a share's rows leaves: to the share's slot when several
-// make up a row of the gate, else to dgate and the block's slot of dw_post.
-template <bool VEC>
-__device__ __forceinline__ void leave_a(const Params &p, float v, int c, long long item, long long gi,
-                                        const float *gate, bool fresh)
-{
-    if (c >= p.cols) return;
-    if (p.splits > 1) {
-        p.part_gate[item * p.cols + c] = v;
-        return;
-    }
-    if (p.dgate) p.dgate[gi * p.cols + c] = p.alpha * (p.w_post ? p.w_post[c] : 1.0f) * v;
-    if (p.dw_post) {
-        float *slot = p.part_post + (long long)blockIdx.x * p.cols + c;
-        *slot = fmaf(p.alpha * (gate ? gate[c] : 1.0f), v, fresh ? 0.0f : *slot);
-    }
-}
+__device__ __forceinline__ float element(const float2 &v, int e) { return e & 1 ? v.y : v.x; }
 
-// A thread's words of one step of a row in the backward pass.
-template <typename X, typename Y, typename N>
-struct Step {
-    Raw<X> dr, r;
-    Raw<Y> y;
-    Raw<N> dn;
-};
-
-// The gradients of one row.  The second norm's mean is wanted of s = wu dx,
-// which itself contains the first norm's mean m = mean(t rh); as
-//   dx = q - pre m rh,  q = dr + pre t,
-//   mean(s yh) = mean(wu yh q) - pre m mean(wu yh rh),
-// all three means come from one pass over the row and one barrier.
-// `load(k)`: the thread's words of step k; `wq(k)`: w_pre; `wu(k)`: alpha gate
-// w_post.  Rows of up to two steps per thread stay in registers between the
-// two passes; wider ones are loaded again (from shared memory or the L1 cache),
-// which leaves the registers to the column sums.  `met(barrier)` runs between
-// the passes, `barrier` telling whether every thread was waited for there.
-template <int NV, bool VEC, typename X, typename Y, typename N, typename LOAD, typename WQ, typename WU, typename F>
-__device__ __forceinline__ void bwd_row(const Params &p, float pre, float post, long long row, int t, int cols,
-                                        int warps, float (*red)[3][32], int &which, float (&a)[NV * kE],
-                                        float (&b)[NV * kE], LOAD load, WQ wq, WU wu, F met)
+// ------------------------------------------------------------------ direct loads
+template <int NV, int THREADS, bool VEC, typename X, typename Y, typename N>
+__global__ void __launch_bounds__(THREADS) fwd_kernel(const Params p)
 {
-    const bool want_y = p.y != nullptr, want_n = p.dn != nullptr;
-    const float inv = 1.0f / (float)p.cols;
-    constexpr bool keep = NV <= 2;
-    Four qs[keep ? NV : 1], rhs[keep ? NV : 1], yhs[keep ? NV : 1];
-    auto widened = [&](const Step<X, Y, N> &in, int k, Four &q, Four &rh, Four &yh, Four &t) {
-        if (p.dr) {
-            q = widen(in.dr);
-        } else {
+    __shared__ float red[2][1][32];
+    int which = 0;
+    const int t = threadIdx.x % p.tpr, warps = p.tpr >> 5;
+    const long long row = (long long)blockIdx.x * p.rpb + threadIdx.x / p.tpr;
+    const bool on = row < p.rows;
+    const int cols = on ? p.cols : 0;
+    Raw<X> xr[NV];
+    Raw<Y> yr[NV];
 #pragma unroll
-            for (int e = 0; e < kE; ++e) q.v[e] = 0.0f;
-        }
-        if (want_n) {
-            rh = widen(in.r);
-            const Four n = widen(in.dn), w = wq(k);
+    for (int k = 0; k < NV; ++k) load_raw<VEC, X>(xr[k], static_cast<const X *>(p.x) + row * p.ldx, k, t, p.tpr, cols);
+    if (p.y)
 #pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                rh.v[e] *= pre;
-                t.v[e] = n.v[e] * w.v[e];
-                q.v[e] = fmaf(pre, t.v[e], q.v[e]);
-            }
-        }
-        if (want_y) {
-            yh = widen(in.y);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) yh.v[e] *= post;
-        }
-    };
-    Three sum = {{0.0f, 0.0f, 0.0f}};
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const Step<X, Y, N> in = load(k);
-        Four t, &q = qs[keep ? k : 0], &rh = rhs[keep ? k : 0], &yh = yhs[keep ? k : 0];
-        widened(in, k, q, rh, yh, t);
-        if (want_n) {
-            const Four n = widen(in.dn);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                sum.v[0] = fmaf(t.v[e], rh.v[e], sum.v[0]);
-                b[k * kE + e] = fmaf(n.v[e], rh.v[e], b[k * kE + e]);
-            }
-        }
-        if (want_y) {
-            const Four w = wu(k);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                const float u = w.v[e] * yh.v[e];
-                sum.v[1] = fmaf(u, q.v[e], sum.v[1]);
-                if (want_n) sum.v[2] = fmaf(u, rh.v[e], sum.v[2]);
-            }
-        }
-    }
-    const bool means = want_n || (want_y && p.w_post);
-    if (means) sum = row_sums(sum, warps, red, which);
-    met(means && warps > 1);
-    const float m = pre * (sum.v[0] * inv);
-    const float s = !p.w_post ? 0.0f : (want_n ? fmaf(-m, sum.v[2], sum.v[1]) : sum.v[1]) * inv;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        Four &q = qs[keep ? k : 0], &rh = rhs[keep ? k : 0], &yh = yhs[keep ? k : 0];
-        if (!keep) {
-            Four none;
-            widened(load(k), k, q, rh, yh, none);
-        }
-        if (want_n)
-#pragma unroll
-            for (int e = 0; e < kE; ++e) q.v[e] = fmaf(-m, rh.v[e], q.v[e]);
-        if (p.dx) store4<VEC, X>(static_cast<X *>(p.dx) + row * p.lddx, k, t, p.tpr, cols, q);
-        if (!want_y) continue;
-        const Four w = wu(k);
-        Four o;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            a[k * kE + e] = fmaf(q.v[e], yh.v[e], a[k * kE + e]);
-            o.v[e] = post * fmaf(-yh.v[e], s, q.v[e] * w.v[e]);
-        }
-        if (p.dy) store4<VEC, Y>(static_cast<Y *>(p.dy) + row * p.lddy, k, t, p.tpr, cols, o);
-    }
+        for (int k = 0; k < NV; ++k)
+            load_raw<VEC, Y>(yr[k], static_cast<const Y *>(p.y) + row * p.ldy, k, t, p.tpr, cols);
+    const float *gate = p.gate && on ? p.gate + row / p.gate_rows * p.cols : nullptr;
+    fwd_row<NV, VEC, false, X, Y, N>(
+        p, xr, yr, static_cast<X *>(p.r) + row * p.ldr, static_cast<N *>(p.n) + row * p.ldn, row, on, t, cols, warps,
+        red, which, [&](int k) { return weights_u<VEC>(p, gate, k, t, cols); },
+        [&](int k) { return weights<VEC>(p.w_pre, k, t, p.tpr, cols); }, [](bool) {});
 }
 
 // A block takes shares (items) of item_rows rows; the rows of a share have the
@@ -406,53 +439,48 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
     const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, warps = p.tpr >> 5;
     const bool want_y = p.y != nullptr, want_n = p.dn != nullptr;
     const bool sums_a = want_y && (p.dgate || p.dw_post), sums_b = want_n && p.dw_pre;
-    float b[NV * kE];
+    float2 b[NV * kP];
 #pragma unroll
-    for (int i = 0; i < NV * kE; ++i) b[i] = 0.0f;
+    for (int i = 0; i < NV * kP; ++i) b[i] = both(0.0f);
     bool fresh = true;                       // no share has left its sums in part_post yet
     for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
         const long long gi = item / p.splits;
         const long long g0 = gi * p.gate_rows, g1 = min(g0 + p.gate_rows, p.rows);
         const long long r0 = g0 + (item - gi * p.splits) * p.item_rows, r1 = min(r0 + p.item_rows, g1);
         const float *gate = p.gate ? p.gate + gi * p.cols : nullptr;
-        float a[NV * kE];
+        float2 a[NV * kP];
 #pragma unroll
-        for (int i = 0; i < NV * kE; ++i) a[i] = 0.0f;
+        for (int i = 0; i < NV * kP; ++i) a[i] = both(0.0f);
         for (long long rb = r0; rb < r1; rb += p.rpb) {
             const long long row = rb + group;
             const bool on = row < r1;
             const int cols = on ? p.cols : 0;
             const float pre = want_n && on ? p.rstd_pre[row] : 0.0f;
             const float post = !want_y || !p.w_post ? 1.0f : on ? p.rstd_post[row] : 0.0f;
-            bwd_row<NV, VEC, X, Y, N>(
-                p, pre, post, row, t, cols, warps, red, which, a, b,
-                [&](int k) {
+            bwd_row<NV, VEC, false, NV <= 2 || !VEC, X, Y, N>(
+                p, pre, post, static_cast<X *>(p.dx) + row * p.lddx, static_cast<Y *>(p.dy) + row * p.lddy, t, cols,
+                warps, red, which, a, b,
+                [&](int k, bool first) {
                     Step<X, Y, N> in;
-                    if (p.dr) load_raw<VEC, X>(in.dr, static_cast<const X *>(p.dr) + row * p.lddr, k, t, p.tpr, cols);
+                    if (p.dr && first) load_raw<VEC, X>(in.dr, static_cast<const X *>(p.dr) + row * p.lddr, k, t, p.tpr, cols);
                     if (want_n) {
                         load_raw<VEC, X>(in.r, static_cast<const X *>(p.rin) + row * p.ldr, k, t, p.tpr, cols);
-                        load_raw<VEC, N>(in.dn, static_cast<const N *>(p.dn) + row * p.lddn, k, t, p.tpr, cols);
+                        if (first)
+                            load_raw<VEC, N>(in.dn, static_cast<const N *>(p.dn) + row * p.lddn, k, t, p.tpr, cols);
                     }
                     if (want_y) load_raw<VEC, Y>(in.y, static_cast<const Y *>(p.y) + row * p.ldy, k, t, p.tpr, cols);
                     return in;
                 },
                 [&](int k) { return weights<VEC>(p.w_pre, k, t, p.tpr, cols); },
-                [&](int k) {
-                    Four w = weights<VEC>(p.w_post, k, t, p.tpr, cols);
-                    const Four g = weights<VEC>(gate, k, t, p.tpr, cols);
-#pragma unroll
-                    for (int e = 0; e < kE; ++e) w.v[e] *= p.alpha * g.v[e];
-                    return w;
-                },
-                [](bool) {});
+                [&](int k) { return weights_u<VEC>(p, gate, k, t, cols); }, [](bool) {});
         }
         if (!sums_a) continue;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
-                const float v = group_sum(a[k * kE + e], p.tpr, p.rpb, buf);
-                if (group == 0) leave_a<VEC>(p, v, channel<VEC>(k, e, t, p.tpr), item, gi, gate, fresh);
+                const float v = group_sum(element(a[k * kP + (e >> 1)], e), p.tpr, p.rpb, buf);
+                if (group == 0) leave_a(p, v, channel<VEC>(k, e, t, p.tpr), item, gi, gate, fresh);
             }
         fresh = false;
     }
@@ -461,7 +489,7 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
-            const float v = group_sum(b[k * kE + e], p.tpr, p.rpb, buf);
+            const float v = group_sum(element(b[k * kP + (e >> 1)], e), p.tpr, p.rpb, buf);
             const int c = channel<VEC>(k, e, t, p.tpr);
             if (group == 0 && c < p.cols) p.part_pre[(long long)blockIdx.x * p.cols + c] = v;
         }
@@ -472,9 +500,9 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
 // they reduce it: 40 % of the copy bandwidth at 16384 x 4096.  Where rows are
 // vectors of 16 bytes and there are many, a block streams its rows through a
 // ring in shared memory instead: one thread issues whole-row bulk copies, and
-// refills a slot as soon as every thread has its words of it in registers.
-// Channels are dealt to threads, and sums taken, as above, so a row's results
-// do not depend on how many rows come with it.
+// refills a slot once every thread is past it.  Channels are dealt to threads,
+// and sums taken, as above, so a row's results do not depend on how many rows
+// come with it.
 struct Ring {
     uint8_t *slot0;
     uint64_t *full;
@@ -486,9 +514,9 @@ struct Ring {
     __device__ __forceinline__ uint8_t *wait()
     {
         tc::bar_wait(full + at, phase, aborted);
-        return slot0 + (size_t)at * bytes;
+        return slot0 + at * bytes;
     }
-    // The slot just read is free: `at` moves on.
+    // On to the next slot; the number of the one left.
     __device__ __forceinline__ int next()
     {
         const int s = at;
@@ -497,22 +525,17 @@ struct Ring {
     }
 };
 
+constexpr int kRingNV = 4;                 // steps per thread of the ring kernels
 constexpr int kRingBarBytes = 128;         // up to 16 slots
-// Resident blocks of 256 threads per SM, by direction and steps per thread.
-#ifndef RBF2
-#define RBF2 3
-#endif
-#ifndef RBF4
-#define RBF4 2
-#endif
-#ifndef RBB2
-#define RBB2 2
-#endif
-#ifndef RBB4
-#define RBB4 2
-#endif
-__host__ __device__ constexpr int ring_blocks(bool bwd, int nv) { return bwd ? (nv == 2 ? RBB2 : RBB4) : (nv == 2 ? RBF2 : RBF4); }
 constexpr int kRingAlign = 128;
+// Threads per SM that the kernels' registers allow.
+#ifndef RTF
+#define RTF 512
+#endif
+#ifndef RTB
+#define RTB 512
+#endif
+__host__ __device__ constexpr int ring_threads(bool bwd) { return bwd ? RTB : RTF; }
 __host__ __device__ inline int ring_bytes(int cols, int size) { return (cols * size + kRingAlign - 1) / kRingAlign * kRingAlign; }
 
 __device__ __forceinline__ Ring make_ring(const Params &p, uint8_t *smem)
@@ -537,106 +560,84 @@ __device__ __forceinline__ void take(Raw<T> &d, const uint8_t *row, int k, int t
     load_raw<true, T>(d, reinterpret_cast<const T *>(row), k, t, tpr, cols);
 }
 
-template <int NV, int THREADS, typename X, typename Y, typename N>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? ring_blocks(false, NV) : 1) fwd_ring_kernel(const Params p)
+// Four weights that wait in shared memory.
+__device__ __forceinline__ Four kept(const float *w, int k, int t, int tpr, int cols)
+{
+    Raw<float> d;
+    load_raw<true, float>(d, w, k, t, tpr, cols);
+    return widen(d);
+}
+
+template <int THREADS, bool FULL, typename X, typename Y, typename N>
+__global__ void __launch_bounds__(THREADS, ring_threads(false) / THREADS) fwd_ring_kernel(const Params p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[2][32];
+    __shared__ float red[2][1][32];
+    constexpr int NV = kRingNV;
+    const Parts<FULL> has{p};
     int which = 0;
     const int t = threadIdx.x, warps = p.tpr >> 5, cols = p.cols;
     const int xb = cols * (int)sizeof(X), yb = cols * (int)sizeof(Y), yoff = ring_bytes(cols, sizeof(X));
     const long long r0 = blockIdx.x * p.block_rows, r1 = min(r0 + p.block_rows, p.rows);
     Ring ring = make_ring(p, smem);
     auto issue = [&](long long row, int slot) {
-        uint8_t *s = ring.slot0 + (size_t)slot * ring.bytes;
-        tc::bar_expect(ring.full + slot, xb + (p.y ? yb : 0));
+        uint8_t *s = ring.slot0 + slot * ring.bytes;
+        tc::bar_expect(ring.full + slot, xb + (has.y() ? yb : 0));
         tc::copy_bytes(s, static_cast<const X *>(p.x) + row * p.ldx, xb, ring.full + slot);
-        if (p.y) tc::copy_bytes(s + yoff, static_cast<const Y *>(p.y) + row * p.ldy, yb, ring.full + slot);
+        if (has.y()) tc::copy_bytes(s + yoff, static_cast<const Y *>(p.y) + row * p.ldy, yb, ring.full + slot);
     };
     if (t == 0)
         for (int i = 0; i < p.slots && r0 + i < r1; ++i) issue(r0 + i, i);
-    const float inv = 1.0f / (float)cols;
-    Four wq[NV], wu[NV];                  // w_pre, and alpha gate w_post of the rows' gate
-    if (p.n)
+    Four wq[NV], wu[NV];                   // w_pre, and alpha gate w_post of the rows' gate
+    if (has.n())
 #pragma unroll
         for (int k = 0; k < NV; ++k) wq[k] = weights<true>(p.w_pre, k, t, p.tpr, cols);
+    X *ro = static_cast<X *>(p.r) + r0 * p.ldr;
+    N *no = static_cast<N *>(p.n) + r0 * p.ldn;
     long long gate_end = r0;               // first row with another gate
-    for (long long row = r0; row < r1; ++row) {
-        if (p.y && row == gate_end) {
+    for (long long row = r0; row < r1; ++row, ro += p.ldr, no += p.ldn) {
+        if (has.y() && row == gate_end) {
             const long long g = row / p.gate_rows;
+            const float *gate = p.gate ? p.gate + g * cols : nullptr;
             gate_end = (g + 1) * p.gate_rows;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                wu[k] = weights<true>(p.w_post, k, t, p.tpr, cols);
-                const Four a = weights<true>(p.gate ? p.gate + g * cols : nullptr, k, t, p.tpr, cols);
-#pragma unroll
-                for (int e = 0; e < kE; ++e) wu[k].v[e] *= p.alpha * a.v[e];
-            }
+            for (int k = 0; k < NV; ++k) wu[k] = weights_u<true>(p, gate, k, t, cols);
         }
         const uint8_t *slot = ring.wait();
         Raw<X> xr[NV];
         Raw<Y> yr[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) take<X>(xr[k], slot, k, t, p.tpr, cols);
-        if (p.y)
+        if (has.y())
 #pragma unroll
             for (int k = 0; k < NV; ++k) take<Y>(yr[k], slot + yoff, k, t, p.tpr, cols);
-        float post = 1.0f;
-        if (p.w_post) {
-            float s = 0.0f;
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const Four a = widen(yr[k]);
-#pragma unroll
-                for (int e = 0; e < kE; ++e) s = fmaf(a.v[e], a.v[e], s);
-            }
-            post = 1.0f / sqrtf(fmaf(row_sum(s, warps, red, which), inv, p.eps));
-            if (t == 0 && p.rstd_post) p.rstd_post[row] = post;
-        }
-        if (!p.w_post || warps == 1) __syncthreads();      // else row_sum's barrier: the slot has been read
-        const int freed = ring.next();
-        if (t == 0 && row + p.slots < r1) issue(row + p.slots, freed);
-        Four r[NV];
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            r[k] = widen(xr[k]);
-            if (p.y) {
-                const Four a = widen(yr[k]);
-#pragma unroll
-                for (int e = 0; e < kE; ++e) r[k].v[e] = fmaf(post * a.v[e], wu[k].v[e], r[k].v[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < kE; ++e) s = fmaf(r[k].v[e], r[k].v[e], s);
-            if (p.r) store4<true, X>(static_cast<X *>(p.r) + row * p.ldr, k, t, p.tpr, cols, r[k]);
-        }
-        if (!p.n) continue;
-        const float pre = 1.0f / sqrtf(fmaf(row_sum(s, warps, red, which), inv, p.eps));
-        if (t == 0 && p.rstd_pre) p.rstd_pre[row] = pre;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-#pragma unroll
-            for (int e = 0; e < kE; ++e) r[k].v[e] = r[k].v[e] * pre * wq[k].v[e];
-            store4<true, N>(static_cast<N *>(p.n) + row * p.ldn, k, t, p.tpr, cols, r[k]);
-        }
+        fwd_row<NV, true, FULL, X, Y, N>(
+            p, xr, yr, ro, no, row, true, t, cols, warps, red, which,
+            [&](int k) { return wu[k]; }, [&](int k) { return wq[k]; },
+            [&](bool barrier) {
+                if (!barrier) __syncthreads();             // the row is in registers
+                const int freed = ring.next();
+                if (t == 0 && row + p.slots < r1) issue(row + p.slots, freed);
+            });
     }
 }
 
 // As bwd_kernel, one row at a time per block.  The weights wait in shared
 // memory after the ring (w_pre, then alpha gate w_post of the share's gate).
-template <int NV, int THREADS, typename X, typename Y, typename N>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? ring_blocks(true, NV) : 1) bwd_ring_kernel(const Params p)
+template <int THREADS, bool FULL, typename X, typename Y, typename N>
+__global__ void __launch_bounds__(THREADS, ring_threads(true) / THREADS) bwd_ring_kernel(const Params p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][3][32];
+    constexpr int NV = kRingNV;
+    const Parts<FULL> has{p};
     int which = 0;
     const int t = threadIdx.x, warps = p.tpr >> 5, cols = p.cols;
-    const bool want_y = p.y != nullptr, want_n = p.dn != nullptr;
-    const bool sums_a = want_y && (p.dgate || p.dw_post), sums_b = want_n && p.dw_pre;
+    const bool sums_a = has.y() && (p.dgate || p.dw_post), sums_b = has.dn() && p.dw_pre;
     const int xb = cols * (int)sizeof(X), yb = cols * (int)sizeof(Y), nb = cols * (int)sizeof(N);
     const int rxb = ring_bytes(cols, sizeof(X)), rnb = ring_bytes(cols, sizeof(N));
-    const int off_r = p.dr ? rxb : 0, off_n = off_r + (want_n ? rxb : 0), off_y = off_n + (want_n ? rnb : 0);
-    float *wq = reinterpret_cast<float *>(smem + kRingBarBytes + (size_t)p.slots * p.slot_bytes);
+    const int off_r = has.dr() ? rxb : 0, off_n = off_r + (has.dn() ? rxb : 0), off_y = off_n + (has.dn() ? rnb : 0);
+    float *wq = reinterpret_cast<float *>(smem + kRingBarBytes + p.slots * p.slot_bytes);
     float *wu = wq + cols;
     Ring ring = make_ring(p, smem);
     // the rows of this block in order: shares blockIdx.x, + gridDim.x, ...
@@ -650,14 +651,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? ring_blocks(true, NV
         q.end = min(min(q.row + p.item_rows, g0 + p.gate_rows), p.rows);
     };
     auto issue = [&](const Place &q, int slot) {
-        uint8_t *s = ring.slot0 + (size_t)slot * ring.bytes;
-        tc::bar_expect(ring.full + slot, (p.dr ? xb : 0) + (want_n ? xb + nb : 0) + (want_y ? yb : 0));
-        if (p.dr) tc::copy_bytes(s, static_cast<const X *>(p.dr) + q.row * p.lddr, xb, ring.full + slot);
-        if (want_n) {
+        uint8_t *s = ring.slot0 + slot * ring.bytes;
+        tc::bar_expect(ring.full + slot, (has.dr() ? xb : 0) + (has.dn() ? xb + nb : 0) + (has.y() ? yb : 0));
+        if (has.dr()) tc::copy_bytes(s, static_cast<const X *>(p.dr) + q.row * p.lddr, xb, ring.full + slot);
+        if (has.dn()) {
             tc::copy_bytes(s + off_r, static_cast<const X *>(p.rin) + q.row * p.ldr, xb, ring.full + slot);
             tc::copy_bytes(s + off_n, static_cast<const N *>(p.dn) + q.row * p.lddn, nb, ring.full + slot);
         }
-        if (want_y) tc::copy_bytes(s + off_y, static_cast<const Y *>(p.y) + q.row * p.ldy, yb, ring.full + slot);
+        if (has.y()) tc::copy_bytes(s + off_y, static_cast<const Y *>(p.y) + q.row * p.ldy, yb, ring.full + slot);
     };
     auto advance = [&](Place &q) {
         if (++q.row < q.end) return;
@@ -671,16 +672,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? ring_blocks(true, NV
             issue(ahead, i);
             advance(ahead);
         }
-    auto kept = [&](const float *w, int k) {
-        Raw<float> d;
-        load_raw<true, float>(d, w, k, t, p.tpr, cols);
-        return widen(d);
-    };
-    if (want_n)
+    if (has.dn())
         for (int c = t; c < cols; c += p.tpr) wq[c] = p.w_pre ? p.w_pre[c] : 1.0f;
-    float b[NV * kE];
+    float2 b[NV * kP];
 #pragma unroll
-    for (int i = 0; i < NV * kE; ++i) b[i] = 0.0f;
+    for (int i = 0; i < NV * kP; ++i) b[i] = both(0.0f);
     bool fresh = true;                       // no share has left its sums in part_post yet
     int last = -1;                           // the slot of the row before, not yet refilled
     for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
@@ -688,46 +684,47 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? ring_blocks(true, NV
         bounds(q);
         const long long gi = item / p.splits;
         const float *gate = p.gate ? p.gate + gi * cols : nullptr;
-        if (want_y && (fresh || gate)) {
+        if (has.y() && (fresh || gate)) {
             __syncthreads();                 // the last share's weights are no longer read
             for (int c = t; c < cols; c += p.tpr)
                 wu[c] = (p.w_post ? p.w_post[c] : 1.0f) * (p.alpha * (gate ? gate[c] : 1.0f));
         }
         if (fresh || gate) __syncthreads();
-        float a[NV * kE];
+        float2 a[NV * kP];
 #pragma unroll
-        for (int i = 0; i < NV * kE; ++i) a[i] = 0.0f;
-        // a row's own numbers are fetched a row ahead: their latency is longer than the row's work
-        auto pre_of = [&](long long row) { return want_n && row < q.end ? p.rstd_pre[row] : 0.0f; };
-        auto post_of = [&](long long row) { return want_y && p.w_post && row < q.end ? p.rstd_post[row] : 1.0f; };
+        for (int i = 0; i < NV * kP; ++i) a[i] = both(0.0f);
+        // a row's own numbers are fetched a row ahead of its work
+        auto pre_of = [&](long long row) { return has.dn() && row < q.end ? p.rstd_pre[row] : 0.0f; };
+        auto post_of = [&](long long row) { return has.y() && has.post() && row < q.end ? p.rstd_post[row] : 1.0f; };
         float next_pre = pre_of(q.row), next_post = post_of(q.row);
-        for (long long row = q.row; row < q.end; ++row) {
+        X *dxo = static_cast<X *>(p.dx) + q.row * p.lddx;
+        Y *dyo = static_cast<Y *>(p.dy) + q.row * p.lddy;
+        for (long long row = q.row; row < q.end; ++row, dxo += p.lddx, dyo += p.lddy) {
             const float pre = next_pre, post = next_post;
             next_pre = pre_of(row + 1);
             next_post = post_of(row + 1);
             const uint8_t *slot = ring.wait();
-            bwd_row<NV, true, X, Y, N>(
-                p, pre, post, row, t, cols, warps, red, which, a, b,
-                [&](int k) {
+            bwd_row<NV, true, FULL, false, X, Y, N>(
+                p, pre, post, dxo, dyo, t, cols, warps, red, which, a, b,
+                [&](int k, bool first) {
                     Step<X, Y, N> in;
-                    if (p.dr) take<X>(in.dr, slot, k, t, p.tpr, cols);
-                    if (want_n) {
+                    if (has.dr() && first) take<X>(in.dr, slot, k, t, p.tpr, cols);
+                    if (has.dn()) {
                         take<X>(in.r, slot + off_r, k, t, p.tpr, cols);
-                        take<N>(in.dn, slot + off_n, k, t, p.tpr, cols);
+                        if (first) take<N>(in.dn, slot + off_n, k, t, p.tpr, cols);
                     }
-                    if (want_y) take<Y>(in.y, slot + off_y, k, t, p.tpr, cols);
+                    if (has.y()) take<Y>(in.y, slot + off_y, k, t, p.tpr, cols);
                     return in;
                 },
-                [&](int k) { return kept(wq, k); }, [&](int k) { return kept(wu, k); },
+                [&](int k) { return kept(wq, k, t, p.tpr, cols); }, [&](int k) { return kept(wu, k, t, p.tpr, cols); },
                 [&](bool barrier) {
-                    // free now: this row's slot if it stays in registers, else the last row's
+                    // every thread is past the last row: its slot is free
                     if (!barrier) __syncthreads();
-                    const int freed = NV <= 2 ? ring.next() : last;
-                    if (NV > 2) last = ring.next();
-                    if (t == 0 && freed >= 0 && ahead.item < p.items) {
-                        issue(ahead, freed);
+                    if (t == 0 && last >= 0 && ahead.item < p.items) {
+                        issue(ahead, last);
                         advance(ahead);
                     }
+                    last = ring.next();
                 });
         }
         if (sums_a) {
@@ -735,7 +732,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? ring_blocks(true, NV
             for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int e = 0; e < kE; ++e)
-                    leave_a<true>(p, a[k * kE + e], channel<true>(k, e, t, p.tpr), item, gi, gate, fresh);
+                    leave_a(p, element(a[k * kP + (e >> 1)], e), channel<true>(k, e, t, p.tpr), item, gi, gate, fresh);
         }
         fresh = false;
     }
@@ -745,16 +742,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? ring_blocks(true, NV
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
             const int c = channel<true>(k, e, t, p.tpr);
-            if (c < cols) p.part_pre[(long long)blockIdx.x * cols + c] = b[k * kE + e];
+            if (c < cols) p.part_pre[(long long)blockIdx.x * cols + c] = element(b[k * kP + (e >> 1)], e);
         }
 }
 
+// ------------------------------------------------------------------ launches
 // How a call runs: single loads for unaligned rows, vector loads, or the ring.
 enum Loads { kScalar = 0, kVector = 1, kRing = 2 };
 
-// One translation unit per type of the residual stream builds its instances.
-int launch_f32(bool bwd, int nv, Loads loads, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
-int launch_bf16(bool bwd, int nv, Loads loads, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
+// One translation unit per direction and type of the residual stream builds
+// its instances.
+int launch_fwd_f32(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
+int launch_fwd_bf16(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
+int launch_bwd_f32(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
+int launch_bwd_bf16(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
 
 template <typename K>
 int launch_kernel(K kernel, const Params &p, unsigned grid, size_t smem, cudaStream_t st)
@@ -769,38 +770,42 @@ int launch_kernel(K kernel, const Params &p, unsigned grid, size_t smem, cudaStr
     return rc;
 }
 
-template <typename X, typename Y, typename N>
-int launch_types(bool bwd, int nv, Loads loads, const Params &p, unsigned grid, cudaStream_t st)
+template <bool BWD, typename X, typename Y, typename N>
+int launch_types(int nv, Loads loads, bool full, const Params &p, unsigned grid, cudaStream_t st)
 {
     const int threads = p.tpr * p.rpb;
-#define AMSIM_BN(KERNEL, ...) \
-    launch_kernel(bwd ? bwd_##KERNEL<__VA_ARGS__, X, Y, N> : fwd_##KERNEL<__VA_ARGS__, X, Y, N>, p, grid, smem, st)
-    size_t smem = 0;
+#define AMSIM_BN(KERNEL, SMEM, ...)                                                        \
+    do {                                                                                    \
+        if constexpr (BWD) return launch_kernel(bwd_##KERNEL<__VA_ARGS__, X, Y, N>, p, grid, SMEM, st); \
+        else return launch_kernel(fwd_##KERNEL<__VA_ARGS__, X, Y, N>, p, grid, SMEM, st);   \
+    } while (0)
     if (loads == kRing) {
-        smem = kRingBarBytes + (size_t)p.slots * p.slot_bytes + (bwd ? 8 * (size_t)p.cols : 0);
-        if (nv == 2) return AMSIM_BN(ring_kernel, 2, 256);
-        if (threads <= 256) return AMSIM_BN(ring_kernel, 4, 256);
-        return AMSIM_BN(ring_kernel, 4, 512);
+        const size_t smem = kRingBarBytes + (size_t)p.slots * p.slot_bytes + (BWD ? 8 * (size_t)p.cols : 0);
+        if (threads > 256) AMSIM_BN(ring_kernel, smem, 512, true);
+        if (full) AMSIM_BN(ring_kernel, smem, 256, true);
+        AMSIM_BN(ring_kernel, smem, 256, false);
     }
     if (loads == kVector) {
-        if (nv == 1) return AMSIM_BN(kernel, 1, 128, true);
-        if (nv == 2) return AMSIM_BN(kernel, 2, 256, true);
-        if (threads <= 512) return AMSIM_BN(kernel, 4, 512, true);
-        return AMSIM_BN(kernel, 4, 1024, true);
+        if (nv == 1) AMSIM_BN(kernel, 0, 1, 128, true);
+        if (nv == 2) AMSIM_BN(kernel, 0, 2, 128, true);
+        if (threads <= 256) AMSIM_BN(kernel, 0, 4, 256, true);
+        AMSIM_BN(kernel, 0, 4, 1024, true);
     }
-    if (nv <= 2) return AMSIM_BN(kernel, 2, 256, false);
-    return AMSIM_BN(kernel, 4, 1024, false);
+    if (nv <= 2) AMSIM_BN(kernel, 0, 2, 128, false);
+    if (threads <= 256) AMSIM_BN(kernel, 0, 4, 256, false);
+    AMSIM_BN(kernel, 0, 4, 1024, false);
 #undef AMSIM_BN
 }
 
-template <typename X>
-int launch_stream(bool bwd, int nv, Loads loads, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st)
+template <bool BWD, typename X>
+int launch_stream(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid,
+                  cudaStream_t st)
 {
     if (y_type == AMSIM_F32)
-        return n_type == AMSIM_F32 ? launch_types<X, float, float>(bwd, nv, loads, p, grid, st)
-                                   : launch_types<X, float, bf16>(bwd, nv, loads, p, grid, st);
-    return n_type == AMSIM_F32 ? launch_types<X, bf16, float>(bwd, nv, loads, p, grid, st)
-                               : launch_types<X, bf16, bf16>(bwd, nv, loads, p, grid, st);
+        return n_type == AMSIM_F32 ? launch_types<BWD, X, float, float>(nv, loads, full, p, grid, st)
+                                   : launch_types<BWD, X, float, bf16>(nv, loads, full, p, grid, st);
+    return n_type == AMSIM_F32 ? launch_types<BWD, X, bf16, float>(nv, loads, full, p, grid, st)
+                               : launch_types<BWD, X, bf16, bf16>(nv, loads, full, p, grid, st);
 }
 
 }  // namespace bn
