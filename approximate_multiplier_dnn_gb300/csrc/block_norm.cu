@@ -106,10 +106,11 @@ Shape shape(int cols, bool vec)
     return s;
 }
 
-// The ring's shape: as many rows ahead as the blocks that share an SM have
+// The ring's shape: rows at work on an SM, in blocks of their own (forward) or
+// in teams of one block (backward), and as many rows ahead of each as there is
 // room for.  slots < 2: the row is too wide (or too narrow).
 struct RingShape {
-    int tpr, blocks, slots, slot_bytes;   // blocks: resident per SM
+    int tpr, at_work, slots, slot_bytes;
 };
 RingShape ring_shape(int cols, int slot_bytes, bool bwd)
 {
@@ -117,20 +118,22 @@ RingShape ring_shape(int cols, int slot_bytes, bool bwd)
     const Shape d = shape(cols, true);
     if (d.nv != amsim::bn::kRingNV || d.tpr > 512) return s;
     s.tpr = d.tpr;
-    s.blocks = std::max(1, std::min(16, amsim::bn::ring_threads(bwd) / s.tpr));
+    s.at_work = (bwd ? amsim::bn::kTeamThreads : amsim::bn::kRingThreads) / s.tpr;
     s.slot_bytes = slot_bytes;
-    // what is not for rows: barriers, sums, the block's own kilobyte, backward the weights
-    const int rest = 2048 + amsim::bn::kRingBarBytes + (bwd ? 8 * cols : 0);
-    for (;; --s.blocks) {
-        s.slots = std::min(8, (amsim::kMaxSmemPerCta / s.blocks - rest) / slot_bytes);
-        if (s.slots >= 2 || s.blocks == 1) return s;
+    for (;; --s.at_work) {
+        // what is not for rows: barriers, sums, a block's own kilobyte, backward the weights and the teams' sums
+        const int joined = s.at_work > 1 ? amsim::bn::kTeamThreads * 16 : 0;
+        const int room = bwd ? (amsim::kMaxSmemPerCta - 2048 - amsim::bn::kRingBarBytes - 8 * cols - joined) / s.at_work
+                             : amsim::kMaxSmemPerCta / s.at_work - 2048 - amsim::bn::kRingBarBytes;
+        s.slots = std::min(8, room / slot_bytes);
+        if (s.slots >= 2 || s.at_work == 1) return s;
     }
 }
 
-// The ring needs rows to stream: at least two per resident block.
+// The ring needs rows to stream: at least two for each at work.
 bool ring_pays(int64_t rows, const RingShape &r, int sms)
 {
-    return r.slots >= 2 && rows >= (int64_t)2 * sms * r.blocks;
+    return r.slots >= 2 && rows >= (int64_t)2 * sms * r.at_work;
 }
 
 // Resident blocks per SM of the kernels that load directly: about 1024 threads.
@@ -220,7 +223,7 @@ extern "C" int amsim_block_norm_fwd(const amsim_block_norm_desc *d, const void *
         p.rpb = 1;
         p.slots = ring.slots;
         p.slot_bytes = ring.slot_bytes;
-        p.block_rows = (d->rows + (int64_t)sms * ring.blocks - 1) / ((int64_t)sms * ring.blocks);
+        p.block_rows = (d->rows + (int64_t)sms * ring.at_work - 1) / ((int64_t)sms * ring.at_work);
         grid = (d->rows + p.block_rows - 1) / p.block_rows;
     } else {
         p.tpr = s.tpr;
@@ -239,7 +242,7 @@ extern "C" size_t amsim_block_norm_workspace_size(const amsim_block_norm_desc *d
     if (check(d) || d->rows == 0) return 0;
     const int sms = device_sms();
     const Shape s = shape(d->cols, true);
-    const Shares h = shares(d, std::max(direct_blocks(s), ring_shape(d->cols, 1, true).blocks), s.rpb, sms ? sms : 1,
+    const Shares h = shares(d, direct_blocks(s), s.rpb, sms ? sms : 1,
                             INT64_MAX);
     if (h.blocks == 1 && h.splits == 1) return 0;
     const int64_t n = (h.splits > 1 ? h.items : h.blocks) + h.blocks;
@@ -320,10 +323,10 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
     if (bulk && ring_pays(d->rows, ring, sms) && (full || ring.tpr <= 256)) {
         loads = amsim::bn::kRing;
         p.tpr = ring.tpr;
-        p.rpb = 1;
+        p.rpb = ring.at_work;
         p.slots = ring.slots;
         p.slot_bytes = ring.slot_bytes;
-        per_sm = ring.blocks;
+        per_sm = 1;
     }
     const bool sums = dgate || dw_post || dw_pre;
     const int64_t slots = sums ? (ws ? (int64_t)(ws_bytes / ((size_t)d->cols * 4)) : 0) : INT64_MAX;

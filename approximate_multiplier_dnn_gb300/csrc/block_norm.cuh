@@ -172,14 +172,14 @@ __device__ __forceinline__ Four weights_u(const Params &p, const float *gate, in
 }
 
 // Sums of S values over the threads of a row (its warps are neighbours in the
-// block), S of them behind one barrier.  `which` alternates between two
+// block), all behind one barrier of at least those threads, `sync`.  `which` alternates between two
 // buffers, so that a barrier per call is enough.
 template <int S>
 struct Sums {
     float v[S];
 };
-template <int S>
-__device__ __forceinline__ void row_sums(Sums<S> &x, int warps, float (*red)[S][32], int &which)
+template <int S, typename SYNC>
+__device__ __forceinline__ void row_sums(Sums<S> &x, int warps, float (*red)[S][32], int &which, SYNC sync)
 {
 #pragma unroll
     for (int d = 16; d; d >>= 1)
@@ -192,7 +192,7 @@ __device__ __forceinline__ void row_sums(Sums<S> &x, int warps, float (*red)[S][
     if (lane == 0)
 #pragma unroll
         for (int i = 0; i < S; ++i) buf[i][warp] = x.v[i];
-    __syncthreads();
+    sync();
     const int first = warp / warps * warps;
     if (warps <= 8) {
         const int j = lane & 7;
@@ -248,7 +248,7 @@ __device__ __forceinline__ void fwd_row(const Params &p, const Raw<X> (&xr)[NV],
             for (int e = 0; e < kP; ++e) s2 = fma2(a.p[e], a.p[e], s2);
         }
         Sums<1> s{{s2.x + s2.y}};
-        row_sums(s, warps, red, which);
+        row_sums(s, warps, red, which, [] { __syncthreads(); });
         post = rsqrtf(fmaf(s.v[0], inv, p.eps));
         if (on && t == 0 && (FULL || p.rstd_post)) p.rstd_post[row] = post;
     }
@@ -269,7 +269,7 @@ __device__ __forceinline__ void fwd_row(const Params &p, const Raw<X> (&xr)[NV],
     }
     if (!has.n()) return;
     Sums<1> s{{s2.x + s2.y}};
-    row_sums(s, warps, red, which);
+    row_sums(s, warps, red, which, [] { __syncthreads(); });
     const float pre = rsqrtf(fmaf(s.v[0], inv, p.eps));
     if (on && t == 0 && (FULL || p.rstd_pre)) p.rstd_pre[row] = pre;
 #pragma unroll
@@ -294,14 +294,15 @@ struct Step {
 //   dx = q - pre m rh,  q = dr + pre t,
 //   mean(s yh) = mean(wu yh q) - pre m mean(wu yh rh),
 // all three means come from one pass over the row and one barrier.  Between the
-// passes a thread keeps q, and loads r and y again (KEEP false: from shared
-// memory or the L1 cache); the rest of its registers are the column sums', two
-// per channel.
+// passes a thread keeps q, and loads r and y again (from shared memory or the
+// L1 cache; with KEEP, narrow or unaligned rows, it keeps them too): the rest of
+// its registers are the column sums', two per channel.  Keeping bf16 rows in
+// the streaming kernel freed their slot a row earlier and was 8 % slower.
 template <int NV, bool VEC, bool FULL, bool KEEP, typename X, typename Y, typename N, typename LOAD, typename WQ,
-          typename WU, typename F>
+          typename WU, typename SYNC, typename F>
 __device__ __forceinline__ void bwd_row(const Params &p, float pre, float post, X *dxo, Y *dyo, int t, int cols,
                                         int warps, float (*red)[3][32], int &which, float2 (&a)[NV * kP],
-                                        float2 (&b)[NV * kP], LOAD load, WQ wq, WU wu, F met)
+                                        float2 (&b)[NV * kP], LOAD load, WQ wq, WU wu, SYNC sync, F met)
 {
     const Parts<FULL> has{p};
     const float inv = 1.0f / (float)p.cols;
@@ -339,7 +340,7 @@ __device__ __forceinline__ void bwd_row(const Params &p, float pre, float post, 
     }
     Sums<3> sum{{s2[0].x + s2[0].y, s2[1].x + s2[1].y, s2[2].x + s2[2].y}};
     const bool means = has.dn() || (has.y() && has.post());
-    if (means) row_sums(sum, warps, red, which);
+    if (means) row_sums(sum, warps, red, which, sync);
     met(means && warps > 1);
     const float m = pre * (sum.v[0] * inv), mr = -m * pre;
     const float s = !has.post() ? 0.0f : (has.dn() ? fmaf(-m, sum.v[2], sum.v[1]) : sum.v[1]) * inv;
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
                     return in;
                 },
                 [&](int k) { return weights<VEC>(p.w_pre, k, t, p.tpr, cols); },
-                [&](int k) { return weights_u<VEC>(p, gate, k, t, cols); }, [](bool) {});
+                [&](int k) { return weights_u<VEC>(p, gate, k, t, cols); }, [] { __syncthreads(); }, [](bool) {});
         }
         if (!sums_a) continue;
 #pragma unroll
@@ -526,26 +527,21 @@ struct Ring {
 };
 
 constexpr int kRingNV = 4;                 // steps per thread of the ring kernels
-constexpr int kRingBarBytes = 128;         // up to 16 slots
+constexpr int kRingBarBytes = 1024;        // up to 16 teams of 8 slots
 constexpr int kRingAlign = 128;
-// Threads per SM that the kernels' registers allow.
-#ifndef RTF
-#define RTF 512
-#endif
-#ifndef RTB
-#define RTB 512
-#endif
-__host__ __device__ constexpr int ring_threads(bool bwd) { return bwd ? RTB : RTF; }
+// Threads per SM that the kernels' registers allow (up to 128 each): forward as
+// blocks of up to 256 or 512, backward as the teams of one block.
+constexpr int kRingThreads = 512, kTeamThreads = 512;
 __host__ __device__ inline int ring_bytes(int cols, int size) { return (cols * size + kRingAlign - 1) / kRingAlign * kRingAlign; }
 
-__device__ __forceinline__ Ring make_ring(const Params &p, uint8_t *smem)
+__device__ __forceinline__ Ring make_ring(const Params &p, uint8_t *smem, int team, int t)
 {
     Ring r;
-    r.full = reinterpret_cast<uint64_t *>(smem);
-    r.slot0 = smem + kRingBarBytes;
+    r.full = reinterpret_cast<uint64_t *>(smem) + team * p.slots;
+    r.slot0 = smem + kRingBarBytes + team * p.slots * p.slot_bytes;
     r.slots = p.slots;
     r.bytes = p.slot_bytes;
-    if (threadIdx.x == 0) {
+    if (t == 0) {
         for (int i = 0; i < p.slots; ++i) tc::bar_init(r.full + i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -569,7 +565,7 @@ __device__ __forceinline__ Four kept(const float *w, int k, int t, int tpr, int 
 }
 
 template <int THREADS, bool FULL, typename X, typename Y, typename N>
-__global__ void __launch_bounds__(THREADS, ring_threads(false) / THREADS) fwd_ring_kernel(const Params p)
+__global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kernel(const Params p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][1][32];
@@ -579,7 +575,7 @@ __global__ void __launch_bounds__(THREADS, ring_threads(false) / THREADS) fwd_ri
     const int t = threadIdx.x, warps = p.tpr >> 5, cols = p.cols;
     const int xb = cols * (int)sizeof(X), yb = cols * (int)sizeof(Y), yoff = ring_bytes(cols, sizeof(X));
     const long long r0 = blockIdx.x * p.block_rows, r1 = min(r0 + p.block_rows, p.rows);
-    Ring ring = make_ring(p, smem);
+    Ring ring = make_ring(p, smem, 0, t);
     auto issue = [&](long long row, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
         tc::bar_expect(ring.full + slot, xb + (has.y() ? yb : 0));
@@ -622,33 +618,43 @@ __global__ void __launch_bounds__(THREADS, ring_threads(false) / THREADS) fwd_ri
     }
 }
 
-// As bwd_kernel, one row at a time per block.  The weights wait in shared
-// memory after the ring (w_pre, then alpha gate w_post of the share's gate).
-template <int THREADS, bool FULL, typename X, typename Y, typename N>
-__global__ void __launch_bounds__(THREADS, ring_threads(true) / THREADS) bwd_ring_kernel(const Params p)
+// As bwd_kernel, with the SM's threads as teams of the threads of a row, each
+// with a ring of its own.  They share the weights, which wait in shared memory
+// (w_pre, then alpha gate w_post of the share's gate): a block per row would
+// hold a copy each, and leave room for one row ahead where teams have two.
+template <bool FULL, typename X, typename Y, typename N>
+__global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][3][32];
     constexpr int NV = kRingNV;
     const Parts<FULL> has{p};
     int which = 0;
-    const int t = threadIdx.x, warps = p.tpr >> 5, cols = p.cols;
+    const int teams = p.rpb, team = threadIdx.x / p.tpr, t = threadIdx.x - team * p.tpr;
+    const int warps = p.tpr >> 5, cols = p.cols;
     const bool sums_a = has.y() && (p.dgate || p.dw_post), sums_b = has.dn() && p.dw_pre;
     const int xb = cols * (int)sizeof(X), yb = cols * (int)sizeof(Y), nb = cols * (int)sizeof(N);
     const int rxb = ring_bytes(cols, sizeof(X)), rnb = ring_bytes(cols, sizeof(N));
     const int off_r = has.dr() ? rxb : 0, off_n = off_r + (has.dn() ? rxb : 0), off_y = off_n + (has.dn() ? rnb : 0);
-    float *wq = reinterpret_cast<float *>(smem + kRingBarBytes + p.slots * p.slot_bytes);
+    float *wq = reinterpret_cast<float *>(smem + kRingBarBytes + teams * p.slots * p.slot_bytes);
     float *wu = wq + cols;
-    Ring ring = make_ring(p, smem);
-    // the rows of this block in order: shares blockIdx.x, + gridDim.x, ...
+    float4 *buf = reinterpret_cast<float4 *>(wu + cols);     // one per thread, with several teams
+    Ring ring = make_ring(p, smem, team, t);
+    auto sync = [&] {
+        if (warps == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(p.tpr) : "memory");
+    };
+    // a team's rows in order: every teams-th of shares blockIdx.x, + gridDim.x, ...
     struct Place {
         long long item, row, end;
     };
-    auto bounds = [&](Place &q) {
-        if (q.item >= p.items) { q.row = q.end = 0; return; }
-        const long long gi = q.item / p.splits, g0 = gi * p.gate_rows;
-        q.row = g0 + (q.item - gi * p.splits) * p.item_rows;
-        q.end = min(min(q.row + p.item_rows, g0 + p.gate_rows), p.rows);
+    auto settle = [&](Place &q) {            // to the share's first row of this team, or on to the next share's
+        for (; q.item < p.items; q.item += gridDim.x) {
+            const long long gi = q.item / p.splits, g0 = gi * p.gate_rows, r0 = g0 + (q.item - gi * p.splits) * p.item_rows;
+            q.row = r0 + team;
+            q.end = min(min(r0 + p.item_rows, g0 + p.gate_rows), p.rows);
+            if (q.row < q.end) return;
+        }
     };
     auto issue = [&](const Place &q, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
@@ -661,32 +667,45 @@ __global__ void __launch_bounds__(THREADS, ring_threads(true) / THREADS) bwd_rin
         if (has.y()) tc::copy_bytes(s + off_y, static_cast<const Y *>(p.y) + q.row * p.ldy, yb, ring.full + slot);
     };
     auto advance = [&](Place &q) {
-        if (++q.row < q.end) return;
+        if ((q.row += teams) < q.end) return;
         q.item += gridDim.x;
-        bounds(q);
+        settle(q);
     };
     Place ahead{(long long)blockIdx.x, 0, 0};
-    bounds(ahead);
+    settle(ahead);
     if (t == 0)
         for (int i = 0; i < p.slots && ahead.item < p.items; ++i) {
             issue(ahead, i);
             advance(ahead);
         }
     if (has.dn())
-        for (int c = t; c < cols; c += p.tpr) wq[c] = p.w_pre ? p.w_pre[c] : 1.0f;
+        for (int c = threadIdx.x; c < cols; c += blockDim.x) wq[c] = p.w_pre ? p.w_pre[c] : 1.0f;
+    // the teams' sums of four channels, in team order, in team 0's hands
+    auto joined = [&](float2 x, float2 y) {
+        float4 v = make_float4(x.x, x.y, y.x, y.y);
+        if (teams == 1) return v;
+        __syncthreads();
+        buf[threadIdx.x] = v;
+        __syncthreads();
+        if (team == 0)
+            for (int g = 1; g < teams; ++g) {
+                const float4 w = buf[g * p.tpr + t];
+                v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+            }
+        return v;
+    };
     float2 b[NV * kP];
 #pragma unroll
     for (int i = 0; i < NV * kP; ++i) b[i] = both(0.0f);
     bool fresh = true;                       // no share has left its sums in part_post yet
     int last = -1;                           // the slot of the row before, not yet refilled
     for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
-        Place q{item, 0, 0};
-        bounds(q);
-        const long long gi = item / p.splits;
+        const long long gi = item / p.splits, g0 = gi * p.gate_rows, r0 = g0 + (item - gi * p.splits) * p.item_rows;
+        const long long end = min(min(r0 + p.item_rows, g0 + p.gate_rows), p.rows), first = r0 + team;
         const float *gate = p.gate ? p.gate + gi * cols : nullptr;
         if (has.y() && (fresh || gate)) {
             __syncthreads();                 // the last share's weights are no longer read
-            for (int c = t; c < cols; c += p.tpr)
+            for (int c = threadIdx.x; c < cols; c += blockDim.x)
                 wu[c] = (p.w_post ? p.w_post[c] : 1.0f) * (p.alpha * (gate ? gate[c] : 1.0f));
         }
         if (fresh || gate) __syncthreads();
@@ -694,15 +713,15 @@ __global__ void __launch_bounds__(THREADS, ring_threads(true) / THREADS) bwd_rin
 #pragma unroll
         for (int i = 0; i < NV * kP; ++i) a[i] = both(0.0f);
         // a row's own numbers are fetched a row ahead of its work
-        auto pre_of = [&](long long row) { return has.dn() && row < q.end ? p.rstd_pre[row] : 0.0f; };
-        auto post_of = [&](long long row) { return has.y() && has.post() && row < q.end ? p.rstd_post[row] : 1.0f; };
-        float next_pre = pre_of(q.row), next_post = post_of(q.row);
-        X *dxo = static_cast<X *>(p.dx) + q.row * p.lddx;
-        Y *dyo = static_cast<Y *>(p.dy) + q.row * p.lddy;
-        for (long long row = q.row; row < q.end; ++row, dxo += p.lddx, dyo += p.lddy) {
+        auto pre_of = [&](long long row) { return has.dn() && row < end ? p.rstd_pre[row] : 0.0f; };
+        auto post_of = [&](long long row) { return has.y() && has.post() && row < end ? p.rstd_post[row] : 1.0f; };
+        float next_pre = pre_of(first), next_post = post_of(first);
+        X *dxo = static_cast<X *>(p.dx) + first * p.lddx;
+        Y *dyo = static_cast<Y *>(p.dy) + first * p.lddy;
+        for (long long row = first; row < end; row += teams, dxo += teams * p.lddx, dyo += teams * p.lddy) {
             const float pre = next_pre, post = next_post;
-            next_pre = pre_of(row + 1);
-            next_post = post_of(row + 1);
+            next_pre = pre_of(row + teams);
+            next_post = post_of(row + teams);
             const uint8_t *slot = ring.wait();
             bwd_row<NV, true, FULL, false, X, Y, N>(
                 p, pre, post, dxo, dyo, t, cols, warps, red, which, a, b,
@@ -717,9 +736,10 @@ __global__ void __launch_bounds__(THREADS, ring_threads(true) / THREADS) bwd_rin
                     return in;
                 },
                 [&](int k) { return kept(wq, k, t, p.tpr, cols); }, [&](int k) { return kept(wu, k, t, p.tpr, cols); },
+                sync,
                 [&](bool barrier) {
-                    // every thread is past the last row: its slot is free
-                    if (!barrier) __syncthreads();
+                    // every thread of the team is past the last row: its slot is free
+                    if (!barrier) sync();
                     if (t == 0 && last >= 0 && ahead.item < p.items) {
                         issue(ahead, last);
                         advance(ahead);
@@ -729,21 +749,27 @@ __global__ void __launch_bounds__(THREADS, ring_threads(true) / THREADS) bwd_rin
         }
         if (sums_a) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int e = 0; e < kE; ++e)
-                    leave_a(p, element(a[k * kP + (e >> 1)], e), channel<true>(k, e, t, p.tpr), item, gi, gate, fresh);
+            for (int k = 0; k < NV; ++k) {
+                const float4 v = joined(a[k * kP], a[k * kP + 1]);
+                const int c = channel<true>(k, 0, t, p.tpr);
+                if (team > 0) continue;
+                leave_a(p, v.x, c, item, gi, gate, fresh);
+                leave_a(p, v.y, c + 1, item, gi, gate, fresh);
+                leave_a(p, v.z, c + 2, item, gi, gate, fresh);
+                leave_a(p, v.w, c + 3, item, gi, gate, fresh);
+            }
         }
         fresh = false;
     }
     if (!sums_b) return;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            const int c = channel<true>(k, e, t, p.tpr);
-            if (c < cols) p.part_pre[(long long)blockIdx.x * cols + c] = element(b[k * kP + (e >> 1)], e);
-        }
+    for (int k = 0; k < NV; ++k) {
+        const float4 v = joined(b[k * kP], b[k * kP + 1]);
+        const int c = channel<true>(k, 0, t, p.tpr);
+        if (team > 0 || c >= cols) continue;
+        float *out = p.part_pre + (long long)blockIdx.x * cols + c;
+        out[0] = v.x; out[1] = v.y; out[2] = v.z; out[3] = v.w;
+    }
 }
 
 // ------------------------------------------------------------------ launches
@@ -774,26 +800,33 @@ template <bool BWD, typename X, typename Y, typename N>
 int launch_types(int nv, Loads loads, bool full, const Params &p, unsigned grid, cudaStream_t st)
 {
     const int threads = p.tpr * p.rpb;
-#define AMSIM_BN(KERNEL, SMEM, ...)                                                        \
-    do {                                                                                    \
-        if constexpr (BWD) return launch_kernel(bwd_##KERNEL<__VA_ARGS__, X, Y, N>, p, grid, SMEM, st); \
-        else return launch_kernel(fwd_##KERNEL<__VA_ARGS__, X, Y, N>, p, grid, SMEM, st);   \
+#define AMSIM_BN(...)                                                                             \
+    do {                                                                                          \
+        if constexpr (BWD) return launch_kernel(bwd_kernel<__VA_ARGS__, X, Y, N>, p, grid, 0, st); \
+        else return launch_kernel(fwd_kernel<__VA_ARGS__, X, Y, N>, p, grid, 0, st);              \
     } while (0)
     if (loads == kRing) {
-        const size_t smem = kRingBarBytes + (size_t)p.slots * p.slot_bytes + (BWD ? 8 * (size_t)p.cols : 0);
-        if (threads > 256) AMSIM_BN(ring_kernel, smem, 512, true);
-        if (full) AMSIM_BN(ring_kernel, smem, 256, true);
-        AMSIM_BN(ring_kernel, smem, 256, false);
+        if constexpr (BWD) {
+            const size_t smem = kRingBarBytes + (size_t)p.rpb * p.slots * p.slot_bytes + 8 * (size_t)p.cols +
+                                (p.rpb > 1 ? kTeamThreads * sizeof(float4) : 0);
+            if (full) return launch_kernel(bwd_ring_kernel<true, X, Y, N>, p, grid, smem, st);
+            return launch_kernel(bwd_ring_kernel<false, X, Y, N>, p, grid, smem, st);
+        } else {
+            const size_t smem = kRingBarBytes + (size_t)p.slots * p.slot_bytes;
+            if (threads > 256) return launch_kernel(fwd_ring_kernel<512, true, X, Y, N>, p, grid, smem, st);
+            if (full) return launch_kernel(fwd_ring_kernel<256, true, X, Y, N>, p, grid, smem, st);
+            return launch_kernel(fwd_ring_kernel<256, false, X, Y, N>, p, grid, smem, st);
+        }
     }
     if (loads == kVector) {
-        if (nv == 1) AMSIM_BN(kernel, 0, 1, 128, true);
-        if (nv == 2) AMSIM_BN(kernel, 0, 2, 128, true);
-        if (threads <= 256) AMSIM_BN(kernel, 0, 4, 256, true);
-        AMSIM_BN(kernel, 0, 4, 1024, true);
+        if (nv == 1) AMSIM_BN(1, 128, true);
+        if (nv == 2) AMSIM_BN(2, 128, true);
+        if (threads <= 256) AMSIM_BN(4, 256, true);
+        AMSIM_BN(4, 1024, true);
     }
-    if (nv <= 2) AMSIM_BN(kernel, 0, 2, 128, false);
-    if (threads <= 256) AMSIM_BN(kernel, 0, 4, 256, false);
-    AMSIM_BN(kernel, 0, 4, 1024, false);
+    if (nv <= 2) AMSIM_BN(2, 128, false);
+    if (threads <= 256) AMSIM_BN(4, 256, false);
+    AMSIM_BN(4, 1024, false);
 #undef AMSIM_BN
 }
 
