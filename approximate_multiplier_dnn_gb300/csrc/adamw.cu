@@ -17,13 +17,22 @@
 #include <cuda_bf16.h>
 
 #include "amsim_internal.h"
+#include "pairs.cuh"
 
 namespace {
 
+using amsim::both;
+using amsim::mul2;
+
 constexpr int kThreads = 256;
 constexpr int kBlock = AMSIM_ADAMW_BLOCK;
-constexpr int kChunk = 4096;                       // elements of one thread block
-static_assert(kChunk % (kThreads * 8) == 0 && kBlock == 32 * 8, "one 8-bit block per warp pass");
+constexpr int kPass = kThreads * 8;                // elements a thread block takes at once
+static_assert(kBlock == 32 * 8, "one 8-bit block per warp and pass");
+// Passes of a thread block: one, so that small steps fill the GPU, and with
+// 8-bit moments eight once there are enough elements to fill it all the same
+// (kLong): the loads of a pass then run ahead of the arithmetic of the last.
+constexpr int kLongPasses = 8;
+constexpr long long kLong = 10'000'000;
 
 struct Tensor {
     float *p;
@@ -47,12 +56,12 @@ struct Hyper {
 template <int CAP>
 struct Launch {
     Hyper h;
-    int count;
+    int count, passes;
     Tensor t[CAP];
 };
 // Capacities: a launch's parameters are copied whole, so a few tensors take a
 // small struct.
-constexpr int kCapacity[] = {8, 64, 400};
+constexpr int kCapacity[] = {8, 128, 400};
 static_assert(sizeof(Launch<400>) <= 32764, "kernel parameters");
 
 __device__ __forceinline__ float bf16_bits(uint32_t half) { return __uint_as_float(half << 16); }
@@ -74,16 +83,23 @@ __device__ __forceinline__ float step1(float p, float g, float &m, float &v, flo
     return __fsub_rn(__fmul_rn(p, t.keep), __fmul_rn(u, t.rate));
 }
 
+// The tensor of a block's chunk: one thread looks, so that the others' issue
+// slots are not spent on it.
 template <int CAP>
 __device__ __forceinline__ const Tensor &find(const Launch<CAP> &L, int chunk)
 {
-    int lo = 0, hi = L.count;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (L.t[mid].first <= chunk) lo = mid;
-        else hi = mid;
+    __shared__ int found;
+    if (threadIdx.x == 0) {
+        int lo = 0, hi = L.count;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (L.t[mid].first <= chunk) lo = mid;
+            else hi = mid;
+        }
+        found = lo;
     }
-    return L.t[lo];
+    __syncthreads();
+    return L.t[found];
 }
 
 // Eight elements of a tensor from element i (i % 8 == 0 within the tensor).
@@ -134,36 +150,26 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const Hyper &h = L.h;
     const float gs = h.grad_scale ? *h.grad_scale : 1.0f;
     const bool scaled = h.grad_scale != nullptr;
-    const long long i0 = (long long)((int)blockIdx.x - t.first) * kChunk;
+    const long long i0 = (long long)((int)blockIdx.x - t.first) * kPass;
     float *m = static_cast<float *>(t.m), *v = static_cast<float *>(t.v);
-    if (t.flags & kVector) {
+    const long long i = i0 + threadIdx.x * 8;
+    if ((t.flags & kVector) && i + 8 <= t.n) {
+        Eight p = load8(t.p, i), g = load8_grad(t, i), mm = load8(m, i), vv = load8(v, i);
 #pragma unroll
-        for (int k = 0; k < kChunk / (kThreads * 8); ++k) {
-            const long long i = i0 + (k * kThreads + threadIdx.x) * 8;
-            if (i + 8 <= t.n) {
-                Eight p = load8(t.p, i), g = load8_grad(t, i), mm = load8(m, i), vv = load8(v, i);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float s;
-                    p.x[j] = step1(p.x[j], scaled ? __fmul_rn(g.x[j], gs) : g.x[j], mm.x[j], vv.x[j], s, h, t);
-                }
-                store8(t.p, i, p);
-                store8(m, i, mm);
-                store8(v, i, vv);
-                if (t.copy) store8(t.copy, i, p);
-            } else {
-                for (long long e = i; e < t.n; ++e) {
-                    float s, g = load_grad(t, e);
-                    const float p = step1(t.p[e], scaled ? __fmul_rn(g, gs) : g, m[e], v[e], s, h, t);
-                    t.p[e] = p;
-                    if (t.copy) t.copy[e] = __float2bfloat16_rn(p);
-                }
-            }
+        for (int j = 0; j < 8; ++j) {
+            float s;
+            p.x[j] = step1(p.x[j], scaled ? __fmul_rn(g.x[j], gs) : g.x[j], mm.x[j], vv.x[j], s, h, t);
         }
+        store8(t.p, i, p);
+        store8(m, i, mm);
+        store8(v, i, vv);
+        if (t.copy) store8(t.copy, i, p);
         return;
     }
-    const long long end = i0 + kChunk < t.n ? i0 + kChunk : t.n;
-    for (long long e = i0 + threadIdx.x; e < end; e += kThreads) {
+    // a tensor's last elements by the thread they fall to, unaligned ones neighbour by neighbour
+    const bool vec = t.flags & kVector;
+    const long long end = min(vec ? i + 8 : i0 + kPass, t.n);
+    for (long long e = vec ? i : i0 + threadIdx.x; e < end; e += vec ? 1 : kThreads) {
         float s, g = load_grad(t, e);
         const float p = step1(t.p[e], scaled ? __fmul_rn(g, gs) : g, m[e], v[e], s, h, t);
         t.p[e] = p;
@@ -176,149 +182,322 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 // of code / top, times the block's scale.  A power of two in the exponent of
 // the map buys range: the smallest second moment a block tells from zero is
 // 255^-4 of its largest.
-__device__ __forceinline__ float value_m(int q, float scale)
+//
+// Codes and floats are converted through the mantissa of 2^23 (or 1.5 * 2^23):
+// the conversion and rounding instructions share the unit of the roots, which
+// at a quarter of the rate would alone take 0.9 of the time of the bytes.
+constexpr uint32_t kOneUlp = 0x4B000000u;          // 2^23: its ulp is 1
+constexpr float kRounder = 12582912.0f;            // 1.5 * 2^23: x + kRounder rounds x to an integer
+
+// Byte `j` of `w` as a float (signed: as int8).
+template <bool SIGNED>
+__device__ __forceinline__ float byte_float(uint32_t w, int j)
 {
-    const float t = __fmul_rn((float)q, 1.0f / 127.0f);
-    return __fmul_rn(__fmul_rn(t, fabsf(t)), scale);
+    const uint32_t bits = __byte_perm(SIGNED ? w ^ 0x80808080u : w, kOneUlp, 0x7540 + j);
+    return __fsub_rn(__uint_as_float(bits), SIGNED ? 8388608.0f + 128.0f : 8388608.0f);
 }
-__device__ __forceinline__ float value_v(unsigned q, float scale)
+
+__device__ __forceinline__ float2 values_m(float2 q, float scale)
 {
-    const float t = __fmul_rn((float)q, 1.0f / 255.0f);
-    const float t2 = __fmul_rn(t, t);
-    return __fmul_rn(__fmul_rn(t2, t2), scale);
+    const float2 t = mul2(q, both(1.0f / 127.0f));
+    return mul2(mul2(t, make_float2(fabsf(t.x), fabsf(t.y))), both(scale));
+}
+__device__ __forceinline__ float2 values_v(float2 q, float scale)
+{
+    const float2 t = mul2(q, both(1.0f / 255.0f)), t2 = mul2(t, t);
+    return mul2(mul2(t2, t2), both(scale));
+}
+
+// Codes round(sqrt(x) * k) of eight values as correctly rounded operations give
+// them, at least `least`, with the sign of `sign`'s top bit; one per byte.  The
+// approximate root (2^-23) moves root * k by less than 1e-4: only when one of
+// the eight is within twice that of a half are the roots taken again, rounded.
+__device__ __forceinline__ float sqrt_fast(float x)
+{
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __noinline__ float root_times(float x, float k) { return __fmul_rn(__fsqrt_rn(x), k); }
+template <typename X, typename LEAST, typename SIGN>
+__device__ __forceinline__ uint2 codes8(float k, X x, LEAST least, SIGN sign)
+{
+    float y[8], far = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        y[j] = fmaxf(__fmul_rn(sqrt_fast(x(j)), k), least(j));
+        far = fmaxf(far, fabsf(__fsub_rn(y[j], __fsub_rn(__fadd_rn(y[j], kRounder), kRounder))));
+    }
+    if (far > 0.4998f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = fmaxf(root_times(x(j), k), least(j));
+    }
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        c[j] = __float_as_uint(__fadd_rn(__uint_as_float(__float_as_uint(y[j]) | sign(j)), kRounder));
+    auto word = [&](int j) {
+        return __byte_perm(__byte_perm(c[j], c[j + 1], 0x0040), __byte_perm(c[j + 2], c[j + 3], 0x0040), 0x5410);
+    };
+    return make_uint2(word(0), word(4));
 }
 
 // Largest value of the warp's lanes; values are magnitudes or NaN (as bits,
 // magnitudes order like integers and every NaN is above infinity).
-__device__ __forceinline__ float warp_top(float x)
-{
-    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu));
-}
-__device__ __forceinline__ float top(float a, float b)
-{
-    const uint32_t x = __float_as_uint(a) & 0x7FFFFFFFu, y = __float_as_uint(b) & 0x7FFFFFFFu;
-    return __uint_as_float(x > y ? x : y);
-}
+__device__ __forceinline__ float warp_top(uint32_t x) { return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, x)); }
 __device__ __forceinline__ float finite_or_nan(float x) { return x <= 3.402823466e38f ? x : __uint_as_float(0x7FC00000u); }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ Launch<CAP> L)
+// The steps of two elements, as step1: products in pairs, sums one by one (a
+// packed product and sum come out contracted).
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 step2(float2 p, float2 g, float2 &m, float2 &v, float2 &s, const Hyper &h,
+                                        const Tensor &t)
 {
+    m = sum2(mul2(m, both(h.beta1)), mul2(g, both(h.one_minus_beta1)));
+    v = sum2(mul2(v, both(h.beta2)), mul2(mul2(g, g), both(h.one_minus_beta2)));
+    s = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+    const float2 d = sum2(mul2(s, both(h.root)), both(h.eps));
+    const float2 u = make_float2(__fdiv_rn(m.x, d.x), __fdiv_rn(m.y, d.y));
+    return sum2(mul2(p, both(t.keep)), mul2(u, both(-t.rate)));
+}
+
+// What a lane holds of a block: elements 4 lane .. and 128 + 4 lane .., so that
+// each load of the warp is of whole neighbouring sectors.
+struct Held {
+    float4 p[2];
+    uint32_t g[8];             // fp32, or bf16 in the first four
+    uint32_t m[2], v[2];
+};
+constexpr int kStages = 3;
+constexpr int kStageWords = 32 * (8 + 8 + 2 + 2);          // of a warp
+constexpr int kAheadBytes = kStages * (kThreads / 32) * kStageWords * 4;
+
+__device__ __forceinline__ void copy_async(uint32_t *dst, const void *src, int bytes)
+{
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+}
+
+// One warp per block of 256 elements.  AHEAD: with several passes, the next two
+// passes' words are on their way to shared memory (each lane copies and reads
+// its own, so nothing but its own copies is waited for).
+template <int CAP, bool AHEAD>
+__global__ void __launch_bounds__(kThreads, AHEAD ? 3 : 4) adamw8_kernel(const __grid_constant__ Launch<CAP> L)
+{
+    extern __shared__ __align__(16) uint32_t staged[];
     const Tensor &t = find(L, (int)blockIdx.x);
     const Hyper &h = L.h;
     const float gs = h.grad_scale ? *h.grad_scale : 1.0f;
-    const bool scaled = h.grad_scale != nullptr;
-    const long long i0 = (long long)((int)blockIdx.x - t.first) * kChunk;
+    const bool scaled = h.grad_scale != nullptr, half = t.flags & kBf16Grad;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int8_t *mq = static_cast<int8_t *>(t.m);
-    uint8_t *vq = static_cast<uint8_t *>(t.v);
+    const int passes = AHEAD ? L.passes : 1;
+    // the warp's first block and the distance to its next
+    const long long first = (long long)((int)blockIdx.x - t.first) * passes * kPass + warp * kBlock;
+    uint8_t *mq = static_cast<uint8_t *>(t.m), *vq = static_cast<uint8_t *>(t.v);
+    uint32_t *const mine = staged + warp * kStages * kStageWords;
+    auto whole = [&](long long b0) { return (t.flags & kVector) && b0 + kBlock <= t.n; };
+    auto fetch = [&](int k) {                  // pass k's words to its stage
+        const long long b0 = first + (long long)k * kPass;
+        if (k < passes && whole(b0)) {
+            uint32_t *s = mine + k % kStages * kStageWords;
 #pragma unroll
-    for (int k = 0; k < kChunk / (kThreads * 8); ++k) {
-        const long long b0 = i0 + (k * (kThreads / 32) + warp) * kBlock;     // the warp's block
-        if (b0 >= t.n) return;
-        const long long i = b0 + lane * 8;
-        const bool vec = (t.flags & kVector) && b0 + kBlock <= t.n;
-        const float ms = t.m_scale[b0 / kBlock], vs = t.v_scale[b0 / kBlock];
-        Eight p, g, mm, vv;
-        if (vec) {
-            p = load8(t.p, i);
-            g = load8_grad(t, i);
-            const uint2 a = *reinterpret_cast<const uint2 *>(mq + i), b = *reinterpret_cast<const uint2 *>(vq + i);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t wa = j < 4 ? a.x : a.y, wb = j < 4 ? b.x : b.y;
-                mm.x[j] = value_m((int8_t)(wa >> (8 * (j & 3)) & 0xFFu), ms);
-                vv.x[j] = value_v(wb >> (8 * (j & 3)) & 0xFFu, vs);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool in = i + j < t.n;
-                p.x[j] = in ? t.p[i + j] : 0.0f;
-                g.x[j] = in ? load_grad(t, i + j) : 0.0f;
-                mm.x[j] = in ? value_m(mq[i + j], ms) : 0.0f;
-                vv.x[j] = in ? value_v(vq[i + j], vs) : 0.0f;
+            for (int q = 0; q < 2; ++q) {
+                const long long i = b0 + q * 128 + lane * 4;
+                copy_async(s + q * 128 + lane * 4, t.p + i, 16);
+                if (half) copy_async(s + 256 + q * 64 + lane * 2, static_cast<const __nv_bfloat16 *>(t.g) + i, 8);
+                else copy_async(s + 256 + q * 128 + lane * 4, static_cast<const float *>(t.g) + i, 16);
+                copy_async(s + 512 + q * 32 + lane, mq + i, 4);
+                copy_async(s + 576 + q * 32 + lane, vq + i, 4);
             }
         }
-        Eight root;
-        float mt = 0.0f, vt = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float s;
-            p.x[j] = step1(p.x[j], scaled ? __fmul_rn(g.x[j], gs) : g.x[j], mm.x[j], vv.x[j], s, h, t);
-            root.x[j] = s;
-            mt = top(mt, mm.x[j]);
-            vt = top(vt, vv.x[j]);
-        }
-        mt = warp_top(mt);
-        vt = warp_top(vt);
-        const float mr = __fsqrt_rn(mt), vr = __fsqrt_rn(__fsqrt_rn(vt));
-        const float mk = mr > 0.0f ? __fdiv_rn(127.0f, mr) : 0.0f, vk = vr > 0.0f ? __fdiv_rn(255.0f, vr) : 0.0f;
-        uint32_t ma[2] = {0, 0}, va[2] = {0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int qm = (int)fminf(rintf(__fmul_rn(__fsqrt_rn(fabsf(mm.x[j])), mk)), 127.0f);
-            const int sm = mm.x[j] < 0.0f ? -qm : qm;
-            int qv = (int)fminf(rintf(__fmul_rn(__fsqrt_rn(root.x[j]), vk)), 255.0f);
-            if (vv.x[j] > 0.0f && qv < 1) qv = 1;
-            ma[j >> 2] |= (uint32_t)(sm & 0xFF) << (8 * (j & 3));
-            va[j >> 2] |= (uint32_t)(qv & 0xFF) << (8 * (j & 3));
-        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto scale_of = [&](const float *s, int k) {
+        const long long b0 = first + (long long)k * kPass;
+        return k < passes && b0 < t.n ? s[b0 / kBlock] : 0.0f;
+    };
+    if (AHEAD) {
+        fetch(0);
+        fetch(1);
+    }
+    float next_ms = scale_of(t.m_scale, 0), next_vs = scale_of(t.v_scale, 0);
+#pragma unroll 1
+    for (int k = 0; k < passes; ++k) {
+        const long long b0 = first + (long long)k * kPass;
+        if (b0 >= t.n) break;
+        const bool vec = whole(b0);
+        const float ms = next_ms, vs = next_vs;
+        float p[8], g[8];
+        uint32_t a[2], b[2];
         if (vec) {
-            store8(t.p, i, p);
-            if (t.copy) store8(t.copy, i, p);
-            *reinterpret_cast<uint2 *>(mq + i) = make_uint2(ma[0], ma[1]);
-            *reinterpret_cast<uint2 *>(vq + i) = make_uint2(va[0], va[1]);
-        } else {
+            Held w;
+            if (AHEAD) {
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                const uint32_t *s = mine + k % kStages * kStageWords;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (i + j < t.n) {
-                    t.p[i + j] = p.x[j];
-                    if (t.copy) t.copy[i + j] = __float2bfloat16_rn(p.x[j]);
-                    mq[i + j] = (int8_t)(ma[j >> 2] >> (8 * (j & 3)) & 0xFFu);
-                    vq[i + j] = (uint8_t)(va[j >> 2] >> (8 * (j & 3)) & 0xFFu);
+                for (int q = 0; q < 2; ++q) {
+                    w.p[q] = *reinterpret_cast<const float4 *>(s + q * 128 + lane * 4);
+                    if (half) *reinterpret_cast<uint2 *>(w.g + q * 2) = *reinterpret_cast<const uint2 *>(s + 256 + q * 64 + lane * 2);
+                    else *reinterpret_cast<uint4 *>(w.g + q * 4) = *reinterpret_cast<const uint4 *>(s + 256 + q * 128 + lane * 4);
+                    w.m[q] = s[512 + q * 32 + lane];
+                    w.v[q] = s[576 + q * 32 + lane];
                 }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const long long i = b0 + q * 128 + lane * 4;
+                    w.p[q] = *reinterpret_cast<const float4 *>(t.p + i);
+                    if (half) *reinterpret_cast<uint2 *>(w.g + q * 2) = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(t.g) + i);
+                    else *reinterpret_cast<uint4 *>(w.g + q * 4) = *reinterpret_cast<const uint4 *>(static_cast<const float *>(t.g) + i);
+                    w.m[q] = *reinterpret_cast<const uint32_t *>(mq + i);
+                    w.v[q] = *reinterpret_cast<const uint32_t *>(vq + i);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                *reinterpret_cast<float4 *>(p + q * 4) = w.p[q];
+                a[q] = w.m[q];
+                b[q] = w.v[q];
+            }
+            if (half) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    g[2 * j] = __uint_as_float(w.g[j] << 16);
+                    g[2 * j + 1] = __uint_as_float(w.g[j] & 0xFFFF0000u);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = __uint_as_float(w.g[j]);
+            }
+        } else {
+            a[0] = a[1] = b[0] = b[1] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const long long e = b0 + (j >> 2) * 128 + lane * 4 + (j & 3);
+                const bool in = e < t.n;
+                p[j] = in ? t.p[e] : 0.0f;
+                g[j] = in ? load_grad(t, e) : 0.0f;
+                a[j >> 2] |= (in ? (uint32_t)mq[e] : 0u) << (8 * (j & 3));
+                b[j >> 2] |= (in ? (uint32_t)vq[e] : 0u) << (8 * (j & 3));
+            }
+        }
+        if (AHEAD) {
+            fetch(k + 2);
+            next_ms = scale_of(t.m_scale, k + 1);
+            next_vs = scale_of(t.v_scale, k + 1);
+        }
+        float2 mm[4], vv[4], root[4];
+        uint32_t mt = 0, vt = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t x = a[j >> 1], y = b[j >> 1];
+            const int o = 2 * (j & 1);
+            mm[j] = values_m(make_float2(byte_float<true>(x, o), byte_float<true>(x, o + 1)), ms);
+            vv[j] = values_v(make_float2(byte_float<false>(y, o), byte_float<false>(y, o + 1)), vs);
+            float2 gg = make_float2(g[2 * j], g[2 * j + 1]);
+            if (scaled) gg = mul2(gg, both(gs));
+            const float2 q = step2(make_float2(p[2 * j], p[2 * j + 1]), gg, mm[j], vv[j], root[j], h, t);
+            p[2 * j] = q.x;
+            p[2 * j + 1] = q.y;
+            mt = max(mt, max(__float_as_uint(mm[j].x) & 0x7FFFFFFFu, __float_as_uint(mm[j].y) & 0x7FFFFFFFu));
+            vt = max(vt, max(__float_as_uint(vv[j].x) & 0x7FFFFFFFu, __float_as_uint(vv[j].y) & 0x7FFFFFFFu));
+        }
+        if (vec) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const long long i = b0 + q * 128 + lane * 4;
+                *reinterpret_cast<float4 *>(t.p + i) = *reinterpret_cast<const float4 *>(p + q * 4);
+                if (t.copy)
+                    *reinterpret_cast<uint2 *>(t.copy + i) =
+                        make_uint2(pack_bf16(p[q * 4], p[q * 4 + 1]), pack_bf16(p[q * 4 + 2], p[q * 4 + 3]));
+            }
+        }
+        const float mtop = warp_top(mt), vtop = warp_top(vt);
+        const float mr = __fsqrt_rn(mtop), vr = __fsqrt_rn(__fsqrt_rn(vtop));
+        const float mk = mr > 0.0f ? __fdiv_rn(127.0f, mr) : 0.0f, vk = vr > 0.0f ? __fdiv_rn(255.0f, vr) : 0.0f;
+        auto at = [](const float2 (&x)[4], int j) { return j & 1 ? x[j >> 1].y : x[j >> 1].x; };
+        const uint2 ma = codes8(mk, [&](int j) { return fabsf(at(mm, j)); }, [](int) { return 0.0f; },
+                                [&](int j) { return __float_as_uint(at(mm, j)) & 0x80000000u; });
+        // a second moment above zero keeps a code above zero
+        const uint2 va = codes8(vk, [&](int j) { return at(root, j); },
+                                [&](int j) { return at(vv, j) > 0.0f ? 1.0f : 0.0f; }, [](int) { return 0u; });
+        if (vec) {
+            *reinterpret_cast<uint32_t *>(mq + b0 + lane * 4) = ma.x;
+            *reinterpret_cast<uint32_t *>(mq + b0 + 128 + lane * 4) = ma.y;
+            *reinterpret_cast<uint32_t *>(vq + b0 + lane * 4) = va.x;
+            *reinterpret_cast<uint32_t *>(vq + b0 + 128 + lane * 4) = va.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const long long e = b0 + (j >> 2) * 128 + lane * 4 + (j & 3);
+                if (e < t.n) {
+                    t.p[e] = p[j];
+                    if (t.copy) t.copy[e] = __float2bfloat16_rn(p[j]);
+                    mq[e] = (uint8_t)((j < 4 ? ma.x : ma.y) >> (8 * (j & 3)) & 0xFFu);
+                    vq[e] = (uint8_t)((j < 4 ? va.x : va.y) >> (8 * (j & 3)) & 0xFFu);
+                }
+            }
         }
         if (lane == 0) {
-            t.m_scale[b0 / kBlock] = finite_or_nan(mt);
-            t.v_scale[b0 / kBlock] = finite_or_nan(vt);
+            t.m_scale[b0 / kBlock] = finite_or_nan(mtop);
+            t.v_scale[b0 / kBlock] = finite_or_nan(vtop);
         }
     }
+    if (AHEAD) asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kThreads) moment_values_kernel(const void *codes, const float *scales, int second,
-                                                                 long long n, float *out, int vec)
+// Four codes per thread and step: whole sectors of both codes and values.
+constexpr int kValueSteps = 4;
+template <bool SECOND>
+__global__ void __launch_bounds__(kThreads) moment_values_kernel(const uint8_t *codes, const float *scales, long long n,
+                                                                 float *out, int vec)
 {
-    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * 8;
-    if (i >= n) return;
-    const float s = scales[i / kBlock];
-    if (vec && i + 8 <= n) {
-        const uint2 a = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(codes) + i);
-        Eight r;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t q = (j < 4 ? a.x : a.y) >> (8 * (j & 3)) & 0xFFu;
-            r.x[j] = second ? value_v(q, s) : value_m((int8_t)q, s);
+    for (int k = 0; k < kValueSteps; ++k) {
+        const long long i = (((long long)blockIdx.x * kValueSteps + k) * kThreads + threadIdx.x) * 4;
+        if (i >= n) return;
+        const float s = scales[i / kBlock];
+        uint32_t w = 0;
+        const bool whole = vec && i + 4 <= n;
+        if (whole) w = *reinterpret_cast<const uint32_t *>(codes + i);
+        else
+            for (int j = 0; j < 4 && i + j < n; ++j) w |= (uint32_t)codes[i + j] << (8 * j);
+        const float2 a = make_float2(byte_float<!SECOND>(w, 0), byte_float<!SECOND>(w, 1));
+        const float2 b = make_float2(byte_float<!SECOND>(w, 2), byte_float<!SECOND>(w, 3));
+        const float2 x = SECOND ? values_v(a, s) : values_m(a, s), y = SECOND ? values_v(b, s) : values_m(b, s);
+        if (whole) {
+            *reinterpret_cast<float4 *>(out + i) = make_float4(x.x, x.y, y.x, y.y);
+        } else {
+            const float r[4] = {x.x, x.y, y.x, y.y};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j < n) out[i + j] = r[j];
         }
-        store8(out, i, r);
-        return;
     }
-    for (long long e = i; e < n && e < i + 8; ++e)
-        out[e] = second ? value_v(static_cast<const uint8_t *>(codes)[e], s)
-                        : value_m(static_cast<const int8_t *>(codes)[e], s);
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 template <int CAP>
-int launch(const Hyper &h, const Tensor *t, int count, int chunks, bool eight, cudaStream_t st)
+int launch(const Hyper &h, const Tensor *t, int count, int chunks, int passes, bool eight, cudaStream_t st)
 {
     Launch<CAP> L;
     L.h = h;
     L.count = count;
+    L.passes = passes;
     for (int i = 0; i < count; ++i) L.t[i] = t[i];
-    if (eight) adamw8_kernel<CAP><<<(unsigned)chunks, kThreads, 0, st>>>(L);
-    else adamw_kernel<CAP><<<(unsigned)chunks, kThreads, 0, st>>>(L);
+    if (!eight) {
+        adamw_kernel<CAP><<<(unsigned)chunks, kThreads, 0, st>>>(L);
+    } else if (passes == 1) {
+        adamw8_kernel<CAP, false><<<(unsigned)chunks, kThreads, 0, st>>>(L);
+    } else {
+        const cudaError_t e = cudaFuncSetAttribute(adamw8_kernel<CAP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kAheadBytes);
+        if (e != cudaSuccess) return amsim::cuda_status(e);
+        adamw8_kernel<CAP, true><<<(unsigned)chunks, kThreads, kAheadBytes, st>>>(L);
+    }
     const int rc = amsim::cuda_status(cudaGetLastError());
     if (rc == AMSIM_OK) amsim::count_launch();
     return rc;
@@ -335,6 +514,7 @@ extern "C" int amsim_adamw_step(int count, const amsim_adamw_tensor *tensors, co
         !(y.eps >= 0.0) || !std::isfinite(y.eps) || y.step < 1 || !aligned(y.grad_scale, 4))
         return AMSIM_EINVAL;
     bool any = false, eight = false;
+    double total = 0.0;
     for (int i = 0; i < count; ++i) {
         const amsim_adamw_tensor &a = tensors[i];
         if (a.n < 0 || (a.g_type != AMSIM_F32 && a.g_type != AMSIM_BF16) || a.reserved != 0 ||
@@ -349,7 +529,8 @@ extern "C" int amsim_adamw_step(int count, const amsim_adamw_tensor *tensors, co
         if (any && e != eight) return AMSIM_EINVAL;
         any = true;
         eight = e;
-        if ((a.n + kChunk - 1) / kChunk > 0x3FFFFFFF) return AMSIM_EINVAL;
+        if ((a.n + kPass - 1) / kPass > 0x3FFFFFFF) return AMSIM_EINVAL;
+        total += (double)a.n;
     }
     Hyper h;
     h.beta1 = (float)y.beta1;
@@ -364,16 +545,18 @@ extern "C" int amsim_adamw_step(int count, const amsim_adamw_tensor *tensors, co
     constexpr int kMost = kCapacity[2];
     Tensor t[kMost];
     int used = 0, chunks = 0;
+    const int passes = eight && total >= (double)kLong ? kLongPasses : 1;
+    const long long chunk = (long long)passes * kPass;
     for (int i = 0; i <= count; ++i) {
         long long add = 0;
         if (i < count) {
-            add = (tensors[i].n + kChunk - 1) / kChunk;
+            add = (tensors[i].n + chunk - 1) / chunk;
             if (add == 0) continue;
         }
         if (used && (i == count || used == kMost || chunks + add > 0x7FFFFFFFLL)) {
-            const int rc = used <= kCapacity[0]   ? launch<kCapacity[0]>(h, t, used, chunks, eight, st)
-                           : used <= kCapacity[1] ? launch<kCapacity[1]>(h, t, used, chunks, eight, st)
-                                                  : launch<kMost>(h, t, used, chunks, eight, st);
+            const int rc = used <= kCapacity[0]   ? launch<kCapacity[0]>(h, t, used, chunks, passes, eight, st)
+                           : used <= kCapacity[1] ? launch<kCapacity[1]>(h, t, used, chunks, passes, eight, st)
+                                                  : launch<kMost>(h, t, used, chunks, passes, eight, st);
             if (rc) return rc;
             used = 0;
             chunks = 0;
@@ -408,10 +591,14 @@ extern "C" int amsim_adamw_moment_values(const void *codes, const float *scales,
     if (n < 0) return AMSIM_EINVAL;
     if (n == 0) return AMSIM_OK;
     if (!codes || !scales || !out || !aligned(scales, 4) || !aligned(out, 4)) return AMSIM_EINVAL;
-    const long long blocks = (n + kThreads * 8 - 1) / (kThreads * 8);
+    constexpr int kPerBlock = kThreads * 4 * kValueSteps;
+    const long long blocks = (n + kPerBlock - 1) / kPerBlock;
     if (blocks > 0x7FFFFFFFLL) return AMSIM_EINVAL;
-    moment_values_kernel<<<(unsigned)blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        codes, scales, second, n, out, aligned(codes, 8) && aligned(out, 16));
+    const uint8_t *q = static_cast<const uint8_t *>(codes);
+    const int vec = aligned(codes, 4) && aligned(out, 16);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (second) moment_values_kernel<true><<<(unsigned)blocks, kThreads, 0, st>>>(q, scales, n, out, vec);
+    else moment_values_kernel<false><<<(unsigned)blocks, kThreads, 0, st>>>(q, scales, n, out, vec);
     const int rc = amsim::cuda_status(cudaGetLastError());
     if (rc == AMSIM_OK) amsim::count_launch();
     return rc;

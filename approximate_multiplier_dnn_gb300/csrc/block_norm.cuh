@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 
 #include "bounded_wait.cuh"
+#include "pairs.cuh"
 
 namespace amsim {
 namespace bn {
@@ -37,25 +38,6 @@ struct Params {
     int slots, slot_bytes;                 // ring kernels: rows ahead in shared memory, bytes of one
     float alpha, eps;
 };
-
-// ------------------------------------------------------------------ pairs
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // Channels a thread takes at a step: 16 bytes of fp32, 8 of bf16, so that a
 // warp's loads and stores are whole neighbouring sectors whichever the type.
