@@ -210,17 +210,19 @@ __device__ __forceinline__ float2 values_v(float2 q, float scale)
 
 // Codes round(sqrt(x) * k) of eight values as correctly rounded operations give
 // them, at least `least`, with the sign of `sign`'s top bit; one per byte.  The
-// approximate root (2^-23) moves root * k by less than 1e-4: only when one of
-// the eight is within twice that of a half are the roots taken again, rounded.
+// approximate root (2^-23) moves root * k by less than 7e-5: only when one of
+// the eight is nearer than 1e-4 to a half (or `precise`: the block's moments are
+// so small that it takes some of them for zero) are the roots taken again,
+// rounded.
 __device__ __forceinline__ float sqrt_fast(float x)
 {
     float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __noinline__ float root_times(float x, float k) { return __fmul_rn(__fsqrt_rn(x), k); }
 template <typename X, typename LEAST, typename SIGN>
-__device__ __forceinline__ uint2 codes8(float k, X x, LEAST least, SIGN sign)
+__device__ __forceinline__ uint2 codes8(float k, bool precise, X x, LEAST least, SIGN sign)
 {
     float y[8], far = 0.0f;
 #pragma unroll
@@ -228,7 +230,7 @@ __device__ __forceinline__ uint2 codes8(float k, X x, LEAST least, SIGN sign)
         y[j] = fmaxf(__fmul_rn(sqrt_fast(x(j)), k), least(j));
         far = fmaxf(far, fabsf(__fsub_rn(y[j], __fsub_rn(__fadd_rn(y[j], kRounder), kRounder))));
     }
-    if (far > 0.4998f) {
+    if (far > 0.4999f || precise) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = fmaxf(root_times(x(j), k), least(j));
     }
@@ -418,10 +420,10 @@ __global__ void __launch_bounds__(kThreads, AHEAD ? 3 : 4) adamw8_kernel(const _
         const float mr = __fsqrt_rn(mtop), vr = __fsqrt_rn(__fsqrt_rn(vtop));
         const float mk = mr > 0.0f ? __fdiv_rn(127.0f, mr) : 0.0f, vk = vr > 0.0f ? __fdiv_rn(255.0f, vr) : 0.0f;
         auto at = [](const float2 (&x)[4], int j) { return j & 1 ? x[j >> 1].y : x[j >> 1].x; };
-        const uint2 ma = codes8(mk, [&](int j) { return fabsf(at(mm, j)); }, [](int) { return 0.0f; },
+        const uint2 ma = codes8(mk, mtop < 1e-30f, [&](int j) { return fabsf(at(mm, j)); }, [](int) { return 0.0f; },
                                 [&](int j) { return __float_as_uint(at(mm, j)) & 0x80000000u; });
         // a second moment above zero keeps a code above zero
-        const uint2 va = codes8(vk, [&](int j) { return at(root, j); },
+        const uint2 va = codes8(vk, vtop < 1e-26f, [&](int j) { return at(root, j); },
                                 [&](int j) { return at(vv, j) > 0.0f ? 1.0f : 0.0f; }, [](int) { return 0u; });
         if (vec) {
             *reinterpret_cast<uint32_t *>(mq + b0 + lane * 4) = ma.x;

@@ -12,6 +12,11 @@ RSCK filters (TF's HWIO), stride/padding/dilation as in ApproxTrain's Conv2D;
 depthwise filters are R x S x C x D (TF's depthwise layout, multiplier D);
 attention takes Q, K, V as [batch, heads, seq, dim].
 
+Between and after the approximate layers of a language model stand exact ones,
+which are not products of the simulated multiplier: BlockNorm (the norms
+around a block with its gate and the residual scale) and VocabHead (the loss
+over the vocabulary); their optimizer is optim.AdamW.
+
 Operand order of every contraction (which operand indexes the LUT's rows;
 it matters only for an asymmetric user LUT): Dense forward (x, w), input
 gradient (dy, w), weight gradient (x, dy); Conv2D likewise (x, w), (dy, w),
@@ -24,7 +29,7 @@ import math
 
 import torch
 
-from . import (ConvDesc, amsim_conv2d_bwd_data, amsim_conv2d_bwd_filter, amsim_conv2d_fwd, amsim_conv2d_out_hw,
+from . import (ConvDesc, block_norm, block_norm_backward, vocab_loss, vocab_loss_grad, amsim_conv2d_bwd_data, amsim_conv2d_bwd_filter, amsim_conv2d_fwd, amsim_conv2d_out_hw,
                amsim_conv2d_workspace_size, amsim_dwconv2d_bwd_data, amsim_dwconv2d_bwd_filter, amsim_dwconv2d_fwd,
                amsim_dwconv2d_workspace_size, amsim_gemm, amsim_gemm_strided_batched, amsim_gemm_workspace_size,
                amsim_softmax_rows, amsim_softmax_rows_backward, workspace)
@@ -276,3 +281,98 @@ class AMAttention(torch.nn.Module):
 
     def forward(self, q, k, v):
         return am_attention(q, k, v, self.lut, self.scale)
+
+
+# ------------------------------------------------------------------ exact: block norm
+class _BlockNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, y, w_post, w_pre, gate, alpha, eps, n_dtype):
+        r, n, rstd_post, rstd_pre = block_norm(x, y, w_post, w_pre, gate=gate, alpha=alpha, eps=eps, n_dtype=n_dtype)
+        ctx.save_for_backward(r, y, w_post, w_pre, gate, rstd_post, rstd_pre)
+        ctx.alpha = alpha
+        if r is x:                       # no block output yet: x passes through
+            r = x.view_as(x)
+        return r, n
+
+    @staticmethod
+    def backward(ctx, dr, dn):
+        r, y, w_post, w_pre, gate, rstd_post, rstd_pre = ctx.saved_tensors
+
+        def rows(t):
+            return None if t is None else t.contiguous()
+        dx, dy, dgate, dw_post, dw_pre = block_norm_backward(rows(dr), rows(dn), r, y, w_post, w_pre, rstd_post,
+                                                             rstd_pre, gate=gate, alpha=ctx.alpha)
+        return dx, dy, dw_post, dw_pre, dgate, None, None, None
+
+
+class BlockNorm(torch.nn.Module):
+    """The norms between two blocks: forward(x, y) takes the residual stream x
+    and a block's output y and returns (r, n), the new residual stream
+    r = x + alpha gate rms_norm(y) w_post and the next block's input
+    n = rms_norm(r) w_pre.  forward(x) alone returns (x, rms_norm(x) w_pre).
+    post: norm y (else it enters as it is); gate: None, "channel" (a learnt
+    gate of ones at the start), or a [groups, channels] tensor given to
+    forward, one row for each rows / groups rows."""
+
+    def __init__(self, channels: int, *, post: bool = True, gate: str | None = None, alpha: float = 1.0,
+                 eps: float = 1e-6, n_dtype=None, device="cuda"):
+        super().__init__()
+        if gate not in (None, "channel"):
+            raise ValueError('gate is None or "channel"; a gate per group of rows is given to forward')
+        self.alpha, self.eps, self.n_dtype = float(alpha), float(eps), n_dtype
+        self.w_pre = torch.nn.Parameter(torch.ones(channels, device=device))
+        self.w_post = torch.nn.Parameter(torch.ones(channels, device=device)) if post else None
+        self.gate = torch.nn.Parameter(torch.ones(1, channels, device=device)) if gate else None
+
+    def forward(self, x, y=None, gate=None):
+        shape = x.shape
+        rows = x.reshape(-1, shape[-1])
+        if y is None:
+            r, n = _BlockNormFn.apply(rows, None, None, self.w_pre, None, self.alpha, self.eps, self.n_dtype)
+        else:
+            r, n = _BlockNormFn.apply(rows, y.reshape(rows.shape), self.w_post, self.w_pre,
+                                      self.gate if gate is None else gate, self.alpha, self.eps, self.n_dtype)
+        return r.reshape(shape), n.reshape(shape)
+
+
+# ------------------------------------------------------------------ exact: vocabulary loss
+class _VocabLossFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, w, targets, row_weight, ignore_index, reduction):
+        kw = dict(row_weight=row_weight, ignore_index=ignore_index, reduction=reduction)
+        if not (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
+            return vocab_loss(h, w, targets, **kw)[0][0]
+        loss, _, _, dh, dw = vocab_loss_grad(h, w, targets, **kw)   # the gradients for an upstream one of 1
+        ctx.save_for_backward(dh, dw)
+        return loss[0]
+
+    @staticmethod
+    def backward(ctx, g):
+        dh, dw = ctx.saved_tensors
+        g = g.to(dh.dtype) if g.dim() == 0 else g
+        return dh * g, dw * g, None, None, None, None
+
+
+def am_vocab_loss(h, w, targets, *, row_weight=None, ignore_index=-100, reduction="mean"):
+    """Cross entropy of softmax(h w^T) against the targets without keeping the
+    logits, differentiable in h [tokens, dim] and w [vocab, dim] (both bf16).
+    The gradients come with the loss, in the same pass, and backward scales
+    them."""
+    return _VocabLossFn.apply(h, w, targets, row_weight, ignore_index, reduction)
+
+
+class VocabHead(torch.nn.Module):
+    """The last layer of a language model with its loss: forward(h, targets)
+    with h [..., dim] bf16 and targets [...] int64.  The weight is bf16;
+    optim.AdamW keeps its fp32 master."""
+
+    def __init__(self, dim: int, vocab: int, *, ignore_index: int = -100, reduction: str = "mean", device="cuda",
+                 generator: torch.Generator | None = None):
+        super().__init__()
+        self.ignore_index, self.reduction = ignore_index, reduction
+        w = torch.randn((vocab, dim), generator=generator) / math.sqrt(dim)
+        self.weight = torch.nn.Parameter(w.to(device=device, dtype=torch.bfloat16))
+
+    def forward(self, h, targets, row_weight=None):
+        return am_vocab_loss(h.reshape(-1, h.shape[-1]), self.weight, targets.reshape(-1), row_weight=row_weight,
+                             ignore_index=self.ignore_index, reduction=self.reduction)

@@ -147,6 +147,56 @@ def test_8_bit_moments(amd, g_bf16, off):
         assert np.array_equal(amd.adamw_moment_values(d[3], vs).cpu().numpy(), decode(wv, wvs, True))
 
 
+@pytest.mark.parametrize("size", [1e-14, 1e-18, 1e-22, 1e15])
+def test_8_bit_moments_of_any_size(amd, size):
+    """Gradients whose moments are near fp32's ends, a step of the state from zero: the documented bits."""
+    import torch
+    n = 3000
+    p, g, _, _ = inputs(n, 21)
+    g = g * float(size) * 1e3
+    g[::3] *= 1e-4
+    zero = np.zeros(n, f32)
+    (mq, vq, ms, vs), host = state8(torch.zeros(n), torch.zeros(n))
+    d = p.cuda()
+    amd.adamw_step(amd.adamw_table([amd.AdamwTensor.make(d, g.cuda(), mq, vq, m_scale=ms, v_scale=vs)]), lr=LR,
+                   beta1=B1, beta2=B2, eps=EPS, step=1)
+    want, m, v = adam32(p.numpy(), g.numpy(), zero, zero, 1, wd=0.0)
+    wm, wms = encode(m, False)
+    wv, wvs = encode(v, True)
+    assert np.array_equal(d.cpu().numpy(), want)
+    assert np.array_equal(mq.cpu().numpy(), wm) and np.array_equal(ms.cpu().numpy(), wms)
+    assert np.array_equal(vq.cpu().numpy(), wv) and np.array_equal(vs.cpu().numpy(), wvs)
+
+
+def test_8_bit_moments_of_a_large_tensor(amd):
+    """Enough elements for blocks of several passes, with a ragged end: every
+    tensor moves as it does in a step of its own."""
+    import torch
+    sizes = [7_000_001, 3_500_130, 255, 4096 * 8 + 17]
+    parts = [[t.cuda() for t in inputs(n, 30 + i, True)] for i, n in enumerate(sizes)]
+    state = []
+    for p, g, m, v in parts:
+        nb = -(-p.numel() // BLOCK)
+        q = [torch.zeros(p.numel(), dtype=torch.int8, device="cuda"), torch.zeros(p.numel(), dtype=torch.uint8, device="cuda"),
+             torch.zeros(nb, device="cuda"), torch.zeros(nb, device="cuda")]
+        state.append([p] + q + [torch.zeros(p.numel(), dtype=torch.bfloat16, device="cuda")])
+    other = [[t.clone() for t in st] for st in state]
+
+    def entry(st, g):
+        return amd.AdamwTensor.make(st[0], g, st[1], st[2], m_scale=st[3], v_scale=st[4], copy=st[5], weight_decay=WD)
+    for step in (1, 2):
+        amd.adamw_step(amd.adamw_table([entry(st, p[1]) for st, p in zip(state, parts)]), lr=LR, step=step)
+        for st, p in zip(other, parts):
+            chunk = 4096 * BLOCK                         # whole blocks, few enough for one pass each
+            for a in range(0, p[0].numel(), chunk):
+                b, s = min(a + chunk, p[0].numel()), a // BLOCK
+                e = -(-b // BLOCK)
+                cut = [st[0][a:b], st[1][a:b], st[2][a:b], st[3][s:e], st[4][s:e], st[5][a:b]]
+                amd.adamw_step(amd.adamw_table([entry(cut, p[1][a:b])]), lr=LR, step=step)
+    for st, ot in zip(state, other):
+        assert all(torch.equal(x, y) for x, y in zip(st, ot))
+
+
 def test_8_bit_codes_are_near_their_values(amd):
     """Nearest code in the root domain: the first moment's root is within half
     a step (1/254 of the block's root), the second's fourth root within 1/510,
