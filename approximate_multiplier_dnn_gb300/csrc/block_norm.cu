@@ -15,6 +15,7 @@ constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(kSumWarps * 32) sums_kernel(const Params p, int blocks)
 {
     __shared__ float part[kSumWarps][33];
+    amsim::chain_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (int)blockIdx.x * 32 + lane;
     const bool on = c < p.cols;
@@ -150,9 +151,9 @@ Shares shares(const amsim_block_norm_desc *d, int per_sm, int rpb, int sms, int6
 {
     const int64_t gate_rows = d->gate_rows ? d->gate_rows : d->rows;
     const int64_t groups = d->rows / gate_rows;
-    // every SM full, at least 4 passes of a block over its rows
+    // every SM full, at least 2 passes of a block over its rows
     int64_t want = std::max<int64_t>(1, (int64_t)sms * per_sm);
-    want = std::min(want, std::max<int64_t>(1, d->rows / (4 * rpb)));
+    want = std::min(want, std::max<int64_t>(1, d->rows / (2 * rpb)));
     Shares r;
     for (;;) {
         int64_t splits = std::max<int64_t>(1, want / groups);
@@ -349,8 +350,8 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
              ? amsim::bn::launch_bwd_f32(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)h.blocks, st)
              : amsim::bn::launch_bwd_bf16(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)h.blocks, st);
     if (rc || !sums || direct) return rc;
-    sums_kernel<<<dim3((unsigned)((d->cols + 31) / 32), 2), kSumWarps * 32, 0, st>>>(p, h.blocks);
-    rc = amsim::cuda_status(cudaGetLastError());
+    rc = amsim::cuda_status(amsim::chain_launch(true, sums_kernel, dim3((unsigned)((d->cols + 31) / 32), 2),
+                                                kSumWarps * 32, 0, st, p, h.blocks));
     if (rc == AMSIM_OK) amsim::count_launch();
     return rc;
 }

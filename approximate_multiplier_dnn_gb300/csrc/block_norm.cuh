@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 
 #include "bounded_wait.cuh"
+#include "chained.cuh"
 #include "pairs.cuh"
 
 namespace amsim {

@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "chained.cuh"
 #include "tensor_core.cuh"
 
 namespace {
@@ -301,11 +302,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tc::tmem_alloc<512>(slot);
-    if (PRODUCT == kLogits && blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
+    chain_start();
     tc::fence_before();
     tc::pair_sync();
     tc::fence_after();
     const uint32_t tmem = *slot;
+    chain_wait();
+    if (PRODUCT == kLogits && blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
     const int tiles = p.mt * p.nt * p.splits;
     bool aborted = false;
     if (warp == 0) {
@@ -527,6 +530,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
     __shared__ float2 part[kMergeThreads / 32][kMergeRows];
     __shared__ float red[kMergeThreads / 32];
     __shared__ bool last;
+    chain_start();
+    chain_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * kMergeRows + lane;
     float top = -INFINITY, sum = 0.0f;
@@ -587,6 +592,8 @@ constexpr int kGradThreads = 256, kGradSteps = 4;
 constexpr int kGradCols = kGradThreads * 8 * kGradSteps;      // of a block
 __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
 {
+    chain_start();
+    chain_wait();
     const int row = blockIdx.y;
     const int col0 = (int)blockIdx.x * kGradCols + (int)threadIdx.x * 8;
     uint16_t *codes = p.codes + row * p.ld;
@@ -639,6 +646,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
 __global__ void __launch_bounds__(256) join_kernel(const float *acc, int splits, long long split_rows, long long ld_acc,
                                                    int cols, const float *scale, bf16 *out, long long ld)
 {
+    chain_start();
+    chain_wait();
     const long long row = blockIdx.y;
     const int col = (int)(blockIdx.x * 256 + threadIdx.x);
     if (col >= cols) return;
@@ -656,6 +665,8 @@ constexpr int kPackThreads = 256;
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint16_t *src, long long ld, uint16_t *dst,
                                                             long long ld_dst, long long rows, int cols, int block_rows)
 {
+    chain_start();
+    chain_wait();
     const int chunks = (cols + 7) / 8;
     const long long r0 = (long long)blockIdx.x * block_rows;
     const int n = (int)min((long long)block_rows, rows - r0) * chunks;
@@ -685,9 +696,9 @@ __global__ void zero_loss_kernel(float *loss) { *loss = 0.0f; }
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-int launched()
+int launched(cudaError_t e)
 {
-    const int rc = cuda_status(cudaGetLastError());
+    const int rc = cuda_status(e);
     if (rc == AMSIM_OK) count_launch();
     return rc;
 }
@@ -813,8 +824,8 @@ long long full_rows(const amsim_vocab_loss_desc *d)
 }
 
 template <int PRODUCT>
-int launch_product(const ProductParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, int sms,
-                   cudaStream_t st)
+int launch_product(bool chained, const ProductParams &p, const CUtensorMap &a, const CUtensorMap &b,
+                   const CUtensorMap &o, int sms, cudaStream_t st)
 {
     static std::atomic<uint64_t> allowed{0};          // devices on which the kernel may have its shared memory
     int n = 0;
@@ -829,8 +840,7 @@ int launch_product(const ProductParams &p, const CUtensorMap &a, const CUtensorM
     const long long tiles = (long long)p.mt * p.nt * p.splits;
     if (tiles > 0x7FFFFFFFLL - sms) return AMSIM_EUNSUPPORTED;
     const int grid = 2 * (int)std::min<long long>(tiles, std::max(1, sms / 2));
-    product_kernel<PRODUCT><<<grid, kThreads, kSmem, st>>>(p, a, b, o);
-    return launched();
+    return launched(chain_launch(chained, product_kernel<PRODUCT>, grid, kThreads, kSmem, st, p, a, b, o));
 }
 
 ProductParams product(long long m, long long n, long long k, int splits)
@@ -863,7 +873,7 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
             return AMSIM_ECUDA;
         }
         zero_loss_kernel<<<1, 1, 0, st>>>(loss);
-        return launched();
+        return launched(cudaGetLastError());
     }
     if (!h || !targets || !ws || !aligned(h, 2) || !aligned(targets, 8) || !aligned(row_weight, 4) ||
         !aligned(row_loss, 4) || !aligned(lse, 4) || !aligned(ws, 256) || (grad && (!dh || !aligned(dh, 2))))
@@ -880,15 +890,17 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
     }
     uint8_t *base = static_cast<uint8_t *>(ws);
     Totals *totals = reinterpret_cast<Totals *>(base + l.totals);
+    bool chained = false;                     // the first kernel follows whatever the stream holds
     Matrix H{static_cast<const bf16 *>(h), ld_h}, W{static_cast<const bf16 *>(w), ld_w};
     auto pack = [&](Matrix &m, size_t off, long long n) {
         bf16 *dst = reinterpret_cast<bf16 *>(base + off);
         const int block_rows = std::max(1, 2048 / ((d->dim + 7) / 8));
-        pack_kernel<<<(unsigned)((n + block_rows - 1) / block_rows), kPackThreads, 0, st>>>(
-            reinterpret_cast<const uint16_t *>(m.p), m.ld, reinterpret_cast<uint16_t *>(dst), l.ld_pack, n, d->dim,
-            block_rows);
+        const int r = launched(chain_launch(chained, pack_kernel, (unsigned)((n + block_rows - 1) / block_rows),
+                                            kPackThreads, 0, st, reinterpret_cast<const uint16_t *>(m.p), m.ld,
+                                            reinterpret_cast<uint16_t *>(dst), l.ld_pack, n, d->dim, block_rows));
         m = Matrix{dst, l.ld_pack};
-        return launched();
+        chained = true;
+        return r;
     };
     if (copy_h && (rc = pack(H, l.pack_h, d->tokens))) return rc;
     if (copy_w && (rc = pack(W, l.pack_w, d->vocab))) return rc;
@@ -912,7 +924,7 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         if ((rc = matrix_map(&am, H.p + t0 * H.ld, d->dim, n, H.ld, kHalfM)) ||
             (rc = matrix_map(&bm, W.p, d->dim, d->vocab, W.ld, kHalfN)) ||
             (grad && (rc = matrix_map(&om, codes, d->vocab, n, l.ld_codes, 32))) ||
-            (rc = launch_product<kLogits>(p, am, bm, grad ? om : am, sms, st)))
+            (rc = launch_product<kLogits>(chained, p, am, bm, grad ? om : am, sms, st)))
             return rc;
         MergeParams q{};
         q.stats = stats;
@@ -934,12 +946,15 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         q.mean = d->reduction == AMSIM_REDUCE_MEAN;
         q.first_chunk = first;
         q.last_chunk = last;
-        merge_kernel<<<(unsigned)((n + kMergeRows - 1) / kMergeRows), kMergeThreads, 0, st>>>(q);
-        if ((rc = launched())) return rc;
+        chained = true;
+        rc = launched(chain_launch(true, merge_kernel, (unsigned)((n + kMergeRows - 1) / kMergeRows), kMergeThreads, 0,
+                                   st, q));
+        if (rc) return rc;
         if (!grad) continue;
         GradParams e{codes, stats, q.lse, weight, targets + t0, l.ld_codes, (int)n, d->vocab};
-        grad_kernel<<<dim3((unsigned)((d->vocab + kGradCols - 1) / kGradCols), (unsigned)n), kGradThreads, 0, st>>>(e);
-        if ((rc = launched())) return rc;
+        rc = launched(chain_launch(true, grad_kernel, dim3((unsigned)((d->vocab + kGradCols - 1) / kGradCols), (unsigned)n),
+                                   kGradThreads, 0, st, e));
+        if (rc) return rc;
         // dh = G W
         p = product(n, d->dim, d->vocab, l.dh_splits);
         bf16 *dh_out = static_cast<bf16 *>(dh) + t0 * ld_dh;
@@ -959,12 +974,13 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         }
         if (rc || (rc = matrix_map(&am, g, d->vocab, n, l.ld_codes, kHalfM)) ||
             (rc = matrix_map(&bm, W.p, d->dim, d->vocab, W.ld, kTileK)) ||
-            (rc = launch_product<kDh>(p, am, bm, om, sms, st)))
+            (rc = launch_product<kDh>(true, p, am, bm, om, sms, st)))
             return rc;
         if (p.splits > 1) {
-            join_kernel<<<dim3((unsigned)((d->dim + 255) / 256), (unsigned)n), 256, 0, st>>>(
-                p.acc, p.splits, l.split_rows, l.ld_acc, d->dim, &totals->scale, dh_out, ld_dh);
-            if ((rc = launched())) return rc;
+            rc = launched(chain_launch(true, join_kernel, dim3((unsigned)((d->dim + 255) / 256), (unsigned)n), 256, 0, st,
+                                       (const float *)p.acc, p.splits, l.split_rows, l.ld_acc, d->dim,
+                                       (const float *)&totals->scale, dh_out, ld_dh));
+            if (rc) return rc;
         }
         // dW = G^T h, over the chunks so far
         p = product(d->vocab, d->dim, n, 1);
@@ -986,7 +1002,7 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         }
         if (rc || (rc = matrix_map(&am, g, d->vocab, n, l.ld_codes, kTileK)) ||
             (rc = matrix_map(&bm, H.p + t0 * H.ld, d->dim, n, H.ld, kTileK)) ||
-            (rc = launch_product<kDw>(p, am, bm, om, sms, st)))
+            (rc = launch_product<kDw>(true, p, am, bm, om, sms, st)))
             return rc;
     }
     return AMSIM_OK;
