@@ -67,7 +67,7 @@ struct ProductParams {
     // kDh, kDw
     bf16 *out;
     long long ld_out;
-    int boxes;                      // out goes through the tensor map
+    int boxes, pairs;               // out goes through the tensor map; its rows are 4-byte aligned
     const float *scale;             // 1 / A
     float *acc;                     // fp32 sums of earlier chunks (kDw) or the splits' sums (kDh)
     long long ld_acc, split_rows;   // its row stride and rows per split
@@ -136,17 +136,29 @@ struct Out {
         reinterpret_cast<uint4 *>(buffer + lane * 128)[j ^ (lane & 7)] = make_uint4(a, b, c, d);
     }
     // the same, by the warp's own coalesced stores, for rows that box copies
-    // cannot write: `rows` x `cols` elements of 16 bits to `dst`
-    __device__ __forceinline__ void end_rows(bf16 *dst, long long ld, int rows, int cols) const
+    // cannot write: `rows` x `cols` elements of 16 bits to `dst`, two at a time
+    // where they are 4-byte aligned (496 tokens x 68330 x 3356, forward and
+    // gradients: 807 us with single elements, 768 with pairs)
+    __device__ __forceinline__ void end_rows(bf16 *dst, long long ld, int rows, int cols, bool pairs) const
     {
         __syncwarp();
+        if (pairs) {
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                    buffer + r * 128 + ((lane >> 2) ^ (r & 7)) * 16 + (lane & 3) * 4);
+                if (r < rows && 2 * lane + 1 < cols) *reinterpret_cast<uint32_t *>(dst + r * ld + 2 * lane) = w;
+                else if (r < rows && 2 * lane < cols) reinterpret_cast<uint16_t *>(dst)[r * ld + 2 * lane] = (uint16_t)w;
+            }
+        } else {
 #pragma unroll 4
-        for (int r = 0; r < 32; ++r) {
-            const uint16_t *row = reinterpret_cast<const uint16_t *>(buffer + r * 128);
+            for (int r = 0; r < 32; ++r) {
+                const uint16_t *row = reinterpret_cast<const uint16_t *>(buffer + r * 128);
 #pragma unroll
-            for (int e = lane; e < 64; e += 32)
-                if (r < rows && e < cols)
-                    reinterpret_cast<uint16_t *>(dst)[r * ld + e] = row[((e >> 3) ^ (r & 7)) * 8 + (e & 7)];
+                for (int e = lane; e < 64; e += 32)
+                    if (r < rows && e < cols)
+                        reinterpret_cast<uint16_t *>(dst)[r * ld + e] = row[((e >> 3) ^ (r & 7)) * 8 + (e & 7)];
+            }
         }
         __syncwarp();
     }
@@ -267,7 +279,7 @@ __device__ __forceinline__ void store_piece(const ProductParams &p, uint32_t tme
         }
         const int row0 = row - out.lane, col = col0 + c * kBox;
         if (p.boxes) out.end(col, row0, warp_on && col < p.n);
-        else out.end_rows(p.out + row0 * p.ld_out + col, p.ld_out, warp_on ? p.m - row0 : 0, p.n - col);
+        else out.end_rows(p.out + row0 * p.ld_out + col, p.ld_out, warp_on ? p.m - row0 : 0, p.n - col, p.pairs);
     }
 }
 
@@ -969,6 +981,7 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
             p.out = dh_out;
             p.ld_out = ld_dh;
             p.boxes = tma_rows(dh_out, ld_dh);
+            p.pairs = aligned(dh_out, 4) && ld_dh % 2 == 0;
             om = am;
             if (p.boxes) rc = matrix_map(&om, dh_out, d->dim, n, ld_dh, 32);
         }
@@ -996,6 +1009,7 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
             p.out = static_cast<bf16 *>(dw);
             p.ld_out = ld_dw;
             p.boxes = tma_rows(dw, ld_dw);
+            p.pairs = aligned(dw, 4) && ld_dw % 2 == 0;
             if (p.boxes) rc = matrix_map(&om, dw, d->dim, d->vocab, ld_dw, 32);
         } else {
             rc = matrix_map(&om, dw_acc, d->dim, d->vocab, l.ld_acc, 32, true);
