@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) sums_kernel(const Params p, in
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-// Rows that take a thread's four channels as one load, and whole-row bulk copies.
+// Rows that take a thread's four channels as one load, and rows that start and end on 16 bytes.
 bool vector_rows(const void *p, int64_t ld, size_t size)
 {
     return !p || (aligned(p, 4 * size) && ld % 4 == 0);
@@ -206,20 +206,18 @@ extern "C" int amsim_block_norm_fwd(const amsim_block_norm_desc *d, const void *
     for (const void *q : {(const void *)gate, (const void *)w_post, (const void *)w_pre}) vec = vec && aligned(q, 16);
     vec = vec && vector_rows(x, p.ldx, xs) && vector_rows(y, p.ldy, ys) && vector_rows(r, p.ldr, xs) &&
           vector_rows(n, p.ldn, ns);
-    const bool bulk = vec && bulk_rows(x, p.ldx, xs, d->cols) && bulk_rows(y, p.ldy, ys, d->cols);
-    using amsim::bn::kRing;
-    using amsim::bn::kScalar;
-    using amsim::bn::kVector;
+    const bool whole = vec && bulk_rows(x, p.ldx, xs, d->cols) && bulk_rows(y, p.ldy, ys, d->cols);
+    const int slack = whole ? 0 : amsim::bn::kRingSlack;
     const int sms = device_sms();
     if (!sms) return AMSIM_ECUDA;
     const Shape s = shape(d->cols, vec);
     const RingShape ring = ring_shape(
-        d->cols, amsim::bn::ring_bytes(d->cols, (int)xs) + (y ? amsim::bn::ring_bytes(d->cols, (int)ys) : 0), false);
+        d->cols, amsim::bn::ring_bytes(d->cols, (int)xs, slack) + (y ? amsim::bn::ring_bytes(d->cols, (int)ys, slack) : 0), false);
     const bool full = y && w_post && r && n && rstd_post && rstd_pre;
     int64_t grid;
-    amsim::bn::Loads loads = vec ? kVector : kScalar;
-    if (bulk && ring_pays(d->rows, ring, sms) && (full || ring.tpr <= 256)) {
-        loads = kRing;
+    amsim::bn::Loads loads = vec ? amsim::bn::kVector : amsim::bn::kScalar;
+    if (ring_pays(d->rows, ring, sms) && (full || (whole && ring.tpr <= 256))) {
+        loads = whole ? amsim::bn::kRing : vec ? amsim::bn::kPieceRing : amsim::bn::kScalarRing;
         p.tpr = ring.tpr;
         p.rpb = 1;
         p.slots = ring.slots;
@@ -307,22 +305,23 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
     for (const void *q : {(const void *)gate, (const void *)w_post, (const void *)w_pre}) vec = vec && aligned(q, 16);
     vec = vec && vector_rows(r, p.ldr, xs) && vector_rows(dr, p.lddr, xs) && vector_rows(dx, p.lddx, xs) &&
           vector_rows(y, p.ldy, ys) && vector_rows(dy, p.lddy, ys) && vector_rows(dn, p.lddn, ns);
-    const bool bulk = vec && bulk_rows(r, p.ldr, xs, d->cols) && bulk_rows(dr, p.lddr, xs, d->cols) &&
-                      bulk_rows(y, p.ldy, ys, d->cols) && bulk_rows(dn, p.lddn, ns, d->cols);
+    const bool whole = vec && bulk_rows(r, p.ldr, xs, d->cols) && bulk_rows(dr, p.lddr, xs, d->cols) &&
+                       bulk_rows(y, p.ldy, ys, d->cols) && bulk_rows(dn, p.lddn, ns, d->cols);
+    const int slack = whole ? 0 : amsim::bn::kRingSlack;
     const int sms = device_sms();
     if (!sms) return AMSIM_ECUDA;
     const Shape s = shape(d->cols, vec);
-    const int rx = amsim::bn::ring_bytes(d->cols, (int)xs);
+    const int rx = amsim::bn::ring_bytes(d->cols, (int)xs, slack);
     const RingShape ring =
-        ring_shape(d->cols, (dr ? rx : 0) + (dn ? rx + amsim::bn::ring_bytes(d->cols, (int)ns) : 0) +
-                                (y ? amsim::bn::ring_bytes(d->cols, (int)ys) : 0), true);
+        ring_shape(d->cols, (dr ? rx : 0) + (dn ? rx + amsim::bn::ring_bytes(d->cols, (int)ns, slack) : 0) +
+                                (y ? amsim::bn::ring_bytes(d->cols, (int)ys, slack) : 0), true);
     const bool full = dr && dn && y && w_post && dx && dy;
     int per_sm = direct_blocks(s);
     amsim::bn::Loads loads = vec ? amsim::bn::kVector : amsim::bn::kScalar;
     p.tpr = s.tpr;
     p.rpb = s.rpb;
-    if (bulk && ring_pays(d->rows, ring, sms) && (full || ring.tpr <= 256)) {
-        loads = amsim::bn::kRing;
+    if (ring_pays(d->rows, ring, sms) && (full || (whole && ring.tpr <= 256))) {
+        loads = whole ? amsim::bn::kRing : vec ? amsim::bn::kPieceRing : amsim::bn::kScalarRing;
         p.tpr = ring.tpr;
         p.rpb = ring.at_work;
         p.slots = ring.slots;

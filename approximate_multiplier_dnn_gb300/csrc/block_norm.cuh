@@ -481,12 +481,18 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
 
 // ------------------------------------------------------------------ rows by bulk copies
 // The kernels above keep one row's bytes in flight per block, and none while
-// they reduce it: 40 % of the copy bandwidth at 16384 x 4096.  Where rows are
-// vectors of 16 bytes and there are many, a block streams its rows through a
-// ring in shared memory instead: one thread issues whole-row bulk copies, and
-// refills a slot once every thread is past it.  Channels are dealt to threads,
-// and sums taken, as above, so a row's results do not depend on how many rows
-// come with it.
+// they reduce it: 40 % of the copy bandwidth at 16384 x 4096.  Where there are
+// many rows, a block streams them through a ring in shared memory instead: one
+// thread issues whole-row bulk copies, and refills a slot once every thread is
+// past it.  Channels are dealt to threads, and sums taken, as above, so a row's
+// results do not depend on how many rows come with it.
+//
+// Rows that do not start and end on 16 bytes (WHOLE false) come as the aligned
+// pieces of 16 that hold them, and start inside their slot.  (Such a piece lies
+// in one page, so its bytes beside the row can be read; they are not used.)
+// Backward, 5395 x 3047 bf16: 341 us by direct loads, 75 so; 16384 x 1013
+// fp32/bf16: 166, 69.  Whole rows have kernels of their own, as the four rows'
+// ends cost 3 to 7 % of 16384 x 4096 and 8192 x 8192 bf16.
 struct Ring {
     uint8_t *slot0;
     uint64_t *full;
@@ -511,11 +517,16 @@ struct Ring {
 
 constexpr int kRingNV = 4;                 // steps per thread of the ring kernels
 constexpr int kRingBarBytes = 1024;        // up to 16 teams of 8 slots
-constexpr int kRingAlign = 128;
+constexpr int kRingAlign = 128, kRingSlack = 30;   // of a slot; of a row's ends that are off 16 bytes
 // Threads per SM that the kernels' registers allow (up to 128 each): forward as
 // blocks of up to 256 or 512, backward as the teams of one block.
 constexpr int kRingThreads = 512, kTeamThreads = 512;
-__host__ __device__ inline int ring_bytes(int cols, int size) { return (cols * size + kRingAlign - 1) / kRingAlign * kRingAlign; }
+__host__ __device__ inline int ring_bytes(int cols, int size, int slack)
+{
+    return (cols * size + slack + kRingAlign - 1) / kRingAlign * kRingAlign;
+}
+// Weights that wait in shared memory: a row of fp32.
+__host__ __device__ inline int kept_floats(int cols) { return (cols + 3) / 4 * 4; }
 
 __device__ __forceinline__ Ring make_ring(const Params &p, uint8_t *smem, int team, int t)
 {
@@ -532,22 +543,40 @@ __device__ __forceinline__ Ring make_ring(const Params &p, uint8_t *smem, int te
     return r;
 }
 
-// The thread's words of step k of a row in shared memory.
+// The bytes of the aligned piece that holds row `row`, of `bytes`, of a tensor.
 template <typename T>
-__device__ __forceinline__ void take(Raw<T> &d, const uint8_t *row, int k, int t, int tpr, int cols)
+__device__ __forceinline__ int row_bytes(const void *base, long long ld, long long row, int bytes)
 {
-    load_raw<true, T>(d, reinterpret_cast<const T *>(row), k, t, tpr, cols);
+    return (int)(reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + row * ld) & 15) + bytes + 15 & ~15;
+}
+
+// Copies the row, or the piece that holds it, to a slot.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void copy_row(uint8_t *slot, const void *base, long long ld, long long row, int bytes, uint64_t *bar)
+{
+    const T *from = static_cast<const T *>(base) + row * ld;
+    if constexpr (WHOLE) tc::copy_bytes(slot, from, bytes, bar);
+    else tc::copy_bytes(slot, reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)15), bytes, bar);
+}
+
+// Where the row starts in a slot that was filled so.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ const T *in_slot(const uint8_t *slot, const void *base, long long ld, long long row)
+{
+    if constexpr (WHOLE) return reinterpret_cast<const T *>(slot);
+    else return reinterpret_cast<const T *>(slot + (reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + row * ld) & 15));
 }
 
 // Four weights that wait in shared memory.
+template <bool VEC>
 __device__ __forceinline__ Four kept(const float *w, int k, int t, int tpr, int cols)
 {
     Raw<float> d;
-    load_raw<true, float>(d, w, k, t, tpr, cols);
+    load_raw<VEC, float>(d, w, k, t, tpr, cols);
     return widen(d);
 }
 
-template <int THREADS, bool FULL, typename X, typename Y, typename N>
+template <int THREADS, bool VEC, bool WHOLE, bool FULL, typename X, typename Y, typename N>
 __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kernel(const Params p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -556,21 +585,27 @@ __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kern
     const Parts<FULL> has{p};
     int which = 0;
     const int t = threadIdx.x, warps = p.tpr >> 5, cols = p.cols;
-    const int xb = cols * (int)sizeof(X), yb = cols * (int)sizeof(Y), yoff = ring_bytes(cols, sizeof(X));
+    const int bytes_x = cols * (int)sizeof(X), bytes_y = cols * (int)sizeof(Y);
+    const int yoff = ring_bytes(cols, sizeof(X), WHOLE ? 0 : kRingSlack);
     const long long r0 = blockIdx.x * p.block_rows, r1 = min(r0 + p.block_rows, p.rows);
     Ring ring = make_ring(p, smem, 0, t);
     auto issue = [&](long long row, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
+        int xb = bytes_x, yb = bytes_y;
+        if constexpr (!WHOLE) {
+            xb = row_bytes<X>(p.x, p.ldx, row, xb);
+            yb = row_bytes<Y>(p.y, p.ldy, row, yb);
+        }
         tc::bar_expect(ring.full + slot, xb + (has.y() ? yb : 0));
-        tc::copy_bytes(s, static_cast<const X *>(p.x) + row * p.ldx, xb, ring.full + slot);
-        if (has.y()) tc::copy_bytes(s + yoff, static_cast<const Y *>(p.y) + row * p.ldy, yb, ring.full + slot);
+        copy_row<WHOLE, X>(s, p.x, p.ldx, row, xb, ring.full + slot);
+        if (has.y()) copy_row<WHOLE, Y>(s + yoff, p.y, p.ldy, row, yb, ring.full + slot);
     };
     if (t == 0)
         for (int i = 0; i < p.slots && r0 + i < r1; ++i) issue(r0 + i, i);
     Four wq[NV], wu[NV];                   // w_pre, and alpha gate w_post of the rows' gate
     if (has.n())
 #pragma unroll
-        for (int k = 0; k < NV; ++k) wq[k] = weights<true>(p.w_pre, k, t, p.tpr, cols);
+        for (int k = 0; k < NV; ++k) wq[k] = weights<VEC>(p.w_pre, k, t, p.tpr, cols);
     X *ro = static_cast<X *>(p.r) + r0 * p.ldr;
     N *no = static_cast<N *>(p.n) + r0 * p.ldn;
     long long gate_end = r0;               // first row with another gate
@@ -580,17 +615,18 @@ __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kern
             const float *gate = p.gate ? p.gate + g * cols : nullptr;
             gate_end = (g + 1) * p.gate_rows;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) wu[k] = weights_u<true>(p, gate, k, t, cols);
+            for (int k = 0; k < NV; ++k) wu[k] = weights_u<VEC>(p, gate, k, t, cols);
         }
         const uint8_t *slot = ring.wait();
         Raw<X> xr[NV];
         Raw<Y> yr[NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) take<X>(xr[k], slot, k, t, p.tpr, cols);
+        for (int k = 0; k < NV; ++k) load_raw<VEC, X>(xr[k], in_slot<WHOLE, X>(slot, p.x, p.ldx, row), k, t, p.tpr, cols);
         if (has.y())
 #pragma unroll
-            for (int k = 0; k < NV; ++k) take<Y>(yr[k], slot + yoff, k, t, p.tpr, cols);
-        fwd_row<NV, true, FULL, X, Y, N>(
+            for (int k = 0; k < NV; ++k)
+                load_raw<VEC, Y>(yr[k], in_slot<WHOLE, Y>(slot + yoff, p.y, p.ldy, row), k, t, p.tpr, cols);
+        fwd_row<NV, VEC, FULL, X, Y, N>(
             p, xr, yr, ro, no, row, true, t, cols, warps, red, which,
             [&](int k) { return wu[k]; }, [&](int k) { return wq[k]; },
             [&](bool barrier) {
@@ -605,7 +641,7 @@ __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kern
 // with a ring of its own.  They share the weights, which wait in shared memory
 // (w_pre, then alpha gate w_post of the share's gate): a block per row would
 // hold a copy each, and leave room for one row ahead where teams have two.
-template <bool FULL, typename X, typename Y, typename N>
+template <bool VEC, bool WHOLE, bool FULL, typename X, typename Y, typename N>
 __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -616,12 +652,13 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
     const int teams = p.rpb, team = threadIdx.x / p.tpr, t = threadIdx.x - team * p.tpr;
     const int warps = p.tpr >> 5, cols = p.cols;
     const bool sums_a = has.y() && (p.dgate || p.dw_post), sums_b = has.dn() && p.dw_pre;
-    const int xb = cols * (int)sizeof(X), yb = cols * (int)sizeof(Y), nb = cols * (int)sizeof(N);
-    const int rxb = ring_bytes(cols, sizeof(X)), rnb = ring_bytes(cols, sizeof(N));
+    const int bytes_x = cols * (int)sizeof(X), bytes_y = cols * (int)sizeof(Y), bytes_n = cols * (int)sizeof(N);
+    const int rxb = ring_bytes(cols, sizeof(X), WHOLE ? 0 : kRingSlack), rnb = ring_bytes(cols, sizeof(N), WHOLE ? 0 : kRingSlack);
     const int off_r = has.dr() ? rxb : 0, off_n = off_r + (has.dn() ? rxb : 0), off_y = off_n + (has.dn() ? rnb : 0);
     float *wq = reinterpret_cast<float *>(smem + kRingBarBytes + teams * p.slots * p.slot_bytes);
-    float *wu = wq + cols;
-    float4 *buf = reinterpret_cast<float4 *>(wu + cols);     // one per thread, with several teams
+    const int row_floats = VEC ? cols : kept_floats(cols);
+    float *wu = wq + row_floats;
+    float4 *buf = reinterpret_cast<float4 *>(wu + row_floats);     // one per thread, with several teams
     Ring ring = make_ring(p, smem, team, t);
     auto sync = [&] {
         if (warps == 1) __syncwarp();
@@ -641,13 +678,20 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
     };
     auto issue = [&](const Place &q, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
-        tc::bar_expect(ring.full + slot, (has.dr() ? xb : 0) + (has.dn() ? xb + nb : 0) + (has.y() ? yb : 0));
-        if (has.dr()) tc::copy_bytes(s, static_cast<const X *>(p.dr) + q.row * p.lddr, xb, ring.full + slot);
-        if (has.dn()) {
-            tc::copy_bytes(s + off_r, static_cast<const X *>(p.rin) + q.row * p.ldr, xb, ring.full + slot);
-            tc::copy_bytes(s + off_n, static_cast<const N *>(p.dn) + q.row * p.lddn, nb, ring.full + slot);
+        int drb = bytes_x, rb = bytes_x, dnb = bytes_n, yb = bytes_y;
+        if constexpr (!WHOLE) {
+            drb = row_bytes<X>(p.dr, p.lddr, q.row, drb);
+            rb = row_bytes<X>(p.rin, p.ldr, q.row, rb);
+            dnb = row_bytes<N>(p.dn, p.lddn, q.row, dnb);
+            yb = row_bytes<Y>(p.y, p.ldy, q.row, yb);
         }
-        if (has.y()) tc::copy_bytes(s + off_y, static_cast<const Y *>(p.y) + q.row * p.ldy, yb, ring.full + slot);
+        tc::bar_expect(ring.full + slot, (has.dr() ? drb : 0) + (has.dn() ? rb + dnb : 0) + (has.y() ? yb : 0));
+        if (has.dr()) copy_row<WHOLE, X>(s, p.dr, p.lddr, q.row, drb, ring.full + slot);
+        if (has.dn()) {
+            copy_row<WHOLE, X>(s + off_r, p.rin, p.ldr, q.row, rb, ring.full + slot);
+            copy_row<WHOLE, N>(s + off_n, p.dn, p.lddn, q.row, dnb, ring.full + slot);
+        }
+        if (has.y()) copy_row<WHOLE, Y>(s + off_y, p.y, p.ldy, q.row, yb, ring.full + slot);
     };
     auto advance = [&](Place &q) {
         if ((q.row += teams) < q.end) return;
@@ -706,19 +750,20 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
             next_pre = pre_of(row + teams);
             next_post = post_of(row + teams);
             const uint8_t *slot = ring.wait();
-            bwd_row<NV, true, FULL, false, X, Y, N>(
+            bwd_row<NV, VEC, FULL, false, X, Y, N>(
                 p, pre, post, dxo, dyo, t, cols, warps, red, which, a, b,
                 [&](int k, bool first) {
                     Step<X, Y, N> in;
-                    if (has.dr() && first) take<X>(in.dr, slot, k, t, p.tpr, cols);
+                    if (has.dr() && first) load_raw<VEC, X>(in.dr, in_slot<WHOLE, X>(slot, p.dr, p.lddr, row), k, t, p.tpr, cols);
                     if (has.dn()) {
-                        take<X>(in.r, slot + off_r, k, t, p.tpr, cols);
-                        if (first) take<N>(in.dn, slot + off_n, k, t, p.tpr, cols);
+                        load_raw<VEC, X>(in.r, in_slot<WHOLE, X>(slot + off_r, p.rin, p.ldr, row), k, t, p.tpr, cols);
+                        if (first) load_raw<VEC, N>(in.dn, in_slot<WHOLE, N>(slot + off_n, p.dn, p.lddn, row), k, t, p.tpr, cols);
                     }
-                    if (has.y()) take<Y>(in.y, slot + off_y, k, t, p.tpr, cols);
+                    if (has.y()) load_raw<VEC, Y>(in.y, in_slot<WHOLE, Y>(slot + off_y, p.y, p.ldy, row), k, t, p.tpr, cols);
                     return in;
                 },
-                [&](int k) { return kept(wq, k, t, p.tpr, cols); }, [&](int k) { return kept(wu, k, t, p.tpr, cols); },
+                [&](int k) { return kept<VEC>(wq, k, t, p.tpr, cols); },
+                [&](int k) { return kept<VEC>(wu, k, t, p.tpr, cols); },
                 sync,
                 [&](bool barrier) {
                     // every thread of the team is past the last row: its slot is free
@@ -734,12 +779,11 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const float4 v = joined(a[k * kP], a[k * kP + 1]);
-                const int c = channel<true>(k, 0, t, p.tpr);
                 if (team > 0) continue;
-                leave_a(p, v.x, c, item, gi, gate, fresh);
-                leave_a(p, v.y, c + 1, item, gi, gate, fresh);
-                leave_a(p, v.z, c + 2, item, gi, gate, fresh);
-                leave_a(p, v.w, c + 3, item, gi, gate, fresh);
+                leave_a(p, v.x, channel<VEC>(k, 0, t, p.tpr), item, gi, gate, fresh);
+                leave_a(p, v.y, channel<VEC>(k, 1, t, p.tpr), item, gi, gate, fresh);
+                leave_a(p, v.z, channel<VEC>(k, 2, t, p.tpr), item, gi, gate, fresh);
+                leave_a(p, v.w, channel<VEC>(k, 3, t, p.tpr), item, gi, gate, fresh);
             }
         }
         fresh = false;
@@ -748,16 +792,22 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const float4 v = joined(b[k * kP], b[k * kP + 1]);
-        const int c = channel<true>(k, 0, t, p.tpr);
-        if (team > 0 || c >= cols) continue;
-        float *out = p.part_pre + (long long)blockIdx.x * cols + c;
-        out[0] = v.x; out[1] = v.y; out[2] = v.z; out[3] = v.w;
+        if (team > 0) continue;
+        auto leave = [&](int e, float x) {
+            const int c = channel<VEC>(k, e, t, p.tpr);
+            if (c < cols) p.part_pre[(long long)blockIdx.x * cols + c] = x;
+        };
+        leave(0, v.x);
+        leave(1, v.y);
+        leave(2, v.z);
+        leave(3, v.w);
     }
 }
 
 // ------------------------------------------------------------------ launches
-// How a call runs: single loads for unaligned rows, vector loads, or the ring.
-enum Loads { kScalar = 0, kVector = 1, kRing = 2 };
+// How a call runs: single loads for unaligned rows or vector loads, directly or
+// through the ring, where rows off 16 bytes come in pieces.
+enum Loads { kScalar, kVector, kRing, kPieceRing, kScalarRing };
 
 // One translation unit per direction and type of the residual stream builds
 // its instances.
@@ -788,18 +838,23 @@ int launch_types(int nv, Loads loads, bool full, const Params &p, unsigned grid,
         if constexpr (BWD) return launch_kernel(bwd_kernel<__VA_ARGS__, X, Y, N>, p, grid, 0, st); \
         else return launch_kernel(fwd_kernel<__VA_ARGS__, X, Y, N>, p, grid, 0, st);              \
     } while (0)
-    if (loads == kRing) {
-        if constexpr (BWD) {
-            const size_t smem = kRingBarBytes + (size_t)p.rpb * p.slots * p.slot_bytes + 8 * (size_t)p.cols +
-                                (p.rpb > 1 ? kTeamThreads * sizeof(float4) : 0);
-            if (full) return launch_kernel(bwd_ring_kernel<true, X, Y, N>, p, grid, smem, st);
-            return launch_kernel(bwd_ring_kernel<false, X, Y, N>, p, grid, smem, st);
-        } else {
-            const size_t smem = kRingBarBytes + (size_t)p.slots * p.slot_bytes;
-            if (threads > 256) return launch_kernel(fwd_ring_kernel<512, true, X, Y, N>, p, grid, smem, st);
-            if (full) return launch_kernel(fwd_ring_kernel<256, true, X, Y, N>, p, grid, smem, st);
-            return launch_kernel(fwd_ring_kernel<256, false, X, Y, N>, p, grid, smem, st);
-        }
+    const size_t rows_smem = kRingBarBytes + (size_t)(BWD ? p.rpb : 1) * p.slots * p.slot_bytes;
+    if constexpr (BWD) {
+        const size_t smem = rows_smem + 8 * (size_t)kept_floats(p.cols) + (p.rpb > 1 ? kTeamThreads * sizeof(float4) : 0);
+        if (loads == kScalarRing) return launch_kernel(bwd_ring_kernel<false, false, true, X, Y, N>, p, grid, smem, st);
+        if (loads == kPieceRing) return launch_kernel(bwd_ring_kernel<true, false, true, X, Y, N>, p, grid, smem, st);
+        if (loads == kRing && full) return launch_kernel(bwd_ring_kernel<true, true, true, X, Y, N>, p, grid, smem, st);
+        if (loads == kRing) return launch_kernel(bwd_ring_kernel<true, true, false, X, Y, N>, p, grid, smem, st);
+    } else {
+        const size_t smem = rows_smem;
+#define AMSIM_RING(...)                                                                                        \
+    return threads > 256 ? launch_kernel(fwd_ring_kernel<512, __VA_ARGS__, true, X, Y, N>, p, grid, smem, st)  \
+                         : launch_kernel(fwd_ring_kernel<256, __VA_ARGS__, true, X, Y, N>, p, grid, smem, st)
+        if (loads == kScalarRing) AMSIM_RING(false, false);
+        if (loads == kPieceRing) AMSIM_RING(true, false);
+        if (loads == kRing && full) AMSIM_RING(true, true);
+        if (loads == kRing) return launch_kernel(fwd_ring_kernel<256, true, true, false, X, Y, N>, p, grid, smem, st);
+#undef AMSIM_RING
     }
     if (loads == kVector) {
         if (nv == 1) AMSIM_BN(1, 128, true);

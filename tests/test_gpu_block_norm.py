@@ -184,6 +184,82 @@ def test_many_rows(amd, rows, cols, x, y, n, groups):
     assert amd.amsim_device_errors() == (amd.AMSIM_OK, 0)
 
 
+# more of them for narrow rows, which stream several at once, and rows that are
+# no whole 16 bytes, which stream as the aligned pieces that hold them
+STREAMED = [(4900, 512), (2500, 1000), (950, 2056), (4870, 389), (2440, 1013), (2440, 1012), (1300, 2047),
+            (640, 3047), (310, 4099), (308, 8191)]
+
+
+@pytest.mark.parametrize("rows,cols", STREAMED)
+@pytest.mark.parametrize("x,y,n", [("f32", "f32", "f32"), ("bf16", "bf16", "bf16"), ("f32", "bf16", "bf16"),
+                                   ("bf16", "f32", "f32")])
+@pytest.mark.parametrize("groups", [1, 10])
+def test_streamed_rows(amd, rows, cols, x, y, n, groups):
+    """As many rows as stream; and each row's results are those of a call of a few."""
+    import torch
+    rows -= rows % groups
+    a = make(rows, cols, x, y, n, groups, seed=rows + 7 * cols)
+    if groups == 1:
+        a["gate"] = None
+    fwd = amd.block_norm(a["x"], a["y"], a["w_post"], a["w_pre"], gate=a["gate"], alpha=0.5, eps=1e-5,
+                         n_dtype=a["n_type"])
+    r, nn, post, pre = fwd
+    R, N, P, Q, sr, sn = ref_fwd(a, 0.5, 1e-5)
+    check(r, R, K * sr + HALF[x] * (1 + K) * np.abs(R), "r")
+    check(nn, N, 2 * K * sn + K * np.abs(N) + HALF[n] * (1 + K) * np.abs(N) + K * np.abs(N).max(), "n")
+    check(post, P, K * P, "rstd_post")
+    check(pre, Q, 2 * K * Q, "rstd_pre")
+    got = amd.block_norm_backward(a["dr"], a["dn"], r, a["y"], a["w_post"], a["w_pre"], post, pre, gate=a["gate"],
+                                  alpha=0.5)
+    check_bwd(amd, a, r, post, pre, 0.5, got, x, y, rows)
+    last = slice(rows - 3, rows)
+    gate = None if a["gate"] is None else a["gate"][-1:]
+    few = amd.block_norm(a["x"][last], a["y"][last], a["w_post"], a["w_pre"], gate=gate, alpha=0.5, eps=1e-5,
+                         n_dtype=a["n_type"])
+    assert all(torch.equal(p[last], q) for p, q in zip(fwd, few))
+    few = amd.block_norm_backward(a["dr"][last], a["dn"][last], r[last], a["y"][last], a["w_post"], a["w_pre"],
+                                  post[last], pre[last], gate=gate, alpha=0.5)
+    assert torch.equal(got[0][last], few[0]) and torch.equal(got[1][last], few[1])
+    assert amd.amsim_device_errors() == (amd.AMSIM_OK, 0)
+
+
+@pytest.mark.parametrize("cols,pad,off", [(1024, 1, 0), (1024, 0, 3), (1023, 2, 5), (1016, 16, 8)])
+def test_streamed_strides_and_alignment(amd, cols, pad, off):
+    """Rows with a stride and bases off 16 bytes, in place: the dense result, to the bit
+    where both deal the channels to threads alike, and nothing outside the rows is
+    written."""
+    import torch
+    rows, ld = 2500, cols + pad
+    a = make(rows, cols, "bf16", "f32", "bf16", 2, seed=6)
+
+    def spread(t):
+        buf = torch.full((rows * ld + off + 8,), 5.0, dtype=t.dtype, device="cuda")
+        v = buf[off:off + rows * ld].view(rows, ld)[:, :cols]
+        v.copy_(t)
+        return buf, v
+
+    def untouched(buf, v):
+        v.fill_(5.0)
+        return bool((buf == 5.0).all())
+    r, n, post, pre = amd.block_norm(a["x"], a["y"], a["w_post"], a["w_pre"], gate=a["gate"], n_dtype=a["n_type"])
+    back = amd.block_norm_backward(a["dr"], a["dn"], r, a["y"], a["w_post"], a["w_pre"], post, pre, gate=a["gate"])
+    (xb, x), (yb, y), (nb, nv) = spread(a["x"]), spread(a["y"]), spread(n * 0)
+    d = amd.BlockNormDesc(rows=rows, cols=cols, gate_rows=rows // 2, alpha=1.0, eps=1e-6, x_type=1, y_type=0, n_type=1,
+                          ldx=ld, ldy=ld, ldr=ld, ldn=ld, lddr=ld, lddn=ld, lddx=ld, lddy=ld)
+    amd.amsim_block_norm_fwd(d, x, y, a["gate"], a["w_post"], a["w_pre"], x, nv, None, None)
+    same = (lambda p, q: torch.allclose(p.float(), q.float(), rtol=2.0 ** -7, atol=2.0 ** -7)) if cols % 4 == 0 and (
+        ld % 4 or off % 4) else torch.equal
+    assert same(x, r) and same(nv, n)
+    assert untouched(xb, x) and untouched(yb, y) and untouched(nb, nv)
+    (rb, rv), (yb, y), (drb, dr), (dnb, dn) = (spread(t) for t in (r, a["y"], a["dr"], a["dn"]))
+    ws = amd.workspace(amd.amsim_block_norm_workspace_size(d))
+    sums = [torch.empty_like(a["gate"]), torch.empty_like(a["w_post"]), torch.empty_like(a["w_pre"])]
+    amd.amsim_block_norm_bwd(d, dr, dn, rv, y, a["gate"], a["w_post"], a["w_pre"], post, pre, dr, y, *sums, ws=ws)
+    check_bwd(amd, a, r, post, pre, 1.0, [dr, y, *sums], "bf16", "f32", rows)
+    assert same(dr, back[0]) and same(y, back[1])
+    assert untouched(drb, dr) and untouched(yb, y)
+
+
 @pytest.mark.parametrize("drop", ["dr", "dn", "y", "w_post", "w_pre", "gate"])
 def test_many_rows_without_parts(amd, drop):
     a = make(2600, 512, "f32", "bf16", "f32", 4, seed=9)
