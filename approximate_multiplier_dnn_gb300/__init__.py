@@ -271,6 +271,11 @@ def _ptr(t) -> int | None:
     raise TypeError(f"cannot take a pointer of {type(t)}")
 
 
+def _at(t) -> int | None:
+    """_ptr of a checked tensor or None, in half the time (a small call's time is the host's)."""
+    return None if t is None else t.data_ptr()
+
+
 _raw_stream = None
 
 
@@ -635,23 +640,29 @@ def gemm(A, B, lut, *, transA=False, transB=False, alpha=1.0, beta=0.0, C=None, 
     return C
 
 
+_dtypes = {}
+
+
 def _dtype(t) -> int:
     """amsim_dtype of a tensor (or of a torch dtype)."""
-    import torch
     dtype = getattr(t, "dtype", t)
-    if dtype == torch.float32:
-        return AMSIM_F32
-    if dtype == torch.bfloat16:
-        return AMSIM_BF16
+    if dtype in _dtypes:
+        return _dtypes[dtype]
+    import torch
+    if dtype in (torch.float32, torch.bfloat16):
+        _dtypes.update({torch.float32: AMSIM_F32, torch.bfloat16: AMSIM_BF16})
+        return _dtypes[dtype]
     raise TypeError(f"exact operators take fp32 or bf16 tensors, not {dtype}")
 
 
 def _rows(name, t, rows, cols, dtype=None) -> int:
     """Row stride of a CUDA matrix of `rows` x `cols` whose rows are contiguous."""
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {rows} x {cols}, not {tuple(t.shape)}")
     if not t.is_cuda or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be a CUDA tensor{'' if dtype is None else ' of ' + str(dtype)}")
+    if t.is_contiguous():
+        return cols
     outer, inner = t.stride()
     if cols > 1 and inner != 1 or rows > 1 and outer < cols:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
@@ -686,7 +697,7 @@ def _vocab_plan(tokens, vocab, dim, ld_h, ld_w, ignore_index, reduction):
 def _gate_rows(first, gate, w_post, w_pre):
     """Rows per row of the gate (0 without one), the vectors of a block norm over rows like `first`'s checked."""
     import torch
-    if first.dim() != 2:
+    if first.ndim != 2:
         raise ValueError("block norms take matrices of rows x channels")
     rows, cols = first.shape
     if w_post is not None:
@@ -720,8 +731,8 @@ def block_norm(x, y=None, w_post=None, w_pre=None, *, gate=None, alpha=1.0, eps=
     rstd_pre = empty(rows, dtype=torch.float32, device=device)
     rstd_post = None if w_post is None else empty(rows, dtype=torch.float32, device=device)
     _check("amsim_block_norm_fwd",
-           lib().amsim_block_norm_fwd(desc, x.data_ptr(), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre),
-                                      None if y is None else r.data_ptr(), n.data_ptr(), _ptr(rstd_post),
+           lib().amsim_block_norm_fwd(desc, x.data_ptr(), _at(y), _at(gate), _at(w_post), _at(w_pre),
+                                      None if y is None else r.data_ptr(), n.data_ptr(), _at(rstd_post),
                                       rstd_pre.data_ptr(), _current_stream()))
     return r, n, rstd_post, rstd_pre
 
@@ -755,9 +766,9 @@ def block_norm_backward(dr, dn, r, y, w_post, w_pre, rstd_post, rstd_pre, *, gat
     desc, nb = _block_norm_plan(rows, cols, gate_rows, (_dtype(r), 0), ys, ns, ldr, lddr, lddn, alpha, 0.0, True)
     ws = empty(nb, dtype=torch.uint8, device=device) if nb else None
     _check("amsim_block_norm_bwd",
-           lib().amsim_block_norm_bwd(desc, _ptr(dr), _ptr(dn), r.data_ptr(), _ptr(y), _ptr(gate), _ptr(w_post),
-                                      _ptr(w_pre), _ptr(rstd_post), _ptr(rstd_pre), dx.data_ptr(), _ptr(dy),
-                                      _ptr(dgate), _ptr(dw_post), _ptr(dw_pre) if dn is not None else None, _ptr(ws),
+           lib().amsim_block_norm_bwd(desc, _at(dr), _at(dn), r.data_ptr(), _at(y), _at(gate), _at(w_post),
+                                      _at(w_pre), _at(rstd_post), _at(rstd_pre), dx.data_ptr(), _at(dy),
+                                      _at(dgate), _at(dw_post), _at(dw_pre) if dn is not None else None, _at(ws),
                                       nb, _current_stream()))
     return dx, dy, dgate, dw_post, dw_pre
 
@@ -786,7 +797,7 @@ def vocab_loss(h, w, targets, *, row_weight=None, ignore_index=-100, reduction="
     (desc, nb, _), loss, row, lse = _vocab_call(h, w, targets, row_weight, ignore_index, reduction)
     ws = torch.empty(nb, dtype=torch.uint8, device=h.device)
     _check("amsim_vocab_loss",
-           lib().amsim_vocab_loss(desc, h.data_ptr(), w.data_ptr(), targets.data_ptr(), _ptr(row_weight),
+           lib().amsim_vocab_loss(desc, h.data_ptr(), w.data_ptr(), targets.data_ptr(), _at(row_weight),
                                   loss.data_ptr(), row.data_ptr(), lse.data_ptr(), ws.data_ptr(), nb,
                                   _current_stream()))
     return loss, row, lse
@@ -800,7 +811,7 @@ def vocab_loss_grad(h, w, targets, *, row_weight=None, ignore_index=-100, reduct
     dh, dw = empty(h.shape, dtype=bf16, device=device), empty(w.shape, dtype=bf16, device=device)
     ws = empty(nb, dtype=torch.uint8, device=device)
     _check("amsim_vocab_loss_grad",
-           lib().amsim_vocab_loss_grad(desc, h.data_ptr(), w.data_ptr(), targets.data_ptr(), _ptr(row_weight),
+           lib().amsim_vocab_loss_grad(desc, h.data_ptr(), w.data_ptr(), targets.data_ptr(), _at(row_weight),
                                        loss.data_ptr(), row.data_ptr(), lse.data_ptr(), dh.data_ptr(), dw.data_ptr(),
                                        ws.data_ptr(), nb, _current_stream()))
     return loss, row, lse, dh, dw
