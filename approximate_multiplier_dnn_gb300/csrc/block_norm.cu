@@ -48,13 +48,35 @@ __global__ void __launch_bounds__(kSumWarps * 32) sums_kernel(const Params p, in
         return;
     }
     if (!p.part_gate) return;
+    // as many rows of the gate at once as the warps make, `per` warps each (8 of
+    // them at 16384 x 4096, one after the other with all warps: 18 us)
     const long long groups = p.items / p.splits;
-    const float w = out && p.w_post ? p.w_post[mine] : 1.0f;
+    int per = kSumWarps;
+    while (per > 1 && kSumWarps / per < groups) per >>= 1;
+    const float w = mine < p.cols && p.w_post ? p.w_post[mine] : 1.0f;
     float dw = 0.0f;
-    for (long long g = 0; g < groups; ++g) {
-        const float s = total(p.part_gate + g * p.splits * p.cols, p.splits);
-        if (out && p.dgate) p.dgate[g * p.cols + mine] = p.alpha * w * s;
-        dw = fmaf(p.alpha * (out && p.gate ? p.gate[g * p.cols + mine] : 1.0f), s, dw);
+    for (long long g0 = 0; g0 < groups; g0 += kSumWarps / per) {
+        const long long from = g0 + warp / per;
+        float s = 0.0f;
+        if (on && from < groups) {
+            const float *src = p.part_gate + from * p.splits * p.cols + c;
+#pragma unroll 8
+            for (int i = warp % per; i < p.splits; i += per) s += src[(long long)i * p.cols];
+        }
+        __syncthreads();
+        part[warp][lane] = s;
+        __syncthreads();
+        s = part[lane][warp];                  // channel `warp` of the block: the gate's rows across the lanes
+        for (int d = 1; d < per; d <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        const long long g = g0 + lane / per;
+        float add = 0.0f;
+        if (lane % per == 0 && mine < p.cols && g < groups) {
+            if (p.dgate) p.dgate[g * p.cols + mine] = p.alpha * w * s;
+            add = p.alpha * (p.gate ? p.gate[g * p.cols + mine] : 1.0f) * s;
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) add += __shfl_xor_sync(0xFFFFFFFFu, add, d);
+        dw += add;
     }
     if (out && p.dw_post) p.dw_post[mine] = dw;
 }
@@ -124,7 +146,7 @@ RingShape ring_shape(int cols, int slot_bytes, bool bwd)
     for (;; --s.at_work) {
         // what is not for rows: barriers, sums, a block's own kilobyte, backward the weights and the teams' sums
         const int joined = s.at_work > 1 ? amsim::bn::kTeamThreads * 16 : 0;
-        const int room = bwd ? (amsim::kMaxSmemPerCta - 2048 - amsim::bn::kRingBarBytes - 8 * cols - joined) / s.at_work
+        const int room = bwd ? (amsim::kMaxSmemPerCta - 2048 - 8 * cols - joined) / s.at_work - amsim::bn::kRingBarBytes
                              : amsim::kMaxSmemPerCta / s.at_work - 2048 - amsim::bn::kRingBarBytes;
         s.slots = std::min(8, room / slot_bytes);
         if (s.slots >= 2 || s.at_work == 1) return s;

@@ -9,6 +9,11 @@
 // arithmetic goes through the packed fp32 instructions, two channels each, and
 // what a row costs besides its channels (sums across warps, addresses, roots)
 // is spread over many channels per thread.
+//
+// Measured, of 6768 GB/s for a plain copy: forward 5.3 TB/s at 16384 x 4096
+// bf16 (102 us) and 5.5 at 16384 x 2048 with an fp32 stream, backward 5.3
+// (152 us) and 5.7 (107 us).  Backward at 8192 x 8192 bf16 (173 us, 4.7 TB/s)
+// has room in shared memory for two rows, and at 16384 columns for none.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -493,9 +498,11 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
 // Backward, 5395 x 3047 bf16: 341 us by direct loads, 75 so; 16384 x 1013
 // fp32/bf16: 166, 69.  Whole rows have kernels of their own, as the four rows'
 // ends cost 3 to 7 % of 16384 x 4096 and 8192 x 8192 bf16.
+// PARTS: a slot's parts arrive, and are refilled, each by itself.
+template <int PARTS>
 struct Ring {
     uint8_t *slot0;
-    uint64_t *full;
+    uint64_t *full;                        // [part][slot]
     int slots, bytes;
     int at = 0;
     uint32_t phase = 0;
@@ -503,7 +510,8 @@ struct Ring {
 
     __device__ __forceinline__ uint8_t *wait()
     {
-        tc::bar_wait(full + at, phase, aborted);
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) tc::bar_wait(full + i * slots + at, phase, aborted);
         return slot0 + at * bytes;
     }
     // On to the next slot; the number of the one left.
@@ -516,7 +524,7 @@ struct Ring {
 };
 
 constexpr int kRingNV = 4;                 // steps per thread of the ring kernels
-constexpr int kRingBarBytes = 1024;        // up to 16 teams of 8 slots
+constexpr int kRingBarBytes = 128;         // of a ring: 2 parts of 8 slots
 constexpr int kRingAlign = 128, kRingSlack = 30;   // of a slot; of a row's ends that are off 16 bytes
 // Threads per SM that the kernels' registers allow (up to 128 each): forward as
 // blocks of up to 256 or 512, backward as the teams of one block.
@@ -528,15 +536,16 @@ __host__ __device__ inline int ring_bytes(int cols, int size, int slack)
 // Weights that wait in shared memory: a row of fp32.
 __host__ __device__ inline int kept_floats(int cols) { return (cols + 3) / 4 * 4; }
 
-__device__ __forceinline__ Ring make_ring(const Params &p, uint8_t *smem, int team, int t)
+template <int PARTS>
+__device__ __forceinline__ Ring<PARTS> make_ring(const Params &p, uint8_t *smem, int teams, int team, int t)
 {
-    Ring r;
-    r.full = reinterpret_cast<uint64_t *>(smem) + team * p.slots;
-    r.slot0 = smem + kRingBarBytes + team * p.slots * p.slot_bytes;
+    Ring<PARTS> r;
+    r.full = reinterpret_cast<uint64_t *>(smem + team * kRingBarBytes);
+    r.slot0 = smem + teams * kRingBarBytes + team * p.slots * p.slot_bytes;
     r.slots = p.slots;
     r.bytes = p.slot_bytes;
     if (t == 0) {
-        for (int i = 0; i < p.slots; ++i) tc::bar_init(r.full + i, 1);
+        for (int i = 0; i < p.slots * PARTS; ++i) tc::bar_init(r.full + i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kern
     const int bytes_x = cols * (int)sizeof(X), bytes_y = cols * (int)sizeof(Y);
     const int yoff = ring_bytes(cols, sizeof(X), WHOLE ? 0 : kRingSlack);
     const long long r0 = blockIdx.x * p.block_rows, r1 = min(r0 + p.block_rows, p.rows);
-    Ring ring = make_ring(p, smem, 0, t);
+    Ring<1> ring = make_ring<1>(p, smem, 1, 0, t);
     auto issue = [&](long long row, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
         int xb = bytes_x, yb = bytes_y;
@@ -654,12 +663,12 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
     const bool sums_a = has.y() && (p.dgate || p.dw_post), sums_b = has.dn() && p.dw_pre;
     const int bytes_x = cols * (int)sizeof(X), bytes_y = cols * (int)sizeof(Y), bytes_n = cols * (int)sizeof(N);
     const int rxb = ring_bytes(cols, sizeof(X), WHOLE ? 0 : kRingSlack), rnb = ring_bytes(cols, sizeof(N), WHOLE ? 0 : kRingSlack);
-    const int off_r = has.dr() ? rxb : 0, off_n = off_r + (has.dn() ? rxb : 0), off_y = off_n + (has.dn() ? rnb : 0);
-    float *wq = reinterpret_cast<float *>(smem + kRingBarBytes + teams * p.slots * p.slot_bytes);
+    const int off_n = has.dr() ? rxb : 0, off_r = off_n + (has.dn() ? rnb : 0), off_y = off_r + (has.dn() ? rxb : 0);
+    float *wq = reinterpret_cast<float *>(smem + teams * (kRingBarBytes + p.slots * p.slot_bytes));
     const int row_floats = VEC ? cols : kept_floats(cols);
     float *wu = wq + row_floats;
     float4 *buf = reinterpret_cast<float4 *>(wu + row_floats);     // one per thread, with several teams
-    Ring ring = make_ring(p, smem, team, t);
+    Ring<2> ring = make_ring<2>(p, smem, teams, team, t);
     auto sync = [&] {
         if (warps == 1) __syncwarp();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(p.tpr) : "memory");
@@ -676,22 +685,35 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
             if (q.row < q.end) return;
         }
     };
-    auto issue = [&](const Place &q, int slot) {
+    // A slot's first part, dr and dn, is read by a row's first pass alone, and
+    // refilled half a row before the second part, r and y, is free.  (8192 x
+    // 8192 bf16, room for two rows: 203 us with whole slots, 173 so; 16384 x
+    // 4096: 159, 152; 8192 x 4096 fp32, room for three: 146, 152, as the one
+    // thread issues twice a row.  A second warp's thread for the second part
+    // made the first 183.)
+    auto issue_first = [&](long long row, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
-        int drb = bytes_x, rb = bytes_x, dnb = bytes_n, yb = bytes_y;
+        uint64_t *full = ring.full + slot;
+        int drb = bytes_x, dnb = bytes_n;
         if constexpr (!WHOLE) {
-            drb = row_bytes<X>(p.dr, p.lddr, q.row, drb);
-            rb = row_bytes<X>(p.rin, p.ldr, q.row, rb);
-            dnb = row_bytes<N>(p.dn, p.lddn, q.row, dnb);
-            yb = row_bytes<Y>(p.y, p.ldy, q.row, yb);
+            drb = row_bytes<X>(p.dr, p.lddr, row, drb);
+            dnb = row_bytes<N>(p.dn, p.lddn, row, dnb);
         }
-        tc::bar_expect(ring.full + slot, (has.dr() ? drb : 0) + (has.dn() ? rb + dnb : 0) + (has.y() ? yb : 0));
-        if (has.dr()) copy_row<WHOLE, X>(s, p.dr, p.lddr, q.row, drb, ring.full + slot);
-        if (has.dn()) {
-            copy_row<WHOLE, X>(s + off_r, p.rin, p.ldr, q.row, rb, ring.full + slot);
-            copy_row<WHOLE, N>(s + off_n, p.dn, p.lddn, q.row, dnb, ring.full + slot);
+        tc::bar_expect(full, (has.dr() ? drb : 0) + (has.dn() ? dnb : 0));
+        if (has.dr()) copy_row<WHOLE, X>(s, p.dr, p.lddr, row, drb, full);
+        if (has.dn()) copy_row<WHOLE, N>(s + off_n, p.dn, p.lddn, row, dnb, full);
+    };
+    auto issue_second = [&](long long row, int slot) {
+        uint8_t *s = ring.slot0 + slot * ring.bytes;
+        uint64_t *full = ring.full + ring.slots + slot;
+        int rb = bytes_x, yb = bytes_y;
+        if constexpr (!WHOLE) {
+            rb = row_bytes<X>(p.rin, p.ldr, row, rb);
+            yb = row_bytes<Y>(p.y, p.ldy, row, yb);
         }
-        if (has.y()) copy_row<WHOLE, Y>(s + off_y, p.y, p.ldy, q.row, yb, ring.full + slot);
+        tc::bar_expect(full, (has.dn() ? rb : 0) + (has.y() ? yb : 0));
+        if (has.dn()) copy_row<WHOLE, X>(s + off_r, p.rin, p.ldr, row, rb, full);
+        if (has.y()) copy_row<WHOLE, Y>(s + off_y, p.y, p.ldy, row, yb, full);
     };
     auto advance = [&](Place &q) {
         if ((q.row += teams) < q.end) return;
@@ -702,7 +724,8 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
     settle(ahead);
     if (t == 0)
         for (int i = 0; i < p.slots && ahead.item < p.items; ++i) {
-            issue(ahead, i);
+            issue_first(ahead.row, i);
+            issue_second(ahead.row, i);
             advance(ahead);
         }
     if (has.dn())
@@ -725,7 +748,8 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
 #pragma unroll
     for (int i = 0; i < NV * kP; ++i) b[i] = both(0.0f);
     bool fresh = true;                       // no share has left its sums in part_post yet
-    int last = -1;                           // the slot of the row before, not yet refilled
+    int last = -1;                           // the slot of the row before, not yet refilled,
+    long long refill = -1;                   // and the row whose first part it already has
     for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
         const long long gi = item / p.splits, g0 = gi * p.gate_rows, r0 = g0 + (item - gi * p.splits) * p.item_rows;
         const long long end = min(min(r0 + p.item_rows, g0 + p.gate_rows), p.rows), first = r0 + team;
@@ -766,11 +790,15 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
                 [&](int k) { return kept<VEC>(wu, k, t, p.tpr, cols); },
                 sync,
                 [&](bool barrier) {
-                    // every thread of the team is past the last row: its slot is free
+                    // every thread of the team is past the last row, and this one's first pass
                     if (!barrier) sync();
-                    if (t == 0 && last >= 0 && ahead.item < p.items) {
-                        issue(ahead, last);
-                        advance(ahead);
+                    if (t == 0) {
+                        if (refill >= 0) issue_second(refill, last);
+                        refill = -1;
+                        if (ahead.item < p.items) {
+                            issue_first(refill = ahead.row, ring.at);
+                            advance(ahead);
+                        }
                     }
                     last = ring.next();
                 });
@@ -838,7 +866,7 @@ int launch_types(int nv, Loads loads, bool full, const Params &p, unsigned grid,
         if constexpr (BWD) return launch_kernel(bwd_kernel<__VA_ARGS__, X, Y, N>, p, grid, 0, st); \
         else return launch_kernel(fwd_kernel<__VA_ARGS__, X, Y, N>, p, grid, 0, st);              \
     } while (0)
-    const size_t rows_smem = kRingBarBytes + (size_t)(BWD ? p.rpb : 1) * p.slots * p.slot_bytes;
+    const size_t rows_smem = (size_t)(BWD ? p.rpb : 1) * (kRingBarBytes + p.slots * p.slot_bytes);
     if constexpr (BWD) {
         const size_t smem = rows_smem + 8 * (size_t)kept_floats(p.cols) + (p.rpb > 1 ? kTeamThreads * sizeof(float4) : 0);
         if (loads == kScalarRing) return launch_kernel(bwd_ring_kernel<false, false, true, X, Y, N>, p, grid, smem, st);
