@@ -10,9 +10,9 @@
 //
 // Measured: 256 million parameters in 200 tensors, fp32 moments and a bf16
 // copy, 1.08 ms (7.1 TB/s, a little over a plain copy's rate).  With 8-bit
-// moments and bf16 gradients the same step takes 820 us of the bytes' 530: some
-// 105 instructions an element (decode, two roundings to codes, the block's
-// maximum) fill 0.78 of the issue slots.
+// moments and bf16 gradients the same step takes 829 us of the bytes' 608: some
+// 100 instructions an element (decode, two roundings to codes, the block's
+// maximum) fill 0.72 of the issue slots.
 //
 // Every operation is its correctly rounded fp32 one, in the documented order
 // and with no contraction into fused multiply-adds: the step is then the same
@@ -34,11 +34,6 @@ constexpr int kThreads = 256;
 constexpr int kBlock = AMSIM_ADAMW_BLOCK;
 constexpr int kPass = kThreads * 8;                // elements a thread block takes at once
 static_assert(kBlock == 32 * 8, "one 8-bit block per warp and pass");
-// Passes of a thread block: one, so that small steps fill the GPU, and with
-// 8-bit moments eight once there are enough elements to fill it all the same
-// (kLong): the loads of a pass then run ahead of the arithmetic of the last.
-constexpr int kLongPasses = 8;
-constexpr long long kLong = 10'000'000;
 
 struct Tensor {
     float *p;
@@ -62,7 +57,7 @@ struct Hyper {
 template <int CAP>
 struct Launch {
     Hyper h;
-    int count, passes;
+    int count;
     Tensor t[CAP];
 };
 // Capacities: a launch's parameters are copied whole, so a few tensors take a
@@ -269,191 +264,115 @@ __device__ __forceinline__ float2 step2(float2 p, float2 g, float2 &m, float2 &v
     return sum2(mul2(p, both(t.keep)), mul2(u, both(-t.rate)));
 }
 
-// What a lane holds of a block: elements 4 lane .. and 128 + 4 lane .., so that
-// each load of the warp is of whole neighbouring sectors.
-struct Held {
-    float4 p[2];
-    uint32_t g[8];             // fp32, or bf16 in the first four
-    uint32_t m[2], v[2];
-};
-constexpr int kStages = 3;
-constexpr int kStageWords = 32 * (8 + 8 + 2 + 2);          // of a warp
-constexpr int kAheadBytes = kStages * (kThreads / 32) * kStageWords * 4;
-
-__device__ __forceinline__ void copy_async(uint32_t *dst, const void *src, int bytes)
+// One warp per block of 256 elements, of which a lane holds elements 4 lane ..
+// and 128 + 4 lane .., so that each load of the warp is of whole neighbouring
+// sectors.  A thread block takes one pass, and the blocks of an SM cover one
+// another's loads.  (Eight passes a block, with the next two's words copied
+// ahead to shared memory: 256 M elements in 200 tensors with bf16 gradients and
+// copies 792 us instead of 823, with fp32 ones 856 instead of 833, 300 M in one
+// tensor 860 instead of 820, 12 M in 100 tensors 51 instead of 44.)
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_constant__ Launch<CAP> L)
 {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-    else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
-}
-
-// One warp per block of 256 elements.  AHEAD: with several passes, the next two
-// passes' words are on their way to shared memory (each lane copies and reads
-// its own, so nothing but its own copies is waited for).
-template <int CAP, bool AHEAD>
-__global__ void __launch_bounds__(kThreads, AHEAD ? 3 : 4) adamw8_kernel(const __grid_constant__ Launch<CAP> L)
-{
-    extern __shared__ __align__(16) uint32_t staged[];
     const Tensor &t = find(L, (int)blockIdx.x);
     const Hyper &h = L.h;
     const float gs = h.grad_scale ? *h.grad_scale : 1.0f;
     const bool scaled = h.grad_scale != nullptr, half = t.flags & kBf16Grad;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int passes = AHEAD ? L.passes : 1;
-    // the warp's first block and the distance to its next
-    const long long first = (long long)((int)blockIdx.x - t.first) * passes * kPass + warp * kBlock;
+    const long long b0 = (long long)((int)blockIdx.x - t.first) * kPass + warp * kBlock;
+    if (b0 >= t.n) return;
     uint8_t *mq = static_cast<uint8_t *>(t.m), *vq = static_cast<uint8_t *>(t.v);
-    uint32_t *const mine = staged + warp * kStages * kStageWords;
-    auto whole = [&](long long b0) { return (t.flags & kVector) && b0 + kBlock <= t.n; };
-    auto fetch = [&](int k) {                  // pass k's words to its stage
-        const long long b0 = first + (long long)k * kPass;
-        if (k < passes && whole(b0)) {
-            uint32_t *s = mine + k % kStages * kStageWords;
+    const bool vec = (t.flags & kVector) && b0 + kBlock <= t.n;
+    const float ms = t.m_scale[b0 / kBlock], vs = t.v_scale[b0 / kBlock];
+    float p[8], g[8];
+    uint32_t a[2], b[2];
+    if (vec) {
+        uint2 gh[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const long long i = b0 + q * 128 + lane * 4;
+            *reinterpret_cast<float4 *>(p + q * 4) = *reinterpret_cast<const float4 *>(t.p + i);
+            if (half) gh[q] = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(t.g) + i);
+            else *reinterpret_cast<float4 *>(g + q * 4) = *reinterpret_cast<const float4 *>(static_cast<const float *>(t.g) + i);
+            a[q] = *reinterpret_cast<const uint32_t *>(mq + i);
+            b[q] = *reinterpret_cast<const uint32_t *>(vq + i);
+        }
+        if (half)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const long long i = b0 + q * 128 + lane * 4;
-                copy_async(s + q * 128 + lane * 4, t.p + i, 16);
-                if (half) copy_async(s + 256 + q * 64 + lane * 2, static_cast<const __nv_bfloat16 *>(t.g) + i, 8);
-                else copy_async(s + 256 + q * 128 + lane * 4, static_cast<const float *>(t.g) + i, 16);
-                copy_async(s + 512 + q * 32 + lane, mq + i, 4);
-                copy_async(s + 576 + q * 32 + lane, vq + i, 4);
+                g[q * 4] = bf16_bits(gh[q].x);
+                g[q * 4 + 1] = __uint_as_float(gh[q].x & 0xFFFF0000u);
+                g[q * 4 + 2] = bf16_bits(gh[q].y);
+                g[q * 4 + 3] = __uint_as_float(gh[q].y & 0xFFFF0000u);
             }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    auto scale_of = [&](const float *s, int k) {
-        const long long b0 = first + (long long)k * kPass;
-        return k < passes && b0 < t.n ? s[b0 / kBlock] : 0.0f;
-    };
-    if (AHEAD) {
-        fetch(0);
-        fetch(1);
-    }
-    float next_ms = scale_of(t.m_scale, 0), next_vs = scale_of(t.v_scale, 0);
-#pragma unroll 1
-    for (int k = 0; k < passes; ++k) {
-        const long long b0 = first + (long long)k * kPass;
-        if (b0 >= t.n) break;
-        const bool vec = whole(b0);
-        const float ms = next_ms, vs = next_vs;
-        float p[8], g[8];
-        uint32_t a[2], b[2];
-        if (vec) {
-            Held w;
-            if (AHEAD) {
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-                const uint32_t *s = mine + k % kStages * kStageWords;
+    } else {
+        a[0] = a[1] = b[0] = b[1] = 0;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    w.p[q] = *reinterpret_cast<const float4 *>(s + q * 128 + lane * 4);
-                    if (half) *reinterpret_cast<uint2 *>(w.g + q * 2) = *reinterpret_cast<const uint2 *>(s + 256 + q * 64 + lane * 2);
-                    else *reinterpret_cast<uint4 *>(w.g + q * 4) = *reinterpret_cast<const uint4 *>(s + 256 + q * 128 + lane * 4);
-                    w.m[q] = s[512 + q * 32 + lane];
-                    w.v[q] = s[576 + q * 32 + lane];
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const long long i = b0 + q * 128 + lane * 4;
-                    w.p[q] = *reinterpret_cast<const float4 *>(t.p + i);
-                    if (half) *reinterpret_cast<uint2 *>(w.g + q * 2) = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(t.g) + i);
-                    else *reinterpret_cast<uint4 *>(w.g + q * 4) = *reinterpret_cast<const uint4 *>(static_cast<const float *>(t.g) + i);
-                    w.m[q] = *reinterpret_cast<const uint32_t *>(mq + i);
-                    w.v[q] = *reinterpret_cast<const uint32_t *>(vq + i);
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                *reinterpret_cast<float4 *>(p + q * 4) = w.p[q];
-                a[q] = w.m[q];
-                b[q] = w.v[q];
-            }
-            if (half) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    g[2 * j] = __uint_as_float(w.g[j] << 16);
-                    g[2 * j + 1] = __uint_as_float(w.g[j] & 0xFFFF0000u);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = __uint_as_float(w.g[j]);
-            }
-        } else {
-            a[0] = a[1] = b[0] = b[1] = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const long long e = b0 + (j >> 2) * 128 + lane * 4 + (j & 3);
-                const bool in = e < t.n;
-                p[j] = in ? t.p[e] : 0.0f;
-                g[j] = in ? load_grad(t, e) : 0.0f;
-                a[j >> 2] |= (in ? (uint32_t)mq[e] : 0u) << (8 * (j & 3));
-                b[j >> 2] |= (in ? (uint32_t)vq[e] : 0u) << (8 * (j & 3));
-            }
-        }
-        if (AHEAD) {
-            fetch(k + 2);
-            next_ms = scale_of(t.m_scale, k + 1);
-            next_vs = scale_of(t.v_scale, k + 1);
-        }
-        float2 mm[4], vv[4], root[4];
-        uint32_t mt = 0, vt = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t x = a[j >> 1], y = b[j >> 1];
-            const int o = 2 * (j & 1);
-            mm[j] = values_m(make_float2(byte_float<true>(x, o), byte_float<true>(x, o + 1)), ms);
-            vv[j] = values_v(make_float2(byte_float<false>(y, o), byte_float<false>(y, o + 1)), vs);
-            float2 gg = make_float2(g[2 * j], g[2 * j + 1]);
-            if (scaled) gg = mul2(gg, both(gs));
-            const float2 q = step2(make_float2(p[2 * j], p[2 * j + 1]), gg, mm[j], vv[j], root[j], h, t);
-            p[2 * j] = q.x;
-            p[2 * j + 1] = q.y;
-            mt = max(mt, max(__float_as_uint(mm[j].x) & 0x7FFFFFFFu, __float_as_uint(mm[j].y) & 0x7FFFFFFFu));
-            vt = max(vt, max(__float_as_uint(vv[j].x) & 0x7FFFFFFFu, __float_as_uint(vv[j].y) & 0x7FFFFFFFu));
-        }
-        if (vec) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const long long i = b0 + q * 128 + lane * 4;
-                *reinterpret_cast<float4 *>(t.p + i) = *reinterpret_cast<const float4 *>(p + q * 4);
-                if (t.copy)
-                    *reinterpret_cast<uint2 *>(t.copy + i) =
-                        make_uint2(pack_bf16(p[q * 4], p[q * 4 + 1]), pack_bf16(p[q * 4 + 2], p[q * 4 + 3]));
-            }
-        }
-        const float mtop = warp_top(mt), vtop = warp_top(vt);
-        const float mr = __fsqrt_rn(mtop), vr = __fsqrt_rn(__fsqrt_rn(vtop));
-        const float mk = mr > 0.0f ? __fdiv_rn(127.0f, mr) : 0.0f, vk = vr > 0.0f ? __fdiv_rn(255.0f, vr) : 0.0f;
-        auto at = [](const float2 (&x)[4], int j) { return j & 1 ? x[j >> 1].y : x[j >> 1].x; };
-        const uint2 ma = codes8(mk, mtop < 1e-30f, [&](int j) { return fabsf(at(mm, j)); }, [](int) { return 0.0f; },
-                                [&](int j) { return __float_as_uint(at(mm, j)) & 0x80000000u; });
-        // a second moment above zero keeps a code above zero
-        const uint2 va = codes8(vk, vtop < 1e-26f, [&](int j) { return at(root, j); },
-                                [&](int j) { return at(vv, j) > 0.0f ? 1.0f : 0.0f; }, [](int) { return 0u; });
-        if (vec) {
-            *reinterpret_cast<uint32_t *>(mq + b0 + lane * 4) = ma.x;
-            *reinterpret_cast<uint32_t *>(mq + b0 + 128 + lane * 4) = ma.y;
-            *reinterpret_cast<uint32_t *>(vq + b0 + lane * 4) = va.x;
-            *reinterpret_cast<uint32_t *>(vq + b0 + 128 + lane * 4) = va.y;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const long long e = b0 + (j >> 2) * 128 + lane * 4 + (j & 3);
-                if (e < t.n) {
-                    t.p[e] = p[j];
-                    if (t.copy) t.copy[e] = __float2bfloat16_rn(p[j]);
-                    mq[e] = (uint8_t)((j < 4 ? ma.x : ma.y) >> (8 * (j & 3)) & 0xFFu);
-                    vq[e] = (uint8_t)((j < 4 ? va.x : va.y) >> (8 * (j & 3)) & 0xFFu);
-                }
-            }
-        }
-        if (lane == 0) {
-            t.m_scale[b0 / kBlock] = finite_or_nan(mtop);
-            t.v_scale[b0 / kBlock] = finite_or_nan(vtop);
+        for (int j = 0; j < 8; ++j) {
+            const long long e = b0 + (j >> 2) * 128 + lane * 4 + (j & 3);
+            const bool in = e < t.n;
+            p[j] = in ? t.p[e] : 0.0f;
+            g[j] = in ? load_grad(t, e) : 0.0f;
+            a[j >> 2] |= (in ? (uint32_t)mq[e] : 0u) << (8 * (j & 3));
+            b[j >> 2] |= (in ? (uint32_t)vq[e] : 0u) << (8 * (j & 3));
         }
     }
-    if (AHEAD) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    float2 mm[4], vv[4], root[4];
+    uint32_t mt = 0, vt = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t x = a[j >> 1], y = b[j >> 1];
+        const int o = 2 * (j & 1);
+        mm[j] = values_m(make_float2(byte_float<true>(x, o), byte_float<true>(x, o + 1)), ms);
+        vv[j] = values_v(make_float2(byte_float<false>(y, o), byte_float<false>(y, o + 1)), vs);
+        float2 gg = make_float2(g[2 * j], g[2 * j + 1]);
+        if (scaled) gg = mul2(gg, both(gs));
+        const float2 q = step2(make_float2(p[2 * j], p[2 * j + 1]), gg, mm[j], vv[j], root[j], h, t);
+        p[2 * j] = q.x;
+        p[2 * j + 1] = q.y;
+        mt = max(mt, max(__float_as_uint(mm[j].x) & 0x7FFFFFFFu, __float_as_uint(mm[j].y) & 0x7FFFFFFFu));
+        vt = max(vt, max(__float_as_uint(vv[j].x) & 0x7FFFFFFFu, __float_as_uint(vv[j].y) & 0x7FFFFFFFu));
+    }
+    if (vec) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const long long i = b0 + q * 128 + lane * 4;
+            *reinterpret_cast<float4 *>(t.p + i) = *reinterpret_cast<const float4 *>(p + q * 4);
+            if (t.copy)
+                *reinterpret_cast<uint2 *>(t.copy + i) =
+                    make_uint2(pack_bf16(p[q * 4], p[q * 4 + 1]), pack_bf16(p[q * 4 + 2], p[q * 4 + 3]));
+        }
+    }
+    const float mtop = warp_top(mt), vtop = warp_top(vt);
+    const float mr = __fsqrt_rn(mtop), vr = __fsqrt_rn(__fsqrt_rn(vtop));
+    const float mk = mr > 0.0f ? __fdiv_rn(127.0f, mr) : 0.0f, vk = vr > 0.0f ? __fdiv_rn(255.0f, vr) : 0.0f;
+    auto at = [](const float2 (&x)[4], int j) { return j & 1 ? x[j >> 1].y : x[j >> 1].x; };
+    const uint2 ma = codes8(mk, mtop < 1e-30f, [&](int j) { return fabsf(at(mm, j)); }, [](int) { return 0.0f; },
+                            [&](int j) { return __float_as_uint(at(mm, j)) & 0x80000000u; });
+    // a second moment above zero keeps a code above zero
+    const uint2 va = codes8(vk, vtop < 1e-26f, [&](int j) { return at(root, j); },
+                            [&](int j) { return at(vv, j) > 0.0f ? 1.0f : 0.0f; }, [](int) { return 0u; });
+    if (vec) {
+        *reinterpret_cast<uint32_t *>(mq + b0 + lane * 4) = ma.x;
+        *reinterpret_cast<uint32_t *>(mq + b0 + 128 + lane * 4) = ma.y;
+        *reinterpret_cast<uint32_t *>(vq + b0 + lane * 4) = va.x;
+        *reinterpret_cast<uint32_t *>(vq + b0 + 128 + lane * 4) = va.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const long long e = b0 + (j >> 2) * 128 + lane * 4 + (j & 3);
+            if (e < t.n) {
+                t.p[e] = p[j];
+                if (t.copy) t.copy[e] = __float2bfloat16_rn(p[j]);
+                mq[e] = (uint8_t)((j < 4 ? ma.x : ma.y) >> (8 * (j & 3)) & 0xFFu);
+                vq[e] = (uint8_t)((j < 4 ? va.x : va.y) >> (8 * (j & 3)) & 0xFFu);
+            }
+        }
+    }
+    if (lane == 0) {
+        t.m_scale[b0 / kBlock] = finite_or_nan(mtop);
+        t.v_scale[b0 / kBlock] = finite_or_nan(vtop);
+    }
 }
 
 // Four codes per thread and step: whole sectors of both codes and values.
@@ -489,23 +408,14 @@ __global__ void __launch_bounds__(kThreads) moment_values_kernel(const uint8_t *
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 template <int CAP>
-int launch(const Hyper &h, const Tensor *t, int count, int chunks, int passes, bool eight, cudaStream_t st)
+int launch(const Hyper &h, const Tensor *t, int count, int chunks, bool eight, cudaStream_t st)
 {
     Launch<CAP> L;
     L.h = h;
     L.count = count;
-    L.passes = passes;
     for (int i = 0; i < count; ++i) L.t[i] = t[i];
-    if (!eight) {
-        adamw_kernel<CAP><<<(unsigned)chunks, kThreads, 0, st>>>(L);
-    } else if (passes == 1) {
-        adamw8_kernel<CAP, false><<<(unsigned)chunks, kThreads, 0, st>>>(L);
-    } else {
-        const cudaError_t e = cudaFuncSetAttribute(adamw8_kernel<CAP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kAheadBytes);
-        if (e != cudaSuccess) return amsim::cuda_status(e);
-        adamw8_kernel<CAP, true><<<(unsigned)chunks, kThreads, kAheadBytes, st>>>(L);
-    }
+    if (eight) adamw8_kernel<CAP><<<(unsigned)chunks, kThreads, 0, st>>>(L);
+    else adamw_kernel<CAP><<<(unsigned)chunks, kThreads, 0, st>>>(L);
     const int rc = amsim::cuda_status(cudaGetLastError());
     if (rc == AMSIM_OK) amsim::count_launch();
     return rc;
@@ -522,7 +432,6 @@ extern "C" int amsim_adamw_step(int count, const amsim_adamw_tensor *tensors, co
         !(y.eps >= 0.0) || !std::isfinite(y.eps) || y.step < 1 || !aligned(y.grad_scale, 4))
         return AMSIM_EINVAL;
     bool any = false, eight = false;
-    double total = 0.0;
     for (int i = 0; i < count; ++i) {
         const amsim_adamw_tensor &a = tensors[i];
         if (a.n < 0 || (a.g_type != AMSIM_F32 && a.g_type != AMSIM_BF16) || a.reserved != 0 ||
@@ -538,7 +447,6 @@ extern "C" int amsim_adamw_step(int count, const amsim_adamw_tensor *tensors, co
         any = true;
         eight = e;
         if ((a.n + kPass - 1) / kPass > 0x3FFFFFFF) return AMSIM_EINVAL;
-        total += (double)a.n;
     }
     Hyper h;
     h.beta1 = (float)y.beta1;
@@ -553,18 +461,16 @@ extern "C" int amsim_adamw_step(int count, const amsim_adamw_tensor *tensors, co
     constexpr int kMost = kCapacity[2];
     Tensor t[kMost];
     int used = 0, chunks = 0;
-    const int passes = eight && total >= (double)kLong ? kLongPasses : 1;
-    const long long chunk = (long long)passes * kPass;
     for (int i = 0; i <= count; ++i) {
         long long add = 0;
         if (i < count) {
-            add = (tensors[i].n + chunk - 1) / chunk;
+            add = (tensors[i].n + kPass - 1) / kPass;
             if (add == 0) continue;
         }
         if (used && (i == count || used == kMost || chunks + add > 0x7FFFFFFFLL)) {
-            const int rc = used <= kCapacity[0]   ? launch<kCapacity[0]>(h, t, used, chunks, passes, eight, st)
-                           : used <= kCapacity[1] ? launch<kCapacity[1]>(h, t, used, chunks, passes, eight, st)
-                                                  : launch<kMost>(h, t, used, chunks, passes, eight, st);
+            const int rc = used <= kCapacity[0]   ? launch<kCapacity[0]>(h, t, used, chunks, eight, st)
+                           : used <= kCapacity[1] ? launch<kCapacity[1]>(h, t, used, chunks, eight, st)
+                                                  : launch<kMost>(h, t, used, chunks, eight, st);
             if (rc) return rc;
             used = 0;
             chunks = 0;
