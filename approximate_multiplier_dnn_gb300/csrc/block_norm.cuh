@@ -21,6 +21,7 @@
 #include "bounded_wait.cuh"
 #include "chained.cuh"
 #include "pairs.cuh"
+#include "row_pieces.cuh"
 
 namespace amsim {
 namespace bn {
@@ -493,8 +494,7 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
 // results do not depend on how many rows come with it.
 //
 // Rows that do not start and end on 16 bytes (WHOLE false) come as the aligned
-// pieces of 16 that hold them, and start inside their slot.  (Such a piece lies
-// in one page, so its bytes beside the row can be read; they are not used.)
+// pieces of 16 that hold them (row_pieces.cuh), and start inside their slot.
 // Backward, 5395 x 3047 bf16: 341 us by direct loads, 75 so; 16384 x 1013
 // fp32/bf16: 166, 69.  Whole rows have kernels of their own, as the four rows'
 // ends cost 3 to 7 % of 16384 x 4096 and 8192 x 8192 bf16.
@@ -552,20 +552,33 @@ __device__ __forceinline__ Ring<PARTS> make_ring(const Params &p, uint8_t *smem,
     return r;
 }
 
-// The bytes of the aligned piece that holds row `row`, of `bytes`, of a tensor.
-template <typename T>
-__device__ __forceinline__ int row_bytes(const void *base, long long ld, long long row, int bytes)
+template <int SIZE> struct Bits;
+template <> struct Bits<2> { using type = uint16_t; };
+template <> struct Bits<4> { using type = uint32_t; };
+
+// A row's way to a slot: the row itself, or its pieces, after the elements that
+// they leave out have been copied.  The thread that issues the copy calls it
+// before it arrives on the slot's barrier.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ Pieces row_to(uint8_t *slot, const void *base, long long ld, long long row, long long rows, int bytes)
 {
-    return (int)(reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + row * ld) & 15) + bytes + 15 & ~15;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + row * ld);
+    if constexpr (WHOLE) {
+        return Pieces{a, 0, bytes};
+    } else {
+        using W = typename Bits<sizeof(T)>::type;
+        const bool first = row == 0, last = row == rows - 1;
+        if (first || last) {
+            copy_ends<W>(slot, a, bytes, first, last);
+            tc::fence_staged();
+        }
+        return row_pieces(a, bytes, first, last);
+    }
 }
 
-// Copies the row, or the piece that holds it, to a slot.
-template <bool WHOLE, typename T>
-__device__ __forceinline__ void copy_row(uint8_t *slot, const void *base, long long ld, long long row, int bytes, uint64_t *bar)
+__device__ __forceinline__ void copy_pieces(uint8_t *slot, const Pieces &r, uint64_t *bar)
 {
-    const T *from = static_cast<const T *>(base) + row * ld;
-    if constexpr (WHOLE) tc::copy_bytes(slot, from, bytes, bar);
-    else tc::copy_bytes(slot, reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)15), bytes, bar);
+    tc::copy_bytes(slot + r.at, reinterpret_cast<const void *>(r.from), r.bytes, bar);
 }
 
 // Where the row starts in a slot that was filled so.
@@ -600,14 +613,12 @@ __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kern
     Ring<1> ring = make_ring<1>(p, smem, 1, 0, t);
     auto issue = [&](long long row, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
-        int xb = bytes_x, yb = bytes_y;
-        if constexpr (!WHOLE) {
-            xb = row_bytes<X>(p.x, p.ldx, row, xb);
-            yb = row_bytes<Y>(p.y, p.ldy, row, yb);
-        }
-        tc::bar_expect(ring.full + slot, xb + (has.y() ? yb : 0));
-        copy_row<WHOLE, X>(s, p.x, p.ldx, row, xb, ring.full + slot);
-        if (has.y()) copy_row<WHOLE, Y>(s + yoff, p.y, p.ldy, row, yb, ring.full + slot);
+        uint64_t *full = ring.full + slot;
+        const Pieces x = row_to<WHOLE, X>(s, p.x, p.ldx, row, p.rows, bytes_x);
+        const Pieces y = row_to<WHOLE, Y>(s + yoff, p.y, p.ldy, row, p.rows, bytes_y);
+        tc::bar_expect(full, x.bytes + (has.y() ? y.bytes : 0));
+        copy_pieces(s, x, full);
+        if (has.y()) copy_pieces(s + yoff, y, full);
     };
     if (t == 0)
         for (int i = 0; i < p.slots && r0 + i < r1; ++i) issue(r0 + i, i);
@@ -694,26 +705,20 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
     auto issue_first = [&](long long row, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
         uint64_t *full = ring.full + slot;
-        int drb = bytes_x, dnb = bytes_n;
-        if constexpr (!WHOLE) {
-            drb = row_bytes<X>(p.dr, p.lddr, row, drb);
-            dnb = row_bytes<N>(p.dn, p.lddn, row, dnb);
-        }
-        tc::bar_expect(full, (has.dr() ? drb : 0) + (has.dn() ? dnb : 0));
-        if (has.dr()) copy_row<WHOLE, X>(s, p.dr, p.lddr, row, drb, full);
-        if (has.dn()) copy_row<WHOLE, N>(s + off_n, p.dn, p.lddn, row, dnb, full);
+        const Pieces dr = row_to<WHOLE, X>(s, p.dr, p.lddr, row, p.rows, bytes_x);
+        const Pieces dn = row_to<WHOLE, N>(s + off_n, p.dn, p.lddn, row, p.rows, bytes_n);
+        tc::bar_expect(full, (has.dr() ? dr.bytes : 0) + (has.dn() ? dn.bytes : 0));
+        if (has.dr()) copy_pieces(s, dr, full);
+        if (has.dn()) copy_pieces(s + off_n, dn, full);
     };
     auto issue_second = [&](long long row, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
         uint64_t *full = ring.full + ring.slots + slot;
-        int rb = bytes_x, yb = bytes_y;
-        if constexpr (!WHOLE) {
-            rb = row_bytes<X>(p.rin, p.ldr, row, rb);
-            yb = row_bytes<Y>(p.y, p.ldy, row, yb);
-        }
-        tc::bar_expect(full, (has.dn() ? rb : 0) + (has.y() ? yb : 0));
-        if (has.dn()) copy_row<WHOLE, X>(s + off_r, p.rin, p.ldr, row, rb, full);
-        if (has.y()) copy_row<WHOLE, Y>(s + off_y, p.y, p.ldy, row, yb, full);
+        const Pieces r = row_to<WHOLE, X>(s + off_r, p.rin, p.ldr, row, p.rows, bytes_x);
+        const Pieces y = row_to<WHOLE, Y>(s + off_y, p.y, p.ldy, row, p.rows, bytes_y);
+        tc::bar_expect(full, (has.dn() ? r.bytes : 0) + (has.y() ? y.bytes : 0));
+        if (has.dn()) copy_pieces(s + off_r, r, full);
+        if (has.y()) copy_pieces(s + off_y, y, full);
     };
     auto advance = [&](Place &q) {
         if ((q.row += teams) < q.end) return;

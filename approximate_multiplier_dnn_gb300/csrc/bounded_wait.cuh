@@ -124,6 +124,8 @@ __device__ __forceinline__ void copy_bytes(void *dst, const void *src, uint32_t 
         "l"(src), "r"(bytes), "r"(smem_addr(bar))
         : "memory");
 }
+// Shared-memory writes of this thread before become visible to copies issued after.
+__device__ __forceinline__ void fence_staged() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 }  // namespace tc
 }  // namespace amsim

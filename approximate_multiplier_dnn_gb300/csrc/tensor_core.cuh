@@ -65,8 +65,6 @@ __device__ __forceinline__ void stores_commit() { asm volatile("cp.async.bulk.co
 // The thread's committed stores have read their shared memory / are done.
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// Shared-memory writes of this thread before become visible to copies issued after.
-__device__ __forceinline__ void fence_staged() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {

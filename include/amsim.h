@@ -561,8 +561,9 @@ enum amsim_dtype { AMSIM_F32 = 0, AMSIM_BF16 = 1 };
  * its type.  Norm weights and gates are fp32.  `gate` (or null: ones) has one
  * row of `cols` values for each `gate_rows` consecutive rows (0: one for all).
  * Rows need no alignment beyond their elements'.  Inputs whose rows do not
- * start and end on 16 bytes may be read in whole aligned 16-byte pieces; the
- * bytes beside a row have no effect.
+ * start and end on 16 bytes may be read in whole aligned 16-byte pieces: up to
+ * 15 bytes beside a row, between a tensor's first element and its last, are
+ * then read and have no effect.
  */
 typedef struct amsim_block_norm_desc {
     int64_t rows;
