@@ -498,6 +498,17 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
 // Backward, 5395 x 3047 bf16: 341 us by direct loads, 75 so; 16384 x 1013
 // fp32/bf16: 166, 69.  Whole rows have kernels of their own, as the four rows'
 // ends cost 3 to 7 % of 16384 x 4096 and 8192 x 8192 bf16.
+
+// Waits, up to the limit once more, for the copies into a ring whose next slot is `at`.
+static __device__ __noinline__ void settle_copies(uint64_t *full, int parts, int slots, int at, uint32_t phase)
+{
+    const unsigned long long t0 = tc::now_ns();
+    for (int i = 0; i < parts * slots; ++i) {
+        const int slot = i % slots;
+        while (!tc::bar_try(full + i, slot < at ? phase ^ 1 : phase) && tc::now_ns() - t0 <= tc::kWaitLimitNs) {}
+    }
+}
+
 // PARTS: a slot's parts arrive, and are refilled, each by itself.
 template <int PARTS>
 struct Ring {
@@ -508,10 +519,15 @@ struct Ring {
     uint32_t phase = 0;
     bool aborted = false;
 
+    // A thread whose wait gives up waits for nothing from then on, and issues
+    // nothing, so that no copy is on its way when the block ends.
     __device__ __forceinline__ uint8_t *wait()
     {
+        if (!aborted) {
 #pragma unroll
-        for (int i = 0; i < PARTS; ++i) tc::bar_wait(full + i * slots + at, phase, aborted);
+            for (int i = 0; i < PARTS; ++i) tc::bar_wait(full + i * slots + at, phase, aborted);
+            if (aborted) settle_copies(full, PARTS, slots, at, phase);
+        }
         return slot0 + at * bytes;
     }
     // On to the next slot; the number of the one left.
@@ -652,7 +668,7 @@ __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kern
             [&](bool barrier) {
                 if (!barrier) __syncthreads();             // the row is in registers
                 const int freed = ring.next();
-                if (t == 0 && row + p.slots < r1) issue(row + p.slots, freed);
+                if (t == 0 && row + p.slots < r1 && !ring.aborted) issue(row + p.slots, freed);
             });
     }
 }
@@ -797,7 +813,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
                 [&](bool barrier) {
                     // every thread of the team is past the last row, and this one's first pass
                     if (!barrier) sync();
-                    if (t == 0) {
+                    if (t == 0 && !ring.aborted) {
                         if (refill >= 0) issue_second(refill, last);
                         refill = -1;
                         if (ahead.item < p.items) {
