@@ -757,7 +757,7 @@ def block_norm_backward(dr, dn, r, y, w_post, w_pre, rstd_post, rstd_pre, *, gat
         ys = (_dtype(y), _rows("y", y, rows, cols))
         dy = empty((rows, cols), dtype=y.dtype, device=device)
     if gate is not None:
-        dgate = torch.empty_like(gate)
+        dgate = torch.empty_like(gate) if rows else torch.zeros_like(gate)
     if w_post is not None:
         _vector("rstd_post", rstd_post, rows, f32)
         dw_post = torch.empty_like(w_post)

@@ -282,8 +282,8 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
     int rc = check(d);
     if (rc) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (d->rows == 0) {                      // sums over no rows
-        for (float *f : {dw_post, dw_pre})
+    if (d->rows == 0) {                      // sums over no rows; gate_rows 0: the gate has a row all the same
+        for (float *f : {d->gate_rows ? nullptr : dgate, dw_post, dw_pre})
             if (f && cudaMemsetAsync(f, 0, (size_t)d->cols * 4, st) != cudaSuccess) {
                 cudaGetLastError();
                 return AMSIM_ECUDA;

@@ -601,7 +601,8 @@ int amsim_block_norm_fwd(const amsim_block_norm_desc *desc, const void *x, const
  *   dw_pre  = sum over rows of dn * rh.
  * Outputs that are null are not computed; dy, dgate and dw_post need y, dw_pre
  * needs dn.  dx may alias dr; dy may alias y or dn (equal types and strides).
- * Row sums are kept per row share in scratch and added in share order.
+ * Row sums are kept per row share in scratch and added in share order.  Without
+ * rows, dw_post, dw_pre and (gate_rows 0) the one row of dgate are zeros.
  * Scratch: amsim_block_norm_workspace_size; with less (even none) a call uses
  * fewer row shares, down to one, which needs none.
  */

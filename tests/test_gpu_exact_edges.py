@@ -34,3 +34,31 @@ def test_streamed_ends_off_16_bytes(amd, off, cols):
         few = amd.block_norm_backward(dr[s], dn[s], ro[s], y[s], w, v, fwd[2][s], fwd[3][s], **kw)
         assert torch.equal(back[0][s], few[0]) and torch.equal(back[1][s], few[1])
     assert amd.amsim_device_errors() == (amd.AMSIM_OK, 0)
+
+
+@pytest.mark.parametrize("groups", [1, 3])
+def test_empty_batch_has_a_zero_gate_gradient(amd, groups):
+    """Every sum over no rows is zero, whatever the memory held before."""
+    import torch
+    f = dict(device="cuda")
+    x, w, gate = torch.empty((0, 24), **f), torch.ones(24, **f), torch.ones((groups, 24), **f)
+    for _ in range(3):
+        torch.full((4096,), float("nan"), **f)               # what the allocator hands out next
+        r, n, post, pre = amd.block_norm(x, x, w, w, gate=gate)
+        assert r.shape == n.shape == (0, 24)
+        for t in amd.block_norm_backward(x, x, r, x, w, w, post, pre, gate=gate)[2:]:
+            assert not t.any()
+    d = amd.BlockNormDesc(rows=0, cols=24, alpha=1.0)
+    sums = [torch.full((24,), 3.0, **f) for _ in range(3)]
+    amd.amsim_block_norm_bwd(d, x, x, x, x, gate, w, w, post, pre, x, x, *sums)
+    assert not torch.stack(sums).any()
+
+
+def test_layer_on_an_empty_batch(amd):
+    import torch
+    from approximate_multiplier_dnn_gb300.layers import BlockNorm
+    norm = BlockNorm(24, gate="channel")
+    r, n = norm(torch.zeros((0, 5, 24), device="cuda"), torch.zeros((0, 5, 24), device="cuda"))
+    assert r.shape == n.shape == (0, 5, 24)
+    (r.sum() + n.sum()).backward()
+    assert not torch.stack([norm.gate.grad[0], norm.w_post.grad, norm.w_pre.grad]).any()
