@@ -156,8 +156,7 @@ RingShape ring_shape(int cols, int slot_bytes, bool bwd)
 // The ring from half a row for each at work on.  By kernels alone, bf16: 608 x
 // 1024 forward 3.9 us by direct loads, 3.2 so, backward 17.3 and 13.8; 152 x
 // 4096 3.9, 3.2 and 16.0, 15.9; 304 x 2048 backward 14.7, 14.3.  With half of
-// that backward is no faster, and a small call's time is the host's, which a
-// large share of shared memory costs a call to ask for.
+// that backward is no faster, and a small call's time is the host's.
 bool ring_pays(int64_t rows, const RingShape &r, int sms)
 {
     return r.slots >= 2 && 2 * rows >= (int64_t)sms * r.at_work;

@@ -16,6 +16,8 @@
 // has room in shared memory for two rows, and at 16384 columns for none.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 
 #include "bounded_wait.cuh"
@@ -865,14 +867,29 @@ int launch_fwd_bf16(int nv, Loads loads, bool full, int y_type, int n_type, cons
 int launch_bwd_f32(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
 int launch_bwd_bf16(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
 
-template <typename K>
-int launch_kernel(K kernel, const Params &p, unsigned grid, size_t smem, cudaStream_t st)
+// The kernel is a template argument, so that `allowed` is its own: the devices
+// on which it may have all the shared memory there is.  (A limit set to each
+// call's own size would be lowered by a call from another thread between here
+// and the launch.)
+template <auto KERNEL>
+int launch_kernel(const Params &p, unsigned grid, size_t smem, cudaStream_t st)
 {
+    static std::atomic<uint64_t> allowed{0};
     if (smem > 40 * 1024) {                // with the static shared memory, 48 KB go without asking
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return cuda_status(e);
+        int sms = 0;
+        const int dev = current_device(&sms);
+        const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+        if (!bit || !(allowed.load(std::memory_order_relaxed) & bit)) {
+            cudaFuncAttributes a;
+            cudaError_t e = cudaFuncGetAttributes(&a, KERNEL);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kMaxSmemPerCta - (int)a.sharedSizeBytes);
+            if (e != cudaSuccess) return cuda_status(e);
+            allowed.fetch_or(bit, std::memory_order_relaxed);
+        }
     }
-    kernel<<<grid, (unsigned)(p.tpr * p.rpb), smem, st>>>(p);
+    KERNEL<<<grid, (unsigned)(p.tpr * p.rpb), smem, st>>>(p);
     const int rc = cuda_status(cudaGetLastError());
     if (rc == AMSIM_OK) count_launch();
     return rc;
@@ -884,25 +901,25 @@ int launch_types(int nv, Loads loads, bool full, const Params &p, unsigned grid,
     const int threads = p.tpr * p.rpb;
 #define AMSIM_BN(...)                                                                             \
     do {                                                                                          \
-        if constexpr (BWD) return launch_kernel(bwd_kernel<__VA_ARGS__, X, Y, N>, p, grid, 0, st); \
-        else return launch_kernel(fwd_kernel<__VA_ARGS__, X, Y, N>, p, grid, 0, st);              \
+        if constexpr (BWD) return launch_kernel<bwd_kernel<__VA_ARGS__, X, Y, N>>(p, grid, 0, st); \
+        else return launch_kernel<fwd_kernel<__VA_ARGS__, X, Y, N>>(p, grid, 0, st);               \
     } while (0)
     const size_t rows_smem = (size_t)(BWD ? p.rpb : 1) * (kRingBarBytes + p.slots * p.slot_bytes);
     if constexpr (BWD) {
         const size_t smem = rows_smem + 8 * (size_t)kept_floats(p.cols) + (p.rpb > 1 ? kTeamThreads * sizeof(float4) : 0);
-        if (loads == kScalarRing) return launch_kernel(bwd_ring_kernel<false, false, true, X, Y, N>, p, grid, smem, st);
-        if (loads == kPieceRing) return launch_kernel(bwd_ring_kernel<true, false, true, X, Y, N>, p, grid, smem, st);
-        if (loads == kRing && full) return launch_kernel(bwd_ring_kernel<true, true, true, X, Y, N>, p, grid, smem, st);
-        if (loads == kRing) return launch_kernel(bwd_ring_kernel<true, true, false, X, Y, N>, p, grid, smem, st);
+        if (loads == kScalarRing) return launch_kernel<bwd_ring_kernel<false, false, true, X, Y, N>>(p, grid, smem, st);
+        if (loads == kPieceRing) return launch_kernel<bwd_ring_kernel<true, false, true, X, Y, N>>(p, grid, smem, st);
+        if (loads == kRing && full) return launch_kernel<bwd_ring_kernel<true, true, true, X, Y, N>>(p, grid, smem, st);
+        if (loads == kRing) return launch_kernel<bwd_ring_kernel<true, true, false, X, Y, N>>(p, grid, smem, st);
     } else {
         const size_t smem = rows_smem;
 #define AMSIM_RING(...)                                                                                        \
-    return threads > 256 ? launch_kernel(fwd_ring_kernel<512, __VA_ARGS__, true, X, Y, N>, p, grid, smem, st)  \
-                         : launch_kernel(fwd_ring_kernel<256, __VA_ARGS__, true, X, Y, N>, p, grid, smem, st)
+    return threads > 256 ? launch_kernel<fwd_ring_kernel<512, __VA_ARGS__, true, X, Y, N>>(p, grid, smem, st)  \
+                         : launch_kernel<fwd_ring_kernel<256, __VA_ARGS__, true, X, Y, N>>(p, grid, smem, st)
         if (loads == kScalarRing) AMSIM_RING(false, false);
         if (loads == kPieceRing) AMSIM_RING(true, false);
         if (loads == kRing && full) AMSIM_RING(true, true);
-        if (loads == kRing) return launch_kernel(fwd_ring_kernel<256, true, true, false, X, Y, N>, p, grid, smem, st);
+        if (loads == kRing) return launch_kernel<fwd_ring_kernel<256, true, true, false, X, Y, N>>(p, grid, smem, st);
 #undef AMSIM_RING
     }
     if (loads == kVector) {

@@ -62,3 +62,40 @@ def test_layer_on_an_empty_batch(amd):
     assert r.shape == n.shape == (0, 5, 24)
     (r.sum() + n.sum()).backward()
     assert not torch.stack([norm.gate.grad[0], norm.w_post.grad, norm.w_pre.grad]).any()
+
+
+def test_threads_with_different_widths(amd):
+    """Host threads that launch one kernel with different amounts of shared
+    memory at once: every call launches, and leaves what a call by itself does."""
+    import ctypes
+    import threading
+
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(0)
+    fn, start, failed = amd.lib().amsim_block_norm_fwd, threading.Barrier(8), []
+
+    def job(rows, cols):
+        x, y = (torch.randn((rows, cols), generator=g, device="cuda") for _ in range(2))
+        w = torch.ones(cols, device="cuda")
+        want = amd.block_norm(x, y, w, w)
+        out = [torch.zeros_like(t) for t in want]
+        d = amd.BlockNormDesc(rows=rows, cols=cols, alpha=1.0, eps=1e-6)
+        stream = torch.cuda.Stream()
+        args = [ctypes.byref(d)] + [t.data_ptr() if t is not None else None for t in (x, y, None, w, w, *out)]
+        args.append(stream.cuda_stream)
+
+        def run():
+            start.wait()
+            failed.extend(rc for rc in (fn(*args) for _ in range(4000)) if rc)
+        return run, want, out, (x, y, w, d, stream)
+    jobs = [job(rows, cols) for rows, cols in ((160, 4096), (320, 2048), (160, 3584), (320, 1800)) for _ in range(2)]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=j[0]) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, f"{len(failed)} calls failed: {sorted(set(failed))}"
+    for _, want, out, _ in jobs:
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
