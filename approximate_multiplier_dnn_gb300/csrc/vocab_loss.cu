@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
     }
     uint4 q[kGradSteps];
     float base[kGradSteps];
-    const float lse = p.lse[row];
+    const float lse = p.lse[row], none = lse - lse;   // 0; NaN in a row of NaN logits, whose codes tell nothing
 #pragma unroll
     for (int k = 0; k < kGradSteps; ++k) {
         const int col = col0 + k * kGradThreads * 8;
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
             const uint32_t bits = __byte_perm(c[j >> 1], 0x4B00u, j & 1 ? 0x5432 : 0x5410);
             const float code = __uint_as_float(bits) - 8388608.0f;
             // the last code stands for everything from 32 below the maximum on
-            g[j] = code == 65535.0f ? 0.0f : exp2_fast(fmaf(code, -kLog2e / kSteps, shift));
+            g[j] = code == 65535.0f ? none : exp2_fast(fmaf(code, -kLog2e / kSteps, shift));
         }
         const long long d = target - col;
         if (d >= 0 && d < 8) {

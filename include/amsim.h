@@ -624,7 +624,9 @@ size_t amsim_block_norm_workspace_size(const amsim_block_norm_desc *desc);
  * tokens that count (AMSIM_REDUCE_MEAN) or 1 (AMSIM_REDUCE_SUM).  A token
  * whose target is `ignore_index` does not count: row_loss 0, no gradient, and
  * with no token that counts the loss is 0.  Any other target outside
- * [0, vocab) makes row_loss and loss NaN and adds no gradient.
+ * [0, vocab) makes row_loss and loss NaN and adds no gradient.  A token that
+ * counts and whose logits hold a NaN or +infinity has a NaN row_loss, and NaN
+ * gradients as the formulas give them (its row of dh, and all of dw).
  * h: tokens x dim, w: vocab x dim, both bf16; products are exact, sums fp32.
  */
 enum amsim_reduction { AMSIM_REDUCE_MEAN = 0, AMSIM_REDUCE_SUM = 1 };

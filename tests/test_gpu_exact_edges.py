@@ -99,3 +99,28 @@ def test_threads_with_different_widths(amd):
     assert not failed, f"{len(failed)} calls failed: {sorted(set(failed))}"
     for _, want, out, _ in jobs:
         assert all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+def vocab_inputs(tokens, vocab, dim, seed=0):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    h = torch.randn((tokens, dim), generator=g).to(torch.bfloat16).cuda()
+    w = (torch.randn((vocab, dim), generator=g) * 2 / dim ** 0.5).to(torch.bfloat16).cuda()
+    return h, w, torch.randint(0, vocab, (tokens,), generator=g).cuda()
+
+
+@pytest.mark.parametrize("value", ["nan", "inf"])
+@pytest.mark.parametrize("tokens,vocab,dim", [(60, 500, 64), (300, 1000, 130)])
+def test_non_finite_hidden_state_gives_nan_gradients(amd, value, tokens, vocab, dim):
+    """A token that counts and has a non-finite hidden state has a NaN loss: its
+    gradient is NaN, and dw, to which it adds, not one that could be taken for
+    a token's."""
+    import torch
+    h, w, t = vocab_inputs(tokens, vocab, dim)
+    clean = amd.vocab_loss_grad(h, w, t)
+    h[7, 5] = float(value)
+    loss, row, lse, dh, dw = amd.vocab_loss_grad(h, w, t)
+    assert bool(torch.isnan(torch.stack([loss[0], row[7], lse[7]])).all())
+    assert bool(torch.isnan(dh[7]).all()) and bool(torch.isnan(dw).all())
+    keep = [i for i in range(tokens) if i != 7]
+    assert torch.equal(dh[keep], clean[3][keep]) and torch.equal(row[keep], clean[1][keep])
