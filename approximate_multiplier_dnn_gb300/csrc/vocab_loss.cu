@@ -606,6 +606,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
 // 4 bytes of traffic per element; the conversion of a code goes through the
 // mantissa of 2^23 + code, since the conversion instructions share the
 // exponential's unit, which alone needs 0.4 of the time of the bytes.
+// The blocks of a row also copy its hidden state, a slice each, for dW = G^T h,
+// with zeros where the weight is zero: a row of G that is zero would still make
+// NaN of a masked token's infinities.  (4 bytes per element of h: 4096 x 32768 x
+// 1024 takes 569 us instead of 559; with the copy in a block of its own per row
+// it took 596.)
 struct GradParams {
     uint16_t *codes;
     const float2 *stats;
@@ -613,6 +618,10 @@ struct GradParams {
     const int64_t *targets;
     long long ld;
     int rows, vocab;
+    const uint16_t *h;       // rows on 16 bytes
+    uint16_t *kept;
+    long long ld_h, ld_kept;
+    int dim, slice;          // of h; 16-byte words of it that a block copies
 };
 constexpr int kGradThreads = 256, kGradSteps = 4;
 constexpr int kGradCols = kGradThreads * 8 * kGradSteps;      // of a block
@@ -621,10 +630,25 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
     chain_start();
     chain_wait();
     const int row = blockIdx.y;
+    const float w = p.weight[row];
+    const uint16_t *from = p.h + row * p.ld_h;
+    uint16_t *to = p.kept + row * p.ld_kept;
+    const int word0 = (int)blockIdx.x * p.slice, words = min(p.slice, p.dim / 8 - word0);
+    uint4 kept = make_uint4(0, 0, 0, 0);       // loaded ahead of the codes, stored behind their loads
+    const bool keeps = (int)threadIdx.x < words;
+    if (keeps && w != 0.0f) kept = reinterpret_cast<const uint4 *>(from)[word0 + threadIdx.x];
+    auto keep = [&] {
+        if (keeps) reinterpret_cast<uint4 *>(to)[word0 + threadIdx.x] = kept;
+        for (int i = threadIdx.x + kGradThreads; i < words; i += kGradThreads)
+            reinterpret_cast<uint4 *>(to)[word0 + i] =
+                w != 0.0f ? reinterpret_cast<const uint4 *>(from)[word0 + i] : make_uint4(0, 0, 0, 0);
+        const int e = p.dim / 8 * 8 + threadIdx.x;         // the elements behind the last whole word
+        if (blockIdx.x == 0 && e < p.dim) to[e] = w != 0.0f ? from[e] : (uint16_t)0;
+    };
     const int col0 = (int)blockIdx.x * kGradCols + (int)threadIdx.x * 8;
     uint16_t *codes = p.codes + row * p.ld;
-    const float w = p.weight[row];
     if (w == 0.0f) {
+        keep();
 #pragma unroll
         for (int k = 0; k < kGradSteps; ++k)
             if (col0 + k * kGradThreads * 8 < p.vocab)
@@ -642,6 +666,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
             base[k] = p.stats[(long long)(col / kPiece) * p.rows + row].x;
         }
     }
+    keep();
     const long long target = p.targets[row];
 #pragma unroll
     for (int k = 0; k < kGradSteps; ++k) {
@@ -776,7 +801,7 @@ int device_sms()
 
 // Scratch of a call over chunks of `rows` tokens.
 struct Layout {
-    size_t totals, row_loss, lse, weight, target_logit, stats, codes, dw_acc, dh_acc, pack_h, pack_w, bytes;
+    size_t totals, row_loss, lse, weight, target_logit, stats, codes, kept, dw_acc, dh_acc, pack_h, pack_w, bytes;
     long long ld_codes, ld_pack, ld_acc, split_rows;
     int dh_splits;
 };
@@ -817,6 +842,7 @@ Layout layout(const amsim_vocab_loss_desc *d, bool grad, long long rows, bool pa
     l.dh_splits = 1;
     if (grad) {
         l.codes = take((size_t)rows * l.ld_codes * 2);
+        l.kept = take((size_t)rows * l.ld_pack * 2);
         if (rows < d->tokens) l.dw_acc = take((size_t)d->vocab * l.ld_acc * 4);
         l.dh_splits = dh_splits(rows, d, sms);
         if (l.dh_splits > 1) l.dh_acc = take((size_t)l.dh_splits * l.split_rows * l.ld_acc * 4);
@@ -977,9 +1003,12 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
                                    st, q));
         if (rc) return rc;
         if (!grad) continue;
-        GradParams e{codes, stats, q.lse, weight, targets + t0, l.ld_codes, (int)n, d->vocab};
-        rc = launched(chain_launch(true, grad_kernel, dim3((unsigned)((d->vocab + kGradCols - 1) / kGradCols), (unsigned)n),
-                                   kGradThreads, 0, st, e));
+        bf16 *kept = reinterpret_cast<bf16 *>(base + l.kept);
+        const int grad_blocks = (d->vocab + kGradCols - 1) / kGradCols;
+        GradParams e{codes, stats, q.lse, weight, targets + t0, l.ld_codes, (int)n, d->vocab,
+                     reinterpret_cast<const uint16_t *>(H.p + t0 * H.ld), reinterpret_cast<uint16_t *>(kept), H.ld,
+                     l.ld_pack, d->dim, (d->dim / 8 + grad_blocks - 1) / grad_blocks};
+        rc = launched(chain_launch(true, grad_kernel, dim3((unsigned)grad_blocks, (unsigned)n), kGradThreads, 0, st, e));
         if (rc) return rc;
         // dh = G W
         p = product(n, d->dim, d->vocab, l.dh_splits);
@@ -1029,7 +1058,7 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
             rc = matrix_map(&om, dw_acc, d->dim, d->vocab, l.ld_acc, 32, true);
         }
         if (rc || (rc = matrix_map(&am, g, d->vocab, n, l.ld_codes, kTileK)) ||
-            (rc = matrix_map(&bm, H.p + t0 * H.ld, d->dim, n, H.ld, kTileK)) ||
+            (rc = matrix_map(&bm, kept, d->dim, n, l.ld_pack, kTileK)) ||
             (rc = launch_product<kDw>(true, p, am, bm, om, sms, st)))
             return rc;
     }

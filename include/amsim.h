@@ -622,8 +622,8 @@ size_t amsim_block_norm_workspace_size(const amsim_block_norm_desc *desc);
  *   loss = sum_t a[t] row_loss[t] / A,
  * with a[t] the token's weight (row_weight[t], or 1), A = sum_t a[t] over the
  * tokens that count (AMSIM_REDUCE_MEAN) or 1 (AMSIM_REDUCE_SUM).  A token
- * whose target is `ignore_index` does not count: row_loss 0, no gradient, and
- * with no token that counts the loss is 0.  Any other target outside
+ * whose target is `ignore_index` does not count: row_loss 0 and no gradient,
+ * whatever its row of h holds, and with no token that counts the loss is 0.  Any other target outside
  * [0, vocab) makes row_loss and loss NaN and adds no gradient.  A token that
  * counts and whose logits hold a NaN or +infinity has a NaN row_loss, and NaN
  * gradients as the formulas give them (its row of dh, and all of dw).

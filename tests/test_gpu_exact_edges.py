@@ -124,3 +124,22 @@ def test_non_finite_hidden_state_gives_nan_gradients(amd, value, tokens, vocab, 
     assert bool(torch.isnan(dh[7]).all()) and bool(torch.isnan(dw).all())
     keep = [i for i in range(tokens) if i != 7]
     assert torch.equal(dh[keep], clean[3][keep]) and torch.equal(row[keep], clean[1][keep])
+
+
+@pytest.mark.parametrize("value", ["nan", "inf"])
+@pytest.mark.parametrize("tokens,vocab,dim", [(60, 500, 64), (300, 1000, 130), (1100, 700, 2100)])
+def test_ignored_tokens_add_nothing(amd, value, tokens, vocab, dim):
+    """Tokens without a target, or with one outside the vocabulary, add nothing
+    to dh and dw, whatever their hidden states hold (padding, say)."""
+    import torch
+    h, w, t = vocab_inputs(tokens, vocab, dim, seed=1)
+    t[3::5] = -100
+    t[11] = vocab
+    want = amd.vocab_loss_grad(h, w, t)
+    h[3::5, ::2] = float(value)
+    h[11] = float(value)
+    loss, row, lse, dh, dw = amd.vocab_loss_grad(h, w, t)
+    assert torch.equal(dh, want[3]) and torch.equal(dw, want[4])
+    assert not dh[3::5].any() and not dh[11].any() and bool(torch.isfinite(dw).all())
+    t[11] = -100
+    assert bool(torch.isfinite(amd.vocab_loss_grad(h, w, t)[0]).all())
