@@ -515,7 +515,8 @@ struct Sum {
     __device__ __forceinline__ void add(float x)
     {
         const float y = __fsub_rn(x, lost), t = __fadd_rn(s, y);
-        lost = __fsub_rn(__fsub_rn(t, s), y);
+        const float l = __fsub_rn(__fsub_rn(t, s), y);
+        lost = l == l ? l : 0.0f;          // an infinite sum stays infinite
         s = t;
     }
 };

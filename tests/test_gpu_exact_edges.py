@@ -143,3 +143,19 @@ def test_ignored_tokens_add_nothing(amd, value, tokens, vocab, dim):
     assert not dh[3::5].any() and not dh[11].any() and bool(torch.isfinite(dw).all())
     t[11] = -100
     assert bool(torch.isfinite(amd.vocab_loss_grad(h, w, t)[0]).all())
+
+
+@pytest.mark.parametrize("tokens", [1000, 5000])
+def test_infinite_row_loss_makes_the_loss_infinite(amd, tokens):
+    """A target with probability zero costs infinity, and so does the batch,
+    however many other tokens are added to it."""
+    import torch
+    h, w, t = vocab_inputs(tokens, 100, 16, seed=2)
+    h[:, 0] = 1.0
+    w[37, 0] = float("-inf")                                # no token can be 37
+    t[t == 37] = 36
+    assert bool(torch.isfinite(amd.vocab_loss(h, w, t)[0]))
+    t[5] = t[tokens - 7] = 37
+    loss, row, lse = amd.vocab_loss(h, w, t)
+    assert bool(torch.isposinf(row[5])) and bool(torch.isfinite(lse).all())
+    assert bool(torch.isposinf(loss))
