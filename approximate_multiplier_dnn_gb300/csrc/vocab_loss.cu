@@ -1098,5 +1098,7 @@ extern "C" size_t amsim_vocab_loss_workspace_min(const amsim_vocab_loss_desc *de
 {
     if (check(desc) || (which != 0 && which != 1) || desc->tokens == 0) return 0;
     const int sms = device_sms();
-    return layout(desc, which == 1, std::min<long long>(desc->tokens, kTileM), true, true, sms ? sms : 1).bytes;
+    // one chunk needs no sums of dw between chunks, and may need less than several
+    return std::min(layout(desc, which == 1, std::min<long long>(desc->tokens, kTileM), true, true, sms ? sms : 1).bytes,
+                    amsim_vocab_loss_workspace_size(desc, which));
 }
