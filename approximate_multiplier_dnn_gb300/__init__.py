@@ -187,6 +187,7 @@ def lib():
         "amsim_vocab_loss": ([ctypes.POINTER(VocabLossDesc)] + [vp] * 8 + [sz, vp], i32),
         "amsim_vocab_loss_grad": ([ctypes.POINTER(VocabLossDesc)] + [vp] * 10 + [sz, vp], i32),
         "amsim_vocab_loss_workspace_size": ([ctypes.POINTER(VocabLossDesc), i32], sz),
+        "amsim_vocab_loss_workspace_size_at": ([ctypes.POINTER(VocabLossDesc), i32, vp, vp], sz),
         "amsim_vocab_loss_workspace_min": ([ctypes.POINTER(VocabLossDesc), i32], sz),
         "amsim_adamw_step": ([i32, ctypes.POINTER(AdamwTensor), ctypes.POINTER(AdamwHyper), vp], i32),
         "amsim_adamw_moment_values": ([vp, vp, i32, i64, vp, vp], i32),
@@ -602,6 +603,10 @@ def amsim_vocab_loss_workspace_size(desc: VocabLossDesc, which: int) -> int:
     return int(lib().amsim_vocab_loss_workspace_size(ctypes.byref(desc), int(which)))
 
 
+def amsim_vocab_loss_workspace_size_at(desc: VocabLossDesc, which: int, h, w) -> int:
+    return int(lib().amsim_vocab_loss_workspace_size_at(ctypes.byref(desc), int(which), _ptr(h), _ptr(w)))
+
+
 def amsim_vocab_loss_workspace_min(desc: VocabLossDesc, which: int) -> int:
     return int(lib().amsim_vocab_loss_workspace_min(ctypes.byref(desc), int(which)))
 
@@ -687,11 +692,11 @@ def _block_norm_plan(rows, cols, gate_rows, x, y, n, r, dr, dn, alpha, eps, back
 
 
 @functools.lru_cache(maxsize=1024)
-def _vocab_plan(tokens, vocab, dim, ld_h, ld_w, ignore_index, reduction):
-    """(descriptor by reference, scratch bytes of the loss, of the gradients)."""
+def _vocab_plan(tokens, vocab, dim, ld_h, ld_w, ignore_index, reduction, h, w):
+    """(descriptor by reference, scratch bytes of the loss, of the gradients); h, w: addresses alike in their last bits."""
     d = VocabLossDesc(tokens=tokens, vocab=vocab, dim=dim, ld_h=ld_h, ld_w=ld_w, ignore_index=ignore_index,
                       reduction=REDUCTIONS[reduction])
-    return ctypes.byref(d), amsim_vocab_loss_workspace_size(d, 0), amsim_vocab_loss_workspace_size(d, 1)
+    return ctypes.byref(d), *(amsim_vocab_loss_workspace_size_at(d, which, h, w) for which in (0, 1))
 
 
 def _gate_rows(first, gate, w_post, w_pre):
@@ -781,7 +786,7 @@ def _vocab_call(h, w, targets, row_weight, ignore_index, reduction):
     vocab = w.shape[0]
     bf16 = torch.bfloat16
     plan = _vocab_plan(tokens, vocab, dim, _rows("h", h, tokens, dim, bf16), _rows("w", w, vocab, dim, bf16),
-                       ignore_index, reduction)
+                       ignore_index, reduction, 128 + h.data_ptr() % 128, 128 + w.data_ptr() % 128)
     _vector("targets", targets, tokens, torch.int64)
     if row_weight is not None:
         _vector("row_weight", row_weight, tokens, torch.float32)

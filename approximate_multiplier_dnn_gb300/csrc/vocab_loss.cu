@@ -1084,14 +1084,22 @@ extern "C" int amsim_vocab_loss_grad(const amsim_vocab_loss_desc *desc, const vo
                static_cast<cudaStream_t>(stream));
 }
 
-// Both sizes leave room for packed copies where a row stride asks for them (a
-// base address off 16 bytes is not in the descriptor: such a call packs too,
-// and the sizes cover it).
+// The sizes by the descriptor alone leave room for packed copies of h and w,
+// whose base addresses may be off 16 bytes.
 extern "C" size_t amsim_vocab_loss_workspace_size(const amsim_vocab_loss_desc *desc, int which)
 {
     if (check(desc) || (which != 0 && which != 1) || desc->tokens == 0) return 0;
     const int sms = device_sms();
     return layout(desc, which == 1, full_rows(desc), true, true, sms ? sms : 1).bytes;
+}
+
+extern "C" size_t amsim_vocab_loss_workspace_size_at(const amsim_vocab_loss_desc *desc, int which, const void *h,
+                                                     const void *w)
+{
+    if (check(desc) || (which != 0 && which != 1) || desc->tokens == 0) return 0;
+    const int sms = device_sms();
+    return layout(desc, which == 1, full_rows(desc), pack_h(h, desc->ld_h ? desc->ld_h : desc->dim, desc->tokens),
+                  !tma_rows(w, desc->ld_w ? desc->ld_w : desc->dim), sms ? sms : 1).bytes;
 }
 
 extern "C" size_t amsim_vocab_loss_workspace_min(const amsim_vocab_loss_desc *desc, int which)

@@ -664,9 +664,14 @@ int amsim_vocab_loss_grad(const amsim_vocab_loss_desc *desc, const void *h, cons
 /*
  * Bytes of scratch of the two calls (which: 0 the loss, 1 with gradients) for
  * the fastest plan (its exponentials capped at 4 GiB), and the least a call
- * runs with.  0 for an invalid descriptor.
+ * runs with.  0 for an invalid descriptor.  Operands whose rows are not on 16
+ * bytes are copied to scratch (h also for speed, where it is long and its rows
+ * are no whole 128-byte lines), and these sizes leave room for both copies:
+ * vocab x dim x 2 bytes for w.  The size at given addresses of h and w (which
+ * are not read) has room only for the copies that such a call makes.
  */
 size_t amsim_vocab_loss_workspace_size(const amsim_vocab_loss_desc *desc, int which);
+size_t amsim_vocab_loss_workspace_size_at(const amsim_vocab_loss_desc *desc, int which, const void *h, const void *w);
 size_t amsim_vocab_loss_workspace_min(const amsim_vocab_loss_desc *desc, int which);
 
 /*

@@ -159,3 +159,15 @@ def test_infinite_row_loss_makes_the_loss_infinite(amd, tokens):
     loss, row, lse = amd.vocab_loss(h, w, t)
     assert bool(torch.isposinf(row[5])) and bool(torch.isfinite(lse).all())
     assert bool(torch.isposinf(loss))
+
+
+def test_evaluation_scratch_is_small(amd):
+    """Aligned operands are not copied, and take no scratch for copies: the loss
+    alone needs far less than a copy of w."""
+    import torch
+    h, w, t = vocab_inputs(256, 65536, 512, seed=3)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    amd.vocab_loss(h, w, t)
+    assert torch.cuda.max_memory_allocated() - before < 4 << 20        # w: 64 MiB
