@@ -339,10 +339,8 @@ class BlockNorm(torch.nn.Module):
 class _VocabLossFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, w, targets, row_weight, ignore_index, reduction):
-        kw = dict(row_weight=row_weight, ignore_index=ignore_index, reduction=reduction)
-        if not (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
-            return vocab_loss(h, w, targets, **kw)[0][0]
-        loss, _, _, dh, dw = vocab_loss_grad(h, w, targets, **kw)   # the gradients for an upstream one of 1
+        loss, _, _, dh, dw = vocab_loss_grad(h, w, targets, row_weight=row_weight, ignore_index=ignore_index,
+                                             reduction=reduction)   # the gradients for an upstream one of 1
         ctx.save_for_backward(dh, dw)
         return loss[0]
 
@@ -357,7 +355,9 @@ def am_vocab_loss(h, w, targets, *, row_weight=None, ignore_index=-100, reductio
     """Cross entropy of softmax(h w^T) against the targets without keeping the
     logits, differentiable in h [tokens, dim] and w [vocab, dim] (both bf16).
     The gradients come with the loss, in the same pass, and backward scales
-    them."""
+    them; where none is wanted (evaluation), the loss is computed alone."""
+    if not (torch.is_grad_enabled() and (h.requires_grad or w.requires_grad)):
+        return vocab_loss(h, w, targets, row_weight=row_weight, ignore_index=ignore_index, reduction=reduction)[0][0]
     return _VocabLossFn.apply(h, w, targets, row_weight, ignore_index, reduction)
 
 

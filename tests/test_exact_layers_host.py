@@ -1,0 +1,54 @@
+"""Host logic of the exact layers and their optimizer (no GPU needed): the
+operators' calls are replaced by plain torch on the CPU, or recorded."""
+import pytest
+import torch
+
+import approximate_multiplier_dnn_gb300 as am
+from approximate_multiplier_dnn_gb300 import layers
+
+
+@pytest.fixture
+def losses(monkeypatch):
+    """The vocabulary loss in plain torch; the list of calls made."""
+    calls = []
+
+    def loss(h, w, targets, *, row_weight=None, ignore_index=-100, reduction="mean"):
+        calls.append("loss")
+        z = h.detach().float() @ w.detach().float().t()
+        row = torch.nn.functional.cross_entropy(z, targets, ignore_index=ignore_index, reduction="none")
+        lse = torch.logsumexp(z, 1)
+        return row.sum().reshape(1) / (targets != ignore_index).sum(), row, lse
+
+    def grad(h, w, targets, **kw):
+        out = loss(h, w, targets, **kw)
+        calls[-1] = "grad"
+        H, W = h.detach().float().requires_grad_(), w.detach().float().requires_grad_()
+        with torch.enable_grad():
+            z = torch.nn.functional.cross_entropy(H @ W.t(), targets, ignore_index=kw.get("ignore_index", -100))
+        dh, dw = torch.autograd.grad(z, (H, W))
+        return *out, dh.to(h.dtype), dw.to(w.dtype)
+    monkeypatch.setattr(layers, "vocab_loss", loss)
+    monkeypatch.setattr(layers, "vocab_loss_grad", grad)
+    return calls
+
+
+def head_inputs(seed=0):
+    g = torch.Generator().manual_seed(seed)
+    head = layers.VocabHead(16, 50, device="cpu", generator=g)
+    return head, torch.randn((3, 7, 16), generator=g).to(torch.bfloat16), torch.randint(0, 50, (3, 7), generator=g)
+
+
+def test_evaluation_computes_the_loss_alone(losses):
+    """No gradient is computed where none can be asked for: without grad mode,
+    whatever requires one, and where nothing does."""
+    head, h, t = head_inputs()
+    with torch.no_grad():
+        head(h, t)
+        head(h.requires_grad_(), t)
+    with torch.inference_mode():
+        head(h, t)
+    head.weight.requires_grad_(False)
+    head(h.detach(), t)
+    assert losses == ["loss"] * 4
+    head(h, t).backward()                              # a frozen head, hidden states that are trained
+    assert losses[4:] == ["grad"] and h.grad is not None and head.weight.grad is None

@@ -171,3 +171,17 @@ def test_evaluation_scratch_is_small(amd):
     torch.cuda.reset_peak_memory_stats()
     amd.vocab_loss(h, w, t)
     assert torch.cuda.max_memory_allocated() - before < 4 << 20        # w: 64 MiB
+
+
+def test_head_evaluation_launches_the_loss_alone(amd):
+    """Two kernels (the logits' product and the merge) and the same value."""
+    import torch
+    from approximate_multiplier_dnn_gb300.layers import VocabHead
+    h, _, t = vocab_inputs(64, 500, 64)
+    head = VocabHead(64, 500, generator=torch.Generator().manual_seed(0))
+    train = head(h, t).detach()
+    before = amd.amsim_kernel_launches()
+    with torch.no_grad():
+        loss = head(h, t)
+    assert amd.amsim_kernel_launches() - before == 2
+    assert torch.equal(loss, train) and not loss.requires_grad
