@@ -28,6 +28,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (ConvDesc, block_norm, block_norm_backward, vocab_loss, vocab_loss_grad, amsim_conv2d_bwd_data, amsim_conv2d_bwd_filter, amsim_conv2d_fwd, amsim_conv2d_out_hw,
                amsim_conv2d_workspace_size, amsim_dwconv2d_bwd_data, amsim_dwconv2d_bwd_filter, amsim_dwconv2d_fwd,
@@ -295,6 +296,7 @@ class _BlockNormFn(torch.autograd.Function):
         return r, n
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dr, dn):
         r, y, w_post, w_pre, gate, rstd_post, rstd_pre = ctx.saved_tensors
 
@@ -345,6 +347,7 @@ class _VocabLossFn(torch.autograd.Function):
         return loss[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         dh, dw = ctx.saved_tensors
         g = g.to(dh.dtype) if g.dim() == 0 else g

@@ -32,6 +32,27 @@ def losses(monkeypatch):
     return calls
 
 
+@pytest.fixture
+def norms(monkeypatch):
+    """The block norm without gate and weight gradients in plain torch; the
+    list of (dr, dn) that its backward was given."""
+    calls = []
+
+    def forward(x, y=None, w_post=None, w_pre=None, *, gate=None, alpha=1.0, eps=1e-6, n_dtype=None):
+        def rstd(t):
+            return torch.rsqrt(t.square().mean(1) + eps)
+        r = x if y is None else x + alpha * y * rstd(y)[:, None]
+        return r, r * rstd(r)[:, None], None if y is None else rstd(y), rstd(r)
+
+    def backward(dr, dn, r, y, w_post, w_pre, rstd_post, rstd_pre, *, gate=None, alpha=1.0):
+        calls.append((dr, dn))
+        return (torch.zeros_like(r), None if y is None else torch.zeros_like(y), None if gate is None else torch.zeros_like(gate),
+                None if w_post is None else torch.zeros_like(w_post), None if w_pre is None else torch.zeros_like(w_pre))
+    monkeypatch.setattr(layers, "block_norm", forward)
+    monkeypatch.setattr(layers, "block_norm_backward", backward)
+    return calls
+
+
 def head_inputs(seed=0):
     g = torch.Generator().manual_seed(seed)
     head = layers.VocabHead(16, 50, device="cpu", generator=g)
@@ -52,3 +73,17 @@ def test_evaluation_computes_the_loss_alone(losses):
     assert losses == ["loss"] * 4
     head(h, t).backward()                              # a frozen head, hidden states that are trained
     assert losses[4:] == ["grad"] and h.grad is not None and head.weight.grad is None
+
+
+def test_second_derivatives_are_refused(losses, norms):
+    """They would come out without the terms that pass through the kernels."""
+    head, h, t = head_inputs()
+    loss = head(h.requires_grad_(), t)
+    (dh,) = torch.autograd.grad(loss.square(), h, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dh.float().sum().backward()
+    x = torch.ones(4, 8, requires_grad=True)
+    r, n = layers.BlockNorm(8, device="cpu")(x, 2 * x)
+    (dx,) = torch.autograd.grad(n.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()
