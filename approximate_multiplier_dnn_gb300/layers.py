@@ -358,7 +358,10 @@ def am_vocab_loss(h, w, targets, *, row_weight=None, ignore_index=-100, reductio
     """Cross entropy of softmax(h w^T) against the targets without keeping the
     logits, differentiable in h [tokens, dim] and w [vocab, dim] (both bf16).
     The gradients come with the loss, in the same pass, and backward scales
-    them; where none is wanted (evaluation), the loss is computed alone."""
+    them; where none is wanted (evaluation), the loss is computed alone.
+    row_weight gets no gradient, so one that requires it is refused."""
+    if row_weight is not None and row_weight.requires_grad and torch.is_grad_enabled():
+        raise ValueError("the vocabulary loss has no gradient for row_weight: detach it")
     if not (torch.is_grad_enabled() and (h.requires_grad or w.requires_grad)):
         return vocab_loss(h, w, targets, row_weight=row_weight, ignore_index=ignore_index, reduction=reduction)[0][0]
     return _VocabLossFn.apply(h, w, targets, row_weight, ignore_index, reduction)

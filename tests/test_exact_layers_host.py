@@ -87,3 +87,15 @@ def test_second_derivatives_are_refused(losses, norms):
     (dx,) = torch.autograd.grad(n.square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         dx.sum().backward()
+
+
+def test_row_weight_that_requires_a_gradient_is_refused(losses):
+    """It would silently get none."""
+    head, h, t = head_inputs()
+    a = torch.ones(21, requires_grad=True)
+    with pytest.raises(ValueError):
+        head(h, t, row_weight=a)
+    with torch.no_grad():
+        head(h, t, row_weight=a)
+    head(h, t, row_weight=a.detach())
+    assert losses == ["loss", "grad"]
