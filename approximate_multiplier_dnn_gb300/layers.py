@@ -349,16 +349,17 @@ class _VocabLossFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, g):
+        def scaled(t):                   # fp32 products (a factor without dimensions would be rounded to bf16 first)
+            return torch.mul(t, g.reshape(1, 1), out=torch.empty_like(t))
         dh, dw = ctx.saved_tensors
-        g = g.to(dh.dtype) if g.dim() == 0 else g
-        return dh * g, dw * g, None, None, None, None
+        return scaled(dh), scaled(dw), None, None, None, None
 
 
 def am_vocab_loss(h, w, targets, *, row_weight=None, ignore_index=-100, reduction="mean"):
     """Cross entropy of softmax(h w^T) against the targets without keeping the
     logits, differentiable in h [tokens, dim] and w [vocab, dim] (both bf16).
     The gradients come with the loss, in the same pass, and backward scales
-    them; where none is wanted (evaluation), the loss is computed alone.
+    them by its fp32 factor, which rounds them to bf16 once more; where none is wanted (evaluation), the loss is computed alone.
     row_weight gets no gradient, so one that requires it is refused."""
     if row_weight is not None and row_weight.requires_grad and torch.is_grad_enabled():
         raise ValueError("the vocabulary loss has no gradient for row_weight: detach it")

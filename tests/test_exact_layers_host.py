@@ -99,3 +99,15 @@ def test_row_weight_that_requires_a_gradient_is_refused(losses):
         head(h, t, row_weight=a)
     head(h, t, row_weight=a.detach())
     assert losses == ["loss", "grad"]
+
+
+@pytest.mark.parametrize("factor", [1 / 3, 1e-3, 65537.0, 1.0])
+def test_upstream_factor_is_not_rounded(losses, factor):
+    """Gradients are scaled by the fp32 factor and rounded once: to the bit."""
+    head, h, t = head_inputs()
+    loss = head(h.requires_grad_(), t)
+    one = torch.autograd.grad(loss, (h, head.weight), retain_graph=True)
+    got = torch.autograd.grad(loss * factor, (h, head.weight))
+    for p, q in zip(got, one):
+        assert p.dtype == torch.bfloat16
+        assert torch.equal(p, (q.float() * torch.tensor(factor, dtype=torch.float32)).to(torch.bfloat16))

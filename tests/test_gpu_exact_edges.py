@@ -185,3 +185,18 @@ def test_head_evaluation_launches_the_loss_alone(amd):
         loss = head(h, t)
     assert amd.amsim_kernel_launches() - before == 2
     assert torch.equal(loss, train) and not loss.requires_grad
+
+
+@pytest.mark.parametrize("factor", [1 / 3, 0.01])
+def test_upstream_factor_is_not_rounded(amd, factor):
+    """Gradients of the head scaled by an fp32 factor that bf16 does not hold, to the bit."""
+    import torch
+    from approximate_multiplier_dnn_gb300.layers import VocabHead
+    h, _, t = vocab_inputs(100, 300, 40, seed=4)
+    head = VocabHead(40, 300, generator=torch.Generator().manual_seed(1))
+    loss = head(h.requires_grad_(), t)
+    _, _, _, dh, dw = amd.vocab_loss_grad(h.detach(), head.weight.detach(), t)
+    (loss * factor).backward()
+    f = torch.tensor(factor, dtype=torch.float32, device="cuda")
+    assert torch.equal(h.grad, (dh.float() * f).to(torch.bfloat16))
+    assert torch.equal(head.weight.grad, (dw.float() * f).to(torch.bfloat16))
