@@ -238,10 +238,10 @@ extern "C" int amsim_block_norm_fwd(const amsim_block_norm_desc *d, const void *
     const Shape s = shape(d->cols, vec);
     const RingShape ring = ring_shape(
         d->cols, amsim::bn::ring_bytes(d->cols, (int)xs, slack) + (y ? amsim::bn::ring_bytes(d->cols, (int)ys, slack) : 0), false);
-    const bool full = y && w_post && r && n && rstd_post && rstd_pre;
+    const amsim::bn::Has has = y && w_post && r && n && rstd_post && rstd_pre ? amsim::bn::kAll : amsim::bn::kSome;
     int64_t grid;
     amsim::bn::Loads loads = vec ? amsim::bn::kVector : amsim::bn::kScalar;
-    if (ring_pays(d->rows, ring, sms) && (full || (whole && ring.tpr <= 256))) {
+    if (ring_pays(d->rows, ring, sms) && (has == amsim::bn::kAll || (whole && ring.tpr <= 256))) {
         loads = whole ? amsim::bn::kRing : vec ? amsim::bn::kPieceRing : amsim::bn::kScalarRing;
         p.tpr = ring.tpr;
         p.rpb = 1;
@@ -257,8 +257,8 @@ extern "C" int amsim_block_norm_fwd(const amsim_block_norm_desc *d, const void *
     if (grid > 0x7FFFFFFF) return AMSIM_EINVAL;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return d->x_type == AMSIM_F32
-               ? amsim::bn::launch_fwd_f32(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)grid, st)
-               : amsim::bn::launch_fwd_bf16(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)grid, st);
+               ? amsim::bn::launch_fwd_f32(s.nv, loads, has, d->y_type, d->n_type, p, (unsigned)grid, st)
+               : amsim::bn::launch_fwd_bf16(s.nv, loads, has, d->y_type, d->n_type, p, (unsigned)grid, st);
 }
 
 extern "C" size_t amsim_block_norm_workspace_size(const amsim_block_norm_desc *d)
@@ -340,12 +340,13 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
     const RingShape ring =
         ring_shape(d->cols, (dr ? rx : 0) + (dn ? rx + amsim::bn::ring_bytes(d->cols, (int)ns, slack) : 0) +
                                 (y ? amsim::bn::ring_bytes(d->cols, (int)ys, slack) : 0), true);
-    const bool full = dr && dn && y && w_post && dx && dy;
+    const bool rest = dn && y && w_post && dx && dy;
+    const amsim::bn::Has has = !rest ? amsim::bn::kSome : dr ? amsim::bn::kAll : amsim::bn::kNoDr;
     int per_sm = direct_blocks(s);
     amsim::bn::Loads loads = vec ? amsim::bn::kVector : amsim::bn::kScalar;
     p.tpr = s.tpr;
     p.rpb = s.rpb;
-    if (ring_pays(d->rows, ring, sms) && (full || (whole && ring.tpr <= 256))) {
+    if (ring_pays(d->rows, ring, sms)) {
         loads = whole ? amsim::bn::kRing : vec ? amsim::bn::kPieceRing : amsim::bn::kScalarRing;
         p.tpr = ring.tpr;
         p.rpb = ring.at_work;
@@ -371,8 +372,8 @@ extern "C" int amsim_block_norm_bwd(const amsim_block_norm_desc *d, const void *
         p.part_pre = dw_pre;
     }
     rc = d->x_type == AMSIM_F32
-             ? amsim::bn::launch_bwd_f32(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)h.blocks, st)
-             : amsim::bn::launch_bwd_bf16(s.nv, loads, full, d->y_type, d->n_type, p, (unsigned)h.blocks, st);
+             ? amsim::bn::launch_bwd_f32(s.nv, loads, has, d->y_type, d->n_type, p, (unsigned)h.blocks, st)
+             : amsim::bn::launch_bwd_bf16(s.nv, loads, has, d->y_type, d->n_type, p, (unsigned)h.blocks, st);
     if (rc || !sums || direct) return rc;
     rc = amsim::cuda_status(amsim::chain_launch(true, sums_kernel, dim3((unsigned)((d->cols + 31) / 32), 2),
                                                 kSumWarps * 32, 0, st, p, h.blocks));

@@ -203,31 +203,34 @@ __device__ __forceinline__ void row_sums(Sums<S> &x, int warps, float (*red)[S][
         for (int i = 0; i < S; ++i) x.v[i] += __shfl_xor_sync(0xFFFFFFFFu, x.v[i], d);
 }
 
-// The parts of a call.  Kernels built for FULL calls (every part there) test
-// none of them.
-template <bool FULL>
+// The parts of a call.  Kernels built for calls with every part (kAll), or with
+// every part but dr (kNoDr: the last norm of a model, whose r is not used), test
+// none of them.  (Backward without dr: 5395 x 3047 bf16 78 us with zeros in its
+// place, 96 with the tests, 62 so; 16384 x 4096 190, 168, 115.)
+enum Has { kSome, kAll, kNoDr };
+template <int HAS>
 struct Parts {
     const Params &p;
-    __device__ __forceinline__ bool y() const { return FULL || p.y; }
-    __device__ __forceinline__ bool post() const { return FULL || p.w_post; }
-    __device__ __forceinline__ bool r() const { return FULL || p.r; }
-    __device__ __forceinline__ bool n() const { return FULL || p.n; }
-    __device__ __forceinline__ bool dr() const { return FULL || p.dr; }
-    __device__ __forceinline__ bool dn() const { return FULL || p.dn; }
-    __device__ __forceinline__ bool dx() const { return FULL || p.dx; }
-    __device__ __forceinline__ bool dy() const { return FULL || p.dy; }
+    __device__ __forceinline__ bool y() const { return HAS || p.y; }
+    __device__ __forceinline__ bool post() const { return HAS || p.w_post; }
+    __device__ __forceinline__ bool r() const { return HAS || p.r; }
+    __device__ __forceinline__ bool n() const { return HAS || p.n; }
+    __device__ __forceinline__ bool dr() const { return HAS == kAll || (HAS == kSome && p.dr); }
+    __device__ __forceinline__ bool dn() const { return HAS || p.dn; }
+    __device__ __forceinline__ bool dx() const { return HAS || p.dx; }
+    __device__ __forceinline__ bool dy() const { return HAS || p.dy; }
 };
 
 // ------------------------------------------------------------------ one row
 // Forward.  `xr`, `yr`: the thread's words of the row; `wu(k)`: alpha gate
 // w_post, `wq(k)`: w_pre; `met(barrier)` runs after the first sum (or where it
 // would be), `barrier` telling whether every thread was waited for there.
-template <int NV, bool VEC, bool FULL, typename X, typename Y, typename N, typename WU, typename WQ, typename F>
+template <int NV, bool VEC, int HAS, typename X, typename Y, typename N, typename WU, typename WQ, typename F>
 __device__ __forceinline__ void fwd_row(const Params &p, const Raw<X> (&xr)[NV], const Raw<Y> (&yr)[NV], X *ro, N *no,
                                         long long row, bool on, int t, int cols, int warps, float (*red)[1][32],
                                         int &which, WU wu, WQ wq, F met)
 {
-    const Parts<FULL> has{p};
+    const Parts<HAS> has{p};
     const float inv = 1.0f / (float)p.cols;
     float post = 1.0f;
     if (has.post()) {
@@ -241,7 +244,7 @@ __device__ __forceinline__ void fwd_row(const Params &p, const Raw<X> (&xr)[NV],
         Sums<1> s{{s2.x + s2.y}};
         row_sums(s, warps, red, which, [] { __syncthreads(); });
         post = rsqrtf(fmaf(s.v[0], inv, p.eps));
-        if (on && t == 0 && (FULL || p.rstd_post)) p.rstd_post[row] = post;
+        if (on && t == 0 && (HAS || p.rstd_post)) p.rstd_post[row] = post;
     }
     met(has.post() && warps > 1);
     Four r[NV];
@@ -262,7 +265,7 @@ __device__ __forceinline__ void fwd_row(const Params &p, const Raw<X> (&xr)[NV],
     Sums<1> s{{s2.x + s2.y}};
     row_sums(s, warps, red, which, [] { __syncthreads(); });
     const float pre = rsqrtf(fmaf(s.v[0], inv, p.eps));
-    if (on && t == 0 && (FULL || p.rstd_pre)) p.rstd_pre[row] = pre;
+    if (on && t == 0 && (HAS || p.rstd_pre)) p.rstd_pre[row] = pre;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const Four w = wq(k);
@@ -289,13 +292,13 @@ struct Step {
 // L1 cache; with KEEP, narrow or unaligned rows, it keeps them too): the rest of
 // its registers are the column sums', two per channel.  Keeping bf16 rows in
 // the streaming kernel freed their slot a row earlier and was 8 % slower.
-template <int NV, bool VEC, bool FULL, bool KEEP, typename X, typename Y, typename N, typename LOAD, typename WQ,
+template <int NV, bool VEC, int HAS, bool KEEP, typename X, typename Y, typename N, typename LOAD, typename WQ,
           typename WU, typename SYNC, typename F>
 __device__ __forceinline__ void bwd_row(const Params &p, float pre, float post, X *dxo, Y *dyo, int t, int cols,
                                         int warps, float (*red)[3][32], int &which, float2 (&a)[NV * kP],
                                         float2 (&b)[NV * kP], LOAD load, WQ wq, WU wu, SYNC sync, F met)
 {
-    const Parts<FULL> has{p};
+    const Parts<HAS> has{p};
     const float inv = 1.0f / (float)p.cols;
     Four q[NV];
     Step<X, Y, N> in[KEEP ? NV : 1];
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(const Params p)
         for (int k = 0; k < NV; ++k)
             load_raw<VEC, Y>(yr[k], static_cast<const Y *>(p.y) + row * p.ldy, k, t, p.tpr, cols);
     const float *gate = p.gate && on ? p.gate + row / p.gate_rows * p.cols : nullptr;
-    fwd_row<NV, VEC, false, X, Y, N>(
+    fwd_row<NV, VEC, kSome, X, Y, N>(
         p, xr, yr, static_cast<X *>(p.r) + row * p.ldr, static_cast<N *>(p.n) + row * p.ldn, row, on, t, cols, warps,
         red, which, [&](int k) { return weights_u<VEC>(p, gate, k, t, cols); },
         [&](int k) { return weights<VEC>(p.w_pre, k, t, p.tpr, cols); }, [](bool) {});
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
             const int cols = on ? p.cols : 0;
             const float pre = want_n && on ? p.rstd_pre[row] : 0.0f;
             const float post = !want_y || !p.w_post ? 1.0f : on ? p.rstd_post[row] : 0.0f;
-            bwd_row<NV, VEC, false, NV <= 2 || !VEC, X, Y, N>(
+            bwd_row<NV, VEC, kSome, NV <= 2 || !VEC, X, Y, N>(
                 p, pre, post, static_cast<X *>(p.dx) + row * p.lddx, static_cast<Y *>(p.dy) + row * p.lddy, t, cols,
                 warps, red, which, a, b,
                 [&](int k, bool first) {
@@ -616,13 +619,13 @@ __device__ __forceinline__ Four kept(const float *w, int k, int t, int tpr, int 
     return widen(d);
 }
 
-template <int THREADS, bool VEC, bool WHOLE, bool FULL, typename X, typename Y, typename N>
+template <int THREADS, bool VEC, bool WHOLE, int HAS, typename X, typename Y, typename N>
 __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kernel(const Params p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][1][32];
     constexpr int NV = kRingNV;
-    const Parts<FULL> has{p};
+    const Parts<HAS> has{p};
     int which = 0;
     const int t = threadIdx.x, warps = p.tpr >> 5, cols = p.cols;
     const int bytes_x = cols * (int)sizeof(X), bytes_y = cols * (int)sizeof(Y);
@@ -633,8 +636,9 @@ __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kern
         uint8_t *s = ring.slot0 + slot * ring.bytes;
         uint64_t *full = ring.full + slot;
         const Pieces x = row_to<WHOLE, X>(s, p.x, p.ldx, row, p.rows, bytes_x);
-        const Pieces y = row_to<WHOLE, Y>(s + yoff, p.y, p.ldy, row, p.rows, bytes_y);
-        tc::bar_expect(full, x.bytes + (has.y() ? y.bytes : 0));
+        Pieces y{};
+        if (has.y()) y = row_to<WHOLE, Y>(s + yoff, p.y, p.ldy, row, p.rows, bytes_y);
+        tc::bar_expect(full, x.bytes + y.bytes);
         copy_pieces(s, x, full);
         if (has.y()) copy_pieces(s + yoff, y, full);
     };
@@ -664,7 +668,7 @@ __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kern
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 load_raw<VEC, Y>(yr[k], in_slot<WHOLE, Y>(slot + yoff, p.y, p.ldy, row), k, t, p.tpr, cols);
-        fwd_row<NV, VEC, FULL, X, Y, N>(
+        fwd_row<NV, VEC, HAS, X, Y, N>(
             p, xr, yr, ro, no, row, true, t, cols, warps, red, which,
             [&](int k) { return wu[k]; }, [&](int k) { return wq[k]; },
             [&](bool barrier) {
@@ -679,13 +683,13 @@ __global__ void __launch_bounds__(THREADS, kRingThreads / THREADS) fwd_ring_kern
 // with a ring of its own.  They share the weights, which wait in shared memory
 // (w_pre, then alpha gate w_post of the share's gate): a block per row would
 // hold a copy each, and leave room for one row ahead where teams have two.
-template <bool VEC, bool WHOLE, bool FULL, typename X, typename Y, typename N>
+template <bool VEC, bool WHOLE, int HAS, typename X, typename Y, typename N>
 __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][3][32];
     constexpr int NV = kRingNV;
-    const Parts<FULL> has{p};
+    const Parts<HAS> has{p};
     int which = 0;
     const int teams = p.rpb, team = threadIdx.x / p.tpr, t = threadIdx.x - team * p.tpr;
     const int warps = p.tpr >> 5, cols = p.cols;
@@ -723,18 +727,20 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
     auto issue_first = [&](long long row, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
         uint64_t *full = ring.full + slot;
-        const Pieces dr = row_to<WHOLE, X>(s, p.dr, p.lddr, row, p.rows, bytes_x);
-        const Pieces dn = row_to<WHOLE, N>(s + off_n, p.dn, p.lddn, row, p.rows, bytes_n);
-        tc::bar_expect(full, (has.dr() ? dr.bytes : 0) + (has.dn() ? dn.bytes : 0));
+        Pieces dr{}, dn{};
+        if (has.dr()) dr = row_to<WHOLE, X>(s, p.dr, p.lddr, row, p.rows, bytes_x);
+        if (has.dn()) dn = row_to<WHOLE, N>(s + off_n, p.dn, p.lddn, row, p.rows, bytes_n);
+        tc::bar_expect(full, dr.bytes + dn.bytes);
         if (has.dr()) copy_pieces(s, dr, full);
         if (has.dn()) copy_pieces(s + off_n, dn, full);
     };
     auto issue_second = [&](long long row, int slot) {
         uint8_t *s = ring.slot0 + slot * ring.bytes;
         uint64_t *full = ring.full + ring.slots + slot;
-        const Pieces r = row_to<WHOLE, X>(s + off_r, p.rin, p.ldr, row, p.rows, bytes_x);
-        const Pieces y = row_to<WHOLE, Y>(s + off_y, p.y, p.ldy, row, p.rows, bytes_y);
-        tc::bar_expect(full, (has.dn() ? r.bytes : 0) + (has.y() ? y.bytes : 0));
+        Pieces r{}, y{};
+        if (has.dn()) r = row_to<WHOLE, X>(s + off_r, p.rin, p.ldr, row, p.rows, bytes_x);
+        if (has.y()) y = row_to<WHOLE, Y>(s + off_y, p.y, p.ldy, row, p.rows, bytes_y);
+        tc::bar_expect(full, r.bytes + y.bytes);
         if (has.dn()) copy_pieces(s + off_r, r, full);
         if (has.y()) copy_pieces(s + off_y, y, full);
     };
@@ -797,7 +803,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) bwd_ring_kernel(const Params 
             next_pre = pre_of(row + teams);
             next_post = post_of(row + teams);
             const uint8_t *slot = ring.wait();
-            bwd_row<NV, VEC, FULL, false, X, Y, N>(
+            bwd_row<NV, VEC, HAS, false, X, Y, N>(
                 p, pre, post, dxo, dyo, t, cols, warps, red, which, a, b,
                 [&](int k, bool first) {
                     Step<X, Y, N> in;
@@ -862,10 +868,10 @@ enum Loads { kScalar, kVector, kRing, kPieceRing, kScalarRing };
 
 // One translation unit per direction and type of the residual stream builds
 // its instances.
-int launch_fwd_f32(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
-int launch_fwd_bf16(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
-int launch_bwd_f32(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
-int launch_bwd_bf16(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
+int launch_fwd_f32(int nv, Loads loads, Has has, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
+int launch_fwd_bf16(int nv, Loads loads, Has has, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
+int launch_bwd_f32(int nv, Loads loads, Has has, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
+int launch_bwd_bf16(int nv, Loads loads, Has has, int y_type, int n_type, const Params &p, unsigned grid, cudaStream_t st);
 
 // The kernel is a template argument, so that `allowed` is its own: the devices
 // on which it may have all the shared memory there is.  (A limit set to each
@@ -896,7 +902,7 @@ int launch_kernel(const Params &p, unsigned grid, size_t smem, cudaStream_t st)
 }
 
 template <bool BWD, typename X, typename Y, typename N>
-int launch_types(int nv, Loads loads, bool full, const Params &p, unsigned grid, cudaStream_t st)
+int launch_types(int nv, Loads loads, Has has, const Params &p, unsigned grid, cudaStream_t st)
 {
     const int threads = p.tpr * p.rpb;
 #define AMSIM_BN(...)                                                                             \
@@ -907,19 +913,23 @@ int launch_types(int nv, Loads loads, bool full, const Params &p, unsigned grid,
     const size_t rows_smem = (size_t)(BWD ? p.rpb : 1) * (kRingBarBytes + p.slots * p.slot_bytes);
     if constexpr (BWD) {
         const size_t smem = rows_smem + 8 * (size_t)kept_floats(p.cols) + (p.rpb > 1 ? kTeamThreads * sizeof(float4) : 0);
-        if (loads == kScalarRing) return launch_kernel<bwd_ring_kernel<false, false, true, X, Y, N>>(p, grid, smem, st);
-        if (loads == kPieceRing) return launch_kernel<bwd_ring_kernel<true, false, true, X, Y, N>>(p, grid, smem, st);
-        if (loads == kRing && full) return launch_kernel<bwd_ring_kernel<true, true, true, X, Y, N>>(p, grid, smem, st);
-        if (loads == kRing) return launch_kernel<bwd_ring_kernel<true, true, false, X, Y, N>>(p, grid, smem, st);
+#define AMSIM_RING(...)                                                                                  \
+    return has == kAll    ? launch_kernel<bwd_ring_kernel<__VA_ARGS__, kAll, X, Y, N>>(p, grid, smem, st)  \
+           : has == kNoDr ? launch_kernel<bwd_ring_kernel<__VA_ARGS__, kNoDr, X, Y, N>>(p, grid, smem, st) \
+                          : launch_kernel<bwd_ring_kernel<__VA_ARGS__, kSome, X, Y, N>>(p, grid, smem, st)
+        if (loads == kScalarRing) AMSIM_RING(false, false);
+        if (loads == kPieceRing) AMSIM_RING(true, false);
+        if (loads == kRing) AMSIM_RING(true, true);
+#undef AMSIM_RING
     } else {
         const size_t smem = rows_smem;
 #define AMSIM_RING(...)                                                                                        \
-    return threads > 256 ? launch_kernel<fwd_ring_kernel<512, __VA_ARGS__, true, X, Y, N>>(p, grid, smem, st)  \
-                         : launch_kernel<fwd_ring_kernel<256, __VA_ARGS__, true, X, Y, N>>(p, grid, smem, st)
+    return threads > 256 ? launch_kernel<fwd_ring_kernel<512, __VA_ARGS__, kAll, X, Y, N>>(p, grid, smem, st)  \
+                         : launch_kernel<fwd_ring_kernel<256, __VA_ARGS__, kAll, X, Y, N>>(p, grid, smem, st)
         if (loads == kScalarRing) AMSIM_RING(false, false);
         if (loads == kPieceRing) AMSIM_RING(true, false);
-        if (loads == kRing && full) AMSIM_RING(true, true);
-        if (loads == kRing) return launch_kernel<fwd_ring_kernel<256, true, true, false, X, Y, N>>(p, grid, smem, st);
+        if (loads == kRing && has == kAll) AMSIM_RING(true, true);
+        if (loads == kRing) return launch_kernel<fwd_ring_kernel<256, true, true, kSome, X, Y, N>>(p, grid, smem, st);
 #undef AMSIM_RING
     }
     if (loads == kVector) {
@@ -935,14 +945,14 @@ int launch_types(int nv, Loads loads, bool full, const Params &p, unsigned grid,
 }
 
 template <bool BWD, typename X>
-int launch_stream(int nv, Loads loads, bool full, int y_type, int n_type, const Params &p, unsigned grid,
+int launch_stream(int nv, Loads loads, Has has, int y_type, int n_type, const Params &p, unsigned grid,
                   cudaStream_t st)
 {
     if (y_type == AMSIM_F32)
-        return n_type == AMSIM_F32 ? launch_types<BWD, X, float, float>(nv, loads, full, p, grid, st)
-                                   : launch_types<BWD, X, float, bf16>(nv, loads, full, p, grid, st);
-    return n_type == AMSIM_F32 ? launch_types<BWD, X, bf16, float>(nv, loads, full, p, grid, st)
-                               : launch_types<BWD, X, bf16, bf16>(nv, loads, full, p, grid, st);
+        return n_type == AMSIM_F32 ? launch_types<BWD, X, float, float>(nv, loads, has, p, grid, st)
+                                   : launch_types<BWD, X, float, bf16>(nv, loads, has, p, grid, st);
+    return n_type == AMSIM_F32 ? launch_types<BWD, X, bf16, float>(nv, loads, has, p, grid, st)
+                               : launch_types<BWD, X, bf16, bf16>(nv, loads, has, p, grid, st);
 }
 
 }  // namespace bn

@@ -290,6 +290,7 @@ class _BlockNormFn(torch.autograd.Function):
     def forward(ctx, x, y, w_post, w_pre, gate, alpha, eps, n_dtype):
         r, n, rstd_post, rstd_pre = block_norm(x, y, w_post, w_pre, gate=gate, alpha=alpha, eps=eps, n_dtype=n_dtype)
         ctx.save_for_backward(r, y, w_post, w_pre, gate, rstd_post, rstd_pre)
+        ctx.set_materialize_grads(False)     # an output that is not used has no gradient to read
         ctx.alpha = alpha
         if r is x:                       # no block output yet: x passes through
             r = x.view_as(x)

@@ -111,3 +111,13 @@ def test_upstream_factor_is_not_rounded(losses, factor):
     for p, q in zip(got, one):
         assert p.dtype == torch.bfloat16
         assert torch.equal(p, (q.float() * torch.tensor(factor, dtype=torch.float32)).to(torch.bfloat16))
+
+
+def test_unused_outputs_have_no_gradient(norms):
+    """The gradient of an output that is not used is no tensor of zeros."""
+    norm = layers.BlockNorm(8, device="cpu")
+    x, y = torch.randn(4, 8, requires_grad=True), torch.randn(4, 8)
+    norm(x, y)[1].sum().backward()
+    norm(x, y)[0].sum().backward()
+    sum(t.sum() for t in norm(x, y)).backward()
+    assert [(dr is None, dn is None) for dr, dn in norms] == [(True, False), (False, True), (False, False)]

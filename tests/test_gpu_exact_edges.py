@@ -200,3 +200,53 @@ def test_upstream_factor_is_not_rounded(amd, factor):
     f = torch.tensor(factor, dtype=torch.float32, device="cuda")
     assert torch.equal(h.grad, (dh.float() * f).to(torch.bfloat16))
     assert torch.equal(head.weight.grad, (dw.float() * f).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("used", ["r", "n"])
+@pytest.mark.parametrize("first", [False, True])
+def test_layer_with_an_unused_output(amd, used, first):
+    """Gradients through one output of BlockNorm are those with zeros for the
+    other's, to the bit."""
+    import torch
+    from approximate_multiplier_dnn_gb300.layers import BlockNorm
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, y, c = (torch.randn((30, 48), generator=g, device="cuda") for _ in range(3))
+    norm = BlockNorm(48, gate=None if first else "channel")
+    leaves = [x.requires_grad_(), *([] if first else [y.requires_grad_()]), *norm.parameters()]
+    out = norm(x) if first else norm(x, y)
+    got = torch.autograd.grad((out[used == "n"] * c).sum(), leaves, allow_unused=True)
+    out = norm(x) if first else norm(x, y)
+    want = torch.autograd.grad((out[used == "n"] * c).sum() + (out[used == "r"] * 0).sum(), leaves, allow_unused=True)
+    for p, q in zip(got, want):
+        assert (p is None) == (q is None) and (p is None or torch.equal(p, q))
+
+
+@pytest.mark.parametrize("drop", ["dr", "dn"])
+@pytest.mark.parametrize("rows,cols", [(2600, 512), (640, 3047), (308, 8191), (308, 8192), (2440, 1013), (2440, 1012)])
+@pytest.mark.parametrize("x,n", [("float32", "float32"), ("bfloat16", "bfloat16"), ("float32", "bfloat16")])
+def test_streamed_backward_without_a_gradient(amd, drop, rows, cols, x, n):
+    """A gradient that is not there is one of zeros: dx and dy to the bit, the
+    sums over rows up to the order of their terms (two sums of R terms, each
+    within R + 64 u of the sum of magnitudes); without y as well."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    X, N = getattr(torch, x), getattr(torch, n)
+    a, y, dr, dn = (torch.randn((rows, cols), generator=g, device="cuda").to(t) for t in (X, N, X, N))
+    w, v = (1 + 0.1 * torch.randn(cols, generator=g, device="cuda") for _ in range(2))
+    gate = torch.rand((2, cols), generator=g, device="cuda")
+    r, _, post, pre = amd.block_norm(a, y, w, v, gate=gate, n_dtype=N)
+    want = amd.block_norm_backward(dr * (drop != "dr"), dn * (drop != "dn"), r, y, w, v, post, pre, gate=gate)
+    got = amd.block_norm_backward(None if drop == "dr" else dr, None if drop == "dn" else dn, r, y, w, v, post, pre,
+                                  gate=gate)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    yh, rh = (y.double() * post[:, None]).abs(), (r.double() * pre[:, None]).abs()
+    u = got[0].double().abs() * yh * 1.01                    # dx as the sums take it, before its rounding
+    mags = [(u * w).view(2, rows // 2, cols).sum(1), (u.view(2, rows // 2, cols) * gate[:, None]).sum((0, 1)),
+            (dn.double().abs() * rh).sum(0)]
+    for p, q, mag in zip(got[2:], want[2:], mags):
+        assert bool(((p.double() - q.double()).abs() <= 2 * (rows + 64) * 2.0 ** -24 * mag).all())
+    if drop == "dr":                                          # neither y nor a gradient of r
+        dx, _, _, _, dw = amd.block_norm_backward(None, dn, r, None, None, v, None, pre)
+        assert torch.equal(dx, want[0])
+        assert bool(((dw.double() - want[4].double()).abs() <= 2 * (rows + 64) * 2.0 ** -24 * mags[2]).all())
+    assert amd.amsim_device_errors() == (amd.AMSIM_OK, 0)
