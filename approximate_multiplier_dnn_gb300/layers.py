@@ -285,6 +285,13 @@ class AMAttention(torch.nn.Module):
 
 
 # ------------------------------------------------------------------ exact: block norm
+def _dense_rows(t: torch.Tensor) -> torch.Tensor:
+    """A matrix whose rows are contiguous and do not overlap: t, or a copy (of a transposed or expanded one)."""
+    if t.dim() != 2 or t.is_contiguous() or (t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
+        return t
+    return t.contiguous()
+
+
 class _BlockNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y, w_post, w_pre, gate, alpha, eps, n_dtype):
@@ -329,11 +336,11 @@ class BlockNorm(torch.nn.Module):
 
     def forward(self, x, y=None, gate=None):
         shape = x.shape
-        rows = x.reshape(-1, shape[-1])
+        rows = _dense_rows(x.reshape(-1, shape[-1]))
         if y is None:
             r, n = _BlockNormFn.apply(rows, None, None, self.w_pre, None, self.alpha, self.eps, self.n_dtype)
         else:
-            r, n = _BlockNormFn.apply(rows, y.reshape(rows.shape), self.w_post, self.w_pre,
+            r, n = _BlockNormFn.apply(rows, _dense_rows(y.reshape(rows.shape)), self.w_post, self.w_pre,
                                       self.gate if gate is None else gate, self.alpha, self.eps, self.n_dtype)
         return r.reshape(shape), n.reshape(shape)
 
@@ -364,6 +371,8 @@ def am_vocab_loss(h, w, targets, *, row_weight=None, ignore_index=-100, reductio
     row_weight gets no gradient, so one that requires it is refused."""
     if row_weight is not None and row_weight.requires_grad and torch.is_grad_enabled():
         raise ValueError("the vocabulary loss has no gradient for row_weight: detach it")
+    h, w, targets = _dense_rows(h), _dense_rows(w), targets.contiguous()
+    row_weight = None if row_weight is None else row_weight.contiguous()
     if not (torch.is_grad_enabled() and (h.requires_grad or w.requires_grad)):
         return vocab_loss(h, w, targets, row_weight=row_weight, ignore_index=ignore_index, reduction=reduction)[0][0]
     return _VocabLossFn.apply(h, w, targets, row_weight, ignore_index, reduction)

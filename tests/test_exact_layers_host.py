@@ -121,3 +121,34 @@ def test_unused_outputs_have_no_gradient(norms):
     norm(x, y)[0].sum().backward()
     sum(t.sum() for t in norm(x, y)).backward()
     assert [(dr is None, dn is None) for dr, dn in norms] == [(True, False), (False, True), (False, False)]
+
+
+def dense(t):
+    return t.is_contiguous() or (t.stride(1) == 1 and t.stride(0) >= t.shape[1])
+
+
+def test_layers_take_any_layout(monkeypatch):
+    """Transposed, expanded and strided inputs reach the operators as rows that
+    they take (others are refused there)."""
+    seen = []
+
+    def norm(x, y=None, *a, **kw):
+        assert dense(x) and (y is None or dense(y))
+        seen.append("norm")
+        return (x if y is None else x + y), x.clone(), None, x[:, 0]
+
+    def loss(h, w, targets, *, row_weight=None, **kw):
+        assert dense(h) and dense(w) and targets.is_contiguous() and row_weight.is_contiguous()
+        seen.append("loss")
+        return torch.zeros(1), None, None
+    monkeypatch.setattr(layers, "block_norm", norm)
+    monkeypatch.setattr(layers, "vocab_loss", loss)
+    block = layers.BlockNorm(6, device="cpu")
+    block(torch.ones(6, 9).t(), torch.ones(6).expand(9, 6))
+    block(torch.ones(1, 6).expand(4, 6))
+    wide = torch.ones(9, 20)[:, 3:9]
+    assert block(wide)[0].data_ptr() == wide.data_ptr()                  # a stride of rows is no reason to copy
+    with torch.no_grad():
+        layers.am_vocab_loss(torch.ones(6, 9).t(), torch.ones(6, 5).t(), torch.zeros(18, dtype=torch.int64)[::2],
+                             row_weight=torch.ones(9, 2)[:, 0])
+    assert seen == ["norm"] * 3 + ["loss"]
