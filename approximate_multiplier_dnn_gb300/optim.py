@@ -56,7 +56,7 @@ class AdamW(torch.optim.Optimizer):
             g = p.grad if p.grad.is_contiguous() else p.grad.contiguous()
             st = self._state(p, group["moment_bits"])
             entries.append((p, g, st))
-            key.append((p.data_ptr(), g.data_ptr(), g.dtype, st["m"].data_ptr()))
+            key.append((p.data_ptr(), p.numel(), g.data_ptr(), g.dtype, *[t.data_ptr() for t in st.values()]))
         key = (tuple(key), group["weight_decay"])
         kept = self._tables.get(index)
         if kept is not None and kept[0] == key:
