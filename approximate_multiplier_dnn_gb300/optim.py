@@ -14,7 +14,9 @@ class AdamW(torch.optim.Optimizer):
     keep an fp32 master in the state, which is updated; the step writes its
     rounding to the parameter.  Gradients may be fp32 or bf16.
     moment_bits: 32, or 8 (one byte per moment and element and an fp32 scale
-    per 256 of them).  grad_scale given to step() is one fp32 CUDA value that
+    per 256 of them).  Each parameter counts its own updates, by which its
+    moments' bias is corrected; those with the same count share a launch.
+    grad_scale given to step() is one fp32 CUDA value that
     multiplies every gradient, such as the factor of clipping by the norm;
     reading it costs no synchronisation.
     """
@@ -24,14 +26,15 @@ class AdamW(torch.optim.Optimizer):
         if moment_bits not in (8, 32):
             raise ValueError("moment_bits is 8 or 32")
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
-                                      moment_bits=moment_bits, step=0))
+                                      moment_bits=moment_bits))
         self._tables = {}
 
     def _state(self, p, bits):
+        if p.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("AdamW takes fp32 and bf16 parameters")
         st = self.state[p]
-        if st:
-            return st
         n = p.numel()
+        st["step"] = 0
         if bits == 32:
             st["m"], st["v"] = (torch.zeros(n, dtype=torch.float32, device=p.device) for _ in range(2))
         else:
@@ -43,31 +46,40 @@ class AdamW(torch.optim.Optimizer):
             st["master"] = p.detach().float().reshape(-1)
         return st
 
-    def _table(self, index, group):
-        """The group's table; built again only when an address in it changed."""
-        entries, key = [], []
+    def _group_tables(self, index, group):
+        """The group's tables, one for each count of updates, as (count so far, table), and the gradients and states
+        of their parameters.  Built again only when an address in them changed, or some counts against others.  (The
+        loop is the host's time of a step: some 1.2 us a parameter.)"""
+        entries, key, first, state = [], [group["weight_decay"]], None, self.state
         for p in group["params"]:
-            if p.grad is None or p.numel() == 0:
+            g = p.grad
+            if g is None or p.numel() == 0:
                 continue
-            if p.dtype not in (torch.float32, torch.bfloat16):
-                raise TypeError("AdamW takes fp32 and bf16 parameters")
-            if not p.is_contiguous() or p.grad.is_sparse:
+            if not p.is_contiguous() or g.is_sparse:
                 raise ValueError("AdamW takes contiguous parameters with dense gradients")
-            g = p.grad if p.grad.is_contiguous() else p.grad.contiguous()
-            st = self._state(p, group["moment_bits"])
+            if not g.is_contiguous():
+                g = g.contiguous()
+            st = state[p] or self._state(p, group["moment_bits"])
+            count = st["step"]
+            if first is None:
+                first = count
             entries.append((p, g, st))
-            key.append((p.data_ptr(), p.numel(), g.data_ptr(), g.dtype, *[t.data_ptr() for t in st.values()]))
-        key = (tuple(key), group["weight_decay"])
+            key += (p.data_ptr(), p.numel(), g.data_ptr(), g.dtype, count - first, st["m"].data_ptr(), st["v"].data_ptr())
+            if "m_scale" in st:
+                key += (st["m_scale"].data_ptr(), st["v_scale"].data_ptr())
+            if "master" in st:
+                key.append(st["master"].data_ptr())
         kept = self._tables.get(index)
-        if kept is not None and kept[0] == key:
-            return kept[1], [g for _, g, _ in entries]
-        table = adamw_table(
-            AdamwTensor.make(st.get("master", p.detach().reshape(-1)), g.reshape(-1), st["m"], st["v"],
-                             m_scale=st.get("m_scale"), v_scale=st.get("v_scale"),
-                             copy=p.detach().reshape(-1) if "master" in st else None,
-                             weight_decay=group["weight_decay"]) for p, g, st in entries)
-        self._tables[index] = (key, table)
-        return table, [g for _, g, _ in entries]
+        if kept is None or kept[0] != key:
+            by_count = {}
+            for p, g, st in entries:
+                by_count.setdefault(st["step"] - first, []).append(
+                    AdamwTensor.make(st.get("master", p.detach().reshape(-1)), g.reshape(-1), st["m"], st["v"],
+                                     m_scale=st.get("m_scale"), v_scale=st.get("v_scale"),
+                                     copy=p.detach().reshape(-1) if "master" in st else None,
+                                     weight_decay=group["weight_decay"]))
+            kept = self._tables[index] = (key, [(ahead, adamw_table(es)) for ahead, es in by_count.items()])
+        return [(first + ahead, table) for ahead, table in kept[1]], [g for _, g, _ in entries], [st for _, _, st in entries]
 
     @torch.no_grad()
     def step(self, closure=None, *, grad_scale: torch.Tensor | None = None):
@@ -76,11 +88,12 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         for i, group in enumerate(self.param_groups):
-            table, hold = self._table(i, group)
-            group["step"] += 1
-            if len(table):
+            tables, hold, states = self._group_tables(i, group)
+            for count, table in tables:
                 adamw_step(table, lr=group["lr"], beta1=group["betas"][0], beta2=group["betas"][1], eps=group["eps"],
-                           step=group["step"], grad_scale=grad_scale)
+                           step=count + 1, grad_scale=grad_scale)
+            for st in states:
+                st["step"] += 1
             del hold                     # gradients made contiguous live until the launch
         return loss
 
@@ -93,11 +106,18 @@ class AdamW(torch.optim.Optimizer):
                 adamw_moment_values(st["v"], st["v_scale"]).view(p.shape))
 
     def load_state_dict(self, state_dict):
-        """As torch's, but the state keeps its own types (torch would cast it to the parameter's)."""
+        """As torch's, but the state keeps its own types (torch would cast it to the parameter's).  A state that was
+        saved with one count of updates for a group, not one for each parameter, goes on with that."""
         super().load_state_dict(state_dict)
         saved = state_dict["state"]
         order = [p for g in self.param_groups for p in g["params"]]
         for index, st in saved.items():
             for name, t in st.items():
-                self.state[order[index]][name] = t.detach().clone().to(order[index].device)
+                if isinstance(t, torch.Tensor):
+                    self.state[order[index]][name] = t.detach().clone().to(order[index].device)
+        for group in self.param_groups:
+            count = group.pop("step", None)
+            for p in group["params"]:
+                if count is not None and p in self.state:
+                    self.state[p].setdefault("step", count)
         self._tables = {}

@@ -82,3 +82,74 @@ def test_table_is_kept_while_nothing_moves(steps, monkeypatch):
     p.grad = p.grad.clone()
     opt.step()
     assert len(made) == 2
+
+
+def formula(p, gs, lr=1e-3, wd=0.01):
+    """AdamW in 64 bits over the gradients that a parameter got (None: none in that step)."""
+    p, m, v, t = p.detach().double().clone(), 0.0, 0.0, 0
+    for g in gs:
+        if g is None:
+            continue
+        t, g = t + 1, g.double()
+        m, v = 0.9 * m + 0.1 * g, 0.999 * v + 0.001 * g * g
+        p = p * (1 - lr * wd) - lr * (m / (1 - 0.9 ** t)) / ((v / (1 - 0.999 ** t)).sqrt() + 1e-8)
+    return p
+
+
+def train(opt, ps, plan, seed=0):
+    """Steps; plan[i] names the parameters that get a gradient in step i. The gradients of each parameter."""
+    g = torch.Generator().manual_seed(seed)
+    got = [[] for _ in ps]
+    for which in plan:
+        for i, p in enumerate(ps):
+            p.grad = torch.randn(p.shape, generator=g) if i in which else None
+            got[i].append(p.grad)
+        opt.step()
+    return got
+
+
+def test_late_and_paused_gradients(steps):
+    """Bias correction counts a parameter's own updates: parameters whose
+    gradients start late, pause or never come follow the formula (fp32 rounding:
+    30 steps of 1e-3 with some 10 roundings each)."""
+    ps = params(50, 60, 70, 80)
+    start = [p.detach().clone() for p in ps]
+    opt = optim.AdamW(ps)
+    plan = [{0}] * 20 + [set()] + [{0, 1}] * 5 + [{0, 2}, {0, 1, 2}, {1}, {0, 1, 2}]
+    got = train(opt, ps, plan)
+    for p, first, gs in zip(ps, start, got):
+        assert float((p.detach().double() - formula(first, gs)).abs().max()) <= 30 * (1e-3 * 10 + 4) * 2.0 ** -24
+    assert not opt.state[ps[3]]
+    assert [opt.state[p]["step"] for p in ps[:3]] == [28, 8, 3]
+    # one launch for each count of updates among a step's parameters, none without gradients
+    assert [n for _, n in steps[:20]] == [1] * 20 and steps[20:22] == [(21, 1), (1, 1)]
+    assert len(steps) == 20 + 0 + 5 * 2 + 2 + 3 + 1 + 3
+
+
+def test_parameters_in_step_share_a_launch(steps):
+    ps = params(*range(1, 12))
+    opt = optim.AdamW(ps)
+    train(opt, ps, [set(range(11))] * 3)
+    assert steps == [(1, 11), (2, 11), (3, 11)]
+
+
+def test_step_counts_are_saved(steps):
+    """A reloaded optimizer goes on with each parameter's own count; a state
+    saved with one count for a group goes on with that."""
+    ps = params(9, 10)
+    opt = optim.AdamW(ps)
+    train(opt, ps, [{0}] * 4 + [{0, 1}] * 2)
+    saved = copy.deepcopy(opt.state_dict())
+    qs = [torch.nn.Parameter(p.detach().clone()) for p in ps]
+    again = optim.AdamW(qs)
+    again.load_state_dict(saved)
+    assert [again.state[q]["step"] for q in qs] == [6, 2]
+    train(opt, ps, [{0, 1}], seed=7)
+    train(again, qs, [{0, 1}], seed=7)
+    assert all(torch.equal(p, q) for p, q in zip(ps, qs))
+    old = copy.deepcopy(saved)
+    for st in old["state"].values():
+        del st["step"]
+    old["param_groups"][0]["step"] = 6
+    again.load_state_dict(old)
+    assert [again.state[q]["step"] for q in qs] == [6, 6] and "step" not in again.param_groups[0]
