@@ -29,6 +29,10 @@ class AdamW(torch.optim.Optimizer):
                                       moment_bits=moment_bits))
         self._tables = {}
 
+    def __setstate__(self, state):       # of a copy, whose tables are made at its first step
+        super().__setstate__(state)
+        self._tables = {}
+
     def _state(self, p, bits):
         if p.dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("AdamW takes fp32 and bf16 parameters")

@@ -153,3 +153,23 @@ def test_step_counts_are_saved(steps):
     old["param_groups"][0]["step"] = 6
     again.load_state_dict(old)
     assert [again.state[q]["step"] for q in qs] == [6, 6] and "step" not in again.param_groups[0]
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "pickle"])
+def test_copies_go_on(steps, how):
+    """A copied optimizer (with its parameters) steps on like the original."""
+    ps = params(9, 10)
+    opt = optim.AdamW(ps)
+    train(opt, ps, [{0, 1}] * 2)
+    if how == "deepcopy":
+        again = copy.deepcopy(opt)
+    else:
+        buf = io.BytesIO()
+        torch.save(opt, buf)
+        buf.seek(0)
+        again = torch.load(buf, weights_only=False)
+    qs = again.param_groups[0]["params"]
+    assert qs[0] is not ps[0]
+    train(opt, ps, [{0, 1}] * 2, seed=3)
+    train(again, qs, [{0, 1}] * 2, seed=3)
+    assert all(torch.equal(p, q) for p, q in zip(ps, qs)) and again.state[qs[0]]["step"] == 4
