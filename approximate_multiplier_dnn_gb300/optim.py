@@ -12,7 +12,9 @@ class AdamW(torch.optim.Optimizer):
 
     fp32 parameters are updated in place.  bf16 parameters (VocabHead's weight)
     keep an fp32 master in the state, which is updated; the step writes its
-    rounding to the parameter.  Gradients may be fp32 or bf16.
+    rounding to the parameter.  Weights that are put into such a parameter in
+    place (a module's load_state_dict) go into its master before the next step;
+    writes through .data are not seen.  Gradients may be fp32 or bf16.
     moment_bits: 32, or 8 (one byte per moment and element and an fp32 scale
     per 256 of them).  Each parameter counts its own updates, by which its
     moments' bias is corrected; those with the same count share a launch.
@@ -27,11 +29,11 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError("moment_bits is 8 or 32")
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
                                       moment_bits=moment_bits))
-        self._tables = {}
+        self._tables, self._versions = {}, {}
 
     def __setstate__(self, state):       # of a copy, whose tables are made at its first step
         super().__setstate__(state)
-        self._tables = {}
+        self._tables, self._versions = {}, {}
 
     def _state(self, p, bits):
         if p.dtype not in (torch.float32, torch.bfloat16):
@@ -48,7 +50,14 @@ class AdamW(torch.optim.Optimizer):
             st["m_scale"], st["v_scale"] = (torch.zeros(blocks, dtype=torch.float32, device=p.device) for _ in range(2))
         if p.dtype == torch.bfloat16:
             st["master"] = p.detach().float().reshape(-1)
+            self._versions[p] = p._version
         return st
+
+    def _follow(self, p, st):
+        """The master takes the elements of a bf16 parameter that are no longer its rounding."""
+        new, master = p.detach().reshape(-1), st["master"].view(-1)
+        master.copy_(torch.where(master.to(new.dtype) == new, master, new.float()))
+        self._versions[p] = p._version
 
     def _group_tables(self, index, group):
         """The group's tables, one for each count of updates, as (count so far, table), and the gradients and states
@@ -72,6 +81,8 @@ class AdamW(torch.optim.Optimizer):
             if "m_scale" in st:
                 key += (st["m_scale"].data_ptr(), st["v_scale"].data_ptr())
             if "master" in st:
+                if self._versions.get(p) != p._version:
+                    self._follow(p, st)
                 key.append(st["master"].data_ptr())
         kept = self._tables.get(index)
         if kept is None or kept[0] != key:
@@ -119,6 +130,7 @@ class AdamW(torch.optim.Optimizer):
             for name, t in st.items():
                 if isinstance(t, torch.Tensor):
                     self.state[order[index]][name] = t.detach().clone().to(order[index].device)
+            self._versions[order[index]] = order[index]._version         # the master comes with the state
         for group in self.param_groups:
             count = group.pop("step", None)
             for p in group["params"]:

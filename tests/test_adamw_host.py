@@ -173,3 +173,34 @@ def test_copies_go_on(steps, how):
     train(opt, ps, [{0, 1}] * 2, seed=3)
     train(again, qs, [{0, 1}] * 2, seed=3)
     assert all(torch.equal(p, q) for p, q in zip(ps, qs)) and again.state[qs[0]]["step"] == 4
+
+
+def test_loaded_weights_are_kept(steps):
+    """Weights put into a bf16 parameter after its first step are what the next
+    step starts from; elements that stay keep their master's low bits."""
+    (p,) = params(64, dtype=torch.bfloat16)
+    opt = optim.AdamW([p], lr=1e-2, weight_decay=0.0)
+    grads([p], 0)
+    opt.step()
+    master = opt.state[p]["master"].clone()
+    new = torch.linspace(-3, 3, 64).to(torch.bfloat16)
+    new[32:] = p.detach()[32:]
+    with torch.no_grad():
+        p.copy_(new)                                           # as a module's load_state_dict does
+    p.grad = torch.zeros_like(p)
+    opt.param_groups[0]["lr"] = 0.0
+    opt.step()
+    assert torch.equal(p.detach(), new)
+    assert torch.equal(opt.state[p]["master"][:32], new[:32].float())
+    assert torch.equal(opt.state[p]["master"][32:], master[32:])
+    # the same weights loaded again change nothing, and an optimizer's own state comes with its master
+    with torch.no_grad():
+        p.copy_(p.clone())
+    opt.step()
+    assert torch.equal(opt.state[p]["master"][32:], master[32:])
+    saved = copy.deepcopy(opt.state_dict())
+    with torch.no_grad():
+        p.zero_()
+    opt.load_state_dict(saved)
+    opt.step()
+    assert torch.equal(p.detach(), new)

@@ -250,3 +250,42 @@ def test_streamed_backward_without_a_gradient(amd, drop, rows, cols, x, n):
         assert torch.equal(dx, want[0])
         assert bool(((dw.double() - want[4].double()).abs() <= 2 * (rows + 64) * 2.0 ** -24 * mags[2]).all())
     assert amd.amsim_device_errors() == (amd.AMSIM_OK, 0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_optimizer_follows_loaded_weights(amd, bits):
+    """Weights loaded into the head between steps stay (their gradients are
+    zero and decay is off), and a step's own writes are not taken for a load."""
+    import torch
+    from approximate_multiplier_dnn_gb300.layers import VocabHead
+    from approximate_multiplier_dnn_gb300.optim import AdamW
+    head, other = (VocabHead(40, 300, generator=torch.Generator().manual_seed(i)) for i in (1, 2))
+    opt = AdamW(head.parameters(), lr=1e-2, weight_decay=0.0, moment_bits=bits)
+    w = head.weight
+    for _ in range(3):
+        w.grad = torch.randn_like(w)
+        opt.step()
+        master = opt.state[w]["master"]
+        assert torch.equal(w.detach().view(-1), master.to(torch.bfloat16)) and not torch.equal(w.float().view(-1), master)
+    head.load_state_dict(other.state_dict())
+    opt.param_groups[0]["lr"] = 0.0
+    opt.step()
+    assert torch.equal(w, other.weight) and torch.equal(opt.state[w]["master"], other.weight.detach().float().view(-1))
+
+
+def test_optimizer_with_late_gradients(amd):
+    """A parameter that joins at step 40 moves as in an optimizer of its own, to the bit."""
+    import torch
+    from approximate_multiplier_dnn_gb300.optim import AdamW
+    g = torch.Generator(device="cuda").manual_seed(0)
+    a, b = (torch.nn.Parameter(torch.randn(n, generator=g, device="cuda")) for n in (1000, 777))
+    c = torch.nn.Parameter(b.detach().clone())
+    both, alone = AdamW([a, b]), AdamW([c])
+    for i in range(45):
+        a.grad = torch.randn(a.shape, generator=g, device="cuda")
+        if i >= 40:
+            b.grad = torch.randn(b.shape, generator=g, device="cuda")
+            c.grad = b.grad.clone()
+            alone.step()
+        both.step()
+    assert torch.equal(b, c) and both.state[b]["step"] == 5 and both.state[a]["step"] == 45
