@@ -105,7 +105,7 @@ class AdamwTensor(ctypes.Structure):
         """From contiguous CUDA tensors: p fp32; g fp32 or bf16; m, v fp32, or int8 and uint8 codes with their
         block scales; copy bf16 or None.  The tensors must outlive the table."""
         import torch
-        n, eight = p.numel(), m_scale is not None
+        n, eight, here = p.numel(), m_scale is not None, _current_device()
         want = [("p", p, torch.float32, n), ("m", m, torch.int8 if eight else torch.float32, n),
                 ("v", v, torch.uint8 if eight else torch.float32, n), ("g", g, g.dtype, n)]
         blocks = -(-n // AMSIM_ADAMW_BLOCK)
@@ -116,8 +116,12 @@ class AdamwTensor(ctypes.Structure):
         for name, t, dtype, size in want:
             if t is None or t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != size:
                 raise TypeError(f"AdamwTensor: {name} must be a contiguous CUDA tensor of {size} {dtype} values")
-        return cls(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale), _ptr(copy), n, float(lr_scale),
-                   float(weight_decay), _dtype(g), 0)
+            if t.get_device() != here:
+                raise _elsewhere(name, t, here)
+        entry = cls(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale), _ptr(copy), n, float(lr_scale),
+                    float(weight_decay), _dtype(g), 0)
+        entry.device = here
+        return entry
 
 
 class AdamwHyper(ctypes.Structure):
@@ -275,6 +279,29 @@ def _ptr(t) -> int | None:
 def _at(t) -> int | None:
     """_ptr of a checked tensor or None, in half the time (a small call's time is the host's)."""
     return None if t is None else t.data_ptr()
+
+
+_device_index = None
+
+
+def _current_device() -> int:
+    """torch's current CUDA device, on which a call's tensors must be: its stream and its kernels are that one's.  Less
+    than any tensor's device without one."""
+    global _device_index
+    try:
+        if _device_index is None:
+            import torch
+            _device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        return _device_index()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _elsewhere(name, t, here):
+    """The error of a tensor that is not on device `here`."""
+    if not t.is_cuda:
+        return TypeError(f"{name} must be a CUDA tensor")
+    return ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{here}")
 
 
 _raw_stream = None
@@ -660,12 +687,14 @@ def _dtype(t) -> int:
     raise TypeError(f"exact operators take fp32 or bf16 tensors, not {dtype}")
 
 
-def _rows(name, t, rows, cols, dtype=None) -> int:
-    """Row stride of a CUDA matrix of `rows` x `cols` whose rows are contiguous."""
+def _rows(name, t, rows, cols, here, dtype=None) -> int:
+    """Row stride of a matrix of `rows` x `cols` on device `here` whose rows are contiguous."""
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {rows} x {cols}, not {tuple(t.shape)}")
-    if not t.is_cuda or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} must be a CUDA tensor{'' if dtype is None else ' of ' + str(dtype)}")
+    if t.get_device() != here:
+        raise _elsewhere(name, t, here)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
     if t.is_contiguous():
         return cols
     outer, inner = t.stride()
@@ -674,8 +703,10 @@ def _rows(name, t, rows, cols, dtype=None) -> int:
     return outer if rows > 1 else cols
 
 
-def _vector(name, t, n, dtype):
-    if t.dtype != dtype or not t.is_cuda:
+def _vector(name, t, n, dtype, here):
+    if t.get_device() != here:
+        raise _elsewhere(name, t, here)
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must hold {n} contiguous values")
@@ -699,20 +730,20 @@ def _vocab_plan(tokens, vocab, dim, ld_h, ld_w, ignore_index, reduction, h, w):
     return ctypes.byref(d), *(amsim_vocab_loss_workspace_size_at(d, which, h, w) for which in (0, 1))
 
 
-def _gate_rows(first, gate, w_post, w_pre):
+def _gate_rows(first, gate, w_post, w_pre, here):
     """Rows per row of the gate (0 without one), the vectors of a block norm over rows like `first`'s checked."""
     import torch
     if first.ndim != 2:
         raise ValueError("block norms take matrices of rows x channels")
     rows, cols = first.shape
     if w_post is not None:
-        _vector("w_post", w_post, cols, torch.float32)
+        _vector("w_post", w_post, cols, torch.float32, here)
     if w_pre is not None:
-        _vector("w_pre", w_pre, cols, torch.float32)
+        _vector("w_pre", w_pre, cols, torch.float32, here)
     if gate is None:
         return 0
     groups = gate.numel() // cols
-    _vector("gate", gate, max(1, groups) * cols, torch.float32)
+    _vector("gate", gate, max(1, groups) * cols, torch.float32, here)
     if groups < 1 or rows % groups:
         raise ValueError(f"gate must have one row of {cols} values for every so many of the {rows} rows")
     return rows // groups
@@ -725,10 +756,11 @@ def block_norm(x, y=None, w_post=None, w_pre=None, *, gate=None, alpha=1.0, eps=
     gate: [groups, channels], one row for each rows / groups consecutive rows, or None.  n has type `n_dtype` (y's,
     or x's).  rstd_post is None without w_post."""
     import torch
-    gate_rows = _gate_rows(x, gate, w_post, w_pre)
+    here = _current_device()
+    gate_rows = _gate_rows(x, gate, w_post, w_pre, here)
     rows, cols = x.shape
-    xs = (_dtype(x), _rows("x", x, rows, cols))
-    ys = (AMSIM_F32, 0) if y is None else (_dtype(y), _rows("y", y, rows, cols))
+    xs = (_dtype(x), _rows("x", x, rows, cols, here))
+    ys = (AMSIM_F32, 0) if y is None else (_dtype(y), _rows("y", y, rows, cols, here))
     empty, device = torch.empty, x.device
     n = empty((rows, cols), dtype=n_dtype or (x if y is None else y).dtype, device=device)
     desc, _ = _block_norm_plan(rows, cols, gate_rows, xs, ys, (_dtype(n), 0), 0, 0, 0, alpha, eps, False)
@@ -746,25 +778,26 @@ def block_norm_backward(dr, dn, r, y, w_post, w_pre, rstd_post, rstd_pre, *, gat
     """Gradients of block_norm: (dx, dy, dgate, dw_post, dw_pre), None where there was no such input.  dr or dn may
     be None (zeros); r, rstd_post and rstd_pre are block_norm's."""
     import torch
-    gate_rows = _gate_rows(r, gate, w_post, w_pre)
+    here = _current_device()
+    gate_rows = _gate_rows(r, gate, w_post, w_pre, here)
     rows, cols = r.shape
     f32, empty, device = torch.float32, torch.empty, r.device
     ys, ns, lddr, lddn = (AMSIM_F32, 0), (AMSIM_F32, 0), 0, 0
-    ldr = _rows("r", r, rows, cols)
+    ldr = _rows("r", r, rows, cols, here)
     if dr is not None:
-        lddr = _rows("dr", dr, rows, cols, r.dtype)
+        lddr = _rows("dr", dr, rows, cols, here, r.dtype)
     if dn is not None:
-        ns, lddn = (_dtype(dn), 0), _rows("dn", dn, rows, cols)
-        _vector("rstd_pre", rstd_pre, rows, f32)
+        ns, lddn = (_dtype(dn), 0), _rows("dn", dn, rows, cols, here)
+        _vector("rstd_pre", rstd_pre, rows, f32, here)
     dx = empty((rows, cols), dtype=r.dtype, device=device)
     dy = dgate = dw_post = dw_pre = None
     if y is not None:
-        ys = (_dtype(y), _rows("y", y, rows, cols))
+        ys = (_dtype(y), _rows("y", y, rows, cols, here))
         dy = empty((rows, cols), dtype=y.dtype, device=device)
     if gate is not None:
         dgate = torch.empty_like(gate) if rows else torch.zeros_like(gate)
     if w_post is not None:
-        _vector("rstd_post", rstd_post, rows, f32)
+        _vector("rstd_post", rstd_post, rows, f32, here)
         dw_post = torch.empty_like(w_post)
     if w_pre is not None:
         dw_pre = torch.empty_like(w_pre) if dn is not None else torch.zeros_like(w_pre)
@@ -784,12 +817,12 @@ def _vocab_call(h, w, targets, row_weight, ignore_index, reduction):
         raise ValueError("the vocabulary loss takes h [tokens, dim] and w [vocab, dim]")
     tokens, dim = h.shape
     vocab = w.shape[0]
-    bf16 = torch.bfloat16
-    plan = _vocab_plan(tokens, vocab, dim, _rows("h", h, tokens, dim, bf16), _rows("w", w, vocab, dim, bf16),
+    bf16, here = torch.bfloat16, _current_device()
+    plan = _vocab_plan(tokens, vocab, dim, _rows("h", h, tokens, dim, here, bf16), _rows("w", w, vocab, dim, here, bf16),
                        ignore_index, reduction, 128 + h.data_ptr() % 128, 128 + w.data_ptr() % 128)
-    _vector("targets", targets, tokens, torch.int64)
+    _vector("targets", targets, tokens, torch.int64, here)
     if row_weight is not None:
-        _vector("row_weight", row_weight, tokens, torch.float32)
+        _vector("row_weight", row_weight, tokens, torch.float32, here)
     empty, device = torch.empty, h.device
     row = empty(tokens, dtype=torch.float32, device=device)
     return plan, empty(1, dtype=torch.float32, device=device), row, torch.empty_like(row)
@@ -823,16 +856,25 @@ def vocab_loss_grad(h, w, targets, *, row_weight=None, ignore_index=-100, reduct
 
 
 def adamw_table(tensors):
-    """The table adamw_step takes, from AdamwTensor entries; it holds their addresses only."""
+    """The table adamw_step takes, from AdamwTensor entries; it holds their addresses only, and their device."""
     tensors = list(tensors)
-    return (AdamwTensor * len(tensors))(*tensors)
+    devices = {t.device for t in tensors if hasattr(t, "device")}
+    if len(devices) > 1:
+        raise ValueError("the tensors of a table must be on one device")
+    table = (AdamwTensor * len(tensors))(*tensors)
+    table.device = devices.pop() if devices else None
+    return table
 
 
 def adamw_step(table, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, step, grad_scale=None):
-    """One AdamW step over a table of tensors; `step` counts from 1, grad_scale is one fp32 CUDA value or None."""
+    """One AdamW step over a table of tensors on the current device; `step` counts from 1, grad_scale is one fp32 CUDA
+    value or None."""
+    device, here = getattr(table, "device", None), _current_device()
     if grad_scale is not None:
         import torch
-        _vector("grad_scale", grad_scale, 1, torch.float32)
+        _vector("grad_scale", grad_scale, 1, torch.float32, here)
+    if device is not None and device != here:
+        raise ValueError(f"the table's tensors are on cuda:{device}, the current device is cuda:{here}")
     amsim_adamw_step(table, AdamwHyper(lr, beta1, beta2, eps, step, _ptr(grad_scale)))
 
 
@@ -842,8 +884,9 @@ def adamw_moment_values(codes, scales):
     n, second = codes.numel(), codes.dtype == torch.uint8
     if not second and codes.dtype != torch.int8:
         raise TypeError("moment codes are int8 (first moment) or uint8 (second)")
-    _vector("codes", codes, n, codes.dtype)
-    _vector("scales", scales, -(-n // AMSIM_ADAMW_BLOCK), torch.float32)
+    here = _current_device()
+    _vector("codes", codes, n, codes.dtype, here)
+    _vector("scales", scales, -(-n // AMSIM_ADAMW_BLOCK), torch.float32, here)
     out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
     _check("amsim_adamw_moment_values",
            lib().amsim_adamw_moment_values(codes.data_ptr(), scales.data_ptr(), 1 if second else 0, n, out.data_ptr(),
