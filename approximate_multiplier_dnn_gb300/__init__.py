@@ -742,10 +742,10 @@ def _gate_rows(first, gate, w_post, w_pre, here):
         _vector("w_pre", w_pre, cols, torch.float32, here)
     if gate is None:
         return 0
-    groups = gate.numel() // cols
-    _vector("gate", gate, max(1, groups) * cols, torch.float32, here)
-    if groups < 1 or rows % groups:
+    groups = gate.shape[0] if gate.ndim == 2 else 1
+    if gate.ndim not in (1, 2) or gate.shape[-1] != cols or groups < 1 or rows % groups:
         raise ValueError(f"gate must have one row of {cols} values for every so many of the {rows} rows")
+    _vector("gate", gate, groups * cols, torch.float32, here)
     return rows // groups
 
 

@@ -98,3 +98,14 @@ def _moved(entry):
     copy = am.AdamwTensor()
     copy.device = entry.device + 1
     return copy
+
+
+@pytest.mark.parametrize("shape", [(8, 2), (2, 2, 4), (4, 4), (1, 2, 8), (3, 8), (0, 8), (12,), ()])
+def test_gate_of_another_shape(launched, shape):
+    """As many values as a gate's, but no rows of channels: refused, not read as if they were."""
+    x = On(0, 4, 8)
+    with pytest.raises(ValueError):
+        am.block_norm(x, x, gate=On(0, *shape))
+    with pytest.raises(ValueError):
+        am.block_norm_backward(x, None, x, x, None, None, None, None, gate=On(0, *shape))
+    assert not launched()
