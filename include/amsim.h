@@ -581,7 +581,8 @@ typedef struct amsim_block_norm_desc {
  * (w_post null: no norm after the block; w_pre null with n: unit weights);
  * r: written, or null (allowed only when n is not); n: written, or null.
  * rstd_post, rstd_pre: `rows` values each, written for the backward pass, or
- * null.  r may alias x or y; n may alias y (equal types and strides).
+ * null; not written where there is no such norm (w_post null; n null).  r may
+ * alias x or y; n may alias y (equal types and strides).
  * Errors: AMSIM_EINVAL for a null x, no output, a bad size, stride, type or
  * eps, or a gate without y; AMSIM_EUNSUPPORTED for more channels than
  * AMSIM_BLOCK_NORM_MAX_COLS.  rows == 0 is a no-op.

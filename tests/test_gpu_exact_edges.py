@@ -292,3 +292,40 @@ def test_optimizer_with_late_gradients(amd):
             alone.step()
         both.step()
     assert torch.equal(b, c) and both.state[b]["step"] == 5 and both.state[a]["step"] == 45
+
+
+@pytest.mark.parametrize("cols,ld,off", [(1024, 1024, 0), (1024, 1040, 8), (1016, 1019, 3), (1013, 1013, 1)])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_streamed_in_place_with_strides(amd, cols, ld, off, groups):
+    """Streamed rows with a stride, r over x and n over y, dx over dr and dy over
+    dn: what the same layout gives beside its inputs, to the bit, and nothing
+    between the rows is written."""
+    import torch
+    rows, B = 2500, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(cols)
+
+    def place(t=None):
+        buf = torch.full((rows * ld + off + 8,), 5.0, dtype=B, device="cuda")
+        v = buf[off:off + rows * ld].view(rows, ld)[:, :cols]
+        v.copy_(torch.randn((rows, cols), generator=g, device="cuda") if t is None else t)
+        return buf, v
+    w, v = (1 + 0.1 * torch.randn(cols, generator=g, device="cuda") for _ in range(2))
+    gate = torch.rand((groups, cols), generator=g, device="cuda")
+    d = amd.BlockNormDesc(rows=rows, cols=cols, gate_rows=rows // groups, alpha=0.5, eps=1e-6, x_type=1, y_type=1,
+                          n_type=1, ldx=ld, ldy=ld, ldr=ld, ldn=ld, lddr=ld, lddn=ld, lddx=ld, lddy=ld)
+    (xb, x), (yb, y), (_, r), (_, n) = (place() for _ in range(4))
+    post, pre = (torch.empty(rows, device="cuda") for _ in range(2))
+    y0 = place(y)[1]
+    amd.amsim_block_norm_fwd(d, x, y, gate, w, v, r, n, post, pre)
+    amd.amsim_block_norm_fwd(d, x, y, gate, w, v, x, y, post, pre)
+    assert torch.equal(x, r) and torch.equal(y, n)
+    (drb, dr), (dnb, dn), (_, dx), (_, dy) = (place() for _ in range(4))
+    ws = amd.workspace(amd.amsim_block_norm_workspace_size(d))
+    sums = [[torch.empty_like(t) for t in (gate, w, v)] for _ in range(2)]
+    amd.amsim_block_norm_bwd(d, dr, dn, r, y0, gate, w, v, post, pre, dx, dy, *sums[0], ws=ws)
+    amd.amsim_block_norm_bwd(d, dr, dn, r, y0, gate, w, v, post, pre, dr, dn, *sums[1], ws=ws)
+    assert torch.equal(dr, dx) and torch.equal(dn, dy) and all(torch.equal(p, q) for p, q in zip(*sums))
+    for buf, t in ((xb, x), (yb, y), (drb, dr), (dnb, dn)):
+        t.fill_(5.0)
+        assert bool((buf == 5.0).all())
+    assert amd.amsim_device_errors() == (amd.AMSIM_OK, 0)
