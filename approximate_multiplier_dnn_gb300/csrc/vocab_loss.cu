@@ -505,7 +505,19 @@ struct MergeParams {
     long long tokens, first, ignore;   // all tokens, the chunk's first
     int rows, pieces, vocab, mean;
     int first_chunk, last_chunk;
+    int blocks;                   // that merge; those behind them copy h
+    const uint16_t *h;            // of the chunk, rows on 16 bytes
+    uint16_t *kept;
+    long long ld_h, ld_kept;
+    int dim, copy_rows;           // of h; rows of it that a block copies
 };
+
+// Weight of a row in the gradients: 0 for a token that does not count or whose target is no entry.
+__device__ __forceinline__ float row_weight(const MergeParams &p, int row)
+{
+    const long long target = p.targets[row];
+    return target == p.ignore || target < 0 || target >= p.vocab ? 0.0f : p.row_weight ? p.row_weight[p.first + row] : 1.0f;
+}
 
 // A running sum with the rounding errors carried along (compensated
 // summation): thousands of terms per thread stay at one rounding, without fp64,
@@ -551,7 +563,14 @@ __device__ __forceinline__ void add_piece(float &top, float &sum, float2 s)
 
 // lse and loss of each row from its pieces (lane by lane over the rows, so
 // that a warp reads neighbouring rows); the last block adds the losses.
-constexpr int kMergeThreads = 1024, kMergeRows = 32;
+//
+// With gradients, more blocks copy the hidden states for dW = G^T h, with zeros
+// where a row's weight is zero: a row of G that is zero would still make NaN of
+// a masked token's infinities.  (4 bytes per element of h, on SMs that the merge
+// leaves idle: 4096 x 32768 x 1024 with gradients 560 us, 555 without.  In the
+// pass that forms G, which has no registers to spare, it took 569, and 596 in
+// blocks of its own there.)
+constexpr int kMergeThreads = 1024, kMergeRows = 32, kCopyWords = 4 * kMergeThreads;
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p)
 {
     __shared__ float2 part[kMergeThreads / 32][kMergeRows];
@@ -559,6 +578,24 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
     __shared__ bool last;
     chain_start();
     chain_wait();
+    if ((int)blockIdx.x >= p.blocks) {
+        const int r0 = ((int)blockIdx.x - p.blocks) * p.copy_rows, words = (p.dim + 7) / 8;
+        const int n = min(p.copy_rows, p.rows - r0) * words;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += kMergeThreads) {
+            const int r = i / words, c = (i - r * words) * 8;
+            const uint16_t *from = p.h + (r0 + r) * p.ld_h + c;
+            uint16_t *to = p.kept + (r0 + r) * p.ld_kept + c;
+            const bool zero = row_weight(p, r0 + r) == 0.0f;
+            if (c + 8 <= p.dim) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(from);
+                *reinterpret_cast<uint4 *>(to) = zero ? make_uint4(0, 0, 0, 0) : v;
+            } else {
+                for (int j = 0; c + j < p.dim; ++j) to[j] = zero ? (uint16_t)0 : from[j];
+            }
+        }
+        return;
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * kMergeRows + lane;
     float top = -INFINITY, sum = 0.0f;
@@ -576,11 +613,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
         const bool counts = target != p.ignore, valid = target >= 0 && target < p.vocab;
         p.lse[row] = lse;
         p.row_loss[row] = !counts ? 0.0f : valid ? lse - p.target_logit[row] : __uint_as_float(0x7FC00000u);
-        p.weight[row] = !counts || !valid ? 0.0f : p.row_weight ? p.row_weight[p.first + row] : 1.0f;
+        p.weight[row] = row_weight(p, row);
     }
     __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(&p.totals->done, 1u) == gridDim.x - 1;
+    if (threadIdx.x == 0) last = atomicAdd(&p.totals->done, 1u) == (unsigned)p.blocks - 1;
     __syncthreads();
     if (!last) return;
     __threadfence();
@@ -607,11 +644,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
 // 4 bytes of traffic per element; the conversion of a code goes through the
 // mantissa of 2^23 + code, since the conversion instructions share the
 // exponential's unit, which alone needs 0.4 of the time of the bytes.
-// The blocks of a row also copy its hidden state, a slice each, for dW = G^T h,
-// with zeros where the weight is zero: a row of G that is zero would still make
-// NaN of a masked token's infinities.  (4 bytes per element of h: 4096 x 32768 x
-// 1024 takes 569 us instead of 559; with the copy in a block of its own per row
-// it took 596.)
 struct GradParams {
     uint16_t *codes;
     const float2 *stats;
@@ -619,10 +651,6 @@ struct GradParams {
     const int64_t *targets;
     long long ld;
     int rows, vocab;
-    const uint16_t *h;       // rows on 16 bytes
-    uint16_t *kept;
-    long long ld_h, ld_kept;
-    int dim, slice;          // of h; 16-byte words of it that a block copies
 };
 constexpr int kGradThreads = 256, kGradSteps = 4;
 constexpr int kGradCols = kGradThreads * 8 * kGradSteps;      // of a block
@@ -631,25 +659,10 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
     chain_start();
     chain_wait();
     const int row = blockIdx.y;
-    const float w = p.weight[row];
-    const uint16_t *from = p.h + row * p.ld_h;
-    uint16_t *to = p.kept + row * p.ld_kept;
-    const int word0 = (int)blockIdx.x * p.slice, words = min(p.slice, p.dim / 8 - word0);
-    uint4 kept = make_uint4(0, 0, 0, 0);       // loaded ahead of the codes, stored behind their loads
-    const bool keeps = (int)threadIdx.x < words;
-    if (keeps && w != 0.0f) kept = reinterpret_cast<const uint4 *>(from)[word0 + threadIdx.x];
-    auto keep = [&] {
-        if (keeps) reinterpret_cast<uint4 *>(to)[word0 + threadIdx.x] = kept;
-        for (int i = threadIdx.x + kGradThreads; i < words; i += kGradThreads)
-            reinterpret_cast<uint4 *>(to)[word0 + i] =
-                w != 0.0f ? reinterpret_cast<const uint4 *>(from)[word0 + i] : make_uint4(0, 0, 0, 0);
-        const int e = p.dim / 8 * 8 + threadIdx.x;         // the elements behind the last whole word
-        if (blockIdx.x == 0 && e < p.dim) to[e] = w != 0.0f ? from[e] : (uint16_t)0;
-    };
     const int col0 = (int)blockIdx.x * kGradCols + (int)threadIdx.x * 8;
     uint16_t *codes = p.codes + row * p.ld;
+    const float w = p.weight[row];
     if (w == 0.0f) {
-        keep();
 #pragma unroll
         for (int k = 0; k < kGradSteps; ++k)
             if (col0 + k * kGradThreads * 8 < p.vocab)
@@ -667,7 +680,6 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const GradParams p)
             base[k] = p.stats[(long long)(col / kPiece) * p.rows + row].x;
         }
     }
-    keep();
     const long long target = p.targets[row];
 #pragma unroll
     for (int k = 0; k < kGradSteps; ++k) {
@@ -1000,16 +1012,24 @@ int run(const amsim_vocab_loss_desc *d, bool grad, const void *h, const void *w,
         q.first_chunk = first;
         q.last_chunk = last;
         chained = true;
-        rc = launched(chain_launch(true, merge_kernel, (unsigned)((n + kMergeRows - 1) / kMergeRows), kMergeThreads, 0,
-                                   st, q));
+        q.blocks = (int)((n + kMergeRows - 1) / kMergeRows);
+        int copies = 0;
+        bf16 *kept = reinterpret_cast<bf16 *>(base + l.kept);
+        if (grad) {
+            q.h = reinterpret_cast<const uint16_t *>(H.p + t0 * H.ld);
+            q.kept = reinterpret_cast<uint16_t *>(kept);
+            q.ld_h = H.ld;
+            q.ld_kept = l.ld_pack;
+            q.dim = d->dim;
+            q.copy_rows = std::max(1, kCopyWords / ((d->dim + 7) / 8));
+            copies = (int)((n + q.copy_rows - 1) / q.copy_rows);
+        }
+        rc = launched(chain_launch(true, merge_kernel, (unsigned)(q.blocks + copies), kMergeThreads, 0, st, q));
         if (rc) return rc;
         if (!grad) continue;
-        bf16 *kept = reinterpret_cast<bf16 *>(base + l.kept);
-        const int grad_blocks = (d->vocab + kGradCols - 1) / kGradCols;
-        GradParams e{codes, stats, q.lse, weight, targets + t0, l.ld_codes, (int)n, d->vocab,
-                     reinterpret_cast<const uint16_t *>(H.p + t0 * H.ld), reinterpret_cast<uint16_t *>(kept), H.ld,
-                     l.ld_pack, d->dim, (d->dim / 8 + grad_blocks - 1) / grad_blocks};
-        rc = launched(chain_launch(true, grad_kernel, dim3((unsigned)grad_blocks, (unsigned)n), kGradThreads, 0, st, e));
+        GradParams e{codes, stats, q.lse, weight, targets + t0, l.ld_codes, (int)n, d->vocab};
+        rc = launched(chain_launch(true, grad_kernel, dim3((unsigned)((d->vocab + kGradCols - 1) / kGradCols), (unsigned)n),
+                                   kGradThreads, 0, st, e));
         if (rc) return rc;
         // dh = G W
         p = product(n, d->dim, d->vocab, l.dh_splits);
