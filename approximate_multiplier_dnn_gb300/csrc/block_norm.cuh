@@ -12,7 +12,7 @@
 //
 // Measured, of 6768 GB/s for a plain copy: forward 5.3 TB/s at 16384 x 4096
 // bf16 (102 us) and 5.5 at 16384 x 2048 with an fp32 stream, backward 5.3
-// (152 us) and 5.7 (107 us).  Backward at 8192 x 8192 bf16 (173 us, 4.7 TB/s)
+// (152 us) and 5.6 (108 us).  Backward at 8192 x 8192 bf16 (173 to 178 us, 4.6 TB/s)
 // has room in shared memory for two rows, and at 16384 columns for none.
 #pragma once
 
@@ -500,8 +500,8 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p)
 //
 // Rows that do not start and end on 16 bytes (WHOLE false) come as the aligned
 // pieces of 16 that hold them (row_pieces.cuh), and start inside their slot.
-// Backward, 5395 x 3047 bf16: 341 us by direct loads, 75 so; 16384 x 1013
-// fp32/bf16: 166, 69.  Whole rows have kernels of their own, as the four rows'
+// Backward, 5395 x 3047 bf16: 341 us by direct loads, 73 so; 16384 x 1013
+// fp32/bf16: 166, 68.  Whole rows have kernels of their own, as the four rows'
 // ends cost 3 to 7 % of 16384 x 4096 and 8192 x 8192 bf16.
 
 // Waits, up to the limit once more, for the copies into a ring whose next slot is `at`.

@@ -23,14 +23,14 @@
 // run along M or N instead of K only changes its descriptor.
 //
 // Bound by the matrix pipe where the sizes are large: 4096 tokens x 32768 x
-// 1024 takes 150 us a product (1.8e15 operations/s; the pipe 86 to 96 %
-// active) and 80 us for G, whose 4 bytes per logit run at the memory's rate;
-// 8192 x 65536 x 4096 takes 7.8 ms (1.7e15/s), at the power limit.  With few
+// 1024 takes 148 to 158 us a product (1.8e15 operations/s; the pipe 87 to 96 %
+// active) and 81 us for G, whose 4 bytes per logit run at the memory's rate;
+// 8192 x 65536 x 4096 takes 8.0 ms (1.64e15/s), at the power limit.  With few
 // tokens it reads W twice and writes dW, and a tile of 256 rows is mostly
 // padding: 19 x 46024 x 2048 takes 55, 38 and 50 us for its products, the
 // first two for 189 MB (28 us) each.  The smallest calls cost their chain of
 // six launches, which start while the one before ends: 24 x 8192 x 256 takes
-// 36 us.
+// 37 us.
 #include <algorithm>
 #include <atomic>
 
