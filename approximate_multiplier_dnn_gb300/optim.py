@@ -12,15 +12,16 @@ class AdamW(torch.optim.Optimizer):
 
     fp32 parameters are updated in place.  bf16 parameters (VocabHead's weight)
     keep an fp32 master in the state, which is updated; the step writes its
-    rounding to the parameter.  Weights that are put into such a parameter in
-    place (a module's load_state_dict) go into its master before the next step;
-    writes through .data are not seen.  Gradients may be fp32 or bf16.
+    rounding to the parameter.  Weights that are put into such a parameter (a
+    module's load_state_dict, other memory given to p.data) go into its master
+    before the next step; writes in place through .data are not seen.
+    Gradients may be fp32 or bf16.
     moment_bits: 32, or 8 (one byte per moment and element and an fp32 scale
     per 256 of them).  Each parameter counts its own updates, by which its
     moments' bias is corrected; those with the same count share a launch.
-    grad_scale given to step() is one fp32 CUDA value that
-    multiplies every gradient, such as the factor of clipping by the norm;
-    reading it costs no synchronisation.
+    grad_scale given to step() is one fp32 CUDA value that multiplies every
+    gradient, such as the factor of clipping by the norm; reading it costs no
+    synchronisation.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
@@ -50,19 +51,19 @@ class AdamW(torch.optim.Optimizer):
             st["m_scale"], st["v_scale"] = (torch.zeros(blocks, dtype=torch.float32, device=p.device) for _ in range(2))
         if p.dtype == torch.bfloat16:
             st["master"] = p.detach().float().reshape(-1)
-            self._versions[p] = p._version
+            self._versions[p] = p._version, p.data_ptr()
         return st
 
     def _follow(self, p, st):
         """The master takes the elements of a bf16 parameter that are no longer its rounding."""
         new, master = p.detach().reshape(-1), st["master"].view(-1)
         master.copy_(torch.where(master.to(new.dtype) == new, master, new.float()))
-        self._versions[p] = p._version
+        self._versions[p] = p._version, p.data_ptr()
 
     def _group_tables(self, index, group):
         """The group's tables, one for each count of updates, as (count so far, table), and the gradients and states
         of their parameters.  Built again only when an address in them changed, or some counts against others.  (The
-        loop is the host's time of a step: some 1.2 us a parameter.)"""
+        loop is the host's time of a step: some 1.3 us a parameter.)"""
         entries, key, first, state = [], [group["weight_decay"]], None, self.state
         for p in group["params"]:
             g = p.grad
@@ -81,7 +82,7 @@ class AdamW(torch.optim.Optimizer):
             if "m_scale" in st:
                 key += (st["m_scale"].data_ptr(), st["v_scale"].data_ptr())
             if "master" in st:
-                if self._versions.get(p) != p._version:
+                if self._versions.get(p) != (p._version, p.data_ptr()):
                     self._follow(p, st)
                 key.append(st["master"].data_ptr())
         kept = self._tables.get(index)
@@ -130,7 +131,7 @@ class AdamW(torch.optim.Optimizer):
             for name, t in st.items():
                 if isinstance(t, torch.Tensor):
                     self.state[order[index]][name] = t.detach().clone().to(order[index].device)
-            self._versions[order[index]] = order[index]._version         # the master comes with the state
+            self._versions[order[index]] = order[index]._version, order[index].data_ptr()    # the state has its master
         for group in self.param_groups:
             count = group.pop("step", None)
             for p in group["params"]:

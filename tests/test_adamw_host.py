@@ -204,3 +204,21 @@ def test_loaded_weights_are_kept(steps):
     opt.load_state_dict(saved)
     opt.step()
     assert torch.equal(p.detach(), new)
+
+
+def test_weights_in_new_memory_are_kept(steps):
+    """A bf16 parameter that is given other memory (p.data = ...) goes on from
+    what that holds; where it is the master's rounding its low bits stay."""
+    (p,) = params(64, dtype=torch.bfloat16)
+    opt = optim.AdamW([p], lr=1e-2, weight_decay=0.0)
+    grads([p], 0)
+    opt.step()
+    master = opt.state[p]["master"].clone()
+    new = p.detach().clone()
+    new[:32] += 1
+    p.data = new.clone()
+    p.grad = torch.zeros_like(p)
+    opt.param_groups[0]["lr"] = 0.0
+    opt.step()
+    assert torch.equal(p.detach(), new)
+    assert torch.equal(opt.state[p]["master"], torch.cat([new[:32].float(), master[32:]]))
