@@ -39,19 +39,21 @@ class AdamW(torch.optim.Optimizer):
     def _state(self, p, bits):
         if p.dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("AdamW takes fp32 and bf16 parameters")
-        st = self.state[p]
         n = p.numel()
-        st["step"] = 0
+
+        def zeros(count, dtype):
+            return torch.zeros(count, dtype=dtype, device=p.device)
         if bits == 32:
-            st["m"], st["v"] = (torch.zeros(n, dtype=torch.float32, device=p.device) for _ in range(2))
+            new = dict(m=zeros(n, torch.float32), v=zeros(n, torch.float32))
         else:
-            st["m"] = torch.zeros(n, dtype=torch.int8, device=p.device)
-            st["v"] = torch.zeros(n, dtype=torch.uint8, device=p.device)
             blocks = -(-n // AMSIM_ADAMW_BLOCK)
-            st["m_scale"], st["v_scale"] = (torch.zeros(blocks, dtype=torch.float32, device=p.device) for _ in range(2))
+            new = dict(m=zeros(n, torch.int8), v=zeros(n, torch.uint8), m_scale=zeros(blocks, torch.float32),
+                       v_scale=zeros(blocks, torch.float32))
         if p.dtype == torch.bfloat16:
-            st["master"] = p.detach().float().reshape(-1)
+            new["master"] = p.detach().float().reshape(-1)
             self._versions[p] = p._version, p.data_ptr()
+        st = self.state[p]
+        st.update(new, step=0)
         return st
 
     def _follow(self, p, st):

@@ -222,3 +222,23 @@ def test_weights_in_new_memory_are_kept(steps):
     opt.step()
     assert torch.equal(p.detach(), new)
     assert torch.equal(opt.state[p]["master"], torch.cat([new[:32].float(), master[32:]]))
+
+
+def test_state_is_whole_or_absent(steps, monkeypatch):
+    """A state whose memory runs out half way is made again at the next step."""
+    (p,) = params(20)
+    opt = optim.AdamW([p])
+    grads([p], 0)
+    zeros, left = torch.zeros, [1]
+
+    def failing(*a, **kw):
+        if not left.pop():
+            raise MemoryError
+        left.append(0)
+        return zeros(*a, **kw)
+    monkeypatch.setattr(optim.torch, "zeros", failing)
+    with pytest.raises(MemoryError):
+        opt.step()
+    monkeypatch.setattr(optim.torch, "zeros", zeros)
+    opt.step()
+    assert steps == [(1, 1)] and sorted(opt.state[p]) == ["m", "step", "v"]
