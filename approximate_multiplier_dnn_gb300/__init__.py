@@ -77,6 +77,11 @@ AMSIM_REDUCE_SUM = 1
 REDUCTIONS = {"mean": AMSIM_REDUCE_MEAN, "sum": AMSIM_REDUCE_SUM}
 AMSIM_ADAMW_BLOCK = 256
 AMSIM_BLOCK_NORM_MAX_COLS = 16384
+AMSIM_MAX_DISTANCE = 1024
+AMSIM_ACT_NONE = 0
+AMSIM_ACT_RELU = 1
+AMSIM_ACT_SILU = 2
+ACTIVATIONS = {"none": AMSIM_ACT_NONE, "relu": AMSIM_ACT_RELU, "silu": AMSIM_ACT_SILU}
 
 
 class BlockNormDesc(ctypes.Structure):
@@ -128,6 +133,27 @@ class AdamwHyper(ctypes.Structure):
     """amsim_adamw_hyper."""
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("grad_scale", ctypes.c_void_p)]
+
+
+class DropoutDesc(ctypes.Structure):
+    """amsim_dropout_desc."""
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("call", ctypes.c_uint64), ("step", ctypes.c_void_p)]
+
+
+class AttentionSoftmaxDesc(ctypes.Structure):
+    """amsim_attention_softmax_desc (row strides of 0 mean dense rows)."""
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "heads", "queries", "keys", "ld_scores", "ld_probs",
+                                               "ld_dprobs", "ld_dscores", "offset")] +
+                [("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p)] +
+                [(n, ctypes.c_int) for n in ("causal", "num_buckets", "max_distance", "reserved")] +
+                [("dropout", DropoutDesc)])
+
+
+class GroupNormDesc(ctypes.Structure):
+    """amsim_group_norm_desc (pixel strides of 0 mean dense channels)."""
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "pixels", "ldx", "ldy", "lddx")] +
+                [(n, ctypes.c_int) for n in ("channels", "groups", "x_type", "y_type", "activation")] +
+                [("eps", ctypes.c_float)])
 
 
 def build():
@@ -195,6 +221,13 @@ def lib():
         "amsim_vocab_loss_workspace_min": ([ctypes.POINTER(VocabLossDesc), i32], sz),
         "amsim_adamw_step": ([i32, ctypes.POINTER(AdamwTensor), ctypes.POINTER(AdamwHyper), vp], i32),
         "amsim_adamw_moment_values": ([vp, vp, i32, i64, vp, vp], i32),
+        "amsim_dropout": ([ctypes.POINTER(DropoutDesc), i32, i64, vp, vp, vp, vp], i32),
+        "amsim_attention_softmax_fwd": ([ctypes.POINTER(AttentionSoftmaxDesc)] + [vp] * 6, i32),
+        "amsim_attention_softmax_bwd": ([ctypes.POINTER(AttentionSoftmaxDesc)] + [vp] * 9 + [sz, vp], i32),
+        "amsim_attention_softmax_workspace_size": ([ctypes.POINTER(AttentionSoftmaxDesc)], sz),
+        "amsim_group_norm_fwd": ([ctypes.POINTER(GroupNormDesc)] + [vp] * 7 + [sz, vp], i32),
+        "amsim_group_norm_bwd": ([ctypes.POINTER(GroupNormDesc)] + [vp] * 10 + [sz, vp], i32),
+        "amsim_group_norm_workspace_size": ([ctypes.POINTER(GroupNormDesc), i32], sz),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -649,6 +682,48 @@ def amsim_adamw_moment_values(codes, scales, second: bool, n: int, out, stream=N
                                            _stream(stream)))
 
 
+def amsim_dropout(desc: DropoutDesc, type: int, n: int, x, residual, y, stream=None):
+    _check("amsim_dropout", lib().amsim_dropout(ctypes.byref(desc), int(type), int(n), _ptr(x), _ptr(residual), _ptr(y),
+                                                _stream(stream)))
+
+
+def amsim_attention_softmax_fwd(desc: AttentionSoftmaxDesc, scores, table, buckets, probs, stats, stream=None):
+    _check("amsim_attention_softmax_fwd",
+           lib().amsim_attention_softmax_fwd(ctypes.byref(desc), _ptr(scores), _ptr(table), _ptr(buckets), _ptr(probs),
+                                             _ptr(stats), _stream(stream)))
+
+
+def amsim_attention_softmax_bwd(desc: AttentionSoftmaxDesc, dprobs, scores, stats, probs, table, buckets, dscores,
+                                dtable, ws=None, ws_bytes=None, stream=None):
+    ws_bytes = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check("amsim_attention_softmax_bwd",
+           lib().amsim_attention_softmax_bwd(ctypes.byref(desc), _ptr(dprobs), _ptr(scores), _ptr(stats), _ptr(probs),
+                                             _ptr(table), _ptr(buckets), _ptr(dscores), _ptr(dtable), _ptr(ws),
+                                             ws_bytes, _stream(stream)))
+
+
+def amsim_attention_softmax_workspace_size(desc: AttentionSoftmaxDesc) -> int:
+    return int(lib().amsim_attention_softmax_workspace_size(ctypes.byref(desc)))
+
+
+def amsim_group_norm_fwd(desc: GroupNormDesc, x, w, b, y, mean, rstd, ws=None, ws_bytes=None, stream=None):
+    ws_bytes = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check("amsim_group_norm_fwd",
+           lib().amsim_group_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(b), _ptr(y), _ptr(mean), _ptr(rstd),
+                                      _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def amsim_group_norm_bwd(desc: GroupNormDesc, dy, x, w, b, mean, rstd, dx, dw, db, ws=None, ws_bytes=None, stream=None):
+    ws_bytes = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check("amsim_group_norm_bwd",
+           lib().amsim_group_norm_bwd(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(w), _ptr(b), _ptr(mean), _ptr(rstd),
+                                      _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def amsim_group_norm_workspace_size(desc: GroupNormDesc, which: int) -> int:
+    return int(lib().amsim_group_norm_workspace_size(ctypes.byref(desc), int(which)))
+
+
 # ------------------------------------------------------------------ conveniences (still marshalling only)
 def workspace(nbytes: int, device=None):
     """A caller-owned scratch buffer (uint8 torch tensor, 256-byte aligned by the caching allocator)."""
@@ -892,3 +967,269 @@ def adamw_moment_values(codes, scales):
            lib().amsim_adamw_moment_values(codes.data_ptr(), scales.data_ptr(), 1 if second else 0, n, out.data_ptr(),
                                            _current_stream()))
     return out
+
+
+# ------------------------------------------------------------------ between two contractions
+def _drop(p, seed, call, step, here) -> DropoutDesc:
+    if step is not None:
+        import torch
+        _vector("step", step, 1, torch.int64, here)
+    return DropoutDesc(p, seed & 0xFFFFFFFFFFFFFFFF, call & 0xFFFFFFFFFFFFFFFF, _at(step))
+
+
+def dropout(x, p, *, seed, call=0, step=None, residual=None):
+    """residual + (x / (1 - p) where x stays, else 0), elements dropped with probability p.
+
+    x: contiguous, fp32 or bf16, any shape; residual: alike, or None.  The mask is a function of (seed, call + step)
+    and the element's place: the same numbers give the same mask, so dropout(dy, p, ...) is the gradient of x.  step: one
+    int64 CUDA value or None, read when the kernel runs, so that a captured graph can draw another mask each time."""
+    import torch
+    here, n = _current_device(), x.numel()
+    _vector("x", x, n, x.dtype, here)
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must be of x's shape {tuple(x.shape)}, not {tuple(residual.shape)}")
+        _vector("residual", residual, n, x.dtype, here)
+    y = torch.empty_like(x)
+    _check("amsim_dropout",
+           lib().amsim_dropout(ctypes.byref(_drop(p, seed, call, step, here)), _dtype(x), n, x.data_ptr(), _at(residual),
+                               y.data_ptr(), _current_stream()))
+    return y
+
+
+def relative_buckets(buckets: int, max_distance: int, bidirectional: bool = True):
+    """Bucket numbers of the distances -max_distance .. max_distance (key's position minus query's), an int32 CPU tensor.
+
+    In both directions the first half of the buckets is for keys up to the query's place and the second for later ones;
+    else all are for keys up to its place, and later ones share the first.  Half of a direction's buckets hold one
+    distance each; the others' sizes grow by a constant factor up to max_distance, from which on all share the last."""
+    import torch
+    count = buckets // 2 if bidirectional else buckets
+    near = count // 2
+    if near < 1 or max_distance <= near or max_distance > AMSIM_MAX_DISTANCE:
+        raise ValueError(f"relative_buckets: {buckets} buckets need a max_distance above {near} (and at least one near "
+                         f"bucket each way), at most {AMSIM_MAX_DISTANCE}")
+    steps = count - near
+
+    def bucket(far):
+        if far < near:
+            return far
+        k = 0                            # the last k with near (max_distance / near)^(k / steps) <= far, in whole numbers
+        while k + 1 < steps and max_distance ** (k + 1) * near ** steps <= far ** steps * near ** (k + 1):
+            k += 1
+        return near + k
+    up_to = [bucket(d) for d in range(max_distance, -1, -1)]
+    later = [count + bucket(d) if bidirectional else 0 for d in range(1, max_distance + 1)]
+    return torch.tensor(up_to + later, dtype=torch.int32)
+
+
+def _score_rows(name, t, shape, here) -> int:
+    """Row stride of a [batch, heads, queries, keys] tensor whose rows are evenly spaced and contiguous."""
+    import torch
+    if t.shape != shape:
+        raise ValueError(f"{name} must be of shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != here:
+        raise _elsewhere(name, t, here)
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a CUDA tensor of torch.float32")
+    if t.is_contiguous():
+        return shape[3]
+    b, h, q, k = shape
+    outer, inner = t.stride()[:3], t.stride(3)
+    ld = outer[2] if q > 1 else outer[1] if h > 1 else outer[0] if b > 1 else k
+    want = (h * q * ld, q * ld, ld)
+    if k > 1 and inner != 1 or ld < k or any(n > 1 and s != w for n, s, w in zip((b, h, q), outer, want)):
+        raise ValueError(f"{name} must have contiguous rows, evenly spaced")
+    return ld
+
+
+def _softmax_call(shape, table, buckets, lengths, causal, offset, p, seed, call, step, here):
+    """The descriptor of an attention softmax over checked arguments (without row strides)."""
+    import torch
+    b, h, q, k = shape
+    d = AttentionSoftmaxDesc(batch=b, heads=h, queries=q, keys=k, causal=1 if causal else 0,
+                             dropout=_drop(p, seed, call, step, here))
+    if table is not None:
+        if buckets is None:
+            raise ValueError("a table of biases needs the buckets of its distances")
+        if table.dim() != 2 or table.shape[1] != h or table.shape[0] < 1:
+            raise ValueError(f"table must be buckets x {h} heads, not {tuple(table.shape)}")
+        _vector("table", table, table.numel(), torch.float32, here)
+        d.num_buckets = table.shape[0]
+    if buckets is not None:
+        if buckets.numel() % 2 != 1:
+            raise ValueError("buckets must hold an odd number of values, from distance -D to D")
+        _vector("buckets", buckets, buckets.numel(), torch.int32, here)
+        d.max_distance = buckets.numel() // 2
+    if lengths is not None:
+        _vector("lengths", lengths, b, torch.int32, here)
+        d.lengths = lengths.data_ptr()
+    if isinstance(offset, int):
+        d.offset = offset
+    else:
+        _vector("offset", offset, b, torch.int32, here)
+        d.offsets = offset.data_ptr()
+    return d
+
+
+def attention_softmax(scores, *, table=None, buckets=None, lengths=None, causal=False, offset=0, p=0.0, seed=0, call=0,
+                      step=None, out=None):
+    """Softmax over the keys of scores [batch, heads, queries, keys] fp32: (probs, stats).
+
+    table [num_buckets, heads] fp32 and buckets (int32, 2 D + 1 values, see relative_buckets): a bias by the distance
+    between key and query, added to the scores.  lengths (int32 [batch]): keys from there on are not seen.  causal: keys
+    after the query's position are not seen.  offset: the position of the first query, an int or an int32 tensor
+    [batch] (a single token's place in its cache).  A row that sees no key is zeros.  p, seed, call, step: dropout of
+    the probabilities, as in dropout().  out: the tensor to write, which may be scores.
+    stats [batch, heads, queries, 2] is what attention_softmax_backward needs where p > 0."""
+    import torch
+    here = _current_device()
+    if scores.dim() != 4:
+        raise ValueError("scores must be [batch, heads, queries, keys]")
+    shape = scores.shape
+    ld = _score_rows("scores", scores, shape, here)
+    if (table is None) != (buckets is None):
+        raise ValueError("a bias needs both its table and the buckets of its distances")
+    d = _softmax_call(shape, table, buckets, lengths, causal, offset, p, seed, call, step, here)
+    d.ld_scores = ld
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=scores.device)
+    else:
+        d.ld_probs = _score_rows("out", out, shape, here)
+    stats = torch.empty((*shape[:3], 2), dtype=torch.float32, device=scores.device)
+    _check("amsim_attention_softmax_fwd",
+           lib().amsim_attention_softmax_fwd(ctypes.byref(d), scores.data_ptr(), _at(table), _at(buckets),
+                                             out.data_ptr(), stats.data_ptr(), _current_stream()))
+    if stats.numel() and not shape[3]:       # rows without keys
+        stats[..., 0], stats[..., 1] = -float("inf"), 0.0
+    return out, stats
+
+
+def attention_softmax_backward(dprobs, *, probs=None, scores=None, stats=None, table=None, buckets=None, lengths=None,
+                               causal=False, offset=0, p=0.0, seed=0, call=0, step=None, table_grad=True, out=None):
+    """Gradients of attention_softmax: (dscores, dtable), dtable None without a table or with table_grad false.
+
+    Without dropout from probs, the forward pass's output; with dropout from the scores and stats it was given and
+    left.  The other arguments are the forward pass's.  out: the tensor to write, which may be dprobs, probs or scores."""
+    import torch
+    here = _current_device()
+    if dprobs.dim() != 4:
+        raise ValueError("dprobs must be [batch, heads, queries, keys]")
+    shape = dprobs.shape
+    ld = _score_rows("dprobs", dprobs, shape, here)
+    if (probs is None) == (scores is None) or (scores is None) != (stats is None):
+        raise ValueError("the gradient is taken from probs, or from scores with their stats")
+    if probs is not None and p > 0.0:
+        raise ValueError("with dropout the gradient needs the scores and stats: dropped probabilities are gone")
+    d = _softmax_call(shape, table, buckets, lengths, causal, offset, p, seed, call, step, here)
+    d.ld_dprobs = ld
+    if probs is not None:
+        d.ld_probs = _score_rows("probs", probs, shape, here)
+    else:
+        d.ld_scores = _score_rows("scores", scores, shape, here)
+        _vector("stats", stats, 2 * shape[0] * shape[1] * shape[2], torch.float32, here)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=dprobs.device)
+    else:
+        d.ld_dscores = _score_rows("out", out, shape, here)
+    dtable = torch.empty_like(table) if table is not None and table_grad else None
+    nb = amsim_attention_softmax_workspace_size(d) if dtable is not None else 0
+    ws = torch.empty(nb, dtype=torch.uint8, device=dprobs.device) if nb else None
+    _check("amsim_attention_softmax_bwd",
+           lib().amsim_attention_softmax_bwd(ctypes.byref(d), dprobs.data_ptr(), _at(scores), _at(stats), _at(probs),
+                                             None if probs is not None else _at(table), _at(buckets), out.data_ptr(),
+                                             _at(dtable), _at(ws), nb, _current_stream()))
+    return out, dtable
+
+
+def _pixels(name, t, here, shape=None) -> int:
+    """Pixel stride of a [batch, ..., channels] tensor whose pixels are evenly spaced and their channels contiguous."""
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be of shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != here:
+        raise _elsewhere(name, t, here)
+    c = t.shape[-1]
+    if t.is_contiguous():
+        return c
+    strides = t.stride()
+    ld, at = None, 1
+    for n, s in zip(reversed(t.shape[:-1]), reversed(strides[:-1])):
+        if n > 1:
+            ld = s // at if ld is None else ld
+            if s != ld * at:
+                ld = -1
+        at *= n
+    ld = c if ld is None else ld
+    if c > 1 and strides[-1] != 1 or ld < c:
+        raise ValueError(f"{name} must have contiguous channels and evenly spaced pixels")
+    return ld
+
+
+@functools.lru_cache(maxsize=1024)
+def _group_norm_plan(batch, pixels, channels, groups, x, y, activation, eps, lddx, which):
+    """(descriptor by reference, scratch bytes); x, y: (type, pixel stride)."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, not {activation!r}")
+    d = GroupNormDesc(batch=batch, pixels=pixels, channels=channels, groups=groups, x_type=x[0], ldx=x[1], y_type=y[0],
+                      ldy=y[1], lddx=lddx, activation=ACTIVATIONS[activation], eps=eps)
+    return ctypes.byref(d), amsim_group_norm_workspace_size(d, which)
+
+
+def _norm_shape(x, groups, w, b, here):
+    import torch
+    if x.dim() < 2:
+        raise ValueError("group norms take [batch, ..., channels]")
+    batch, channels = x.shape[0], x.shape[-1]
+    if groups < 1 or channels < 1 or channels % groups:
+        raise ValueError(f"{groups} groups do not divide {channels} channels")
+    if w is not None:
+        _vector("w", w, channels, torch.float32, here)
+    if b is not None:
+        _vector("b", b, channels, torch.float32, here)
+    pixels = 1
+    for n in x.shape[1:-1]:
+        pixels *= n
+    return batch, pixels, channels
+
+
+def group_norm(x, groups, w=None, b=None, *, eps=1e-5, activation="none", y_dtype=None):
+    """y = act(xh w + b), xh = x normalised over each group of a sample's channels and all its pixels: (y, mean, rstd).
+
+    x: [batch, ..., channels] fp32 or bf16, channels last; w, b: [channels] fp32, or None (ones, zeros); activation:
+    "none", "relu" or "silu"; y has x's shape and type `y_dtype` (x's).  mean, rstd: [batch, groups] fp32."""
+    import torch
+    here = _current_device()
+    batch, pixels, channels = _norm_shape(x, groups, w, b, here)
+    empty, device = torch.empty, x.device
+    xs = (_dtype(x), _pixels("x", x, here))
+    y = empty(x.shape, dtype=y_dtype or x.dtype, device=device)
+    desc, nb = _group_norm_plan(batch, pixels, channels, groups, xs, (_dtype(y), 0), activation, eps, 0, 0)
+    mean, rstd = (empty((batch, groups), dtype=torch.float32, device=device) for _ in range(2))
+    ws = empty(nb, dtype=torch.uint8, device=device) if nb else None
+    _check("amsim_group_norm_fwd",
+           lib().amsim_group_norm_fwd(desc, x.data_ptr(), _at(w), _at(b), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                      _at(ws), nb, _current_stream()))
+    return y, mean, rstd
+
+
+def group_norm_backward(dy, x, w, b, mean, rstd, *, activation="none"):
+    """Gradients of group_norm: (dx, dw, db), None where there was no such input.  mean and rstd are group_norm's."""
+    import torch
+    here = _current_device()
+    if mean.dim() != 2:
+        raise ValueError("mean must be [batch, groups]")
+    groups = mean.shape[1]
+    batch, pixels, channels = _norm_shape(x, groups, w, b, here)
+    _vector("mean", mean, batch * groups, torch.float32, here)
+    _vector("rstd", rstd, batch * groups, torch.float32, here)
+    xs, ys = (_dtype(x), _pixels("x", x, here)), (_dtype(dy), _pixels("dy", dy, here, x.shape))
+    empty, device = torch.empty, x.device
+    desc, nb = _group_norm_plan(batch, pixels, channels, groups, xs, ys, activation, 0.0, 0, 1)
+    dx = empty(x.shape, dtype=x.dtype, device=device)
+    dw = None if w is None else torch.empty_like(w)
+    db = None if b is None else torch.empty_like(b)
+    ws = empty(nb, dtype=torch.uint8, device=device) if nb else None
+    _check("amsim_group_norm_bwd",
+           lib().amsim_group_norm_bwd(desc, dy.data_ptr(), x.data_ptr(), _at(w), _at(b), mean.data_ptr(),
+                                      rstd.data_ptr(), dx.data_ptr(), _at(dw), _at(db), _at(ws), nb, _current_stream()))
+    return dx, dw, db

@@ -731,6 +731,149 @@ int amsim_adamw_step(int count, const amsim_adamw_tensor *tensors, const amsim_a
 int amsim_adamw_moment_values(const void *codes, const float *scales, int second, int64_t n, float *out,
                               amsim_stream_t stream);
 
+/* ------------------------------------------------------------------ exact operators between two contractions */
+
+/*
+ * What stands between the simulated contractions of attention and of
+ * convolutions: attention's softmax with a learned relative position bias,
+ * key lengths, a causal mask and dropout; dropout of a tensor; the group norm
+ * with its activation.  None of them is simulated: all arithmetic is IEEE fp32
+ * and a bf16 result is rounded once, to nearest even.
+ *
+ * Random numbers: Philox4x32-10 (Salmon et al., SC 2011) with the key `seed`
+ * and the counter (quad, call + *step), 64 bits each, gives the four 32-bit
+ * words of a quad of elements.  An element stays when its word is at least
+ * p 2^32 (rounded to a whole number) and is then multiplied by 1 / (1 - p),
+ * else it is zero.  No mask is stored: the backward pass draws it again from
+ * the same seed, call and step.  `step` (one device value, or null: 0) lets a
+ * captured graph draw new numbers each time it is launched.
+ */
+typedef struct amsim_dropout_desc {
+    double p;                        /* 0 <= p < 1; 0: everything stays, nothing is drawn */
+    uint64_t seed, call;
+    const int64_t *step;
+} amsim_dropout_desc;
+
+/*
+ * y[i] = residual[i] + (stays(i) ? x[i] / (1 - p) : 0), i < n; element i is
+ * number i % 4 of quad i / 4.  x, residual (or null: zeros) and y are of one
+ * type and contiguous; y may alias either.  The gradient of x is this same
+ * call on the gradient of y, without a residual.  A dropped element adds
+ * nothing whatever it holds.  An input of NaN that stays is NaN.
+ * Errors: AMSIM_EINVAL for a p outside [0, 1), n < 0, a bad type, a null x or
+ * y with n > 0, or a pointer off its element's alignment.
+ */
+int amsim_dropout(const amsim_dropout_desc *desc, int type, int64_t n, const void *x, const void *residual, void *y,
+                  amsim_stream_t stream);
+
+/*
+ * The softmax between attention's contractions.  Row (b, h, i) of
+ * batch x heads x queries rows of `keys` scores; the row's query is at
+ * position pos = (offsets ? offsets[b] : offset) + i, key j at position j:
+ *   visible(j): j < lengths[b] (without lengths: keys) and, if causal, j <= pos
+ *   a[j] = scores[j] + table[buckets[clamp(j - pos, -D, D) + D] * heads + h]
+ *   P[j] = exp(a[j] - max) / sum exp(a - max) over the visible j, else 0
+ *   probs[j] = dropout of P[j]: number j % 4 of quad row * ceil(keys / 4) + j / 4
+ * with D = max_distance.  A row that sees no key, or whose visible scores are
+ * all -infinity, is zeros; a NaN or +infinity among its visible scores makes
+ * its visible probabilities NaN.  Scores of keys that are not visible are not
+ * looked at.  `buckets` holds 2 D + 1 bucket numbers, from distance -D to D;
+ * a number outside [0, num_buckets) means no bias (and no gradient) there.
+ */
+typedef struct amsim_attention_softmax_desc {
+    int64_t batch, heads, queries, keys;
+    int64_t ld_scores, ld_probs;     /* row strides in elements, >= keys; 0: keys */
+    int64_t ld_dprobs, ld_dscores;
+    int64_t offset;                  /* position of the first query, where offsets is null */
+    const int32_t *lengths;          /* `batch` values (below 0 acts as 0), or null */
+    const int32_t *offsets;          /* `batch` values, or null */
+    int causal;                      /* 0 or 1 */
+    int num_buckets, max_distance;   /* of the bias: >= 1, and 0 .. AMSIM_MAX_DISTANCE; without a table not looked at */
+    int reserved;                    /* 0 */
+    amsim_dropout_desc dropout;
+} amsim_attention_softmax_desc;
+#define AMSIM_MAX_DISTANCE 1024
+
+/*
+ * Forward.  table: num_buckets x heads, buckets: 2 max_distance + 1 (both, or
+ * both null: no bias).  probs is written whole and may alias scores (equal
+ * strides).  stats (or null): two values a row for the backward pass, the
+ * largest a[j] and 1 / sum; a row of zeros has (-infinity, 0).
+ * Errors: AMSIM_EINVAL for null scores or probs, a bad size, stride, p or flag, or one of
+ * table and buckets alone; AMSIM_EUNSUPPORTED for a max_distance above
+ * AMSIM_MAX_DISTANCE.  Without rows or keys it is a no-op.
+ */
+int amsim_attention_softmax_fwd(const amsim_attention_softmax_desc *desc, const float *scores, const float *table,
+                                const int32_t *buckets, float *probs, float *stats, amsim_stream_t stream);
+
+/*
+ * Backward, with g = dropout of dprobs (the forward pass's mask):
+ *   dscores[j] = P[j] (g[j] - sum_k P[k] g[k]),
+ *   dtable[k, h] = sum over the rows of head h and the j in bucket k of dscores[j].
+ * P comes from probs, which without dropout are P themselves (scores, stats
+ * and table then null), or from scores and stats (with dropout; probs null),
+ * with the same table as forward.  dscores is written whole, zero where a key
+ * is not visible, and may alias dprobs, probs or scores (equal strides).
+ * dtable (or null) needs buckets; its sums are kept per share of a head's rows
+ * in scratch and added in share order.  Without rows or keys dtable is zeros.
+ * Scratch: amsim_attention_softmax_workspace_size; with less (even none) a
+ * call uses fewer shares, down to one a head.
+ * Errors: as above, and AMSIM_EINVAL for neither or both of scores and probs,
+ * probs with p > 0, scores without stats, or a dtable without buckets.
+ */
+int amsim_attention_softmax_bwd(const amsim_attention_softmax_desc *desc, const float *dprobs, const float *scores,
+                                const float *stats, const float *probs, const float *table, const int32_t *buckets,
+                                float *dscores, float *dtable, void *ws, size_t ws_bytes, amsim_stream_t stream);
+
+/* Bytes of scratch with which a backward pass with a dtable fills the GPU. */
+size_t amsim_attention_softmax_workspace_size(const amsim_attention_softmax_desc *desc);
+
+/*
+ * The group norm with its activation, channels last.  x is batch x pixels x
+ * channels; group g of `groups` holds channels / groups consecutive channels:
+ *   mean, var: over the pixels and channels of (n, g) (var divides by their number),
+ *   rstd = 1 / sqrt(var + eps),  xh = (x - mean) rstd,  z = xh w + b,  y = act(z).
+ * Squares are summed about a value near the mean, so a mean that is large
+ * against the deviation costs no digits.  w and b (or null: ones, zeros) are
+ * fp32.  A non-finite value makes its whole group NaN.
+ */
+enum amsim_activation { AMSIM_ACT_NONE = 0, AMSIM_ACT_RELU = 1, AMSIM_ACT_SILU = 2 };
+typedef struct amsim_group_norm_desc {
+    int64_t batch, pixels;
+    int64_t ldx, ldy, lddx;          /* strides between pixels in elements (ldy: of y and of dy), >= channels; 0: channels */
+    int channels, groups;            /* groups divides channels */
+    int x_type, y_type;              /* amsim_dtype of x, dx; of y, dy */
+    int activation;                  /* amsim_activation */
+    float eps;                       /* >= 0 */
+} amsim_group_norm_desc;
+
+/*
+ * Forward.  y is written and may alias x (equal types and strides); mean,
+ * rstd: batch x groups values, written for the backward pass.  Scratch:
+ * amsim_group_norm_workspace_size(desc, 0) or more, else AMSIM_EINVAL.
+ * Errors: AMSIM_EINVAL also for a null x, y, mean or rstd, or a bad size,
+ * stride, type, activation or eps.  Without a batch it is a no-op; without
+ * pixels mean is 0 and rstd 1 / sqrt(eps).
+ */
+int amsim_group_norm_fwd(const amsim_group_norm_desc *desc, const void *x, const float *w, const float *b, void *y,
+                         float *mean, float *rstd, void *ws, size_t ws_bytes, amsim_stream_t stream);
+
+/*
+ * Backward, with dz = dy act'(z) (0 for relu where z <= 0; z's sign is taken
+ * from more than 32 bits where these do not decide it) and t = dz w:
+ *   dx = rstd (t - mean(t) - xh mean(t xh)),  means over the group,
+ *   dw = sum over batch and pixels of dz xh,  db = the same sum of dz.
+ * dx is written and may alias dy or x (equal types and strides); dw, db: or
+ * null.  Sums are kept per share and added in a fixed order.  Without a batch
+ * or pixels dw and db are zeros.  Scratch as above with which = 1.
+ */
+int amsim_group_norm_bwd(const amsim_group_norm_desc *desc, const void *dy, const void *x, const float *w,
+                         const float *b, const float *mean, const float *rstd, void *dx, float *dw, float *db,
+                         void *ws, size_t ws_bytes, amsim_stream_t stream);
+
+/* Bytes of scratch of the two calls (which: 0 forward, 1 backward); 0 for an invalid descriptor. */
+size_t amsim_group_norm_workspace_size(const amsim_group_norm_desc *desc, int which);
+
 #ifdef __cplusplus
 }
 #endif
