@@ -15,7 +15,10 @@ attention takes Q, K, V as [batch, heads, seq, dim].
 Between and after the approximate layers of a language model stand exact ones,
 which are not products of the simulated multiplier: BlockNorm (the norms
 around a block with its gate and the residual scale) and VocabHead (the loss
-over the vocabulary); their optimizer is optim.AdamW.
+over the vocabulary); their optimizer is optim.AdamW.  Between two
+contractions stand, exact as well: in attention a softmax with a learned bias by
+distance (RelativeBias), key lengths, a causal mask and dropout; GroupNorm with
+its activation between convolutions; Dropout after either.
 
 Operand order of every contraction (which operand indexes the LUT's rows;
 it matters only for an asymmetric user LUT): Dense forward (x, w), input
@@ -30,7 +33,8 @@ import math
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (ConvDesc, block_norm, block_norm_backward, vocab_loss, vocab_loss_grad, amsim_conv2d_bwd_data, amsim_conv2d_bwd_filter, amsim_conv2d_fwd, amsim_conv2d_out_hw,
+from . import (ConvDesc, attention_softmax, attention_softmax_backward, block_norm, block_norm_backward, dropout,
+               group_norm, group_norm_backward, relative_buckets, vocab_loss, vocab_loss_grad, amsim_conv2d_bwd_data, amsim_conv2d_bwd_filter, amsim_conv2d_fwd, amsim_conv2d_out_hw,
                amsim_conv2d_workspace_size, amsim_dwconv2d_bwd_data, amsim_dwconv2d_bwd_filter, amsim_dwconv2d_fwd,
                amsim_dwconv2d_workspace_size, amsim_gemm, amsim_gemm_strided_batched, amsim_gemm_workspace_size,
                amsim_softmax_rows, amsim_softmax_rows_backward, workspace)
@@ -264,24 +268,224 @@ class _AttentionFn(torch.autograd.Function):
         return dQ.reshape(b, h, s, d), dK.reshape(b, h, t, d), dV.reshape(b, h, t, d), None, None
 
 
-def am_attention(q, k, v, lut, scale: float | None = None):
+def _seen_only(t, lengths):
+    """[batch, heads, keys, dim] with zeros for the keys from a sequence's length on: a simulated product of a zero
+    probability with a padded key's infinity would be NaN."""
+    hidden = torch.arange(t.shape[2], device=t.device) >= lengths[:, None]
+    return t.masked_fill(hidden[:, None, :, None], 0.0)
+
+
+class _MaskedAttentionFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, table, lut, scale, buckets, lengths, offset, step, causal, p, seed, call):
+        q, k, v = _f32(q), _f32(k), _f32(v)
+        if lengths is not None:
+            k, v = _seen_only(k, lengths), _seen_only(v, lengths)
+        b, h, s, d = q.shape
+        t = k.shape[2]
+        qf, kf, vf = q.reshape(b * h, s, d), k.reshape(b * h, t, d), v.reshape(b * h, t, d)
+        S = _bgemm("N", "T", qf, kf, s, t, d, lut, alpha=scale).view(b, h, s, t)
+        args = dict(buckets=buckets, lengths=lengths, causal=causal, offset=offset, p=p, seed=seed, call=call, step=step)
+        P, stats = attention_softmax(S, table=table, out=None if p else S, **args)   # dropped ones are gone: S stays
+        O = _bgemm("N", "N", P.view(b * h, s, t), vf, s, d, t, lut)
+        keep = [buckets, lengths, step, offset if isinstance(offset, torch.Tensor) else None]
+        ctx.save_for_backward(qf, kf, vf, P, *((S, stats) if p else (None, None)), table, *keep)
+        ctx.lut, ctx.scale, ctx.shape, ctx.args = lut, scale, (b, h, s, t, d), args
+        return O.reshape(b, h, s, d)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dO):
+        qf, kf, vf, P, S, stats, table, *_ = ctx.saved_tensors
+        b, h, s, t, d = ctx.shape
+        lut, scale = ctx.lut, ctx.scale
+        dOf = _f32(dO).reshape(b * h, s, d)
+        dV = _bgemm("T", "N", P.view(b * h, s, t), dOf, t, d, s, lut)
+        dP = _bgemm("N", "T", dOf, vf, s, t, d, lut).view(b, h, s, t)
+        source = dict(probs=P) if S is None else dict(scores=S, stats=stats)
+        dS, dtable = attention_softmax_backward(dP, table=table, table_grad=ctx.needs_input_grad[3], out=dP, **source,
+                                                **ctx.args)
+        dS = dS.view(b * h, s, t)
+        dQ = _bgemm("N", "N", dS, kf, s, d, t, lut, alpha=scale)
+        dK = _bgemm("T", "N", dS, qf, t, d, s, lut, alpha=scale)
+        return dQ.reshape(b, h, s, d), dK.reshape(b, h, t, d), dV.reshape(b, h, t, d), dtable, *[None] * 10
+
+
+def am_attention(q, k, v, lut, scale: float | None = None, *, table=None, buckets=None, lengths=None, causal=False,
+                 offset=0, dropout: float = 0.0, seed: int = 0, call: int = 0, step=None):
     """softmax(scale q k^T) v per (batch, head), contractions approximate,
-    softmax exact; scale defaults to 1/sqrt(dim)."""
+    softmax exact; scale defaults to 1/sqrt(dim).
+
+    The rest is attention_softmax's, with `dropout` for its p: a bias by distance
+    (table, which gets a gradient, and buckets), lengths of the keys (cross
+    attention to a padded batch of another length; what k and v hold behind a
+    length has no effect and no gradient), a causal mask, the first query's
+    position, dropout of the probabilities."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
-    return _AttentionFn.apply(q, k, v, lut, float(scale))
+    if (table is None) != (buckets is None):
+        raise ValueError("a bias needs both its table and the buckets of its distances")
+    if table is None and lengths is None and not causal and dropout == 0.0:
+        return _AttentionFn.apply(q, k, v, lut, float(scale))
+    return _MaskedAttentionFn.apply(q, k, v, table, lut, float(scale), buckets, lengths, offset, step, bool(causal),
+                                    float(dropout), seed, call)
+
+
+class _Draws(torch.nn.Module):
+    """What a layer that draws keeps: a seed of its own and the number of its next call, both part of its state."""
+
+    def __init__(self, seed, generator):
+        super().__init__()
+        self.seed = int(torch.randint(0, 2 ** 62, (), generator=generator)) if seed is None else int(seed)
+        self.calls = 0
+
+    def get_extra_state(self):
+        return dict(seed=self.seed, calls=self.calls)
+
+    def set_extra_state(self, state):
+        self.seed, self.calls = state["seed"], state["calls"]
+
+    def next(self, call, step) -> dict:
+        """Seed and number of a call: the caller's number, or one more than the last."""
+        if call is None:
+            if step is None and torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a captured call draws the same mask at every replay: give it a step on the device")
+            call, self.calls = self.calls, self.calls + 1
+        return dict(seed=self.seed, call=call, step=step)
+
+
+class RelativeBias(torch.nn.Module):
+    """A learned bias for every head by the distance between key and query, in
+    buckets (relative_buckets); several layers may share one."""
+
+    def __init__(self, heads: int, buckets: int = 32, max_distance: int = 128, bidirectional: bool = True,
+                 device="cuda", generator: torch.Generator | None = None):
+        super().__init__()
+        self.table = torch.nn.Parameter((torch.randn((buckets, heads), generator=generator) * 0.1).to(device))
+        self.register_buffer("buckets", relative_buckets(buckets, max_distance, bidirectional).to(device),
+                             persistent=False)
 
 
 class AMAttention(torch.nn.Module):
     """Scaled dot-product attention over [batch, heads, seq, dim] tensors
-    with approximate contractions (no projections)."""
+    with approximate contractions (no projections).
 
-    def __init__(self, lut, scale: float | None = None):
+    bias: a RelativeBias or None; causal: keys after a query's position are not
+    seen; dropout: of the probabilities, in training.  forward(q, k, v,
+    lengths=None, offset=0) takes the keys' lengths (int32 [batch]: an encoder's
+    padded states) and the first query's position (an int, or int32 [batch]: a
+    single token's place in its cache).  Dropout draws a new mask at each call;
+    step (one int64 CUDA value, raised once a replay) does so for a captured
+    one, and call repeats a given call's mask (activation checkpointing)."""
+
+    def __init__(self, lut, scale: float | None = None, *, bias: RelativeBias | None = None, causal: bool = False,
+                 dropout: float = 0.0, seed: int | None = None, generator: torch.Generator | None = None):
         super().__init__()
-        self.lut, self.scale = lut, scale
+        if not 0.0 <= dropout < 1.0:
+            raise ValueError("dropout takes a p in [0, 1)")
+        self.lut, self.scale, self.bias, self.causal, self.dropout = lut, scale, bias, causal, float(dropout)
+        self.draws = _Draws(seed, generator) if dropout else None
 
-    def forward(self, q, k, v):
-        return am_attention(q, k, v, self.lut, self.scale)
+    def forward(self, q, k, v, lengths=None, offset=0, *, step=None, call=None):
+        table, buckets = (None, None) if self.bias is None else (self.bias.table, self.bias.buckets)
+        drawn = dict(dropout=self.dropout, **self.draws.next(call, step)) if self.draws and self.training else {}
+        return am_attention(q, k, v, self.lut, self.scale, table=table, buckets=buckets, lengths=lengths,
+                            causal=self.causal, offset=offset, **drawn)
+
+
+# ------------------------------------------------------------------ exact: dropout
+class _DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, step, p, seed, call):
+        ctx.save_for_backward(step)      # raised before backward, the mask would be another: torch then refuses
+        ctx.drawn = p, seed, call
+        return dropout(x.contiguous(), p, seed=seed, call=call, step=step,
+                       residual=None if residual is None else residual.contiguous())
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        (step,), (p, seed, call) = ctx.saved_tensors, ctx.drawn
+        dx = dropout(dy.contiguous(), p, seed=seed, call=call, step=step) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None, None
+
+
+def am_dropout(x, p: float, *, seed: int, call: int = 0, step=None, residual=None):
+    """residual + dropout(x), differentiable in both; the mask is a function of
+    (seed, call + step) and is drawn again in the backward pass."""
+    return _DropoutFn.apply(x, residual, step, float(p), seed, call)
+
+
+class Dropout(torch.nn.Module):
+    """forward(x, residual=None): in training residual + x / (1 - p) where x
+    stays and residual where it is dropped, with a new mask at each call; in
+    evaluation residual + x.  No mask is kept.  step and call: as AMAttention's."""
+
+    def __init__(self, p: float = 0.1, *, seed: int | None = None, generator: torch.Generator | None = None):
+        super().__init__()
+        if not 0.0 <= p < 1.0:
+            raise ValueError("dropout takes a p in [0, 1)")
+        self.p, self.draws = float(p), _Draws(seed, generator)
+
+    def forward(self, x, residual=None, *, step=None, call=None):
+        if not self.training or self.p == 0.0:
+            return x if residual is None else residual + x
+        return am_dropout(x, self.p, residual=residual, **self.draws.next(call, step))
+
+
+# ------------------------------------------------------------------ exact: group norm
+def _even_pixels(t: torch.Tensor) -> torch.Tensor:
+    """A tensor whose pixels are evenly spaced with contiguous channels: t (a slice of wider pixels, say), or a copy."""
+    if t.is_contiguous() or t.dim() < 2 or not t.numel():
+        return t.contiguous()
+    if t.shape[-1] == 1 or t.stride(-1) == 1:
+        ld = at = None
+        for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+            if n == 1:
+                continue
+            ld, at = (s, 1) if ld is None else (ld, at)
+            if s != ld * at:
+                return t.contiguous()
+            at *= n
+        if ld is None or ld >= t.shape[-1]:
+            return t
+    return t.contiguous()
+
+
+class _GroupNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, groups, eps, activation, y_dtype):
+        x = _even_pixels(x)
+        y, mean, rstd = group_norm(x, groups, w, b, eps=eps, activation=activation, y_dtype=y_dtype)
+        ctx.save_for_backward(x, w, b, mean, rstd)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, b, mean, rstd = ctx.saved_tensors
+        dx, dw, db = group_norm_backward(_even_pixels(dy), x, w, b, mean, rstd, activation=ctx.activation)
+        return dx, dw, db, None, None, None, None
+
+
+class GroupNorm(torch.nn.Module):
+    """Group norm with its activation over [batch, ..., channels] tensors:
+    forward(x) = act(xh weight + bias), with xh the channels of a group
+    normalised over all of a sample's pixels.  activation: "none", "relu" or
+    "silu"; y_dtype: the output's type (x's)."""
+
+    def __init__(self, groups: int, channels: int, *, activation: str = "none", eps: float = 1e-5, affine: bool = True,
+                 y_dtype=None, device="cuda"):
+        super().__init__()
+        if groups < 1 or channels % groups:
+            raise ValueError(f"{groups} groups do not divide {channels} channels")
+        self.groups, self.activation, self.eps, self.y_dtype = groups, activation, float(eps), y_dtype
+        self.weight = torch.nn.Parameter(torch.ones(channels, device=device)) if affine else None
+        self.bias = torch.nn.Parameter(torch.zeros(channels, device=device)) if affine else None
+
+    def forward(self, x):
+        return _GroupNormFn.apply(x, self.weight, self.bias, self.groups, self.eps, self.activation, self.y_dtype)
 
 
 # ------------------------------------------------------------------ exact: block norm
