@@ -1,4 +1,12 @@
 // The group norm with its activation, channels last, and its gradients.
+//
+// Two ways.  Where a slab (a sample's pixels over some whole groups, at least
+// 128 bytes of a pixel) fits the shared memory of a cluster, its blocks keep it
+// there: x (backward: x and dy) is read once and the result written, which is
+// all that has to move.  Each thread copies, sums and finishes pieces of its
+// own, so the copies need no barrier between threads; the blocks of a cluster
+// exchange the groups' sums through distributed shared memory.  Larger slabs go
+// through three launches that read x (and dy) twice.
 #include <algorithm>
 #include <cmath>
 
@@ -6,6 +14,7 @@
 
 #include "amsim_internal.h"
 #include "chained.cuh"
+#include "pairs.cuh"
 
 namespace {
 
@@ -18,6 +27,8 @@ struct Params {
     int64_t pixels, ldx, ldy, lddx, chunk;   // chunk: pixels of a share
     int batch, chunks, channels, groups, size;   // size: channels of a group
     int act, tx, tiles;                      // tx: threads side by side over channels
+    int slab, slab_groups, slabs, cluster;   // resident: channels and groups of a slab; blocks of a cluster,
+    int rows, step, steps;                   // pixels of a block, of its threads at once, of a thread
     float eps;
 };
 
@@ -54,34 +65,70 @@ struct Moments {
 };
 __device__ __forceinline__ Moments join(const Moments &a, const Moments &b)
 {
+    if (b.n == 0.0f) return a;
+    if (a.n == 0.0f) return b;
     const float n = a.n + b.n;
-    if (n == 0.0f) return a;
-    const float d = b.mean - a.mean, f = b.n / n;
+    const float d = b.mean - a.mean, f = __fdividef(b.n, n);
     return Moments{n, a.mean + d * f, a.m2 + b.m2 + d * d * (a.n * f)};
 }
 
-__device__ __forceinline__ float activate(float z, int act)
+// 1 / (1 + exp(-z)), from t = -z log2(e).  The approximate instructions' errors
+// are a rounding of t and some 2^-22, no more than z's own rounding leaves; expf
+// and an exact quotient take three times the instructions, and the kernels are
+// near the issue limit.
+constexpr float kMinusLog2E = -1.44269504088896341f;
+__device__ __forceinline__ float power_of_2(float t)
 {
-    if (act == AMSIM_ACT_RELU) return z < 0.0f ? 0.0f : z;
-    if (act == AMSIM_ACT_SILU) return z / (1.0f + expf(-z));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return e;
+}
+__device__ __forceinline__ float reciprocal(float d)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
+}
+__device__ __forceinline__ float sigmoid(float z) { return reciprocal(1.0f + power_of_2(z * kMinusLog2E)); }
+template <int ACT>
+__device__ __forceinline__ float activate(float z)
+{
+    if (ACT == AMSIM_ACT_RELU) return z < 0.0f ? 0.0f : z;
+    if (ACT == AMSIM_ACT_SILU) return z * sigmoid(z);
     return z;
+}
+
+// The activation as a constant of the loop that `use` holds.
+template <int ACT>
+struct Act {
+    static constexpr int value = ACT;
+};
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F use)
+{
+    if (act == AMSIM_ACT_RELU)
+        use(Act<AMSIM_ACT_RELU>{});
+    else if (act == AMSIM_ACT_SILU)
+        use(Act<AMSIM_ACT_SILU>{});
+    else
+        use(Act<AMSIM_ACT_NONE>{});
 }
 
 // dy act'(z).  relu's gradient jumps where z = 0: a z that its own roundings
 // (three of xh w, one of the sum: at most 2^-22 of the terms) could carry
 // across is computed again in 64 bits.
-__device__ __forceinline__ float before_activation(float dy, float x, float xh, float mean, float rstd, float w, float b,
-                                                   int act)
+template <int ACT>
+__device__ __forceinline__ float before_activation(float dy, float x, float xh, float mean, float rstd, float w, float b)
 {
-    if (act == AMSIM_ACT_NONE) return dy;
+    if (ACT == AMSIM_ACT_NONE) return dy;
     const float z = fmaf(xh, w, b);
-    if (act == AMSIM_ACT_RELU) {
+    if (ACT == AMSIM_ACT_RELU) {
         bool on = z > 0.0f;
         if (fabsf(z) <= 0x1p-21f * (fabsf(xh * w) + fabsf(b)))
             on = ((double)x - (double)mean) * (double)rstd * (double)w + (double)b > 0.0;
         return on ? dy : 0.0f;
     }
-    const float s = 1.0f / (1.0f + expf(-z));
+    const float s = sigmoid(z);
     return dy * (s * fmaf(z, 1.0f - s, 1.0f));
 }
 
@@ -204,14 +251,17 @@ __global__ void __launch_bounds__(kThreads) apply_kernel(const Params p)
     const TX *x = static_cast<const TX *>(p.x) + t.n * p.pixels * p.ldx + t.c;
     TY *y = static_cast<TY *>(p.y) + t.n * p.pixels * p.ldy + t.c;
     const Channels<E> k = channels<E>(p, t.n, t.c);
+    with_activation(p.act, [&](auto act) {
 #pragma unroll 4
-    for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
-        float v[E];
-        load<E>(x + i * p.ldx, v);
+        for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
+            float v[E];
+            load<E>(x + i * p.ldx, v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = activate(fmaf((v[e] - k.mean[e]) * k.rstd[e], k.w[e], k.b[e]), p.act);
-        store<E>(y + i * p.ldy, v);
-    }
+            for (int e = 0; e < E; ++e)
+                v[e] = activate<act.value>(fmaf((v[e] - k.mean[e]) * k.rstd[e], k.w[e], k.b[e]));
+            store<E>(y + i * p.ldy, v);
+        }
+    });
 }
 
 // Each channel's sums of dz and dz xh over a chunk of pixels.
@@ -225,19 +275,21 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const Params p)
         const TX *x = static_cast<const TX *>(p.x) + t.n * p.pixels * p.ldx + t.c;
         const TY *dy = static_cast<const TY *>(p.dy) + t.n * p.pixels * p.ldy + t.c;
         const Channels<E> k = channels<E>(p, t.n, t.c);
+        with_activation(p.act, [&](auto act) {
 #pragma unroll 2
-        for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
-            float v[E], d[E];
-            load<E>(x + i * p.ldx, v);
-            load<E>(dy + i * p.ldy, d);
+            for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
+                float v[E], d[E];
+                load<E>(x + i * p.ldx, v);
+                load<E>(dy + i * p.ldy, d);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float xh = (v[e] - k.mean[e]) * k.rstd[e];
-                const float dz = before_activation(d[e], v[e], xh, k.mean[e], k.rstd[e], k.w[e], k.b[e], p.act);
-                s[e].x += dz;
-                s[e].y = fmaf(dz, xh, s[e].y);
+                for (int e = 0; e < E; ++e) {
+                    const float xh = (v[e] - k.mean[e]) * k.rstd[e];
+                    const float dz = before_activation<act.value>(d[e], v[e], xh, k.mean[e], k.rstd[e], k.w[e], k.b[e]);
+                    s[e].x += dz;
+                    s[e].y = fmaf(dz, xh, s[e].y);
+                }
             }
-        }
+        });
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) all[e][threadIdx.x] = s[e];
@@ -330,19 +382,420 @@ __global__ void __launch_bounds__(kThreads) gradient_kernel(const Params p)
     float2 m[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) m[e] = p.means[(int64_t)t.n * p.groups + (t.c + e) / p.size];
+    with_activation(p.act, [&](auto act) {
 #pragma unroll 2
-    for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
-        float v[E], d[E];
-        load<E>(x + i * p.ldx, v);
-        load<E>(dy + i * p.ldy, d);
+        for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
+            float v[E], d[E];
+            load<E>(x + i * p.ldx, v);
+            load<E>(dy + i * p.ldy, d);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float xh = (v[e] - k.mean[e]) * k.rstd[e];
-            const float dz = before_activation(d[e], v[e], xh, k.mean[e], k.rstd[e], k.w[e], k.b[e], p.act);
-            v[e] = k.rstd[e] * (fmaf(dz, k.w[e], -m[e].x) - xh * m[e].y);
+            for (int e = 0; e < E; ++e) {
+                const float xh = (v[e] - k.mean[e]) * k.rstd[e];
+                const float dz = before_activation<act.value>(d[e], v[e], xh, k.mean[e], k.rstd[e], k.w[e], k.b[e]);
+                v[e] = k.rstd[e] * (fmaf(dz, k.w[e], -m[e].x) - xh * m[e].y);
+            }
+            store<E>(dx + i * p.lddx, v);
         }
-        store<E>(dx + i * p.lddx, v);
+    });
+}
+
+// ------------------------------------------------------------------ resident slabs
+constexpr int kSlabThreads = 256, kSlabBlocks = 2;       // blocks: of an SM
+constexpr int kSlabGroups = 64;              // at most: 128 bytes of bf16 channels, a group each
+
+__device__ __forceinline__ uint32_t shared_address(const void *q)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(q));
+}
+// BYTES from global to this thread's own slot; done after copies_wait.
+template <int BYTES>
+__device__ __forceinline__ void copy_in(uint8_t *to, const void *from)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared_address(to)), "l"(from) : "memory");
+    else if constexpr (BYTES >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(shared_address(to)), "l"(from), "n"(BYTES)
+                     : "memory");
+    else
+        *reinterpret_cast<uint16_t *>(to) = *static_cast<const uint16_t *>(from);
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// No block leaves while another reads its sums: it says that it has read, and
+// waits at its end for all to have said so.  Nothing it wrote is handed over,
+// so its stores are not waited for.
+__device__ __forceinline__ void cluster_has_read() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_leave() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+// A float2 of block `rank` of the cluster at the place of this block's `q`.
+__device__ __forceinline__ float2 of_rank(const float2 *q, int rank)
+{
+    uint32_t at;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(shared_address(q)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+// A thread's part of a slab: the channels of one piece, every `step`-th pixel
+// of the block's from `first` on.
+struct Part {
+    int n, c0, channels, groups;             // sample, first channel, channels and groups of the slab
+    int rank, wide, piece, row, step;        // wide: pieces of a pixel
+    int64_t first;                           // the block's first pixel
+    int rows, count;                         // the block's pixels, this thread's
+};
+template <int E>
+__device__ __forceinline__ Part part_of(const Params &p)
+{
+    Part t;
+    unsigned unit;
+    asm("mov.u32 %0, %%clusterid.x;" : "=r"(unit));
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(t.rank));
+    t.n = (int)(unit / (unsigned)p.slabs);
+    t.c0 = (int)(unit - (unsigned)t.n * (unsigned)p.slabs) * p.slab;
+    t.channels = p.slab;
+    t.groups = p.slab_groups;
+    t.step = p.step;
+    if (t.c0 + p.slab > p.channels) {        // the last slab is narrower
+        t.channels = p.channels - t.c0;
+        t.groups = t.channels / p.size;
+        t.step = kSlabThreads / (t.channels / E);
     }
+    t.wide = t.channels / E;
+    t.row = (int)(threadIdx.x / (unsigned)t.wide);
+    t.piece = (int)threadIdx.x - t.row * t.wide;
+    t.first = (int64_t)t.rank * p.rows;
+    t.rows = (int)max((int64_t)0, min((int64_t)p.rows, p.pixels - t.first));
+    t.count = t.row < t.step ? (int)((unsigned)max(0, t.rows - t.row + t.step - 1) / (unsigned)t.step) : 0;
+    return t;
+}
+
+// Packed arithmetic on a piece's values, two an instruction.
+template <int E>
+struct Values {
+    float2 v[(E + 1) / 2];
+};
+template <int E, typename F>
+__device__ __forceinline__ void each_pair(F use)
+{
+#pragma unroll
+    for (int i = 0; i < (E + 1) / 2; ++i) use(i);
+}
+template <int E, typename T>
+__device__ __forceinline__ Values<E> take(const void *slot)
+{
+    float f[E];
+    load<E>(static_cast<const T *>(slot), f);
+    Values<E> r;
+    each_pair<E>([&](int i) { r.v[i] = make_float2(f[2 * i], 2 * i + 1 < E ? f[2 * i + 1 < E ? 2 * i + 1 : 0] : 0.0f); });
+    return r;
+}
+template <int E, typename T>
+__device__ __forceinline__ void put(T *at, const Values<E> &r)
+{
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = e & 1 ? r.v[e >> 1].y : r.v[e >> 1].x;
+    store<E>(at, f);
+}
+
+using amsim::add2;
+using amsim::both;
+using amsim::fma2;
+using amsim::mul2;
+
+__device__ __forceinline__ float2 sigmoid2(float2 z)
+{
+    const float2 t = mul2(z, both(kMinusLog2E));
+    const float2 d = add2(make_float2(power_of_2(t.x), power_of_2(t.y)), both(1.0f));
+    return make_float2(reciprocal(d.x), reciprocal(d.y));
+}
+template <int ACT>
+__device__ __forceinline__ float2 activate2(float2 z)
+{
+    if (ACT == AMSIM_ACT_SILU) return mul2(z, sigmoid2(z));
+    return make_float2(activate<ACT>(z.x), activate<ACT>(z.y));
+}
+// before_activation of a pair.
+template <int ACT>
+__device__ __forceinline__ float2 before2(float2 dy, float2 x, float2 xh, float mean, float rstd, float2 w, float2 b)
+{
+    if (ACT == AMSIM_ACT_NONE) return dy;
+    if (ACT == AMSIM_ACT_RELU)
+        return make_float2(before_activation<ACT>(dy.x, x.x, xh.x, mean, rstd, w.x, b.x),
+                           before_activation<ACT>(dy.y, x.y, xh.y, mean, rstd, w.y, b.y));
+    const float2 z = fma2(xh, w, b), s = sigmoid2(z);
+    return mul2(mul2(dy, s), fma2(z, fma2(s, both(-1.0f), both(1.0f)), both(1.0f)));
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    return v;
+}
+
+// The copies are told apart in two halves, so that a thread sums what has
+// arrived while the rest is on its way.
+template <typename F>
+__device__ __forceinline__ void in_halves(int count, F use)
+{
+    const int half = (count + 1) >> 1;
+    copies_wait<1>();
+#pragma unroll 4
+    for (int i = 0; i < half; ++i) use(i);
+    copies_wait<0>();
+#pragma unroll 4
+    for (int i = half; i < count; ++i) use(i);
+}
+
+// Dynamic shared memory: the slots [steps][threads] of x (then of dy), then
+// (backward) sums by channel.  A piece lies within one group.
+template <typename TX, typename TY, int E>
+__global__ void __launch_bounds__(kSlabThreads, kSlabBlocks) slab_forward_kernel(const Params p)
+{
+    extern __shared__ __align__(16) uint8_t slots[];
+    __shared__ Moments all[kSlabThreads];
+    __shared__ float2 found[kSlabGroups], stats[kSlabGroups];
+    constexpr int bytes = E * (int)sizeof(TX);
+    const Part t = part_of<E>(p);
+    const int c = t.c0 + t.piece * E, mine = t.piece * E / p.size, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t pixel = t.n * p.pixels + t.first + t.row;
+    uint8_t *slot = slots + threadIdx.x * bytes;
+    {
+        const TX *x = static_cast<const TX *>(p.x) + pixel * p.ldx + c;
+        const int64_t far = (int64_t)t.step * p.ldx;
+        const int half = (t.count + 1) >> 1;
+#pragma unroll 4
+        for (int i = 0; i < half; ++i) copy_in<bytes>(slot + i * (kSlabThreads * bytes), x + i * far);
+        copies_commit();
+#pragma unroll 4
+        for (int i = half; i < t.count; ++i) copy_in<bytes>(slot + i * (kSlabThreads * bytes), x + i * far);
+        copies_commit();
+    }
+    // Sums about the thread's first value: what cancels is no larger than the
+    // values' own spread.
+    float2 s1 = both(0.0f), s2 = both(0.0f);
+    float about = 0.0f;
+    in_halves(t.count, [&](int i) {
+        const Values<E> r = take<E, TX>(slot + i * (kSlabThreads * bytes));
+        if (i == 0) about = r.v[0].x;
+        each_pair<E>([&](int j) {
+            float2 d = add2(r.v[j], both(-about));
+            if (E == 1) d.y = 0.0f;
+            s1 = add2(s1, d);
+            s2 = fma2(d, d, s2);
+        });
+    });
+    {
+        const float n = (float)(t.count * E), sum = s1.x + s1.y, m = t.count ? sum / n : 0.0f;
+        all[threadIdx.x] = Moments{n, about + m, fmaxf((s2.x + s2.y) - sum * m, 0.0f)};
+    }
+    __syncthreads();
+    // a warp per group joins its threads: pieces side by side, then rows
+    const int wide = p.size / E, threads = wide * t.step;
+    for (int g = warp; g < t.groups; g += kSlabThreads / 32) {
+        Moments m{0.0f, 0.0f, 0.0f};
+        for (int i = lane; i < threads; i += 32) {
+            const int row = (int)((unsigned)i / (unsigned)wide);
+            m = join(m, all[row * t.wide + g * wide + (i - row * wide)]);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            m = join(m, Moments{__shfl_down_sync(0xFFFFFFFFu, m.n, d), __shfl_down_sync(0xFFFFFFFFu, m.mean, d),
+                                __shfl_down_sync(0xFFFFFFFFu, m.m2, d)});
+        if (lane == 0) found[g] = make_float2(m.mean, m.m2);
+    }
+    if (p.cluster > 1)
+        cluster_barrier();
+    else
+        __syncthreads();
+    for (int g = threadIdx.x; g < t.groups; g += kSlabThreads) {
+        Moments m{0.0f, 0.0f, 0.0f};
+        for (int r = 0; r < p.cluster; ++r) {
+            const float2 f = p.cluster > 1 ? of_rank(&found[g], r) : found[g];
+            const int64_t rows = max((int64_t)0, min((int64_t)p.rows, p.pixels - (int64_t)r * p.rows));
+            m = join(m, Moments{(float)rows * (float)p.size, f.x, f.y});
+        }
+        const float2 f = make_float2(m.mean, 1.0f / sqrtf(m.m2 / m.n + p.eps));
+        stats[g] = f;
+        if (t.rank == 0) {
+            const int64_t at = (int64_t)t.n * p.groups + t.c0 / p.size + g;
+            p.mean[at] = f.x;
+            p.rstd[at] = f.y;
+        }
+    }
+    __syncthreads();
+    if (p.cluster > 1) cluster_has_read();
+    const float2 f = stats[mine];
+    float2 w[(E + 1) / 2], b[(E + 1) / 2];
+    each_pair<E>([&](int j) {
+        const bool two = 2 * j + 1 < E;
+        w[j] = p.w ? make_float2(p.w[c + 2 * j], two ? p.w[c + 2 * j + two] : 0.0f) : both(1.0f);
+        b[j] = p.b ? make_float2(p.b[c + 2 * j], two ? p.b[c + 2 * j + two] : 0.0f) : both(0.0f);
+        // z = x (rstd w) + (b - mean rstd w): what this rounds is of the size of what the mean's rounding leaves
+        w[j] = mul2(w[j], both(f.y));
+        b[j] = fma2(w[j], both(-f.x), b[j]);
+    });
+    TY *y = static_cast<TY *>(p.y) + pixel * p.ldy + c;
+    const int64_t far = (int64_t)t.step * p.ldy;
+    with_activation(p.act, [&](auto act) {
+#pragma unroll 4
+        for (int i = 0; i < t.count; ++i) {
+            Values<E> r = take<E, TX>(slot + i * (kSlabThreads * bytes));
+            each_pair<E>([&](int j) { r.v[j] = activate2<act.value>(fma2(r.v[j], w[j], b[j])); });
+            put<E>(y + i * far, r);
+        }
+    });
+    if (p.cluster > 1) cluster_leave();
+}
+
+template <typename TX, typename TY, int E>
+__global__ void __launch_bounds__(kSlabThreads, kSlabBlocks) slab_backward_kernel(const Params p)
+{
+    extern __shared__ __align__(16) uint8_t slots[];
+    __shared__ float2 sums[E][kSlabThreads], means[kSlabGroups];
+    constexpr int xb = E * (int)sizeof(TX), yb = E * (int)sizeof(TY);
+    // fp32 slots of x and dy give their places to xh and dz, so that these are computed once
+    constexpr bool kKeepY = sizeof(TY) == 4, kKeepX = kKeepY && sizeof(TX) == 4;
+    const Part t = part_of<E>(p);
+    const int c = t.c0 + t.piece * E, mine = t.piece * E / p.size, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t pixel = t.n * p.pixels + t.first + t.row;
+    uint8_t *sx = slots + threadIdx.x * xb, *sy = slots + p.steps * (kSlabThreads * xb) + threadIdx.x * yb;
+    float2 *by_channel = reinterpret_cast<float2 *>(slots + p.steps * (kSlabThreads * (xb + yb)));
+    {
+        const TX *x = static_cast<const TX *>(p.x) + pixel * p.ldx + c;
+        const TY *dy = static_cast<const TY *>(p.dy) + pixel * p.ldy + c;
+        const int64_t xfar = (int64_t)t.step * p.ldx, yfar = (int64_t)t.step * p.ldy;
+        auto copy = [&](int from, int to) {
+#pragma unroll 4
+            for (int i = from; i < to; ++i) {
+                copy_in<xb>(sx + i * (kSlabThreads * xb), x + i * xfar);
+                copy_in<yb>(sy + i * (kSlabThreads * yb), dy + i * yfar);
+            }
+            copies_commit();
+        };
+        copy(0, (t.count + 1) >> 1);
+        copy((t.count + 1) >> 1, t.count);
+    }
+    const int64_t group = (int64_t)t.n * p.groups + t.c0 / p.size + mine;
+    const float mean = p.mean[group], rstd = p.rstd[group];
+    float2 w[(E + 1) / 2], b[(E + 1) / 2];
+    each_pair<E>([&](int j) {
+        const bool two = 2 * j + 1 < E;
+        w[j] = p.w ? make_float2(p.w[c + 2 * j], two ? p.w[c + 2 * j + two] : 0.0f) : both(1.0f);
+        b[j] = p.b ? make_float2(p.b[c + 2 * j], two ? p.b[c + 2 * j + two] : 0.0f) : both(0.0f);
+    });
+    auto values = [&](auto act, int i, Values<E> &xh, Values<E> &dz) {
+        const Values<E> x = take<E, TX>(sx + i * (kSlabThreads * xb));
+        dz = take<E, TY>(sy + i * (kSlabThreads * yb));
+        each_pair<E>([&](int j) {
+            xh.v[j] = mul2(add2(x.v[j], both(-mean)), both(rstd));
+            dz.v[j] = before2<act.value>(dz.v[j], x.v[j], xh.v[j], mean, rstd, w[j], b[j]);
+        });
+    };
+    float2 s[(E + 1) / 2], q[(E + 1) / 2];
+    each_pair<E>([&](int j) { s[j] = q[j] = both(0.0f); });
+    with_activation(p.act, [&](auto act) {
+        in_halves(t.count, [&](int i) {
+            Values<E> xh, dz;
+            values(act, i, xh, dz);
+            if (kKeepX) put<E>(reinterpret_cast<TX *>(sx + i * (kSlabThreads * xb)), xh);
+            if (kKeepY) put<E>(reinterpret_cast<TY *>(sy + i * (kSlabThreads * yb)), dz);
+            each_pair<E>([&](int j) {
+                s[j] = add2(s[j], dz.v[j]);
+                q[j] = fma2(dz.v[j], xh.v[j], q[j]);
+            });
+        });
+    });
+    // over the rows of threads, in a fixed order: where a warp holds whole rows
+    // across its lanes first, then rows (or warps) across shared memory
+    int rows = t.step, row = t.row, apart = t.wide;
+    if (32 % t.wide == 0) {
+        for (int d = t.wide; d < 32; d <<= 1)
+            each_pair<E>([&](int j) {
+                s[j] = add2(s[j], make_float2(__shfl_xor_sync(0xFFFFFFFFu, s[j].x, d),
+                                              __shfl_xor_sync(0xFFFFFFFFu, s[j].y, d)));
+                q[j] = add2(q[j], make_float2(__shfl_xor_sync(0xFFFFFFFFu, q[j].x, d),
+                                              __shfl_xor_sync(0xFFFFFFFFu, q[j].y, d)));
+            });
+        rows = kSlabThreads / 32;
+        row = lane < t.wide ? warp : rows;
+        apart = 32;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        sums[e][threadIdx.x] = e & 1 ? make_float2(s[e >> 1].y, q[e >> 1].y) : make_float2(s[e >> 1].x, q[e >> 1].x);
+    while (rows > 1) {
+        const int half = (rows + 1) >> 1;
+        __syncthreads();
+        if (row + half < rows)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                sums[e][threadIdx.x] = add2(sums[e][threadIdx.x], sums[e][threadIdx.x + half * apart]);
+        rows = half;
+    }
+    if (row == 0)
+#pragma unroll
+        for (int e = 0; e < E; ++e) by_channel[t.piece * E + e] = sums[e][threadIdx.x];
+    if (p.cluster > 1)
+        cluster_barrier();
+    else
+        __syncthreads();
+    // the slab's sums by channel, over its blocks in their order; the group's means from them
+    for (int g = warp; g < t.groups; g += kSlabThreads / 32) {
+        float2 m = both(0.0f);
+        for (int i = lane; i < p.size; i += 32) {
+            const int at = g * p.size + i;
+            float2 v = both(0.0f);
+            if (p.cluster > 1)
+                for (int r = 0; r < p.cluster; ++r) v = add2(v, of_rank(&by_channel[at], r));
+            else
+                v = by_channel[at];
+            if (t.rank == 0) p.sums[(int64_t)t.n * p.channels + t.c0 + at] = v;
+            m = fma2(v, both(p.w ? p.w[t.c0 + at] : 1.0f), m);
+        }
+        m.x = warp_sum(m.x);
+        m.y = warp_sum(m.y);
+        const float count = (float)p.size * (float)p.pixels;
+        if (lane == 0) means[g] = make_float2(m.x / count, m.y / count);
+    }
+    __syncthreads();
+    if (p.cluster > 1) cluster_has_read();
+    // dx = dz (w rstd) - mean(t) rstd - xh (mean(t xh) rstd)
+    const float2 m = mul2(means[mine], both(-rstd));
+    each_pair<E>([&](int j) { s[j] = mul2(w[j], both(rstd)); });
+    TX *dx = static_cast<TX *>(p.dx) + pixel * p.lddx + c;
+    const int64_t far = (int64_t)t.step * p.lddx;
+    auto finish = [&](auto act) {
+#pragma unroll 4
+        for (int i = 0; i < t.count; ++i) {
+            Values<E> xh, dz;
+            if (kKeepY) {
+                xh = take<E, TX>(sx + i * (kSlabThreads * xb));
+                dz = take<E, TY>(sy + i * (kSlabThreads * yb));
+                if (!kKeepX) each_pair<E>([&](int j) { xh.v[j] = mul2(add2(xh.v[j], both(-mean)), both(rstd)); });
+            } else {
+                values(act, i, xh, dz);
+            }
+            each_pair<E>([&](int j) { dz.v[j] = fma2(xh.v[j], both(m.y), fma2(dz.v[j], s[j], both(m.x))); });
+            put<E>(dx + i * far, dz);
+        }
+    };
+    if (kKeepY)
+        finish(Act<AMSIM_ACT_NONE>{});
+    else
+        with_activation(p.act, finish);
+    if (p.cluster > 1) cluster_leave();
 }
 
 size_t type_size(int t) { return t == AMSIM_BF16 ? 2 : 4; }
@@ -389,6 +842,39 @@ void split(Params &p, int E, int sms)
     p.chunks = (int)std::max<int64_t>(1, (p.pixels + p.chunk - 1) / p.chunk);
 }
 
+// The resident way's shape, or false.  A slab is some 128 bytes of a pixel, in
+// whole groups; its cluster has as many blocks as hold it, and more where the
+// machine is not full and threads keep four pixels.  A slab that is too large
+// for eight blocks of which an SM takes two is taken narrower, or in larger blocks.
+constexpr int kHalfSm = 96 * 1024, kWholeSm = 200 * 1024;
+constexpr int kMaxCluster = 8;
+constexpr int kSums = 8;                     // bytes of a channel's sums, backward
+// E: of a piece; bytes: of an element on chip (x; backward x and dy); chan: of a channel's sums there
+bool resident(Params &p, int E, int bytes, int chan, int sms)
+{
+    struct Try {
+        int width, room;
+    };
+    for (const Try t : {Try{128, kHalfSm}, Try{64, kHalfSm}, Try{64, kWholeSm}, Try{32, kWholeSm}}) {
+        p.slab = std::min(p.channels, std::max(1, t.width / (bytes * p.size)) * p.size);
+        if (p.slab / E > kSlabThreads || p.slab / p.size > kSlabGroups) continue;
+        p.slab_groups = p.slab / p.size;
+        p.slabs = (p.channels + p.slab - 1) / p.slab;
+        const int step = p.step = kSlabThreads / (p.slab / E), most = (t.room - p.slab * chan) / (kSlabThreads * E * bytes);
+        if (most < 1) continue;
+        const int64_t need = (p.pixels + (int64_t)step * most - 1) / ((int64_t)step * most);
+        if (need > kMaxCluster) continue;
+        const int64_t units = (int64_t)p.batch * p.slabs;
+        const int64_t fill = std::min((2 * (int64_t)sms + units - 1) / units, p.pixels / (4 * step));
+        p.cluster = (int)std::max<int64_t>(need, std::min<int64_t>(kMaxCluster, fill));
+        while (p.cluster > need && (p.cluster & (p.cluster - 1))) --p.cluster;
+        p.rows = (int)((p.pixels + p.cluster - 1) / p.cluster);
+        p.steps = (p.rows + step - 1) / step;
+        if (units * p.cluster <= 0x7FFFFFFF) return true;
+    }
+    return false;
+}
+
 Params params(const amsim_group_norm_desc *d)
 {
     Params p{};
@@ -414,17 +900,46 @@ int start(bool chained, void (*kernel)(Params), dim3 grid, int threads, const Pa
     return rc;
 }
 
-template <typename TX, typename TY, int E>
-int forward(const Params &p, cudaStream_t st)
+int start_slabs(void (*kernel)(Params), const Params &p, int bytes, int chan, cudaStream_t st)
 {
-    if (int rc = start(false, moments_kernel<TX, E>, grid(p), kThreads, p, st)) return rc;
-    if (int rc = start(true, join_kernel, dim3((unsigned)(p.batch * p.groups)), kThreads, p, st)) return rc;
-    return start(true, apply_kernel<TX, TY, E>, grid(p), kThreads, p, st);
+    int rc = amsim::cuda_status(
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWholeSm));
+    if (!rc && p.cluster > 8)
+        rc = amsim::cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    if (rc) return rc;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)((int64_t)p.batch * p.slabs * p.cluster));
+    c.blockDim = dim3(kSlabThreads);
+    c.dynamicSmemBytes = (size_t)p.steps * kSlabThreads * bytes + (size_t)p.slab * chan;
+    c.stream = st;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = (unsigned)p.cluster;
+    a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+    c.attrs = a;
+    c.numAttrs = p.cluster > 1 ? 1 : 0;
+    rc = amsim::cuda_status(cudaLaunchKernelEx(&c, kernel, p));
+    if (rc == AMSIM_OK) amsim::count_launch();
+    return rc;
 }
 
 template <typename TX, typename TY, int E>
-int backward(const Params &p, cudaStream_t st)
+int slab_pass(bool fwd, const Params &p, cudaStream_t st)
 {
+    if (fwd) return start_slabs(slab_forward_kernel<TX, TY, E>, p, E * (int)sizeof(TX), 0, st);
+    const int rc = start_slabs(slab_backward_kernel<TX, TY, E>, p, E * (int)(sizeof(TX) + sizeof(TY)), kSums, st);
+    if (rc || (!p.dw && !p.db)) return rc;
+    return start(true, weights_kernel, dim3((unsigned)((p.channels + 31) / 32)), 1024, p, st);
+}
+
+template <typename TX, typename TY, int E>
+int wide_pass(bool fwd, const Params &p, cudaStream_t st)
+{
+    if (fwd) {
+        if (int rc = start(false, moments_kernel<TX, E>, grid(p), kThreads, p, st)) return rc;
+        if (int rc = start(true, join_kernel, dim3((unsigned)(p.batch * p.groups)), kThreads, p, st)) return rc;
+        return start(true, apply_kernel<TX, TY, E>, grid(p), kThreads, p, st);
+    }
     if (int rc = start(false, sums_kernel<TX, TY, E>, grid(p), kThreads, p, st)) return rc;
     if (int rc = start(true, means_kernel, dim3((unsigned)(p.batch * p.groups)), kThreads, p, st)) return rc;
     if (int rc = start(true, gradient_kernel<TX, TY, E>, grid(p), kThreads, p, st)) return rc;
@@ -432,17 +947,41 @@ int backward(const Params &p, cudaStream_t st)
     return start(false, weights_kernel, dim3((unsigned)((p.channels + 31) / 32)), 1024, p, st);
 }
 
-template <int EB, int EF>
-int run(bool fwd, const amsim_group_norm_desc *d, const Params &p, cudaStream_t st)
+template <typename TX, typename TY>
+int pass(bool fwd, int E, const Params &p, cudaStream_t st)
+{
+    constexpr int most = sizeof(TX) + sizeof(TY) == 4 ? 8 : 4;   // 16 bytes of the wider type
+    if (p.cluster)
+        return E == 4   ? slab_pass<TX, TY, 4>(fwd, p, st)
+               : E == 2 ? slab_pass<TX, TY, 2>(fwd, p, st)
+                        : slab_pass<TX, TY, 1>(fwd, p, st);
+    return E == most ? wide_pass<TX, TY, most>(fwd, p, st) : wide_pass<TX, TY, 1>(fwd, p, st);
+}
+
+// The way a call goes: slabs in pieces of up to four channels that lie within
+// one group, else whole pieces of 16 bytes, or single channels.  `fits(E)`: the
+// call's rows are on E elements.
+template <typename F>
+int plan(const amsim_group_norm_desc *d, bool fwd, int sms, Params &p, F fits)
+{
+    const int bytes = (int)(type_size(d->x_type) + (fwd ? 0 : type_size(d->y_type)));
+    int E = 4;
+    while (E > 1 && (p.size % E || !fits(E))) E /= 2;
+    if (resident(p, E, bytes, fwd ? 0 : kSums, sms)) return E;
+    p.cluster = 0;
+    E = piece(d);
+    if (d->channels % E || !fits(E)) E = 1;
+    split(p, E, sms);
+    return E;
+}
+
+int run(const amsim_group_norm_desc *d, bool fwd, int E, const Params &p, cudaStream_t st)
 {
     using B = __nv_bfloat16;
     if (d->x_type == AMSIM_F32)
-        return d->y_type == AMSIM_F32 ? (fwd ? forward<float, float, EF>(p, st) : backward<float, float, EF>(p, st))
-                                      : (fwd ? forward<float, B, EF>(p, st) : backward<float, B, EF>(p, st));
-    return d->y_type == AMSIM_F32 ? (fwd ? forward<B, float, EF>(p, st) : backward<B, float, EF>(p, st))
-                                  : (fwd ? forward<B, B, EB>(p, st) : backward<B, B, EB>(p, st));
+        return d->y_type == AMSIM_F32 ? pass<float, float>(fwd, E, p, st) : pass<float, B>(fwd, E, p, st);
+    return d->y_type == AMSIM_F32 ? pass<B, float>(fwd, E, p, st) : pass<B, B>(fwd, E, p, st);
 }
-
 }  // namespace
 
 extern "C" size_t amsim_group_norm_workspace_size(const amsim_group_norm_desc *d, int which)
@@ -451,9 +990,9 @@ extern "C" size_t amsim_group_norm_workspace_size(const amsim_group_norm_desc *d
     const int sms = device_sms();
     Params p = params(d);
     size_t most = 0;
-    for (int E : {1, piece(d)}) {                // the calls' pointers decide which
-        split(p, E, sms ? sms : 1);
-        most = std::max(most, (size_t)p.batch * p.chunks * p.channels);
+    for (int on : {1, 2, 4, 8}) {                // the calls' pointers and strides decide which
+        plan(d, !which, sms ? sms : 1, p, [&](int E) { return E <= on; });
+        if (!p.cluster) most = std::max(most, (size_t)p.batch * p.chunks * p.channels);
     }
     return (most + (which ? (size_t)p.batch * (p.channels + p.groups) : 0)) * sizeof(float2);
 }
@@ -469,7 +1008,8 @@ extern "C" int amsim_group_norm_fwd(const amsim_group_norm_desc *d, const void *
     if (!aligned(x, xs) || !aligned(y, ys) || !aligned(ws, 8)) return AMSIM_EINVAL;
     for (const float *f : {w, b, (const float *)mean, (const float *)rstd})
         if (!aligned(f, 4)) return AMSIM_EINVAL;
-    if (d->pixels && (!ws || ws_bytes < amsim_group_norm_workspace_size(d, 0))) return AMSIM_EINVAL;
+    const size_t need = d->pixels ? amsim_group_norm_workspace_size(d, 0) : 0;
+    if (need && (!ws || ws_bytes < need)) return AMSIM_EINVAL;
     Params p = params(d);
     p.x = x;
     p.y = y;
@@ -482,10 +1022,8 @@ extern "C" int amsim_group_norm_fwd(const amsim_group_norm_desc *d, const void *
     const int sms = device_sms();
     if (!sms) return AMSIM_ECUDA;
     if (!d->pixels) return start(false, join_kernel, dim3((unsigned)(p.batch * p.groups)), kThreads, p, st);
-    const int E = piece(d);
-    const bool vec = d->channels % E == 0 && whole(x, p.ldx, xs, E) && whole(y, p.ldy, ys, E);
-    split(p, vec ? E : 1, sms);
-    return vec ? run<8, 4>(true, d, p, st) : run<1, 1>(true, d, p, st);
+    const int E = plan(d, true, sms, p, [&](int n) { return whole(x, p.ldx, xs, n) && whole(y, p.ldy, ys, n); });
+    return run(d, true, E, p, st);
 }
 
 extern "C" int amsim_group_norm_bwd(const amsim_group_norm_desc *d, const void *dy, const void *x, const float *w,
@@ -520,12 +1058,11 @@ extern "C" int amsim_group_norm_bwd(const amsim_group_norm_desc *d, const void *
     p.db = db;
     const int sms = device_sms();
     if (!sms) return AMSIM_ECUDA;
-    const int E = piece(d);
-    const bool vec = d->channels % E == 0 && whole(x, p.ldx, xs, E) && whole(dx, p.lddx, xs, E) &&
-                     whole(dy, p.ldy, ys, E);
-    split(p, vec ? E : 1, sms);
+    const int E = plan(d, false, sms, p, [&](int n) {
+        return whole(x, p.ldx, xs, n) && whole(dx, p.lddx, xs, n) && whole(dy, p.ldy, ys, n);
+    });
     p.sums = static_cast<float2 *>(ws);
     p.means = p.sums + (size_t)p.batch * p.channels;
     p.part = p.means + (size_t)p.batch * p.groups;
-    return vec ? run<8, 4>(false, d, p, st) : run<1, 1>(false, d, p, st);
+    return run(d, false, E, p, st);
 }
