@@ -1,211 +1,394 @@
 // The softmax between attention's contractions, with a relative position bias,
 // lengths, a causal mask and dropout, and its gradient with the bias table's.
 //
-// A row is read once and kept in registers, a quad of columns at a time per
-// thread, so the traffic is the compulsory one: scores in, probabilities out.
+// A row is read once and kept in registers, so the traffic is the compulsory
+// one.  It is taken in chunks of 128 columns, a chunk by a warp: up to 512
+// columns one warp has the whole row, longer rows are shared by the warps of a
+// block and then by the blocks of a cluster, whose maxima and sums are joined
+// once per row (each warp's exponentials are relative to its own maximum until
+// then).  Rows beyond what a cluster's registers hold are read twice.
+//
+// Within a chunk a lane has four columns: neighbours where rows are on 16 bytes
+// (one load of 16 bytes), else every 32nd (four coalesced loads).
+//
 // Blocks belong to one head and keep its bias by distance in shared memory.
 // dtable wants the sum of dS along each diagonal of the scores (one distance,
-// all of a head's rows): within a row every distance inside (-D, D) occurs at
-// one column, so a warp (or the block that shares a row) adds its row to an
-// array by distance in shared memory without conflicts; columns further away
-// go to two registers.  The arrays are added in a fixed order, then by bucket.
+// all of a head's rows).  Within a row every distance inside (-D, D) occurs at
+// one column, so a warp adds its row to an array by distance in shared memory
+// without conflicts; columns further away go to two registers.  The arrays are
+// added in a fixed order, then by bucket.
 #include <algorithm>
 
 #include "chained.cuh"
+#include "pairs.cuh"
 #include "philox.cuh"
 
 namespace {
 
+using amsim::add2;
+using amsim::both;
 using amsim::Drop;
+using amsim::fma2;
+using amsim::mul2;
 
 struct Params {
     const float *scores, *probs, *dprobs, *stats, *table;   // inputs
     const int32_t *buckets, *lengths, *offsets;
     float *out, *out_stats, *dtable, *part;
-    int64_t queries, ld_in, ld_g, ld_out, offset;            // ld_in: of scores or probs
-    int keys, heads, rows, share_rows, shares;               // rows: of one head
-    int causal, num_buckets, D;
+    int64_t ld_in, ld_g, ld_out, offset;     // ld_in: of scores or probs
+    int queries, keys, quads, chunks, heads;
+    int groups, row_groups, shares;          // groups of rows of one head, of one sequence and head
+    int cluster, causal, num_buckets, D;
     Drop drop;
 };
 
 constexpr int kWarpRows = 8;                 // warps of a block that each take a row
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr float kLog2E = 1.44269504088896341f;
 
-// Arrays by distance: lanes read and write every fourth entry at a time, and a
-// word more every 32 lets those fall into 32 banks.
-__host__ __device__ __forceinline__ int place(int i) { return i + (i >> 5); }
-__host__ __device__ __forceinline__ int places(int D) { return place(2 * D) + 1; }
-
-// One row: where it is, what it sees, and its query's place, brought near enough for 32 bits.
-struct Row {
-    int64_t row;
-    int visible, pos;
+// Four values of a lane.
+struct Four {
+    float2 a, b;
 };
-__device__ __forceinline__ Row row_of(const Params &p, int head, int r)
+__device__ __forceinline__ Four four(float v) { return Four{both(v), both(v)}; }
+template <typename F>
+__device__ __forceinline__ void each(Four &v, F use)
 {
-    const int b = (int)((unsigned)r / (unsigned)p.queries), i = r - b * (int)p.queries;
-    Row w;
-    w.row = ((int64_t)b * p.heads + head) * p.queries + i;
-    const int64_t pos = (p.offsets ? (int64_t)p.offsets[b] : p.offset) + i;
-    int64_t end = p.keys;
-    if (p.lengths) end = min(end, (int64_t)max(p.lengths[b], 0));
-    if (p.causal) end = min(end, max(pos + 1, (int64_t)0));
-    w.visible = (int)end;
-    w.pos = (int)max(min(pos, (int64_t)p.keys + p.D), -(int64_t)p.D - 1);
-    return w;
+    use(v.a.x, 0);
+    use(v.a.y, 1);
+    use(v.b.x, 2);
+    use(v.b.y, 3);
+}
+__device__ __forceinline__ Four add(const Four &x, const Four &y) { return Four{add2(x.a, y.a), add2(x.b, y.b)}; }
+__device__ __forceinline__ Four mul(const Four &x, const Four &y) { return Four{mul2(x.a, y.a), mul2(x.b, y.b)}; }
+__device__ __forceinline__ float sum(const Four &v)
+{
+    const float2 s = add2(v.a, v.b);
+    return s.x + s.y;
+}
+
+// Column k of a lane's four in a chunk.
+template <bool VEC>
+__device__ __forceinline__ int column(int chunk, int lane, int k)
+{
+    return chunk * 128 + (VEC ? 4 * lane + k : 32 * k + lane);
 }
 
 template <bool VEC>
-__device__ __forceinline__ void load_quad(const float *row, int col, int limit, float fill, float (&v)[4])
+__device__ __forceinline__ Four load_chunk(const float *row, int chunk, int lane, int visible, float fill)
 {
+    Four v = four(fill);
+    const int c = column<VEC>(chunk, lane, 0);
     if (VEC) {
-        float4 f = make_float4(fill, fill, fill, fill);
-        if (col < limit) f = *reinterpret_cast<const float4 *>(row + col);
-        v[0] = f.x;
-        v[1] = col + 1 < limit ? f.y : fill;
-        v[2] = col + 2 < limit ? f.z : fill;
-        v[3] = col + 3 < limit ? f.w : fill;
+        if (c < visible) {
+            const float4 f = *reinterpret_cast<const float4 *>(row + c);
+            v = Four{make_float2(f.x, f.y), make_float2(f.z, f.w)};
+            if (c + 4 > visible) each(v, [&](float &x, int k) { x = c + k < visible ? x : fill; });
+        }
     } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = col + k < limit ? row[col + k] : fill;
+        each(v, [&](float &x, int k) { if (c + 32 * k < visible) x = row[c + 32 * k]; });
+    }
+    return v;
+}
+// Zeros where no key is visible.
+template <bool VEC>
+__device__ __forceinline__ void hide(Four &v, int chunk, int lane, int visible)
+{
+    if ((chunk + 1) * 128 > visible) each(v, [&](float &x, int k) { if (column<VEC>(chunk, lane, k) >= visible) x = 0.0f; });
+}
+template <bool VEC>
+__device__ __forceinline__ void store_chunk(float *row, int chunk, int lane, int keys, Four v)
+{
+    const int c = column<VEC>(chunk, lane, 0);
+    if (VEC) {
+        if (c < keys) *reinterpret_cast<float4 *>(row + c) = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
+    } else {
+        each(v, [&](float &x, int k) { if (c + 32 * k < keys) row[c + 32 * k] = x; });
     }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store_quad(float *row, int col, int keys, const float (&v)[4])
+// exp((a - base)): the difference first, so that rows of the type's lowest value
+// stay finite; two roundings of the difference and some 2^-22 of the instruction.
+__device__ __forceinline__ float power_of_2(float t)
 {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return e;
+}
+__device__ __forceinline__ Four exponentials(Four v, float base)
+{
+    v = Four{mul2(add2(v.a, both(-base)), both(kLog2E)), mul2(add2(v.b, both(-base)), both(kLog2E))};
+    each(v, [](float &x, int) { x = power_of_2(x); });
+    return v;
+}
+__device__ __forceinline__ float finite_base(float top) { return top == -INFINITY ? 0.0f : top; }
+
+// Dropout of a chunk's values, which stay times `scale`.  A lane draws the quad
+// of columns 4 lane ..; where it has other columns the lanes exchange one bit a column.
+template <bool VEC>
+__device__ __forceinline__ void drop_chunk(Four &v, int64_t row, int chunk, int lane, const Params &p, uint64_t call,
+                                           float scale)
+{
+    const uint4 w = amsim::philox((uint64_t)row * (unsigned)p.quads + (unsigned)(chunk * 32 + lane), call, p.drop.seed);
+    const uint32_t border = p.drop.border;
+    v = mul(v, four(scale));
     if (VEC) {
-        if (col < keys) *reinterpret_cast<float4 *>(row + col) = make_float4(v[0], v[1], v[2], v[3]);
+        v.a.x = w.x >= border ? v.a.x : 0.0f;
+        v.a.y = w.y >= border ? v.a.y : 0.0f;
+        v.b.x = w.z >= border ? v.b.x : 0.0f;
+        v.b.y = w.w >= border ? v.b.y : 0.0f;
     } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (col + k < keys) row[col + k] = v[k];
+        const unsigned m0 = __ballot_sync(kAll, w.x >= border), m1 = __ballot_sync(kAll, w.y >= border),
+                       m2 = __ballot_sync(kAll, w.z >= border), m3 = __ballot_sync(kAll, w.w >= border);
+        const unsigned mine = (lane & 2 ? (lane & 1 ? m3 : m2) : (lane & 1 ? m1 : m0)) >> (lane >> 2);
+        each(v, [&](float &x, int k) { x = mine >> (8 * k) & 1 ? x : 0.0f; });
     }
 }
+
+// Arrays by distance hold four entries more at each end, where distances beyond
+// D act as D: entry i is distance i - D - 4.  A lane's four neighbours then take
+// one access of 16 bytes, whose place is off by `i & 3`: the bias is kept in four
+// copies, copy k from entry k on.
+__host__ __device__ __forceinline__ int entries(int D) { return (2 * D + 15) & ~3; }
 
 // The head's bias by distance, into shared memory.
 __device__ __forceinline__ void load_bias(const Params &p, int head, float *bias)
 {
-    for (int i = threadIdx.x; i <= 2 * p.D; i += blockDim.x) {
-        const int k = p.buckets[i];
-        bias[place(i)] = (unsigned)k < (unsigned)p.num_buckets ? p.table[(int64_t)k * p.heads + head] : 0.0f;
-    }
-    __syncthreads();
-}
-__device__ __forceinline__ void add_bias(const Params &p, const float *bias, int col, int pos, float (&v)[4])
-{
+    const int n = entries(p.D);
+    for (int i = threadIdx.x; i < n + 3; i += blockDim.x) {
+        const int k = p.buckets[min(max(i - 4, 0), 2 * p.D)];
+        const float v = (unsigned)k < (unsigned)p.num_buckets ? p.table[(int64_t)k * p.heads + head] : 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] += bias[place(min(max(col + k - pos + p.D, 0), 2 * p.D))];
+        for (int c = 0; c < 4; ++c)
+            if (i >= c && i - c < n) bias[c * n + i - c] = v;
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void add_bias(Four &v, const float *bias, int chunk, int lane, int pos, const Params &p)
+{
+    const int first = column<VEC>(chunk, lane, 0) - pos + p.D + 4;
+    if (VEC) {
+        const int i = min(max(first, 0), 2 * p.D + 5), k = i & 3;
+        const float4 f = *reinterpret_cast<const float4 *>(bias + k * entries(p.D) + (i - k));
+        v = add(v, Four{make_float2(f.x, f.y), make_float2(f.z, f.w)});
+    } else {
+        each(v, [&](float &x, int k) { x += bias[min(max(first + 32 * k, 0), 2 * p.D + 8)]; });
+    }
 }
 
-// Maximum or sum over the threads of a row: a warp's, or (BLOCK) the block's.
-template <bool BLOCK, bool MAX>
-__device__ __forceinline__ float reduce(float v, float *shared)
+// One row: where it is, what it sees, and its query's place, brought near enough
+// for 32 bits.  Warps that take rows of their own take them by the place modulo
+// eight, so that a warp's sums by distance keep their place modulo four.
+struct Row {
+    int64_t row;
+    int visible, pos;
+    bool on;
+};
+template <bool BLOCK>
+__device__ __forceinline__ Row row_of(const Params &p, int head, int group)
+{
+    const int b = (int)((unsigned)group / (unsigned)p.row_groups);
+    int i = group - b * p.row_groups;
+    const int64_t first = p.offsets ? (int64_t)p.offsets[b] : p.offset;
+    if (!BLOCK) i = kWarpRows * i + (((int)(threadIdx.x >> 5) - (int)first) & (kWarpRows - 1));
+    Row w;
+    w.on = i < p.queries;
+    w.row = ((int64_t)b * p.heads + head) * p.queries + i;
+    const int64_t pos = first + i;
+    int64_t end = p.keys;
+    if (p.lengths) end = min(end, (int64_t)max(p.lengths[b], 0));
+    if (p.causal) end = min(end, max(pos + 1, (int64_t)0));
+    w.visible = (int)end;
+    // every column of the row's chunks stays further than D from a place that is brought near
+    w.pos = (int)max(min(pos, (int64_t)p.chunks * 128 + p.D + 8), -(int64_t)p.D - 8);
+    return w;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const float o = __shfl_xor_sync(kAll, v, d);
-        v = MAX ? fmaxf(v, o) : v + o;
-    }
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+}
+
+// A cluster's blocks.
+__device__ __forceinline__ int cluster_rank()
+{
+    int r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float2 of_rank(const float2 *q, int rank)
+{
+    uint32_t at;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(q)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+// exp(mine - top), 0 for a part that sees nothing.
+__device__ __forceinline__ float part_factor(float mine, float top)
+{
+    return mine == -INFINITY ? 0.0f : power_of_2((mine - top) * kLog2E);
+}
+
+// What the warps (and blocks) that share a row exchange, once per row; two sets
+// in turn, so that one barrier a row is enough: a set is written again only
+// after the barrier that follows its last reader.
+struct Exchange {
+    float2 warps[2][32], blocks[2];
+};
+
+// The row's maximum, and 1 / sum, from each warp's (maximum, sum).
+template <bool BLOCK>
+__device__ __forceinline__ float2 join_rows(const Params &p, float top, float total, Exchange &x, int turn)
+{
     if (BLOCK) {
         const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-        __syncthreads();                     // the values of the reduction before have been read
-        if (lane == 0) shared[threadIdx.x >> 5] = v;
+        if (lane == 0) x.warps[turn][threadIdx.x >> 5] = make_float2(top, total);
         __syncthreads();
-        v = lane < warps ? shared[lane] : MAX ? -INFINITY : 0.0f;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const float o = __shfl_xor_sync(kAll, v, d);
-            v = MAX ? fmaxf(v, o) : v + o;
+        const float2 v = lane < warps ? x.warps[turn][lane] : make_float2(-INFINITY, 0.0f);
+        top = warp_max(v.x);
+        total = warp_sum(v.y == 0.0f ? 0.0f : v.y * part_factor(v.x, top));
+        if (p.cluster > 1) {
+            if (threadIdx.x == 0) x.blocks[turn] = make_float2(top, total);
+            cluster_barrier();
+            const float2 b = lane < p.cluster ? of_rank(&x.blocks[turn], lane) : make_float2(-INFINITY, 0.0f);
+            top = warp_max(b.x);
+            total = warp_sum(b.y == 0.0f ? 0.0f : b.y * part_factor(b.x, top));
+        }
+    }
+    return make_float2(top, total == 0.0f ? 0.0f : 1.0f / total);
+}
+template <bool BLOCK>
+__device__ __forceinline__ float join_sums(const Params &p, float v, Exchange &x, int turn)
+{
+    if (BLOCK) {
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) x.warps[turn][threadIdx.x >> 5].x = v;
+        __syncthreads();
+        v = warp_sum(lane < warps ? x.warps[turn][lane].x : 0.0f);
+        if (p.cluster > 1) {
+            if (threadIdx.x == 0) x.blocks[turn].x = v;
+            cluster_barrier();
+            v = warp_sum(lane < p.cluster ? of_rank(&x.blocks[turn], lane).x : 0.0f);
         }
     }
     return v;
 }
 
-__device__ __forceinline__ float finite_base(float top) { return top == -INFINITY ? 0.0f : top; }
-
-// Probabilities of a quad from its exponentials: dropout, zeros where no key is visible.
-__device__ __forceinline__ void finish_probs(const Params &p, const Row &w, int col, uint64_t call, float inv, float (&v)[4])
+// A block's part of the work: a head, and which of its groups of rows.
+struct Part {
+    int head, share, rank;
+    int first_chunk, step;                   // this warp's chunks
+};
+template <bool BLOCK>
+__device__ __forceinline__ Part part_of(const Params &p)
 {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = col + k < w.visible ? v[k] * inv : 0.0f;
-    if (p.drop.border && col < w.visible)
-        amsim::drop_quad(v, (uint64_t)w.row * (unsigned)((p.keys + 3) >> 2) + (unsigned)(col >> 2), p.drop, call);
+    Part t;
+    unsigned unit = blockIdx.x;
+    t.rank = 0;
+    if (BLOCK && p.cluster > 1) {
+        t.rank = cluster_rank();
+        unit /= (unsigned)p.cluster;
+    }
+    t.head = (int)(unit / (unsigned)p.shares);
+    t.share = (int)(unit - (unsigned)t.head * (unsigned)p.shares);
+    const int warps = BLOCK ? (int)(blockDim.x >> 5) : 1;
+    t.first_chunk = BLOCK ? t.rank * warps + (int)(threadIdx.x >> 5) : 0;
+    t.step = BLOCK ? warps * p.cluster : 1;
+    return t;
 }
 
-// NV > 0: the row's quads stay in NV x 4 registers a thread; NV == 0: a row of
-// any length, read twice.
+// NV > 0: a warp's part of the row is NV chunks, kept in registers; NV == 0: a
+// row of any length, read twice.
 template <int NV, bool VEC, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(const Params p)
 {
-    extern __shared__ float shared[];
-    __shared__ float sums[32];
-    const int head = blockIdx.x / p.shares, share = blockIdx.x % p.shares;
-    const int width = BLOCK ? blockDim.x : 32, lane = BLOCK ? threadIdx.x : threadIdx.x & 31;
-    if (p.table) load_bias(p, head, shared);
+    extern __shared__ __align__(16) float bias[];
+    __shared__ Exchange exchange;
+    const Part t = part_of<BLOCK>(p);
+    const int lane = threadIdx.x & 31;
+    if (p.table) {
+        load_bias(p, t.head, bias);
+        __syncthreads();
+    }
     const uint64_t call = amsim::drop_call(p.drop);
-    const int last = min(p.rows, (share + 1) * p.share_rows);
-    for (int r = share * p.share_rows + (BLOCK ? 0 : threadIdx.x >> 5); r < last; r += BLOCK ? 1 : kWarpRows) {
-        const Row w = row_of(p, head, r);
+    int turn = 0;
+    for (int g = t.share; g < p.groups; g += p.shares, turn ^= 1) {
+        const Row w = row_of<BLOCK>(p, t.head, g);
+        if (!BLOCK && !w.on) continue;
         const float *in = p.scores + w.row * p.ld_in;
         float *out = p.out + w.row * p.ld_out;
-        float top = -INFINITY, sum = 0.0f, base, inv;
-        auto quad = [&](int col, float (&v)[4]) {
-            load_quad<VEC>(in, col, w.visible, -INFINITY, v);
-            if (p.table) add_bias(p, shared, col, w.pos, v);
+        auto logits = [&](int chunk) {
+            Four a = load_chunk<VEC>(in, chunk, lane, w.visible, -INFINITY);
+            if (p.table && chunk * 128 < w.visible) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
+            return a;
         };
+        auto finish = [&](Four e, int chunk, float factor) {
+            if (chunk * 128 >= w.visible)
+                e = four(0.0f);
+            else if (p.drop.border)
+                drop_chunk<VEC>(e, w.row, chunk, lane, p, call, factor * p.drop.scale);
+            else
+                e = mul(e, four(factor));
+            hide<VEC>(e, chunk, lane, w.visible);
+            store_chunk<VEC>(out, chunk, lane, p.keys, e);
+        };
+        float mine = -INFINITY, total = 0.0f;
+        float2 joined;
         if (NV) {
-            float a[NV ? NV : 1][4];
+            Four a[NV ? NV : 1];
 #pragma unroll
-            for (int v = 0; v < NV; ++v) quad(4 * (lane + v * width), a[v]);
-#pragma unroll
-            for (int v = 0; v < NV; ++v) top = fmaxf(fmaxf(fmaxf(top, a[v][0]), fmaxf(a[v][1], a[v][2])), a[v][3]);
-            top = reduce<BLOCK, true>(top, sums);
-            base = finite_base(top);
+            for (int v = 0; v < NV; ++v) a[v] = logits(t.first_chunk + v * t.step);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sum += a[v][k] = expf(a[v][k] - base);
-            sum = reduce<BLOCK, false>(sum, sums);
-            inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                mine = fmaxf(fmaxf(mine, fmaxf(a[v].a.x, a[v].a.y)), fmaxf(a[v].b.x, a[v].b.y));
+            mine = warp_max(mine);
+            const float base = finite_base(mine);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int col = 4 * (lane + v * width);
-                finish_probs(p, w, col, call, inv, a[v]);
-                store_quad<VEC>(out, col, p.keys, a[v]);
+                a[v] = exponentials(a[v], base);
+                total += sum(a[v]);
             }
+            total = warp_sum(total);
+            joined = join_rows<BLOCK>(p, mine, total, exchange, turn);
+            const float factor = BLOCK ? joined.y * part_factor(mine, joined.x) : joined.y;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) finish(a[v], t.first_chunk + v * t.step, factor);
         } else {
-            for (int col = 4 * lane; col < w.visible; col += 4 * width) {
-                float a[4];
-                quad(col, a);
-                const float most = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
-                if (most > top) {
-                    sum *= expf(top - most);             // exp(-infinity) = 0 the first time
-                    top = most;
+            for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += t.step) {
+                const Four a = logits(chunk);
+                const float most = fmaxf(fmaxf(a.a.x, a.a.y), fmaxf(a.b.x, a.b.y));
+                if (most > mine) {
+                    total *= part_factor(mine, most);
+                    mine = most;
                 }
-                base = finite_base(top);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sum += expf(a[k] - base);
+                total += sum(exponentials(a, finite_base(mine)));
             }
-            const float mine = top;
-            top = reduce<BLOCK, true>(top, sums);
-            base = finite_base(top);
-            sum = reduce<BLOCK, false>(mine == -INFINITY ? sum : sum * expf(mine - base), sums);
-            inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            for (int col = 4 * lane; col < p.keys; col += 4 * width) {
-                float a[4];
-                quad(col, a);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) a[k] = expf(a[k] - base);
-                finish_probs(p, w, col, call, inv, a);
-                store_quad<VEC>(out, col, p.keys, a);
-            }
+            const float top = warp_max(mine);
+            total = warp_sum(mine == -INFINITY ? total : total * part_factor(mine, top));
+            joined = join_rows<BLOCK>(p, top, total, exchange, turn);
+            const float base = finite_base(joined.x);
+            for (int chunk = t.first_chunk; chunk < p.chunks; chunk += t.step)
+                finish(exponentials(logits(chunk), base), chunk, joined.y);
         }
-        if (p.out_stats && lane == 0) {
-            p.out_stats[2 * w.row] = top;
-            p.out_stats[2 * w.row + 1] = inv;
-        }
+        if (p.out_stats && lane == 0 && (!BLOCK || (threadIdx.x == 0 && t.rank == 0)))
+            *reinterpret_cast<float2 *>(p.out_stats + 2 * w.row) = joined;
     }
+    if (BLOCK && p.cluster > 1) cluster_barrier();       // no block leaves while another reads from it
 }
 
 // dtable of a head from its sums by distance; each warp takes buckets of its own.
@@ -215,8 +398,8 @@ __device__ __forceinline__ void by_bucket(const Params &p, int head, const float
     for (int k = threadIdx.x >> 5; k < p.num_buckets; k += blockDim.x >> 5) {
         float s = 0.0f;
         for (int i = lane; i <= 2 * p.D; i += 32)
-            if (p.buckets[i] == k) s += total[place(i)];
-        s = reduce<false, false>(s, nullptr);
+            if (p.buckets[i] == k) s += total[i];
+        s = warp_sum(s);
         if (lane == 0) p.dtable[(int64_t)k * p.heads + head] = s;
     }
 }
@@ -224,129 +407,163 @@ __device__ __forceinline__ void by_bucket(const Params &p, int head, const float
 template <int NV, bool VEC, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) backward_kernel(const Params p)
 {
-    extern __shared__ float shared[];
-    __shared__ float sums[32];
-    const int head = blockIdx.x / p.shares, share = blockIdx.x % p.shares;
-    const int width = BLOCK ? blockDim.x : 32, lane = BLOCK ? threadIdx.x : threadIdx.x & 31;
-    const int size = places(p.D), teams = BLOCK ? 1 : kWarpRows;
-    float *bias = shared, *diagonals = shared + (p.table ? size : 0);
-    float *mine = diagonals + (BLOCK ? 0 : (threadIdx.x >> 5) * size);
+    extern __shared__ __align__(16) float shared[];
+    __shared__ Exchange exchange;
+    __shared__ float ends[2][32];
+    const Part t = part_of<BLOCK>(p);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // sums by distance: an array a warp, shifted by its rows' place modulo four
+    // (BLOCK: four copies, as the bias has, since a block takes rows of every place)
+    const int n = entries(p.D), arrays = BLOCK ? 4 : kWarpRows, size = n + 4;
+    float *bias = shared, *diagonals = shared + (p.table ? 4 * n : 0);
     if (p.dtable)
-        for (int i = threadIdx.x; i < teams * size; i += blockDim.x) diagonals[i] = 0.0f;
-    if (p.table)
-        load_bias(p, head, bias);
-    else
-        __syncthreads();
+        for (int i = threadIdx.x; i < arrays * size; i += blockDim.x) diagonals[i] = 0.0f;
+    if (p.table) load_bias(p, t.head, bias);
+    __syncthreads();
     const uint64_t call = amsim::drop_call(p.drop);
-    float before = 0.0f, behind = 0.0f;      // columns at distances up to -D, from D on
-    const int last = min(p.rows, (share + 1) * p.share_rows);
-    for (int r = share * p.share_rows + (BLOCK ? 0 : threadIdx.x >> 5); r < last; r += BLOCK ? 1 : kWarpRows) {
-        const Row w = row_of(p, head, r);
+    float2 before = both(0.0f), behind = both(0.0f);     // columns at distances up to -D, from D on
+    const int shift = VEC && !BLOCK ? (warp - p.D) & 3 : 0;
+    int turn = 0;
+    for (int g = t.share; g < p.groups; g += p.shares, turn ^= 1) {
+        const Row w = row_of<BLOCK>(p, t.head, g);
+        if (!BLOCK && !w.on) continue;
         const float *in = (p.probs ? p.probs : p.scores) + w.row * p.ld_in, *up = p.dprobs + w.row * p.ld_g;
         float *out = p.out + w.row * p.ld_out;
         float base = 0.0f, inv = 1.0f;
         if (!p.probs) {
-            base = finite_base(p.stats[2 * w.row]);
-            inv = p.stats[2 * w.row + 1];
+            const float2 f = *reinterpret_cast<const float2 *>(p.stats + 2 * w.row);
+            base = finite_base(f.x);
+            inv = f.y;
         }
-        auto load = [&](int col, float (&a)[4], float (&g)[4]) {
-            load_quad<VEC>(in, col, w.visible, p.probs ? 0.0f : -INFINITY, a);
-            load_quad<VEC>(up, col, w.visible, 0.0f, g);
+        const int origin = p.D + 4 - w.pos;              // entry of column 0
+        auto values = [&](int chunk, Four &a, Four &d) {
+            if (p.probs || chunk * 128 >= w.visible) return;
+            if (p.table) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
+            a = mul(exponentials(a, base), four(inv));
+            hide<VEC>(a, chunk, lane, w.visible);
+            if (p.drop.border) drop_chunk<VEC>(d, w.row, chunk, lane, p, call, p.drop.scale);
         };
-        auto values = [&](int col, float (&a)[4], float (&g)[4]) {
-            if (!p.probs) {
-                if (p.table) add_bias(p, bias, col, w.pos, a);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) a[k] = col + k < w.visible ? expf(a[k] - base) * inv : 0.0f;
-                if (p.drop.border && col < w.visible)
-                    amsim::drop_quad(g, (uint64_t)w.row * (unsigned)((p.keys + 3) >> 2) + (unsigned)(col >> 2), p.drop,
-                                     call);
-            }
-        };
-        auto finish = [&](int col, float dot, float (&a)[4], const float (&g)[4]) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a[k] = col + k < w.visible ? a[k] * (g[k] - dot) : 0.0f;
-            if (p.dtable) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = col + k - w.pos + p.D;
-                    if (i <= 0)
-                        before += a[k];
-                    else if (i >= 2 * p.D)
-                        behind += a[k];
-                    else if (col + k < w.visible)
-                        mine[place(i)] += a[k];
+        auto finish = [&](int chunk, float dot, Four a, const Four &d) {
+            a = chunk * 128 < w.visible ? mul(a, add(d, four(-dot))) : four(0.0f);
+            hide<VEC>(a, chunk, lane, w.visible);
+            if (p.dtable && chunk * 128 < w.visible) {
+                const int first = column<VEC>(chunk, lane, 0) + origin;
+                if (VEC) {
+                    if ((unsigned)first <= (unsigned)(2 * p.D + 5)) {
+                        const int k = first & 3;
+                        float4 *to = reinterpret_cast<float4 *>(BLOCK ? diagonals + k * size + (first - k)
+                                                                      : diagonals + warp * size + (first + shift));
+                        const float4 s = *to;
+                        const Four v = add(a, Four{make_float2(s.x, s.y), make_float2(s.z, s.w)});
+                        *to = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
+                    } else if (first < 0) {
+                        before = add2(before, add2(a.a, a.b));
+                    } else {
+                        behind = add2(behind, add2(a.a, a.b));
+                    }
+                } else {
+                    float *to = diagonals + (BLOCK ? 0 : warp * size);
+                    each(a, [&](float &x, int k) {
+                        const int i = first + 32 * k;
+                        if ((unsigned)i <= (unsigned)(2 * p.D + 8))
+                            to[i] += x;
+                        else if (i < 0)
+                            before.x += x;
+                        else
+                            behind.x += x;
+                    });
                 }
             }
-            store_quad<VEC>(out, col, p.keys, a);
+            store_chunk<VEC>(out, chunk, lane, p.keys, a);
         };
-        float dot = 0.0f;
+        Four part = four(0.0f);
         if (NV) {
-            float a[NV ? NV : 1][4], g[NV ? NV : 1][4];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) load(4 * (lane + v * width), a[v], g[v]);
+            Four a[NV ? NV : 1], d[NV ? NV : 1];
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                values(4 * (lane + v * width), a[v], g[v]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) dot = fmaf(a[v][k], g[v][k], dot);
+                const int chunk = t.first_chunk + v * t.step;
+                a[v] = load_chunk<VEC>(in, chunk, lane, w.visible, p.probs ? 0.0f : -INFINITY);
+                d[v] = load_chunk<VEC>(up, chunk, lane, w.visible, 0.0f);
             }
-            dot = reduce<BLOCK, false>(dot, sums);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) finish(4 * (lane + v * width), dot, a[v], g[v]);
+            for (int v = 0; v < NV; ++v) {
+                const int chunk = t.first_chunk + v * t.step;
+                values(chunk, a[v], d[v]);
+                if (chunk * 128 < w.visible)
+                    part = Four{fma2(a[v].a, d[v].a, part.a), fma2(a[v].b, d[v].b, part.b)};
+            }
+            const float dot = join_sums<BLOCK>(p, warp_sum(sum(part)), exchange, turn);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) finish(t.first_chunk + v * t.step, dot, a[v], d[v]);
         } else {
-            float a[4], g[4];
-            for (int col = 4 * lane; col < w.visible; col += 4 * width) {
-                load(col, a, g);
-                values(col, a, g);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) dot = fmaf(a[k], g[k], dot);
+            auto both_of = [&](int chunk, Four &a, Four &d) {
+                a = load_chunk<VEC>(in, chunk, lane, w.visible, p.probs ? 0.0f : -INFINITY);
+                d = load_chunk<VEC>(up, chunk, lane, w.visible, 0.0f);
+                values(chunk, a, d);
+            };
+            Four a, d;
+            for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += t.step) {
+                both_of(chunk, a, d);
+                part = Four{fma2(a.a, d.a, part.a), fma2(a.b, d.b, part.b)};
             }
-            dot = reduce<BLOCK, false>(dot, sums);
-            for (int col = 4 * lane; col < p.keys; col += 4 * width) {
-                load(col, a, g);
-                values(col, a, g);
-                finish(col, dot, a, g);
+            const float dot = join_sums<BLOCK>(p, warp_sum(sum(part)), exchange, turn);
+            for (int chunk = t.first_chunk; chunk < p.chunks; chunk += t.step) {
+                both_of(chunk, a, d);
+                finish(chunk, dot, a, d);
             }
         }
         if (!BLOCK) __syncwarp();            // other lanes add to the same distances for the next row
     }
+    if (BLOCK && p.cluster > 1) cluster_barrier();       // no block leaves while another reads from it
     if (!p.dtable) return;
     amsim::chain_start();
-    before = reduce<BLOCK, false>(before, sums);
-    behind = reduce<BLOCK, false>(behind, sums);
-    __syncthreads();
+    const float low = warp_sum(before.x + before.y), high = warp_sum(behind.x + behind.y);
     if (lane == 0) {
-        mine[place(0)] += before;
-        mine[place(2 * p.D)] += behind;
+        ends[0][warp] = low;
+        ends[1][warp] = high;
     }
     __syncthreads();
+    // the block's sum of an entry, in a fixed order
+    auto entry = [&](int i) {
+        float s = 0.0f;
+        for (int k = 0; k < (BLOCK ? (VEC ? 4 : 1) : kWarpRows); ++k) {
+            const int at = BLOCK ? i - k : VEC ? i + ((k - p.D) & 3) : i;
+            if (at >= 0) s += diagonals[k * size + at];
+        }
+        return s;
+    };
+    float *total = p.shares * p.cluster > 1 ? p.part + (int64_t)blockIdx.x * (2 * p.D + 1) : bias;
+    if (p.shares * p.cluster == 1 && !p.table) total = diagonals + arrays * size;
     for (int i = threadIdx.x; i <= 2 * p.D; i += blockDim.x) {
-        float s = diagonals[place(i)];
-        for (int t = 1; t < teams; ++t) s += diagonals[t * size + place(i)];
-        if (p.shares > 1)
-            p.part[(int64_t)blockIdx.x * (2 * p.D + 1) + i] = s;
-        else
-            diagonals[place(i)] = s;         // read by this thread alone so far
+        float s = entry(i + 4);
+        if (i == 0) {
+            for (int j = 0; j < 4; ++j) s += entry(j);
+            for (int k = 0; k < (int)(blockDim.x >> 5); ++k) s += ends[0][k];
+        }
+        if (i == 2 * p.D) {
+            for (int j = 5; j <= 8; ++j) s += entry(2 * p.D + j);
+            for (int k = 0; k < (int)(blockDim.x >> 5); ++k) s += ends[1][k];
+        }
+        total[i] = s;
     }
-    if (p.shares > 1) return;
+    if (p.shares * p.cluster > 1) return;
     __syncthreads();
-    by_bucket(p, head, diagonals);
+    by_bucket(p, t.head, total);
 }
 
-// dtable from the shares' sums by distance: a block per head.
+// dtable from the blocks' sums by distance: a block per head.
 constexpr int kTableThreads = 1024;
 __global__ void __launch_bounds__(kTableThreads) table_kernel(const Params p)
 {
-    extern __shared__ float shared[];
+    extern __shared__ __align__(16) float shared[];
     amsim::chain_wait();
-    const int n = 2 * p.D + 1;
-    const float *part = p.part + (int64_t)blockIdx.x * p.shares * n;
+    const int n = 2 * p.D + 1, blocks = p.shares * p.cluster;
+    const float *part = p.part + (int64_t)blockIdx.x * blocks * n;
     for (int i = threadIdx.x; i < n; i += kTableThreads) {
         float s = 0.0f;
 #pragma unroll 8
-        for (int t = 0; t < p.shares; ++t) s += part[(int64_t)t * n + i];
-        shared[place(i)] = s;
+        for (int t = 0; t < blocks; ++t) s += part[(int64_t)t * n + i];
+        shared[i] = s;
     }
     __syncthreads();
     by_bucket(p, (int)blockIdx.x, shared);
@@ -361,6 +578,7 @@ int check(const amsim_attention_softmax_desc *d, Drop *drop)
     constexpr int64_t most = 0x7FFFFFFF - 4096;
     for (int64_t n : {d->batch, d->heads, d->queries, d->keys})
         if (n > most) return AMSIM_EINVAL;
+    if (d->keys > (int64_t)1 << 30) return AMSIM_EINVAL;             // columns of chunks behind the last fit 32 bits
     if (d->batch * d->queries > most || d->batch * d->queries * d->heads > (int64_t)1 << 40) return AMSIM_EINVAL;
     for (int64_t ld : {d->ld_scores, d->ld_probs, d->ld_dprobs, d->ld_dscores})
         if (ld != 0 && (ld < d->keys || ld > (int64_t)1 << 31)) return AMSIM_EINVAL;
@@ -370,32 +588,44 @@ int check(const amsim_attention_softmax_desc *d, Drop *drop)
     return amsim::make_drop(d->dropout, drop) ? AMSIM_OK : AMSIM_EINVAL;
 }
 
-// Threads of a row and quads a thread: a warp up to 1024 columns, then a block
-// of up to 1024 threads; longer rows are read twice.
+// How rows are shared: up to four chunks by a warp; then by a block, two chunks a
+// warp (forward four where that spares a cluster), then by a cluster of blocks.
+// Backward keeps two tensors: twice the registers.
+constexpr int kMaxCluster = 8;
 struct Shape {
-    int nv, threads;
+    int nv, threads, cluster;
     bool block;
 };
-Shape shape(int64_t keys)
+Shape shape(int64_t keys, bool fwd)
 {
-    const int64_t quads = (keys + 3) / 4;
-    Shape s{1, 32 * kWarpRows, false};
-    if (quads <= 256) {
-        while (32 * s.nv < quads) s.nv *= 2;
+    const int64_t chunks = (keys + 127) / 128;
+    Shape s{1, 32 * kWarpRows, 1, false};
+    if (chunks <= 4) {
+        while (s.nv < chunks) s.nv *= 2;
         return s;
     }
     s.block = true;
-    s.nv = quads <= 4096 ? 4 : 0;
-    s.threads = s.nv ? (int)((quads + s.nv * 32 - 1) / (s.nv * 32)) * 32 : 1024;
+    s.nv = chunks <= 64 || !fwd ? 2 : 4;
+    const int64_t blocks = (chunks + 32 * s.nv - 1) / (32 * s.nv);
+    s.cluster = 1;
+    while (s.cluster < blocks && s.cluster < kMaxCluster) s.cluster *= 2;
+    if (blocks > kMaxCluster) s.nv = 0;
+    const int64_t warps = s.nv ? (chunks + s.nv * s.cluster - 1) / (s.nv * s.cluster) : 32;
+    s.threads = 32 * (int)warps;
     return s;
 }
 
-// Shares of a head's rows: as many blocks as fill the SMs, no more than rows.
+int64_t row_groups(const amsim_attention_softmax_desc *d, const Shape &s)
+{
+    return s.block ? d->queries : (d->queries + kWarpRows - 1) / kWarpRows;
+}
+
+// Shares of a head's groups of rows: as many blocks as fill the SMs, no more than groups.
 int share_count(const amsim_attention_softmax_desc *d, const Shape &s, int sms)
 {
-    const int64_t rows = d->batch * d->queries, at_once = s.block ? 1 : kWarpRows;
-    const int64_t want = std::max<int64_t>(1, (int64_t)sms * std::max(1, 2048 / s.threads) / std::max<int64_t>(1, d->heads));
-    return (int)std::min(want, (rows + at_once - 1) / at_once);
+    const int64_t groups = d->batch * row_groups(d, s);
+    const int64_t blocks = (int64_t)sms * std::max(1, 2048 / s.threads) / s.cluster;
+    return (int)std::max<int64_t>(1, std::min(blocks / std::max<int64_t>(1, d->heads), groups));
 }
 
 template <bool VEC>
@@ -403,21 +633,27 @@ auto *forward_of(const Shape &s)
 {
     if (!s.block)
         return s.nv == 1 ? forward_kernel<1, VEC, false> : s.nv == 2 ? forward_kernel<2, VEC, false>
-               : s.nv == 4 ? forward_kernel<4, VEC, false> : forward_kernel<8, VEC, false>;
-    return s.nv ? forward_kernel<4, VEC, true> : forward_kernel<0, VEC, true>;
+                                                                     : forward_kernel<4, VEC, false>;
+    return s.nv == 2 ? forward_kernel<2, VEC, true> : s.nv == 4 ? forward_kernel<4, VEC, true>
+                                                                : forward_kernel<0, VEC, true>;
 }
 template <bool VEC>
 auto *backward_of(const Shape &s)
 {
     if (!s.block)
         return s.nv == 1 ? backward_kernel<1, VEC, false> : s.nv == 2 ? backward_kernel<2, VEC, false>
-               : s.nv == 4 ? backward_kernel<4, VEC, false> : backward_kernel<8, VEC, false>;
-    return s.nv ? backward_kernel<4, VEC, true> : backward_kernel<0, VEC, true>;
+                                                                      : backward_kernel<4, VEC, false>;
+    return s.nv == 2 ? backward_kernel<2, VEC, true> : backward_kernel<0, VEC, true>;
 }
 
-// The most shared memory a kernel here takes; every call sets this same limit,
-// so that host threads do not lower one another's.
-constexpr int kMaxShared = (kWarpRows + 1) * (2 * AMSIM_MAX_DISTANCE + 2 * AMSIM_MAX_DISTANCE / 32 + 1) * 4;
+// Shared memory of the bias and of the sums by distance, and the most of it;
+// every call that needs it sets this same limit, so that host threads do not lower one another's.
+constexpr int entries_at(int D) { return (2 * D + 15) & ~3; }
+constexpr int shared_bytes(int D, bool table, bool dtable, int arrays)
+{
+    return 4 * ((table ? 4 * entries_at(D) : 0) + (dtable ? arrays * (entries_at(D) + 4) + (table ? 0 : 2 * D + 1) : 0));
+}
+constexpr int kMaxShared = shared_bytes(AMSIM_MAX_DISTANCE, true, true, kWarpRows);
 
 int launch(void (*kernel)(Params), const Params &p, const Shape &s, int bytes, cudaStream_t st)
 {
@@ -426,30 +662,39 @@ int launch(void (*kernel)(Params), const Params &p, const Shape &s, int bytes, c
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared));
         if (rc) return rc;
     }
-    const int64_t grid = (int64_t)p.heads * p.shares;
+    const int64_t grid = (int64_t)p.heads * p.shares * p.cluster;
     if (grid > 0x7FFFFFFF) return AMSIM_EINVAL;
-    kernel<<<(unsigned)grid, s.threads, bytes, st>>>(p);
-    const int rc = amsim::cuda_status(cudaGetLastError());
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3((unsigned)s.threads);
+    c.dynamicSmemBytes = (size_t)bytes;
+    c.stream = st;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = (unsigned)p.cluster;
+    a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+    c.attrs = a;
+    c.numAttrs = p.cluster > 1 ? 1 : 0;
+    const int rc = amsim::cuda_status(cudaLaunchKernelEx(&c, kernel, p));
     if (rc == AMSIM_OK) amsim::count_launch();
     return rc;
 }
 
-void fill(Params &p, const amsim_attention_softmax_desc *d)
+void fill(Params &p, const amsim_attention_softmax_desc *d, const Shape &s, int shares)
 {
     p.lengths = d->lengths;
     p.offsets = d->offsets;
     p.offset = d->offset;
-    p.queries = d->queries;
+    p.queries = (int)d->queries;
     p.keys = (int)d->keys;
+    p.quads = (int)((d->keys + 3) / 4);
+    p.chunks = (int)((d->keys + 127) / 128);
     p.heads = (int)d->heads;
-    p.rows = (int)(d->batch * d->queries);
+    p.row_groups = (int)row_groups(d, s);
+    p.groups = (int)(d->batch * p.row_groups);
+    p.shares = shares;
+    p.cluster = s.cluster;
     p.causal = d->causal;
-}
-
-void share_rows(Params &p, int shares)
-{
-    p.share_rows = (p.rows + shares - 1) / shares;
-    p.shares = (p.rows + p.share_rows - 1) / p.share_rows;
 }
 
 int check_bias(const amsim_attention_softmax_desc *d, Params &p)
@@ -481,19 +726,18 @@ extern "C" int amsim_attention_softmax_fwd(const amsim_attention_softmax_desc *d
     p.buckets = buckets;
     if (table && (rc = check_bias(d, p))) return rc;
     if (!d->batch || !d->heads || !d->queries || !d->keys) return AMSIM_OK;
-    if (!scores || !probs || !aligned(scores, 4) || !aligned(probs, 4) || !aligned(stats, 4)) return AMSIM_EINVAL;
-    fill(p, d);
+    if (!scores || !probs || !aligned(scores, 4) || !aligned(probs, 4) || !aligned(stats, 8)) return AMSIM_EINVAL;
+    const int sms = device_sms();
+    if (!sms) return AMSIM_ECUDA;
+    const Shape s = shape(d->keys, true);
+    fill(p, d, s, share_count(d, s, sms));
     p.scores = scores;
     p.out = probs;
     p.out_stats = stats;
     p.ld_in = stride(d->ld_scores, d->keys);
     p.ld_out = stride(d->ld_probs, d->keys);
     const bool vec = aligned(scores, 16) && aligned(probs, 16) && !((d->keys | p.ld_in | p.ld_out) & 3);
-    const int sms = device_sms();
-    if (!sms) return AMSIM_ECUDA;
-    const Shape s = shape(d->keys);
-    share_rows(p, share_count(d, s, sms));
-    return launch(vec ? forward_of<true>(s) : forward_of<false>(s), p, s, table ? 4 * places(p.D) : 0,
+    return launch(vec ? forward_of<true>(s) : forward_of<false>(s), p, s, shared_bytes(p.D, table, false, 0),
                   static_cast<cudaStream_t>(stream));
 }
 
@@ -503,8 +747,9 @@ extern "C" size_t amsim_attention_softmax_workspace_size(const amsim_attention_s
     if (check(d, &drop) || d->max_distance > AMSIM_MAX_DISTANCE) return 0;
     if (!d->batch || !d->heads || !d->queries || !d->keys) return 0;
     const int sms = device_sms();
-    const int shares = share_count(d, shape(d->keys), sms ? sms : 1);
-    return shares > 1 ? (size_t)d->heads * shares * (2 * d->max_distance + 1) * 4 : 0;
+    const Shape s = shape(d->keys, false);
+    const int64_t blocks = (int64_t)share_count(d, s, sms ? sms : 1) * s.cluster;
+    return blocks > 1 ? (size_t)d->heads * blocks * (2 * d->max_distance + 1) * 4 : 0;
 }
 
 extern "C" int amsim_attention_softmax_bwd(const amsim_attention_softmax_desc *d, const float *dprobs,
@@ -529,34 +774,38 @@ extern "C" int amsim_attention_softmax_bwd(const amsim_attention_softmax_desc *d
         return AMSIM_OK;
     }
     if (!dprobs || !dscores || (!scores && !probs) || (scores && !stats)) return AMSIM_EINVAL;
-    for (const float *f : {dprobs, scores, stats, probs, (const float *)dscores})
+    for (const float *f : {dprobs, scores, probs, (const float *)dscores})
         if (!aligned(f, 4)) return AMSIM_EINVAL;
-    fill(p, d);
+    if (!aligned(stats, 8)) return AMSIM_EINVAL;
+    const int sms = device_sms();
+    if (!sms) return AMSIM_ECUDA;
+    Shape s = shape(d->keys, false);
+    int shares = share_count(d, s, sms);
+    if (dtable) {
+        const size_t one = (size_t)d->heads * (2 * p.D + 1) * 4, room = ws ? ws_bytes / one : 0;
+        if (s.cluster > 1 && room < (size_t)s.cluster) {     // no room for a cluster's sums: one block, rows read twice
+            s = Shape{0, 1024, 1, true};
+            shares = share_count(d, s, sms);
+        }
+        shares = (int)std::max<size_t>(1, std::min<size_t>(shares, room / s.cluster));
+    }
+    fill(p, d, s, shares);
     p.dprobs = dprobs;
     p.scores = scores;
     p.stats = stats;
     p.probs = probs;
     p.out = dscores;
+    p.part = static_cast<float *>(ws);
     p.ld_in = stride(scores ? d->ld_scores : d->ld_probs, d->keys);
     p.ld_g = stride(d->ld_dprobs, d->keys);
     p.ld_out = stride(d->ld_dscores, d->keys);
     const bool vec = aligned(scores, 16) && aligned(probs, 16) && aligned(dprobs, 16) && aligned(dscores, 16) &&
                      !((d->keys | p.ld_in | p.ld_g | p.ld_out) & 3);
-    const int sms = device_sms();
-    if (!sms) return AMSIM_ECUDA;
-    const Shape s = shape(d->keys);
-    int shares = share_count(d, s, sms);
-    if (dtable) {
-        const size_t one = (size_t)d->heads * (2 * p.D + 1) * 4;
-        shares = (int)std::max<size_t>(1, std::min<size_t>(shares, ws ? ws_bytes / one : 1));
-    }
-    share_rows(p, shares);
-    p.part = static_cast<float *>(ws);
-    const int arrays = (table ? 1 : 0) + (dtable ? (s.block ? 1 : kWarpRows) : 0);
-    rc = launch(vec ? backward_of<true>(s) : backward_of<false>(s), p, s, arrays * 4 * places(p.D), st);
-    if (rc || !dtable || p.shares == 1) return rc;
+    rc = launch(vec ? backward_of<true>(s) : backward_of<false>(s), p, s,
+                shared_bytes(p.D, table, dtable, s.block ? 4 : kWarpRows), st);
+    if (rc || !dtable || p.shares * p.cluster == 1) return rc;
     rc = amsim::cuda_status(amsim::chain_launch(true, table_kernel, dim3((unsigned)p.heads), kTableThreads,
-                                                4 * places(p.D), st, p));
+                                                4 * (2 * p.D + 1), st, p));
     if (rc == AMSIM_OK) amsim::count_launch();
     return rc;
 }

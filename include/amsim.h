@@ -797,8 +797,8 @@ typedef struct amsim_attention_softmax_desc {
 /*
  * Forward.  table: num_buckets x heads, buckets: 2 max_distance + 1 (both, or
  * both null: no bias).  probs is written whole and may alias scores (equal
- * strides).  stats (or null): two values a row for the backward pass, the
- * largest a[j] and 1 / sum; a row of zeros has (-infinity, 0).
+ * strides).  stats (or null): two values a row for the backward pass, on 8
+ * bytes, the largest a[j] and 1 / sum; a row of zeros has (-infinity, 0).
  * Errors: AMSIM_EINVAL for null scores or probs, a bad size, stride, p or flag, or one of
  * table and buckets alone; AMSIM_EUNSUPPORTED for a max_distance above
  * AMSIM_MAX_DISTANCE.  Without rows or keys it is a no-op.
