@@ -18,6 +18,7 @@
 // without conflicts; columns further away go to two registers.  The arrays are
 // added in a fixed order, then by bucket.
 #include <algorithm>
+#include <mutex>
 
 #include "chained.cuh"
 #include "pairs.cuh"
@@ -38,6 +39,7 @@ struct Params {
     int64_t ld_in, ld_g, ld_out, offset;     // ld_in: of scores or probs
     int queries, keys, quads, chunks, heads;
     int groups, row_groups, shares;          // groups of rows of one head, of one sequence and head
+    int ahead_b, ahead_i;                    // shares, in sequences and groups
     int cluster, causal, num_buckets, D;
     Drop drop;
 };
@@ -74,21 +76,28 @@ __device__ __forceinline__ int column(int chunk, int lane, int k)
     return chunk * 128 + (VEC ? 4 * lane + k : 32 * k + lane);
 }
 
+// A chunk as it is loaded: nothing waits for it here, so that a row's loads are
+// all under way before the first is used.  Pieces that begin at a visible key are whole.
 template <bool VEC>
 __device__ __forceinline__ Four load_chunk(const float *row, int chunk, int lane, int visible, float fill)
 {
     Four v = four(fill);
     const int c = column<VEC>(chunk, lane, 0);
     if (VEC) {
-        if (c < visible) {
-            const float4 f = *reinterpret_cast<const float4 *>(row + c);
-            v = Four{make_float2(f.x, f.y), make_float2(f.z, f.w)};
-            if (c + 4 > visible) each(v, [&](float &x, int k) { x = c + k < visible ? x : fill; });
-        }
+        float4 f = make_float4(fill, fill, fill, fill);
+        if (c < visible) f = *reinterpret_cast<const float4 *>(row + c);
+        v = Four{make_float2(f.x, f.y), make_float2(f.z, f.w)};
     } else {
         each(v, [&](float &x, int k) { if (c + 32 * k < visible) x = row[c + 32 * k]; });
     }
     return v;
+}
+// `fill` behind the last visible key of a whole piece.
+template <bool VEC>
+__device__ __forceinline__ void fill_chunk(Four &v, int chunk, int lane, int visible, float fill)
+{
+    if (VEC && (chunk + 1) * 128 > visible)
+        each(v, [&](float &x, int k) { if (column<VEC>(chunk, lane, k) >= visible) x = fill; });
 }
 // Zeros where no key is visible.
 template <bool VEC>
@@ -123,13 +132,32 @@ __device__ __forceinline__ Four exponentials(Four v, float base)
 }
 __device__ __forceinline__ float finite_base(float top) { return top == -INFINITY ? 0.0f : top; }
 
+// The quads of a row: their numbers' lower halves from `lower` on.  (A row whose
+// numbers pass 2^32 has `split`, and each lane takes the upper half of its own.)
+struct RowDraws {
+    amsim::QuadStream stream;
+    uint32_t lower, upper;
+    bool split;
+};
+__device__ __forceinline__ RowDraws row_draws(int64_t row, const Params &p, uint64_t call)
+{
+    const uint64_t first = (uint64_t)row * (unsigned)p.quads;
+    RowDraws r;
+    r.lower = (uint32_t)first;
+    r.upper = (uint32_t)(first >> 32);
+    r.split = r.lower + (unsigned)p.chunks * 32u < r.lower;
+    r.stream = amsim::quad_stream(r.upper, call, p.drop);
+    return r;
+}
 // Dropout of a chunk's values, which stay times `scale`.  A lane draws the quad
 // of columns 4 lane ..; where it has other columns the lanes exchange one bit a column.
 template <bool VEC>
-__device__ __forceinline__ void drop_chunk(Four &v, int64_t row, int chunk, int lane, const Params &p, uint64_t call,
-                                           float scale)
+__device__ __forceinline__ void drop_chunk(Four &v, const RowDraws &r, int chunk, int lane, const Params &p,
+                                           uint64_t call, float scale)
 {
-    const uint4 w = amsim::philox((uint64_t)row * (unsigned)p.quads + (unsigned)(chunk * 32 + lane), call, p.drop.seed);
+    const uint32_t quad = r.lower + (uint32_t)(chunk * 32 + lane);
+    const uint4 w = amsim::quad_words(
+        quad, r.split && quad < r.lower ? amsim::quad_stream(r.upper + 1, call, p.drop) : r.stream, p.drop);
     const uint32_t border = p.drop.border;
     v = mul(v, four(scale));
     if (VEC) {
@@ -176,8 +204,7 @@ __device__ __forceinline__ void add_bias(Four &v, const float *bias, int chunk, 
     }
 }
 
-// One row: where it is, what it sees, and its query's place, brought near enough
-// for 32 bits.  Warps that take rows of their own take them by the place modulo
+// One row: where it is, what it sees, and its query's place.  Warps that take rows of their own take them by the place modulo
 // eight, so that a warp's sums by distance keep their place modulo four.
 struct Row {
     int64_t row;
@@ -185,23 +212,41 @@ struct Row {
     bool on;
 };
 template <bool BLOCK>
-__device__ __forceinline__ Row row_of(const Params &p, int head, int group)
+__device__ __forceinline__ Row row_of(const Params &p, int head, int b, int i)
 {
-    const int b = (int)((unsigned)group / (unsigned)p.row_groups);
-    int i = group - b * p.row_groups;
     const int64_t first = p.offsets ? (int64_t)p.offsets[b] : p.offset;
     if (!BLOCK) i = kWarpRows * i + (((int)(threadIdx.x >> 5) - (int)first) & (kWarpRows - 1));
     Row w;
     w.on = i < p.queries;
     w.row = ((int64_t)b * p.heads + head) * p.queries + i;
-    const int64_t pos = first + i;
-    int64_t end = p.keys;
-    if (p.lengths) end = min(end, (int64_t)max(p.lengths[b], 0));
-    if (p.causal) end = min(end, max(pos + 1, (int64_t)0));
-    w.visible = (int)end;
-    // every column of the row's chunks stays further than D from a place that is brought near
-    w.pos = (int)max(min(pos, (int64_t)p.chunks * 128 + p.D + 8), -(int64_t)p.D - 8);
+    int end = p.keys;
+    if (p.lengths) end = min(end, max(p.lengths[b], 0));
+    // brought near enough for 32 bits; every column of the row's chunks then stays further than D
+    const int64_t pos = max(min(first + i, (int64_t)p.chunks * 128 + p.D + 8), -(int64_t)p.D - 8);
+    w.pos = (int)pos;
+    if (p.causal) end = min(end, max(w.pos + 1, 0));
+    w.visible = end;
     return w;
+}
+// A head's groups of rows in turn, from the share's first on: sequence and place in it.
+struct Place {
+    int b, i;
+};
+__device__ __forceinline__ Place first_place(const Params &p, int share)
+{
+    Place t;
+    t.b = (int)((unsigned)share / (unsigned)p.row_groups);
+    t.i = share - t.b * p.row_groups;
+    return t;
+}
+__device__ __forceinline__ void advance(const Params &p, Place &t)
+{
+    t.i += p.ahead_i;
+    t.b += p.ahead_b;
+    if (t.i >= p.row_groups) {
+        t.i -= p.row_groups;
+        ++t.b;
+    }
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -212,9 +257,9 @@ __device__ __forceinline__ float warp_sum(float v)
 }
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
-    return v;
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 
 // A cluster's blocks.
@@ -327,13 +372,16 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(
     }
     const uint64_t call = amsim::drop_call(p.drop);
     int turn = 0;
-    for (int g = t.share; g < p.groups; g += p.shares, turn ^= 1) {
-        const Row w = row_of<BLOCK>(p, t.head, g);
+    Place at = first_place(p, t.share);
+    for (int g = t.share; g < p.groups; g += p.shares, turn ^= 1, advance(p, at)) {
+        const Row w = row_of<BLOCK>(p, t.head, at.b, at.i);
         if (!BLOCK && !w.on) continue;
         const float *in = p.scores + w.row * p.ld_in;
         float *out = p.out + w.row * p.ld_out;
-        auto logits = [&](int chunk) {
-            Four a = load_chunk<VEC>(in, chunk, lane, w.visible, -INFINITY);
+        RowDraws draws{};
+        if (p.drop.border) draws = row_draws(w.row, p, call);
+        auto logits = [&](Four a, int chunk) {
+            fill_chunk<VEC>(a, chunk, lane, w.visible, -INFINITY);
             if (p.table && chunk * 128 < w.visible) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
             return a;
         };
@@ -341,7 +389,7 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(
             if (chunk * 128 >= w.visible)
                 e = four(0.0f);
             else if (p.drop.border)
-                drop_chunk<VEC>(e, w.row, chunk, lane, p, call, factor * p.drop.scale);
+                drop_chunk<VEC>(e, draws, chunk, lane, p, call, factor * p.drop.scale);
             else
                 e = mul(e, four(factor));
             hide<VEC>(e, chunk, lane, w.visible);
@@ -352,7 +400,10 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(
         if (NV) {
             Four a[NV ? NV : 1];
 #pragma unroll
-            for (int v = 0; v < NV; ++v) a[v] = logits(t.first_chunk + v * t.step);
+            for (int v = 0; v < NV; ++v)
+                a[v] = load_chunk<VEC>(in, t.first_chunk + v * t.step, lane, w.visible, -INFINITY);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) a[v] = logits(a[v], t.first_chunk + v * t.step);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
                 mine = fmaxf(fmaxf(mine, fmaxf(a[v].a.x, a[v].a.y)), fmaxf(a[v].b.x, a[v].b.y));
@@ -370,7 +421,7 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(
             for (int v = 0; v < NV; ++v) finish(a[v], t.first_chunk + v * t.step, factor);
         } else {
             for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += t.step) {
-                const Four a = logits(chunk);
+                const Four a = logits(load_chunk<VEC>(in, chunk, lane, w.visible, -INFINITY), chunk);
                 const float most = fmaxf(fmaxf(a.a.x, a.a.y), fmaxf(a.b.x, a.b.y));
                 if (most > mine) {
                     total *= part_factor(mine, most);
@@ -383,7 +434,8 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(
             joined = join_rows<BLOCK>(p, top, total, exchange, turn);
             const float base = finite_base(joined.x);
             for (int chunk = t.first_chunk; chunk < p.chunks; chunk += t.step)
-                finish(exponentials(logits(chunk), base), chunk, joined.y);
+                finish(exponentials(logits(load_chunk<VEC>(in, chunk, lane, w.visible, -INFINITY), chunk), base), chunk,
+                       joined.y);
         }
         if (p.out_stats && lane == 0 && (!BLOCK || (threadIdx.x == 0 && t.rank == 0)))
             *reinterpret_cast<float2 *>(p.out_stats + 2 * w.row) = joined;
@@ -424,8 +476,9 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) backward_kernel
     float2 before = both(0.0f), behind = both(0.0f);     // columns at distances up to -D, from D on
     const int shift = VEC && !BLOCK ? (warp - p.D) & 3 : 0;
     int turn = 0;
-    for (int g = t.share; g < p.groups; g += p.shares, turn ^= 1) {
-        const Row w = row_of<BLOCK>(p, t.head, g);
+    Place at = first_place(p, t.share);
+    for (int g = t.share; g < p.groups; g += p.shares, turn ^= 1, advance(p, at)) {
+        const Row w = row_of<BLOCK>(p, t.head, at.b, at.i);
         if (!BLOCK && !w.on) continue;
         const float *in = (p.probs ? p.probs : p.scores) + w.row * p.ld_in, *up = p.dprobs + w.row * p.ld_g;
         float *out = p.out + w.row * p.ld_out;
@@ -436,12 +489,16 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) backward_kernel
             inv = f.y;
         }
         const int origin = p.D + 4 - w.pos;              // entry of column 0
+        RowDraws draws{};
+        if (p.drop.border) draws = row_draws(w.row, p, call);
         auto values = [&](int chunk, Four &a, Four &d) {
+            fill_chunk<VEC>(a, chunk, lane, w.visible, p.probs ? 0.0f : -INFINITY);
+            fill_chunk<VEC>(d, chunk, lane, w.visible, 0.0f);
             if (p.probs || chunk * 128 >= w.visible) return;
             if (p.table) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
             a = mul(exponentials(a, base), four(inv));
             hide<VEC>(a, chunk, lane, w.visible);
-            if (p.drop.border) drop_chunk<VEC>(d, w.row, chunk, lane, p, call, p.drop.scale);
+            if (p.drop.border) drop_chunk<VEC>(d, draws, chunk, lane, p, call, p.drop.scale);
         };
         auto finish = [&](int chunk, float dot, Four a, const Four &d) {
             a = chunk * 128 < w.visible ? mul(a, add(d, four(-dot))) : four(0.0f);
@@ -620,14 +677,6 @@ int64_t row_groups(const amsim_attention_softmax_desc *d, const Shape &s)
     return s.block ? d->queries : (d->queries + kWarpRows - 1) / kWarpRows;
 }
 
-// Shares of a head's groups of rows: as many blocks as fill the SMs, no more than groups.
-int share_count(const amsim_attention_softmax_desc *d, const Shape &s, int sms)
-{
-    const int64_t groups = d->batch * row_groups(d, s);
-    const int64_t blocks = (int64_t)sms * std::max(1, 2048 / s.threads) / s.cluster;
-    return (int)std::max<int64_t>(1, std::min(blocks / std::max<int64_t>(1, d->heads), groups));
-}
-
 template <bool VEC>
 auto *forward_of(const Shape &s)
 {
@@ -654,6 +703,40 @@ constexpr int shared_bytes(int D, bool table, bool dtable, int arrays)
     return 4 * ((table ? 4 * entries_at(D) : 0) + (dtable ? arrays * (entries_at(D) + 4) + (table ? 0 : 2 * D + 1) : 0));
 }
 constexpr int kMaxShared = shared_bytes(AMSIM_MAX_DISTANCE, true, true, kWarpRows);
+
+// How many of a kernel's blocks an SM holds; asked once for each kernel and shape.
+int resident_blocks(void (*kernel)(Params), int threads, int bytes)
+{
+    struct Known {
+        void (*kernel)(Params);
+        int threads, bytes, count;
+    };
+    constexpr int kMost = 64;
+    static std::mutex mutex;
+    static Known known[kMost];
+    static int held, next;
+    std::lock_guard<std::mutex> lock(mutex);
+    for (int i = 0; i < held; ++i)
+        if (known[i].kernel == kernel && known[i].threads == threads && known[i].bytes == bytes) return known[i].count;
+    int count = 0;
+    if (bytes > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&count, kernel, threads, (size_t)bytes) != cudaSuccess || count < 1) {
+        cudaGetLastError();
+        return std::max(1, 1024 / threads);              // no device here
+    }
+    known[next] = Known{kernel, threads, bytes, count};
+    held = std::max(held, next + 1);
+    next = (next + 1) % kMost;
+    return count;
+}
+
+// Shares of a head's groups of rows: as many blocks as the SMs hold at once, no more than groups.
+int share_count(const amsim_attention_softmax_desc *d, const Shape &s, void (*kernel)(Params), int bytes, int sms)
+{
+    const int64_t groups = d->batch * row_groups(d, s);
+    const int64_t blocks = (int64_t)sms * resident_blocks(kernel, s.threads, bytes) / s.cluster;
+    return (int)std::max<int64_t>(1, std::min(blocks / std::max<int64_t>(1, d->heads), groups));
+}
 
 int launch(void (*kernel)(Params), const Params &p, const Shape &s, int bytes, cudaStream_t st)
 {
@@ -693,6 +776,8 @@ void fill(Params &p, const amsim_attention_softmax_desc *d, const Shape &s, int 
     p.row_groups = (int)row_groups(d, s);
     p.groups = (int)(d->batch * p.row_groups);
     p.shares = shares;
+    p.ahead_b = shares / p.row_groups;
+    p.ahead_i = shares % p.row_groups;
     p.cluster = s.cluster;
     p.causal = d->causal;
 }
@@ -730,15 +815,17 @@ extern "C" int amsim_attention_softmax_fwd(const amsim_attention_softmax_desc *d
     const int sms = device_sms();
     if (!sms) return AMSIM_ECUDA;
     const Shape s = shape(d->keys, true);
-    fill(p, d, s, share_count(d, s, sms));
+    const bool vec = aligned(scores, 16) && aligned(probs, 16) && !((d->keys | stride(d->ld_scores, d->keys) |
+                                                                     stride(d->ld_probs, d->keys)) & 3);
+    auto *kernel = vec ? forward_of<true>(s) : forward_of<false>(s);
+    const int bytes = shared_bytes(p.D, table, false, 0);
+    fill(p, d, s, share_count(d, s, kernel, bytes, sms));
     p.scores = scores;
     p.out = probs;
     p.out_stats = stats;
     p.ld_in = stride(d->ld_scores, d->keys);
     p.ld_out = stride(d->ld_probs, d->keys);
-    const bool vec = aligned(scores, 16) && aligned(probs, 16) && !((d->keys | p.ld_in | p.ld_out) & 3);
-    return launch(vec ? forward_of<true>(s) : forward_of<false>(s), p, s, shared_bytes(p.D, table, false, 0),
-                  static_cast<cudaStream_t>(stream));
+    return launch(kernel, p, s, bytes, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t amsim_attention_softmax_workspace_size(const amsim_attention_softmax_desc *d)
@@ -748,7 +835,13 @@ extern "C" size_t amsim_attention_softmax_workspace_size(const amsim_attention_s
     if (!d->batch || !d->heads || !d->queries || !d->keys) return 0;
     const int sms = device_sms();
     const Shape s = shape(d->keys, false);
-    const int64_t blocks = (int64_t)share_count(d, s, sms ? sms : 1) * s.cluster;
+    int shares = 0;
+    for (const bool vec : {false, true})         // the calls' pointers and arguments decide which
+        for (const bool table : {false, true})
+            shares = std::max(shares, share_count(d, s, vec ? backward_of<true>(s) : backward_of<false>(s),
+                                                  shared_bytes(d->max_distance, table, true, s.block ? 4 : kWarpRows),
+                                                  sms ? sms : 1));
+    const int64_t blocks = (int64_t)shares * s.cluster;
     return blocks > 1 ? (size_t)d->heads * blocks * (2 * d->max_distance + 1) * 4 : 0;
 }
 
@@ -779,16 +872,17 @@ extern "C" int amsim_attention_softmax_bwd(const amsim_attention_softmax_desc *d
     if (!aligned(stats, 8)) return AMSIM_EINVAL;
     const int sms = device_sms();
     if (!sms) return AMSIM_ECUDA;
+    const bool vec = aligned(scores, 16) && aligned(probs, 16) && aligned(dprobs, 16) && aligned(dscores, 16) &&
+                     !((d->keys | stride(scores ? d->ld_scores : d->ld_probs, d->keys) |
+                        stride(d->ld_dprobs, d->keys) | stride(d->ld_dscores, d->keys)) & 3);
     Shape s = shape(d->keys, false);
-    int shares = share_count(d, s, sms);
-    if (dtable) {
-        const size_t one = (size_t)d->heads * (2 * p.D + 1) * 4, room = ws ? ws_bytes / one : 0;
-        if (s.cluster > 1 && room < (size_t)s.cluster) {     // no room for a cluster's sums: one block, rows read twice
-            s = Shape{0, 1024, 1, true};
-            shares = share_count(d, s, sms);
-        }
-        shares = (int)std::max<size_t>(1, std::min<size_t>(shares, room / s.cluster));
-    }
+    const size_t one = (size_t)d->heads * (2 * p.D + 1) * 4, room = ws ? ws_bytes / one : 0;
+    if (dtable && s.cluster > 1 && room < (size_t)s.cluster)
+        s = Shape{0, 1024, 1, true};             // no room for a cluster's sums: one block, rows read twice
+    auto *kernel = vec ? backward_of<true>(s) : backward_of<false>(s);
+    const int bytes = shared_bytes(p.D, table, dtable, s.block ? 4 : kWarpRows);
+    int shares = share_count(d, s, kernel, bytes, sms);
+    if (dtable) shares = (int)std::max<size_t>(1, std::min<size_t>(shares, room / s.cluster));
     fill(p, d, s, shares);
     p.dprobs = dprobs;
     p.scores = scores;
@@ -799,10 +893,7 @@ extern "C" int amsim_attention_softmax_bwd(const amsim_attention_softmax_desc *d
     p.ld_in = stride(scores ? d->ld_scores : d->ld_probs, d->keys);
     p.ld_g = stride(d->ld_dprobs, d->keys);
     p.ld_out = stride(d->ld_dscores, d->keys);
-    const bool vec = aligned(scores, 16) && aligned(probs, 16) && aligned(dprobs, 16) && aligned(dscores, 16) &&
-                     !((d->keys | p.ld_in | p.ld_g | p.ld_out) & 3);
-    rc = launch(vec ? backward_of<true>(s) : backward_of<false>(s), p, s,
-                shared_bytes(p.D, table, dtable, s.block ? 4 : kWarpRows), st);
+    rc = launch(kernel, p, s, bytes, st);
     if (rc || !dtable || p.shares * p.cluster == 1) return rc;
     rc = amsim::cuda_status(amsim::chain_launch(true, table_kernel, dim3((unsigned)p.heads), kTableThreads,
                                                 4 * (2 * p.D + 1), st, p));

@@ -54,7 +54,14 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T *x, const T *
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = widen(in[i].e[q + k]);
-            if (d.border) amsim::drop_quad(v, (uint64_t)(at + q) >> 2, d, call);
+            if (d.border) {
+                const uint64_t quad = (uint64_t)(at + q) >> 2;
+                const uint4 u = amsim::quad_words((uint32_t)quad, amsim::quad_stream((uint32_t)(quad >> 32), call, d), d);
+                v[0] = u.x >= d.border ? v[0] * d.scale : 0.0f;
+                v[1] = u.y >= d.border ? v[1] * d.scale : 0.0f;
+                v[2] = u.z >= d.border ? v[2] * d.scale : 0.0f;
+                v[3] = u.w >= d.border ? v[3] * d.scale : 0.0f;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) narrow(RESIDUAL ? v[k] + widen(res[i].e[q + k]) : v[k], &out.e[q + k]);
         }
