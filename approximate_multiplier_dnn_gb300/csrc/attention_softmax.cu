@@ -45,6 +45,7 @@ struct Params {
 };
 
 constexpr int kWarpRows = 8;                 // warps of a block that each take a row
+constexpr int kFewThreads = 768;             // of a block that keeps four chunks of two tensors a warp
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr float kLog2E = 1.44269504088896341f;
 
@@ -87,6 +88,8 @@ __device__ __forceinline__ Four load_chunk(const float *row, int chunk, int lane
         float4 f = make_float4(fill, fill, fill, fill);
         if (c < visible) f = *reinterpret_cast<const float4 *>(row + c);
         v = Four{make_float2(f.x, f.y), make_float2(f.z, f.w)};
+    } else if ((chunk + 1) * 128 <= visible) {
+        each(v, [&](float &x, int k) { x = row[c + 32 * k]; });
     } else {
         each(v, [&](float &x, int k) { if (c + 32 * k < visible) x = row[c + 32 * k]; });
     }
@@ -111,6 +114,8 @@ __device__ __forceinline__ void store_chunk(float *row, int chunk, int lane, int
     const int c = column<VEC>(chunk, lane, 0);
     if (VEC) {
         if (c < keys) *reinterpret_cast<float4 *>(row + c) = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
+    } else if ((chunk + 1) * 128 <= keys) {
+        each(v, [&](float &x, int k) { row[c + 32 * k] = x; });
     } else {
         each(v, [&](float &x, int k) { if (c + 32 * k < keys) row[c + 32 * k] = x; });
     }
@@ -149,6 +154,10 @@ __device__ __forceinline__ RowDraws row_draws(int64_t row, const Params &p, uint
     r.stream = amsim::quad_stream(r.upper, call, p.drop);
     return r;
 }
+__device__ __noinline__ amsim::QuadStream next_stream(uint32_t upper, uint64_t call, const Drop &d)
+{
+    return amsim::quad_stream(upper + 1, call, d);
+}
 // Dropout of a chunk's values, which stay times `scale`.  A lane draws the quad
 // of columns 4 lane ..; where it has other columns the lanes exchange one bit a column.
 template <bool VEC>
@@ -156,8 +165,9 @@ __device__ __forceinline__ void drop_chunk(Four &v, const RowDraws &r, int chunk
                                            uint64_t call, float scale)
 {
     const uint32_t quad = r.lower + (uint32_t)(chunk * 32 + lane);
-    const uint4 w = amsim::quad_words(
-        quad, r.split && quad < r.lower ? amsim::quad_stream(r.upper + 1, call, p.drop) : r.stream, p.drop);
+    amsim::QuadStream stream = r.stream;
+    if (r.split && quad < r.lower) stream = next_stream(r.upper, call, p.drop);
+    const uint4 w = amsim::quad_words(quad, stream, p.drop);
     const uint32_t border = p.drop.border;
     v = mul(v, four(scale));
     if (VEC) {
@@ -457,7 +467,7 @@ __device__ __forceinline__ void by_bucket(const Params &p, int head, const float
 }
 
 template <int NV, bool VEC, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) backward_kernel(const Params p)
+__global__ void __launch_bounds__(!BLOCK ? 32 * kWarpRows : NV == 4 ? kFewThreads : 1024) backward_kernel(const Params p)
 {
     extern __shared__ __align__(16) float shared[];
     __shared__ Exchange exchange;
@@ -616,12 +626,17 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const Params p)
     amsim::chain_wait();
     const int n = 2 * p.D + 1, blocks = p.shares * p.cluster;
     const float *part = p.part + (int64_t)blockIdx.x * blocks * n;
-    for (int i = threadIdx.x; i < n; i += kTableThreads) {
+    // as many threads for an entry as there are, each every parts-th block, sixteen loads at a time
+    const int parts = max(1, min(kTableThreads / n, blocks / 16)), mine = (int)threadIdx.x / n;
+    for (int i = (int)threadIdx.x - mine * n; mine < parts && i < n; i += kTableThreads) {
         float s = 0.0f;
-#pragma unroll 8
-        for (int t = 0; t < blocks; ++t) s += part[(int64_t)t * n + i];
-        shared[i] = s;
+#pragma unroll 16
+        for (int t = mine; t < blocks; t += parts) s += part[(int64_t)t * n + i];
+        shared[mine * n + i] = s;
     }
+    __syncthreads();
+    for (int i = threadIdx.x; parts > 1 && i < n; i += kTableThreads)
+        for (int q = 1; q < parts; ++q) shared[i] += shared[q * n + i];
     __syncthreads();
     by_bucket(p, (int)blockIdx.x, shared);
 }
@@ -645,9 +660,10 @@ int check(const amsim_attention_softmax_desc *d, Drop *drop)
     return amsim::make_drop(d->dropout, drop) ? AMSIM_OK : AMSIM_EINVAL;
 }
 
-// How rows are shared: up to four chunks by a warp; then by a block, two chunks a
-// warp (forward four where that spares a cluster), then by a cluster of blocks.
-// Backward keeps two tensors: twice the registers.
+// How rows are shared: up to four chunks by a warp, then by a block, four chunks a
+// warp (what a row costs each warp is spread over 16 columns a lane), then by a
+// cluster of blocks.  Backward keeps two tensors, and beyond 512 threads of them
+// two chunks a warp.
 constexpr int kMaxCluster = 8;
 struct Shape {
     int nv, threads, cluster;
@@ -662,7 +678,7 @@ Shape shape(int64_t keys, bool fwd)
         return s;
     }
     s.block = true;
-    s.nv = chunks <= 64 || !fwd ? 2 : 4;
+    s.nv = fwd || chunks <= 4 * kFewThreads / 32 ? 4 : 2;
     const int64_t blocks = (chunks + 32 * s.nv - 1) / (32 * s.nv);
     s.cluster = 1;
     while (s.cluster < blocks && s.cluster < kMaxCluster) s.cluster *= 2;
@@ -683,8 +699,7 @@ auto *forward_of(const Shape &s)
     if (!s.block)
         return s.nv == 1 ? forward_kernel<1, VEC, false> : s.nv == 2 ? forward_kernel<2, VEC, false>
                                                                      : forward_kernel<4, VEC, false>;
-    return s.nv == 2 ? forward_kernel<2, VEC, true> : s.nv == 4 ? forward_kernel<4, VEC, true>
-                                                                : forward_kernel<0, VEC, true>;
+    return s.nv ? forward_kernel<4, VEC, true> : forward_kernel<0, VEC, true>;
 }
 template <bool VEC>
 auto *backward_of(const Shape &s)
@@ -692,7 +707,9 @@ auto *backward_of(const Shape &s)
     if (!s.block)
         return s.nv == 1 ? backward_kernel<1, VEC, false> : s.nv == 2 ? backward_kernel<2, VEC, false>
                                                                       : backward_kernel<4, VEC, false>;
-    return s.nv == 2 ? backward_kernel<2, VEC, true> : backward_kernel<0, VEC, true>;
+    return s.nv == 4   ? backward_kernel<4, VEC, true>
+           : s.nv == 2 ? backward_kernel<2, VEC, true>
+                       : backward_kernel<0, VEC, true>;
 }
 
 // Shared memory of the bias and of the sums by distance, and the most of it;
@@ -896,7 +913,7 @@ extern "C" int amsim_attention_softmax_bwd(const amsim_attention_softmax_desc *d
     rc = launch(kernel, p, s, bytes, st);
     if (rc || !dtable || p.shares * p.cluster == 1) return rc;
     rc = amsim::cuda_status(amsim::chain_launch(true, table_kernel, dim3((unsigned)p.heads), kTableThreads,
-                                                4 * (2 * p.D + 1), st, p));
+                                                4 * std::max(kTableThreads, 2 * p.D + 1), st, p));
     if (rc == AMSIM_OK) amsim::count_launch();
     return rc;
 }
