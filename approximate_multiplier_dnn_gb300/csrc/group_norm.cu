@@ -1,14 +1,14 @@
 // The group norm with its activation, channels last, and its gradients.
 //
-// Two ways.  Where a slab (a sample's pixels over some whole groups, at least
-// 128 bytes of a pixel) fits the shared memory of a cluster, its blocks keep it
-// there: x (backward: x and dy) is read once and the result written, which is
-// all that has to move.  Each thread copies, sums and finishes pieces of its
-// own, so the copies need no barrier between threads; the blocks of a cluster
-// exchange the groups' sums through distributed shared memory.  Larger slabs go
-// through three launches that read x (and dy) twice.
+// x is needed twice, for the statistics and for the result; what has to move is
+// one reading.  So the tensor goes through in waves of some megabytes: a launch
+// works out the statistics of one wave and the results of the wave before, whose
+// x (and dy) it then finds in the L2 cache.  Blocks of both roles stream and
+// share nothing, statistics are joined by whoever needs them, in a fixed order,
+// and the launches overlap: a wave's statistics wait for nothing.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -18,21 +18,50 @@
 
 namespace {
 
+using amsim::add2;
+using amsim::both;
+using amsim::fma2;
+using amsim::mul2;
+
+// Quotients by a number that the host knows: a product's upper half (exact for
+// dividends below 2^31: the multiplier is the next whole number above 2^(32 + shift) / d).
+struct Divisor {
+    unsigned d, mul, shift;
+    __device__ __forceinline__ unsigned operator()(unsigned n) const
+    {
+        return d == 1 ? n : __umulhi(n, mul) >> shift;
+    }
+};
+Divisor divisor(unsigned d)
+{
+    Divisor r{d, 0, 0};
+    if (d == 1) return r;
+    while ((1ull << (r.shift + 1)) < d) ++r.shift;
+    r.mul = (unsigned)(((1ull << (32 + r.shift)) + d - 1) / d);
+    return r;
+}
+
 struct Params {
     const void *x, *dy;
     const float *w, *b;
     void *y, *dx;
     float *mean, *rstd, *dw, *db;
-    float2 *part, *sums, *means;             // scratch: [batch][chunks][channels], [batch][channels], [batch][groups]
-    int64_t pixels, ldx, ldy, lddx, chunk;   // chunk: pixels of a share
-    int batch, chunks, channels, groups, size;   // size: channels of a group
-    int act, tx, tiles;                      // tx: threads side by side over channels
-    int slab, slab_groups, slabs, cluster;   // resident: channels and groups of a slab; blocks of a cluster,
-    int rows, step, steps;                   // pixels of a block, of its threads at once, of a thread
+    // scratch: of each sample's chunk of pixels, per part of a group (mean, sum of
+    // squares about it; backward the sums of dz w and dz w xh), per channel (dz, dz xh)
+    float2 *by_part, *by_channel;
+    int64_t pixels, ldx, ldy, lddx, samples_chunks;
+    int channels, groups, size;              // size: channels of a group
+    int act;
     float eps;
+    // A tile is some channels of a sample: whole groups, or (splits > 1) a part of one.
+    int tile, tiles, splits, chunks, rows;   // tile: channels; rows: pixels of a chunk
+    int step, vec;                           // pixels of a block at once; w and b on 16 bytes
+    Divisor by_tiles, by_splits, by_chunks, by_wide, by_step, by_group_wide, by_size;
+    unsigned stat_units, stat_first, apply_units, apply_first;   // units (sample, tile) of a launch's two roles
 };
 
 constexpr int kThreads = 256;
+constexpr int kTileGroups = 128;             // at most
 
 template <typename T, int E>
 struct alignas(sizeof(T) * E) Vec {
@@ -132,353 +161,6 @@ __device__ __forceinline__ float before_activation(float dy, float x, float xh, 
     return dy * (s * fmaf(z, 1.0f - s, 1.0f));
 }
 
-// A thread's place: its first channel and its first pixel, by blocks of
-// (chunk of pixels, tile of channels, sample).
-struct Place {
-    int n, chunk, c, y, ty;
-    int64_t first, last;
-    bool on;
-};
-template <int E>
-__device__ __forceinline__ Place place(const Params &p)
-{
-    Place t;
-    const int tile = (int)(blockIdx.x / (unsigned)p.chunks) % p.tiles;
-    t.n = (int)(blockIdx.x / (unsigned)p.chunks) / p.tiles;
-    t.chunk = (int)(blockIdx.x % (unsigned)p.chunks);
-    t.ty = kThreads / p.tx;
-    t.y = threadIdx.x / p.tx;
-    t.c = (tile * p.tx + (int)threadIdx.x % p.tx) * E;
-    t.on = t.c < p.channels;
-    t.first = t.chunk * p.chunk;
-    t.last = min(t.first + p.chunk, p.pixels);
-    return t;
-}
-
-// Each channel's moments over a chunk of pixels.  A thread sums about its first
-// value, so what cancels is no larger than the values' own spread.
-template <typename TX, int E>
-__global__ void __launch_bounds__(kThreads) moments_kernel(const Params p)
-{
-    __shared__ Moments all[E][kThreads];
-    const Place t = place<E>(p);
-    float s1[E] = {}, s2[E] = {}, about[E] = {};
-    int count = 0;
-    if (t.on) {
-        const TX *x = static_cast<const TX *>(p.x) + t.n * p.pixels * p.ldx + t.c;
-#pragma unroll 4
-        for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
-            float v[E];
-            load<E>(x + i * p.ldx, v);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (count == 0) about[e] = v[e];
-                const float d = v[e] - about[e];
-                s1[e] += d;
-                s2[e] = fmaf(d, d, s2[e]);
-            }
-            ++count;
-        }
-    }
-    const float n = (float)count, inv = count ? 1.0f / n : 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float m = s1[e] * inv;
-        all[e][threadIdx.x] = Moments{n, about[e] + m, fmaxf(s2[e] - s1[e] * m, 0.0f)};
-    }
-    for (int half = t.ty >> 1; half; half >>= 1) {
-        __syncthreads();
-        if (t.y < half)
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                all[e][threadIdx.x] = join(all[e][threadIdx.x], all[e][threadIdx.x + half * p.tx]);
-    }
-    if (t.on && t.y == 0)
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            p.part[((int64_t)t.n * p.chunks + t.chunk) * p.channels + t.c + e] =
-                make_float2(all[e][threadIdx.x].mean, all[e][threadIdx.x].m2);
-}
-
-// A group's moments from its channels' over all chunks: a block per (n, g).
-__global__ void __launch_bounds__(kThreads) join_kernel(const Params p)
-{
-    __shared__ Moments all[kThreads];
-    amsim::chain_wait();
-    const int n = blockIdx.x / p.groups, g = blockIdx.x % p.groups;
-    Moments m{0.0f, 0.0f, 0.0f};
-    for (int64_t i = threadIdx.x; i < (int64_t)p.chunks * p.size; i += kThreads) {
-        const int64_t chunk = i / p.size;
-        const float2 v = p.part[((int64_t)n * p.chunks + chunk) * p.channels + g * p.size + i % p.size];
-        m = join(m, Moments{(float)(min((chunk + 1) * p.chunk, p.pixels) - chunk * p.chunk), v.x, v.y});
-    }
-    all[threadIdx.x] = m;
-    for (int half = kThreads / 2; half; half >>= 1) {
-        __syncthreads();
-        if (threadIdx.x < half) all[threadIdx.x] = join(all[threadIdx.x], all[threadIdx.x + half]);
-    }
-    if (threadIdx.x == 0) {
-        p.mean[blockIdx.x] = all[0].mean;
-        p.rstd[blockIdx.x] = 1.0f / sqrtf((all[0].n > 0.0f ? all[0].m2 / all[0].n : 0.0f) + p.eps);
-    }
-}
-
-template <int E>
-struct Channels {
-    float mean[E], rstd[E], w[E], b[E];
-};
-template <int E>
-__device__ __forceinline__ Channels<E> channels(const Params &p, int n, int c)
-{
-    Channels<E> k;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int g = (c + e) / p.size;
-        k.mean[e] = p.mean[(int64_t)n * p.groups + g];
-        k.rstd[e] = p.rstd[(int64_t)n * p.groups + g];
-        k.w[e] = p.w ? p.w[c + e] : 1.0f;
-        k.b[e] = p.b ? p.b[c + e] : 0.0f;
-    }
-    return k;
-}
-
-template <typename TX, typename TY, int E>
-__global__ void __launch_bounds__(kThreads) apply_kernel(const Params p)
-{
-    amsim::chain_wait();
-    const Place t = place<E>(p);
-    if (!t.on) return;
-    const TX *x = static_cast<const TX *>(p.x) + t.n * p.pixels * p.ldx + t.c;
-    TY *y = static_cast<TY *>(p.y) + t.n * p.pixels * p.ldy + t.c;
-    const Channels<E> k = channels<E>(p, t.n, t.c);
-    with_activation(p.act, [&](auto act) {
-#pragma unroll 4
-        for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
-            float v[E];
-            load<E>(x + i * p.ldx, v);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                v[e] = activate<act.value>(fmaf((v[e] - k.mean[e]) * k.rstd[e], k.w[e], k.b[e]));
-            store<E>(y + i * p.ldy, v);
-        }
-    });
-}
-
-// Each channel's sums of dz and dz xh over a chunk of pixels.
-template <typename TX, typename TY, int E>
-__global__ void __launch_bounds__(kThreads) sums_kernel(const Params p)
-{
-    __shared__ float2 all[E][kThreads];
-    const Place t = place<E>(p);
-    float2 s[E] = {};
-    if (t.on) {
-        const TX *x = static_cast<const TX *>(p.x) + t.n * p.pixels * p.ldx + t.c;
-        const TY *dy = static_cast<const TY *>(p.dy) + t.n * p.pixels * p.ldy + t.c;
-        const Channels<E> k = channels<E>(p, t.n, t.c);
-        with_activation(p.act, [&](auto act) {
-#pragma unroll 2
-            for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
-                float v[E], d[E];
-                load<E>(x + i * p.ldx, v);
-                load<E>(dy + i * p.ldy, d);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float xh = (v[e] - k.mean[e]) * k.rstd[e];
-                    const float dz = before_activation<act.value>(d[e], v[e], xh, k.mean[e], k.rstd[e], k.w[e], k.b[e]);
-                    s[e].x += dz;
-                    s[e].y = fmaf(dz, xh, s[e].y);
-                }
-            }
-        });
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) all[e][threadIdx.x] = s[e];
-    for (int half = t.ty >> 1; half; half >>= 1) {
-        __syncthreads();
-        if (t.y < half)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                all[e][threadIdx.x].x += all[e][threadIdx.x + half * p.tx].x;
-                all[e][threadIdx.x].y += all[e][threadIdx.x + half * p.tx].y;
-            }
-    }
-    if (t.on && t.y == 0)
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            p.part[((int64_t)t.n * p.chunks + t.chunk) * p.channels + t.c + e] = all[e][threadIdx.x];
-}
-
-// A sample's sums by channel over its chunks, and a group's means of t and t xh: a block per (n, g).
-__global__ void __launch_bounds__(kThreads) means_kernel(const Params p)
-{
-    __shared__ float2 all[kThreads];
-    amsim::chain_wait();
-    const int n = blockIdx.x / p.groups, g = blockIdx.x % p.groups;
-    float2 m = make_float2(0.0f, 0.0f);
-    for (int i = threadIdx.x; i < p.size; i += kThreads) {
-        const int c = g * p.size + i;
-        float2 s = make_float2(0.0f, 0.0f);
-        for (int k = 0; k < p.chunks; ++k) {
-            const float2 v = p.part[((int64_t)n * p.chunks + k) * p.channels + c];
-            s.x += v.x;
-            s.y += v.y;
-        }
-        p.sums[(int64_t)n * p.channels + c] = s;
-        const float w = p.w ? p.w[c] : 1.0f;
-        m.x = fmaf(w, s.x, m.x);
-        m.y = fmaf(w, s.y, m.y);
-    }
-    all[threadIdx.x] = m;
-    for (int half = kThreads / 2; half; half >>= 1) {
-        __syncthreads();
-        if (threadIdx.x < half) {
-            all[threadIdx.x].x += all[threadIdx.x + half].x;
-            all[threadIdx.x].y += all[threadIdx.x + half].y;
-        }
-    }
-    if (threadIdx.x == 0) {
-        const float count = (float)p.size * (float)p.pixels;
-        p.means[blockIdx.x] = make_float2(all[0].x / count, all[0].y / count);
-    }
-}
-
-// dw and db from the samples' sums: a block takes 32 channels, its 32 warps every 32nd sample.
-__global__ void __launch_bounds__(1024) weights_kernel(const Params p)
-{
-    __shared__ float2 part[32][33];
-    amsim::chain_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = (int)blockIdx.x * 32 + lane;
-    float2 s = make_float2(0.0f, 0.0f);
-    if (c < p.channels)
-        for (int n = warp; n < p.batch; n += 32) {
-            const float2 v = p.sums[(int64_t)n * p.channels + c];
-            s.x += v.x;
-            s.y += v.y;
-        }
-    part[warp][lane] = s;
-    __syncthreads();
-    s = part[lane][warp];
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, d);
-        s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, d);
-    }
-    const int mine = (int)blockIdx.x * 32 + warp;
-    if (lane || mine >= p.channels) return;
-    if (p.db) p.db[mine] = s.x;
-    if (p.dw) p.dw[mine] = s.y;
-}
-
-template <typename TX, typename TY, int E>
-__global__ void __launch_bounds__(kThreads) gradient_kernel(const Params p)
-{
-    amsim::chain_wait();
-    const Place t = place<E>(p);
-    if (!t.on) return;
-    const TX *x = static_cast<const TX *>(p.x) + t.n * p.pixels * p.ldx + t.c;
-    const TY *dy = static_cast<const TY *>(p.dy) + t.n * p.pixels * p.ldy + t.c;
-    TX *dx = static_cast<TX *>(p.dx) + t.n * p.pixels * p.lddx + t.c;
-    const Channels<E> k = channels<E>(p, t.n, t.c);
-    float2 m[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) m[e] = p.means[(int64_t)t.n * p.groups + (t.c + e) / p.size];
-    with_activation(p.act, [&](auto act) {
-#pragma unroll 2
-        for (int64_t i = t.first + t.y; i < t.last; i += t.ty) {
-            float v[E], d[E];
-            load<E>(x + i * p.ldx, v);
-            load<E>(dy + i * p.ldy, d);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float xh = (v[e] - k.mean[e]) * k.rstd[e];
-                const float dz = before_activation<act.value>(d[e], v[e], xh, k.mean[e], k.rstd[e], k.w[e], k.b[e]);
-                v[e] = k.rstd[e] * (fmaf(dz, k.w[e], -m[e].x) - xh * m[e].y);
-            }
-            store<E>(dx + i * p.lddx, v);
-        }
-    });
-}
-
-// ------------------------------------------------------------------ resident slabs
-constexpr int kSlabThreads = 256, kSlabBlocks = 2;       // blocks: of an SM
-constexpr int kSlabGroups = 64;              // at most: 128 bytes of bf16 channels, a group each
-
-__device__ __forceinline__ uint32_t shared_address(const void *q)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(q));
-}
-// BYTES from global to this thread's own slot; done after copies_wait.
-template <int BYTES>
-__device__ __forceinline__ void copy_in(uint8_t *to, const void *from)
-{
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared_address(to)), "l"(from) : "memory");
-    else if constexpr (BYTES >= 4)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(shared_address(to)), "l"(from), "n"(BYTES)
-                     : "memory");
-    else
-        *reinterpret_cast<uint16_t *>(to) = *static_cast<const uint16_t *>(from);
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copies_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
-
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// No block leaves while another reads its sums: it says that it has read, and
-// waits at its end for all to have said so.  Nothing it wrote is handed over,
-// so its stores are not waited for.
-__device__ __forceinline__ void cluster_has_read() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
-__device__ __forceinline__ void cluster_leave() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
-// A float2 of block `rank` of the cluster at the place of this block's `q`.
-__device__ __forceinline__ float2 of_rank(const float2 *q, int rank)
-{
-    uint32_t at;
-    float2 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(shared_address(q)), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
-    return v;
-}
-
-// A thread's part of a slab: the channels of one piece, every `step`-th pixel
-// of the block's from `first` on.
-struct Part {
-    int n, c0, channels, groups;             // sample, first channel, channels and groups of the slab
-    int rank, wide, piece, row, step;        // wide: pieces of a pixel
-    int64_t first;                           // the block's first pixel
-    int rows, count;                         // the block's pixels, this thread's
-};
-template <int E>
-__device__ __forceinline__ Part part_of(const Params &p)
-{
-    Part t;
-    unsigned unit;
-    asm("mov.u32 %0, %%clusterid.x;" : "=r"(unit));
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(t.rank));
-    t.n = (int)(unit / (unsigned)p.slabs);
-    t.c0 = (int)(unit - (unsigned)t.n * (unsigned)p.slabs) * p.slab;
-    t.channels = p.slab;
-    t.groups = p.slab_groups;
-    t.step = p.step;
-    if (t.c0 + p.slab > p.channels) {        // the last slab is narrower
-        t.channels = p.channels - t.c0;
-        t.groups = t.channels / p.size;
-        t.step = kSlabThreads / (t.channels / E);
-    }
-    t.wide = t.channels / E;
-    t.row = (int)(threadIdx.x / (unsigned)t.wide);
-    t.piece = (int)threadIdx.x - t.row * t.wide;
-    t.first = (int64_t)t.rank * p.rows;
-    t.rows = (int)max((int64_t)0, min((int64_t)p.rows, p.pixels - t.first));
-    t.count = t.row < t.step ? (int)((unsigned)max(0, t.rows - t.row + t.step - 1) / (unsigned)t.step) : 0;
-    return t;
-}
-
 // Packed arithmetic on a piece's values, two an instruction.
 template <int E>
 struct Values {
@@ -502,16 +184,17 @@ __device__ __forceinline__ Values<E> take(const void *slot)
 template <int E, typename T>
 __device__ __forceinline__ void put(T *at, const Values<E> &r)
 {
-    float f[E];
+    if constexpr (sizeof(T) == 2 && E > 1) {     // a pair's rounding is one instruction
+        Vec<__nv_bfloat162, E / 2> v;
+        each_pair<E>([&](int j) { v.e[j] = __float22bfloat162_rn(r.v[j]); });
+        *reinterpret_cast<Vec<__nv_bfloat162, E / 2> *>(at) = v;
+    } else {
+        float f[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = e & 1 ? r.v[e >> 1].y : r.v[e >> 1].x;
-    store<E>(at, f);
+        for (int e = 0; e < E; ++e) f[e] = e & 1 ? r.v[e >> 1].y : r.v[e >> 1].x;
+        store<E>(at, f);
+    }
 }
-
-using amsim::add2;
-using amsim::both;
-using amsim::fma2;
-using amsim::mul2;
 
 __device__ __forceinline__ float2 sigmoid2(float2 z)
 {
@@ -537,6 +220,7 @@ __device__ __forceinline__ float2 before2(float2 dy, float2 x, float2 xh, float 
     return mul2(mul2(dy, s), fma2(z, fma2(s, both(-1.0f), both(1.0f)), both(1.0f)));
 }
 
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -544,178 +228,326 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// The copies are told apart in two halves, so that a thread sums what has
-// arrived while the rest is on its way.
-template <typename F>
-__device__ __forceinline__ void in_halves(int count, F use)
+// A block's part: a role, a tile of a sample, a chunk of its pixels; a thread's
+// part of that: the channels of one piece, which lies within one group, and
+// every step-th pixel.
+struct Part {
+    bool stats;
+    int n, chunk, c0, channels, groups;      // the tile's first channel, channels, groups (1: a part of one)
+    int group, split;                        // its first group, and which part of it
+    int wide, piece, row, step, count;       // pieces of a pixel; this thread's, its first pixel, how many
+    int mine;                                // its piece's group in the tile
+    int64_t first;                           // the chunk's first pixel in the sample
+    int rows;                                // and its pixels
+};
+template <int E>
+__device__ __forceinline__ Part part_of(const Params &p)
 {
-    const int half = (count + 1) >> 1;
-    copies_wait<1>();
-#pragma unroll 4
-    for (int i = 0; i < half; ++i) use(i);
-    copies_wait<0>();
-#pragma unroll 4
-    for (int i = half; i < count; ++i) use(i);
+    Part t;
+    // the roles' blocks in turn, as long as there are both
+    unsigned b = blockIdx.x;
+    const unsigned stats = p.stat_units * (unsigned)p.chunks, apply = p.apply_units * (unsigned)p.chunks;
+    const unsigned less = min(stats, apply);
+    t.stats = b < 2 * less ? !(b & 1) : stats > apply;
+    b = b < 2 * less ? b >> 1 : b - less;
+    const unsigned local = p.by_chunks(b), unit = local + (t.stats ? p.stat_first : p.apply_first);
+    t.chunk = (int)(b - local * (unsigned)p.chunks);
+    t.n = (int)p.by_tiles(unit);
+    const int tile = (int)(unit - (unsigned)t.n * (unsigned)p.tiles);
+    t.wide = p.tile / E;
+    t.step = p.step;
+    bool odd;                                // a tile that is narrower than the others
+    if (p.splits > 1) {
+        t.group = (int)p.by_splits((unsigned)tile);
+        t.split = tile - t.group * p.splits;
+        t.c0 = t.group * p.size + t.split * p.tile;
+        t.channels = min(p.tile, p.size - t.split * p.tile);
+        t.groups = 1;
+        odd = t.channels < p.tile;
+    } else {
+        t.c0 = tile * p.tile;
+        t.channels = min(p.tile, p.channels - t.c0);
+        t.group = (int)p.by_size((unsigned)t.c0);
+        t.split = 0;
+        t.groups = (int)p.by_size((unsigned)t.channels);
+        odd = t.channels < p.tile;
+    }
+    if (odd) {
+        t.wide = t.channels / E;
+        t.step = kThreads / t.wide;
+        t.row = (int)(threadIdx.x / (unsigned)t.wide);
+    } else {
+        t.row = (int)p.by_wide(threadIdx.x);
+    }
+    t.piece = (int)threadIdx.x - t.row * t.wide;
+    t.mine = p.splits > 1 ? 0 : (int)p.by_group_wide((unsigned)t.piece);
+    t.first = (int64_t)t.chunk * p.rows;
+    t.rows = (int)min((int64_t)p.rows, p.pixels - t.first);
+    const unsigned more = (unsigned)max(0, t.rows - t.row + t.step - 1);
+    t.count = t.row >= t.step ? 0 : (int)(odd ? more / (unsigned)t.step : p.by_step(more));
+    return t;
+}
+// Where the parts of a sample's chunk lie: one for each group, or for each split of it.
+__device__ __forceinline__ int64_t parts_at(const Params &p, int n, int chunk)
+{
+    return ((int64_t)n * p.chunks + chunk) * ((int64_t)p.groups * p.splits);
+}
+// How many values a part holds.
+__device__ __forceinline__ float values_of(const Params &p, int chunk, int split)
+{
+    const int64_t rows = min((int64_t)p.rows, p.pixels - (int64_t)chunk * p.rows);
+    const int channels = p.splits > 1 ? min(p.tile, p.size - split * p.tile) : p.size;
+    return (float)rows * (float)channels;
 }
 
-// Dynamic shared memory: the slots [steps][threads] of x (then of dy), then
-// (backward) sums by channel.  A piece lies within one group.
-template <typename TX, typename TY, int E>
-__global__ void __launch_bounds__(kSlabThreads, kSlabBlocks) slab_forward_kernel(const Params p)
+// The weights of a piece's channels.
+template <int E>
+__device__ __forceinline__ Values<E> weights_of(const Params &p, const float *w, int c, float otherwise)
 {
-    extern __shared__ __align__(16) uint8_t slots[];
-    __shared__ Moments all[kSlabThreads];
-    __shared__ float2 found[kSlabGroups], stats[kSlabGroups];
-    constexpr int bytes = E * (int)sizeof(TX);
-    const Part t = part_of<E>(p);
-    const int c = t.c0 + t.piece * E, mine = t.piece * E / p.size, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t pixel = t.n * p.pixels + t.first + t.row;
-    uint8_t *slot = slots + threadIdx.x * bytes;
-    {
-        const TX *x = static_cast<const TX *>(p.x) + pixel * p.ldx + c;
-        const int64_t far = (int64_t)t.step * p.ldx;
-        const int half = (t.count + 1) >> 1;
-#pragma unroll 4
-        for (int i = 0; i < half; ++i) copy_in<bytes>(slot + i * (kSlabThreads * bytes), x + i * far);
-        copies_commit();
-#pragma unroll 4
-        for (int i = half; i < t.count; ++i) copy_in<bytes>(slot + i * (kSlabThreads * bytes), x + i * far);
-        copies_commit();
+    Values<E> r;
+    if (E >= 4 && w && p.vec) {
+#pragma unroll
+        for (int j = 0; j < (E + 3) / 4; ++j) {
+            const float4 f = *reinterpret_cast<const float4 *>(w + c + 4 * j);
+            r.v[2 * j < (E + 1) / 2 ? 2 * j : 0] = make_float2(f.x, f.y);
+            r.v[2 * j + 1 < (E + 1) / 2 ? 2 * j + 1 : 0] = make_float2(f.z, f.w);
+        }
+        return r;
     }
-    // Sums about the thread's first value: what cancels is no larger than the
-    // values' own spread.
+    each_pair<E>([&](int j) {
+        const bool two = 2 * j + 1 < E;
+        r.v[j] = w ? make_float2(w[c + 2 * j], two ? w[c + 2 * j + two] : 0.0f) : both(otherwise);
+    });
+    return r;
+}
+
+// A piece as it is in memory, to be widened where it is used.  What is read for
+// the last time, and what is written, leaves the cache first: its room is for the
+// next wave.
+template <typename T, int E>
+struct Raw {
+    static constexpr int bytes = E * (int)sizeof(T);
+    using Word = std::conditional_t<bytes == 16, uint4,
+                                    std::conditional_t<bytes == 8, uint2, std::conditional_t<bytes == 4, uint32_t, uint16_t>>>;
+    Word w;
+    __device__ __forceinline__ Values<E> values() const
+    {
+        union {
+            Word w;
+            Vec<T, E> v;
+        } u{w};
+        Values<E> r;
+        float f[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = widen(u.v.e[e]);
+        each_pair<E>([&](int i) { r.v[i] = make_float2(f[2 * i], 2 * i + 1 < E ? f[2 * i + 1 < E ? 2 * i + 1 : 0] : 0.0f); });
+        return r;
+    }
+};
+template <int E, typename T>
+__device__ __forceinline__ Raw<T, E> read(const T *at)
+{
+    return Raw<T, E>{*reinterpret_cast<const typename Raw<T, E>::Word *>(at)};
+}
+template <int E, typename T>
+__device__ __forceinline__ Raw<T, E> read_last(const T *at)
+{
+    return Raw<T, E>{__ldcs(reinterpret_cast<const typename Raw<T, E>::Word *>(at))};
+}
+template <int E, typename T>
+__device__ __forceinline__ void put_last(T *at, const Values<E> &r)
+{
+    alignas(16) T out[E];
+    put<E>(out, r);
+    __stcs(reinterpret_cast<typename Raw<T, E>::Word *>(at), *reinterpret_cast<const typename Raw<T, E>::Word *>(out));
+}
+
+// Runs over a thread's pieces: `load(i, k)` four at a time, then `use(i, k)`.
+constexpr int kAhead = 4;
+template <typename L, typename U>
+__device__ __forceinline__ void over_pieces(int count, L load, U use)
+{
+    int i = 0;
+#pragma unroll 1
+    for (; i + kAhead <= count; i += kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) load(i + k, k);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) use(i + k, k);
+    }
+#pragma unroll 1
+    for (; i < count; ++i) {
+        load(i, 0);
+        use(i, 0);
+    }
+}
+
+// Forward, statistics: a chunk's moments by part.  A thread sums about its first
+// value: what cancels is no larger than the values' own spread.
+template <typename TX, int E>
+__device__ __forceinline__ void moments(const Params &p, const Part &t)
+{
+    __shared__ Moments all[kThreads];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const TX *x = static_cast<const TX *>(p.x) + (t.n * p.pixels + t.first + t.row) * p.ldx + t.c0 + t.piece * E;
+    const int64_t far = (int64_t)t.step * p.ldx;
     float2 s1 = both(0.0f), s2 = both(0.0f);
     float about = 0.0f;
-    in_halves(t.count, [&](int i) {
-        const Values<E> r = take<E, TX>(slot + i * (kSlabThreads * bytes));
-        if (i == 0) about = r.v[0].x;
-        each_pair<E>([&](int j) {
-            float2 d = add2(r.v[j], both(-about));
-            if (E == 1) d.y = 0.0f;
-            s1 = add2(s1, d);
-            s2 = fma2(d, d, s2);
+    if (t.count) about = read<E>(x).values().v[0].x;
+    Raw<TX, E> r[kAhead];
+    over_pieces(
+        t.count, [&](int i, int k) { r[k] = read<E>(x + i * far); },
+        [&](int, int k) {
+            const Values<E> v = r[k].values();
+            each_pair<E>([&](int j) {
+                float2 d = add2(v.v[j], both(-about));
+                if (E == 1) d.y = 0.0f;
+                s1 = add2(s1, d);
+                s2 = fma2(d, d, s2);
+            });
         });
-    });
-    {
-        const float n = (float)(t.count * E), sum = s1.x + s1.y, m = t.count ? sum / n : 0.0f;
-        all[threadIdx.x] = Moments{n, about + m, fmaxf((s2.x + s2.y) - sum * m, 0.0f)};
-    }
+    const float n = (float)(t.count * E), sum = s1.x + s1.y, m = t.count ? __fdividef(sum, n) : 0.0f;
+    all[threadIdx.x] = Moments{n, about + m, fmaxf((s2.x + s2.y) - sum * m, 0.0f)};
     __syncthreads();
     // a warp per group joins its threads: pieces side by side, then rows
-    const int wide = p.size / E, threads = wide * t.step;
-    for (int g = warp; g < t.groups; g += kSlabThreads / 32) {
+    const int wide = p.splits > 1 ? t.wide : p.size / E, threads = wide * t.step;
+    for (int g = warp; g < t.groups; g += kThreads / 32) {
         Moments m{0.0f, 0.0f, 0.0f};
         for (int i = lane; i < threads; i += 32) {
-            const int row = (int)((unsigned)i / (unsigned)wide);
+            const int row = p.splits > 1 ? i / wide : (int)p.by_group_wide((unsigned)i);
             m = join(m, all[row * t.wide + g * wide + (i - row * wide)]);
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1)
             m = join(m, Moments{__shfl_down_sync(0xFFFFFFFFu, m.n, d), __shfl_down_sync(0xFFFFFFFFu, m.mean, d),
                                 __shfl_down_sync(0xFFFFFFFFu, m.m2, d)});
-        if (lane == 0) found[g] = make_float2(m.mean, m.m2);
+        if (lane == 0)
+            p.by_part[parts_at(p, t.n, t.chunk) + (int64_t)(t.group + g) * p.splits + t.split] =
+                make_float2(m.mean, m.m2);
     }
-    if (p.cluster > 1)
-        cluster_barrier();
-    else
-        __syncthreads();
-    for (int g = threadIdx.x; g < t.groups; g += kSlabThreads) {
+}
+
+// Forward, results.
+template <typename TX, typename TY, int E>
+__device__ __forceinline__ void normalise(const Params &p, const Part &t)
+{
+    __shared__ float2 stats[kTileGroups];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int g = warp; g < t.groups; g += kThreads / 32) {
         Moments m{0.0f, 0.0f, 0.0f};
-        for (int r = 0; r < p.cluster; ++r) {
-            const float2 f = p.cluster > 1 ? of_rank(&found[g], r) : found[g];
-            const int64_t rows = max((int64_t)0, min((int64_t)p.rows, p.pixels - (int64_t)r * p.rows));
-            m = join(m, Moments{(float)rows * (float)p.size, f.x, f.y});
+        for (int i = lane; i < p.chunks * p.splits; i += 32) {
+            const int chunk = (int)p.by_splits((unsigned)i), split = i - chunk * p.splits;
+            const float2 f = p.by_part[parts_at(p, t.n, chunk) + (int64_t)(t.group + g) * p.splits + split];
+            m = join(m, Moments{values_of(p, chunk, split), f.x, f.y});
         }
-        const float2 f = make_float2(m.mean, 1.0f / sqrtf(m.m2 / m.n + p.eps));
-        stats[g] = f;
-        if (t.rank == 0) {
-            const int64_t at = (int64_t)t.n * p.groups + t.c0 / p.size + g;
-            p.mean[at] = f.x;
-            p.rstd[at] = f.y;
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            m = join(m, Moments{__shfl_down_sync(0xFFFFFFFFu, m.n, d), __shfl_down_sync(0xFFFFFFFFu, m.mean, d),
+                                __shfl_down_sync(0xFFFFFFFFu, m.m2, d)});
+        if (lane == 0) {
+            const float2 f = make_float2(m.mean, __frsqrt_rn(m.m2 / m.n + p.eps));
+            stats[g] = f;
+            if (t.chunk == 0 && t.split == 0) {
+                p.mean[(int64_t)t.n * p.groups + t.group + g] = f.x;
+                p.rstd[(int64_t)t.n * p.groups + t.group + g] = f.y;
+            }
         }
     }
+    const int c = t.c0 + t.piece * E;
+    Values<E> w = weights_of<E>(p, p.w, c, 1.0f), b = weights_of<E>(p, p.b, c, 0.0f);
     __syncthreads();
-    if (p.cluster > 1) cluster_has_read();
-    const float2 f = stats[mine];
-    float2 w[(E + 1) / 2], b[(E + 1) / 2];
+    const float2 f = stats[t.mine];
     each_pair<E>([&](int j) {
-        const bool two = 2 * j + 1 < E;
-        w[j] = p.w ? make_float2(p.w[c + 2 * j], two ? p.w[c + 2 * j + two] : 0.0f) : both(1.0f);
-        b[j] = p.b ? make_float2(p.b[c + 2 * j], two ? p.b[c + 2 * j + two] : 0.0f) : both(0.0f);
         // z = x (rstd w) + (b - mean rstd w): what this rounds is of the size of what the mean's rounding leaves
-        w[j] = mul2(w[j], both(f.y));
-        b[j] = fma2(w[j], both(-f.x), b[j]);
+        w.v[j] = mul2(w.v[j], both(f.y));
+        b.v[j] = fma2(w.v[j], both(-f.x), b.v[j]);
     });
+    const int64_t pixel = t.n * p.pixels + t.first + t.row;
+    const TX *x = static_cast<const TX *>(p.x) + pixel * p.ldx + c;
     TY *y = static_cast<TY *>(p.y) + pixel * p.ldy + c;
-    const int64_t far = (int64_t)t.step * p.ldy;
+    const int64_t far_x = (int64_t)t.step * p.ldx, far_y = (int64_t)t.step * p.ldy;
     with_activation(p.act, [&](auto act) {
-#pragma unroll 4
-        for (int i = 0; i < t.count; ++i) {
-            Values<E> r = take<E, TX>(slot + i * (kSlabThreads * bytes));
-            each_pair<E>([&](int j) { r.v[j] = activate2<act.value>(fma2(r.v[j], w[j], b[j])); });
-            put<E>(y + i * far, r);
-        }
+        Raw<TX, E> r[kAhead];
+        over_pieces(
+            t.count, [&](int i, int k) { r[k] = read_last<E>(x + i * far_x); },
+            [&](int i, int k) {
+                Values<E> v = r[k].values();
+                each_pair<E>([&](int j) { v.v[j] = activate2<act.value>(fma2(v.v[j], w.v[j], b.v[j])); });
+                put_last<E>(y + i * far_y, v);
+            });
     });
-    if (p.cluster > 1) cluster_leave();
 }
 
 template <typename TX, typename TY, int E>
-__global__ void __launch_bounds__(kSlabThreads, kSlabBlocks) slab_backward_kernel(const Params p)
+__global__ void __launch_bounds__(kThreads, 4) forward_kernel(const Params p)
 {
-    extern __shared__ __align__(16) uint8_t slots[];
-    __shared__ float2 sums[E][kSlabThreads], means[kSlabGroups];
-    constexpr int xb = E * (int)sizeof(TX), yb = E * (int)sizeof(TY);
-    // fp32 slots of x and dy give their places to xh and dz, so that these are computed once
-    constexpr bool kKeepY = sizeof(TY) == 4, kKeepX = kKeepY && sizeof(TX) == 4;
+    amsim::chain_start();
     const Part t = part_of<E>(p);
-    const int c = t.c0 + t.piece * E, mine = t.piece * E / p.size, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t pixel = t.n * p.pixels + t.first + t.row;
-    uint8_t *sx = slots + threadIdx.x * xb, *sy = slots + p.steps * (kSlabThreads * xb) + threadIdx.x * yb;
-    float2 *by_channel = reinterpret_cast<float2 *>(slots + p.steps * (kSlabThreads * (xb + yb)));
-    {
-        const TX *x = static_cast<const TX *>(p.x) + pixel * p.ldx + c;
-        const TY *dy = static_cast<const TY *>(p.dy) + pixel * p.ldy + c;
-        const int64_t xfar = (int64_t)t.step * p.ldx, yfar = (int64_t)t.step * p.ldy;
-        auto copy = [&](int from, int to) {
-#pragma unroll 4
-            for (int i = from; i < to; ++i) {
-                copy_in<xb>(sx + i * (kSlabThreads * xb), x + i * xfar);
-                copy_in<yb>(sy + i * (kSlabThreads * yb), dy + i * yfar);
-            }
-            copies_commit();
-        };
-        copy(0, (t.count + 1) >> 1);
-        copy((t.count + 1) >> 1, t.count);
+    if (t.stats) {
+        moments<TX, E>(p, t);
+    } else {
+        amsim::chain_wait();                 // for the wave's statistics
+        normalise<TX, TY, E>(p, t);
     }
-    const int64_t group = (int64_t)t.n * p.groups + t.c0 / p.size + mine;
-    const float mean = p.mean[group], rstd = p.rstd[group];
-    float2 w[(E + 1) / 2], b[(E + 1) / 2];
+}
+
+// What backward knows of a thread's group and channels.
+template <int E>
+struct Known {
+    float mean, rstd;
+    Values<E> w, b;
+};
+template <int E>
+__device__ __forceinline__ Known<E> known(const Params &p, const Part &t)
+{
+    Known<E> k;
+    const int c = t.c0 + t.piece * E;
+    const int64_t group = (int64_t)t.n * p.groups + t.group + t.mine;
+    k.mean = p.mean[group];
+    k.rstd = p.rstd[group];
+    k.w = weights_of<E>(p, p.w, c, 1.0f);
+    k.b = weights_of<E>(p, p.b, c, 0.0f);
+    return k;
+}
+template <int ACT, int E>
+__device__ __forceinline__ void derive(const Known<E> &k, const Values<E> &x, Values<E> &xh, Values<E> &dz)
+{
     each_pair<E>([&](int j) {
-        const bool two = 2 * j + 1 < E;
-        w[j] = p.w ? make_float2(p.w[c + 2 * j], two ? p.w[c + 2 * j + two] : 0.0f) : both(1.0f);
-        b[j] = p.b ? make_float2(p.b[c + 2 * j], two ? p.b[c + 2 * j + two] : 0.0f) : both(0.0f);
+        xh.v[j] = mul2(add2(x.v[j], both(-k.mean)), both(k.rstd));
+        dz.v[j] = before2<ACT>(dz.v[j], x.v[j], xh.v[j], k.mean, k.rstd, k.w.v[j], k.b.v[j]);
     });
-    auto values = [&](auto act, int i, Values<E> &xh, Values<E> &dz) {
-        const Values<E> x = take<E, TX>(sx + i * (kSlabThreads * xb));
-        dz = take<E, TY>(sy + i * (kSlabThreads * yb));
-        each_pair<E>([&](int j) {
-            xh.v[j] = mul2(add2(x.v[j], both(-mean)), both(rstd));
-            dz.v[j] = before2<act.value>(dz.v[j], x.v[j], xh.v[j], mean, rstd, w[j], b[j]);
-        });
-    };
+}
+
+// Backward, statistics: a chunk's sums of dz and dz xh by channel, and of these times w by part.
+template <typename TX, typename TY, int E>
+__device__ __forceinline__ void channel_sums(const Params &p, const Part &t)
+{
+    __shared__ float2 sums[E][kThreads];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = t.c0 + t.piece * E;
+    const int64_t pixel = t.n * p.pixels + t.first + t.row;
+    const TX *x = static_cast<const TX *>(p.x) + pixel * p.ldx + c;
+    const TY *dy = static_cast<const TY *>(p.dy) + pixel * p.ldy + c;
+    const int64_t far_x = (int64_t)t.step * p.ldx, far_y = (int64_t)t.step * p.ldy;
+    const Known<E> k = known<E>(p, t);
     float2 s[(E + 1) / 2], q[(E + 1) / 2];
     each_pair<E>([&](int j) { s[j] = q[j] = both(0.0f); });
     with_activation(p.act, [&](auto act) {
-        in_halves(t.count, [&](int i) {
-            Values<E> xh, dz;
-            values(act, i, xh, dz);
-            if (kKeepX) put<E>(reinterpret_cast<TX *>(sx + i * (kSlabThreads * xb)), xh);
-            if (kKeepY) put<E>(reinterpret_cast<TY *>(sy + i * (kSlabThreads * yb)), dz);
-            each_pair<E>([&](int j) {
-                s[j] = add2(s[j], dz.v[j]);
-                q[j] = fma2(dz.v[j], xh.v[j], q[j]);
+        Raw<TX, E> r[kAhead];
+        Raw<TY, E> d[kAhead];
+        over_pieces(
+            t.count,
+            [&](int i, int k) {
+                r[k] = read<E>(x + i * far_x);
+                d[k] = read<E>(dy + i * far_y);
+            },
+            [&](int, int n) {
+                Values<E> xh, dz = d[n].values();
+                derive<act.value>(k, r[n].values(), xh, dz);
+                each_pair<E>([&](int j) {
+                    s[j] = add2(s[j], dz.v[j]);
+                    q[j] = fma2(dz.v[j], xh.v[j], q[j]);
+                });
             });
-        });
     });
     // over the rows of threads, in a fixed order: where a warp holds whole rows
     // across its lanes first, then rows (or warps) across shared memory
@@ -728,7 +560,7 @@ __global__ void __launch_bounds__(kSlabThreads, kSlabBlocks) slab_backward_kerne
                 q[j] = add2(q[j], make_float2(__shfl_xor_sync(0xFFFFFFFFu, q[j].x, d),
                                               __shfl_xor_sync(0xFFFFFFFFu, q[j].y, d)));
             });
-        rows = kSlabThreads / 32;
+        rows = kThreads / 32;
         row = lane < t.wide ? warp : rows;
         apart = 32;
     }
@@ -744,71 +576,122 @@ __global__ void __launch_bounds__(kSlabThreads, kSlabBlocks) slab_backward_kerne
                 sums[e][threadIdx.x] = add2(sums[e][threadIdx.x], sums[e][threadIdx.x + half * apart]);
         rows = half;
     }
-    if (row == 0)
-#pragma unroll
-        for (int e = 0; e < E; ++e) by_channel[t.piece * E + e] = sums[e][threadIdx.x];
-    if (p.cluster > 1)
-        cluster_barrier();
-    else
-        __syncthreads();
-    // the slab's sums by channel, over its blocks in their order; the group's means from them
-    for (int g = warp; g < t.groups; g += kSlabThreads / 32) {
+    __syncthreads();
+    // channel i of the tile is now sums[i % E][i / E]
+    float2 *out = p.by_channel + ((int64_t)t.n * p.chunks + t.chunk) * p.channels + t.c0;
+    const int size = p.splits > 1 ? t.channels : p.size;
+    for (int g = warp; g < t.groups; g += kThreads / 32) {
         float2 m = both(0.0f);
-        for (int i = lane; i < p.size; i += 32) {
-            const int at = g * p.size + i;
-            float2 v = both(0.0f);
-            if (p.cluster > 1)
-                for (int r = 0; r < p.cluster; ++r) v = add2(v, of_rank(&by_channel[at], r));
-            else
-                v = by_channel[at];
-            if (t.rank == 0) p.sums[(int64_t)t.n * p.channels + t.c0 + at] = v;
-            m = fma2(v, both(p.w ? p.w[t.c0 + at] : 1.0f), m);
+        for (int i = g * size + lane; i < (g + 1) * size; i += 32) {
+            const float2 v = sums[i % E][i / E];
+            out[i] = v;
+            m = fma2(v, both(p.w ? p.w[t.c0 + i] : 1.0f), m);
         }
-        m.x = warp_sum(m.x);
-        m.y = warp_sum(m.y);
+        m = make_float2(warp_sum(m.x), warp_sum(m.y));
+        if (lane == 0) p.by_part[parts_at(p, t.n, t.chunk) + (int64_t)(t.group + g) * p.splits + t.split] = m;
+    }
+}
+
+// Backward, results: dx = dz (w rstd) - mean(t) rstd - xh (mean(t xh) rstd).
+template <typename TX, typename TY, int E>
+__device__ __forceinline__ void gradients(const Params &p, const Part &t)
+{
+    __shared__ float2 means[kTileGroups];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = t.c0 + t.piece * E;
+    const Known<E> k = known<E>(p, t);
+    amsim::chain_wait();                     // for the wave's sums
+    for (int g = warp; g < t.groups; g += kThreads / 32) {
+        float2 m = both(0.0f);
+        for (int i = lane; i < p.chunks * p.splits; i += 32) {
+            const int chunk = (int)p.by_splits((unsigned)i), split = i - chunk * p.splits;
+            m = add2(m, p.by_part[parts_at(p, t.n, chunk) + (int64_t)(t.group + g) * p.splits + split]);
+        }
+        m = make_float2(warp_sum(m.x), warp_sum(m.y));
         const float count = (float)p.size * (float)p.pixels;
         if (lane == 0) means[g] = make_float2(m.x / count, m.y / count);
     }
     __syncthreads();
-    if (p.cluster > 1) cluster_has_read();
-    // dx = dz (w rstd) - mean(t) rstd - xh (mean(t xh) rstd)
-    const float2 m = mul2(means[mine], both(-rstd));
-    each_pair<E>([&](int j) { s[j] = mul2(w[j], both(rstd)); });
+    const float2 m = mul2(means[t.mine], both(-k.rstd));
+    Values<E> scale;
+    each_pair<E>([&](int j) { scale.v[j] = mul2(k.w.v[j], both(k.rstd)); });
+    const int64_t pixel = t.n * p.pixels + t.first + t.row;
+    const TX *x = static_cast<const TX *>(p.x) + pixel * p.ldx + c;
+    const TY *dy = static_cast<const TY *>(p.dy) + pixel * p.ldy + c;
     TX *dx = static_cast<TX *>(p.dx) + pixel * p.lddx + c;
-    const int64_t far = (int64_t)t.step * p.lddx;
-    auto finish = [&](auto act) {
-#pragma unroll 4
-        for (int i = 0; i < t.count; ++i) {
-            Values<E> xh, dz;
-            if (kKeepY) {
-                xh = take<E, TX>(sx + i * (kSlabThreads * xb));
-                dz = take<E, TY>(sy + i * (kSlabThreads * yb));
-                if (!kKeepX) each_pair<E>([&](int j) { xh.v[j] = mul2(add2(xh.v[j], both(-mean)), both(rstd)); });
-            } else {
-                values(act, i, xh, dz);
-            }
-            each_pair<E>([&](int j) { dz.v[j] = fma2(xh.v[j], both(m.y), fma2(dz.v[j], s[j], both(m.x))); });
-            put<E>(dx + i * far, dz);
-        }
-    };
-    if (kKeepY)
-        finish(Act<AMSIM_ACT_NONE>{});
+    const int64_t far_x = (int64_t)t.step * p.ldx, far_y = (int64_t)t.step * p.ldy, far = (int64_t)t.step * p.lddx;
+    with_activation(p.act, [&](auto act) {
+        Raw<TX, E> r[kAhead];
+        Raw<TY, E> d[kAhead];
+        over_pieces(
+            t.count,
+            [&](int i, int n) {
+                r[n] = read_last<E>(x + i * far_x);
+                d[n] = read_last<E>(dy + i * far_y);
+            },
+            [&](int i, int n) {
+                Values<E> xh, dz = d[n].values();
+                derive<act.value>(k, r[n].values(), xh, dz);
+                each_pair<E>([&](int j) { dz.v[j] = fma2(xh.v[j], both(m.y), fma2(dz.v[j], scale.v[j], both(m.x))); });
+                put_last<E>(dx + i * far, dz);
+            });
+    });
+}
+
+template <typename TX, typename TY, int E>
+__global__ void __launch_bounds__(kThreads, E == 8 ? 2 : 3) backward_kernel(const Params p)
+{
+    amsim::chain_start();
+    const Part t = part_of<E>(p);
+    if (t.stats)
+        channel_sums<TX, TY, E>(p, t);
     else
-        with_activation(p.act, finish);
-    if (p.cluster > 1) cluster_leave();
+        gradients<TX, TY, E>(p, t);
+}
+
+// Without pixels: mean 0, rstd 1 / sqrt(eps).
+__global__ void __launch_bounds__(kThreads) empty_kernel(const Params p, int64_t n)
+{
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= n) return;
+    p.mean[i] = 0.0f;
+    p.rstd[i] = 1.0f / sqrtf(p.eps);
+}
+
+// dw and db from the sums by channel: a block takes 32 channels, its 32 warps
+// every 32nd chunk, eight loads at a time.
+__global__ void __launch_bounds__(1024) weights_kernel(const Params p)
+{
+    __shared__ float2 part[32][33];
+    amsim::chain_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = (int)blockIdx.x * 32 + lane;
+    float2 s = make_float2(0.0f, 0.0f);
+    if (c < p.channels) {
+#pragma unroll 8
+        for (int64_t n = warp; n < p.samples_chunks; n += 32) s = add2(s, p.by_channel[n * p.channels + c]);
+    }
+    part[warp][lane] = s;
+    __syncthreads();
+    s = part[lane][warp];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, d);
+        s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, d);
+    }
+    const int mine = (int)blockIdx.x * 32 + warp;
+    if (lane || mine >= p.channels) return;
+    if (p.db) p.db[mine] = s.x;
+    if (p.dw) p.dw[mine] = s.y;
 }
 
 size_t type_size(int t) { return t == AMSIM_BF16 ? 2 : 4; }
 bool aligned(const void *q, size_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; }
+bool whole(const void *q, int64_t ld, size_t size, int E) { return aligned(q, E * size) && ld % E == 0; }
 
 int check(const amsim_group_norm_desc *d)
 {
     if (!d || d->batch < 0 || d->pixels < 0 || d->channels < 1 || d->groups < 1 || d->channels % d->groups)
         return AMSIM_EINVAL;
-    // a block for each sample and tile of at least 32 channels, or group, fits a grid
-    if (d->batch > 0x7FFFFFFF || d->pixels > (int64_t)1 << 40 || d->channels > 1 << 24 ||
-        d->batch * std::max<int64_t>(d->groups, (d->channels + 31) / 32) > 0x7FFFFFFF)
-        return AMSIM_EINVAL;
+    if (d->batch > 0x7FFFFFFF || d->pixels > (int64_t)1 << 40 || d->channels > 1 << 24) return AMSIM_EINVAL;
     for (int t : {d->x_type, d->y_type})
         if (t != AMSIM_F32 && t != AMSIM_BF16) return AMSIM_EINVAL;
     for (int64_t ld : {d->ldx, d->ldy, d->lddx})
@@ -823,63 +706,10 @@ int device_sms()
     return amsim::current_device(&sms) < 0 ? 0 : sms;
 }
 
-// Elements of a thread's piece: 16 bytes of the wider type, where every row of them is on its size.
-int piece(const amsim_group_norm_desc *d)
-{
-    return d->x_type == AMSIM_BF16 && d->y_type == AMSIM_BF16 ? 8 : 4;
-}
-bool whole(const void *q, int64_t ld, size_t size, int E) { return aligned(q, E * size) && ld % E == 0; }
-
-// Chunks of pixels: about eight blocks an SM, no chunk below 64 pixels.
-void split(Params &p, int E, int sms)
-{
-    p.tx = 1;
-    while (p.tx < 32 && p.tx * E < p.channels) p.tx *= 2;
-    p.tiles = (p.channels + p.tx * E - 1) / (p.tx * E);
-    int64_t chunks = std::max<int64_t>(1, (int64_t)sms * 8 / ((int64_t)p.tiles * std::max(1, p.batch)));
-    chunks = std::min(chunks, std::max<int64_t>(1, p.pixels / 64));
-    p.chunk = std::max<int64_t>(1, (p.pixels + chunks - 1) / chunks);
-    p.chunks = (int)std::max<int64_t>(1, (p.pixels + p.chunk - 1) / p.chunk);
-}
-
-// The resident way's shape, or false.  A slab is some 128 bytes of a pixel, in
-// whole groups; its cluster has as many blocks as hold it, and more where the
-// machine is not full and threads keep four pixels.  A slab that is too large
-// for eight blocks of which an SM takes two is taken narrower, or in larger blocks.
-constexpr int kHalfSm = 96 * 1024, kWholeSm = 200 * 1024;
-constexpr int kMaxCluster = 8;
-constexpr int kSums = 8;                     // bytes of a channel's sums, backward
-// E: of a piece; bytes: of an element on chip (x; backward x and dy); chan: of a channel's sums there
-bool resident(Params &p, int E, int bytes, int chan, int sms)
-{
-    struct Try {
-        int width, room;
-    };
-    for (const Try t : {Try{128, kHalfSm}, Try{64, kHalfSm}, Try{64, kWholeSm}, Try{32, kWholeSm}}) {
-        p.slab = std::min(p.channels, std::max(1, t.width / (bytes * p.size)) * p.size);
-        if (p.slab / E > kSlabThreads || p.slab / p.size > kSlabGroups) continue;
-        p.slab_groups = p.slab / p.size;
-        p.slabs = (p.channels + p.slab - 1) / p.slab;
-        const int step = p.step = kSlabThreads / (p.slab / E), most = (t.room - p.slab * chan) / (kSlabThreads * E * bytes);
-        if (most < 1) continue;
-        const int64_t need = (p.pixels + (int64_t)step * most - 1) / ((int64_t)step * most);
-        if (need > kMaxCluster) continue;
-        const int64_t units = (int64_t)p.batch * p.slabs;
-        const int64_t fill = std::min((2 * (int64_t)sms + units - 1) / units, p.pixels / (4 * step));
-        p.cluster = (int)std::max<int64_t>(need, std::min<int64_t>(kMaxCluster, fill));
-        while (p.cluster > need && (p.cluster & (p.cluster - 1))) --p.cluster;
-        p.rows = (int)((p.pixels + p.cluster - 1) / p.cluster);
-        p.steps = (p.rows + step - 1) / step;
-        if (units * p.cluster <= 0x7FFFFFFF) return true;
-    }
-    return false;
-}
-
 Params params(const amsim_group_norm_desc *d)
 {
     Params p{};
     p.pixels = d->pixels;
-    p.batch = (int)d->batch;
     p.channels = d->channels;
     p.groups = d->groups;
     p.size = d->channels / d->groups;
@@ -891,110 +721,122 @@ Params params(const amsim_group_norm_desc *d)
     return p;
 }
 
-dim3 grid(const Params &p) { return dim3((unsigned)((int64_t)p.batch * p.tiles * p.chunks)); }
+// Channels of a piece, tiles, chunks and waves of a call.
+struct Plan {
+    int E;
+    int64_t units, wave;                     // tiles of all samples, of one wave
+};
+constexpr int kTileBytes = 256;              // of a pixel, about
+constexpr int kPieces = 16;                  // of a thread, where there are enough
+constexpr int64_t kWaveBytes = 32 << 20;     // of what is read twice
 
-int start(bool chained, void (*kernel)(Params), dim3 grid, int threads, const Params &p, cudaStream_t st)
-{
-    const int rc = amsim::cuda_status(amsim::chain_launch(chained, kernel, grid, dim3((unsigned)threads), 0, st, p));
-    if (rc == AMSIM_OK) amsim::count_launch();
-    return rc;
-}
-
-int start_slabs(void (*kernel)(Params), const Params &p, int bytes, int chan, cudaStream_t st)
-{
-    int rc = amsim::cuda_status(
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWholeSm));
-    if (!rc && p.cluster > 8)
-        rc = amsim::cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-    if (rc) return rc;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)((int64_t)p.batch * p.slabs * p.cluster));
-    c.blockDim = dim3(kSlabThreads);
-    c.dynamicSmemBytes = (size_t)p.steps * kSlabThreads * bytes + (size_t)p.slab * chan;
-    c.stream = st;
-    cudaLaunchAttribute a[1];
-    a[0].id = cudaLaunchAttributeClusterDimension;
-    a[0].val.clusterDim.x = (unsigned)p.cluster;
-    a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
-    c.attrs = a;
-    c.numAttrs = p.cluster > 1 ? 1 : 0;
-    rc = amsim::cuda_status(cudaLaunchKernelEx(&c, kernel, p));
-    if (rc == AMSIM_OK) amsim::count_launch();
-    return rc;
-}
-
-template <typename TX, typename TY, int E>
-int slab_pass(bool fwd, const Params &p, cudaStream_t st)
-{
-    if (fwd) return start_slabs(slab_forward_kernel<TX, TY, E>, p, E * (int)sizeof(TX), 0, st);
-    const int rc = start_slabs(slab_backward_kernel<TX, TY, E>, p, E * (int)(sizeof(TX) + sizeof(TY)), kSums, st);
-    if (rc || (!p.dw && !p.db)) return rc;
-    return start(true, weights_kernel, dim3((unsigned)((p.channels + 31) / 32)), 1024, p, st);
-}
-
-template <typename TX, typename TY, int E>
-int wide_pass(bool fwd, const Params &p, cudaStream_t st)
-{
-    if (fwd) {
-        if (int rc = start(false, moments_kernel<TX, E>, grid(p), kThreads, p, st)) return rc;
-        if (int rc = start(true, join_kernel, dim3((unsigned)(p.batch * p.groups)), kThreads, p, st)) return rc;
-        return start(true, apply_kernel<TX, TY, E>, grid(p), kThreads, p, st);
-    }
-    if (int rc = start(false, sums_kernel<TX, TY, E>, grid(p), kThreads, p, st)) return rc;
-    if (int rc = start(true, means_kernel, dim3((unsigned)(p.batch * p.groups)), kThreads, p, st)) return rc;
-    if (int rc = start(true, gradient_kernel<TX, TY, E>, grid(p), kThreads, p, st)) return rc;
-    if (!p.dw && !p.db) return AMSIM_OK;
-    return start(false, weights_kernel, dim3((unsigned)((p.channels + 31) / 32)), 1024, p, st);
-}
-
-template <typename TX, typename TY>
-int pass(bool fwd, int E, const Params &p, cudaStream_t st)
-{
-    constexpr int most = sizeof(TX) + sizeof(TY) == 4 ? 8 : 4;   // 16 bytes of the wider type
-    if (p.cluster)
-        return E == 4   ? slab_pass<TX, TY, 4>(fwd, p, st)
-               : E == 2 ? slab_pass<TX, TY, 2>(fwd, p, st)
-                        : slab_pass<TX, TY, 1>(fwd, p, st);
-    return E == most ? wide_pass<TX, TY, most>(fwd, p, st) : wide_pass<TX, TY, 1>(fwd, p, st);
-}
-
-// The way a call goes: slabs in pieces of up to four channels that lie within
-// one group, else whole pieces of 16 bytes, or single channels.  `fits(E)`: the
-// call's rows are on E elements.
+// `fits(E)`: the call's rows are on E elements.  false: too many blocks.
 template <typename F>
-int plan(const amsim_group_norm_desc *d, bool fwd, int sms, Params &p, F fits)
+bool plan(const amsim_group_norm_desc *d, bool fwd, int sms, Params &p, Plan *out, F fits)
 {
-    const int bytes = (int)(type_size(d->x_type) + (fwd ? 0 : type_size(d->y_type)));
-    int E = 4;
+    const int xs = (int)type_size(d->x_type), ys = (int)type_size(d->y_type), bytes = xs + (fwd ? 0 : ys);
+    int E = xs + ys == 4 ? 8 : 4;                // 16 bytes of the wider type
     while (E > 1 && (p.size % E || !fits(E))) E /= 2;
-    if (resident(p, E, bytes, fwd ? 0 : kSums, sms)) return E;
-    p.cluster = 0;
-    E = piece(d);
-    if (d->channels % E || !fits(E)) E = 1;
-    split(p, E, sms);
-    return E;
+    const int widest = std::min(kThreads * E, std::max(E, kTileBytes / std::max(xs, ys)));
+    if (p.size > widest) {                       // parts of one group, alike up to a piece
+        p.splits = (p.size + widest - 1) / widest;
+        p.tile = ((p.size / E + p.splits - 1) / p.splits) * E;
+        p.splits = (p.size + p.tile - 1) / p.tile;
+        p.tiles = p.groups * p.splits;
+    } else {
+        p.splits = 1;
+        p.tile = std::min({widest / p.size, p.groups, kTileGroups}) * p.size;
+        p.tiles = (p.channels + p.tile - 1) / p.tile;
+    }
+    if (p.splits == 1 && p.tiles * p.tile < p.channels) return false;
+    const int64_t units = d->batch * p.tiles;
+    const int step = kThreads / (p.tile / E);
+    // chunks of kPieces a thread, smaller where these do not give every SM four blocks
+    int64_t chunks = (d->pixels + (int64_t)step * kPieces - 1) / ((int64_t)step * kPieces);
+    const int64_t enough = (4 * (int64_t)sms + units - 1) / units, most = (d->pixels + 2 * step - 1) / (2 * step);
+    chunks = std::max<int64_t>(1, std::min<int64_t>(std::max(chunks, std::min(enough, most)), 1024));
+    const int64_t rows = (d->pixels + chunks - 1) / chunks;
+    if (rows > 0x7FFFFFFF - kThreads) return false;
+    p.rows = (int)rows;
+    p.chunks = (int)((d->pixels + rows - 1) / rows);
+    p.samples_chunks = d->batch * p.chunks;
+    p.step = step;
+    p.by_tiles = divisor((unsigned)p.tiles);
+    p.by_splits = divisor((unsigned)p.splits);
+    p.by_chunks = divisor((unsigned)p.chunks);
+    p.by_wide = divisor((unsigned)(p.tile / E));
+    p.by_step = divisor((unsigned)step);
+    p.by_group_wide = divisor((unsigned)std::max(1, p.size / E));
+    p.by_size = divisor((unsigned)p.size);
+    p.vec = aligned(p.w, 16) && aligned(p.b, 16);
+    // waves alike in size
+    const int64_t unit_bytes = std::max<int64_t>(1, d->pixels * p.tile * bytes);
+    const int64_t waves = std::max<int64_t>(1, units * unit_bytes / kWaveBytes);
+    *out = Plan{E, units, (units + waves - 1) / waves};
+    return 2 * out->wave * p.chunks <= 0x7FFFFFFF && units <= 0x7FFFFFFF;
 }
 
-int run(const amsim_group_norm_desc *d, bool fwd, int E, const Params &p, cudaStream_t st)
+int start(bool chained, void (*kernel)(Params), int64_t blocks, int threads, const Params &p, cudaStream_t st)
+{
+    const int rc = amsim::cuda_status(
+        amsim::chain_launch(chained, kernel, dim3((unsigned)blocks), dim3((unsigned)threads), 0, st, p));
+    if (rc == AMSIM_OK) amsim::count_launch();
+    return rc;
+}
+
+// A launch for each wave's statistics, which also has the wave before's results, and one for the last's.
+int waves(void (*kernel)(Params), Params p, const Plan &plan, cudaStream_t st)
+{
+    p.apply_units = 0;
+    for (int64_t at = 0; at < plan.units || p.stat_units; at += plan.wave) {
+        p.apply_first = p.stat_first;
+        p.apply_units = p.stat_units;
+        p.stat_first = (unsigned)at;
+        p.stat_units = (unsigned)std::max<int64_t>(0, std::min(plan.wave, plan.units - at));
+        const int64_t blocks = ((int64_t)p.stat_units + p.apply_units) * p.chunks;
+        if (const int rc = start(at > 0, kernel, blocks, kThreads, p, st)) return rc;
+    }
+    return AMSIM_OK;
+}
+
+template <typename TX, typename TY, int E>
+int pass(bool fwd, const Params &p, const Plan &plan, cudaStream_t st)
+{
+    const int rc = waves(fwd ? forward_kernel<TX, TY, E> : backward_kernel<TX, TY, E>, p, plan, st);
+    if (rc || fwd || (!p.dw && !p.db)) return rc;
+    return start(true, weights_kernel, (p.channels + 31) / 32, 1024, p, st);
+}
+template <typename TX, typename TY>
+int pass(bool fwd, const Params &p, const Plan &plan, cudaStream_t st)
+{
+    if constexpr (sizeof(TX) + sizeof(TY) == 4)
+        if (plan.E == 8) return pass<TX, TY, 8>(fwd, p, plan, st);
+    return plan.E == 4   ? pass<TX, TY, 4>(fwd, p, plan, st)
+           : plan.E == 2 ? pass<TX, TY, 2>(fwd, p, plan, st)
+                         : pass<TX, TY, 1>(fwd, p, plan, st);
+}
+int run(const amsim_group_norm_desc *d, bool fwd, const Params &p, const Plan &plan, cudaStream_t st)
 {
     using B = __nv_bfloat16;
     if (d->x_type == AMSIM_F32)
-        return d->y_type == AMSIM_F32 ? pass<float, float>(fwd, E, p, st) : pass<float, B>(fwd, E, p, st);
-    return d->y_type == AMSIM_F32 ? pass<B, float>(fwd, E, p, st) : pass<B, B>(fwd, E, p, st);
+        return d->y_type == AMSIM_F32 ? pass<float, float>(fwd, p, plan, st) : pass<float, B>(fwd, p, plan, st);
+    return d->y_type == AMSIM_F32 ? pass<B, float>(fwd, p, plan, st) : pass<B, B>(fwd, p, plan, st);
 }
+
 }  // namespace
 
 extern "C" size_t amsim_group_norm_workspace_size(const amsim_group_norm_desc *d, int which)
 {
     if (check(d) || which < 0 || which > 1 || !d->batch || !d->pixels) return 0;
     const int sms = device_sms();
-    Params p = params(d);
     size_t most = 0;
     for (int on : {1, 2, 4, 8}) {                // the calls' pointers and strides decide which
-        plan(d, !which, sms ? sms : 1, p, [&](int E) { return E <= on; });
-        if (!p.cluster) most = std::max(most, (size_t)p.batch * p.chunks * p.channels);
+        Params p = params(d);
+        Plan q;
+        if (!plan(d, !which, sms ? sms : 1, p, &q, [&](int E) { return E <= on; })) return 0;
+        most = std::max(most, (size_t)p.samples_chunks * ((size_t)p.groups * p.splits + (which ? p.channels : 0)));
     }
-    return (most + (which ? (size_t)p.batch * (p.channels + p.groups) : 0)) * sizeof(float2);
+    return most * sizeof(float2);
 }
 
 extern "C" int amsim_group_norm_fwd(const amsim_group_norm_desc *d, const void *x, const float *w, const float *b,
@@ -1008,8 +850,7 @@ extern "C" int amsim_group_norm_fwd(const amsim_group_norm_desc *d, const void *
     if (!aligned(x, xs) || !aligned(y, ys) || !aligned(ws, 8)) return AMSIM_EINVAL;
     for (const float *f : {w, b, (const float *)mean, (const float *)rstd})
         if (!aligned(f, 4)) return AMSIM_EINVAL;
-    const size_t need = d->pixels ? amsim_group_norm_workspace_size(d, 0) : 0;
-    if (need && (!ws || ws_bytes < need)) return AMSIM_EINVAL;
+    const int sms = device_sms();
     Params p = params(d);
     p.x = x;
     p.y = y;
@@ -1017,13 +858,23 @@ extern "C" int amsim_group_norm_fwd(const amsim_group_norm_desc *d, const void *
     p.b = b;
     p.mean = mean;
     p.rstd = rstd;
-    p.part = static_cast<float2 *>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int sms = device_sms();
+    if (!d->pixels) {
+        const int64_t n = d->batch * d->groups, blocks = (n + kThreads - 1) / kThreads;
+        if (blocks > 0x7FFFFFFF) return AMSIM_EINVAL;
+        empty_kernel<<<(unsigned)blocks, kThreads, 0, st>>>(p, n);
+        const int rc = amsim::cuda_status(cudaGetLastError());
+        if (rc == AMSIM_OK) amsim::count_launch();
+        return rc;
+    }
+    Plan q;
+    if (!plan(d, true, sms ? sms : 1, p, &q,
+              [&](int n) { return whole(x, p.ldx, xs, n) && whole(y, p.ldy, ys, n); }))
+        return AMSIM_EINVAL;
+    if (!ws || ws_bytes < (size_t)p.samples_chunks * p.groups * p.splits * sizeof(float2)) return AMSIM_EINVAL;
     if (!sms) return AMSIM_ECUDA;
-    if (!d->pixels) return start(false, join_kernel, dim3((unsigned)(p.batch * p.groups)), kThreads, p, st);
-    const int E = plan(d, true, sms, p, [&](int n) { return whole(x, p.ldx, xs, n) && whole(y, p.ldy, ys, n); });
-    return run(d, true, E, p, st);
+    p.by_part = static_cast<float2 *>(ws);
+    return run(d, true, p, q, st);
 }
 
 extern "C" int amsim_group_norm_bwd(const amsim_group_norm_desc *d, const void *dy, const void *x, const float *w,
@@ -1044,8 +895,8 @@ extern "C" int amsim_group_norm_bwd(const amsim_group_norm_desc *d, const void *
             }
         return AMSIM_OK;
     }
-    if (!x || !dy || !dx || !mean || !rstd || !ws || ws_bytes < amsim_group_norm_workspace_size(d, 1))
-        return AMSIM_EINVAL;
+    if (!x || !dy || !dx || !mean || !rstd) return AMSIM_EINVAL;
+    const int sms = device_sms();
     Params p = params(d);
     p.x = x;
     p.dy = dy;
@@ -1056,13 +907,15 @@ extern "C" int amsim_group_norm_bwd(const amsim_group_norm_desc *d, const void *
     p.rstd = const_cast<float *>(rstd);
     p.dw = dw;
     p.db = db;
-    const int sms = device_sms();
+    Plan q;
+    if (!plan(d, false, sms ? sms : 1, p, &q, [&](int n) {
+            return whole(x, p.ldx, xs, n) && whole(dx, p.lddx, xs, n) && whole(dy, p.ldy, ys, n);
+        }))
+        return AMSIM_EINVAL;
+    const size_t parts = (size_t)p.samples_chunks * p.groups * p.splits;
+    if (!ws || ws_bytes < (parts + (size_t)p.samples_chunks * p.channels) * sizeof(float2)) return AMSIM_EINVAL;
     if (!sms) return AMSIM_ECUDA;
-    const int E = plan(d, false, sms, p, [&](int n) {
-        return whole(x, p.ldx, xs, n) && whole(dx, p.lddx, xs, n) && whole(dy, p.ldy, ys, n);
-    });
-    p.sums = static_cast<float2 *>(ws);
-    p.means = p.sums + (size_t)p.batch * p.channels;
-    p.part = p.means + (size_t)p.batch * p.groups;
-    return run(d, false, E, p, st);
+    p.by_part = static_cast<float2 *>(ws);
+    p.by_channel = p.by_part + parts;
+    return run(d, false, p, q, st);
 }
