@@ -19,6 +19,7 @@
 // added in a fixed order, then by bucket.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "chained.cuh"
 #include "pairs.cuh"
@@ -79,16 +80,16 @@ __device__ __forceinline__ int column(int chunk, int lane, int k)
 
 // A chunk as it is loaded: nothing waits for it here, so that a row's loads are
 // all under way before the first is used.  Pieces that begin at a visible key are whole.
-template <bool VEC>
+template <bool VEC, bool FULL = false>
 __device__ __forceinline__ Four load_chunk(const float *row, int chunk, int lane, int visible, float fill)
 {
     Four v = four(fill);
     const int c = column<VEC>(chunk, lane, 0);
     if (VEC) {
         float4 f = make_float4(fill, fill, fill, fill);
-        if (c < visible) f = *reinterpret_cast<const float4 *>(row + c);
+        if (FULL || c < visible) f = *reinterpret_cast<const float4 *>(row + c);
         v = Four{make_float2(f.x, f.y), make_float2(f.z, f.w)};
-    } else if ((chunk + 1) * 128 <= visible) {
+    } else if (FULL || (chunk + 1) * 128 <= visible) {
         each(v, [&](float &x, int k) { x = row[c + 32 * k]; });
     } else {
         each(v, [&](float &x, int k) { if (c + 32 * k < visible) x = row[c + 32 * k]; });
@@ -96,25 +97,25 @@ __device__ __forceinline__ Four load_chunk(const float *row, int chunk, int lane
     return v;
 }
 // `fill` behind the last visible key of a whole piece.
-template <bool VEC>
+template <bool VEC, bool FULL = false>
 __device__ __forceinline__ void fill_chunk(Four &v, int chunk, int lane, int visible, float fill)
 {
-    if (VEC && (chunk + 1) * 128 > visible)
+    if (VEC && !FULL && (chunk + 1) * 128 > visible)
         each(v, [&](float &x, int k) { if (column<VEC>(chunk, lane, k) >= visible) x = fill; });
 }
 // Zeros where no key is visible.
-template <bool VEC>
+template <bool VEC, bool FULL = false>
 __device__ __forceinline__ void hide(Four &v, int chunk, int lane, int visible)
 {
-    if ((chunk + 1) * 128 > visible) each(v, [&](float &x, int k) { if (column<VEC>(chunk, lane, k) >= visible) x = 0.0f; });
+    if (!FULL && (chunk + 1) * 128 > visible) each(v, [&](float &x, int k) { if (column<VEC>(chunk, lane, k) >= visible) x = 0.0f; });
 }
-template <bool VEC>
+template <bool VEC, bool FULL = false>
 __device__ __forceinline__ void store_chunk(float *row, int chunk, int lane, int keys, Four v)
 {
     const int c = column<VEC>(chunk, lane, 0);
     if (VEC) {
-        if (c < keys) *reinterpret_cast<float4 *>(row + c) = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
-    } else if ((chunk + 1) * 128 <= keys) {
+        if (FULL || c < keys) *reinterpret_cast<float4 *>(row + c) = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
+    } else if (FULL || (chunk + 1) * 128 <= keys) {
         each(v, [&](float &x, int k) { row[c + 32 * k] = x; });
     } else {
         each(v, [&](float &x, int k) { if (c + 32 * k < keys) row[c + 32 * k] = x; });
@@ -367,20 +368,13 @@ __device__ __forceinline__ Part part_of(const Params &p)
     return t;
 }
 
-// NV > 0: a warp's part of the row is NV chunks, kept in registers; NV == 0: a
-// row of any length, read twice.
-template <int NV, bool VEC, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(const Params p)
+// The rows of a block.  NV > 0: a warp's part of the row is NV chunks, kept in
+// registers; NV == 0: a row of any length, read twice.
+template <int NV, bool VEC, bool BLOCK, bool BIAS, bool DROP>
+__device__ __forceinline__ void forward_rows(const Params &p, const Part &t, const float *bias, Exchange &exchange)
 {
-    extern __shared__ __align__(16) float bias[];
-    __shared__ Exchange exchange;
-    const Part t = part_of<BLOCK>(p);
     const int lane = threadIdx.x & 31;
-    if (p.table) {
-        load_bias(p, t.head, bias);
-        __syncthreads();
-    }
-    const uint64_t call = amsim::drop_call(p.drop);
+    const uint64_t call = DROP ? amsim::drop_call(p.drop) : 0;
     int turn = 0;
     Place at = first_place(p, t.share);
     for (int g = t.share; g < p.groups; g += p.shares, turn ^= 1, advance(p, at)) {
@@ -389,49 +383,70 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(
         const float *in = p.scores + w.row * p.ld_in;
         float *out = p.out + w.row * p.ld_out;
         RowDraws draws{};
-        if (p.drop.border) draws = row_draws(w.row, p, call);
-        auto logits = [&](Four a, int chunk) {
-            fill_chunk<VEC>(a, chunk, lane, w.visible, -INFINITY);
-            if (p.table && chunk * 128 < w.visible) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
+        if (DROP) draws = row_draws(w.row, p, call);
+        auto logits = [&](auto full, Four a, int chunk) {
+            constexpr bool FULL = decltype(full)::value;
+            fill_chunk<VEC, FULL>(a, chunk, lane, w.visible, -INFINITY);
+            if (BIAS && (FULL || chunk * 128 < w.visible)) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
             return a;
         };
-        auto finish = [&](Four e, int chunk, float factor) {
-            if (chunk * 128 >= w.visible)
+        auto finish = [&](auto full, Four e, int chunk, float factor) {
+            constexpr bool FULL = decltype(full)::value;
+            if (!FULL && chunk * 128 >= w.visible)
                 e = four(0.0f);
-            else if (p.drop.border)
+            else if (DROP)
                 drop_chunk<VEC>(e, draws, chunk, lane, p, call, factor * p.drop.scale);
             else
                 e = mul(e, four(factor));
-            hide<VEC>(e, chunk, lane, w.visible);
-            store_chunk<VEC>(out, chunk, lane, p.keys, e);
+            hide<VEC, FULL>(e, chunk, lane, w.visible);
+            store_chunk<VEC, FULL>(out, chunk, lane, p.keys, e);
         };
         float mine = -INFINITY, total = 0.0f;
         float2 joined;
         if (NV) {
             Four a[NV ? NV : 1];
+            // `full`: every key of this warp's chunks is visible, and nothing has to be checked
+            auto begin = [&](auto full) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                a[v] = load_chunk<VEC>(in, t.first_chunk + v * t.step, lane, w.visible, -INFINITY);
+                for (int v = 0; v < NV; ++v)
+                    a[v] = load_chunk<VEC, decltype(full)::value>(in, t.first_chunk + v * t.step, lane, w.visible, -INFINITY);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) a[v] = logits(a[v], t.first_chunk + v * t.step);
+                for (int v = 0; v < NV; ++v) a[v] = logits(full, a[v], t.first_chunk + v * t.step);
+            };
+            const bool all = (t.first_chunk + (NV - 1) * t.step + 1) * 128 <= w.visible;
+            if (all)
+                begin(std::true_type{});
+            else
+                begin(std::false_type{});
 #pragma unroll
             for (int v = 0; v < NV; ++v)
                 mine = fmaxf(fmaxf(mine, fmaxf(a[v].a.x, a[v].a.y)), fmaxf(a[v].b.x, a[v].b.y));
             mine = warp_max(mine);
             const float base = finite_base(mine);
+            Four sums = four(0.0f);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 a[v] = exponentials(a[v], base);
-                total += sum(a[v]);
+                sums = add(sums, a[v]);
             }
-            total = warp_sum(total);
+            total = warp_sum(sum(sums));
             joined = join_rows<BLOCK>(p, mine, total, exchange, turn);
             const float factor = BLOCK ? joined.y * part_factor(mine, joined.x) : joined.y;
+            auto end = [&](auto full) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) finish(a[v], t.first_chunk + v * t.step, factor);
+                for (int v = 0; v < NV; ++v) finish(full, a[v], t.first_chunk + v * t.step, factor);
+            };
+            if (all)
+                end(std::true_type{});
+            else
+                end(std::false_type{});
         } else {
+            std::false_type some;
+            auto logits_of = [&](int chunk) {
+                return logits(some, load_chunk<VEC>(in, chunk, lane, w.visible, -INFINITY), chunk);
+            };
             for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += t.step) {
-                const Four a = logits(load_chunk<VEC>(in, chunk, lane, w.visible, -INFINITY), chunk);
+                const Four a = logits_of(chunk);
                 const float most = fmaxf(fmaxf(a.a.x, a.a.y), fmaxf(a.b.x, a.b.y));
                 if (most > mine) {
                     total *= part_factor(mine, most);
@@ -444,11 +459,30 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(
             joined = join_rows<BLOCK>(p, top, total, exchange, turn);
             const float base = finite_base(joined.x);
             for (int chunk = t.first_chunk; chunk < p.chunks; chunk += t.step)
-                finish(exponentials(logits(load_chunk<VEC>(in, chunk, lane, w.visible, -INFINITY), chunk), base), chunk,
-                       joined.y);
+                finish(some, exponentials(logits_of(chunk), base), chunk, joined.y);
         }
         if (p.out_stats && lane == 0 && (!BLOCK || (threadIdx.x == 0 && t.rank == 0)))
             *reinterpret_cast<float2 *>(p.out_stats + 2 * w.row) = joined;
+    }
+}
+
+template <int NV, bool VEC, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kWarpRows) forward_kernel(const Params p)
+{
+    extern __shared__ __align__(16) float bias[];
+    __shared__ Exchange exchange;
+    const Part t = part_of<BLOCK>(p);
+    if (p.table) {
+        load_bias(p, t.head, bias);
+        __syncthreads();
+        if (p.drop.border)
+            forward_rows<NV, VEC, BLOCK, true, true>(p, t, bias, exchange);
+        else
+            forward_rows<NV, VEC, BLOCK, true, false>(p, t, bias, exchange);
+    } else if (p.drop.border) {
+        forward_rows<NV, VEC, BLOCK, false, true>(p, t, bias, exchange);
+    } else {
+        forward_rows<NV, VEC, BLOCK, false, false>(p, t, bias, exchange);
     }
     if (BLOCK && p.cluster > 1) cluster_barrier();       // no block leaves while another reads from it
 }
@@ -618,27 +652,52 @@ __global__ void __launch_bounds__(!BLOCK ? 32 * kWarpRows : NV == 4 ? kFewThread
     by_bucket(p, t.head, total);
 }
 
-// dtable from the blocks' sums by distance: a block per head.
+// dtable from the blocks' sums by distance: a block per head and bucket, whose
+// threads go through the bucket's distances in every block's sums.
 constexpr int kTableThreads = 1024;
 __global__ void __launch_bounds__(kTableThreads) table_kernel(const Params p)
 {
-    extern __shared__ __align__(16) float shared[];
-    amsim::chain_wait();
-    const int n = 2 * p.D + 1, blocks = p.shares * p.cluster;
-    const float *part = p.part + (int64_t)blockIdx.x * blocks * n;
-    // as many threads for an entry as there are, each every parts-th block, sixteen loads at a time
-    const int parts = max(1, min(kTableThreads / n, blocks / 16)), mine = (int)threadIdx.x / n;
-    for (int i = (int)threadIdx.x - mine * n; mine < parts && i < n; i += kTableThreads) {
-        float s = 0.0f;
-#pragma unroll 16
-        for (int t = mine; t < blocks; t += parts) s += part[(int64_t)t * n + i];
-        shared[mine * n + i] = s;
+    extern __shared__ __align__(16) int list[];          // the bucket's distances
+    __shared__ int count;
+    __shared__ float sums[32];
+    const int n = 2 * p.D + 1, blocks = p.shares * p.cluster, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int head = (int)(blockIdx.x / (unsigned)p.num_buckets), k = (int)blockIdx.x - head * p.num_buckets;
+    if (warp == 0) {
+        int found = 0;
+#pragma unroll 4
+        for (int i = lane; i < n + lane; i += 32) {
+            const bool mine = i < n && p.buckets[min(i, n - 1)] == k;
+            const unsigned all = __ballot_sync(kAll, mine);
+            if (mine) list[found + __popc(all & ((1u << lane) - 1))] = i;
+            found += __popc(all);
+        }
+        if (lane == 0) count = found;
     }
+    amsim::chain_wait();
     __syncthreads();
-    for (int i = threadIdx.x; parts > 1 && i < n; i += kTableThreads)
-        for (int q = 1; q < parts; ++q) shared[i] += shared[q * n + i];
+    const int each = count;
+    const int64_t pairs = (int64_t)each * blocks;
+    const float *part = p.part + (int64_t)head * blocks * n;
+    // pair i is distance i % each of block i / each
+    int t = each ? (int)threadIdx.x / each : 0, j = each ? (int)threadIdx.x % each : 0;
+    const int dt = each ? kTableThreads / each : 0, dj = each ? kTableThreads % each : 0;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < pairs; i += kTableThreads) {
+        s += part[(int64_t)t * n + list[j]];
+        t += dt;
+        j += dj;
+        if (j >= each) {
+            j -= each;
+            ++t;
+        }
+    }
+    s = warp_sum(s);
+    if (lane == 0) sums[warp] = s;
     __syncthreads();
-    by_bucket(p, (int)blockIdx.x, shared);
+    if (warp) return;
+    s = warp_sum(sums[lane]);
+    if (lane == 0) p.dtable[(int64_t)k * p.heads + head] = s;
 }
 
 bool aligned(const void *q, size_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; }
@@ -802,6 +861,7 @@ void fill(Params &p, const amsim_attention_softmax_desc *d, const Shape &s, int 
 int check_bias(const amsim_attention_softmax_desc *d, Params &p)
 {
     if (!aligned(p.table, 4) || !aligned(p.buckets, 4) || d->num_buckets < 1) return AMSIM_EINVAL;
+    if ((int64_t)d->num_buckets * d->heads > 0x7FFFFFFF) return AMSIM_EINVAL;
     if (d->max_distance > AMSIM_MAX_DISTANCE) return AMSIM_EUNSUPPORTED;
     p.num_buckets = d->num_buckets;
     p.D = d->max_distance;
@@ -912,8 +972,8 @@ extern "C" int amsim_attention_softmax_bwd(const amsim_attention_softmax_desc *d
     p.ld_out = stride(d->ld_dscores, d->keys);
     rc = launch(kernel, p, s, bytes, st);
     if (rc || !dtable || p.shares * p.cluster == 1) return rc;
-    rc = amsim::cuda_status(amsim::chain_launch(true, table_kernel, dim3((unsigned)p.heads), kTableThreads,
-                                                4 * std::max(kTableThreads, 2 * p.D + 1), st, p));
+    rc = amsim::cuda_status(amsim::chain_launch(true, table_kernel, dim3((unsigned)(p.heads * p.num_buckets)),
+                                                kTableThreads, 4 * (2 * p.D + 1), st, p));
     if (rc == AMSIM_OK) amsim::count_launch();
     return rc;
 }
