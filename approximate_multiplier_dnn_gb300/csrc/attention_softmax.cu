@@ -500,8 +500,148 @@ __device__ __forceinline__ void by_bucket(const Params &p, int head, const float
     }
 }
 
+// The sums by distance of a block: arrays in shared memory, and what lies further away.
+struct Distances {
+    float *diagonals;
+    int size, shift;
+    float2 before, behind;                   // columns at distances up to -D, from D on
+};
+
+// The rows of a block.  PROBS: the probabilities are given; else they come from
+// the scores and statistics, DROP with the forward pass's mask.
+template <int NV, bool VEC, bool BLOCK, bool PROBS, bool DROP>
+__device__ __forceinline__ void backward_rows(const Params &p, const Part &t, const float *bias, Distances &d,
+                                              Exchange &exchange)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint64_t call = DROP ? amsim::drop_call(p.drop) : 0;
+    constexpr float kHidden = PROBS ? 0.0f : -INFINITY;
+    int turn = 0;
+    Place at = first_place(p, t.share);
+    for (int g = t.share; g < p.groups; g += p.shares, turn ^= 1, advance(p, at)) {
+        const Row w = row_of<BLOCK>(p, t.head, at.b, at.i);
+        if (!BLOCK && !w.on) continue;
+        const float *in = (PROBS ? p.probs : p.scores) + w.row * p.ld_in, *up = p.dprobs + w.row * p.ld_g;
+        float *out = p.out + w.row * p.ld_out;
+        float base = 0.0f, inv = 1.0f;
+        if (!PROBS) {
+            const float2 f = *reinterpret_cast<const float2 *>(p.stats + 2 * w.row);
+            base = finite_base(f.x);
+            inv = f.y;
+        }
+        const int origin = p.D + 4 - w.pos;              // entry of column 0
+        RowDraws draws{};
+        if (DROP) draws = row_draws(w.row, p, call);
+        auto values = [&](auto full, int chunk, Four &a, Four &g) {
+            constexpr bool FULL = decltype(full)::value;
+            fill_chunk<VEC, FULL>(a, chunk, lane, w.visible, kHidden);
+            fill_chunk<VEC, FULL>(g, chunk, lane, w.visible, 0.0f);
+            if (PROBS || (!FULL && chunk * 128 >= w.visible)) return;
+            if (p.table) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
+            a = mul(exponentials(a, base), four(inv));
+            hide<VEC, FULL>(a, chunk, lane, w.visible);
+            if (DROP) drop_chunk<VEC>(g, draws, chunk, lane, p, call, p.drop.scale);
+        };
+        auto finish = [&](auto full, int chunk, float dot, Four a, const Four &g) {
+            constexpr bool FULL = decltype(full)::value;
+            const bool seen = FULL || chunk * 128 < w.visible;
+            a = seen ? mul(a, add(g, four(-dot))) : four(0.0f);
+            hide<VEC, FULL>(a, chunk, lane, w.visible);
+            if (p.dtable && seen) {
+                const int first = column<VEC>(chunk, lane, 0) + origin;
+                if (VEC) {
+                    if ((unsigned)first <= (unsigned)(2 * p.D + 5)) {
+                        const int k = first & 3;
+                        float4 *to = reinterpret_cast<float4 *>(BLOCK ? d.diagonals + k * d.size + (first - k)
+                                                                      : d.diagonals + warp * d.size + (first + d.shift));
+                        const float4 s = *to;
+                        const Four v = add(a, Four{make_float2(s.x, s.y), make_float2(s.z, s.w)});
+                        *to = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
+                    } else if (first < 0) {
+                        d.before = add2(d.before, add2(a.a, a.b));
+                    } else {
+                        d.behind = add2(d.behind, add2(a.a, a.b));
+                    }
+                } else {
+                    const int low = chunk * 128 + origin;        // the chunk's first entry
+                    if (low + 127 < 0) {                         // all of it far away
+                        d.before = add2(d.before, add2(a.a, a.b));
+                    } else if (low > 2 * p.D + 8) {
+                        d.behind = add2(d.behind, add2(a.a, a.b));
+                    } else {
+                        float *to = d.diagonals + (BLOCK ? 0 : warp * d.size);
+                        each(a, [&](float &x, int k) {
+                            const int i = first + 32 * k;
+                            if ((unsigned)i <= (unsigned)(2 * p.D + 8))
+                                to[i] += x;
+                            else if (i < 0)
+                                d.before.x += x;
+                            else
+                                d.behind.x += x;
+                        });
+                    }
+                }
+            }
+            store_chunk<VEC, FULL>(out, chunk, lane, p.keys, a);
+        };
+        Four part = four(0.0f);
+        if (NV) {
+            Four a[NV ? NV : 1], g[NV ? NV : 1];
+            // `full`: every key of this warp's chunks is visible, and nothing has to be checked
+            auto begin = [&](auto full) {
+                constexpr bool FULL = decltype(full)::value;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int chunk = t.first_chunk + v * t.step;
+                    a[v] = load_chunk<VEC, FULL>(in, chunk, lane, w.visible, kHidden);
+                    g[v] = load_chunk<VEC, FULL>(up, chunk, lane, w.visible, 0.0f);
+                }
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int chunk = t.first_chunk + v * t.step;
+                    values(full, chunk, a[v], g[v]);
+                    if (FULL || chunk * 128 < w.visible)
+                        part = Four{fma2(a[v].a, g[v].a, part.a), fma2(a[v].b, g[v].b, part.b)};
+                }
+            };
+            const bool all = (t.first_chunk + (NV - 1) * t.step + 1) * 128 <= w.visible;
+            if (all)
+                begin(std::true_type{});
+            else
+                begin(std::false_type{});
+            const float dot = join_sums<BLOCK>(p, warp_sum(sum(part)), exchange, turn);
+            auto end = [&](auto full) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) finish(full, t.first_chunk + v * t.step, dot, a[v], g[v]);
+            };
+            if (all)
+                end(std::true_type{});
+            else
+                end(std::false_type{});
+        } else {
+            std::false_type some;
+            auto both_of = [&](int chunk, Four &a, Four &g) {
+                a = load_chunk<VEC>(in, chunk, lane, w.visible, kHidden);
+                g = load_chunk<VEC>(up, chunk, lane, w.visible, 0.0f);
+                values(some, chunk, a, g);
+            };
+            Four a, g;
+            for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += t.step) {
+                both_of(chunk, a, g);
+                part = Four{fma2(a.a, g.a, part.a), fma2(a.b, g.b, part.b)};
+            }
+            const float dot = join_sums<BLOCK>(p, warp_sum(sum(part)), exchange, turn);
+            for (int chunk = t.first_chunk; chunk < p.chunks; chunk += t.step) {
+                both_of(chunk, a, g);
+                finish(some, chunk, dot, a, g);
+            }
+        }
+        if (!BLOCK) __syncwarp();            // other lanes add to the same distances for the next row
+    }
+}
+
 template <int NV, bool VEC, bool BLOCK>
-__global__ void __launch_bounds__(!BLOCK ? 32 * kWarpRows : NV == 4 ? kFewThreads : 1024) backward_kernel(const Params p)
+__global__ void __launch_bounds__(!BLOCK ? 32 * kWarpRows : NV == 4 ? kFewThreads : 1024, BLOCK ? 1 : 3) backward_kernel(const Params p)
 {
     extern __shared__ __align__(16) float shared[];
     __shared__ Exchange exchange;
@@ -516,109 +656,17 @@ __global__ void __launch_bounds__(!BLOCK ? 32 * kWarpRows : NV == 4 ? kFewThread
         for (int i = threadIdx.x; i < arrays * size; i += blockDim.x) diagonals[i] = 0.0f;
     if (p.table) load_bias(p, t.head, bias);
     __syncthreads();
-    const uint64_t call = amsim::drop_call(p.drop);
-    float2 before = both(0.0f), behind = both(0.0f);     // columns at distances up to -D, from D on
-    const int shift = VEC && !BLOCK ? (warp - p.D) & 3 : 0;
-    int turn = 0;
-    Place at = first_place(p, t.share);
-    for (int g = t.share; g < p.groups; g += p.shares, turn ^= 1, advance(p, at)) {
-        const Row w = row_of<BLOCK>(p, t.head, at.b, at.i);
-        if (!BLOCK && !w.on) continue;
-        const float *in = (p.probs ? p.probs : p.scores) + w.row * p.ld_in, *up = p.dprobs + w.row * p.ld_g;
-        float *out = p.out + w.row * p.ld_out;
-        float base = 0.0f, inv = 1.0f;
-        if (!p.probs) {
-            const float2 f = *reinterpret_cast<const float2 *>(p.stats + 2 * w.row);
-            base = finite_base(f.x);
-            inv = f.y;
-        }
-        const int origin = p.D + 4 - w.pos;              // entry of column 0
-        RowDraws draws{};
-        if (p.drop.border) draws = row_draws(w.row, p, call);
-        auto values = [&](int chunk, Four &a, Four &d) {
-            fill_chunk<VEC>(a, chunk, lane, w.visible, p.probs ? 0.0f : -INFINITY);
-            fill_chunk<VEC>(d, chunk, lane, w.visible, 0.0f);
-            if (p.probs || chunk * 128 >= w.visible) return;
-            if (p.table) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
-            a = mul(exponentials(a, base), four(inv));
-            hide<VEC>(a, chunk, lane, w.visible);
-            if (p.drop.border) drop_chunk<VEC>(d, draws, chunk, lane, p, call, p.drop.scale);
-        };
-        auto finish = [&](int chunk, float dot, Four a, const Four &d) {
-            a = chunk * 128 < w.visible ? mul(a, add(d, four(-dot))) : four(0.0f);
-            hide<VEC>(a, chunk, lane, w.visible);
-            if (p.dtable && chunk * 128 < w.visible) {
-                const int first = column<VEC>(chunk, lane, 0) + origin;
-                if (VEC) {
-                    if ((unsigned)first <= (unsigned)(2 * p.D + 5)) {
-                        const int k = first & 3;
-                        float4 *to = reinterpret_cast<float4 *>(BLOCK ? diagonals + k * size + (first - k)
-                                                                      : diagonals + warp * size + (first + shift));
-                        const float4 s = *to;
-                        const Four v = add(a, Four{make_float2(s.x, s.y), make_float2(s.z, s.w)});
-                        *to = make_float4(v.a.x, v.a.y, v.b.x, v.b.y);
-                    } else if (first < 0) {
-                        before = add2(before, add2(a.a, a.b));
-                    } else {
-                        behind = add2(behind, add2(a.a, a.b));
-                    }
-                } else {
-                    float *to = diagonals + (BLOCK ? 0 : warp * size);
-                    each(a, [&](float &x, int k) {
-                        const int i = first + 32 * k;
-                        if ((unsigned)i <= (unsigned)(2 * p.D + 8))
-                            to[i] += x;
-                        else if (i < 0)
-                            before.x += x;
-                        else
-                            behind.x += x;
-                    });
-                }
-            }
-            store_chunk<VEC>(out, chunk, lane, p.keys, a);
-        };
-        Four part = four(0.0f);
-        if (NV) {
-            Four a[NV ? NV : 1], d[NV ? NV : 1];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int chunk = t.first_chunk + v * t.step;
-                a[v] = load_chunk<VEC>(in, chunk, lane, w.visible, p.probs ? 0.0f : -INFINITY);
-                d[v] = load_chunk<VEC>(up, chunk, lane, w.visible, 0.0f);
-            }
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int chunk = t.first_chunk + v * t.step;
-                values(chunk, a[v], d[v]);
-                if (chunk * 128 < w.visible)
-                    part = Four{fma2(a[v].a, d[v].a, part.a), fma2(a[v].b, d[v].b, part.b)};
-            }
-            const float dot = join_sums<BLOCK>(p, warp_sum(sum(part)), exchange, turn);
-#pragma unroll
-            for (int v = 0; v < NV; ++v) finish(t.first_chunk + v * t.step, dot, a[v], d[v]);
-        } else {
-            auto both_of = [&](int chunk, Four &a, Four &d) {
-                a = load_chunk<VEC>(in, chunk, lane, w.visible, p.probs ? 0.0f : -INFINITY);
-                d = load_chunk<VEC>(up, chunk, lane, w.visible, 0.0f);
-                values(chunk, a, d);
-            };
-            Four a, d;
-            for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += t.step) {
-                both_of(chunk, a, d);
-                part = Four{fma2(a.a, d.a, part.a), fma2(a.b, d.b, part.b)};
-            }
-            const float dot = join_sums<BLOCK>(p, warp_sum(sum(part)), exchange, turn);
-            for (int chunk = t.first_chunk; chunk < p.chunks; chunk += t.step) {
-                both_of(chunk, a, d);
-                finish(chunk, dot, a, d);
-            }
-        }
-        if (!BLOCK) __syncwarp();            // other lanes add to the same distances for the next row
-    }
+    Distances d{diagonals, size, VEC && !BLOCK ? (warp - p.D) & 3 : 0, both(0.0f), both(0.0f)};
+    if (p.probs)
+        backward_rows<NV, VEC, BLOCK, true, false>(p, t, bias, d, exchange);
+    else if (p.drop.border)
+        backward_rows<NV, VEC, BLOCK, false, true>(p, t, bias, d, exchange);
+    else
+        backward_rows<NV, VEC, BLOCK, false, false>(p, t, bias, d, exchange);
     if (BLOCK && p.cluster > 1) cluster_barrier();       // no block leaves while another reads from it
     if (!p.dtable) return;
     amsim::chain_start();
-    const float low = warp_sum(before.x + before.y), high = warp_sum(behind.x + behind.y);
+    const float low = warp_sum(d.before.x + d.before.y), high = warp_sum(d.behind.x + d.behind.y);
     if (lane == 0) {
         ends[0][warp] = low;
         ends[1][warp] = high;
