@@ -56,6 +56,7 @@ struct Params {
     // A tile is some channels of a sample: whole groups, or (splits > 1) a part of one.
     int tile, tiles, splits, chunks, rows;   // tile: channels; rows: pixels of a chunk
     int step, vec;                           // pixels of a block at once; w and b on 16 bytes
+    int whole;                               // a block has all of its tile's pixels, and does both parts
     Divisor by_tiles, by_splits, by_chunks, by_wide, by_step, by_group_wide, by_size;
     unsigned stat_units, stat_first, apply_units, apply_first;   // units (sample, tile) of a launch's two roles
 };
@@ -143,6 +144,13 @@ __device__ __forceinline__ void with_activation(int act, F use)
         use(Act<AMSIM_ACT_NONE>{});
 }
 
+// Whether z > 0, in 64 bits.  Not inlined: the few calls that need it branch to
+// it, and no other pays for 64-bit arithmetic, which this machine does slowly.
+__device__ __noinline__ bool above_zero(float x, float mean, float rstd, float w, float b)
+{
+    return ((double)x - (double)mean) * (double)rstd * (double)w + (double)b > 0.0;
+}
+
 // dy act'(z).  relu's gradient jumps where z = 0: a z that its own roundings
 // (three of xh w, one of the sum: at most 2^-22 of the terms) could carry
 // across is computed again in 64 bits.
@@ -153,8 +161,7 @@ __device__ __forceinline__ float before_activation(float dy, float x, float xh, 
     const float z = fmaf(xh, w, b);
     if (ACT == AMSIM_ACT_RELU) {
         bool on = z > 0.0f;
-        if (fabsf(z) <= 0x1p-21f * (fabsf(xh * w) + fabsf(b)))
-            on = ((double)x - (double)mean) * (double)rstd * (double)w + (double)b > 0.0;
+        if (fabsf(z) <= 0x1p-21f * (fabsf(xh * w) + fabsf(b))) on = above_zero(x, mean, rstd, w, b);
         return on ? dy : 0.0f;
     }
     const float s = sigmoid(z);
@@ -478,12 +485,17 @@ __device__ __forceinline__ void normalise(const Params &p, const Part &t)
     });
 }
 
-template <typename TX, typename TY, int E>
-__global__ void __launch_bounds__(kThreads, 4) forward_kernel(const Params p)
+// WHOLE: a block has all of its tile's pixels, and does both parts.
+template <typename TX, typename TY, int E, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, WHOLE ? 3 : 4) forward_kernel(const Params p)
 {
     amsim::chain_start();
     const Part t = part_of<E>(p);
-    if (t.stats) {
+    if (WHOLE) {
+        moments<TX, E>(p, t);
+        __syncthreads();
+        normalise<TX, TY, E>(p, t);
+    } else if (t.stats) {
         moments<TX, E>(p, t);
     } else {
         amsim::chain_wait();                 // for the wave's statistics
@@ -593,13 +605,13 @@ __device__ __forceinline__ void channel_sums(const Params &p, const Part &t)
 }
 
 // Backward, results: dx = dz (w rstd) - mean(t) rstd - xh (mean(t xh) rstd).
-template <typename TX, typename TY, int E>
+template <typename TX, typename TY, int E, bool WHOLE>
 __device__ __forceinline__ void gradients(const Params &p, const Part &t)
 {
     __shared__ float2 means[kTileGroups];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = t.c0 + t.piece * E;
     const Known<E> k = known<E>(p, t);
-    amsim::chain_wait();                     // for the wave's sums
+    if (!WHOLE) amsim::chain_wait();         // for the wave's sums
     for (int g = warp; g < t.groups; g += kThreads / 32) {
         float2 m = both(0.0f);
         for (int i = lane; i < p.chunks * p.splits; i += 32) {
@@ -637,15 +649,20 @@ __device__ __forceinline__ void gradients(const Params &p, const Part &t)
     });
 }
 
-template <typename TX, typename TY, int E>
-__global__ void __launch_bounds__(kThreads, E == 8 ? 2 : 3) backward_kernel(const Params p)
+template <typename TX, typename TY, int E, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, WHOLE || E == 8 ? 2 : 3) backward_kernel(const Params p)
 {
     amsim::chain_start();
     const Part t = part_of<E>(p);
-    if (t.stats)
+    if (WHOLE) {
         channel_sums<TX, TY, E>(p, t);
-    else
-        gradients<TX, TY, E>(p, t);
+        __syncthreads();
+        gradients<TX, TY, E, WHOLE>(p, t);
+    } else if (t.stats) {
+        channel_sums<TX, TY, E>(p, t);
+    } else {
+        gradients<TX, TY, E, WHOLE>(p, t);
+    }
 }
 
 // Without pixels: mean 0, rstd 1 / sqrt(eps).
@@ -728,6 +745,7 @@ struct Plan {
 };
 constexpr int kTileBytes = 256;              // of a pixel, about
 constexpr int kPieces = 16;                  // of a thread, where there are enough
+constexpr int kWholePieces = 32;             // of a thread of a block that has all of its tile's pixels
 constexpr int64_t kWaveBytes = 32 << 20;     // of what is read twice
 
 // `fits(E)`: the call's rows are on E elements.  false: too many blocks.
@@ -751,10 +769,12 @@ bool plan(const amsim_group_norm_desc *d, bool fwd, int sms, Params &p, Plan *ou
     if (p.splits == 1 && p.tiles * p.tile < p.channels) return false;
     const int64_t units = d->batch * p.tiles;
     const int step = kThreads / (p.tile / E);
+    p.whole = p.splits == 1 && d->pixels <= (int64_t)step * kWholePieces;
     // chunks of kPieces a thread, smaller where these do not give every SM four blocks
     int64_t chunks = (d->pixels + (int64_t)step * kPieces - 1) / ((int64_t)step * kPieces);
     const int64_t enough = (4 * (int64_t)sms + units - 1) / units, most = (d->pixels + 2 * step - 1) / (2 * step);
     chunks = std::max<int64_t>(1, std::min<int64_t>(std::max(chunks, std::min(enough, most)), 1024));
+    if (p.whole) chunks = 1;
     const int64_t rows = (d->pixels + chunks - 1) / chunks;
     if (rows > 0x7FFFFFFF - kThreads) return false;
     p.rows = (int)rows;
@@ -771,7 +791,7 @@ bool plan(const amsim_group_norm_desc *d, bool fwd, int sms, Params &p, Plan *ou
     p.vec = aligned(p.w, 16) && aligned(p.b, 16);
     // waves alike in size
     const int64_t unit_bytes = std::max<int64_t>(1, d->pixels * p.tile * bytes);
-    const int64_t waves = std::max<int64_t>(1, units * unit_bytes / kWaveBytes);
+    const int64_t waves = p.whole ? 1 : std::max<int64_t>(1, units * unit_bytes / kWaveBytes);
     *out = Plan{E, units, (units + waves - 1) / waves};
     return 2 * out->wave * p.chunks <= 0x7FFFFFFF && units <= 0x7FFFFFFF;
 }
@@ -788,6 +808,10 @@ int start(bool chained, void (*kernel)(Params), int64_t blocks, int threads, con
 int waves(void (*kernel)(Params), Params p, const Plan &plan, cudaStream_t st)
 {
     p.apply_units = 0;
+    if (p.whole) {
+        p.stat_units = (unsigned)plan.units;
+        return start(false, kernel, plan.units, kThreads, p, st);
+    }
     for (int64_t at = 0; at < plan.units || p.stat_units; at += plan.wave) {
         p.apply_first = p.stat_first;
         p.apply_units = p.stat_units;
@@ -802,7 +826,9 @@ int waves(void (*kernel)(Params), Params p, const Plan &plan, cudaStream_t st)
 template <typename TX, typename TY, int E>
 int pass(bool fwd, const Params &p, const Plan &plan, cudaStream_t st)
 {
-    const int rc = waves(fwd ? forward_kernel<TX, TY, E> : backward_kernel<TX, TY, E>, p, plan, st);
+    auto *kernel = p.whole ? (fwd ? forward_kernel<TX, TY, E, true> : backward_kernel<TX, TY, E, true>)
+                           : (fwd ? forward_kernel<TX, TY, E, false> : backward_kernel<TX, TY, E, false>);
+    const int rc = waves(kernel, p, plan, st);
     if (rc || fwd || (!p.dw && !p.db)) return rc;
     return start(true, weights_kernel, (p.channels + 31) / 32, 1024, p, st);
 }
