@@ -1,11 +1,15 @@
 // The group norm with its activation, channels last, and its gradients.
 //
 // x is needed twice, for the statistics and for the result; what has to move is
-// one reading.  So the tensor goes through in waves of some megabytes: a launch
-// works out the statistics of one wave and the results of the wave before, whose
-// x (and dy) it then finds in the L2 cache.  Blocks of both roles stream and
-// share nothing, statistics are joined by whoever needs them, in a fixed order,
-// and the launches overlap: a wave's statistics wait for nothing.
+// one reading.  So the results of a tile follow its statistics some 32 MB behind,
+// and find x (and dy) in the L2 cache.  Both are blocks of one launch, whose order
+// is that in which they start: a block takes the next number, the even ones of a
+// pair work out results, the odd ones the statistics that come 32 MB later.  A
+// block of results waits until all of its tile's statistics are there, which
+// blocks that started before it work on; these wait for nothing.  Statistics are
+// joined by whoever needs them, in a fixed order.  Launches of a wave each (13 of
+// them for 617 MB) lost 4 us apiece at their ends; slabs kept in a cluster's shared
+// memory lost as much at its barriers (64 x 56 x 56 x 256 fp32 backward 159 and 154 us).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -41,6 +45,26 @@ Divisor divisor(unsigned d)
     return r;
 }
 
+// The waits that gave up, and after how long.
+__device__ unsigned int g_wait_timeouts;
+__device__ long long g_wait_limit_ns = 2000000000LL;
+int wait_status(unsigned int *bits, int clear)
+{
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_wait_timeouts, sizeof(v)) != cudaSuccess) return AMSIM_ECUDA;
+    *bits |= v;
+    if (clear && v) {
+        const unsigned int zero = 0;
+        if (cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(zero)) != cudaSuccess) return AMSIM_ECUDA;
+    }
+    return AMSIM_OK;
+}
+int wait_limit(long long ns)
+{
+    return cudaMemcpyToSymbol(g_wait_limit_ns, &ns, sizeof(ns)) == cudaSuccess ? AMSIM_OK : AMSIM_ECUDA;
+}
+[[maybe_unused]] const bool g_wait_words = amsim::register_wait_words(&wait_status, &wait_limit);
+
 struct Params {
     const void *x, *dy;
     const float *w, *b;
@@ -58,7 +82,9 @@ struct Params {
     int step, vec;                           // pixels of a block at once; w and b on 16 bytes
     int whole;                               // a block has all of its tile's pixels, and does both parts
     Divisor by_tiles, by_splits, by_chunks, by_wide, by_step, by_group_wide, by_size;
-    unsigned stat_units, stat_first, apply_units, apply_first;   // units (sample, tile) of a launch's two roles
+    Divisor by_pair;                         // of 2 chunks
+    unsigned units, lag;                     // tiles of all samples; how many the results are behind
+    unsigned *next, *ready;                  // the next block's number; statistics of a tile (or group) that are there
 };
 
 constexpr int kThreads = 256;
@@ -240,6 +266,7 @@ __device__ __forceinline__ float warp_sum(float v)
 // every step-th pixel.
 struct Part {
     bool stats;
+    unsigned unit;
     int n, chunk, c0, channels, groups;      // the tile's first channel, channels, groups (1: a part of one)
     int group, split;                        // its first group, and which part of it
     int wide, piece, row, step, count;       // pieces of a pixel; this thread's, its first pixel, how many
@@ -247,18 +274,30 @@ struct Part {
     int64_t first;                           // the chunk's first pixel in the sample
     int rows;                                // and its pixels
 };
-template <int E>
-__device__ __forceinline__ Part part_of(const Params &p)
+template <int E, bool WHOLE>
+__device__ __forceinline__ Part part_of(const Params &p, unsigned number)
 {
     Part t;
-    // the roles' blocks in turn, as long as there are both
-    unsigned b = blockIdx.x;
-    const unsigned stats = p.stat_units * (unsigned)p.chunks, apply = p.apply_units * (unsigned)p.chunks;
-    const unsigned less = min(stats, apply);
-    t.stats = b < 2 * less ? !(b & 1) : stats > apply;
-    b = b < 2 * less ? b >> 1 : b - less;
-    const unsigned local = p.by_chunks(b), unit = local + (t.stats ? p.stat_first : p.apply_first);
-    t.chunk = (int)(b - local * (unsigned)p.chunks);
+    unsigned unit = blockIdx.x;
+    t.stats = true;
+    t.chunk = 0;
+    if (!WHOLE) {
+        // the first `lag` tiles' statistics, then pairs of results and statistics, then the last results
+        const unsigned chunks = (unsigned)p.chunks, b = number, lead = p.lag * chunks, pairs = 2 * (p.units - p.lag) * chunks;
+        if (b < lead || b >= lead + pairs) {
+            t.stats = b < lead;
+            const unsigned m = t.stats ? b : b - lead - pairs;
+            unit = p.by_chunks(m);
+            t.chunk = (int)(m - unit * chunks);
+            if (!t.stats) unit += p.units - p.lag;
+        } else {
+            const unsigned m = b - lead, pair = p.by_pair(m), r = m - pair * 2 * chunks;
+            t.stats = r & 1;
+            t.chunk = (int)(r >> 1);
+            unit = t.stats ? pair + p.lag : pair;
+        }
+    }
+    t.unit = unit;
     t.n = (int)p.by_tiles(unit);
     const int tile = (int)(unit - (unsigned)t.n * (unsigned)p.tiles);
     t.wide = p.tile / E;
@@ -294,6 +333,51 @@ __device__ __forceinline__ Part part_of(const Params &p)
     t.count = t.row >= t.step ? 0 : (int)(odd ? more / (unsigned)t.step : p.by_step(more));
     return t;
 }
+// The block's number in the order in which blocks start.
+__device__ __forceinline__ unsigned take_number(const Params &p)
+{
+    __shared__ unsigned number;
+    if (threadIdx.x == 0) number = atomicAdd(p.next, 1u);
+    __syncthreads();
+    return number;
+}
+__device__ __forceinline__ unsigned *ready_of(const Params &p, const Part &t)
+{
+    return p.ready + (p.splits > 1 ? (unsigned)t.n * (unsigned)p.groups + (unsigned)t.group : t.unit);
+}
+// A block's statistics are written.
+__device__ __forceinline__ void announce(const Params &p, const Part &t)
+{
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        atomicAdd(ready_of(p, t), 1u);
+    }
+}
+// Until all statistics that the block's results need are there, or the limit has
+// passed: then it says so, and its results are wrong.
+__device__ __forceinline__ void await(const Params &p, const Part &t)
+{
+    if (threadIdx.x == 0) {
+        const unsigned all = (unsigned)p.chunks * (unsigned)p.splits, *flag = ready_of(p, t);
+        long long since = 0;
+        for (unsigned i = 0;; ++i) {
+            unsigned there;
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(flag) : "memory");
+            if (there >= all) break;
+            if (i & 63) continue;            // the timer once in 64 polls
+            long long now;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+            if (!since) since = now;
+            if (now - since >= g_wait_limit_ns) {
+                atomicOr(&g_wait_timeouts, (unsigned)AMSIM_WAIT_PARTIAL);
+                break;
+            }
+        }
+    }
+    __syncthreads();
+}
+
 // Where the parts of a sample's chunk lie: one for each group, or for each split of it.
 __device__ __forceinline__ int64_t parts_at(const Params &p, int n, int chunk)
 {
@@ -369,18 +453,30 @@ __device__ __forceinline__ void put_last(T *at, const Values<E> &r)
     __stcs(reinterpret_cast<typename Raw<T, E>::Word *>(at), *reinterpret_cast<const typename Raw<T, E>::Word *>(out));
 }
 
-// Runs over a thread's pieces: `load(i, k)` four at a time, then `use(i, k)`.
-constexpr int kAhead = 4;
-template <typename L, typename U>
+// Runs over a thread's pieces: `load(i, k)` A at a time into places k, `use(i, k)`
+// of A while the next are under way.
+template <int A, typename L, typename U>
 __device__ __forceinline__ void over_pieces(int count, L load, U use)
 {
+    auto load_all = [&](int i, int place) {
+#pragma unroll
+        for (int k = 0; k < A; ++k) load(i + k, place + k);
+    };
+    auto use_all = [&](int i, int place) {
+#pragma unroll
+        for (int k = 0; k < A; ++k) use(i + k, place + k);
+    };
     int i = 0;
+    if (A <= count) load_all(0, 0);
 #pragma unroll 1
-    for (; i + kAhead <= count; i += kAhead) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) load(i + k, k);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) use(i + k, k);
+    while (i + A <= count) {
+        if (i + 2 * A <= count) load_all(i + A, A);
+        use_all(i, 0);
+        i += A;
+        if (i + A > count) break;
+        if (i + 2 * A <= count) load_all(i + A, 0);
+        use_all(i, A);
+        i += A;
     }
 #pragma unroll 1
     for (; i < count; ++i) {
@@ -388,6 +484,7 @@ __device__ __forceinline__ void over_pieces(int count, L load, U use)
         use(i, 0);
     }
 }
+constexpr int kForwardAhead = 4, kBackwardAhead = 2;
 
 // Forward, statistics: a chunk's moments by part.  A thread sums about its first
 // value: what cancels is no larger than the values' own spread.
@@ -401,8 +498,8 @@ __device__ __forceinline__ void moments(const Params &p, const Part &t)
     float2 s1 = both(0.0f), s2 = both(0.0f);
     float about = 0.0f;
     if (t.count) about = read<E>(x).values().v[0].x;
-    Raw<TX, E> r[kAhead];
-    over_pieces(
+    Raw<TX, E> r[2 * kForwardAhead];
+    over_pieces<kForwardAhead>(
         t.count, [&](int i, int k) { r[k] = read<E>(x + i * far); },
         [&](int, int k) {
             const Values<E> v = r[k].values();
@@ -444,7 +541,7 @@ __device__ __forceinline__ void normalise(const Params &p, const Part &t)
         Moments m{0.0f, 0.0f, 0.0f};
         for (int i = lane; i < p.chunks * p.splits; i += 32) {
             const int chunk = (int)p.by_splits((unsigned)i), split = i - chunk * p.splits;
-            const float2 f = p.by_part[parts_at(p, t.n, chunk) + (int64_t)(t.group + g) * p.splits + split];
+            const float2 f = __ldcg(&p.by_part[parts_at(p, t.n, chunk) + (int64_t)(t.group + g) * p.splits + split]);
             m = join(m, Moments{values_of(p, chunk, split), f.x, f.y});
         }
 #pragma unroll
@@ -474,8 +571,8 @@ __device__ __forceinline__ void normalise(const Params &p, const Part &t)
     TY *y = static_cast<TY *>(p.y) + pixel * p.ldy + c;
     const int64_t far_x = (int64_t)t.step * p.ldx, far_y = (int64_t)t.step * p.ldy;
     with_activation(p.act, [&](auto act) {
-        Raw<TX, E> r[kAhead];
-        over_pieces(
+        Raw<TX, E> r[2 * kForwardAhead];
+        over_pieces<kForwardAhead>(
             t.count, [&](int i, int k) { r[k] = read_last<E>(x + i * far_x); },
             [&](int i, int k) {
                 Values<E> v = r[k].values();
@@ -489,16 +586,16 @@ __device__ __forceinline__ void normalise(const Params &p, const Part &t)
 template <typename TX, typename TY, int E, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, WHOLE ? 3 : 4) forward_kernel(const Params p)
 {
-    amsim::chain_start();
-    const Part t = part_of<E>(p);
+    const Part t = part_of<E, WHOLE>(p, WHOLE ? 0 : take_number(p));
     if (WHOLE) {
         moments<TX, E>(p, t);
         __syncthreads();
         normalise<TX, TY, E>(p, t);
     } else if (t.stats) {
         moments<TX, E>(p, t);
+        announce(p, t);
     } else {
-        amsim::chain_wait();                 // for the wave's statistics
+        await(p, t);
         normalise<TX, TY, E>(p, t);
     }
 }
@@ -544,9 +641,9 @@ __device__ __forceinline__ void channel_sums(const Params &p, const Part &t)
     float2 s[(E + 1) / 2], q[(E + 1) / 2];
     each_pair<E>([&](int j) { s[j] = q[j] = both(0.0f); });
     with_activation(p.act, [&](auto act) {
-        Raw<TX, E> r[kAhead];
-        Raw<TY, E> d[kAhead];
-        over_pieces(
+        Raw<TX, E> r[2 * kBackwardAhead];
+        Raw<TY, E> d[2 * kBackwardAhead];
+        over_pieces<kBackwardAhead>(
             t.count,
             [&](int i, int k) {
                 r[k] = read<E>(x + i * far_x);
@@ -611,12 +708,12 @@ __device__ __forceinline__ void gradients(const Params &p, const Part &t)
     __shared__ float2 means[kTileGroups];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = t.c0 + t.piece * E;
     const Known<E> k = known<E>(p, t);
-    if (!WHOLE) amsim::chain_wait();         // for the wave's sums
+    if (!WHOLE) await(p, t);
     for (int g = warp; g < t.groups; g += kThreads / 32) {
         float2 m = both(0.0f);
         for (int i = lane; i < p.chunks * p.splits; i += 32) {
             const int chunk = (int)p.by_splits((unsigned)i), split = i - chunk * p.splits;
-            m = add2(m, p.by_part[parts_at(p, t.n, chunk) + (int64_t)(t.group + g) * p.splits + split]);
+            m = add2(m, __ldcg(&p.by_part[parts_at(p, t.n, chunk) + (int64_t)(t.group + g) * p.splits + split]));
         }
         m = make_float2(warp_sum(m.x), warp_sum(m.y));
         const float count = (float)p.size * (float)p.pixels;
@@ -632,9 +729,9 @@ __device__ __forceinline__ void gradients(const Params &p, const Part &t)
     TX *dx = static_cast<TX *>(p.dx) + pixel * p.lddx + c;
     const int64_t far_x = (int64_t)t.step * p.ldx, far_y = (int64_t)t.step * p.ldy, far = (int64_t)t.step * p.lddx;
     with_activation(p.act, [&](auto act) {
-        Raw<TX, E> r[kAhead];
-        Raw<TY, E> d[kAhead];
-        over_pieces(
+        Raw<TX, E> r[2 * kBackwardAhead];
+        Raw<TY, E> d[2 * kBackwardAhead];
+        over_pieces<kBackwardAhead>(
             t.count,
             [&](int i, int n) {
                 r[n] = read_last<E>(x + i * far_x);
@@ -653,13 +750,14 @@ template <typename TX, typename TY, int E, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, WHOLE || E == 8 ? 2 : 3) backward_kernel(const Params p)
 {
     amsim::chain_start();
-    const Part t = part_of<E>(p);
+    const Part t = part_of<E, WHOLE>(p, WHOLE ? 0 : take_number(p));
     if (WHOLE) {
         channel_sums<TX, TY, E>(p, t);
         __syncthreads();
         gradients<TX, TY, E, WHOLE>(p, t);
     } else if (t.stats) {
         channel_sums<TX, TY, E>(p, t);
+        announce(p, t);
     } else {
         gradients<TX, TY, E, WHOLE>(p, t);
     }
@@ -738,15 +836,16 @@ Params params(const amsim_group_norm_desc *d)
     return p;
 }
 
-// Channels of a piece, tiles, chunks and waves of a call.
+// Channels of a piece, and scratch of a call: values by part and by channel, flags.
 struct Plan {
     int E;
-    int64_t units, wave;                     // tiles of all samples, of one wave
+    size_t parts, sums, flags;
+    size_t bytes() const { return (parts + sums) * sizeof(float2) + flags * sizeof(unsigned); }
 };
 constexpr int kTileBytes = 256;              // of a pixel, about
 constexpr int kPieces = 16;                  // of a thread, where there are enough
 constexpr int kWholePieces = 32;             // of a thread of a block that has all of its tile's pixels
-constexpr int64_t kWaveBytes = 32 << 20;     // of what is read twice
+constexpr int64_t kBehind = 32 << 20;        // bytes of what is read twice between a tile's statistics and results
 
 // `fits(E)`: the call's rows are on E elements.  false: too many blocks.
 template <typename F>
@@ -789,11 +888,24 @@ bool plan(const amsim_group_norm_desc *d, bool fwd, int sms, Params &p, Plan *ou
     p.by_group_wide = divisor((unsigned)std::max(1, p.size / E));
     p.by_size = divisor((unsigned)p.size);
     p.vec = aligned(p.w, 16) && aligned(p.b, 16);
-    // waves alike in size
+    p.by_pair = divisor(2u * (unsigned)p.chunks);
     const int64_t unit_bytes = std::max<int64_t>(1, d->pixels * p.tile * bytes);
-    const int64_t waves = p.whole ? 1 : std::max<int64_t>(1, units * unit_bytes / kWaveBytes);
-    *out = Plan{E, units, (units + waves - 1) / waves};
-    return 2 * out->wave * p.chunks <= 0x7FFFFFFF && units <= 0x7FFFFFFF;
+    if (units > 0x7FFFFFFF || 2 * units * p.chunks > 0x7FFFFFFF) return false;
+    p.units = (unsigned)units;
+    p.lag = (unsigned)std::min(units, std::max<int64_t>(p.splits, (kBehind + unit_bytes - 1) / unit_bytes));
+    out->E = E;
+    out->parts = (size_t)p.samples_chunks * p.groups * p.splits;
+    out->sums = fwd ? 0 : (size_t)p.samples_chunks * p.channels;
+    out->flags = p.whole ? 0 : 1 + (size_t)(p.splits > 1 ? d->batch * p.groups : units);
+    return true;
+}
+
+void scratch(Params &p, const Plan &q, void *ws)
+{
+    p.by_part = static_cast<float2 *>(ws);
+    p.by_channel = p.by_part + q.parts;
+    p.next = reinterpret_cast<unsigned *>(p.by_channel + q.sums);
+    p.ready = p.next + 1;
 }
 
 int start(bool chained, void (*kernel)(Params), int64_t blocks, int threads, const Params &p, cudaStream_t st)
@@ -804,31 +916,18 @@ int start(bool chained, void (*kernel)(Params), int64_t blocks, int threads, con
     return rc;
 }
 
-// A launch for each wave's statistics, which also has the wave before's results, and one for the last's.
-int waves(void (*kernel)(Params), Params p, const Plan &plan, cudaStream_t st)
-{
-    p.apply_units = 0;
-    if (p.whole) {
-        p.stat_units = (unsigned)plan.units;
-        return start(false, kernel, plan.units, kThreads, p, st);
-    }
-    for (int64_t at = 0; at < plan.units || p.stat_units; at += plan.wave) {
-        p.apply_first = p.stat_first;
-        p.apply_units = p.stat_units;
-        p.stat_first = (unsigned)at;
-        p.stat_units = (unsigned)std::max<int64_t>(0, std::min(plan.wave, plan.units - at));
-        const int64_t blocks = ((int64_t)p.stat_units + p.apply_units) * p.chunks;
-        if (const int rc = start(at > 0, kernel, blocks, kThreads, p, st)) return rc;
-    }
-    return AMSIM_OK;
-}
-
 template <typename TX, typename TY, int E>
 int pass(bool fwd, const Params &p, const Plan &plan, cudaStream_t st)
 {
-    auto *kernel = p.whole ? (fwd ? forward_kernel<TX, TY, E, true> : backward_kernel<TX, TY, E, true>)
-                           : (fwd ? forward_kernel<TX, TY, E, false> : backward_kernel<TX, TY, E, false>);
-    const int rc = waves(kernel, p, plan, st);
+    int rc;
+    if (p.whole) {
+        rc = start(false, fwd ? forward_kernel<TX, TY, E, true> : backward_kernel<TX, TY, E, true>, p.units, kThreads, p, st);
+    } else {
+        rc = amsim::cuda_status(cudaMemsetAsync(p.next, 0, plan.flags * sizeof(unsigned), st));
+        if (rc) return rc;
+        rc = start(false, fwd ? forward_kernel<TX, TY, E, false> : backward_kernel<TX, TY, E, false>,
+                   2 * (int64_t)p.units * p.chunks, kThreads, p, st);
+    }
     if (rc || fwd || (!p.dw && !p.db)) return rc;
     return start(true, weights_kernel, (p.channels + 31) / 32, 1024, p, st);
 }
@@ -860,9 +959,9 @@ extern "C" size_t amsim_group_norm_workspace_size(const amsim_group_norm_desc *d
         Params p = params(d);
         Plan q;
         if (!plan(d, !which, sms ? sms : 1, p, &q, [&](int E) { return E <= on; })) return 0;
-        most = std::max(most, (size_t)p.samples_chunks * ((size_t)p.groups * p.splits + (which ? p.channels : 0)));
+        most = std::max(most, q.bytes());
     }
-    return most * sizeof(float2);
+    return most;
 }
 
 extern "C" int amsim_group_norm_fwd(const amsim_group_norm_desc *d, const void *x, const float *w, const float *b,
@@ -897,9 +996,9 @@ extern "C" int amsim_group_norm_fwd(const amsim_group_norm_desc *d, const void *
     if (!plan(d, true, sms ? sms : 1, p, &q,
               [&](int n) { return whole(x, p.ldx, xs, n) && whole(y, p.ldy, ys, n); }))
         return AMSIM_EINVAL;
-    if (!ws || ws_bytes < (size_t)p.samples_chunks * p.groups * p.splits * sizeof(float2)) return AMSIM_EINVAL;
+    if (!ws || ws_bytes < q.bytes()) return AMSIM_EINVAL;
     if (!sms) return AMSIM_ECUDA;
-    p.by_part = static_cast<float2 *>(ws);
+    scratch(p, q, ws);
     return run(d, true, p, q, st);
 }
 
@@ -938,10 +1037,8 @@ extern "C" int amsim_group_norm_bwd(const amsim_group_norm_desc *d, const void *
             return whole(x, p.ldx, xs, n) && whole(dx, p.lddx, xs, n) && whole(dy, p.ldy, ys, n);
         }))
         return AMSIM_EINVAL;
-    const size_t parts = (size_t)p.samples_chunks * p.groups * p.splits;
-    if (!ws || ws_bytes < (parts + (size_t)p.samples_chunks * p.channels) * sizeof(float2)) return AMSIM_EINVAL;
+    if (!ws || ws_bytes < q.bytes()) return AMSIM_EINVAL;
     if (!sms) return AMSIM_ECUDA;
-    p.by_part = static_cast<float2 *>(ws);
-    p.by_channel = p.by_part + parts;
+    scratch(p, q, ws);
     return run(d, false, p, q, st);
 }

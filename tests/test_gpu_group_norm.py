@@ -144,6 +144,39 @@ def test_large_samples(amd, pixels, channels, groups, x):
     both(amd, make(2, pixels, channels, x, x, seed=channels), groups, "silu", x=x, y=x)
 
 
+# tensors of which only a part is under way at once: results far behind the statistics, groups of many tiles
+@pytest.mark.parametrize("batch,pixels,channels,groups", [(6, 9000, 256, 32), (3, 5000, 1500, 1), (2, 9000, 1024, 2)])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_large_batches(amd, batch, pixels, channels, groups, x):
+    both(amd, make(batch, pixels, channels, x, x, seed=channels), groups, "silu", x=x, y=x)
+
+
+@pytest.mark.parametrize("way", ["forward", "backward"])
+def test_wait_that_gives_up_is_reported(amd, way):
+    """With no patience the blocks of results stop waiting for statistics: the
+    call ends and says so, and the next one is right."""
+    import torch
+    a = make(4, 20000, 64)
+    want = amd.group_norm(a["x"], 8, a["w"], a["b"])
+    back = amd.group_norm_backward(a["dy"], a["x"], a["w"], a["b"], *want[1:])
+    amd.amsim_device_errors()
+    try:
+        amd.amsim_set_flag_wait_limit(0)
+        for _ in range(5):
+            if way == "forward":
+                amd.group_norm(a["x"], 8, a["w"], a["b"])
+            else:
+                amd.group_norm_backward(a["dy"], a["x"], a["w"], a["b"], *want[1:])
+        rc, bits = amd.amsim_device_errors()
+    finally:
+        amd.amsim_set_flag_wait_limit(2_000_000_000)
+    assert rc == amd.AMSIM_ETIMEOUT and bits == amd.AMSIM_WAIT_PARTIAL
+    assert all(torch.equal(p, q) for p, q in zip(amd.group_norm(a["x"], 8, a["w"], a["b"]), want))
+    assert all(torch.equal(p, q) for p, q in zip(
+        amd.group_norm_backward(a["dy"], a["x"], a["w"], a["b"], *want[1:]), back))
+    assert amd.amsim_device_errors() == (amd.AMSIM_OK, 0)
+
+
 @pytest.mark.parametrize("w,b", [(False, False), (True, False), (False, True)])
 def test_without_weights(amd, w, b):
     both(amd, make(2, 77, 24, w=w, b=b), 3, "silu")
