@@ -44,10 +44,17 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T *x, const T *
                 }
         }
     }
+    // the numbers' upper halves are the same for all of a thread's quads but where they pass 2^32
+    uint32_t upper = (uint32_t)((uint64_t)(first * E) >> 34);
+    amsim::QuadStream stream = amsim::quad_stream(upper, call, d);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int64_t at = (first + i * kThreads) * E;
         if (at >= n) return;
+        if ((uint32_t)((uint64_t)at >> 34) != upper) {
+            upper = (uint32_t)((uint64_t)at >> 34);
+            stream = amsim::quad_stream(upper, call, d);
+        }
         Piece<T> out;
 #pragma unroll
         for (int q = 0; q < E; q += 4) {
@@ -55,8 +62,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T *x, const T *
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = widen(in[i].e[q + k]);
             if (d.border) {
-                const uint64_t quad = (uint64_t)(at + q) >> 2;
-                const uint4 u = amsim::quad_words((uint32_t)quad, amsim::quad_stream((uint32_t)(quad >> 32), call, d), d);
+                const uint4 u = amsim::quad_words((uint32_t)((uint64_t)(at + q) >> 2), stream, d);
                 v[0] = u.x >= d.border ? v[0] * d.scale : 0.0f;
                 v[1] = u.y >= d.border ? v[1] * d.scale : 0.0f;
                 v[2] = u.z >= d.border ? v[2] * d.scale : 0.0f;

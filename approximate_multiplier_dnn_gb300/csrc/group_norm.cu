@@ -100,13 +100,6 @@ __device__ __forceinline__ void narrow(float v, float *o) { *o = v; }
 __device__ __forceinline__ void narrow(float v, __nv_bfloat16 *o) { *o = __float2bfloat16_rn(v); }
 
 template <int E, typename T>
-__device__ __forceinline__ void load(const T *at, float (&v)[E])
-{
-    const Vec<T, E> r = *reinterpret_cast<const Vec<T, E> *>(at);
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = widen(r.e[e]);
-}
-template <int E, typename T>
 __device__ __forceinline__ void store(T *at, const float (&v)[E])
 {
     Vec<T, E> r;
@@ -204,15 +197,6 @@ __device__ __forceinline__ void each_pair(F use)
 {
 #pragma unroll
     for (int i = 0; i < (E + 1) / 2; ++i) use(i);
-}
-template <int E, typename T>
-__device__ __forceinline__ Values<E> take(const void *slot)
-{
-    float f[E];
-    load<E>(static_cast<const T *>(slot), f);
-    Values<E> r;
-    each_pair<E>([&](int i) { r.v[i] = make_float2(f[2 * i], 2 * i + 1 < E ? f[2 * i + 1 < E ? 2 * i + 1 : 0] : 0.0f); });
-    return r;
 }
 template <int E, typename T>
 __device__ __forceinline__ void put(T *at, const Values<E> &r)
