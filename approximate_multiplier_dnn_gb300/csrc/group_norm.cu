@@ -472,8 +472,9 @@ constexpr int kForwardAhead = 4, kBackwardAhead = 2;
 
 // Forward, statistics: a chunk's moments by part.  A thread sums about its first
 // value: what cancels is no larger than the values' own spread.
-template <typename TX, int E>
-__device__ __forceinline__ void moments(const Params &p, const Part &t)
+// They go to `found` where the block itself works out the results.
+template <typename TX, int E, bool WHOLE>
+__device__ __forceinline__ void moments(const Params &p, const Part &t, float2 *found)
 {
     __shared__ Moments all[kThreads];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -510,28 +511,29 @@ __device__ __forceinline__ void moments(const Params &p, const Part &t)
             m = join(m, Moments{__shfl_down_sync(0xFFFFFFFFu, m.n, d), __shfl_down_sync(0xFFFFFFFFu, m.mean, d),
                                 __shfl_down_sync(0xFFFFFFFFu, m.m2, d)});
         if (lane == 0)
-            p.by_part[parts_at(p, t.n, t.chunk) + (int64_t)(t.group + g) * p.splits + t.split] =
+            *(WHOLE ? found + g : p.by_part + parts_at(p, t.n, t.chunk) + (int64_t)(t.group + g) * p.splits + t.split) =
                 make_float2(m.mean, m.m2);
     }
 }
 
 // Forward, results.
-template <typename TX, typename TY, int E>
-__device__ __forceinline__ void normalise(const Params &p, const Part &t)
+template <typename TX, typename TY, int E, bool WHOLE>
+__device__ __forceinline__ void normalise(const Params &p, const Part &t, float2 *stats)
 {
-    __shared__ float2 stats[kTileGroups];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int g = warp; g < t.groups; g += kThreads / 32) {
         Moments m{0.0f, 0.0f, 0.0f};
-        for (int i = lane; i < p.chunks * p.splits; i += 32) {
+        if (WHOLE) m = Moments{values_of(p, 0, 0), stats[g].x, stats[g].y};
+        for (int i = lane; !WHOLE && i < p.chunks * p.splits; i += 32) {
             const int chunk = (int)p.by_splits((unsigned)i), split = i - chunk * p.splits;
             const float2 f = __ldcg(&p.by_part[parts_at(p, t.n, chunk) + (int64_t)(t.group + g) * p.splits + split]);
             m = join(m, Moments{values_of(p, chunk, split), f.x, f.y});
         }
 #pragma unroll
-        for (int d = 16; d; d >>= 1)
+        for (int d = 16; d && !WHOLE; d >>= 1)
             m = join(m, Moments{__shfl_down_sync(0xFFFFFFFFu, m.n, d), __shfl_down_sync(0xFFFFFFFFu, m.mean, d),
                                 __shfl_down_sync(0xFFFFFFFFu, m.m2, d)});
+        __syncwarp();                        // every lane has read stats[g]
         if (lane == 0) {
             const float2 f = make_float2(m.mean, __frsqrt_rn(m.m2 / m.n + p.eps));
             stats[g] = f;
@@ -545,11 +547,14 @@ __device__ __forceinline__ void normalise(const Params &p, const Part &t)
     Values<E> w = weights_of<E>(p, p.w, c, 1.0f), b = weights_of<E>(p, p.b, c, 0.0f);
     __syncthreads();
     const float2 f = stats[t.mine];
-    each_pair<E>([&](int j) {
-        // z = x (rstd w) + (b - mean rstd w): what this rounds is of the size of what the mean's rounding leaves
-        w.v[j] = mul2(w.v[j], both(f.y));
-        b.v[j] = fma2(w.v[j], both(-f.x), b.v[j]);
-    });
+    // bf16 results: z = x (rstd w) + (b - mean rstd w).  What that rounds is of the
+    // size of what the mean's rounding leaves, twice the error of (x - mean) rstd w + b.
+    constexpr bool kFold = sizeof(TY) == 2;
+    if (kFold)
+        each_pair<E>([&](int j) {
+            w.v[j] = mul2(w.v[j], both(f.y));
+            b.v[j] = fma2(w.v[j], both(-f.x), b.v[j]);
+        });
     const int64_t pixel = t.n * p.pixels + t.first + t.row;
     const TX *x = static_cast<const TX *>(p.x) + pixel * p.ldx + c;
     TY *y = static_cast<TY *>(p.y) + pixel * p.ldy + c;
@@ -560,7 +565,10 @@ __device__ __forceinline__ void normalise(const Params &p, const Part &t)
             t.count, [&](int i, int k) { r[k] = read_last<E>(x + i * far_x); },
             [&](int i, int k) {
                 Values<E> v = r[k].values();
-                each_pair<E>([&](int j) { v.v[j] = activate2<act.value>(fma2(v.v[j], w.v[j], b.v[j])); });
+                each_pair<E>([&](int j) {
+                    const float2 h = kFold ? v.v[j] : mul2(add2(v.v[j], both(-f.x)), both(f.y));
+                    v.v[j] = activate2<act.value>(fma2(h, w.v[j], b.v[j]));
+                });
                 put_last<E>(y + i * far_y, v);
             });
     });
@@ -570,17 +578,18 @@ __device__ __forceinline__ void normalise(const Params &p, const Part &t)
 template <typename TX, typename TY, int E, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, WHOLE ? 3 : 4) forward_kernel(const Params p)
 {
+    __shared__ float2 stats[kTileGroups];
     const Part t = part_of<E, WHOLE>(p, WHOLE ? 0 : take_number(p));
     if (WHOLE) {
-        moments<TX, E>(p, t);
+        moments<TX, E, WHOLE>(p, t, stats);
         __syncthreads();
-        normalise<TX, TY, E>(p, t);
+        normalise<TX, TY, E, WHOLE>(p, t, stats);
     } else if (t.stats) {
-        moments<TX, E>(p, t);
+        moments<TX, E, WHOLE>(p, t, stats);
         announce(p, t);
     } else {
         await(p, t);
-        normalise<TX, TY, E>(p, t);
+        normalise<TX, TY, E, WHOLE>(p, t, stats);
     }
 }
 
@@ -887,7 +896,7 @@ bool plan(const amsim_group_norm_desc *d, bool fwd, int sms, Params &p, Plan *ou
     p.units = (unsigned)units;
     p.lag = (unsigned)std::min(units, std::max<int64_t>(p.splits, (kBehind + unit_bytes - 1) / unit_bytes));
     out->E = E;
-    out->parts = (size_t)p.samples_chunks * p.groups * p.splits;
+    out->parts = fwd && p.whole ? 0 : (size_t)p.samples_chunks * p.groups * p.splits;
     out->sums = fwd ? 0 : (size_t)p.samples_chunks * p.channels;
     out->flags = p.whole ? 0 : 1 + (size_t)(p.splits > 1 ? d->batch * p.groups : units);
     return true;
@@ -989,7 +998,7 @@ extern "C" int amsim_group_norm_fwd(const amsim_group_norm_desc *d, const void *
     if (!plan(d, true, sms ? sms : 1, p, &q,
               [&](int n) { return whole(x, p.ldx, xs, n) && whole(y, p.ldy, ys, n); }))
         return AMSIM_EINVAL;
-    if (!ws || ws_bytes < q.bytes()) return AMSIM_EINVAL;
+    if (q.bytes() && (!ws || ws_bytes < q.bytes())) return AMSIM_EINVAL;
     if (!sms) return AMSIM_ECUDA;
     scratch(p, q, ws);
     return run(d, true, p, q, st);
