@@ -441,25 +441,41 @@ __device__ __forceinline__ void forward_rows(const Params &p, const Part &t, con
             else
                 end(std::false_type{});
         } else {
+            // four chunks at a time, whose loads are under way together
             std::false_type some;
-            auto logits_of = [&](int chunk) {
-                return logits(some, load_chunk<VEC>(in, chunk, lane, w.visible, -INFINITY), chunk);
+            auto logits_of = [&](int chunk, Four (&a)[4]) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    a[v] = load_chunk<VEC>(in, chunk + v * t.step, lane, w.visible, -INFINITY);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) a[v] = logits(some, a[v], chunk + v * t.step);
             };
-            for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += t.step) {
-                const Four a = logits_of(chunk);
-                const float most = fmaxf(fmaxf(a.a.x, a.a.y), fmaxf(a.b.x, a.b.y));
+            Four a[4];
+            for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += 4 * t.step) {
+                logits_of(chunk, a);
+                float most = -INFINITY;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    most = fmaxf(fmaxf(most, fmaxf(a[v].a.x, a[v].a.y)), fmaxf(a[v].b.x, a[v].b.y));
                 if (most > mine) {
                     total *= part_factor(mine, most);
                     mine = most;
                 }
-                total += sum(exponentials(a, finite_base(mine)));
+                const float base = finite_base(mine);
+                Four sums = exponentials(a[0], base);
+#pragma unroll
+                for (int v = 1; v < 4; ++v) sums = add(sums, exponentials(a[v], base));
+                total += sum(sums);
             }
             const float top = warp_max(mine);
             total = warp_sum(mine == -INFINITY ? total : total * part_factor(mine, top));
             joined = join_rows<BLOCK>(p, top, total, exchange, turn);
             const float base = finite_base(joined.x);
-            for (int chunk = t.first_chunk; chunk < p.chunks; chunk += t.step)
-                finish(some, exponentials(logits_of(chunk), base), chunk, joined.y);
+            for (int chunk = t.first_chunk; chunk < p.chunks; chunk += 4 * t.step) {
+                logits_of(chunk, a);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) finish(some, exponentials(a[v], base), chunk + v * t.step, joined.y);
+            }
         }
         if (p.out_stats && lane == 0 && (!BLOCK || (threadIdx.x == 0 && t.rank == 0)))
             *reinterpret_cast<float2 *>(p.out_stats + 2 * w.row) = joined;
@@ -619,21 +635,30 @@ __device__ __forceinline__ void backward_rows(const Params &p, const Part &t, co
             else
                 end(std::false_type{});
         } else {
+            // two chunks at a time, whose loads are under way together
             std::false_type some;
-            auto both_of = [&](int chunk, Four &a, Four &g) {
-                a = load_chunk<VEC>(in, chunk, lane, w.visible, kHidden);
-                g = load_chunk<VEC>(up, chunk, lane, w.visible, 0.0f);
-                values(some, chunk, a, g);
+            auto both_of = [&](int chunk, Four (&a)[2], Four (&g)[2]) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    a[v] = load_chunk<VEC>(in, chunk + v * t.step, lane, w.visible, kHidden);
+                    g[v] = load_chunk<VEC>(up, chunk + v * t.step, lane, w.visible, 0.0f);
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v) values(some, chunk + v * t.step, a[v], g[v]);
             };
-            Four a, g;
-            for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += t.step) {
+            Four a[2], g[2];
+            for (int chunk = t.first_chunk; chunk * 128 < w.visible; chunk += 2 * t.step) {
                 both_of(chunk, a, g);
-                part = Four{fma2(a.a, g.a, part.a), fma2(a.b, g.b, part.b)};
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+                    if ((chunk + v * t.step) * 128 < w.visible)
+                        part = Four{fma2(a[v].a, g[v].a, part.a), fma2(a[v].b, g[v].b, part.b)};
             }
             const float dot = join_sums<BLOCK>(p, warp_sum(sum(part)), exchange, turn);
-            for (int chunk = t.first_chunk; chunk < p.chunks; chunk += t.step) {
+            for (int chunk = t.first_chunk; chunk < p.chunks; chunk += 2 * t.step) {
                 both_of(chunk, a, g);
-                finish(some, chunk, dot, a, g);
+#pragma unroll
+                for (int v = 0; v < 2; ++v) finish(some, chunk + v * t.step, dot, a[v], g[v]);
             }
         }
         if (!BLOCK) __syncwarp();            // other lanes add to the same distances for the next row
@@ -754,7 +779,7 @@ int64_t stride(int64_t ld, int64_t keys) { return ld ? ld : keys; }
 int check(const amsim_attention_softmax_desc *d, Drop *drop)
 {
     if (!d || d->batch < 0 || d->heads < 0 || d->queries < 0 || d->keys < 0 || d->reserved) return AMSIM_EINVAL;
-    constexpr int64_t most = 0x7FFFFFFF - 4096;
+    constexpr int64_t most = 0x7FFFFFFF - (1 << 20);         // indexes of rows stay in 32 bits a step behind the last
     for (int64_t n : {d->batch, d->heads, d->queries, d->keys})
         if (n > most) return AMSIM_EINVAL;
     if (d->keys > (int64_t)1 << 30) return AMSIM_EINVAL;             // columns of chunks behind the last fit 32 bits

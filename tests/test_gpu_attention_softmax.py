@@ -125,7 +125,7 @@ def test_rows(amd, keys, bias, p):
     both_ways(amd, *make(2, 3, 13, keys, keys, bias), p=p)
 
 
-@pytest.mark.parametrize("keys", [16384, 16387, 20000, 32768, 40001, 131072])
+@pytest.mark.parametrize("keys", [16384, 16387, 20000, 32768, 40001, 131072, 200001, 262144, 300000])
 @pytest.mark.parametrize("p", [0.0, 0.1])
 def test_long_rows(amd, keys, p):
     both_ways(amd, *make(1, 2, 3, keys, keys, "past"), p=p, offset=keys - 3, causal=True)
