@@ -796,14 +796,19 @@ int check(const amsim_attention_softmax_desc *d, Drop *drop)
 // warp (what a row costs each warp is spread over 16 columns a lane), then by a
 // cluster of blocks.  Backward keeps two tensors, and beyond 512 threads of them
 // two chunks a warp.
+// Rows that two blocks of 1024 threads do not hold are read twice (the second
+// time from the cache) by clusters of eight small blocks, four or more an SM, whose
+// loads, exchanges and stores overlap: 300 rows of 131072 keys 77 us, of blocks
+// that fill an SM each and hold the row 133 us.  Few rows get those: one alone is
+// done sooner the more threads it has.
 constexpr int kMaxCluster = 8;
 struct Shape {
     int nv, threads, cluster;
     bool block;
 };
-Shape shape(int64_t keys, bool fwd)
+Shape shape(const amsim_attention_softmax_desc *d, bool fwd, int sms)
 {
-    const int64_t chunks = (keys + 127) / 128;
+    const int64_t chunks = (d->keys + 127) / 128;
     Shape s{1, 32 * kWarpRows, 1, false};
     if (chunks <= 4) {
         while (s.nv < chunks) s.nv *= 2;
@@ -811,12 +816,11 @@ Shape shape(int64_t keys, bool fwd)
     }
     s.block = true;
     s.nv = fwd || chunks <= 4 * kFewThreads / 32 ? 4 : 2;
-    const int64_t blocks = (chunks + 32 * s.nv - 1) / (32 * s.nv);
-    s.cluster = 1;
-    while (s.cluster < blocks && s.cluster < kMaxCluster) s.cluster *= 2;
-    if (blocks > kMaxCluster) s.nv = 0;
-    const int64_t warps = s.nv ? (chunks + s.nv * s.cluster - 1) / (s.nv * s.cluster) : 32;
-    s.threads = 32 * (int)warps;
+    const int64_t blocks = (chunks + 32 * s.nv - 1) / (32 * s.nv), rows = d->batch * d->heads * d->queries;
+    const bool many = rows * std::min<int64_t>(blocks, kMaxCluster) > 2 * (int64_t)sms;
+    if (blocks > kMaxCluster || (blocks > 2 && many)) return Shape{0, many ? 256 : 1024, kMaxCluster, true};
+    while (s.cluster < blocks) s.cluster *= 2;
+    s.threads = 32 * (int)((chunks + s.nv * s.cluster - 1) / (s.nv * s.cluster));
     return s;
 }
 
@@ -964,7 +968,7 @@ extern "C" int amsim_attention_softmax_fwd(const amsim_attention_softmax_desc *d
     if (!scores || !probs || !aligned(scores, 4) || !aligned(probs, 4) || !aligned(stats, 8)) return AMSIM_EINVAL;
     const int sms = device_sms();
     if (!sms) return AMSIM_ECUDA;
-    const Shape s = shape(d->keys, true);
+    const Shape s = shape(d, true, sms);
     const bool vec = aligned(scores, 16) && aligned(probs, 16) && !((d->keys | stride(d->ld_scores, d->keys) |
                                                                      stride(d->ld_probs, d->keys)) & 3);
     auto *kernel = vec ? forward_of<true>(s) : forward_of<false>(s);
@@ -984,7 +988,7 @@ extern "C" size_t amsim_attention_softmax_workspace_size(const amsim_attention_s
     if (check(d, &drop) || d->max_distance > AMSIM_MAX_DISTANCE) return 0;
     if (!d->batch || !d->heads || !d->queries || !d->keys) return 0;
     const int sms = device_sms();
-    const Shape s = shape(d->keys, false);
+    const Shape s = shape(d, false, sms ? sms : 1);
     int shares = 0;
     for (const bool vec : {false, true})         // the calls' pointers and arguments decide which
         for (const bool table : {false, true})
@@ -1025,7 +1029,7 @@ extern "C" int amsim_attention_softmax_bwd(const amsim_attention_softmax_desc *d
     const bool vec = aligned(scores, 16) && aligned(probs, 16) && aligned(dprobs, 16) && aligned(dscores, 16) &&
                      !((d->keys | stride(scores ? d->ld_scores : d->ld_probs, d->keys) |
                         stride(d->ld_dprobs, d->keys) | stride(d->ld_dscores, d->keys)) & 3);
-    Shape s = shape(d->keys, false);
+    Shape s = shape(d, false, sms);
     const size_t one = (size_t)d->heads * (2 * p.D + 1) * 4, room = ws ? ws_bytes / one : 0;
     if (dtable && s.cluster > 1 && room < (size_t)s.cluster)
         s = Shape{0, 1024, 1, true};             // no room for a cluster's sums: one block, rows read twice
