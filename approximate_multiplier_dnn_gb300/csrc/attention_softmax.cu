@@ -817,7 +817,7 @@ Shape shape(const amsim_attention_softmax_desc *d, bool fwd, int sms)
     s.block = true;
     s.nv = fwd || chunks <= 4 * kFewThreads / 32 ? 4 : 2;
     const int64_t blocks = (chunks + 32 * s.nv - 1) / (32 * s.nv), rows = d->batch * d->heads * d->queries;
-    const bool many = rows * std::min<int64_t>(blocks, kMaxCluster) > 2 * (int64_t)sms;
+    const bool many = rows * std::min<int64_t>(blocks, kMaxCluster) > (int64_t)sms;
     if (blocks > kMaxCluster || (blocks > 2 && many)) return Shape{0, many ? 256 : 1024, kMaxCluster, true};
     while (s.cluster < blocks) s.cluster *= 2;
     s.threads = 32 * (int)((chunks + s.nv * s.cluster - 1) / (s.nv * s.cluster));

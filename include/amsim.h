@@ -101,7 +101,8 @@ int amsim_last_path(void);
  *   AMSIM_WAIT_COPY     a CTA waited for its own asynchronous copies or for
  *                       another warp of its CTA (limit 2 s);
  *   AMSIM_WAIT_PARTIAL  a CTA waited for another CTA's partial sums of a
- *                       tile split across CTAs (stream-K);
+ *                       tile split across CTAs (stream-K), or for the
+ *                       statistics of a group norm's tile;
  *   AMSIM_WAIT_PHASE    a CTA of an amsim_gemm_phased launch waited for the
  *                       earlier phases its phase reads.
  * The last two wait on other CTAs of the same launch, with the limit that
@@ -850,7 +851,10 @@ typedef struct amsim_group_norm_desc {
 /*
  * Forward.  y is written and may alias x (equal types and strides); mean,
  * rstd: batch x groups values, written for the backward pass.  Scratch:
- * amsim_group_norm_workspace_size(desc, 0) or more, else AMSIM_EINVAL.
+ * amsim_group_norm_workspace_size(desc, 0) or more, else AMSIM_EINVAL (it may
+ * be 0); calls that are not ordered on the GPU need scratch of their own.
+ * Blocks of results wait for blocks of statistics that started before them
+ * (AMSIM_WAIT_PARTIAL).
  * Errors: AMSIM_EINVAL also for a null x, y, mean or rstd, or a bad size,
  * stride, type, activation or eps.  Without a batch it is a no-op; without
  * pixels mean is 0 and rstd 1 / sqrt(eps).
