@@ -7,9 +7,11 @@
 // pair work out results, the odd ones the statistics that come 32 MB later.  A
 // block of results waits until all of its tile's statistics are there, which
 // blocks that started before it work on; these wait for nothing.  Statistics are
-// joined by whoever needs them, in a fixed order.  Launches of a wave each (13 of
-// them for 617 MB) lost 4 us apiece at their ends; slabs kept in a cluster's shared
-// memory lost as much at its barriers (64 x 56 x 56 x 256 fp32 backward 159 and 154 us).
+// joined by whoever needs them, in a fixed order.  64 x 56 x 56 x 256 fp32
+// backward takes 142 us, 0.65 of a plain copy's rate, and reads 421 of 411 MB; with a launch
+// for each wave it took 159 us, with slabs kept in a cluster's shared memory 154 us.  What
+// bounds it is latency: 22 warps an SM, 36 % of the issue slots.  8 x 128 x 128 x 512 bf16
+// forward takes 74 us, 0.55.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
