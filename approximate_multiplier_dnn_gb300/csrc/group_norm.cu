@@ -400,7 +400,7 @@ __device__ __forceinline__ Values<E> weights_of(const Params &p, const float *w,
 
 // A piece as it is in memory, to be widened where it is used.  What is read for
 // the last time, and what is written, leaves the cache first: its room is for the
-// next wave.
+// tiles that are read again.
 template <typename T, int E>
 struct Raw {
     static constexpr int bytes = E * (int)sizeof(T);
