@@ -327,6 +327,11 @@ def am_attention(q, k, v, lut, scale: float | None = None, *, table=None, bucket
         raise ValueError("a bias needs both its table and the buckets of its distances")
     if table is None and lengths is None and not causal and dropout == 0.0:
         return _AttentionFn.apply(q, k, v, lut, float(scale))
+    if q.dim() != 4 or k.shape != (*q.shape[:2], k.shape[-2], q.shape[3]) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [batch, heads, keys, dim] with q's {tuple(q.shape)} but for the keys, not "
+                         f"{tuple(k.shape)} and {tuple(v.shape)}")
+    if lengths is not None and lengths.shape != q.shape[:1]:
+        raise ValueError(f"lengths must be of shape ({q.shape[0]},), not {tuple(lengths.shape)}")
     return _MaskedAttentionFn.apply(q, k, v, table, lut, float(scale), buckets, lengths, offset, step, bool(causal),
                                     float(dropout), seed, call)
 

@@ -139,6 +139,21 @@ def test_masked_attention(attention):
     assert not k.grad[1, :, 4:].any() and not v.grad[1, :, 4:].any()
 
 
+def test_masked_attention_refuses_shapes(attention):
+    """Lengths of another shape would hide channels in place of keys where a head
+    has as many channels as keys; k and v of another shape would be read as if
+    they had the first's."""
+    q, k = torch.randn(1, 2, 3, 8), torch.randn(1, 2, 8, 8)
+    for lengths in (torch.ones(1, 1, dtype=torch.int32), torch.ones(2, dtype=torch.int32), torch.tensor(1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="lengths"):
+            layers.am_attention(q, k, k, None, lengths=lengths)
+    for other in (torch.randn(1, 2, 4, 16), torch.randn(2, 1, 8, 8), torch.randn(1, 2, 8, 4), torch.randn(2, 8, 8)):
+        with pytest.raises(ValueError, match="k and v"):
+            layers.am_attention(q, k, other, None, causal=True)
+        with pytest.raises(ValueError, match="k and v"):
+            layers.am_attention(q, other, k, None, causal=True)
+
+
 def test_attention_gives_the_table_its_gradient(attention):
     bias = layers.RelativeBias(3, device="cpu")
     layer = layers.AMAttention(None, bias=bias, causal=True)
