@@ -284,20 +284,28 @@ class _MaskedAttentionFn(torch.autograd.Function):
         b, h, s, d = q.shape
         t = k.shape[2]
         qf, kf, vf = q.reshape(b * h, s, d), k.reshape(b * h, t, d), v.reshape(b * h, t, d)
+        ctx.lut, ctx.scale, ctx.shape = lut, scale, (b, h, s, t, d)
+        if not t:                        # no row sees a key, and the contractions take none without
+            ctx.save_for_backward(table)
+            return torch.zeros_like(q)
         S = _bgemm("N", "T", qf, kf, s, t, d, lut, alpha=scale).view(b, h, s, t)
         args = dict(buckets=buckets, lengths=lengths, causal=causal, offset=offset, p=p, seed=seed, call=call, step=step)
         P, stats = attention_softmax(S, table=table, out=None if p else S, **args)   # dropped ones are gone: S stays
         O = _bgemm("N", "N", P.view(b * h, s, t), vf, s, d, t, lut)
         keep = [buckets, lengths, step, offset if isinstance(offset, torch.Tensor) else None]
         ctx.save_for_backward(qf, kf, vf, P, *((S, stats) if p else (None, None)), table, *keep)
-        ctx.lut, ctx.scale, ctx.shape, ctx.args = lut, scale, (b, h, s, t, d), args
+        ctx.args = args
         return O.reshape(b, h, s, d)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dO):
-        qf, kf, vf, P, S, stats, table, *_ = ctx.saved_tensors
         b, h, s, t, d = ctx.shape
+        if not t:
+            table, = ctx.saved_tensors
+            none = dO.new_zeros((b, h, 0, d))
+            return torch.zeros_like(dO), none, none, None if table is None else torch.zeros_like(table), *[None] * 10
+        qf, kf, vf, P, S, stats, table, *_ = ctx.saved_tensors
         lut, scale = ctx.lut, ctx.scale
         dOf = _f32(dO).reshape(b * h, s, d)
         dV = _bgemm("T", "N", P.view(b * h, s, t), dOf, t, d, s, lut)

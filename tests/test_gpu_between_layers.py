@@ -57,6 +57,24 @@ def test_attention_is_its_parts(amd, luts, p, s, t, causal):
     assert torch.equal(layer(q, k, v, lengths=n), layer(q, k, v, lengths=n))
 
 
+@pytest.mark.parametrize("p", [0.0, 0.2])
+@pytest.mark.parametrize("s,t,causal", [(3, 0, False), (0, 5, True), (1, 1, True), (4, 6, False)])
+def test_attention_over_nothing(amd, luts, s, t, causal, p):
+    """No keys, no queries, lengths of zero: zeros out, and zero gradients for
+    what has no effect."""
+    import torch
+    from approximate_multiplier_dnn_gb300 import layers
+    g = torch.Generator().manual_seed(2)
+    bias = layers.RelativeBias(2, generator=g)
+    layer = layers.AMAttention(luts("mitchell", 7), bias=bias, causal=causal, dropout=p, seed=1)
+    q, k, v = (rand(g, 2, 2, n, 8).requires_grad_() for n in (s, t, t))
+    out = layer(q, k, v, lengths=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert out.shape == (2, 2, s, 8) and not out.any()
+    out.sum().backward()
+    for x in (q, k, v, bias.table):
+        assert x.grad.shape == x.shape and not x.grad.any()
+
+
 def test_single_tokens_continue_a_sequence(amd, luts):
     """A cache's next token, one query at its place, as that row of the whole
     sequence: the contractions' sums may be taken in another order (1e-5 of the
