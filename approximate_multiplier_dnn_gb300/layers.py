@@ -345,12 +345,22 @@ def am_attention(q, k, v, lut, scale: float | None = None, *, table=None, bucket
 
 
 class _Draws(torch.nn.Module):
-    """What a layer that draws keeps: a seed of its own and the number of its next call, both part of its state."""
+    """What a layer that draws keeps: a seed of its own and the number of its next call, both part of its state.
+
+    A checkpointed block is run again in the backward pass and has to draw the same masks.  torch.utils.checkpoint
+    gives torch's generator back the state that it had, so each call takes a value from that generator as its mark,
+    and a call within a backward pass takes the number of the call of the same mark.  Where that is not one call (the
+    generator was seeded anew before the first one's backward pass) it is refused."""
+
+    remembered = 1024                    # calls whose marks are known: those between a block's two runs
 
     def __init__(self, seed, generator):
         super().__init__()
         self.seed = int(torch.randint(0, 2 ** 62, (), generator=generator)) if seed is None else int(seed)
-        self.calls = 0
+        self.calls, self.marks = 0, {}
+
+    def __setstate__(self, state):
+        super().__setstate__({**state, "marks": {}})
 
     def get_extra_state(self):
         return dict(seed=self.seed, calls=self.calls)
@@ -363,7 +373,20 @@ class _Draws(torch.nn.Module):
         if call is None:
             if step is None and torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("a captured call draws the same mask at every replay: give it a step on the device")
-            call, self.calls = self.calls, self.calls + 1
+            mark = int(torch.randint(0, 2 ** 62, (), device="cpu"))
+            if torch._C._current_graph_task_id() != -1:              # within a backward pass
+                known = self.marks.get(mark)
+                if known is None or known["call"] is None:
+                    raise RuntimeError("a call within a backward pass that does not repeat one call of the forward "
+                                       "pass (a checkpoint without preserve_rng_state, or torch seeded anew?) would "
+                                       "draw another mask: give it the call's number")
+                call, known["repeated"] = known["call"], True
+            else:
+                call, self.calls = self.calls, self.calls + 1
+                known = self.marks.pop(mark, None)
+                self.marks[mark] = dict(call=call if known is None or known["repeated"] else None, repeated=False)
+                if len(self.marks) > self.remembered:
+                    del self.marks[next(iter(self.marks))]
         return dict(seed=self.seed, call=call, step=step)
 
 
@@ -389,7 +412,8 @@ class AMAttention(torch.nn.Module):
     padded states) and the first query's position (an int, or int32 [batch]: a
     single token's place in its cache).  Dropout draws a new mask at each call;
     step (one int64 CUDA value, raised once a replay) does so for a captured
-    one, and call repeats a given call's mask (activation checkpointing)."""
+    one, and call repeats a given call's mask.  A block that torch.utils.checkpoint
+    runs again draws what it drew; without preserve_rng_state it needs call."""
 
     def __init__(self, lut, scale: float | None = None, *, bias: RelativeBias | None = None, causal: bool = False,
                  dropout: float = 0.0, seed: int | None = None, generator: torch.Generator | None = None):
