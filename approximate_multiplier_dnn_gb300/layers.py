@@ -28,6 +28,7 @@ dQ = (dS, k), dK = (dS, q).
 """
 from __future__ import annotations
 
+import copy
 import math
 
 import torch
@@ -361,6 +362,13 @@ class _Draws(torch.nn.Module):
 
     def __setstate__(self, state):
         super().__setstate__({**state, "marks": {}})
+
+    def __deepcopy__(self, memo):
+        """A copy draws masks of its own, from a seed of its own: blocks are often made by copying one."""
+        memo[id(self)] = new = type(self).__new__(type(self))
+        new.__setstate__(copy.deepcopy({**self.__dict__, "marks": {}}, memo))
+        new.seed = int(torch.randint(0, 2 ** 62, (), device="cpu"))
+        return new
 
     def get_extra_state(self):
         return dict(seed=self.seed, calls=self.calls)

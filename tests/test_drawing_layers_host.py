@@ -112,3 +112,26 @@ def test_numbers_go_on_after_checkpointing(drawn):  # noqa: F811
     checkpoint(lambda t: layer(t * t).sin(), x, use_reentrant=False).sum().backward()
     layer(x)
     assert {n for _, n in drawn} == {0, 1} and layer.draws.calls == 2
+
+
+def test_deep_copies_draw_masks_of_their_own(drawn):  # noqa: F811
+    """Blocks made by copying one; a saved and reloaded layer, pickled or by its state, goes on as before."""
+    for layer in (layers.Dropout(0.5, seed=1), layers.AMAttention(None, dropout=0.5, seed=1)):
+        layer.draws.calls = 3
+        copies = [copy.deepcopy(layer), *copy.deepcopy(torch.nn.ModuleList([layer, layer]))]
+        assert copies[1] is copies[2]                                     # one layer at two places stays one
+        seeds = {layer.draws.seed, copies[0].draws.seed, copies[1].draws.seed, copy.deepcopy(copies[0]).draws.seed}
+        assert len(seeds) == 4 and layer.draws.seed == 1
+        assert all(c.draws.calls == 3 and c.draws.marks is not layer.draws.marks for c in copies)
+        again = pickle.loads(pickle.dumps(layer))
+        assert (again.draws.seed, again.draws.calls) == (1, 3)
+        copies[0].load_state_dict(layer.state_dict())
+        assert (copies[0].draws.seed, copies[0].draws.calls) == (1, 3)
+    layer, x = layers.Dropout(0.5, seed=1), torch.ones(100)
+    assert not torch.equal(copy.deepcopy(layer)(x), layer(x))
+    off = layers.Dropout(0.5, seed=1).eval()
+    assert not copy.deepcopy(off).training and not copy.deepcopy(off).draws.training
+    torch.manual_seed(0)
+    a = copy.deepcopy(layer).draws.seed
+    torch.manual_seed(0)
+    assert a == copy.deepcopy(layer).draws.seed                           # repeatable
