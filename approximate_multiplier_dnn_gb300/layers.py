@@ -354,6 +354,7 @@ class _Draws(torch.nn.Module):
     generator was seeded anew before the first one's backward pass) it is refused."""
 
     remembered = 1024                    # calls whose marks are known: those between a block's two runs
+    replays = 2 ** 32                    # numbers that a captured call takes: its own, and one more for each step
 
     def __init__(self, seed, generator):
         super().__init__()
@@ -379,7 +380,8 @@ class _Draws(torch.nn.Module):
     def next(self, call, step) -> dict:
         """Seed and number of a call: the caller's number, or one more than the last."""
         if call is None:
-            if step is None and torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            captured = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+            if captured and step is None:
                 raise RuntimeError("a captured call draws the same mask at every replay: give it a step on the device")
             mark = int(torch.randint(0, 2 ** 62, (), device="cpu"))
             if torch._C._current_graph_task_id() != -1:              # within a backward pass
@@ -390,7 +392,7 @@ class _Draws(torch.nn.Module):
                                        "draw another mask: give it the call's number")
                 call, known["repeated"] = known["call"], True
             else:
-                call, self.calls = self.calls, self.calls + 1
+                call, self.calls = self.calls, self.calls + (self.replays if captured else 1)
                 known = self.marks.pop(mark, None)
                 self.marks[mark] = dict(call=call if known is None or known["repeated"] else None, repeated=False)
                 if len(self.marks) > self.remembered:

@@ -135,3 +135,22 @@ def test_deep_copies_draw_masks_of_their_own(drawn):  # noqa: F811
     a = copy.deepcopy(layer).draws.seed
     torch.manual_seed(0)
     assert a == copy.deepcopy(layer).draws.seed                           # repeatable
+
+
+def test_captured_calls_take_numbers_that_no_replay_repeats(drawn, monkeypatch):  # noqa: F811
+    """A layer that is called twice in a graph, whose step is raised once a
+    replay, and again after it: no two masks are alike."""
+    layer, x, step = layers.Dropout(0.5, seed=1), torch.ones(10), torch.zeros(1, dtype=torch.int64)
+    layer(x, step=step)
+    first = layer.draws.calls
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError):
+        layer(x)
+    layer(x, step=step), layer(x, step=step)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    layer(x)
+    before, *captured, after = [n for _, n in drawn]
+    assert captured[0] == first == 1                                      # the next number, as an eager call's
+    seen = {n + replay for n in captured for replay in range(1000)} | {before, after}
+    assert len(seen) == 2002
