@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import re
 
@@ -1064,11 +1065,13 @@ def _softmax_call(shape, table, buckets, lengths, causal, offset, p, seed, call,
     if lengths is not None:
         _vector("lengths", lengths, b, torch.int32, here)
         d.lengths = lengths.data_ptr()
-    if isinstance(offset, int):
-        d.offset = offset
-    else:
+    if hasattr(offset, "data_ptr"):
         _vector("offset", offset, b, torch.int32, here)
         d.offsets = offset.data_ptr()
+    else:
+        d.offset = operator.index(offset)
+        if abs(offset) > 1 << 40:                # a field of 64 bits would keep some of it
+            raise ValueError(f"offset must be within 2^40, not {offset}")
     return d
 
 
