@@ -793,7 +793,6 @@ int check(const amsim_attention_softmax_desc *d, Drop *drop)
         if (ld != 0 && (ld < d->keys || ld > (int64_t)1 << 31)) return AMSIM_EINVAL;
     if (d->offset > (int64_t)1 << 40 || d->offset < -((int64_t)1 << 40)) return AMSIM_EINVAL;
     if ((d->causal != 0 && d->causal != 1) || !aligned(d->lengths, 4) || !aligned(d->offsets, 4)) return AMSIM_EINVAL;
-    if (d->num_buckets < 0 || d->max_distance < 0) return AMSIM_EINVAL;
     return amsim::make_drop(d->dropout, drop) ? AMSIM_OK : AMSIM_EINVAL;
 }
 
@@ -942,7 +941,7 @@ void fill(Params &p, const amsim_attention_softmax_desc *d, const Shape &s, int 
 
 int check_bias(const amsim_attention_softmax_desc *d, Params &p)
 {
-    if (!aligned(p.table, 4) || !aligned(p.buckets, 4) || d->num_buckets < 1) return AMSIM_EINVAL;
+    if (!aligned(p.table, 4) || !aligned(p.buckets, 4) || d->num_buckets < 1 || d->max_distance < 0) return AMSIM_EINVAL;
     if ((int64_t)d->num_buckets * d->heads > 0x7FFFFFFF) return AMSIM_EINVAL;
     if (d->max_distance > AMSIM_MAX_DISTANCE) return AMSIM_EUNSUPPORTED;
     p.num_buckets = d->num_buckets;
@@ -990,7 +989,7 @@ extern "C" int amsim_attention_softmax_fwd(const amsim_attention_softmax_desc *d
 extern "C" size_t amsim_attention_softmax_workspace_size(const amsim_attention_softmax_desc *d)
 {
     Drop drop;
-    if (check(d, &drop) || d->max_distance > AMSIM_MAX_DISTANCE) return 0;
+    if (check(d, &drop) || d->num_buckets < 0 || d->max_distance < 0 || d->max_distance > AMSIM_MAX_DISTANCE) return 0;
     if (!d->batch || !d->heads || !d->queries || !d->keys) return 0;
     const int sms = device_sms();
     const Shape s = shape(d, false, sms ? sms : 1);

@@ -41,3 +41,17 @@ def test_offset_tensors(described):
                      (Tensor(1, 2, dtype=torch.int32), ValueError)):
         with pytest.raises(error):
             described(t)
+
+
+@pytest.mark.parametrize("bias", [dict(num_buckets=-1), dict(max_distance=-5), dict(max_distance=1 << 30)])
+def test_sizes_of_a_bias_that_is_not_there_are_not_looked_at(bias):
+    am.build()
+    L, P = am.lib(), 1 << 20
+    for size, status in ((0, am.AMSIM_OK), (2, None)):       # with rows a call gets as far as the device
+        d = ctypes.byref(am.AttentionSoftmaxDesc(batch=size, heads=3, queries=4, keys=8, **bias))
+        if size and torch.cuda.is_available():
+            continue
+        for rc in (L.amsim_attention_softmax_fwd(d, P, None, None, P, P, None),
+                   L.amsim_attention_softmax_bwd(d, P, None, None, P, None, None, P, None, None, 0, None)):
+            assert rc == status if status is not None else rc != am.AMSIM_EINVAL
+        assert L.amsim_attention_softmax_fwd(d, P, P, P, P, P, None) in (am.AMSIM_EINVAL, am.AMSIM_EUNSUPPORTED)
