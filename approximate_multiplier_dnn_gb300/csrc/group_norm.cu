@@ -498,7 +498,8 @@ __device__ __forceinline__ void moments(const Params &p, const Part &t, float2 *
             });
         });
     const float n = (float)(t.count * E), sum = s1.x + s1.y, m = t.count ? __fdividef(sum, n) : 0.0f;
-    all[threadIdx.x] = Moments{n, about + m, fmaxf((s2.x + s2.y) - sum * m, 0.0f)};
+    const float m2 = (s2.x + s2.y) - sum * m;
+    all[threadIdx.x] = Moments{n, about + m, m2 < 0.0f ? 0.0f : m2};     // NaN stays
     __syncthreads();
     // a warp per group joins its threads: pieces side by side, then rows
     const int wide = p.splits > 1 ? t.wide : p.size / E, threads = wide * t.step;
