@@ -101,11 +101,11 @@ __device__ __forceinline__ Four load_chunk(const float *row, int chunk, int lane
     }
     return v;
 }
-// `fill` behind the last visible key of a whole piece.
-template <bool VEC, bool FULL = false>
+// `fill` behind the last visible key of a whole piece; of any piece where something was added to it (ADDED).
+template <bool VEC, bool FULL = false, bool ADDED = false>
 __device__ __forceinline__ void fill_chunk(Four &v, int chunk, int lane, int visible, float fill)
 {
-    if (VEC && !FULL && (chunk + 1) * 128 > visible)
+    if ((VEC || ADDED) && !FULL && (chunk + 1) * 128 > visible)
         each(v, [&](float &x, int k) { if (column<VEC>(chunk, lane, k) >= visible) x = fill; });
 }
 // Zeros where no key is visible.
@@ -391,8 +391,10 @@ __device__ __forceinline__ void forward_rows(const Params &p, const Part &t, con
         if (DROP) draws = row_draws(w.row, p, call);
         auto logits = [&](auto full, Four a, int chunk) {
             constexpr bool FULL = decltype(full)::value;
-            fill_chunk<VEC, FULL>(a, chunk, lane, w.visible, -INFINITY);
-            if (BIAS && (FULL || chunk * 128 < w.visible)) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
+            if (FULL || chunk * 128 < w.visible) {
+                if (BIAS) add_bias<VEC>(a, bias, chunk, lane, w.pos, p);
+                fill_chunk<VEC, FULL, BIAS>(a, chunk, lane, w.visible, -INFINITY);   // whatever hidden keys' biases are
+            }
             return a;
         };
         auto finish = [&](auto full, Four e, int chunk, float factor) {
