@@ -374,7 +374,8 @@ def _kind(kind) -> int:
 
 # ------------------------------------------------------------------ LUT
 class Lut:
-    """Owner of an amsim_lut_t handle (device LUT on the current device)."""
+    """Owner of an amsim_lut_t handle (device LUT on the current device).  There is one owner of a handle: a copy, or a
+    copied layer's, is the same object."""
 
     def __init__(self, handle: int, M: int):
         self.handle = handle
@@ -410,6 +411,16 @@ class Lut:
         if self.handle:
             lib().amsim_lut_destroy(self.handle)
             self.handle = None
+
+    def __copy__(self):
+        return self
+
+    def __deepcopy__(self, memo):
+        return self
+
+    def __reduce__(self):
+        raise TypeError("a Lut holds device memory and cannot be pickled: save a layer's state dict, and build the table "
+                        "again")
 
     def __del__(self):
         try:
