@@ -806,7 +806,11 @@ int check(const amsim_attention_softmax_desc *d, Drop *drop)
 // many (the second time from the cache) by clusters of eight small blocks, four or more an SM, whose
 // loads, exchanges and stores overlap: 300 rows of 131072 keys 77 us, of blocks
 // that fill an SM each and hold the row 133 us.  Few rows get those: one alone is
-// done sooner the more threads it has.
+// done sooner the more threads it has.  The border is where the large blocks no longer
+// fit the machine at once, some rows from where both are alike: of 131072 keys (eight
+// blocks a row) 8 rows take 11.2 us in small and 7.4 in large blocks, 16 rows 12.4 and
+// 13.8, 20 rows 12.8 and 14.4, 32 rows 13.7 and 21; of 40000 keys (three) 32 rows 8.2
+// and 6.8, 38 rows 8.8 and 11.4, 64 rows 10.4 and 12.6.
 constexpr int kMaxCluster = 8;
 struct Shape {
     int nv, threads, cluster;

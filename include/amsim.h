@@ -738,8 +738,10 @@ int amsim_adamw_moment_values(const void *codes, const float *scales, int second
  * What stands between the simulated contractions of attention and of
  * convolutions: attention's softmax with a learned relative position bias,
  * key lengths, a causal mask and dropout; dropout of a tensor; the group norm
- * with its activation.  None of them is simulated: all arithmetic is IEEE fp32
- * and a bf16 result is rounded once, to nearest even.
+ * with its activation.  None of them is simulated: all arithmetic is fp32,
+ * exponentials and silu's reciprocal by instructions that are within some 2^-22
+ * (results below the smallest normal number are 0), and a bf16 result is rounded
+ * once, to nearest even.
  *
  * Random numbers: Philox4x32-10 (Salmon et al., SC 2011) with the key `seed`
  * and the counter (quad, call + *step), 64 bits each, gives the four 32-bit
@@ -747,7 +749,8 @@ int amsim_adamw_moment_values(const void *codes, const float *scales, int second
  * p 2^32 (rounded to a whole number) and is then multiplied by 1 / (1 - p),
  * else it is zero.  No mask is stored: the backward pass draws it again from
  * the same seed, call and step.  `step` (one device value, or null: 0) lets a
- * captured graph draw new numbers each time it is launched.
+ * captured graph draw new numbers each time it is launched: calls of one seed
+ * in it want numbers further apart than step is raised.
  */
 typedef struct amsim_dropout_desc {
     double p;                        /* 0 <= p < 1; 0: everything stays, nothing is drawn */
@@ -834,8 +837,10 @@ size_t amsim_attention_softmax_workspace_size(const amsim_attention_softmax_desc
  * channels; group g of `groups` holds channels / groups consecutive channels:
  *   mean, var: over the pixels and channels of (n, g) (var divides by their number),
  *   rstd = 1 / sqrt(var + eps),  xh = (x - mean) rstd,  z = xh w + b,  y = act(z).
- * Squares are summed about a value near the mean, so a mean that is large
- * against the deviation costs no digits.  w and b (or null: ones, zeros) are
+ * Squares are summed about one of the values, so that a mean that is large
+ * against the deviation costs rstd no digits; xh carries the rounding of the
+ * mean to fp32, some 2^-24 |mean| rstd.  Where squares of differences overflow
+ * (above some 1e19) results are NaN, or rstd is 0.  w and b (or null: ones, zeros) are
  * fp32.  A non-finite value makes its whole group NaN.
  */
 enum amsim_activation { AMSIM_ACT_NONE = 0, AMSIM_ACT_RELU = 1, AMSIM_ACT_SILU = 2 };
