@@ -345,13 +345,20 @@ def am_attention(q, k, v, lut, scale: float | None = None, *, table=None, bucket
                                     float(dropout), seed, call)
 
 
+def _may_run_again() -> bool:
+    """Whether torch.utils.checkpoint may be running this code, to run it again in the backward pass: it does so under
+    hooks for saved tensors or (reentrant) without gradients."""
+    hooks = getattr(torch._C._autograd, "_top_saved_tensors_default_hooks", None)
+    return not torch.is_grad_enabled() or hooks is None or hooks(True) is not None
+
+
 class _Draws(torch.nn.Module):
     """What a layer that draws keeps: a seed of its own and the number of its next call, both part of its state.
 
     A checkpointed block is run again in the backward pass and has to draw the same masks.  torch.utils.checkpoint
-    gives torch's generator back the state that it had, so each call takes a value from that generator as its mark,
-    and a call within a backward pass takes the number of the call of the same mark.  Where that is not one call (the
-    generator was seeded anew before the first one's backward pass) it is refused."""
+    gives torch's generator back the state that it had, so each call that may be run again takes a value from that
+    generator as its mark, and a call within a backward pass takes the number of the call of the same mark.  Where that
+    is not one call (the generator was seeded anew before the first one's backward pass) it is refused."""
 
     remembered = 1024                    # calls whose marks are known: those between a block's two runs
     replays = 2 ** 32                    # numbers that a captured call takes: its own, and one more for each step
@@ -383,9 +390,8 @@ class _Draws(torch.nn.Module):
             captured = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
             if captured and step is None:
                 raise RuntimeError("a captured call draws the same mask at every replay: give it a step on the device")
-            mark = int(torch.randint(0, 2 ** 62, (), device="cpu"))
             if torch._C._current_graph_task_id() != -1:              # within a backward pass
-                known = self.marks.get(mark)
+                known = self.marks.get(self.mark())
                 if known is None or known["call"] is None:
                     raise RuntimeError("a call within a backward pass that does not repeat one call of the forward "
                                        "pass (a checkpoint without preserve_rng_state, or torch seeded anew?) would "
@@ -393,11 +399,17 @@ class _Draws(torch.nn.Module):
                 call, known["repeated"] = known["call"], True
             else:
                 call, self.calls = self.calls, self.calls + (self.replays if captured else 1)
-                known = self.marks.pop(mark, None)
-                self.marks[mark] = dict(call=call if known is None or known["repeated"] else None, repeated=False)
-                if len(self.marks) > self.remembered:
-                    del self.marks[next(iter(self.marks))]
+                if _may_run_again():
+                    mark = self.mark()
+                    known = self.marks.pop(mark, None)
+                    self.marks[mark] = dict(call=call if known is None or known["repeated"] else None, repeated=False)
+                    if len(self.marks) > self.remembered:
+                        del self.marks[next(iter(self.marks))]
         return dict(seed=self.seed, call=call, step=step)
+
+    @staticmethod
+    def mark() -> int:
+        return int(torch.randint(0, 2 ** 62, (), device="cpu"))
 
 
 class RelativeBias(torch.nn.Module):

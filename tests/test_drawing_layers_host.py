@@ -99,11 +99,23 @@ def test_marks_are_bounded(drawn, monkeypatch):  # noqa: F811
     monkeypatch.setattr(layers._Draws, "remembered", 5)
     layer, x = layers.Dropout(0.5, seed=1), torch.ones(50, requires_grad=True)
     y = checkpoint(lambda t: layer(t * t).sin(), x, use_reentrant=False).sum()
-    for _ in range(7):
-        layer(x)
+    with torch.no_grad():
+        for _ in range(7):
+            layer(x)
     assert len(layer.draws.marks) == 5
     with pytest.raises(RuntimeError, match="call"):
         y.backward()
+
+
+def test_calls_that_nothing_runs_again_leave_the_generator_alone(drawn):  # noqa: F811
+    """A plain call takes nothing from torch's generator and is not remembered, between checkpointed ones too."""
+    layer, x = layers.Dropout(0.5, seed=1), torch.ones(50, requires_grad=True)
+    y = checkpoint(lambda t: layer(t * t).sin(), x, use_reentrant=False).sum()
+    before = torch.get_rng_state()
+    layer(x).sum().backward()
+    assert torch.equal(torch.get_rng_state(), before) and len(layer.draws.marks) == 1
+    y.backward()
+    assert [n for _, n in drawn] == [0, 1, 1, 0, 0]
 
 
 def test_numbers_go_on_after_checkpointing(drawn):  # noqa: F811
