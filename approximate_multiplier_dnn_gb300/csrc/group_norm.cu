@@ -525,7 +525,8 @@ __device__ __forceinline__ void moments(const Params &p, const Part &t, float2 *
 // bf16 results of groups whose mean is at most so many deviations from zero are x (rstd w) + (b - mean rstd w):
 // what the second factor's rounding loses, u (|b| + 4 |w|), a value four deviations out loses of itself.  Further
 // away it would not (a constant group of 3000 gave -0.025 for b = 0): there the mean is taken off first
-// (8 x 128 x 128 x 512, silu: 75 and 78 us; 64 x 56 x 56 x 256, relu: 61 and 65).
+// (8 x 128 x 128 x 512, silu: 75 and 78 us; 64 x 56 x 56 x 256, relu: 62 and 65), by all of a warp's lanes,
+// which else would run through both forms (every second group far from zero: 108 and 91 us).
 constexpr float kFoldedMean = 4.0f;
 
 // Forward, results.
@@ -580,7 +581,7 @@ __device__ __forceinline__ void normalise(const Params &p, const Part &t, float2
     } else {
         // one factor rstd w, a product an element less
         each_pair<E>([&](int j) { w.v[j] = mul2(w.v[j], both(f.y)); });
-        if (fabsf(f.x) * f.y <= kFoldedMean) {
+        if (!__any_sync(0xFFFFFFFFu, fabsf(f.x) * f.y > kFoldedMean)) {
             each_pair<E>([&](int j) { b.v[j] = fma2(w.v[j], both(-f.x), b.v[j]); });
             results([&](float2 v, int j) { return fma2(v, w.v[j], b.v[j]); });
         } else {

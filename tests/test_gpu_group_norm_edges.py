@@ -89,3 +89,29 @@ def test_groups_far_from_zero(amd, y, pixels, mean, spread):
     ref = xw + b
     tol = R * abs(w) * off * (1 + tr) + abs(xw) * (tr + 4 * U) + 2 * U * (abs(xw) + abs(b))
     assert (abs(f64(got).reshape(ref.shape) - ref) <= tol + HALF[y] * (abs(ref) + tol)).all()
+
+
+@pytest.mark.parametrize("y", ["f32", "bf16"])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("pixels", [60, 5000])
+def test_groups_near_and_far_from_zero_side_by_side(amd, x, y, pixels):
+    """Groups of eight channels whose threads share warps, at -2000, 0, 3, 100
+    and a constant 500.  From mean and rstd as they are: the subtraction, the
+    product with rstd (or of rstd and w) and the sum with b each round once, 4 u
+    |xh w| and 2 u of the terms; a bf16 result whose mean is up to four deviations
+    from zero may first take mean rstd w from b, u 4 |w| more.  bf16 adds half a step."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(10)
+    a = make(2, pixels, 40, y=y, seed=4)
+    at = torch.tensor([-2000.0, 0.0, 3.0, 100.0, 500.0], device="cuda").repeat_interleave(8)
+    wide = torch.tensor([1.0, 1.0, 1.0, 1.0, 0.0], device="cuda").repeat_interleave(8)
+    a["x"] = (at + wide * torch.randn((2, pixels, 40), generator=g, device="cuda")).to(dt(x))
+    got, m, r = amd.group_norm(a["x"], 5, a["w"], a["b"], y_dtype=dt(y))
+    M, R = f64(m)[:, None, :, None], f64(r)[:, None, :, None]
+    w, b = (f64(a[k]).reshape(5, 8) for k in "wb")
+    xh = (f64(a["x"]).reshape(2, pixels, 5, 8) - M) * R
+    ref = xh * w + b
+    near = (abs(M) * R <= 4.001) * (y == "bf16")
+    tol = abs(w) * U * (4 * abs(xh) + 4 * near) + 2 * U * (abs(xh * w) + abs(b))
+    assert (abs(f64(got).reshape(ref.shape) - ref) <= tol + HALF[y] * (abs(ref) + tol)).all()
+    assert not (ref - b)[:, :, 4].any()
